@@ -27,6 +27,9 @@ EXPORTS = (
     "gdn2_chunk_fwd_noalloc", "gdn2_recurrent_update", "gdn2_fg2_inputs", "gdn2_mixer_prologue",
     "gdn2_mixer_epilogue", "gdn2_backward_workspace_size", "gdn2_backward",
     "gdn2_backward_recurrent_workspace_size", "gdn2_backward_recurrent", "gdn2_mixer_decode_step",
+    "gdn2_ssm_prologue", "gdn2_ssm_prologue_backward_workspace_size", "gdn2_ssm_prologue_backward",
+    "gdn2_ssm_chunk_fwd_workspace_size", "gdn2_ssm_chunk_fwd", "gdn2_ssm_backward_workspace_size", "gdn2_ssm_backward",
+    "gdn2_ssm_decode_step", "gdn2_block_norm", "gdn2_block_norm_backward_workspace_size", "gdn2_block_norm_backward",
 )
 
 
@@ -64,6 +67,18 @@ def _load() -> ctypes.CDLL:
         "gdn2_backward_recurrent_workspace_size": (Z, [I] * 6 + [I]),
         "gdn2_backward_recurrent": (I, [P] * 16 + [I] * 6 + [F, I, P, Z, P]),
         "gdn2_mixer_decode_step": (I, [P] * 15 + [F, P] + [I] * 6 + [F, I, P]),
+        "gdn2_ssm_prologue": (I, [P, L, P, L] + [P] * 9 + [I] * 5 + [I, P]),
+        "gdn2_ssm_prologue_backward_workspace_size": (Z, [I] * 5 + [I]),
+        "gdn2_ssm_prologue_backward": (I, [P, L, P, L] + [P] * 5 + [P, L, P, P, P, L, P, L] + [P] * 4 + [I] * 5 + [I, P, Z, P]),
+        "gdn2_ssm_chunk_fwd_workspace_size": (Z, [I] * 8 + [I]),
+        "gdn2_ssm_chunk_fwd": (I, [I, P, L, P, P, P, L, P, L] + [P] * 5 + [I] * 6 + [I, P, Z, P]),
+        "gdn2_ssm_backward_workspace_size": (Z, [I] * 8 + [I]),
+        "gdn2_ssm_backward": (I, [I, P, L, P, P, P, L, P, L, P, P, P, L, P, P, P, L, P, P, P, L, P, L, P, P] + [I] * 6 +
+                              [I, P, Z, P]),
+        "gdn2_ssm_decode_step": (I, [P, L, P, L] + [P] * 7 + [I, P, I, P] + [I] * 5 + [I, P]),
+        "gdn2_block_norm": (I, [P] * 8 + [L, I, I, F, I, P]),
+        "gdn2_block_norm_backward_workspace_size": (Z, [L, I]),
+        "gdn2_block_norm_backward": (I, [P] * 14 + [L, I, I, F, I, P, Z, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -348,3 +363,307 @@ def gdn2_mixer_decode_step(xq, xk, xv, conv_q, conv_k, conv_v, ag, ab, aw, state
                                     int(bool(neg_eigval)), float(scale), _dtype_code(xq), _stream(stream))
     _check(st, "gdn2_mixer_decode_step")
     return y
+
+
+# ---- selective state-space mixer ------------------------------------------------------------------------
+
+def _rows(t, width, name):
+    """(pointer, row stride) of a token tensor [..., *tail] whose last dimensions hold `width` dense elements per
+    row and whose rows lie one stride apart (a slice of a wider row is fine)."""
+    if not t.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    shape, stride = t.shape, t.stride()
+    dense, k = 1, len(shape)
+    while k and dense < width:
+        k -= 1
+        if shape[k] != 1 and stride[k] != dense:
+            raise ValueError(f"{name}: the dimensions within a row must be dense")
+        dense *= shape[k]
+    if dense != width:
+        raise ValueError(f"{name}: rows of {width} elements expected, got shape {tuple(shape)}")
+    ld, reach = None, None
+    for i in range(k - 1, -1, -1) if t.numel() else ():
+        if shape[i] == 1:
+            continue
+        if ld is None:
+            ld = reach = stride[i]
+        elif stride[i] != reach:
+            raise ValueError(f"{name}: rows must lie one stride apart")
+        reach = reach * shape[i]
+    return ctypes.c_void_p(t.data_ptr()), width if ld is None else ld
+
+
+def _f32(t, name, shape=None):
+    import torch
+
+    if t is None:
+        return None
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} is float32")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _lead(t, tail, offsets):
+    """(B, T) of a call: a token tensor's leading dimensions [B, T], or [T] with B from the offsets."""
+    import torch
+
+    lead = t.shape[:t.dim() - tail]
+    if offsets is None:
+        if len(lead) != 2:
+            raise ValueError("token tensors are [B, T, ...] (or [T, ...] with offsets)")
+        return lead[0], lead[1]
+    if len(lead) != 1:
+        raise ValueError("with offsets, token tensors are [T, ...]")
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 1:
+        raise TypeError("offsets is an int32 tensor of one entry more than sequences")
+    return offsets.numel() - 1, lead[0]
+
+
+def _same(dtype, lead, *named):
+    for name, t, tail in named:
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: all token tensors share one dtype")
+        if tuple(t.shape) != (*lead, *tail):
+            raise ValueError(f"{name}: shape {(*lead, *tail)} expected, got {tuple(t.shape)}")
+
+
+def _workspace(need, like, given):
+    import torch
+
+    return given if given is not None else torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
+
+
+def gdn2_ssm_prologue(xbc, delta, conv_weight, conv_bias, a, delta_bias, u, step, g, conv_state=None, offsets=None, *,
+                      silu=True, stream=None):
+    """Causal depthwise convolution (width 4) and gates of the selective state-space mixer (C ABI
+    gdn2_ssm_prologue): u = silu(conv(xbc) + conv_bias), step = softplus(delta + delta_bias), g = a * step.
+
+    xbc, u: [B, T, channels]; delta, step, g: [B, T, H]; conv_weight: float32 [channels, 4]; conv_bias: float32
+    [channels] or None; a, delta_bias: float32 [H]; conv_state: float32 [B, 3, channels], replaced in place, or None.
+    With offsets (int32 [B + 1], on the device) the sequences are packed and token tensors are [T, ...]. xbc and delta
+    may be slices of wider rows.
+    """
+    B, T = _lead(xbc, 1, offsets)
+    ch, H = xbc.shape[-1], delta.shape[-1]
+    lead = xbc.shape[:-1]
+    _same(xbc.dtype, lead, ("delta", delta, (H,)), ("u", u, (ch,)), ("step", step, (H,)), ("g", g, (H,)))
+    (px, lx), (pd, ld) = _rows(xbc, ch, "xbc"), _rows(delta, H, "delta")
+    st = lib.gdn2_ssm_prologue(px, lx, pd, ld, _f32(conv_weight, "conv_weight", (ch, 4)), _f32(conv_bias, "conv_bias", (ch,)),
+                               _f32(a, "a", (H,)), _f32(delta_bias, "delta_bias", (H,)),
+                               _f32(conv_state, "conv_state", (B, 3, ch)), _ptr(offsets), _ptr(u), _ptr(step), _ptr(g), B, T,
+                               ch, H, int(bool(silu)), _dtype_code(xbc), _stream(stream))
+    _check(st, "gdn2_ssm_prologue")
+    return u, step, g
+
+
+def ssm_prologue(xbc, delta, conv_weight, conv_bias, a, delta_bias, conv_state=None, offsets=None, *, silu=True, stream=None):
+    """Returns (u, step, g); conv_state, if given, is updated in place."""
+    import torch
+
+    new = lambda t: torch.empty(t.shape, dtype=xbc.dtype, device=xbc.device)
+    return gdn2_ssm_prologue(xbc, delta, conv_weight, conv_bias, a, delta_bias, new(xbc), new(delta), new(delta), conv_state,
+                             offsets, silu=silu, stream=stream)
+
+
+def gdn2_ssm_prologue_backward(xbc, delta, conv_weight, conv_bias, a, delta_bias, du, dstep, dg, dxbc, ddelta, dconv_weight,
+                               dconv_bias, da, ddelta_bias, offsets=None, *, silu=True, workspace=None, stream=None):
+    """Gradients of gdn2_ssm_prologue from zero convolution states (C ABI gdn2_ssm_prologue_backward); writes dxbc,
+    ddelta (token dtype; may be slices of wider rows) and the float32 parameter gradients (dconv_bias may be None)."""
+    B, T = _lead(xbc, 1, offsets)
+    ch, H = xbc.shape[-1], delta.shape[-1]
+    _same(xbc.dtype, xbc.shape[:-1], ("delta", delta, (H,)), ("du", du, (ch,)), ("dstep", dstep, (H,)), ("dg", dg, (H,)),
+          ("dxbc", dxbc, (ch,)), ("ddelta", ddelta, (H,)))
+    (px, lx), (pd, ld) = _rows(xbc, ch, "xbc"), _rows(delta, H, "delta")
+    (pu, lu), (po, lo), (pe, le) = _rows(du, ch, "du"), _rows(dxbc, ch, "dxbc"), _rows(ddelta, H, "ddelta")
+    dt = _dtype_code(xbc)
+    ws = _workspace(lib.gdn2_ssm_prologue_backward_workspace_size(B, T, ch, H, int(offsets is not None), dt), xbc, workspace)
+    st = lib.gdn2_ssm_prologue_backward(px, lx, pd, ld, _f32(conv_weight, "conv_weight", (ch, 4)),
+                                        _f32(conv_bias, "conv_bias", (ch,)), _f32(a, "a", (H,)),
+                                        _f32(delta_bias, "delta_bias", (H,)), _ptr(offsets), pu, lu, _ptr(dstep), _ptr(dg),
+                                        po, lo, pe, le, _f32(dconv_weight, "dconv_weight", (ch, 4)),
+                                        _f32(dconv_bias, "dconv_bias", (ch,)), _f32(da, "da", (H,)),
+                                        _f32(ddelta_bias, "ddelta_bias", (H,)), B, T, ch, H, int(bool(silu)), dt, _ptr(ws),
+                                        ws.numel(), _stream(stream))
+    _check(st, "gdn2_ssm_prologue_backward")
+    return dxbc, ddelta, dconv_weight, dconv_bias, da, ddelta_bias
+
+
+def ssm_prologue_backward(xbc, delta, conv_weight, conv_bias, a, delta_bias, du, dstep, dg, offsets=None, *, silu=True,
+                          stream=None):
+    """Returns (dxbc, ddelta, dconv_weight, dconv_bias or None, da, ddelta_bias)."""
+    import torch
+
+    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device) if t is not None else None
+    return gdn2_ssm_prologue_backward(xbc, delta, conv_weight, conv_bias, a, delta_bias, du, dstep, dg, new(xbc), new(delta),
+                                      new(conv_weight), new(conv_bias), new(a), new(delta_bias), offsets, silu=silu,
+                                      stream=stream)
+
+
+def _scan_sizes(x, bm, offsets):
+    B, T = _lead(x, 2, offsets)
+    H, P = x.shape[-2:]
+    G, N = bm.shape[-2:]
+    return B, T, H, G, P, N
+
+
+def gdn2_ssm_chunk_fwd(x, step, g, bm, cm, y, d=None, initial_state=None, final_state=None, offsets=None, *, path="auto",
+                       workspace=None, stream=None):
+    """Selective state-space scan (C ABI gdn2_ssm_chunk_fwd): per head H_t = e^{g_t} H_{t-1} + step_t B_t x_t^T,
+    y_t = H_t^T C_t + d x_t; writes y and, if given, final_state.
+
+    x, y: [B, T, H, P]; step, g: [B, T, H]; bm, cm: [B, T, G, N]; d: float32 [H] or None; states: float32
+    [B, H, N, P]. With offsets (int32 [B + 1], on the device) the sequences are packed and token tensors are [T, ...].
+    x, bm and cm may be slices of wider rows.
+    """
+    B, T, H, G, P, N = _scan_sizes(x, bm, offsets)
+    _same(x.dtype, x.shape[:-2], ("step", step, (H,)), ("g", g, (H,)), ("bm", bm, (G, N)), ("cm", cm, (G, N)), ("y", y, (H, P)))
+    (px, lx), (pb, lb), (pc, lc) = _rows(x, H * P, "x"), _rows(bm, G * N, "bm"), _rows(cm, G * N, "cm")
+    dt, packed = _dtype_code(x), int(offsets is not None)
+    ws = _workspace(lib.gdn2_ssm_chunk_fwd_workspace_size(PATHS[path], B, T, H, G, P, N, packed, dt), x, workspace)
+    st = lib.gdn2_ssm_chunk_fwd(PATHS[path], px, lx, _ptr(step), _ptr(g), pb, lb, pc, lc, _f32(d, "d", (H,)),
+                                _f32(initial_state, "initial_state", (B, H, N, P)),
+                                _f32(final_state, "final_state", (B, H, N, P)), _ptr(offsets), _ptr(y), B, T, H, G, P, N, dt,
+                                _ptr(ws), ws.numel(), _stream(stream))
+    _check(st, "gdn2_ssm_chunk_fwd")
+    return y, final_state
+
+
+def ssm_chunk_fwd(x, step, g, bm, cm, d=None, initial_state=None, offsets=None, *, output_final_state=True, path="auto",
+                  workspace=None, stream=None):
+    """Returns (y, final_state or None)."""
+    import torch
+
+    B, T, H, G, P, N = _scan_sizes(x, bm, offsets)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    fs = torch.empty((B, H, N, P), dtype=torch.float32, device=x.device) if output_final_state else None
+    return gdn2_ssm_chunk_fwd(x, step, g, bm, cm, y, d, initial_state, fs, offsets, path=path, workspace=workspace, stream=stream)
+
+
+def gdn2_ssm_backward(x, step, g, bm, cm, d_y, dx, dstep, dg, dbm, dcm, dd=None, d=None, initial_state=None,
+                      d_final_state=None, d_initial_state=None, offsets=None, *, path="auto", workspace=None, stream=None):
+    """Gradients of gdn2_ssm_chunk_fwd (C ABI gdn2_ssm_backward); writes dx, dstep, dg, dbm, dcm (token dtype; dx, dbm
+    and dcm may be slices of wider rows) and, if given, the float32 dd and d_initial_state."""
+    B, T, H, G, P, N = _scan_sizes(x, bm, offsets)
+    _same(x.dtype, x.shape[:-2], ("step", step, (H,)), ("g", g, (H,)), ("bm", bm, (G, N)), ("cm", cm, (G, N)),
+          ("d_y", d_y, (H, P)), ("dx", dx, (H, P)), ("dstep", dstep, (H,)), ("dg", dg, (H,)), ("dbm", dbm, (G, N)),
+          ("dcm", dcm, (G, N)))
+    r = [_rows(t, w, n) for t, w, n in ((x, H * P, "x"), (bm, G * N, "bm"), (cm, G * N, "cm"), (d_y, H * P, "d_y"),
+                                       (dx, H * P, "dx"), (dbm, G * N, "dbm"), (dcm, G * N, "dcm"))]
+    st4 = (B, H, N, P)
+    dt, packed = _dtype_code(x), int(offsets is not None)
+    ws = _workspace(lib.gdn2_ssm_backward_workspace_size(PATHS[path], B, T, H, G, P, N, packed, dt), x, workspace)
+    st = lib.gdn2_ssm_backward(PATHS[path], *r[0], _ptr(step), _ptr(g), *r[1], *r[2], _f32(d, "d", (H,)),
+                               _f32(initial_state, "initial_state", st4), *r[3], _f32(d_final_state, "d_final_state", st4),
+                               _ptr(offsets), *r[4], _ptr(dstep), _ptr(dg), *r[5], *r[6], _f32(dd, "dd", (H,)),
+                               _f32(d_initial_state, "d_initial_state", st4), B, T, H, G, P, N, dt, _ptr(ws), ws.numel(),
+                               _stream(stream))
+    _check(st, "gdn2_ssm_backward")
+    return dx, dstep, dg, dbm, dcm, dd, d_initial_state
+
+
+def ssm_backward(x, step, g, bm, cm, d_y, d=None, initial_state=None, d_final_state=None, offsets=None, *, path="auto",
+                 workspace=None, stream=None):
+    """Returns (dx, dstep, dg, dbm, dcm, dd, d_initial_state); dd is None without d, d_initial_state without initial_state.
+    dx, dbm and dcm are slices of one row [..., H * P + 2 * G * N], the layout of the prologue's u and du."""
+    import torch
+
+    B, T, H, G, P, N = _scan_sizes(x, bm, offsets)
+    new = lambda shape, dt=x.dtype: torch.empty(shape, dtype=dt, device=x.device)
+    row = new((*x.shape[:-2], H * P + 2 * G * N))
+    dx, db, dc = row[..., :H * P], row[..., H * P:H * P + G * N], row[..., H * P + G * N:]
+    return gdn2_ssm_backward(x, step, g, bm, cm, d_y, dx.unflatten(-1, (H, P)), new(step.shape), new(g.shape),
+                             db.unflatten(-1, (G, N)), dc.unflatten(-1, (G, N)),
+                             new((H,), torch.float32) if d is not None else None, d, initial_state, d_final_state,
+                             new((B, H, N, P), torch.float32) if initial_state is not None else None, offsets, path=path,
+                             workspace=workspace, stream=stream)
+
+
+def gdn2_ssm_decode_step(xbc, delta, conv_weight, conv_bias, a, delta_bias, d, conv_state, state, y, slots=None, *, stream=None):
+    """One token of the selective state-space mixer between its projections (C ABI gdn2_ssm_decode_step): convolution
+    with SiLU, gates, state update and readout in one launch.
+
+    xbc: [B, channels] with channels = H P + 2 G N (x, B, C side by side); delta: [B, H] (both may be slices of wider
+    rows); y: [B, H, P]; conv_state: float32 [B, 3, channels]; state: float32 or bfloat16 [B, H, N, P], both updated in
+    place; with slots (int32 [B]) they are pools [n_slots, ...] and a slot out of range leaves its row untouched.
+    """
+    import torch
+
+    B, ch = xbc.shape
+    rows, H, N, P = state.shape
+    G = (ch - H * P) // (2 * N)
+    if ch != H * P + 2 * G * N or G < 1:
+        raise ValueError("xbc holds H * P + 2 * G * N channels")
+    if slots is None and rows != B:
+        raise ValueError("without slots, the states have one row per sequence")
+    if slots is not None and (slots.dtype != torch.int32 or tuple(slots.shape) != (B,)):
+        raise TypeError("slots is int32 [B]")
+    _same(xbc.dtype, (B,), ("delta", delta, (H,)), ("y", y, (H, P)))
+    (px, lx), (pd, ld) = _rows(xbc, ch, "xbc"), _rows(delta, H, "delta")
+    st = lib.gdn2_ssm_decode_step(px, lx, pd, ld, _f32(conv_weight, "conv_weight", (ch, 4)), _f32(conv_bias, "conv_bias", (ch,)),
+                                  _f32(a, "a", (H,)), _f32(delta_bias, "delta_bias", (H,)), _f32(d, "d", (H,)),
+                                  _f32(conv_state, "conv_state", (rows, 3, ch)), _ptr(state), _dtype_code(state), _ptr(slots),
+                                  rows if slots is not None else 0, _ptr(y), B, H, G, P, N, _dtype_code(xbc), _stream(stream))
+    _check(st, "gdn2_ssm_decode_step")
+    return y
+
+
+def ssm_decode_step(xbc, delta, conv_weight, conv_bias, a, delta_bias, d, conv_state, state, slots=None, *, stream=None):
+    """Returns y [B, H, P]; conv_state and state are updated in place. Rows of inactive slots are left unwritten."""
+    import torch
+
+    y = torch.empty((xbc.shape[0], state.shape[1], state.shape[3]), dtype=xbc.dtype, device=xbc.device)
+    return gdn2_ssm_decode_step(xbc, delta, conv_weight, conv_bias, a, delta_bias, d, conv_state, state, y, slots, stream=stream)
+
+
+def gdn2_block_norm(x, z, post_weight, residual, scale, pre_weight, r, n, *, groups=1, eps=1e-5, stream=None):
+    """The residual stream around a block (C ABI gdn2_block_norm): p = post_weight * t / rms_group(t) with
+    t = x silu(z), r = residual + scale p, n = pre_weight * r / rms(r). z, post_weight, residual, scale and pre_weight
+    may each be None; r may be None when n is wanted alone. x, z, residual, r, n: [..., d]; weights: float32 [d]."""
+    dim = x.shape[-1]
+    _same(x.dtype, x.shape[:-1], *((k, t, (dim,)) for k, t in (("z", z), ("residual", residual), ("r", r), ("n", n)) if t is not None))
+    st = lib.gdn2_block_norm(_ptr(x), _ptr(z), _f32(post_weight, "post_weight", (dim,)), _ptr(residual),
+                             _f32(scale, "scale", (dim,)), _f32(pre_weight, "pre_weight", (dim,)), _ptr(r), _ptr(n),
+                             x.numel() // dim if dim else 0, dim, groups, float(eps), _dtype_code(x), _stream(stream))
+    _check(st, "gdn2_block_norm")
+    return r, n
+
+
+def block_norm(x, z=None, post_weight=None, residual=None, scale=None, pre_weight=None, *, groups=1, eps=1e-5, stream=None):
+    """Returns (r, n): r is None when there is a norm before the next block but no residual to carry on; n is None
+    without pre_weight."""
+    import torch
+
+    r = torch.empty_like(x) if residual is not None or pre_weight is None else None
+    n = torch.empty_like(x) if pre_weight is not None else None
+    return gdn2_block_norm(x, z, post_weight, residual, scale, pre_weight, r, n, groups=groups, eps=eps, stream=stream)
+
+
+def gdn2_block_norm_backward(x, z, post_weight, residual, scale, pre_weight, d_r, d_n, dx, dz, dpost_weight, dresidual, dscale,
+                             dpre_weight, *, groups=1, eps=1e-5, workspace=None, stream=None):
+    """Gradients of gdn2_block_norm (C ABI gdn2_block_norm_backward) given those of r (d_r, or None) and n (d_n, with
+    pre_weight): one output for each input given; dresidual may be None."""
+    dim = x.shape[-1]
+    rows = x.numel() // dim if dim else 0
+    _same(x.dtype, x.shape[:-1], *((k, t, (dim,)) for k, t in (("z", z), ("residual", residual), ("d_r", d_r), ("d_n", d_n),
+                                                              ("dx", dx), ("dz", dz), ("dresidual", dresidual)) if t is not None))
+    ws = _workspace(lib.gdn2_block_norm_backward_workspace_size(rows, dim), x, workspace)
+    f = lambda t, k: _f32(t, k, (dim,))
+    st = lib.gdn2_block_norm_backward(_ptr(x), _ptr(z), f(post_weight, "post_weight"), _ptr(residual), f(scale, "scale"),
+                                      f(pre_weight, "pre_weight"), _ptr(d_r), _ptr(d_n), _ptr(dx), _ptr(dz),
+                                      f(dpost_weight, "dpost_weight"), _ptr(dresidual), f(dscale, "dscale"),
+                                      f(dpre_weight, "dpre_weight"), rows, dim, groups, float(eps), _dtype_code(x), _ptr(ws),
+                                      ws.numel(), _stream(stream))
+    _check(st, "gdn2_block_norm_backward")
+    return dx, dz, dpost_weight, dresidual, dscale, dpre_weight
+
+
+def block_norm_backward(x, z=None, post_weight=None, residual=None, scale=None, pre_weight=None, d_r=None, d_n=None, *,
+                        groups=1, eps=1e-5, stream=None):
+    """Returns (dx, dz, dpost_weight, dresidual, dscale, dpre_weight), None for inputs not given."""
+    import torch
+
+    new = lambda t: torch.empty_like(t) if t is not None else None
+    return gdn2_block_norm_backward(x, z, post_weight, residual, scale, pre_weight, d_r, d_n, new(x), new(z), new(post_weight),
+                                    new(residual), new(scale), new(pre_weight), groups=groups, eps=eps, stream=stream)

@@ -1,0 +1,155 @@
+// ssm_common.cuh -- shared by the selective state-space operators: where the sequences of a call lie
+// (equal lengths, or packed one after the other), how they are cut into units, and the gate functions.
+#pragma once
+
+#include "common.cuh"
+
+namespace gdn2 {
+
+// The sequences of a call. offsets == nullptr: B sequences of T tokens, sequence b at rows b*T.. .
+// Otherwise sequence b is rows [offsets[b], offsets[b+1]) of T rows in all. Offsets live on the device
+// and cannot be checked on the host, so every use goes through span(), which clamps them to [0, T]:
+// wrong offsets give wrong results, never an access outside the tensors.
+struct Seqs {
+    const int* offsets;
+    int B, T;
+    __device__ __forceinline__ void span(int b, int& start, int& len) const {
+        if (!offsets) {
+            start = b * T;
+            len = T;
+            return;
+        }
+        const int lo = min(max(__ldg(offsets + b), 0), T), hi = min(max(__ldg(offsets + b + 1), 0), T);
+        start = lo;
+        len = max(hi - lo, 0);
+    }
+    long long rows() const { return offsets ? (long long)T : (long long)B * T; }
+    // Units of `unit` tokens over all sequences, an empty sequence counted as one unit: exact for equal
+    // lengths, an upper bound (unknown to the host) for packed ones.
+    __host__ __device__ long long units(int unit) const {
+        if (!offsets) return (long long)B * (T > 0 ? (T + unit - 1) / unit : 1);
+        return (long long)T / unit + B;
+    }
+    // Units of one sequence.
+    __device__ __forceinline__ static int units_of(int len, int unit) { return len > unit ? (len + unit - 1) / unit : 1; }
+};
+
+// One unit of a sequence: its place among the sequence's units and its tokens.
+struct Unit {
+    int seq, k, count;  // unit k of `count` of sequence seq
+    int row, len;       // first token row and tokens (0 for an empty sequence)
+};
+
+// Unit number `idx` of a call. False past the last one. Every lane of the calling warp gets the answer;
+// the warps of a block may call it independently.
+__device__ __forceinline__ bool find_unit(const Seqs& s, int unit, int idx, Unit& u) {
+    int start = 0, len = 0;
+    if (!s.offsets) {
+        const int per = Seqs::units_of(s.T, unit);
+        u.seq = idx / per;
+        if (u.seq >= s.B) return false;
+        u.k = idx - u.seq * per;
+        start = u.seq * s.T;
+        len = s.T;
+    } else {
+        // 32 sequences at a time: their unit counts, a warp prefix sum, and the lane that holds idx
+        const int lane = threadIdx.x & 31;
+        int base = 0, found = -1;
+        for (int b0 = 0; b0 < s.B; b0 += 32) {
+            int st = 0, ln = 0, n = 0;
+            if (b0 + lane < s.B) {
+                s.span(b0 + lane, st, ln);
+                n = Seqs::units_of(ln, unit);
+            }
+            int incl = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += v;
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, idx < base + incl);
+            if (m) {
+                const int src = __ffs(m) - 1;
+                found = b0 + src;
+                u.k = idx - base - __shfl_sync(0xffffffffu, incl - n, src);
+                start = __shfl_sync(0xffffffffu, st, src);
+                len = __shfl_sync(0xffffffffu, ln, src);
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (found < 0) return false;
+        u.seq = found;
+    }
+    u.count = Seqs::units_of(len, unit);
+    u.row = start + u.k * unit;
+    u.len = min(unit, len - u.k * unit);
+    return true;
+}
+
+// The sequence that holds token row r and the row its successor starts at; false if no sequence holds it.
+__device__ __forceinline__ bool find_row(const Seqs& s, int r, int& seq, int& start, int& end) {
+    if (!s.offsets) {
+        seq = r / s.T;
+        start = seq * s.T;
+        end = start + s.T;
+        return true;
+    }
+    int lo = 0, hi = s.B;  // the last sequence that starts at or before r
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (__ldg(s.offsets + m) <= r) lo = m; else hi = m;
+    }
+    int len;
+    s.span(lo, start, len);
+    seq = lo;
+    end = start + len;
+    return r >= start && r < end;
+}
+
+__device__ __forceinline__ float ssm_sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+// log(1 + e^v), exact to fp32 for either sign
+__device__ __forceinline__ float ssm_softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
+
+// Log-decays enter every exponential floored (common.cuh): a full reset (g = -inf) keeps sums finite.
+__device__ __forceinline__ float ssm_gate(float g) { return fmaxf(g, kGateFloor); }
+
+inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// One tensor of the scan: pointer and row (token) stride in elements; heads and channels are dense.
+struct Rows {
+    const void* p;
+    long long ld;
+};
+struct RowsOut {
+    void* p;
+    long long ld;
+};
+
+struct ScanShape {
+    Seqs seqs;
+    int H, G, P, N;
+    gdn2_dtype dt;
+};
+
+struct ScanIn {
+    Rows x, bm, cm;            // [rows, H, P], [rows, G, N], [rows, G, N]
+    const void *step, *g;      // [rows, H]
+    const float *d, *s0;       // [H] or null; [B, H, N, P] or null
+};
+
+// Launchers of the two kernel families (ssm_scan.cu: CUDA cores; ssm_tc.cu: tensor cores).
+size_t ssm_simt_fwd_workspace(const ScanShape& sh);
+cudaError_t launch_ssm_simt_fwd(const ScanShape& sh, const ScanIn& in, void* y, float* s1, void* ws, cudaStream_t s);
+
+struct ScanGrads {
+    Rows dy;                     // [rows, H, P]
+    const float* ds1;            // [B, H, N, P] or null
+    RowsOut dx, dbm, dcm;        // like x, bm, cm
+    void *dstep, *dg;            // [rows, H]
+    float *dd, *ds0;             // [H] or null; [B, H, N, P] or null
+};
+size_t ssm_simt_bwd_workspace(const ScanShape& sh);
+cudaError_t launch_ssm_simt_bwd(const ScanShape& sh, const ScanIn& in, const ScanGrads& gr, void* ws, cudaStream_t s);
+
+}  // namespace gdn2

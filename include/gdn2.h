@@ -335,6 +335,141 @@ gdn2_status gdn2_backward_recurrent(const void* q, const void* k, const void* v,
                                     void* stream);
 
 /*
+ * The selective state-space mixer: the pieces between a state-space token mixer's projections, next to
+ * the GDN-2 core and with its layouts (grouped key side, fp32 states, decode out of pools).
+ *
+ * Shared by the gdn2_ssm_* entry points:
+ *   - Sequences: offsets == NULL means B sequences of T tokens, token t of sequence b in row b * T + t.
+ *     Otherwise offsets is an int32 device array of B + 1 entries and sequence b is rows
+ *     [offsets[b], offsets[b + 1]) of T rows in all; sequences may be empty, and rows outside all of them
+ *     are left unwritten. Offsets are read on the device and clamped to [0, T] there.
+ *   - Rows: ld_* is the stride from one token row to the next in elements, for tensors that are slices of
+ *     wider rows; within a row heads and channels are dense. Rows of x, bm, cm, d_y and their gradients start
+ *     on 16-byte boundaries and their ld is a multiple of 8 (GDN2_ERR_MISALIGNED). Rows of xbc, du, delta and
+ *     their gradients, and step and g, need only their element's alignment (wider is faster for xbc and du).
+ *     Tensors without ld are contiguous.
+ *   - A token that is not finite makes its own sequence's results from its chunk on (128 tokens, or the
+ *     token itself on the CUDA-core path) not finite; it never reaches another sequence.
+ * Errors: GDN2_ERR_INVALID_ARG (dtype, sizes, H % G, null required pointer, ld below the row's width),
+ * GDN2_ERR_UNSUPPORTED (shape not built, too large), GDN2_ERR_MISALIGNED, GDN2_ERR_WORKSPACE,
+ * GDN2_ERR_CUDA. Asynchronous on `stream`; no entry point allocates or synchronises.
+ */
+
+/*
+ * gdn2_ssm_prologue -- short causal convolution and gates before the scan:
+ *   u_t = silu(conv_bias + sum_{j=0..3} conv_weight[.][j] xbc_{t-3+j})  per channel (no silu when silu == 0)
+ *   step = softplus(delta + delta_bias),  g = a step                    per head
+ *   xbc [rows, channels] dt, delta [rows, H] dt -> u [rows, channels], step, g [rows, H] dt
+ *   conv_weight fp32 [channels][4] (tap 3 = current token), conv_bias fp32 [channels] or NULL
+ *   a (negative for a decay), delta_bias fp32 [H]
+ *   conv_state  fp32 [B][3][channels] (x_{-3}, x_{-2}, x_{-1}) read and then replaced by the last three
+ *               samples of [state, x]; NULL = zeros in, nothing written
+ * channels a multiple of 8 (C of the scan, B and x side by side: H P + 2 G N). For one token pass T = 1.
+ */
+gdn2_status gdn2_ssm_prologue(const void* xbc, long long ld_xbc, const void* delta, long long ld_delta,
+                              const float* conv_weight, const float* conv_bias, const float* a,
+                              const float* delta_bias, float* conv_state, const int32_t* offsets, void* u,
+                              void* step, void* g, int B, int T, int channels, int H, int silu, gdn2_dtype dt,
+                              void* stream);
+
+/*
+ * gdn2_ssm_prologue_backward -- gradients of gdn2_ssm_prologue with zero convolution states, given those
+ * of u, step and g: dxbc, ddelta (dt), and fp32 dconv_weight [channels][4], dconv_bias [channels] (may be
+ * NULL), da, ddelta_bias [H], summed over all rows in a fixed order.
+ * workspace: gdn2_ssm_prologue_backward_workspace_size(...) bytes, 16-byte aligned.
+ */
+size_t gdn2_ssm_prologue_backward_workspace_size(int B, int T, int channels, int H, int packed, gdn2_dtype dt);
+gdn2_status gdn2_ssm_prologue_backward(const void* xbc, long long ld_xbc, const void* delta, long long ld_delta,
+                                       const float* conv_weight, const float* conv_bias, const float* a,
+                                       const float* delta_bias, const int32_t* offsets, const void* du,
+                                       long long ld_du, const void* dstep, const void* dg, void* dxbc,
+                                       long long ld_dxbc, void* ddelta, long long ld_ddelta, float* dconv_weight,
+                                       float* dconv_bias, float* da, float* ddelta_bias, int B, int T, int channels,
+                                       int H, int silu, gdn2_dtype dt, void* workspace, size_t ws_bytes,
+                                       void* stream);
+
+/*
+ * gdn2_ssm_chunk_fwd -- selective state-space scan over whole sequences: per head, on a state in R^{N x P},
+ *     S_t = e^{g_t} S_{t-1} + step_t B_t x_t^T,    y_t = S_t^T C_t + d x_t
+ *   x, y   [rows, H, P] dt;  step, g [rows, H] dt (g = log-decay <= 0, -inf allowed)
+ *   bm, cm [rows, G, N] dt: head h reads group h / (H / G)
+ *   d      fp32 [H] or NULL (0)
+ *   initial_state, final_state  fp32 [B, H, N, P] or NULL (zeros / not written); may alias
+ * The final state of an empty sequence is its initial state. Supported: P a multiple of 8 up to 256, N in
+ * {16, 32, 64, 128, 256}; B <= 65535.
+ * workspace: gdn2_ssm_chunk_fwd_workspace_size(...) bytes (packed != 0 for calls with offsets), 16-byte
+ * aligned; may be NULL when that is 0.
+ */
+size_t gdn2_ssm_chunk_fwd_workspace_size(gdn2_path path, int B, int T, int H, int G, int P, int N, int packed,
+                                         gdn2_dtype dt);
+gdn2_status gdn2_ssm_chunk_fwd(gdn2_path path, const void* x, long long ld_x, const void* step, const void* g,
+                               const void* bm, long long ld_b, const void* cm, long long ld_c, const float* d,
+                               const float* initial_state, float* final_state, const int32_t* offsets, void* y,
+                               int B, int T, int H, int G, int P, int N, gdn2_dtype dt, void* workspace,
+                               size_t ws_bytes, void* stream);
+
+/*
+ * gdn2_ssm_backward -- gradients of gdn2_ssm_chunk_fwd: of sum(y d_y) + sum(final_state d_final_state).
+ *   d_y [rows, H, P] dt; d_final_state fp32 [B, H, N, P] or NULL (zeros)
+ *   dx, dstep, dg, dbm, dcm like x, step, g, bm, cm (dbm and dcm sum the heads of their group)
+ *   dd fp32 [H] or NULL; d_initial_state fp32 [B, H, N, P] or NULL; may alias d_final_state
+ * The forward's outputs are not needed. Sums over heads and rows run in a fixed order. Shapes and
+ * workspace as for the forward.
+ */
+size_t gdn2_ssm_backward_workspace_size(gdn2_path path, int B, int T, int H, int G, int P, int N, int packed,
+                                        gdn2_dtype dt);
+gdn2_status gdn2_ssm_backward(gdn2_path path, const void* x, long long ld_x, const void* step, const void* g,
+                              const void* bm, long long ld_b, const void* cm, long long ld_c, const float* d,
+                              const float* initial_state, const void* d_y, long long ld_dy,
+                              const float* d_final_state, const int32_t* offsets, void* dx, long long ld_dx,
+                              void* dstep, void* dg, void* dbm, long long ld_db, void* dcm, long long ld_dc,
+                              float* dd, float* d_initial_state, int B, int T, int H, int G, int P, int N,
+                              gdn2_dtype dt, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * gdn2_ssm_decode_step -- one token of the mixer between its projections in one launch: the prologue's
+ * convolution (with silu) and gates and the scan's update and readout, with u, step and g kept in fp32.
+ *   xbc        [B, channels] dt, channels = H P + 2 G N: x, B and C side by side; delta [B, H] dt
+ *   conv_state fp32 [B][3][channels] and state [B, H, N, P] of state_dt (GDN2_F32, or GDN2_BF16: widened on
+ *              load, rounded on store), read and replaced; with slots (int32 [B]) both are pools of n_slots
+ *              rows and element b uses row slots[b]. A slot outside [0, n_slots) marks the element
+ *              inactive: nothing of it is read or written. Active elements must name distinct slots.
+ *   y          [B, H, P] dt; d fp32 [H] or NULL
+ * P in {16, 32, 64, 128}, N in {16, 32, 64, 128, 256}, B <= 65535. B == 0 is a no-op.
+ */
+gdn2_status gdn2_ssm_decode_step(const void* xbc, long long ld_xbc, const void* delta, long long ld_delta,
+                                 const float* conv_weight, const float* conv_bias, const float* a,
+                                 const float* delta_bias, const float* d, float* conv_state, void* state,
+                                 gdn2_dtype state_dt, const int32_t* slots, int n_slots, void* y, int B, int H, int G,
+                                 int P, int N, gdn2_dtype dt, void* stream);
+
+/*
+ * gdn2_block_norm -- the residual stream around a block in one pass over its rows:
+ *     t = x silu(z);  p = post_weight t / sqrt(mean_group(t^2) + eps);  r = residual + scale p;
+ *     n = pre_weight r / sqrt(mean(r^2) + eps)
+ * z, post_weight, residual, scale and pre_weight may each be NULL: without them t = x, p = t, no residual, scale 1,
+ * no n. x, z, residual, r, n [rows, d] dt (r and n may alias x or residual); weights and scale fp32 [d].
+ * r may be NULL when n is wanted alone; n and pre_weight go together. groups (1 without post_weight) cuts
+ * the row for the norm after the block. d a multiple of 8 groups, up to 8192; pointers 16-byte aligned.
+ */
+gdn2_status gdn2_block_norm(const void* x, const void* z, const float* post_weight, const void* residual,
+                            const float* scale, const float* pre_weight, void* r, void* n, long long rows, int d,
+                            int groups, float eps, gdn2_dtype dt, void* stream);
+
+/*
+ * gdn2_block_norm_backward -- gradients of gdn2_block_norm given those of r (d_r, may be NULL) and of n (d_n,
+ * with pre_weight). dz, dpost_weight, dscale and dpre_weight go with z, post_weight, scale and pre_weight;
+ * dresidual may be NULL. Parameter gradients are fp32, summed over the rows in a fixed order.
+ * workspace: gdn2_block_norm_backward_workspace_size(rows, d) bytes, 16-byte aligned.
+ */
+size_t gdn2_block_norm_backward_workspace_size(long long rows, int d);
+gdn2_status gdn2_block_norm_backward(const void* x, const void* z, const float* post_weight, const void* residual,
+                                     const float* scale, const float* pre_weight, const void* d_r, const void* d_n,
+                                     void* dx, void* dz, float* dpost_weight, void* dresidual, float* dscale,
+                                     float* dpre_weight, long long rows, int d, int groups, float eps, gdn2_dtype dt,
+                                     void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * gdn2_selftest_umma -- diagnostics: one tcgen05 product D[128][N] = A * B (bf16 in, fp32 out)
  * with the operand layouts the tensor-core chunked kernels use, so that a test can check them
  * against a host matrix product. The operands are row-major bf16 device arrays:
