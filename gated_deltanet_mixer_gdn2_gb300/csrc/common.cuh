@@ -101,6 +101,7 @@ int decode_read_clear_status(cudaStream_t s);
 int step_read_clear_status(cudaStream_t s);
 int chunk_simt_read_clear_status(cudaStream_t s);
 int chunk_tc_read_clear_status(cudaStream_t s);
+int ssm_tc_read_clear_status(cudaStream_t s);
 
 long long wait_limit_ns();
 

@@ -22,9 +22,11 @@ gdn2_status scan_check(gdn2_path path, const ScanShape& sh) {
     if (sh.seqs.B < 0 || sh.seqs.T < 0 || sh.H <= 0 || sh.G <= 0 || sh.P <= 0 || sh.N <= 0 || sh.H % sh.G)
         return GDN2_ERR_INVALID_ARG;
     if (!scan_shape_ok(sh.P, sh.N) || !scan_sizes_ok(sh)) return GDN2_ERR_UNSUPPORTED;
-    if (path == GDN2_PATH_TCGEN05) return GDN2_ERR_UNSUPPORTED;
+    if (path == GDN2_PATH_TCGEN05 && !ssm_tc_shape(sh)) return GDN2_ERR_UNSUPPORTED;
     return GDN2_OK;
 }
+
+bool on_tensor_cores(gdn2_path path, const ScanShape& sh) { return path != GDN2_PATH_SIMT && ssm_tc_shape(sh); }
 
 // Row stride of a token tensor of `width` dense elements: at least the width, rows on 16-byte boundaries.
 gdn2_status row_check(const void* p, long long ld, long long width) {
@@ -45,7 +47,7 @@ extern "C" {
 size_t gdn2_ssm_chunk_fwd_workspace_size(gdn2_path path, int B, int T, int H, int G, int P, int N, int packed, gdn2_dtype dt) {
     const ScanShape sh{{packed ? &kFakeOffset : nullptr, B, T}, H, G, P, N, dt};
     if (scan_check(path, sh) != GDN2_OK || B == 0 || sh.seqs.rows() == 0) return 0;
-    return ssm_simt_fwd_workspace(sh);
+    return on_tensor_cores(path, sh) ? ssm_tc_fwd_workspace(sh) : ssm_simt_fwd_workspace(sh);
 }
 
 size_t gdn2_ssm_backward_workspace_size(gdn2_path path, int B, int T, int H, int G, int P, int N, int packed, gdn2_dtype dt) {
@@ -85,7 +87,9 @@ gdn2_status gdn2_ssm_chunk_fwd(gdn2_path path, const void* x, long long ld_x, co
     if (need && (!workspace || ws_bytes < need)) return GDN2_ERR_WORKSPACE;
     if (need && !aligned16(workspace)) return GDN2_ERR_MISALIGNED;
     const ScanIn in{{x, ld_x}, {bm, ld_b}, {cm, ld_c}, step, g, d, initial_state};
-    return launch_ssm_simt_fwd(sh, in, y, final_state, workspace, s) == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA;
+    const cudaError_t e = on_tensor_cores(path, sh) ? launch_ssm_tc_fwd(sh, in, y, final_state, workspace, s, wait_limit_ns())
+                                                    : launch_ssm_simt_fwd(sh, in, y, final_state, workspace, s);
+    return e == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA;
 }
 
 gdn2_status gdn2_ssm_backward(gdn2_path path, const void* x, long long ld_x, const void* step, const void* g,

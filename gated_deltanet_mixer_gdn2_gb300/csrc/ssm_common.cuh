@@ -152,4 +152,8 @@ struct ScanGrads {
 size_t ssm_simt_bwd_workspace(const ScanShape& sh);
 cudaError_t launch_ssm_simt_bwd(const ScanShape& sh, const ScanIn& in, const ScanGrads& gr, void* ws, cudaStream_t s);
 
+bool ssm_tc_shape(const ScanShape& sh);
+size_t ssm_tc_fwd_workspace(const ScanShape& sh);
+cudaError_t launch_ssm_tc_fwd(const ScanShape& sh, const ScanIn& in, void* y, float* s1, void* ws, cudaStream_t s, long long wait_ns);
+
 }  // namespace gdn2
