@@ -9,6 +9,7 @@ The binding fails loudly: importing it raises if libgdn2.so has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -366,73 +367,114 @@ def gdn2_mixer_decode_step(xq, xk, xv, conv_q, conv_k, conv_v, ag, ab, aw, state
 
 
 # ---- selective state-space mixer ------------------------------------------------------------------------
+# A call here costs as much host time as many of the kernels run for, so arguments are checked and marshalled
+# in one pass, pointers go to ctypes as integers, and workspace sizes are looked up by the call's sizes.
 
-def _rows(t, width, name):
-    """(pointer, row stride) of a token tensor [..., *tail] whose last dimensions hold `width` dense elements per
-    row and whose rows lie one stride apart (a slice of a wider row is fine)."""
+@functools.lru_cache(maxsize=4096)
+def _size_of(fn, *sizes) -> int:
+    return getattr(lib, fn)(*sizes)
+
+
+def _raw_stream(stream, t):
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+
+
+def _dense(t, dtype, shape, name):
+    """Pointer of a contiguous CUDA tensor of this dtype and shape; None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} is {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError("tensors must live on a CUDA device")
-    shape, stride = t.shape, t.stride()
-    dense, k = 1, len(shape)
-    while k and dense < width:
-        k -= 1
-        if shape[k] != 1 and stride[k] != dense:
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, dtype, shape, tail, name):
+    """(pointer, row stride) of a token tensor [..., *tail]: each row's last `tail` dimensions are dense, the rows lie
+    one stride apart (a slice of a wider row is fine)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: all token tensors share one dtype, {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    width = shape[-1] if tail == 1 else shape[-1] * shape[-2]
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    stride = t.stride()
+    dense = 1
+    for i in range(len(shape) - 1, len(shape) - 1 - tail, -1):
+        if shape[i] != 1 and stride[i] != dense:
             raise ValueError(f"{name}: the dimensions within a row must be dense")
-        dense *= shape[k]
-    if dense != width:
-        raise ValueError(f"{name}: rows of {width} elements expected, got shape {tuple(shape)}")
-    ld, reach = None, None
-    for i in range(k - 1, -1, -1) if t.numel() else ():
+        dense *= shape[i]
+    ld = reach = None
+    for i in range(len(shape) - 1 - tail, -1, -1):
         if shape[i] == 1:
             continue
         if ld is None:
             ld = reach = stride[i]
         elif stride[i] != reach:
             raise ValueError(f"{name}: rows must lie one stride apart")
-        reach = reach * shape[i]
-    return ctypes.c_void_p(t.data_ptr()), width if ld is None else ld
-
-
-def _f32(t, name, shape=None):
-    import torch
-
-    if t is None:
-        return None
-    if t.dtype != torch.float32:
-        raise TypeError(f"{name} is float32")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
-    return _ptr(t)
+        reach *= shape[i]
+    return t.data_ptr(), width if ld is None else ld
 
 
 def _lead(t, tail, offsets):
-    """(B, T) of a call: a token tensor's leading dimensions [B, T], or [T] with B from the offsets."""
+    """Leading dimensions, B, T and the offsets' pointer of a call whose token tensors are [B, T, ...], or [T, ...] with
+    offsets."""
     import torch
 
-    lead = t.shape[:t.dim() - tail]
+    lead = tuple(t.shape[:-tail])
     if offsets is None:
         if len(lead) != 2:
             raise ValueError("token tensors are [B, T, ...] (or [T, ...] with offsets)")
-        return lead[0], lead[1]
+        return lead, lead[0], lead[1], None
     if len(lead) != 1:
         raise ValueError("with offsets, token tensors are [T, ...]")
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 1:
+    if offsets.dtype is not torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 1:
         raise TypeError("offsets is an int32 tensor of one entry more than sequences")
-    return offsets.numel() - 1, lead[0]
-
-
-def _same(dtype, lead, *named):
-    for name, t, tail in named:
-        if t.dtype != dtype:
-            raise TypeError(f"{name}: all token tensors share one dtype")
-        if tuple(t.shape) != (*lead, *tail):
-            raise ValueError(f"{name}: shape {(*lead, *tail)} expected, got {tuple(t.shape)}")
+    return lead, offsets.shape[0] - 1, lead[0], _dense(offsets, torch.int32, offsets.shape, "offsets")
 
 
 def _workspace(need, like, given):
+    """(tensor, pointer, bytes) of a call's workspace, allocated when none is given and one is needed."""
     import torch
 
-    return given if given is not None else torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
+    if given is None:
+        if not need:
+            return None, None, 0
+        given = torch.empty(need, dtype=torch.uint8, device=like.device)
+    return given, _dense(given, torch.uint8, given.shape, "workspace"), given.shape[0]
+
+
+def _prologue(xbc, delta, conv_weight, conv_bias, a, delta_bias, conv_state, offsets, silu, stream, outs):
+    import torch
+
+    lead, B, T, off = _lead(xbc, 1, offsets)
+    ch, H, dtype, f32 = xbc.shape[-1], delta.shape[-1], xbc.dtype, torch.float32
+    wide, narrow = (*lead, ch), (*lead, H)
+    px, lx = _rows(xbc, dtype, wide, 1, "xbc")
+    pd, ld = _rows(delta, dtype, narrow, 1, "delta")
+    if outs is None:
+        dev = xbc.device
+        outs = (torch.empty(wide, dtype=dtype, device=dev), torch.empty(narrow, dtype=dtype, device=dev),
+                torch.empty(narrow, dtype=dtype, device=dev))
+        ptrs = [t.data_ptr() for t in outs]
+    else:
+        ptrs = [_dense(t, dtype, s, n) for t, s, n in zip(outs, (wide, narrow, narrow), ("u", "step", "g"))]
+    _check(lib.gdn2_ssm_prologue(px, lx, pd, ld, _dense(conv_weight, f32, (ch, 4), "conv_weight"),
+                                 _dense(conv_bias, f32, (ch,), "conv_bias"), _dense(a, f32, (H,), "a"),
+                                 _dense(delta_bias, f32, (H,), "delta_bias"), _dense(conv_state, f32, (B, 3, ch), "conv_state"),
+                                 off, *ptrs, B, T, ch, H, 1 if silu else 0, _dtype_code(xbc), _raw_stream(stream, xbc)),
+           "gdn2_ssm_prologue")
+    return outs
 
 
 def gdn2_ssm_prologue(xbc, delta, conv_weight, conv_bias, a, delta_bias, u, step, g, conv_state=None, offsets=None, *,
@@ -445,48 +487,32 @@ def gdn2_ssm_prologue(xbc, delta, conv_weight, conv_bias, a, delta_bias, u, step
     With offsets (int32 [B + 1], on the device) the sequences are packed and token tensors are [T, ...]. xbc and delta
     may be slices of wider rows.
     """
-    B, T = _lead(xbc, 1, offsets)
-    ch, H = xbc.shape[-1], delta.shape[-1]
-    lead = xbc.shape[:-1]
-    _same(xbc.dtype, lead, ("delta", delta, (H,)), ("u", u, (ch,)), ("step", step, (H,)), ("g", g, (H,)))
-    (px, lx), (pd, ld) = _rows(xbc, ch, "xbc"), _rows(delta, H, "delta")
-    st = lib.gdn2_ssm_prologue(px, lx, pd, ld, _f32(conv_weight, "conv_weight", (ch, 4)), _f32(conv_bias, "conv_bias", (ch,)),
-                               _f32(a, "a", (H,)), _f32(delta_bias, "delta_bias", (H,)),
-                               _f32(conv_state, "conv_state", (B, 3, ch)), _ptr(offsets), _ptr(u), _ptr(step), _ptr(g), B, T,
-                               ch, H, int(bool(silu)), _dtype_code(xbc), _stream(stream))
-    _check(st, "gdn2_ssm_prologue")
-    return u, step, g
+    return _prologue(xbc, delta, conv_weight, conv_bias, a, delta_bias, conv_state, offsets, silu, stream, (u, step, g))
 
 
 def ssm_prologue(xbc, delta, conv_weight, conv_bias, a, delta_bias, conv_state=None, offsets=None, *, silu=True, stream=None):
     """Returns (u, step, g); conv_state, if given, is updated in place."""
-    import torch
-
-    new = lambda t: torch.empty(t.shape, dtype=xbc.dtype, device=xbc.device)
-    return gdn2_ssm_prologue(xbc, delta, conv_weight, conv_bias, a, delta_bias, new(xbc), new(delta), new(delta), conv_state,
-                             offsets, silu=silu, stream=stream)
+    return _prologue(xbc, delta, conv_weight, conv_bias, a, delta_bias, conv_state, offsets, silu, stream, None)
 
 
 def gdn2_ssm_prologue_backward(xbc, delta, conv_weight, conv_bias, a, delta_bias, du, dstep, dg, dxbc, ddelta, dconv_weight,
                                dconv_bias, da, ddelta_bias, offsets=None, *, silu=True, workspace=None, stream=None):
     """Gradients of gdn2_ssm_prologue from zero convolution states (C ABI gdn2_ssm_prologue_backward); writes dxbc,
     ddelta (token dtype; may be slices of wider rows) and the float32 parameter gradients (dconv_bias may be None)."""
-    B, T = _lead(xbc, 1, offsets)
-    ch, H = xbc.shape[-1], delta.shape[-1]
-    _same(xbc.dtype, xbc.shape[:-1], ("delta", delta, (H,)), ("du", du, (ch,)), ("dstep", dstep, (H,)), ("dg", dg, (H,)),
-          ("dxbc", dxbc, (ch,)), ("ddelta", ddelta, (H,)))
-    (px, lx), (pd, ld) = _rows(xbc, ch, "xbc"), _rows(delta, H, "delta")
-    (pu, lu), (po, lo), (pe, le) = _rows(du, ch, "du"), _rows(dxbc, ch, "dxbc"), _rows(ddelta, H, "ddelta")
-    dt = _dtype_code(xbc)
-    ws = _workspace(lib.gdn2_ssm_prologue_backward_workspace_size(B, T, ch, H, int(offsets is not None), dt), xbc, workspace)
-    st = lib.gdn2_ssm_prologue_backward(px, lx, pd, ld, _f32(conv_weight, "conv_weight", (ch, 4)),
-                                        _f32(conv_bias, "conv_bias", (ch,)), _f32(a, "a", (H,)),
-                                        _f32(delta_bias, "delta_bias", (H,)), _ptr(offsets), pu, lu, _ptr(dstep), _ptr(dg),
-                                        po, lo, pe, le, _f32(dconv_weight, "dconv_weight", (ch, 4)),
-                                        _f32(dconv_bias, "dconv_bias", (ch,)), _f32(da, "da", (H,)),
-                                        _f32(ddelta_bias, "ddelta_bias", (H,)), B, T, ch, H, int(bool(silu)), dt, _ptr(ws),
-                                        ws.numel(), _stream(stream))
-    _check(st, "gdn2_ssm_prologue_backward")
+    import torch
+
+    lead, B, T, off = _lead(xbc, 1, offsets)
+    ch, H, dtype, f32 = xbc.shape[-1], delta.shape[-1], xbc.dtype, torch.float32
+    wide, narrow, dt = (*lead, ch), (*lead, H), _dtype_code(xbc)
+    ws, pw, nw = _workspace(_size_of("gdn2_ssm_prologue_backward_workspace_size", B, T, ch, H, int(off is not None), dt), xbc, workspace)
+    _check(lib.gdn2_ssm_prologue_backward(
+        *_rows(xbc, dtype, wide, 1, "xbc"), *_rows(delta, dtype, narrow, 1, "delta"),
+        _dense(conv_weight, f32, (ch, 4), "conv_weight"), _dense(conv_bias, f32, (ch,), "conv_bias"), _dense(a, f32, (H,), "a"),
+        _dense(delta_bias, f32, (H,), "delta_bias"), off, *_rows(du, dtype, wide, 1, "du"), _dense(dstep, dtype, narrow, "dstep"),
+        _dense(dg, dtype, narrow, "dg"), *_rows(dxbc, dtype, wide, 1, "dxbc"), *_rows(ddelta, dtype, narrow, 1, "ddelta"),
+        _dense(dconv_weight, f32, (ch, 4), "dconv_weight"), _dense(dconv_bias, f32, (ch,), "dconv_bias"), _dense(da, f32, (H,), "da"),
+        _dense(ddelta_bias, f32, (H,), "ddelta_bias"), B, T, ch, H, 1 if silu else 0, dt, pw, nw, _raw_stream(stream, xbc)),
+        "gdn2_ssm_prologue_backward")
     return dxbc, ddelta, dconv_weight, dconv_bias, da, ddelta_bias
 
 
@@ -495,17 +521,36 @@ def ssm_prologue_backward(xbc, delta, conv_weight, conv_bias, a, delta_bias, du,
     """Returns (dxbc, ddelta, dconv_weight, dconv_bias or None, da, ddelta_bias)."""
     import torch
 
-    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device) if t is not None else None
+    dev = xbc.device
+    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=dev)
     return gdn2_ssm_prologue_backward(xbc, delta, conv_weight, conv_bias, a, delta_bias, du, dstep, dg, new(xbc), new(delta),
-                                      new(conv_weight), new(conv_bias), new(a), new(delta_bias), offsets, silu=silu,
-                                      stream=stream)
+                                      new(conv_weight), new(conv_bias) if conv_bias is not None else None, new(a),
+                                      new(delta_bias), offsets, silu=silu, stream=stream)
 
 
-def _scan_sizes(x, bm, offsets):
-    B, T = _lead(x, 2, offsets)
+def _scan(x, step, g, bm, cm, d, initial_state, final_state, offsets, path, workspace, stream, y, want_state):
+    import torch
+
+    lead, B, T, off = _lead(x, 2, offsets)
     H, P = x.shape[-2:]
     G, N = bm.shape[-2:]
-    return B, T, H, G, P, N
+    dtype, f32, dt, pth = x.dtype, torch.float32, _dtype_code(x), PATHS[path]
+    full, heads, keys, state = (*lead, H, P), (*lead, H), (*lead, G, N), (B, H, N, P)
+    rx = _rows(x, dtype, full, 2, "x")
+    if y is None:
+        y = torch.empty(full, dtype=dtype, device=x.device)
+        py = y.data_ptr()
+    else:
+        py = _dense(y, dtype, full, "y")
+    if want_state:
+        final_state = torch.empty(state, dtype=f32, device=x.device)
+    ws, pw, nw = _workspace(_size_of("gdn2_ssm_chunk_fwd_workspace_size", pth, B, T, H, G, P, N, int(off is not None), dt), x, workspace)
+    _check(lib.gdn2_ssm_chunk_fwd(
+        pth, *rx, _dense(step, dtype, heads, "step"), _dense(g, dtype, heads, "g"), *_rows(bm, dtype, keys, 2, "bm"),
+        *_rows(cm, dtype, keys, 2, "cm"), _dense(d, f32, (H,), "d"), _dense(initial_state, f32, state, "initial_state"),
+        _dense(final_state, f32, state, "final_state"), off, py, B, T, H, G, P, N, dt, pw, nw, _raw_stream(stream, x)),
+        "gdn2_ssm_chunk_fwd")
+    return y, final_state
 
 
 def gdn2_ssm_chunk_fwd(x, step, g, bm, cm, y, d=None, initial_state=None, final_state=None, offsets=None, *, path="auto",
@@ -517,67 +562,63 @@ def gdn2_ssm_chunk_fwd(x, step, g, bm, cm, y, d=None, initial_state=None, final_
     [B, H, N, P]. With offsets (int32 [B + 1], on the device) the sequences are packed and token tensors are [T, ...].
     x, bm and cm may be slices of wider rows.
     """
-    B, T, H, G, P, N = _scan_sizes(x, bm, offsets)
-    _same(x.dtype, x.shape[:-2], ("step", step, (H,)), ("g", g, (H,)), ("bm", bm, (G, N)), ("cm", cm, (G, N)), ("y", y, (H, P)))
-    (px, lx), (pb, lb), (pc, lc) = _rows(x, H * P, "x"), _rows(bm, G * N, "bm"), _rows(cm, G * N, "cm")
-    dt, packed = _dtype_code(x), int(offsets is not None)
-    ws = _workspace(lib.gdn2_ssm_chunk_fwd_workspace_size(PATHS[path], B, T, H, G, P, N, packed, dt), x, workspace)
-    st = lib.gdn2_ssm_chunk_fwd(PATHS[path], px, lx, _ptr(step), _ptr(g), pb, lb, pc, lc, _f32(d, "d", (H,)),
-                                _f32(initial_state, "initial_state", (B, H, N, P)),
-                                _f32(final_state, "final_state", (B, H, N, P)), _ptr(offsets), _ptr(y), B, T, H, G, P, N, dt,
-                                _ptr(ws), ws.numel(), _stream(stream))
-    _check(st, "gdn2_ssm_chunk_fwd")
-    return y, final_state
+    return _scan(x, step, g, bm, cm, d, initial_state, final_state, offsets, path, workspace, stream, y, False)
 
 
 def ssm_chunk_fwd(x, step, g, bm, cm, d=None, initial_state=None, offsets=None, *, output_final_state=True, path="auto",
                   workspace=None, stream=None):
     """Returns (y, final_state or None)."""
+    return _scan(x, step, g, bm, cm, d, initial_state, None, offsets, path, workspace, stream, None, output_final_state)
+
+
+def _scan_grad(x, step, g, bm, cm, d_y, d, initial_state, d_final_state, offsets, path, workspace, stream, outs):
     import torch
 
-    B, T, H, G, P, N = _scan_sizes(x, bm, offsets)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    fs = torch.empty((B, H, N, P), dtype=torch.float32, device=x.device) if output_final_state else None
-    return gdn2_ssm_chunk_fwd(x, step, g, bm, cm, y, d, initial_state, fs, offsets, path=path, workspace=workspace, stream=stream)
+    lead, B, T, off = _lead(x, 2, offsets)
+    H, P = x.shape[-2:]
+    G, N = bm.shape[-2:]
+    dtype, f32, dt, pth = x.dtype, torch.float32, _dtype_code(x), PATHS[path]
+    full, heads, keys, state = (*lead, H, P), (*lead, H), (*lead, G, N), (B, H, N, P)
+    rx, rb, rc = _rows(x, dtype, full, 2, "x"), _rows(bm, dtype, keys, 2, "bm"), _rows(cm, dtype, keys, 2, "cm")
+    if outs is None:
+        dev, hp, gn = x.device, H * P, G * N
+        ch = hp + 2 * gn
+        row = torch.empty((*lead, ch), dtype=dtype, device=dev)
+        back = (ch,) if off is not None else (T * ch, ch)
+        dx = row.as_strided(full, (*back, P, 1))
+        dbm, dcm = row.as_strided(keys, (*back, N, 1), hp), row.as_strided(keys, (*back, N, 1), hp + gn)
+        dstep, dg = torch.empty(heads, dtype=dtype, device=dev), torch.empty(heads, dtype=dtype, device=dev)
+        dd = torch.empty((H,), dtype=f32, device=dev) if d is not None else None
+        ds0 = torch.empty(state, dtype=f32, device=dev) if initial_state is not None else None
+        outs = (dx, dstep, dg, dbm, dcm, dd, ds0)
+        base, es = row.data_ptr(), row.element_size()
+        ox, ob, oc = (base, ch), (base + es * hp, ch), (base + es * (hp + gn), ch)
+    else:
+        dx, dstep, dg, dbm, dcm, dd, ds0 = outs
+        ox, ob, oc = _rows(dx, dtype, full, 2, "dx"), _rows(dbm, dtype, keys, 2, "dbm"), _rows(dcm, dtype, keys, 2, "dcm")
+    ws, pw, nw = _workspace(_size_of("gdn2_ssm_backward_workspace_size", pth, B, T, H, G, P, N, int(off is not None), dt), x, workspace)
+    _check(lib.gdn2_ssm_backward(
+        pth, *rx, _dense(step, dtype, heads, "step"), _dense(g, dtype, heads, "g"), *rb, *rc, _dense(d, f32, (H,), "d"),
+        _dense(initial_state, f32, state, "initial_state"), *_rows(d_y, dtype, full, 2, "d_y"),
+        _dense(d_final_state, f32, state, "d_final_state"), off, *ox, _dense(dstep, dtype, heads, "dstep"),
+        _dense(dg, dtype, heads, "dg"), *ob, *oc, _dense(dd, f32, (H,), "dd"), _dense(ds0, f32, state, "d_initial_state"),
+        B, T, H, G, P, N, dt, pw, nw, _raw_stream(stream, x)), "gdn2_ssm_backward")
+    return outs
 
 
 def gdn2_ssm_backward(x, step, g, bm, cm, d_y, dx, dstep, dg, dbm, dcm, dd=None, d=None, initial_state=None,
                       d_final_state=None, d_initial_state=None, offsets=None, *, path="auto", workspace=None, stream=None):
     """Gradients of gdn2_ssm_chunk_fwd (C ABI gdn2_ssm_backward); writes dx, dstep, dg, dbm, dcm (token dtype; dx, dbm
     and dcm may be slices of wider rows) and, if given, the float32 dd and d_initial_state."""
-    B, T, H, G, P, N = _scan_sizes(x, bm, offsets)
-    _same(x.dtype, x.shape[:-2], ("step", step, (H,)), ("g", g, (H,)), ("bm", bm, (G, N)), ("cm", cm, (G, N)),
-          ("d_y", d_y, (H, P)), ("dx", dx, (H, P)), ("dstep", dstep, (H,)), ("dg", dg, (H,)), ("dbm", dbm, (G, N)),
-          ("dcm", dcm, (G, N)))
-    r = [_rows(t, w, n) for t, w, n in ((x, H * P, "x"), (bm, G * N, "bm"), (cm, G * N, "cm"), (d_y, H * P, "d_y"),
-                                       (dx, H * P, "dx"), (dbm, G * N, "dbm"), (dcm, G * N, "dcm"))]
-    st4 = (B, H, N, P)
-    dt, packed = _dtype_code(x), int(offsets is not None)
-    ws = _workspace(lib.gdn2_ssm_backward_workspace_size(PATHS[path], B, T, H, G, P, N, packed, dt), x, workspace)
-    st = lib.gdn2_ssm_backward(PATHS[path], *r[0], _ptr(step), _ptr(g), *r[1], *r[2], _f32(d, "d", (H,)),
-                               _f32(initial_state, "initial_state", st4), *r[3], _f32(d_final_state, "d_final_state", st4),
-                               _ptr(offsets), *r[4], _ptr(dstep), _ptr(dg), *r[5], *r[6], _f32(dd, "dd", (H,)),
-                               _f32(d_initial_state, "d_initial_state", st4), B, T, H, G, P, N, dt, _ptr(ws), ws.numel(),
-                               _stream(stream))
-    _check(st, "gdn2_ssm_backward")
-    return dx, dstep, dg, dbm, dcm, dd, d_initial_state
+    return _scan_grad(x, step, g, bm, cm, d_y, d, initial_state, d_final_state, offsets, path, workspace, stream,
+                      (dx, dstep, dg, dbm, dcm, dd, d_initial_state))
 
 
 def ssm_backward(x, step, g, bm, cm, d_y, d=None, initial_state=None, d_final_state=None, offsets=None, *, path="auto",
                  workspace=None, stream=None):
     """Returns (dx, dstep, dg, dbm, dcm, dd, d_initial_state); dd is None without d, d_initial_state without initial_state.
     dx, dbm and dcm are slices of one row [..., H * P + 2 * G * N], the layout of the prologue's u and du."""
-    import torch
-
-    B, T, H, G, P, N = _scan_sizes(x, bm, offsets)
-    new = lambda shape, dt=x.dtype: torch.empty(shape, dtype=dt, device=x.device)
-    row = new((*x.shape[:-2], H * P + 2 * G * N))
-    dx, db, dc = row[..., :H * P], row[..., H * P:H * P + G * N], row[..., H * P + G * N:]
-    return gdn2_ssm_backward(x, step, g, bm, cm, d_y, dx.unflatten(-1, (H, P)), new(step.shape), new(g.shape),
-                             db.unflatten(-1, (G, N)), dc.unflatten(-1, (G, N)),
-                             new((H,), torch.float32) if d is not None else None, d, initial_state, d_final_state,
-                             new((B, H, N, P), torch.float32) if initial_state is not None else None, offsets, path=path,
-                             workspace=workspace, stream=stream)
+    return _scan_grad(x, step, g, bm, cm, d_y, d, initial_state, d_final_state, offsets, path, workspace, stream, None)
 
 
 def gdn2_ssm_decode_step(xbc, delta, conv_weight, conv_bias, a, delta_bias, d, conv_state, state, y, slots=None, *, stream=None):
@@ -597,36 +638,37 @@ def gdn2_ssm_decode_step(xbc, delta, conv_weight, conv_bias, a, delta_bias, d, c
         raise ValueError("xbc holds H * P + 2 * G * N channels")
     if slots is None and rows != B:
         raise ValueError("without slots, the states have one row per sequence")
-    if slots is not None and (slots.dtype != torch.int32 or tuple(slots.shape) != (B,)):
-        raise TypeError("slots is int32 [B]")
-    _same(xbc.dtype, (B,), ("delta", delta, (H,)), ("y", y, (H, P)))
-    (px, lx), (pd, ld) = _rows(xbc, ch, "xbc"), _rows(delta, H, "delta")
-    st = lib.gdn2_ssm_decode_step(px, lx, pd, ld, _f32(conv_weight, "conv_weight", (ch, 4)), _f32(conv_bias, "conv_bias", (ch,)),
-                                  _f32(a, "a", (H,)), _f32(delta_bias, "delta_bias", (H,)), _f32(d, "d", (H,)),
-                                  _f32(conv_state, "conv_state", (rows, 3, ch)), _ptr(state), _dtype_code(state), _ptr(slots),
-                                  rows if slots is not None else 0, _ptr(y), B, H, G, P, N, _dtype_code(xbc), _stream(stream))
-    _check(st, "gdn2_ssm_decode_step")
+    dtype, f32 = xbc.dtype, torch.float32
+    if y is None:
+        y = torch.empty((B, H, P), dtype=dtype, device=xbc.device)
+    _check(lib.gdn2_ssm_decode_step(
+        *_rows(xbc, dtype, (B, ch), 1, "xbc"), *_rows(delta, dtype, (B, H), 1, "delta"), _dense(conv_weight, f32, (ch, 4), "conv_weight"),
+        _dense(conv_bias, f32, (ch,), "conv_bias"), _dense(a, f32, (H,), "a"), _dense(delta_bias, f32, (H,), "delta_bias"),
+        _dense(d, f32, (H,), "d"), _dense(conv_state, f32, (rows, 3, ch), "conv_state"), _dense(state, state.dtype, state.shape, "state"),
+        _dtype_code(state), _dense(slots, torch.int32, (B,), "slots"), rows if slots is not None else 0,
+        _dense(y, dtype, (B, H, P), "y"), B, H, G, P, N, _dtype_code(xbc), _raw_stream(stream, xbc)), "gdn2_ssm_decode_step")
     return y
 
 
 def ssm_decode_step(xbc, delta, conv_weight, conv_bias, a, delta_bias, d, conv_state, state, slots=None, *, stream=None):
     """Returns y [B, H, P]; conv_state and state are updated in place. Rows of inactive slots are left unwritten."""
-    import torch
-
-    y = torch.empty((xbc.shape[0], state.shape[1], state.shape[3]), dtype=xbc.dtype, device=xbc.device)
-    return gdn2_ssm_decode_step(xbc, delta, conv_weight, conv_bias, a, delta_bias, d, conv_state, state, y, slots, stream=stream)
+    return gdn2_ssm_decode_step(xbc, delta, conv_weight, conv_bias, a, delta_bias, d, conv_state, state, None, slots, stream=stream)
 
 
 def gdn2_block_norm(x, z, post_weight, residual, scale, pre_weight, r, n, *, groups=1, eps=1e-5, stream=None):
     """The residual stream around a block (C ABI gdn2_block_norm): p = post_weight * t / rms_group(t) with
     t = x silu(z), r = residual + scale p, n = pre_weight * r / rms(r). z, post_weight, residual, scale and pre_weight
     may each be None; r may be None when n is wanted alone. x, z, residual, r, n: [..., d]; weights: float32 [d]."""
-    dim = x.shape[-1]
-    _same(x.dtype, x.shape[:-1], *((k, t, (dim,)) for k, t in (("z", z), ("residual", residual), ("r", r), ("n", n)) if t is not None))
-    st = lib.gdn2_block_norm(_ptr(x), _ptr(z), _f32(post_weight, "post_weight", (dim,)), _ptr(residual),
-                             _f32(scale, "scale", (dim,)), _f32(pre_weight, "pre_weight", (dim,)), _ptr(r), _ptr(n),
-                             x.numel() // dim if dim else 0, dim, groups, float(eps), _dtype_code(x), _stream(stream))
-    _check(st, "gdn2_block_norm")
+    import torch
+
+    shape, dtype, f32 = x.shape, x.dtype, torch.float32
+    dim = shape[-1]
+    vec = (dim,)
+    _check(lib.gdn2_block_norm(
+        _dense(x, dtype, shape, "x"), _dense(z, dtype, shape, "z"), _dense(post_weight, f32, vec, "post_weight"),
+        _dense(residual, dtype, shape, "residual"), _dense(scale, f32, vec, "scale"), _dense(pre_weight, f32, vec, "pre_weight"),
+        _dense(r, dtype, shape, "r"), _dense(n, dtype, shape, "n"), x.numel() // dim if dim else 0, dim, groups, float(eps),
+        _dtype_code(x), _raw_stream(stream, x)), "gdn2_block_norm")
     return r, n
 
 
@@ -644,18 +686,19 @@ def gdn2_block_norm_backward(x, z, post_weight, residual, scale, pre_weight, d_r
                              dpre_weight, *, groups=1, eps=1e-5, workspace=None, stream=None):
     """Gradients of gdn2_block_norm (C ABI gdn2_block_norm_backward) given those of r (d_r, or None) and n (d_n, with
     pre_weight): one output for each input given; dresidual may be None."""
-    dim = x.shape[-1]
-    rows = x.numel() // dim if dim else 0
-    _same(x.dtype, x.shape[:-1], *((k, t, (dim,)) for k, t in (("z", z), ("residual", residual), ("d_r", d_r), ("d_n", d_n),
-                                                              ("dx", dx), ("dz", dz), ("dresidual", dresidual)) if t is not None))
-    ws = _workspace(lib.gdn2_block_norm_backward_workspace_size(rows, dim), x, workspace)
-    f = lambda t, k: _f32(t, k, (dim,))
-    st = lib.gdn2_block_norm_backward(_ptr(x), _ptr(z), f(post_weight, "post_weight"), _ptr(residual), f(scale, "scale"),
-                                      f(pre_weight, "pre_weight"), _ptr(d_r), _ptr(d_n), _ptr(dx), _ptr(dz),
-                                      f(dpost_weight, "dpost_weight"), _ptr(dresidual), f(dscale, "dscale"),
-                                      f(dpre_weight, "dpre_weight"), rows, dim, groups, float(eps), _dtype_code(x), _ptr(ws),
-                                      ws.numel(), _stream(stream))
-    _check(st, "gdn2_block_norm_backward")
+    import torch
+
+    shape, dtype, f32 = x.shape, x.dtype, torch.float32
+    dim = shape[-1]
+    rows, vec = x.numel() // dim if dim else 0, (dim,)
+    ws, pw, nw = _workspace(_size_of("gdn2_block_norm_backward_workspace_size", rows, dim), x, workspace)
+    tok = lambda t, k: _dense(t, dtype, shape, k)
+    par = lambda t, k: _dense(t, f32, vec, k)
+    _check(lib.gdn2_block_norm_backward(
+        tok(x, "x"), tok(z, "z"), par(post_weight, "post_weight"), tok(residual, "residual"), par(scale, "scale"),
+        par(pre_weight, "pre_weight"), tok(d_r, "d_r"), tok(d_n, "d_n"), tok(dx, "dx"), tok(dz, "dz"),
+        par(dpost_weight, "dpost_weight"), tok(dresidual, "dresidual"), par(dscale, "dscale"), par(dpre_weight, "dpre_weight"),
+        rows, dim, groups, float(eps), _dtype_code(x), pw, nw, _raw_stream(stream, x)), "gdn2_block_norm_backward")
     return dx, dz, dpost_weight, dresidual, dscale, dpre_weight
 
 

@@ -17,29 +17,34 @@ namespace {
 constexpr int kQ = 128;   // tokens per chunk
 constexpr int kCols = 64; // value columns per block
 
-// shared memory (byte offsets from a 1024-aligned base); tiles are [128 rows][64 bf16], 128-byte swizzle
-namespace so {
-constexpr uint32_t kTile = 16384;
-constexpr uint32_t B = 0;                    // 2 stages x 2 tiles (n 0-63, 64-127)
-constexpr uint32_t C = B + 4 * kTile;        // 2 x 2
-constexpr uint32_t X = C + 4 * kTile;        // 2; Y replaces X for its store
-constexpr uint32_t XW = X + 2 * kTile;       // 2 buffers of X~ parts
-constexpr uint32_t HB = XW + 2 * kTile;      // the state as a bf16 operand
-constexpr uint32_t GATE = HB + kTile;        // 2 stages x {L, col, wend, step} [128] fp32
-constexpr uint32_t kGateStage = 4 * 512;
-constexpr uint32_t BAR = GATE + 2 * kGateStage;
-constexpr uint32_t TOTAL = BAR + 256;
-}  // namespace so
-static_assert(so::TOTAL + 1024 <= 232448, "scan kernel shared memory");
+// Shared memory (byte offsets from a 1024-aligned base); tiles are [128 rows][64 bf16], 128-byte swizzle. With one
+// part of X~ per chunk its buffer is single and X has three stages (a stage is free only when Y has left
+// through it, the longest way of all); with three parts, two buffers and two stages fill the same room.
+template <int kParts>
+struct So {
+    static constexpr uint32_t kTile = 16384;
+    static constexpr int kXS = kParts == 1 ? 3 : 2, kXB = kParts == 1 ? 1 : 2;
+    static constexpr uint32_t B = 0;                  // 2 stages x 2 tiles (n 0-63, 64-127)
+    static constexpr uint32_t C = B + 4 * kTile;      // 2 x 2
+    static constexpr uint32_t X = C + 4 * kTile;      // kXS; Y replaces X for its store
+    static constexpr uint32_t XW = X + kXS * kTile;   // kXB buffers of X~ parts
+    static constexpr uint32_t HB = XW + kXB * kTile;  // the state as a bf16 operand
+    static constexpr uint32_t kGateStage = 4 * 512;   // {L, col, wend, step} [128] fp32, a stage per stage of X
+    static constexpr uint32_t GATE = HB + kTile;
+    static constexpr uint32_t BAR = GATE + kXS * kGateStage;
+    static constexpr uint32_t TOTAL = BAR + 256;
+    static_assert(TOTAL + 1024 <= 232448, "scan kernel shared memory");
+};
 
 enum Bar {
-    kFull = 0, kFullX = 2, kReady = 4, kBcEmpty = 6, kXEmpty = 8, kSFull = 10, kSEmpty = 12, kXwReady = 14, kXwFree = 16,
-    kMReady = 18, kYFull, kYEmpty, kDFull, kDEmpty, kHReady, kHFree, kDrain, kBars
+    kFull = 0, kFullX = 2, kReady = 5, kBcEmpty = 8, kXEmpty = 10, kSFull = 13, kXwReady = 15, kXwFree = 17,
+    kMReady = 19, kYFull, kYEmpty, kDFull, kDEmpty, kHReady, kHFree, kDrain, kBars
 };
 static_assert(kBars * 8 + 16 <= 256, "barrier room");
 
-// tensor-memory columns
-constexpr uint32_t kTS = 0, kTM = 256, kTYi = 320, kTYx = 384, kTD = 448;
+// tensor-memory columns: scores of two chunks, each half replaced by M (16 packed columns at the start of every
+// 32); then Y's two sums and the state's increment
+constexpr uint32_t kTS = 0, kTYi = 256, kTYx = 320, kTD = 384;
 
 struct ScanMaps {
     CUtensorMap x, b, c, y;
@@ -61,6 +66,53 @@ struct ScanTcArgs {
 
 __device__ __forceinline__ float4 exp2_4(float4 v) {
     return make_float4(ex2_approx(v.x), ex2_approx(v.y), ex2_approx(v.z), ex2_approx(v.w));
+}
+
+// Bounded wait on a barrier's phase by a converged warp: the first try inline, the loop out of line (inlined at
+// every wait it made half of the kernel's code). The outcome is the warp's; a warp that gives up records it.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, long long lim, volatile int* err) {
+    return warp_wait(reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(bar)), parity, lim, err);
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, long long lim, volatile int* err) {
+    if (__all_sync(0xffffffffu, lim > 0 && mbar_try_wait(bar, parity))) return true;
+    return wait_on(smem_u32(bar), parity, lim, err);
+}
+
+// One elected lane of a converged warp issues; the operands are warp-uniform, so that descriptors advance
+// in uniform registers (an `if (lane == 0)` around the loop made every product of 8 steps take 1200 cycles to issue).
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+    return e;
+}
+// A value that is the same in all lanes, in a form that the compiler knows to be.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// Shared-memory descriptor: the constant upper word (stride 1024, version, 128-byte swizzle) and the lower one, which
+// holds the start address and the leading offset and advances by plain addition of bytes / 16 (no carry out of
+// the 14-bit address: shared memory ends below 256 KB).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr & 0x3FFFFu) >> 4) | (lbo >> 4 << 16); }
+
+__device__ __forceinline__ void mma_by(uint32_t lead, uint32_t d, uint32_t ad, uint32_t bd, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p, e;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n mov.b64 a, {%1, %6};\n"
+        " mov.b64 b, {%2, %6};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d), "r"(ad), "r"(bd), "r"(id),
+        "r"(acc), "r"(lead), "r"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_by(uint32_t lead, uint32_t d, uint32_t at, uint32_t bd, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p, e;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n mov.b64 b, {%2, %6};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d), "r"(at), "r"(bd), "r"(id), "r"(acc), "r"(lead),
+        "r"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void commit_by(uint32_t lead, uint64_t* bar) {
+    asm volatile(
+        "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)), "r"(lead)
+        : "memory");
 }
 
 // Gate arrays of one chunk, by one warp, four tokens per lane: L and the decay sums in units of log 2.
@@ -96,6 +148,7 @@ __device__ __forceinline__ void gate_arrays(float* arr, int lane, const float (&
 // (2^-24 of every term) where it is returned in fp32.
 template <int kParts>
 __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__ ScanMaps maps, const ScanTcArgs a) {
+    using so = So<kParts>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
@@ -106,11 +159,13 @@ __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__
     const int pb = a.P / kCols, h = blockIdx.x / pb, p0 = (blockIdx.x - h * pb) * kCols, grp = h / (a.H / a.G);
     Unit u;
     if (!find_unit(a.seqs, a.unit, blockIdx.y, u)) return;
+    u.len = uniform(u.len);
+    u.row = uniform(u.row);
     const int NC = (u.len + kQ - 1) / kQ;
     const long long lim = a.wait_ns;
 
     if (tid == 0) {
-        const int counts[kBars] = {1, 1, 1, 1, 1, 1, 1, 1, 4, 4, 1, 1, 4, 4, 4, 4, 1, 1, 4, 1, 4, 1, 4, 4, 1, 1};
+        const int counts[kBars] = {1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 4, 4, 4, 1, 1, 4, 4, 1, 1, 4, 1, 4, 1, 4, 4, 1, 1};
         for (int i = 0; i < kBars; ++i) mbar_init(bars + i, counts[i]);
         *err = 0;
         fence_mbar_init();
@@ -122,7 +177,7 @@ __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    constexpr uint32_t tmem = 0;  // all 512 columns: the allocation starts at column 0
     const int ks = a.N / 16;  // K steps over the state size
     const size_t plane = static_cast<size_t>(a.N) * a.P;
 
@@ -133,10 +188,11 @@ __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__
             const int full = bc ? kFull : kFullX, empty = bc ? kBcEmpty : kXEmpty, halves = a.N / 64;
             prefetch_tensormap(bc ? &maps.b : &maps.x);
             if (bc) prefetch_tensormap(&maps.c);
-            int issued = 0;
+            const int stages = bc ? 2 : so::kXS;
+            int issued = 0, st = 0;
+            uint32_t ph = 0;
             for (int c = 0; c < NC; ++c) {
-                const int st = c & 1;
-                if (c >= 2 && !mbar_wait_or_abort(bars + empty + st, ((c >> 1) & 1) ^ 1, lim, err)) {
+                if (c >= stages && !mbar_wait_or_abort(bars + empty + st, ph ^ 1, lim, err)) {
                     note_failure(err);
                     break;
                 }
@@ -153,74 +209,87 @@ __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__
                     tma_load_3d(sm + so::X + st * so::kTile, &maps.x, p0, h, row, bar);
                 }
                 issued = c + 1;
+                if (++st == stages) {
+                    st = 0;
+                    ph ^= 1;
+                }
             }
-            for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c)  // nothing in flight when the block ends
-                mbar_wait(bars + full + (c & 1), (c >> 1) & 1, kDefaultWaitNs);
+            for (int c = issued > stages ? issued - stages : 0; c < issued; ++c)  // nothing in flight when the block ends
+                mbar_wait(bars + full + c % stages, (c / stages) & 1, kDefaultWaitNs);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t id_s = idesc_bf16(128, 128, false, false), id_d = idesc_bf16(128, 64, true, true),
-                           id_x = idesc_bf16(128, 64, false, true), id_i = idesc_bf16(128, 64, false, true);
-            bool ok = true;
-            auto wait = [&](int bar, uint32_t parity) {
-                if (!mbar_wait_or_abort(bars + bar, parity, lim, err)) {
-                    note_failure(err);
-                    return false;
-                }
-                tc_fence_after();
-                return true;
-            };
-            auto scores = [&](int c) {
-                const int st = c & 1;
-                const uint32_t ph = (c >> 1) & 1;
-                if (!wait(kFull + st, ph)) return false;
-                if (u.len - c * kQ < kQ && !wait(kReady + st, ph)) return false;  // a short chunk's rows of B are cleared first
-                if (c >= 2 && !wait(kSEmpty + st, ph ^ 1)) return false;
-                const uint32_t ca = sb + so::C + 2 * st * so::kTile, ba = sb + so::B + 2 * st * so::kTile;
-                for (int s = 0; s < ks; ++s) {
-                    const uint32_t off = (s >> 2) * so::kTile + (s & 3) * 32;
-                    mma_bf16(tmem + kTS + 128 * st, smem_desc(ca + off, 16, 1024, kSwizzle128B),
-                             smem_desc(ba + off, 16, 1024, kSwizzle128B), id_s, s > 0);
-                }
-                mma_commit(bars + kSFull + st);
-                return true;
-            };
-            ok = NC > 0 && scores(0);
-            for (int c = 0; ok && c < NC; ++c) {
-                const int st = c & 1;
-                const uint32_t ph1 = c & 1;  // phase of the barriers used once per chunk
-                if (c + 1 < NC && !(ok = scores(c + 1))) break;
-                // state increment
-                if (c >= 1 && !(ok = wait(kDEmpty, ph1 ^ 1))) break;
-                for (int k = 0; ok && k < kParts; ++k) {
-                    const int seq = c * kParts + k, buf = seq & 1;
-                    if (!(ok = wait(kXwReady + buf, (seq >> 1) & 1))) break;
-                    const uint32_t ba = sb + so::B + 2 * st * so::kTile, xa = sb + so::XW + buf * so::kTile;
-                    for (int s = 0; s < 8; ++s)
-                        mma_bf16(tmem + kTD, smem_desc(ba + s * 2048, so::kTile, 1024, kSwizzle128B),
-                                 smem_desc(xa + s * 2048, so::kTile, 1024, kSwizzle128B), id_d, k > 0 || s > 0);
-                    mma_commit(bars + kXwFree + buf);
-                }
-                if (!ok) break;
-                mma_commit(bars + kDFull);
-                // readout of the state
-                if (!(ok = wait(kHReady, ph1))) break;
-                if (c >= 1 && !(ok = wait(kYEmpty, ph1 ^ 1))) break;
-                for (int s = 0; s < ks; ++s)
-                    mma_bf16(tmem + kTYx, smem_desc(sb + so::C + 2 * st * so::kTile + (s >> 2) * so::kTile + (s & 3) * 32, 16, 1024, kSwizzle128B),
-                             smem_desc(sb + so::HB + s * 2048, so::kTile, 1024, kSwizzle128B), id_x, s > 0);
-                mma_commit(bars + kBcEmpty + st);
-                mma_commit(bars + kHFree);
-                // within the chunk
-                if (!(ok = wait(kFullX + st, (c >> 1) & 1) && wait(kReady + st, (c >> 1) & 1) && wait(kMReady, ph1))) break;
-                for (int s = 0; s < 8; ++s)
-                    mma_bf16_ts(tmem + kTYi, tmem + kTM + 8 * s, smem_desc(sb + so::X + st * so::kTile + s * 2048, so::kTile, 1024, kSwizzle128B),
-                                id_i, s > 0);
-                mma_commit(bars + kYFull);
+        const uint32_t id_s = idesc_bf16(128, 128, false, false), id_d = idesc_bf16(128, 64, true, true),
+                       id_x = idesc_bf16(128, 64, false, true);
+        const uint32_t lead = elect_one();
+        // K-major tiles: 16 channels are 32 bytes of a row, the next 64 the next tile. MN-major: 16 tokens (or
+        // state rows) are 16 rows of 128 bytes.
+        const uint32_t dk = uniform(desc_lo(sb, 16)), dm = uniform(desc_lo(sb, so::kTile));
+        bool ok = NC > 0;
+        auto wait = [&](int bar, uint32_t parity) {
+            const bool w = wait_bar(bars + bar, parity, lim, err);
+            tc_fence_after();
+            return w;
+        };
+        auto scores = [&](int c) {
+            const int st = c & 1;
+            const uint32_t ph = (c >> 1) & 1;
+            if (!wait(kFull + st, ph)) return false;
+            if (u.len - c * kQ < kQ && !wait(kReady + c % so::kXS, (c / so::kXS) & 1)) return false;  // a short chunk's rows of B are cleared first
+            if (c >= 2 && !wait(kYFull, c & 1)) return false;  // M of two chunks before, in the same columns, has been used
+            const uint32_t ca = dk + ((so::C + 2 * st * so::kTile) >> 4), ba = dk + ((so::B + 2 * st * so::kTile) >> 4);
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const uint32_t off = (s >> 2) * so::kTile + (s & 3) * 32;
+                if (s < ks) mma_by(lead, kTS + 128 * st, ca + ((off) >> 4), ba + ((off) >> 4), id_s, s > 0);
             }
-            mma_commit(bars + kDrain);
-            mbar_wait(bars + kDrain, 0, kDefaultWaitNs);
+            commit_by(lead, bars + kSFull + st);
+            return true;
+        };
+        ok = ok && scores(0);
+        int xs = 0;
+        uint32_t xph = 0;
+        for (int c = 0; ok && c < NC; ++c) {
+            const int st = c & 1;
+            const uint32_t ph1 = c & 1;  // phase of the barriers used once per chunk
+            // state increment
+            if (c >= 1 && !(ok = wait(kDEmpty, ph1 ^ 1))) break;
+            const uint32_t bm = dm + ((so::B + 2 * st * so::kTile) >> 4);
+            for (int k = 0; ok && k < kParts; ++k) {
+                const int seq = c * kParts + k, buf = seq % so::kXB;
+                if (!(ok = wait(kXwReady + buf, (seq / so::kXB) & 1))) break;
+                const uint32_t xa = dm + ((so::XW + buf * so::kTile) >> 4);
+#pragma unroll
+                for (int s = 0; s < 8; ++s) mma_by(lead, kTD, bm + ((s * 2048) >> 4), xa + ((s * 2048) >> 4), id_d, k > 0 || s > 0);
+                commit_by(lead, bars + kXwFree + buf);
+            }
+            if (!ok) break;
+            commit_by(lead, bars + kDFull);
+            // readout of the state
+            if (!(ok = wait(kHReady, ph1))) break;
+            if (c >= 1 && !(ok = wait(kYEmpty, ph1 ^ 1))) break;
+            const uint32_t ck = dk + ((so::C + 2 * st * so::kTile) >> 4), hb = dm + ((so::HB) >> 4);
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                if (s < ks) mma_by(lead, kTYx, ck + (((s >> 2) * so::kTile + (s & 3) * 32) >> 4), hb + ((s * 2048) >> 4), id_x, s > 0);
+            commit_by(lead, bars + kBcEmpty + st);
+            commit_by(lead, bars + kHFree);
+            // The next chunk's scores go in here: their tiles were asked for when the chunk before this one was
+            // read out, and M of the next chunk can start while this one's is still used.
+            if (c + 1 < NC && !(ok = scores(c + 1))) break;
+            // within the chunk
+            if (!(ok = wait(kFullX + xs, xph) && wait(kReady + xs, xph) && wait(kMReady, ph1))) break;
+            const uint32_t xm = dm + ((so::X + xs * so::kTile) >> 4);
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                mma_ts_by(lead, kTYi, kTS + 128 * st + 32 * (s >> 1) + 8 * (s & 1), xm + ((s * 2048) >> 4), id_x, s > 0);
+            commit_by(lead, bars + kYFull);
+            if (++xs == so::kXS) {
+                xs = 0;
+                xph ^= 1;
+            }
         }
+        commit_by(lead, bars + kDrain);
+        mbar_wait(bars + kDrain, 0, kDefaultWaitNs);
     } else if (warp == 2) {
         // gates of the next chunk are in registers before this chunk's are due
         float gn[4], sn[4];
@@ -235,87 +304,83 @@ __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__
         };
         if (NC > 0) fetch(0);
         for (int c = 0; c < NC; ++c) {
-            const int st = c & 1;
-            if (!warp_wait(bars + kFull + st, (c >> 1) & 1, lim, err)) break;
-            // the tail's rows of X are cleared here too; and X's arrival says that the arrays' readers are done
-            if (!warp_wait(bars + kFullX + st, (c >> 1) & 1, lim, err)) break;
-            gate_arrays(reinterpret_cast<float*>(sm + so::GATE + st * so::kGateStage), lane, gn, sn);
+            const int st = c & 1, xs = c % so::kXS;
+            // X's arrival says that the arrays of its stage have been read (Y, the last reader, frees both)
+            if (!wait_bar(bars + kFullX + xs, (c / so::kXS) & 1, lim, err)) break;
+            gate_arrays(reinterpret_cast<float*>(sm + so::GATE + xs * so::kGateStage), lane, gn, sn);
             const int n = u.len - c * kQ;
             if (n < kQ) {
+                if (!wait_bar(bars + kFull + st, (c >> 1) & 1, lim, err)) break;
                 // the rows past the sequence hold other tokens: zeros, so that not even their NaN enters a sum
                 const uint4 z = make_uint4(0, 0, 0, 0);
                 for (int i = n * 8 + lane; i < kQ * 8; i += 32) {
                     reinterpret_cast<uint4*>(sm + so::B + 2 * st * so::kTile)[i] = z;
                     reinterpret_cast<uint4*>(sm + so::B + (2 * st + 1) * so::kTile)[i] = z;
-                    reinterpret_cast<uint4*>(sm + so::X + st * so::kTile)[i] = z;
+                    reinterpret_cast<uint4*>(sm + so::X + xs * so::kTile)[i] = z;
                 }
                 fence_proxy_async_smem();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive1(bars + kReady + st);
+            if (lane == 0) mbar_arrive1(bars + kReady + xs);
             if (c + 1 < NC) fetch(c + 1);
         }
     } else if (warp >= 4 && warp < 8) {
-        // ---- M: row i of the chunk per thread; blocks of 32 columns. Below the diagonal block the decay
-        // factors through the end of the column's block (both factors <= 1), one exponential per row and
-        // block; on it, one per entry. Blocks above stay the zeros written here.
+        // ---- M: row i of the chunk per thread, in place of the scores; blocks of 32 columns. Below the diagonal
+        // block the decay factors through the end of the column's block (both factors <= 1), one
+        // exponential per row and block; on it, one per entry; above it, zeros. The loops of all roles stay
+        // rolled: unrolled, the roles' bodies together overran the instruction cache and fetching them was
+        // the longest stall (a chunk took 9400 cycles).
         const int q = warp & 3, i = 32 * q + lane;
         const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
-        {
-            const uint32_t z[16] = {};
-            for (int b = q + 1; b < 4; ++b) tmem_st16(tmem + lane_base + kTM + 16 * b, z);
-            tmem_st_wait();
-        }
         for (int c = 0; c < NC; ++c) {
             const int st = c & 1;
             const uint32_t ph = (c >> 1) & 1;
-            if (!warp_wait(bars + kReady + st, ph, lim, err)) break;
-            if (!warp_wait(bars + kSFull + st, ph, lim, err)) break;
+            const int xs = c % so::kXS;
+            if (!wait_bar(bars + kReady + xs, (c / so::kXS) & 1, lim, err)) break;
+            if (!wait_bar(bars + kSFull + st, ph, lim, err)) break;
             tc_fence_after();
-            const float* arr = reinterpret_cast<const float*>(sm + so::GATE + st * so::kGateStage);
+            const float* arr = reinterpret_cast<const float*>(sm + so::GATE + xs * so::kGateStage);
             const float Li = arr[i];
-            uint32_t m[4][16];
-#pragma unroll
+            const uint32_t at = tmem + lane_base + kTS + 128 * st;
+#pragma unroll 1
             for (int b = 0; b < 4; ++b) {
-                if (b > q) continue;
-                float x[32];
-                tmem_ld_cols<2>(tmem + lane_base + kTS + 128 * st + 32 * b, x);
-                if (b == q) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive1(bars + kSEmpty + st);
+                uint32_t m[16];
+                if (b > q) {
 #pragma unroll
-                    for (int j4 = 0; j4 < 8; ++j4) {
-                        const float4 L = *reinterpret_cast<const float4*>(arr + 32 * b + 4 * j4);
-                        const float4 s = *reinterpret_cast<const float4*>(arr + 384 + 32 * b + 4 * j4);
-                        const float l4[4] = {L.x, L.y, L.z, L.w}, s4[4] = {s.x, s.y, s.z, s.w};
-                        float v[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float w = ex2_approx(Li - l4[e]) * s4[e];
-                            v[e] = 4 * j4 + e <= lane ? x[4 * j4 + e] * w : 0.f;
-                        }
-                        m[b][2 * j4] = pack_bf16x2(v[0], v[1]);
-                        m[b][2 * j4 + 1] = pack_bf16x2(v[2], v[3]);
-                    }
+                    for (int k = 0; k < 16; ++k) m[k] = 0;
                 } else {
-                    const float rf = ex2_approx(Li - arr[32 * b + 31]);
-                    const uint64_t rf2 = f32x2(rf, rf);
+                    float x[32];
+                    tmem_ld_cols<2>(at + 32 * b, x);
+                    if (b == q) {
 #pragma unroll
-                    for (int j4 = 0; j4 < 8; ++j4) {
-                        const float4 cf = *reinterpret_cast<const float4*>(arr + 128 + 32 * b + 4 * j4);
-                        const uint64_t v0 = mul_f32x2(mul_f32x2(f32x2(x[4 * j4], x[4 * j4 + 1]), rf2), f32x2(cf.x, cf.y));
-                        const uint64_t v1 = mul_f32x2(mul_f32x2(f32x2(x[4 * j4 + 2], x[4 * j4 + 3]), rf2), f32x2(cf.z, cf.w));
-                        m[b][2 * j4] = bf16x2_narrow(v0);
-                        m[b][2 * j4 + 1] = bf16x2_narrow(v1);
+                        for (int j4 = 0; j4 < 8; ++j4) {
+                            const float4 L = *reinterpret_cast<const float4*>(arr + 32 * b + 4 * j4);
+                            const float4 s = *reinterpret_cast<const float4*>(arr + 384 + 32 * b + 4 * j4);
+                            const float l4[4] = {L.x, L.y, L.z, L.w}, s4[4] = {s.x, s.y, s.z, s.w};
+                            float v[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float w = ex2_approx(Li - l4[e]) * s4[e];
+                                v[e] = 4 * j4 + e <= lane ? x[4 * j4 + e] * w : 0.f;
+                            }
+                            m[2 * j4] = pack_bf16x2(v[0], v[1]);
+                            m[2 * j4 + 1] = pack_bf16x2(v[2], v[3]);
+                        }
+                    } else {
+                        const float rf = ex2_approx(Li - arr[32 * b + 31]);
+                        const uint64_t rf2 = f32x2(rf, rf);
+#pragma unroll
+                        for (int j4 = 0; j4 < 8; ++j4) {
+                            const float4 cf = *reinterpret_cast<const float4*>(arr + 128 + 32 * b + 4 * j4);
+                            const uint64_t v0 = mul_f32x2(mul_f32x2(f32x2(x[4 * j4], x[4 * j4 + 1]), rf2), f32x2(cf.x, cf.y));
+                            const uint64_t v1 = mul_f32x2(mul_f32x2(f32x2(x[4 * j4 + 2], x[4 * j4 + 3]), rf2), f32x2(cf.z, cf.w));
+                            m[2 * j4] = bf16x2_narrow(v0);
+                            m[2 * j4 + 1] = bf16x2_narrow(v1);
+                        }
                     }
                 }
+                tmem_st16(at + 32 * b, m);
             }
-            if (c >= 1 && !warp_wait(bars + kYFull, (c - 1) & 1, lim, err)) break;  // the previous M has been used
-            tc_fence_after();
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                if (b <= q) tmem_st16(tmem + lane_base + kTM + 16 * b, m[b]);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -327,37 +392,37 @@ __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__
         const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
         const float dk = a.d ? a.d[h] : 0.f;
         for (int c = 0; c < NC; ++c) {
-            const int st = c & 1;
-            if (!warp_wait(bars + kFullX + st, (c >> 1) & 1, lim, err)) break;
-            if (!warp_wait(bars + kReady + st, (c >> 1) & 1, lim, err)) break;
-            if (!warp_wait(bars + kYFull, c & 1, lim, err)) break;
+            const int xs = c % so::kXS;
+            if (!wait_bar(bars + kFullX + xs, (c / so::kXS) & 1, lim, err)) break;
+            if (!wait_bar(bars + kReady + xs, (c / so::kXS) & 1, lim, err)) break;
+            if (!wait_bar(bars + kYFull, c & 1, lim, err)) break;
             tc_fence_after();
-            const float eL = ex2_approx(reinterpret_cast<const float*>(sm + so::GATE + st * so::kGateStage)[i]);
-            uint8_t* xt = sm + so::X + st * so::kTile;
+            const float eL = ex2_approx(reinterpret_cast<const float*>(sm + so::GATE + xs * so::kGateStage)[i]);
+            uint8_t* xt = sm + so::X + xs * so::kTile;
             const int n = u.len - c * kQ;
             __nv_bfloat16* yrow = a.y + (static_cast<size_t>(u.row + c * kQ + i) * a.H + h) * a.P + p0;
+#pragma unroll 1
+            for (int part = 0; part < 4; ++part) {
+                uint32_t yi[16], yx[16];
+                tmem_ld16(tmem + lane_base + kTYi + 16 * part, yi);
+                tmem_ld16(tmem + lane_base + kTYx + 16 * part, yx);
+                tmem_ld_wait();
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float yi[32], yx[32];
-                tmem_ld_cols<2>(tmem + lane_base + kTYi + 32 * half, yi);
-                tmem_ld_cols<2>(tmem + lane_base + kTYx + 32 * half, yx);
-                if (half) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive1(bars + kYEmpty);
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint4* cell = reinterpret_cast<uint4*>(xt + i * 128 + (((4 * half + k) ^ (i & 7)) << 4));
+                for (int k = 0; k < 2; ++k) {
+                    uint4* cell = reinterpret_cast<uint4*>(xt + i * 128 + (((2 * part + k) ^ (i & 7)) << 4));
                     float xv[8], out[8];
                     unpack8(*cell, xv);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) out[e] = fmaf(dk, xv[e], fmaf(eL, yx[8 * k + e], yi[8 * k + e]));
+                    for (int e = 0; e < 8; ++e)
+                        out[e] = fmaf(dk, xv[e], fmaf(eL, __uint_as_float(yx[8 * k + e]), __uint_as_float(yi[8 * k + e])));
                     const uint4 o = pack8(out);
                     if (n >= kQ) *cell = o;
-                    else if (i < n) reinterpret_cast<uint4*>(yrow)[4 * half + k] = o;
+                    else if (i < n) reinterpret_cast<uint4*>(yrow)[2 * part + k] = o;
                 }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(bars + kYEmpty);
             if (n >= kQ) {
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -368,7 +433,7 @@ __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive1(bars + kXEmpty + st);
+            if (lane == 0) mbar_arrive1(bars + kXEmpty + xs);
         }
         if (lane == 0) bulk_wait_all();
     } else if (warp >= 12) {
@@ -399,20 +464,20 @@ __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__
         // X~ of chunk c, token row r: parts [first, first + 2) or the one at `first`, each the bf16 rounding of
         // what the parts before it leave
         auto weigh = [&](int c, int first, int count) -> bool {
-            const int st = c & 1;
-            if (!warp_wait(bars + kFullX + st, (c >> 1) & 1, lim, err)) return false;
-            if (!warp_wait(bars + kReady + st, (c >> 1) & 1, lim, err)) return false;
-            const float* arr = reinterpret_cast<const float*>(sm + so::GATE + st * so::kGateStage);
+            const int xs = c % so::kXS;
+            if (!wait_bar(bars + kFullX + xs, (c / so::kXS) & 1, lim, err)) return false;
+            if (!wait_bar(bars + kReady + xs, (c / so::kXS) & 1, lim, err)) return false;
+            const float* arr = reinterpret_cast<const float*>(sm + so::GATE + xs * so::kGateStage);
             const float w = arr[256 + r];
             decay_next = ex2_approx(arr[127]);
             for (int k = 0; k < count; ++k) {
                 const int seq = c * kParts + first + k;
-                if (seq >= 2 && !warp_wait(bars + kXwFree + (seq & 1), ((seq >> 1) & 1) ^ 1, lim, err)) return false;
+                if (seq >= so::kXB && !wait_bar(bars + kXwFree + seq % so::kXB, ((seq / so::kXB) & 1) ^ 1, lim, err)) return false;
             }
-            const uint8_t* xt = sm + so::X + st * so::kTile + r * 128;
+            const uint8_t* xt = sm + so::X + xs * so::kTile + r * 128;
             uint8_t* to = sm + so::XW + r * 128;
-            const int buf = (c * kParts + first) & 1;
-#pragma unroll
+            const int buf = (c * kParts + first) % so::kXB;
+#pragma unroll 2
             for (int k = 0; k < 8; ++k) {
                 const int cell = (k ^ (r & 7)) << 4;
                 float v[8], hi[8];
@@ -455,7 +520,7 @@ __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__
         for (int c = 0; ok && c < NC; ++c) {
             const float decay = decay_next;
             if (kParts == 1 && c + 1 < NC && !(ok = weigh_all(c + 1))) break;
-            if (!(ok = warp_wait(bars + kDFull, c & 1, lim, err))) break;
+            if (!(ok = wait_bar(bars + kDFull, c & 1, lim, err))) break;
             tc_fence_after();
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -468,7 +533,7 @@ __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__
             __syncwarp();
             if (lane == 0) mbar_arrive1(bars + kDEmpty);
             if (c + 1 < NC) {
-                if (!(ok = warp_wait(bars + kHFree, c & 1, lim, err))) break;
+                if (!(ok = wait_bar(bars + kHFree, c & 1, lim, err))) break;
                 put_state();
                 if (kParts > 1) ok = weigh_all(c + 1);
             }
@@ -482,7 +547,7 @@ __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, 512);
+    if (warp == 0) tmem_dealloc(*tmem_slot, 512);
 }
 
 // [rows, heads, width] bf16 with a row stride, as (width, heads, rows); box (64, 1, box_rows)
