@@ -17,34 +17,36 @@ namespace {
 constexpr int kQ = 128;   // tokens per chunk
 constexpr int kCols = 64; // value columns per block
 
-// Shared memory (byte offsets from a 1024-aligned base); tiles are [128 rows][64 bf16], 128-byte swizzle. With one
-// part of X~ per chunk its buffer is single and X has three stages (a stage is free only when Y has left
-// through it, the longest way of all); with three parts, two buffers and two stages fill the same room.
+// Shared memory (byte offsets from a 1024-aligned base); tiles are [128 rows][64 bf16], 128-byte swizzle. X has three
+// stages: a stage is free only when Y has left through it, the longest way of all. X~ has one buffer per
+// part; three of them take the room of C's second stage.
 template <int kParts>
 struct So {
     static constexpr uint32_t kTile = 16384;
-    static constexpr int kXS = kParts == 1 ? 3 : 2, kXB = kParts == 1 ? 1 : 2;
+    static constexpr int kXS = 3, kCS = kParts == 1 ? 2 : 1;
     static constexpr uint32_t B = 0;                  // 2 stages x 2 tiles (n 0-63, 64-127)
-    static constexpr uint32_t C = B + 4 * kTile;      // 2 x 2
-    static constexpr uint32_t X = C + 4 * kTile;      // kXS; Y replaces X for its store
-    static constexpr uint32_t XW = X + kXS * kTile;   // kXB buffers of X~ parts
-    static constexpr uint32_t HB = XW + kXB * kTile;  // the state as a bf16 operand
+    static constexpr uint32_t C = B + 4 * kTile;      // kCS x 2
+    static constexpr uint32_t X = C + 2 * kCS * kTile;  // kXS; Y replaces X for its store
+    static constexpr uint32_t XW = X + kXS * kTile;   // parts of X~
+    static constexpr uint32_t HB = XW + kParts * kTile;  // the state as a bf16 operand
     static constexpr uint32_t kGateStage = 4 * 512;   // {L, col, wend, step} [128] fp32, a stage per stage of X
     static constexpr uint32_t GATE = HB + kTile;
     static constexpr uint32_t BAR = GATE + kXS * kGateStage;
-    static constexpr uint32_t TOTAL = BAR + 256;
+    static constexpr uint32_t TOTAL = BAR + 320;
     static_assert(TOTAL + 1024 <= 232448, "scan kernel shared memory");
 };
 
 enum Bar {
-    kFull = 0, kFullX = 2, kReady = 5, kBcEmpty = 8, kXEmpty = 10, kSFull = 13, kXwReady = 15, kXwFree = 17,
-    kMReady = 19, kYFull, kYEmpty, kDFull, kDEmpty, kHReady, kHFree, kDrain, kBars
+    kFullB = 0, kFullC = 2, kFullX = 4, kReady = 7, kBEmpty = 10, kCEmpty = 12, kXEmpty = 14, kSFull = 17, kXwReady = 19,
+    kXwFree = 22, kMReady = 25, kYFull, kYEmpty, kDFull, kDEmpty, kHReady, kHFree, kDrain, kBars
 };
-static_assert(kBars * 8 + 16 <= 256, "barrier room");
+constexpr uint32_t kBarBytes = 8 * kBars + 16;
+static_assert(kBarBytes <= 320, "barrier room");
+constexpr int kScanThreads = 640;
 
 // tensor-memory columns: scores of two chunks, each half replaced by M (16 packed columns at the start of every
-// 32); then Y's two sums and the state's increment
-constexpr uint32_t kTS = 0, kTYi = 256, kTYx = 320, kTD = 384;
+// 32); Y's sum over the chunk, its readouts of the state of two chunks, the state's increment
+constexpr uint32_t kTS = 0, kTYi = 256, kTYx = 320, kTD = 448;
 
 struct ScanMaps {
     CUtensorMap x, b, c, y;
@@ -147,7 +149,7 @@ __device__ __forceinline__ void gate_arrays(float* arr, int lane, const float (&
 // kParts bf16 parts of X~ enter the state's product: one where the state only feeds bf16 results, three
 // (2^-24 of every term) where it is returned in fp32.
 template <int kParts>
-__global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__ ScanMaps maps, const ScanTcArgs a) {
+__global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_constant__ ScanMaps maps, const ScanTcArgs a) {
     using so = So<kParts>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -165,8 +167,11 @@ __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__
     const long long lim = a.wait_ns;
 
     if (tid == 0) {
-        const int counts[kBars] = {1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 4, 4, 4, 1, 1, 4, 4, 1, 1, 4, 1, 4, 1, 4, 4, 1, 1};
-        for (int i = 0; i < kBars; ++i) mbar_init(bars + i, counts[i]);
+        for (int i = 0; i < kBars; ++i) {
+            const bool four = (i >= kXEmpty && i < kXEmpty + 3) || i == kMReady || i == kYEmpty;
+            const bool eight = (i >= kXwReady && i < kXwReady + 3) || i == kDEmpty || i == kHReady;
+            mbar_init(bars + i, four ? 4 : eight ? 8 : 1);
+        }
         *err = 0;
         fence_mbar_init();
     }
@@ -185,37 +190,41 @@ __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__
         // copies: B and C (warp 0) are free again earlier than X, whose room Y leaves through (warp 3)
         if (lane == 0) {
             const bool bc = warp == 0;
-            const int full = bc ? kFull : kFullX, empty = bc ? kBcEmpty : kXEmpty, halves = a.N / 64;
+            const int halves = a.N / 64;
             prefetch_tensormap(bc ? &maps.b : &maps.x);
             if (bc) prefetch_tensormap(&maps.c);
-            const int stages = bc ? 2 : so::kXS;
-            int issued = 0, st = 0;
-            uint32_t ph = 0;
-            for (int c = 0; c < NC; ++c) {
-                if (c >= stages && !mbar_wait_or_abort(bars + empty + st, ph ^ 1, lim, err)) {
-                    note_failure(err);
-                    break;
+            auto drain = [&](int issued, int full, int stages) {  // nothing in flight when the block ends
+                for (int c = issued > stages ? issued - stages : 0; c < issued; ++c)
+                    mbar_wait(bars + full + c % stages, (c / stages) & 1, kDefaultWaitNs);
+            };
+            int n0 = 0, n1 = 0;
+            if (bc) {
+                // tiles of one or two halves lie two tiles apart
+                for (int c = 0; c < NC; ++c, ++n1) {
+                    const int st = c & 1, sc = c % so::kCS;
+                    if (c >= 2 && !mbar_wait_or_abort(bars + kBEmpty + st, ((c >> 1) & 1) ^ 1, lim, err)) break;
+                    mbar_arrive_expect_tx(bars + kFullB + st, so::kTile * halves);
+                    for (int k = 0; k < halves; ++k)
+                        tma_load_3d(sm + so::B + (2 * st + k) * so::kTile, &maps.b, 64 * k, grp, u.row + c * kQ, bars + kFullB + st);
+                    ++n0;
+                    if (c >= so::kCS && !mbar_wait_or_abort(bars + kCEmpty + sc, ((c / so::kCS) & 1) ^ 1, lim, err)) break;
+                    mbar_arrive_expect_tx(bars + kFullC + sc, so::kTile * halves);
+                    for (int k = 0; k < halves; ++k)
+                        tma_load_3d(sm + so::C + (2 * sc + k) * so::kTile, &maps.c, 64 * k, grp, u.row + c * kQ, bars + kFullC + sc);
                 }
-                const int row = u.row + c * kQ;
-                uint64_t* bar = bars + full + st;
-                if (bc) {
-                    mbar_arrive_expect_tx(bar, so::kTile * 2 * halves);
-                    for (int k = 0; k < halves; ++k) {
-                        tma_load_3d(sm + so::B + (2 * st + k) * so::kTile, &maps.b, 64 * k, grp, row, bar);
-                        tma_load_3d(sm + so::C + (2 * st + k) * so::kTile, &maps.c, 64 * k, grp, row, bar);
-                    }
-                } else {
-                    mbar_arrive_expect_tx(bar, so::kTile);
-                    tma_load_3d(sm + so::X + st * so::kTile, &maps.x, p0, h, row, bar);
+                if (n1 < NC) note_failure(err);
+                drain(n0, kFullB, 2);
+                drain(n1, kFullC, so::kCS);
+            } else {
+                for (int c = 0; c < NC; ++c, ++n0) {
+                    const int xs = c % so::kXS;
+                    if (c >= so::kXS && !mbar_wait_or_abort(bars + kXEmpty + xs, ((c / so::kXS) & 1) ^ 1, lim, err)) break;
+                    mbar_arrive_expect_tx(bars + kFullX + xs, so::kTile);
+                    tma_load_3d(sm + so::X + xs * so::kTile, &maps.x, p0, h, u.row + c * kQ, bars + kFullX + xs);
                 }
-                issued = c + 1;
-                if (++st == stages) {
-                    st = 0;
-                    ph ^= 1;
-                }
+                if (n0 < NC) note_failure(err);
+                drain(n0, kFullX, so::kXS);
             }
-            for (int c = issued > stages ? issued - stages : 0; c < issued; ++c)  // nothing in flight when the block ends
-                mbar_wait(bars + full + c % stages, (c / stages) & 1, kDefaultWaitNs);
         }
     } else if (warp == 1) {
         const uint32_t id_s = idesc_bf16(128, 128, false, false), id_d = idesc_bf16(128, 64, true, true),
@@ -224,68 +233,65 @@ __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__
         // K-major tiles: 16 channels are 32 bytes of a row, the next 64 the next tile. MN-major: 16 tokens (or
         // state rows) are 16 rows of 128 bytes.
         const uint32_t dk = uniform(desc_lo(sb, 16)), dm = uniform(desc_lo(sb, so::kTile));
-        bool ok = NC > 0;
         auto wait = [&](int bar, uint32_t parity) {
             const bool w = wait_bar(bars + bar, parity, lim, err);
             tc_fence_after();
             return w;
         };
-        auto scores = [&](int c) {
-            const int st = c & 1;
-            const uint32_t ph = (c >> 1) & 1;
-            if (!wait(kFull + st, ph)) return false;
-            if (u.len - c * kQ < kQ && !wait(kReady + c % so::kXS, (c / so::kXS) & 1)) return false;  // a short chunk's rows of B are cleared first
-            if (c >= 2 && !wait(kYFull, c & 1)) return false;  // M of two chunks before, in the same columns, has been used
-            const uint32_t ca = dk + ((so::C + 2 * st * so::kTile) >> 4), ba = dk + ((so::B + 2 * st * so::kTile) >> 4);
-#pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                const uint32_t off = (s >> 2) * so::kTile + (s & 3) * 32;
-                if (s < ks) mma_by(lead, kTS + 128 * st, ca + ((off) >> 4), ba + ((off) >> 4), id_s, s > 0);
-            }
-            commit_by(lead, bars + kSFull + st);
-            return true;
-        };
-        ok = ok && scores(0);
-        int xs = 0;
-        uint32_t xph = 0;
-        for (int c = 0; ok && c < NC; ++c) {
-            const int st = c & 1;
+        bool ok = true;
+        for (int c = -1; c < NC && NC > 0; ++c) {
             const uint32_t ph1 = c & 1;  // phase of the barriers used once per chunk
-            // state increment
-            if (c >= 1 && !(ok = wait(kDEmpty, ph1 ^ 1))) break;
-            const uint32_t bm = dm + ((so::B + 2 * st * so::kTile) >> 4);
-            for (int k = 0; ok && k < kParts; ++k) {
-                const int seq = c * kParts + k, buf = seq % so::kXB;
-                if (!(ok = wait(kXwReady + buf, (seq / so::kXB) & 1))) break;
-                const uint32_t xa = dm + ((so::XW + buf * so::kTile) >> 4);
+            if (c >= 0) {
+                // state increment
+                const uint32_t bm = dm + ((so::B + 2 * (c & 1) * so::kTile) >> 4);
+                if (c >= 1 && !(ok = wait(kDEmpty, ph1 ^ 1))) break;
+#pragma unroll 1
+                for (int k = 0; k < kParts; ++k) {
+                    if (!(ok = wait(kXwReady + k, ph1))) break;
+                    const uint32_t xa = dm + ((so::XW + k * so::kTile) >> 4);
 #pragma unroll
-                for (int s = 0; s < 8; ++s) mma_by(lead, kTD, bm + ((s * 2048) >> 4), xa + ((s * 2048) >> 4), id_d, k > 0 || s > 0);
-                commit_by(lead, bars + kXwFree + buf);
+                    for (int s = 0; s < 8; ++s) mma_by(lead, kTD, bm + s * 128, xa + s * 128, id_d, k > 0 || s > 0);
+                    commit_by(lead, bars + kXwFree + k);
+                }
+                if (!ok) break;
+                commit_by(lead, bars + kDFull);
+                commit_by(lead, bars + kBEmpty + (c & 1));
+                // readout of the state
+                if (!(ok = wait(kHReady, ph1))) break;
+                const uint32_t ck = dk + ((so::C + 2 * (c % so::kCS) * so::kTile) >> 4), hb = dm + (so::HB >> 4);
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    if (s < ks) mma_by(lead, kTYx + 64 * (c & 1), ck + (((s >> 2) * so::kTile + (s & 3) * 32) >> 4), hb + s * 128, id_x, s > 0);
+                commit_by(lead, bars + kCEmpty + c % so::kCS);
+                commit_by(lead, bars + kHFree);
             }
-            if (!ok) break;
-            commit_by(lead, bars + kDFull);
-            // readout of the state
-            if (!(ok = wait(kHReady, ph1))) break;
-            if (c >= 1 && !(ok = wait(kYEmpty, ph1 ^ 1))) break;
-            const uint32_t ck = dk + ((so::C + 2 * st * so::kTile) >> 4), hb = dm + ((so::HB) >> 4);
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-                if (s < ks) mma_by(lead, kTYx, ck + (((s >> 2) * so::kTile + (s & 3) * 32) >> 4), hb + ((s * 2048) >> 4), id_x, s > 0);
-            commit_by(lead, bars + kBcEmpty + st);
-            commit_by(lead, bars + kHFree);
             // The next chunk's scores go in here: their tiles were asked for when the chunk before this one was
             // read out, and M of the next chunk can start while this one's is still used.
-            if (c + 1 < NC && !(ok = scores(c + 1))) break;
-            // within the chunk
-            if (!(ok = wait(kFullX + xs, xph) && wait(kReady + xs, xph) && wait(kMReady, ph1))) break;
-            const uint32_t xm = dm + ((so::X + xs * so::kTile) >> 4);
+            const int n = c + 1, st = n & 1;
+            if (n < NC) {
+                if (!(ok = wait(kFullB + st, (n >> 1) & 1) && wait(kFullC + n % so::kCS, (n / so::kCS) & 1))) break;
+                // a short chunk's rows of B are cleared first
+                if (u.len - n * kQ < kQ && !(ok = wait(kReady + n % so::kXS, (n / so::kXS) & 1))) break;
+                // M of two chunks before, in the same columns, has been used
+                if (n >= 2 && !(ok = wait(kYFull, n & 1))) break;
+                const uint32_t ca = dk + ((so::C + 2 * (n % so::kCS) * so::kTile) >> 4), ba = dk + ((so::B + 2 * st * so::kTile) >> 4);
 #pragma unroll
-            for (int s = 0; s < 8; ++s)
-                mma_ts_by(lead, kTYi, kTS + 128 * st + 32 * (s >> 1) + 8 * (s & 1), xm + ((s * 2048) >> 4), id_x, s > 0);
-            commit_by(lead, bars + kYFull);
-            if (++xs == so::kXS) {
-                xs = 0;
-                xph ^= 1;
+                for (int s = 0; s < 8; ++s) {
+                    const uint32_t off = ((s >> 2) * so::kTile + (s & 3) * 32) >> 4;
+                    if (s < ks) mma_by(lead, kTS + 128 * st, ca + off, ba + off, id_s, s > 0);
+                }
+                commit_by(lead, bars + kSFull + st);
+            }
+            // within the chunk
+            if (c >= 0) {
+                const int xs = c % so::kXS;
+                if (!(ok = wait(kFullX + xs, (c / so::kXS) & 1) && wait(kReady + xs, (c / so::kXS) & 1) && wait(kMReady, ph1))) break;
+                if (c >= 1 && !(ok = wait(kYEmpty, ph1 ^ 1))) break;
+                const uint32_t xm = dm + ((so::X + xs * so::kTile) >> 4);
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    mma_ts_by(lead, kTYi, kTS + 128 * (c & 1) + 32 * (s >> 1) + 8 * (s & 1), xm + s * 128, id_x, s > 0);
+                commit_by(lead, bars + kYFull);
             }
         }
         commit_by(lead, bars + kDrain);
@@ -310,7 +316,7 @@ __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__
             gate_arrays(reinterpret_cast<float*>(sm + so::GATE + xs * so::kGateStage), lane, gn, sn);
             const int n = u.len - c * kQ;
             if (n < kQ) {
-                if (!wait_bar(bars + kFull + st, (c >> 1) & 1, lim, err)) break;
+                if (!wait_bar(bars + kFullB + st, (c >> 1) & 1, lim, err)) break;
                 // the rows past the sequence hold other tokens: zeros, so that not even their NaN enters a sum
                 const uint4 z = make_uint4(0, 0, 0, 0);
                 for (int i = n * 8 + lane; i < kQ * 8; i += 32) {
@@ -402,22 +408,25 @@ __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__
             const int n = u.len - c * kQ;
             __nv_bfloat16* yrow = a.y + (static_cast<size_t>(u.row + c * kQ + i) * a.H + h) * a.P + p0;
 #pragma unroll 1
-            for (int part = 0; part < 4; ++part) {
-                uint32_t yi[16], yx[16];
-                tmem_ld16(tmem + lane_base + kTYi + 16 * part, yi);
-                tmem_ld16(tmem + lane_base + kTYx + 16 * part, yx);
-                tmem_ld_wait();
+            for (int part = 0; part < 2; ++part) {
+                uint32_t yi[2][16], yx[2][16];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    uint4* cell = reinterpret_cast<uint4*>(xt + i * 128 + (((2 * part + k) ^ (i & 7)) << 4));
+                    tmem_ld16(tmem + lane_base + kTYi + 32 * part + 16 * k, yi[k]);
+                    tmem_ld16(tmem + lane_base + kTYx + 64 * (c & 1) + 32 * part + 16 * k, yx[k]);
+                }
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint4* cell = reinterpret_cast<uint4*>(xt + i * 128 + (((4 * part + k) ^ (i & 7)) << 4));
                     float xv[8], out[8];
                     unpack8(*cell, xv);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        out[e] = fmaf(dk, xv[e], fmaf(eL, __uint_as_float(yx[8 * k + e]), __uint_as_float(yi[8 * k + e])));
+                        out[e] = fmaf(dk, xv[e], fmaf(eL, __uint_as_float(yx[k >> 1][8 * (k & 1) + e]), __uint_as_float(yi[k >> 1][8 * (k & 1) + e])));
                     const uint4 o = pack8(out);
                     if (n >= kQ) *cell = o;
-                    else if (i < n) reinterpret_cast<uint4*>(yrow)[2 * part + k] = o;
+                    else if (i < n) reinterpret_cast<uint4*>(yrow)[4 * part + k] = o;
                 }
             }
             tc_fence_before();
@@ -437,111 +446,84 @@ __global__ void __launch_bounds__(512, 1) scan_tc_kernel(const __grid_constant__
         }
         if (lane == 0) bulk_wait_all();
     } else if (warp >= 12) {
-        // ---- X~ of the next chunk, then the state over this one: row n of the state per thread, 64 columns
-        const int q = warp & 3, r = 32 * q + lane;
+        // ---- X~ of the next chunk, then the state over this one: row n of the state (token of X~) per thread, half
+        // of the 64 columns per group of four warps
+        const int q = warp & 3, half = warp >= 16, r = 32 * q + lane;
         const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
         const bool real = r < a.N;
-        const size_t at = static_cast<size_t>(real ? r : 0) * a.P + p0;
-        float hx[64];
+        const size_t at = static_cast<size_t>(real ? r : 0) * a.P + p0 + 32 * half;
+        float hx[32];
         {
             const float* from = a.cut ? a.states + (static_cast<size_t>(blockIdx.y) * a.H + h) * plane
                                       : (a.s0 ? a.s0 + (static_cast<size_t>(u.seq) * a.H + h) * plane : nullptr);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
+            for (int k = 0; k < 8; ++k) {
                 const float4 f = from && real ? reinterpret_cast<const float4*>(from + at)[k] : make_float4(0.f, 0.f, 0.f, 0.f);
                 hx[4 * k] = f.x; hx[4 * k + 1] = f.y; hx[4 * k + 2] = f.z; hx[4 * k + 3] = f.w;
             }
         }
-        uint8_t* hb = sm + so::HB;
-        auto put_state = [&]() {
-            st_row_bf16x32(hb, r, 0, hx);
-            st_row_bf16x32(hb, r, 4, hx + 32);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive1(bars + kHReady);
-        };
-        float decay_next = 1.f;
-        // X~ of chunk c, token row r: parts [first, first + 2) or the one at `first`, each the bf16 rounding of
-        // what the parts before it leave
-        auto weigh = [&](int c, int first, int count) -> bool {
-            const int xs = c % so::kXS;
-            if (!wait_bar(bars + kFullX + xs, (c / so::kXS) & 1, lim, err)) return false;
-            if (!wait_bar(bars + kReady + xs, (c / so::kXS) & 1, lim, err)) return false;
-            const float* arr = reinterpret_cast<const float*>(sm + so::GATE + xs * so::kGateStage);
-            const float w = arr[256 + r];
-            decay_next = ex2_approx(arr[127]);
-            for (int k = 0; k < count; ++k) {
-                const int seq = c * kParts + first + k;
-                if (seq >= so::kXB && !wait_bar(bars + kXwFree + seq % so::kXB, ((seq / so::kXB) & 1) ^ 1, lim, err)) return false;
-            }
-            const uint8_t* xt = sm + so::X + xs * so::kTile + r * 128;
-            uint8_t* to = sm + so::XW + r * 128;
-            const int buf = (c * kParts + first) % so::kXB;
-#pragma unroll 2
-            for (int k = 0; k < 8; ++k) {
-                const int cell = (k ^ (r & 7)) << 4;
-                float v[8], hi[8];
-                unpack8(*reinterpret_cast<const uint4*>(xt + cell), v);
+        float decay = 1.f;
+        bool ok = true;
+        for (int c = -1; c < NC; ++c) {
+            const int n = c + 1;
+            const float decay_c = decay;
+            if (n < NC) {
+                // X~ of chunk n, row r: each part is the bf16 rounding of what the parts before it leave
+                const int xs = n % so::kXS;
+                if (!(ok = wait_bar(bars + kFullX + xs, (n / so::kXS) & 1, lim, err) && wait_bar(bars + kReady + xs, (n / so::kXS) & 1, lim, err))) break;
+                const float* arr = reinterpret_cast<const float*>(sm + so::GATE + xs * so::kGateStage);
+                const float w = arr[256 + r];
+                decay = ex2_approx(arr[127]);
+                if (n >= 1 && !(ok = wait_bar(bars + kXwFree + kParts - 1, (n & 1) ^ 1, lim, err))) break;  // the last part's product follows the others'
+                const uint8_t* xt = sm + so::X + xs * so::kTile + r * 128;
+                uint8_t* to = sm + so::XW + r * 128;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= w;
-                uint4 o = pack8(v);
-                if (kParts == 3) {
-                    if (first == 0) *reinterpret_cast<uint4*>(to + buf * so::kTile + cell) = o;
-                    unpack8(o, hi);
+                for (int k = 0; k < 4; ++k) {
+                    const int cell = ((4 * half + k) ^ (r & 7)) << 4;
+                    float v[8];
+                    unpack8(*reinterpret_cast<const uint4*>(xt + cell), v);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] -= hi[e];
-                    o = pack8(v);
-                    if (first == 0) {
-                        *reinterpret_cast<uint4*>(to + (buf ^ 1) * so::kTile + cell) = o;
-                    } else {
-                        unpack8(o, hi);
+                    for (int e = 0; e < 8; ++e) v[e] *= w;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] -= hi[e];
-                        *reinterpret_cast<uint4*>(to + buf * so::kTile + cell) = pack8(v);
+                    for (int part = 0; part < kParts; ++part) {
+                        const uint4 o = pack8(v);
+                        *reinterpret_cast<uint4*>(to + part * so::kTile + cell) = o;
+                        if (part + 1 < kParts) {
+                            float hi[8];
+                            unpack8(o, hi);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] -= hi[e];
+                        }
                     }
-                } else {
-                    *reinterpret_cast<uint4*>(to + buf * so::kTile + cell) = o;
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    for (int part = 0; part < kParts; ++part) mbar_arrive1(bars + kXwReady + part);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                for (int k = 0; k < count; ++k) mbar_arrive1(bars + kXwReady + (buf ^ k));
-            return true;
-        };
-        // Three parts share two buffers, so the third waits for the first one's product, and that product
-        // for the previous increment to be read: with three parts X~ is formed after the state's update.
-        auto weigh_all = [&](int c) { return kParts == 1 ? weigh(c, 0, 1) : weigh(c, 0, 2) && weigh(c, 2, 1); };
-        bool ok = NC > 0;
-        if (ok) {
-            put_state();
-            ok = weigh_all(0);
-        }
-        for (int c = 0; ok && c < NC; ++c) {
-            const float decay = decay_next;
-            if (kParts == 1 && c + 1 < NC && !(ok = weigh_all(c + 1))) break;
-            if (!(ok = wait_bar(bars + kDFull, c & 1, lim, err))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            if (c >= 0) {
+                if (!(ok = wait_bar(bars + kDFull, c & 1, lim, err))) break;
+                tc_fence_after();
                 float x[32];
                 tmem_ld_cols<2>(tmem + lane_base + kTD + 32 * half, x);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) hx[32 * half + k] = fmaf(decay, hx[32 * half + k], x[k]);
+                for (int k = 0; k < 32; ++k) hx[k] = fmaf(decay_c, hx[k], x[k]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(bars + kDEmpty);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive1(bars + kDEmpty);
-            if (c + 1 < NC) {
-                if (!(ok = wait_bar(bars + kHFree, c & 1, lim, err))) break;
-                put_state();
-                if (kParts > 1) ok = weigh_all(c + 1);
+            if (n < NC) {
+                if (c >= 0 && !(ok = wait_bar(bars + kHFree, c & 1, lim, err))) break;
+                st_row_bf16x32(sm + so::HB, r, 4 * half, hx);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(bars + kHReady);
             }
         }
-        if ((ok || NC == 0) && a.s1 && u.k == u.count - 1 && real) {
+        if (ok && a.s1 && u.k == u.count - 1 && real) {
             float* to = a.s1 + (static_cast<size_t>(u.seq) * a.H + h) * plane + at;
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
+            for (int k = 0; k < 8; ++k)
                 reinterpret_cast<float4*>(to)[k] = make_float4(hx[4 * k], hx[4 * k + 1], hx[4 * k + 2], hx[4 * k + 3]);
         }
     }
@@ -563,7 +545,7 @@ cudaError_t launch_scan(const ScanMaps& maps, const ScanTcArgs& a, dim3 grid, cu
     cudaError_t e = cudaFuncSetAttribute(scan_tc_kernel<kParts>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
     if (e != cudaSuccess) return e;
     // the whole shared memory: one block per SM, and no operand descriptor reaches past the block's own
-    scan_tc_kernel<kParts><<<grid, 512, 232448, s>>>(maps, a);
+    scan_tc_kernel<kParts><<<grid, kScanThreads, 232448, s>>>(maps, a);
     return cudaGetLastError();
 }
 
