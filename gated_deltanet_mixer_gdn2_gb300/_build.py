@@ -13,7 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn2.so")
 SOURCES = ["api.cu", "decode.cu", "chunk_simt.cu", "chunk_tc.cu", "noalloc.cu", "transforms.cu", "mixer.cu", "mixer_step.cu", "backward.cu", "backward_chunk.cu", "backward_tc.cu",
-           "ssm_api.cu", "ssm_scan.cu", "ssm_tc.cu", "ssm_prologue.cu", "ssm_decode.cu", "block_norm.cu"]
+           "ssm_api.cu", "ssm_scan.cu", "ssm_tc.cu", "ssm_tc_walk.cu", "ssm_tc_grad.cu", "ssm_prologue.cu", "ssm_decode.cu", "block_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"),
          "--expt-relaxed-constexpr"]

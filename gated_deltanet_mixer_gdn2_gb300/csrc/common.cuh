@@ -102,6 +102,8 @@ int step_read_clear_status(cudaStream_t s);
 int chunk_simt_read_clear_status(cudaStream_t s);
 int chunk_tc_read_clear_status(cudaStream_t s);
 int ssm_tc_read_clear_status(cudaStream_t s);
+int ssm_tc_walk_read_clear_status(cudaStream_t s);
+int ssm_tc_grad_read_clear_status(cudaStream_t s);
 
 long long wait_limit_ns();
 

@@ -53,7 +53,7 @@ size_t gdn2_ssm_chunk_fwd_workspace_size(gdn2_path path, int B, int T, int H, in
 size_t gdn2_ssm_backward_workspace_size(gdn2_path path, int B, int T, int H, int G, int P, int N, int packed, gdn2_dtype dt) {
     const ScanShape sh{{packed ? &kFakeOffset : nullptr, B, T}, H, G, P, N, dt};
     if (scan_check(path, sh) != GDN2_OK || B == 0 || sh.seqs.rows() == 0) return 0;
-    return ssm_simt_bwd_workspace(sh);
+    return on_tensor_cores(path, sh) ? ssm_tc_bwd_workspace(sh) : ssm_simt_bwd_workspace(sh);
 }
 
 gdn2_status gdn2_ssm_chunk_fwd(gdn2_path path, const void* x, long long ld_x, const void* step, const void* g,
@@ -130,7 +130,9 @@ gdn2_status gdn2_ssm_backward(gdn2_path path, const void* x, long long ld_x, con
     if (need && !aligned16(workspace)) return GDN2_ERR_MISALIGNED;
     const ScanIn in{{x, ld_x}, {bm, ld_b}, {cm, ld_c}, step, g, d, initial_state};
     const ScanGrads gr{{d_y, ld_dy}, d_final_state, {dx, ld_dx}, {dbm, ld_db}, {dcm, ld_dc}, dstep, dg, dd, d_initial_state};
-    return launch_ssm_simt_bwd(sh, in, gr, workspace, s) == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA;
+    const cudaError_t e = on_tensor_cores(path, sh) ? launch_ssm_tc_bwd(sh, in, gr, workspace, s, wait_limit_ns())
+                                                    : launch_ssm_simt_bwd(sh, in, gr, workspace, s);
+    return e == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -87,6 +87,21 @@ __device__ __forceinline__ bool find_unit(const Seqs& s, int unit, int idx, Unit
     return true;
 }
 
+// Units of the sequences before `seq`, by a whole warp.
+__device__ __forceinline__ int units_before(const Seqs& s, int unit, int seq) {
+    if (!s.offsets) return seq * Seqs::units_of(s.T, unit);
+    const int lane = threadIdx.x & 31;
+    int n = 0;
+    for (int b = lane; b < seq; b += 32) {
+        int start, len;
+        s.span(b, start, len);
+        n += Seqs::units_of(len, unit);
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+    return n;
+}
+
 // The sequence that holds token row r and the row its successor starts at; false if no sequence holds it.
 __device__ __forceinline__ bool find_row(const Seqs& s, int r, int& seq, int& start, int& end) {
     if (!s.offsets) {
@@ -152,8 +167,17 @@ struct ScanGrads {
 size_t ssm_simt_bwd_workspace(const ScanShape& sh);
 cudaError_t launch_ssm_simt_bwd(const ScanShape& sh, const ScanIn& in, const ScanGrads& gr, void* ws, cudaStream_t s);
 
+cudaError_t launch_ssm_chain(const ScanShape& sh, int unit, const float* first, float* last, float* states, const float* decay,
+                             int back, cudaStream_t s);
+
+// dB and dC from the head shares and dD from the units' parts (ssm_scan.cu).
+cudaError_t launch_ssm_grad_sums(const ScanShape& sh, const ScanGrads& gr, const float* part, int splits, const float* dd_part, int units,
+                                 cudaStream_t s);
+
 bool ssm_tc_shape(const ScanShape& sh);
 size_t ssm_tc_fwd_workspace(const ScanShape& sh);
+size_t ssm_tc_bwd_workspace(const ScanShape& sh);
+cudaError_t launch_ssm_tc_bwd(const ScanShape& sh, const ScanIn& in, const ScanGrads& gr, void* ws, cudaStream_t s, long long wait_ns);
 cudaError_t launch_ssm_tc_fwd(const ScanShape& sh, const ScanIn& in, void* y, float* s1, void* ws, cudaStream_t s, long long wait_ns);
 
 }  // namespace gdn2

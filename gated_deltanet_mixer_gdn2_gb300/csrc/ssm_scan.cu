@@ -150,22 +150,8 @@ __global__ void __launch_bounds__(256)
     chain_kernel(Seqs seqs, int unit, const float* __restrict__ first, float* __restrict__ last,
                  float* __restrict__ states, const float* __restrict__ decay, int H, int plane4, int back) {
     const int e = blockIdx.x * blockDim.x + threadIdx.x, h = blockIdx.y, seq = blockIdx.z;
-    int start, len, base = 0;
-    if (seqs.offsets) {
-        const int lane = threadIdx.x & 31;
-        for (int b0 = 0; b0 < seq; b0 += 32) {
-            int n = 0;
-            if (b0 + lane < seq) {
-                seqs.span(b0 + lane, start, len);
-                n = Seqs::units_of(len, unit);
-            }
-#pragma unroll
-            for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
-            base += n;
-        }
-    } else {
-        base = seq * Seqs::units_of(seqs.T, unit);
-    }
+    int start, len;
+    const int base = units_before(seqs, unit, seq);
     seqs.span(seq, start, len);
     const int count = Seqs::units_of(len, unit);
     if (e >= plane4) return;
@@ -635,10 +621,6 @@ cudaError_t grad(const ScanShape& sh, const ScanIn& in, const ScanGrads& gr, flo
         sh.seqs, in.x, in.bm, in.cm, gr.dy, static_cast<const T*>(in.step), static_cast<const T*>(in.g), in.d, ws + w.h0,
         ws + w.dh, gr.dx, gr.dbm, gr.dcm, static_cast<T*>(gr.dstep), static_cast<T*>(gr.dg), ws + w.part,
         gr.dd ? ws + w.dd : nullptr, sh.H, sh.G, sh.P, w.heads, w.splits, sh.seqs.rows());
-    if ((e = cudaGetLastError()) != cudaSuccess || w.splits == 1) return e;
-    const long long n = sh.seqs.rows() * (sh.G * sh.N / 4);
-    share_sum_kernel<T><<<dim3(static_cast<unsigned>((n + 255) / 256), 2), 256, 0, s>>>(ws + w.part, gr.dbm, gr.dcm,
-                                                                                       sh.seqs.rows(), sh.G * sh.N, w.splits);
     return cudaGetLastError();
 }
 
@@ -654,6 +636,26 @@ cudaError_t grad_n(const ScanShape& sh, const ScanIn& in, const ScanGrads& gr, f
 }
 
 }  // namespace
+
+cudaError_t launch_ssm_chain(const ScanShape& sh, int unit, const float* first, float* last, float* states, const float* decay,
+                             int back, cudaStream_t s) {
+    return chain(sh, unit, first, last, states, decay, back, s);
+}
+
+cudaError_t launch_ssm_grad_sums(const ScanShape& sh, const ScanGrads& gr, const float* part, int splits, const float* dd_part, int units,
+                                 cudaStream_t s) {
+    cudaError_t e;
+    if (splits > 1) {
+        const long long rows = sh.seqs.rows(), n = rows * (sh.G * sh.N / 4);
+        const dim3 grid(static_cast<unsigned>((n + 255) / 256), 2);
+        if (sh.dt == GDN2_BF16) share_sum_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(part, gr.dbm, gr.dcm, rows, sh.G * sh.N, splits);
+        else share_sum_kernel<float><<<grid, 256, 0, s>>>(part, gr.dbm, gr.dcm, rows, sh.G * sh.N, splits);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (!gr.dd) return cudaSuccess;
+    dskip_kernel<<<sh.H, 256, 0, s>>>(dd_part, gr.dd, units, sh.H);
+    return cudaGetLastError();
+}
 
 size_t ssm_simt_fwd_workspace(const ScanShape& sh) {
     const int unit = walk_unit(sh);
@@ -688,9 +690,8 @@ cudaError_t launch_ssm_simt_bwd(const ScanShape& sh, const ScanIn& in, const Sca
     if ((e = chain(sh, kGradUnit, in.s0, nullptr, ws + w.h0, ws + w.decay, 0, s)) != cudaSuccess) return e;
     if ((e = chain(sh, kGradUnit, gr.ds1, gr.ds0, ws + w.dh, ws + w.decay_b, 1, s)) != cudaSuccess) return e;
     e = sh.dt == GDN2_BF16 ? grad_n<__nv_bfloat16>(sh, in, gr, ws, w, s) : grad_n<float>(sh, in, gr, ws, w, s);
-    if (e != cudaSuccess || !gr.dd) return e;
-    dskip_kernel<<<sh.H, 256, 0, s>>>(ws + w.dd, gr.dd, static_cast<int>(sh.seqs.units(kGradUnit)), sh.H);
-    return cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_ssm_grad_sums(sh, gr, ws + w.part, w.splits, ws + w.dd, static_cast<int>(sh.seqs.units(kGradUnit)), s);
 }
 
 }  // namespace gdn2

@@ -8,14 +8,10 @@
 // update of the state is serial from chunk to chunk (64 multiply-adds per thread), so the block is a
 // pipeline of warp roles over different chunks: copies (warps 0 and 3), products (warp 1), gates
 // (warp 2), M (warps 4-7), Y (warps 8-11), X~ and state (warps 12-15).
-#include "ssm_common.cuh"
-#include "tc_common.cuh"
+#include "ssm_tc.cuh"
 
 namespace gdn2 {
 namespace {
-
-constexpr int kQ = 128;   // tokens per chunk
-constexpr int kCols = 64; // value columns per block
 
 // Shared memory (byte offsets from a 1024-aligned base); tiles are [128 rows][64 bf16], 128-byte swizzle. X has three
 // stages: a stage is free only when Y has left through it, the longest way of all. X~ has one buffer per
@@ -66,56 +62,6 @@ struct ScanTcArgs {
     long long wait_ns;
 };
 
-__device__ __forceinline__ float4 exp2_4(float4 v) {
-    return make_float4(ex2_approx(v.x), ex2_approx(v.y), ex2_approx(v.z), ex2_approx(v.w));
-}
-
-// Bounded wait on a barrier's phase by a converged warp: the first try inline, the loop out of line (inlined at
-// every wait it made half of the kernel's code). The outcome is the warp's; a warp that gives up records it.
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, long long lim, volatile int* err) {
-    return warp_wait(reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(bar)), parity, lim, err);
-}
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, long long lim, volatile int* err) {
-    if (__all_sync(0xffffffffu, lim > 0 && mbar_try_wait(bar, parity))) return true;
-    return wait_on(smem_u32(bar), parity, lim, err);
-}
-
-// One elected lane of a converged warp issues; the operands are warp-uniform, so that descriptors advance
-// in uniform registers (an `if (lane == 0)` around the loop made every product of 8 steps take 1200 cycles to issue).
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t e;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
-    return e;
-}
-// A value that is the same in all lanes, in a form that the compiler knows to be.
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
-
-// Shared-memory descriptor: the constant upper word (stride 1024, version, 128-byte swizzle) and the lower one, which
-// holds the start address and the leading offset and advances by plain addition of bytes / 16 (no carry out of
-// the 14-bit address: shared memory ends below 256 KB).
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr & 0x3FFFFu) >> 4) | (lbo >> 4 << 16); }
-
-__device__ __forceinline__ void mma_by(uint32_t lead, uint32_t d, uint32_t ad, uint32_t bd, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p, e;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n mov.b64 a, {%1, %6};\n"
-        " mov.b64 b, {%2, %6};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d), "r"(ad), "r"(bd), "r"(id),
-        "r"(acc), "r"(lead), "r"(kDescHi)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts_by(uint32_t lead, uint32_t d, uint32_t at, uint32_t bd, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p, e;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n mov.b64 b, {%2, %6};\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d), "r"(at), "r"(bd), "r"(id), "r"(acc), "r"(lead),
-        "r"(kDescHi)
-        : "memory");
-}
-__device__ __forceinline__ void commit_by(uint32_t lead, uint64_t* bar) {
-    asm volatile(
-        "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
-        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)), "r"(lead)
-        : "memory");
-}
 
 // Gate arrays of one chunk, by one warp, four tokens per lane: L and the decay sums in units of log 2.
 // The decay to the chunk's end is a suffix sum of its own: as a difference of prefix sums it would lose
@@ -532,14 +478,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     if (warp == 0) tmem_dealloc(*tmem_slot, 512);
 }
 
-// [rows, heads, width] bf16 with a row stride, as (width, heads, rows); box (64, 1, box_rows)
-bool rows_map(CUtensorMap* m, const void* p, long long ld, int width, int heads, long long rows, int box_rows) {
-    const uint64_t dims[3] = {(uint64_t)width, (uint64_t)heads, (uint64_t)rows};
-    const uint64_t st[2] = {(uint64_t)width * 2, (uint64_t)ld * 2};
-    const uint32_t box[3] = {64, 1, (uint32_t)box_rows};
-    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
 template <int kParts>
 cudaError_t launch_scan(const ScanMaps& maps, const ScanTcArgs& a, dim3 grid, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(scan_tc_kernel<kParts>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
@@ -578,14 +516,6 @@ cudaError_t launch_ssm_tc_fwd(const ScanShape& sh, const ScanIn& in, void* y, fl
     return s1 ? launch_scan<3>(maps, a, grid, s) : launch_scan<1>(maps, a, grid, s);
 }
 
-int ssm_tc_read_clear_status(cudaStream_t s) {
-    int v = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_status_tc, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess) return -1;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return -1;
-    const int zero = 0;
-    if (v && cudaMemcpyToSymbolAsync(g_status_tc, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess) return -1;
-    cudaStreamSynchronize(s);
-    return v;
-}
+int ssm_tc_read_clear_status(cudaStream_t s) { return read_clear_status(s); }
 
 }  // namespace gdn2

@@ -1,0 +1,705 @@
+// ssm_tc_grad.cu -- the gradients of the selective state-space scan on the tensor cores, one block per (chunk of
+// 128 tokens, group, share of the group's heads), from the state H before the chunk and the adjoint A after it
+// (ssm_tc_walk.cu). With W_ij = e^{L_i - L_j} (i >= j), S = C B^T, R = dY X^T, s the steps:
+//     dC   = (R W s) B + e^{L} dY H^T            dB   = (R W s)^T C + (s e^{L_end - L} X) A^T      (sum over heads)
+//     U    = (S W)^T dY + e^{L_end - L} (B A)    dx_j = s_j U_j + D dY_j,   ds_j = x_j . U_j
+//     dg_t = sum_{i >= t > j} S R W s + sum_{i >= t} e^{L_i} dY_i . (C H)_i
+//            + sum_{j < t} s_j e^{L_end - L_j} x_j . (B A)_j + e^{L_end} <A, H>
+// The pair matrices are formed transposed (a row j of X per thread), so that (R W s)^T and (S W)^T are written back
+// over R^T in tensor memory as operands; dB and dC accumulate there over the block's heads, so the sum over a
+// group's heads costs nothing. The double sum of dg is a suffix sum of (row sums - column sums) of one fp32
+// matrix: what cancels in it cancels exactly.
+// The products of one (chunk, head) take about 2600 tensor-core cycles at these shapes and bound the kernel
+// together with shared-memory bandwidth.
+#include "ssm_tc.cuh"
+
+namespace gdn2 {
+namespace {
+
+// shared memory
+namespace sg {
+constexpr uint32_t B = 0;                         // 2 tiles
+constexpr uint32_t C = B + 2 * kTileBytes;        // 2 tiles
+constexpr uint32_t X = C + 2 * kTileBytes;        // 2 stages; X~ replaces X
+constexpr uint32_t DY = X + 2 * kTileBytes;       // 2 stages; dx leaves through dY's room
+constexpr uint32_t DYW = DY + 2 * kTileBytes;     // e^{L} dY
+constexpr uint32_t H0 = DYW + kTileBytes;
+constexpr uint32_t DH = H0 + kTileBytes;
+constexpr uint32_t P1 = DH + kTileBytes;          // (R W s)^T [j][i]: 2 tiles
+constexpr uint32_t GATE = P1 + 2 * kTileBytes;    // 2 stages x {L, s, wend, eL, col}[128]
+constexpr uint32_t kGateStage = 5 * 512;
+constexpr uint32_t SUM = GATE + 2 * kGateStage;   // 2 heads' {row sums [4], column sums [2], v [2], q [2], du [2]}[128]
+constexpr uint32_t kSumStage = 12 * 512;
+constexpr uint32_t RED = SUM + 2 * kSumStage;     // 2 heads' {<A, H>, dD} per warp
+constexpr uint32_t BAR = RED + 2 * 64;
+constexpr uint32_t TOTAL = BAR + 256;
+}  // namespace sg
+static_assert(sg::TOTAL + 1024 <= 232448, "gradient kernel shared memory");
+
+enum GradBar {
+    gBc = 0, gXy = 1, gXyDone = 3, gXyFree = 5, gGate = 7, gGateFree = 9, gHd = 11, gHdFree, gS, gSRead, gR, gTu, gPReady, gUScaled,
+    gDx, gURead, gAll, gDrain, gBars
+};
+static_assert(gBars * 8 + 16 <= 256, "barrier room");
+
+// tensor-memory columns: S^T, then each head's R^T and, in its place, per 32 columns 16 packed of (R W s)^T and 16
+// of (S W)^T; dB; dC; C H; U
+constexpr uint32_t kTR = 0, kTdB = 128, kTdC = 256, kTT = 384, kTU = 448;
+constexpr int kGradTc = 352;  // eight compute warps, then products, copies, gates
+
+struct GradMaps {
+    CUtensorMap x, dy, b, c, dx;
+};
+struct GradTcArgs {
+    Seqs seqs;
+    int H, G, P, N, heads, splits;
+    long long rows;
+    const __nv_bfloat16 *step, *g;
+    const float* d;
+    const uint8_t *h0, *dh;
+    __nv_bfloat16 *dx, *db, *dc, *dstep, *dg;
+    long long ld_dx, ld_db, ld_dc;
+    float *part, *dd_part;
+    long long wait_ns;
+};
+
+__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Sum over the warp's lanes of each of 32 values: lane l returns the sum of v[l]. Halves the values at each step.
+__device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        const bool up = lane & d;
+#pragma unroll
+        for (int k = 0; k < d; ++k) {
+            const float keep = up ? v[k + d] : v[k], give = up ? v[k] : v[k + d];
+            v[k] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+        }
+    }
+    return v[0];
+}
+
+__global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ GradTcArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(sm);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + sg::BAR);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + sg::BAR + gBars * 8);
+    volatile int* err = reinterpret_cast<volatile int*>(sm + sg::BAR + gBars * 8 + 8);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int grp = blockIdx.x / a.splits, split = blockIdx.x - grp * a.splits, per = a.H / a.G;
+    const int h_lo = grp * per + split * a.heads, h_hi = min(h_lo + a.heads, (grp + 1) * per);
+    const int pbs = a.P / kCols, NI = uniform((h_hi - h_lo) * pbs);
+    Unit u;
+    const bool found = find_unit(a.seqs, kQ, blockIdx.y, u);
+    if (!found || u.len == 0) {  // no such chunk, or an empty sequence: nothing but its share of dD
+        if (a.dd_part)
+            for (int h = h_lo + tid; h < h_hi; h += kGradTc) a.dd_part[static_cast<size_t>(blockIdx.y) * a.H + h] = 0.f;
+        return;
+    }
+    const int n = uniform(u.len), row = uniform(u.row);
+    const bool tail = n < kQ;
+    const long long lim = a.wait_ns;
+    const uint32_t tile = a.N * 128;  // bytes of a saved state
+
+    if (tid == 0) {
+        for (int i = 0; i < gBars; ++i)
+            mbar_init(bars + i, i == gGateFree || i == gGateFree + 1 || i == gSRead || i == gPReady || i == gUScaled || i == gURead ? 8
+                                : i == gHdFree ? 9 : 1);
+        *err = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    if (warp < 8) {
+        // ---- row j of the transposed pair matrices (token j), half of their columns (and of 64 value columns)
+        const int q = warp & 3, half = warp >> 2, j = 32 * q + lane;
+        const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
+        bool ok = wait_bar(bars + gS, 0, lim, err);
+        uint32_t sp[2][16];  // this row and half of S^T, bf16 pairs: kept over the heads
+        if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                float x[32];
+                tmem_ld_cols<2>(lane_base + kTR + 64 * half + 32 * b, x);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) sp[b][k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(bars + gSRead);
+        }
+        float e_acc = 0.f, dd_acc = 0.f;
+        for (int it = 0; it < NI; ++it) {
+            const int st = it & 1, hi_ = it / pbs, pi = it - hi_ * pbs, h = h_lo + hi_;
+            const uint32_t ph = (it >> 1) & 1, ph1 = it & 1;
+            float* sums = reinterpret_cast<float*>(sm + sg::SUM + (hi_ & 1) * sg::kSumStage);
+            const float* arr = reinterpret_cast<const float*>(sm + sg::GATE + st * sg::kGateStage);
+            const bool fresh = pi == 0;
+            const float dk = a.d ? a.d[h] : 0.f;
+            uint8_t *xt = sm + sg::X + st * kTileBytes + j * 128, *yt = sm + sg::DY + st * kTileBytes + j * 128;
+            uint4 xr[4], yr[4];
+            float sj = 0.f, wej = 0.f, eLj = 0.f;
+            if (ok) ok = wait_bar(bars + gXy + st, ph, lim, err) && wait_bar(bars + gGate + st, ph, lim, err) && wait_bar(bars + gR, ph1, lim, err);
+            if (ok) {
+                tc_fence_after();
+                const float Lj = arr[j];
+                sj = arr[128 + j];
+                wej = arr[256 + j];
+                eLj = arr[384 + j];
+                float cols = 0.f;
+#pragma unroll
+                for (int bb = 0; bb < 2; ++bb) {
+                    const int b = 2 * half + bb;
+                    const uint32_t at = lane_base + kTR + 32 * b;
+                    uint8_t* p1t = sm + sg::P1 + half * kTileBytes + j * 128;
+                    uint32_t m1[16], m2[16];
+                    float rowsum = 0.f;
+                    if (b < q) {  // i before j
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) m1[k] = m2[k] = 0;
+                    } else {
+                        float x[32], pf[32];
+                        tmem_ld_cols<2>(at, x);
+                        const float rf = b > q ? ex2_approx(arr[32 * b - 1] - Lj) : 1.f;
+                        // Off the diagonal block the decay factors through the start of the column's block, both
+                        // factors <= 1; on it, one exponential per entry.
+#pragma unroll
+                        for (int k4 = 0; k4 < 8; ++k4) {
+                            const float4 f = *reinterpret_cast<const float4*>(arr + (b > q ? 512 : 0) + 32 * b + 4 * k4);
+                            const float fv[4] = {f.x, f.y, f.z, f.w};
+                            float p1[4], sl[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int k = 4 * k4 + e;
+                                float w;
+                                if (b > q) w = rf * fv[e];
+                                else w = k >= lane ? ex2_approx(fv[e] - Lj) : 0.f;
+                                const uint32_t s2 = sp[bb][k >> 1];
+                                const float S = __uint_as_float(k & 1 ? s2 & 0xffff0000u : s2 << 16);
+                                p1[e] = b == q && k < lane ? 0.f : x[k] * (w * sj);
+                                sl[e] = b == q && k < lane ? 0.f : S * w;
+                                pf[k] = b == q && k <= lane ? 0.f : S * p1[e];
+                                cols += pf[k];
+                            }
+                            m1[2 * k4] = pack_bf16x2(p1[0], p1[1]);
+                            m1[2 * k4 + 1] = pack_bf16x2(p1[2], p1[3]);
+                            m2[2 * k4] = pack_bf16x2(sl[0], sl[1]);
+                            m2[2 * k4 + 1] = pack_bf16x2(sl[2], sl[3]);
+                        }
+                        rowsum = transpose_sum(pf, lane);
+                    }
+                    tmem_st16(at, m1);
+                    tmem_st16(at + 16, m2);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<uint4*>(p1t + (((4 * bb + k) ^ (j & 7)) << 4)) = make_uint4(m1[4 * k], m1[4 * k + 1], m1[4 * k + 2], m1[4 * k + 3]);
+                    float* rs = sums + 128 * q + 32 * b + lane;  // token i = 32 b + lane, over this warp's rows
+                    *rs = fresh ? rowsum : *rs + rowsum;
+                }
+                float* cs = sums + 512 + 128 * half + j;
+                *cs = fresh ? cols : *cs + cols;
+                // X~ in place of X, e^{L} dY beside dY
+                uint8_t* wt = sm + sg::DYW + j * 128;
+                const float wx = sj * wej;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int cell = ((4 * half + k) ^ (j & 7)) << 4;
+                    xr[k] = *reinterpret_cast<const uint4*>(xt + cell);
+                    yr[k] = *reinterpret_cast<const uint4*>(yt + cell);
+                    float v[8];
+                    unpack8(xr[k], v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= wx;
+                    *reinterpret_cast<uint4*>(xt + cell) = pack8(v);
+                    unpack8(yr[k], v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= eLj;
+                    *reinterpret_cast<uint4*>(wt + cell) = pack8(v);
+                }
+                fence_proxy_async_smem();
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(bars + gPReady);
+                ok = wait_bar(bars + gHd, ph1, lim, err);
+            }
+            if (ok) {
+                if (j < a.N) {
+                    const uint8_t *ht = sm + sg::H0 + j * 128, *dt = sm + sg::DH + j * 128;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int cell = ((4 * half + k) ^ (j & 7)) << 4;
+                        float v[8], w[8];
+                        unpack8(*reinterpret_cast<const uint4*>(ht + cell), v);
+                        unpack8(*reinterpret_cast<const uint4*>(dt + cell), w);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) e_acc = fmaf(v[e], w[e], e_acc);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(bars + gHdFree);
+                ok = wait_bar(bars + gTu, ph1, lim, err);
+            }
+            if (ok) {
+                // B A in U's columns: its share of dg, then scaled as U's start; C H: its share of dg
+                tc_fence_after();
+                float t[32], vq = 0.f;
+                tmem_ld_cols<2>(lane_base + kTU + 32 * half, t);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float v[8];
+                    unpack8(xr[k], v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        vq = fmaf(v[e], t[8 * k + e], vq);
+                        t[8 * k + e] *= wej;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(t[16 * k + e]);
+                    tmem_st16(lane_base + kTU + 32 * half + 16 * k, r);
+                }
+                float* vs = sums + 768 + 128 * half + j;
+                vq *= sj * wej;
+                *vs = fresh ? vq : *vs + vq;
+                tmem_ld_cols<2>(lane_base + kTT + 32 * half, t);
+                vq = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float v[8];
+                    unpack8(yr[k], v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) vq = fmaf(v[e], t[8 * k + e], vq);
+                }
+                float* qs = sums + 1024 + 128 * half + j;
+                vq *= eLj;
+                *qs = fresh ? vq : *qs + vq;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(bars + gUScaled);
+                ok = wait_bar(bars + gDx, ph1, lim, err);
+            }
+            if (ok) {
+                tc_fence_after();
+                float t[32], du = 0.f;
+                tmem_ld_cols<2>(lane_base + kTU + 32 * half, t);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(bars + gURead);
+                __nv_bfloat16* to = a.dx + static_cast<size_t>(row + j) * a.ld_dx + static_cast<size_t>(h) * a.P + pi * kCols + 32 * half;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float v[8], w[8];
+                    unpack8(xr[k], v);
+                    unpack8(yr[k], w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        du = fmaf(v[e], t[8 * k + e], du);
+                        dd_acc = fmaf(v[e], w[e], dd_acc);
+                        w[e] = fmaf(dk, w[e], sj * t[8 * k + e]);
+                    }
+                    const uint4 o = pack8(w);
+                    if (!tail) *reinterpret_cast<uint4*>(yt + (((4 * half + k) ^ (j & 7)) << 4)) = o;
+                    else if (j < n) reinterpret_cast<uint4*>(to)[k] = o;
+                }
+                float* ds = sums + 1280 + 128 * half + j;
+                *ds = fresh ? du : *ds + du;
+                fence_proxy_async_smem();
+            }
+            const bool last = pi == pbs - 1;
+            float* red = reinterpret_cast<float*>(sm + sg::RED + (hi_ & 1) * 64);
+            if (last) {
+#pragma unroll
+                for (int d = 16; d; d >>= 1) {
+                    e_acc += __shfl_xor_sync(0xffffffffu, e_acc, d);
+                    dd_acc += __shfl_xor_sync(0xffffffffu, dd_acc, d);
+                }
+                if (lane == 0) {
+                    red[2 * warp] = e_acc;
+                    red[2 * warp + 1] = dd_acc;
+                }
+                e_acc = dd_acc = 0.f;
+            }
+            compute_sync();  // reached by all compute warps in every iteration, whatever happened
+            if (tid == 0 && ok) {
+                if (!tail) {
+                    tma_store_3d(&maps.dx, sm + sg::DY + st * kTileBytes, pi * kCols, h, row);
+                    bulk_commit();
+                    bulk_wait_read_all();
+                }
+                mbar_arrive1(bars + gXyFree + st);
+            }
+            if (last && warp == 1 && ok) {
+                // dg and dstep of the head: four tokens per lane
+                float E = 0.f, D = 0.f;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    E += red[2 * w];
+                    D += red[2 * w + 1];
+                }
+                if (a.dd_part && lane == 0) a.dd_part[static_cast<size_t>(blockIdx.y) * a.H + h] = D;
+                float s4[4], p4[4], v4[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 4 * lane + e;
+                    const float rs = (sums[t] + sums[128 + t]) + (sums[256 + t] + sums[384 + t]);
+                    s4[e] = rs - (sums[512 + t] + sums[640 + t]) + (sums[1024 + t] + sums[1152 + t]);
+                    v4[e] = sums[768 + t] + sums[896 + t];
+                }
+                s4[2] += s4[3]; s4[1] += s4[2]; s4[0] += s4[1];
+                p4[0] = 0.f; p4[1] = v4[0]; p4[2] = p4[1] + v4[1]; p4[3] = p4[2] + v4[2];
+                float suf = s4[0], pre = p4[3] + v4[3];
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const float x = __shfl_down_sync(0xffffffffu, suf, d), y = __shfl_up_sync(0xffffffffu, pre, d);
+                    if (lane + d < 32) suf += x;
+                    if (lane >= d) pre += y;
+                }
+                const float after = __shfl_down_sync(0xffffffffu, suf, 1), before = __shfl_up_sync(0xffffffffu, pre, 1);
+                const float sb_ = lane < 31 ? after : 0.f, pb_ = lane ? before : 0.f, tot = arr[384 + 127] * E;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 4 * lane + e;
+                    if (t < n) {
+                        const size_t at = static_cast<size_t>(row + t) * a.H + h;
+                        a.dg[at] = __float2bfloat16_rn((s4[e] + sb_) + (p4[e] + pb_) + tot);
+                        a.dstep[at] = __float2bfloat16_rn(sums[1280 + t] + sums[1408 + t]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(bars + gGateFree + st);
+        }
+        if (tid == 0) bulk_wait_all();
+        // dB and dC: rows j and i, 64 columns per half
+        if (ok) ok = wait_bar(bars + gAll, (NI - 1) & 1, lim, err);
+        if (ok && 64 * half < a.N) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int o = 0; o < 2; ++o) {
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t r[16];
+                    tmem_ld16(lane_base + (o ? kTdC : kTdB) + 64 * half + 16 * k, r);
+                    tmem_ld_wait();
+                    const int col = grp * a.N + 64 * half + 16 * k;
+                    if (j < n) {
+                        if (a.splits == 1) {
+                            uint4* to = reinterpret_cast<uint4*>((o ? a.dc : a.db) + static_cast<size_t>(row + j) * (o ? a.ld_dc : a.ld_db) + col);
+                            float f[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(r[e]);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                to[e] = make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
+                                                   pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
+                        } else {
+                            const size_t gn = static_cast<size_t>(a.G) * a.N;
+                            uint4* to = reinterpret_cast<uint4*>(a.part + ((static_cast<size_t>(o) * a.splits + split) * a.rows + row + j) * gn + col);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) to[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+                        }
+                    }
+                }
+            }
+        }
+    } else if (warp == 8) {
+        // ---- products
+        const uint32_t lead = elect_one();
+        const uint32_t dk = uniform(desc_lo(sb, 16)), dm = uniform(desc_lo(sb, kTileBytes));
+        const uint32_t id_kk = idesc_bf16(128, 128, false, false), id_t = idesc_bf16(128, 64, false, true);
+        const uint32_t id_nk = idesc_bf16(128, a.N, false, false), id_nm = idesc_bf16(128, a.N, false, true), id_mm = idesc_bf16(128, a.N, true, true);
+        const int ks = a.N / 16;
+        auto wait = [&](int bar, uint32_t parity) {
+            const bool w = wait_bar(bars + bar, parity, lim, err);
+            tc_fence_after();
+            return w;
+        };
+        constexpr uint32_t kT = kTileBytes >> 4;
+        bool ok = wait(gBc, 0) && (!tail || wait(gGate, 0));
+        if (ok) {
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                if (s < ks) mma_by(lead, kTR, dk + (sg::B >> 4) + (s >> 2) * kT + (s & 3) * 2, dk + (sg::C >> 4) + (s >> 2) * kT + (s & 3) * 2, id_kk, s > 0);
+            commit_by(lead, bars + gS);
+        }
+        for (int it = 0; ok && it < NI; ++it) {
+            const int st = it & 1;
+            const uint32_t ph = (it >> 1) & 1, ph1 = it & 1;
+            const uint32_t xo = (sg::X + st * kTileBytes) >> 4, yo = (sg::DY + st * kTileBytes) >> 4;
+            if (!(ok = wait(gXy + st, ph) && (!tail || wait(gGate + st, ph)) && (it ? wait(gAll, ph1 ^ 1) : wait(gSRead, 0)))) break;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) mma_by(lead, kTR, dk + xo + s * 2, dk + yo + s * 2, id_kk, s > 0);  // R^T = X dY^T
+            commit_by(lead, bars + gR);
+            if (!(ok = wait(gHd, ph1) && (it == 0 || wait(gURead, ph1 ^ 1)))) break;
+#pragma unroll
+            for (int s = 0; s < 8; ++s)  // C H and B A
+                if (s < ks) mma_by(lead, kTT, dk + (sg::C >> 4) + (s >> 2) * kT + (s & 3) * 2, dm + (sg::H0 >> 4) + s * 128, id_t, s > 0);
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                if (s < ks) mma_by(lead, kTU, dk + (sg::B >> 4) + (s >> 2) * kT + (s & 3) * 2, dm + (sg::DH >> 4) + s * 128, id_t, s > 0);
+            commit_by(lead, bars + gTu);
+            if (!(ok = wait(gPReady, ph1))) break;
+#pragma unroll
+            for (int s = 0; s < 8; ++s)  // dB += (R W s)^T C + X~ A^T
+                mma_ts_by(lead, kTdB, kTR + 32 * (s >> 1) + 8 * (s & 1), dm + (sg::C >> 4) + s * 128, id_nm, it > 0 || s > 0);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) mma_by(lead, kTdB, dk + xo + s * 2, dk + (sg::DH >> 4) + s * 2, id_nk, 1);
+            if (!(ok = wait(gUScaled, ph1))) break;
+#pragma unroll
+            for (int s = 0; s < 8; ++s)  // U += (S W)^T dY
+                mma_ts_by(lead, kTU, kTR + 32 * (s >> 1) + 16 + 8 * (s & 1), dm + yo + s * 128, id_t, 1);
+            commit_by(lead, bars + gDx);
+#pragma unroll
+            for (int s = 0; s < 8; ++s)  // dC += (R W s) B + (e^L dY) H^T
+                mma_by(lead, kTdC, dm + (sg::P1 >> 4) + s * 128, dm + (sg::B >> 4) + s * 128, id_mm, it > 0 || s > 0);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) mma_by(lead, kTdC, dk + (sg::DYW >> 4) + s * 2, dk + (sg::H0 >> 4) + s * 2, id_nk, 1);
+            commit_by(lead, bars + gAll);
+            commit_by(lead, bars + gXyDone + st);
+            commit_by(lead, bars + gHdFree);
+        }
+        commit_by(lead, bars + gDrain);
+        mbar_wait(bars + gDrain, 0, kDefaultWaitNs);
+    } else if (warp == 9) {
+        // ---- copies
+        if (lane == 0) {
+            const int halves = a.N / 64;
+            mbar_arrive_expect_tx(bars + gBc, kTileBytes * 2 * halves);
+            for (int k = 0; k < halves; ++k) {
+                tma_load_3d(sm + sg::B + k * kTileBytes, &maps.b, 64 * k, grp, row, bars + gBc);
+                tma_load_3d(sm + sg::C + k * kTileBytes, &maps.c, 64 * k, grp, row, bars + gBc);
+            }
+            int xy = 0, hd = 0;
+            auto load_xy = [&](int it) {
+                const int st = it & 1, hh = h_lo + it / pbs, pi = it % pbs;
+                const uint32_t ph = (it >> 1) & 1;
+                if (it >= 2 && !(mbar_wait_or_abort(bars + gXyDone + st, ph ^ 1, lim, err) && mbar_wait_or_abort(bars + gXyFree + st, ph ^ 1, lim, err)))
+                    return false;
+                mbar_arrive_expect_tx(bars + gXy + st, 2 * kTileBytes);
+                tma_load_3d(sm + sg::X + st * kTileBytes, &maps.x, pi * kCols, hh, row, bars + gXy + st);
+                tma_load_3d(sm + sg::DY + st * kTileBytes, &maps.dy, pi * kCols, hh, row, bars + gXy + st);
+                ++xy;
+                return true;
+            };
+            bool ok = load_xy(0);
+            for (int it = 0; ok && it < NI; ++it) {
+                // H and A have one buffer: asked for once this block's previous products and sums have read it
+                if (it >= 1 && !(ok = mbar_wait_or_abort(bars + gHdFree, (it - 1) & 1, lim, err))) break;
+                const size_t at = ((static_cast<size_t>(blockIdx.y) * a.H + h_lo + it / pbs) * pbs + it % pbs) * tile;
+                mbar_arrive_expect_tx(bars + gHd, 2 * tile);
+                bulk_load(sm + sg::H0, a.h0 + at, tile, bars + gHd);
+                bulk_load(sm + sg::DH, a.dh + at, tile, bars + gHd);
+                ++hd;
+                if (it + 1 < NI) ok = load_xy(it + 1);
+            }
+            if (!ok) note_failure(err);
+            mbar_wait(bars + gBc, 0, kDefaultWaitNs);  // nothing in flight when the block ends
+            for (int it = xy > 2 ? xy - 2 : 0; it < xy; ++it) mbar_wait(bars + gXy + (it & 1), (it >> 1) & 1, kDefaultWaitNs);
+            if (hd) mbar_wait(bars + gHd, (hd - 1) & 1, kDefaultWaitNs);
+        }
+    } else {
+        // ---- gates: four tokens per lane; and the rows past the sequence cleared
+        float gn[4], sn[4];
+        auto fetch = [&](int it) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = 4 * lane + e;
+                const size_t at = static_cast<size_t>(row + t) * a.H + h_lo + it / pbs;
+                gn[e] = t < n ? ssm_gate(__bfloat162float(a.g[at])) * kLog2e : 0.f;
+                sn[e] = t < n ? __bfloat162float(a.step[at]) : 0.f;
+            }
+        };
+        fetch(0);
+        for (int it = 0; it < NI; ++it) {
+            const int st = it & 1;
+            const uint32_t ph = (it >> 1) & 1;
+            if (it >= 2 && !wait_bar(bars + gGateFree + st, ph ^ 1, lim, err)) break;
+            if (tail) {
+                const uint4 z = make_uint4(0, 0, 0, 0);
+                if (it == 0) {
+                    if (!wait_bar(bars + gBc, 0, lim, err)) break;
+                    for (int k = 0; k < 4; ++k)
+                        for (int i = n * 8 + lane; i < kQ * 8; i += 32) reinterpret_cast<uint4*>(sm + sg::B + k * kTileBytes)[i] = z;
+                }
+                if (!wait_bar(bars + gXy + st, ph, lim, err)) break;
+                for (int i = n * 8 + lane; i < kQ * 8; i += 32) {
+                    reinterpret_cast<uint4*>(sm + sg::X + st * kTileBytes)[i] = z;
+                    reinterpret_cast<uint4*>(sm + sg::DY + st * kTileBytes)[i] = z;
+                }
+                fence_proxy_async_smem();
+            }
+            float* arr = reinterpret_cast<float*>(sm + sg::GATE + st * sg::kGateStage);
+            float p[4], sfx[4];
+            p[0] = gn[0]; p[1] = p[0] + gn[1]; p[2] = p[1] + gn[2]; p[3] = p[2] + gn[3];
+            sfx[3] = 0.f; sfx[2] = gn[3]; sfx[1] = sfx[2] + gn[2]; sfx[0] = sfx[1] + gn[1];
+            float pre = p[3], suf = p[3];
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const float x = __shfl_up_sync(0xffffffffu, pre, d), y = __shfl_down_sync(0xffffffffu, suf, d);
+                if (lane >= d) pre += x;
+                if (lane + d < 32) suf += y;
+            }
+            const float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
+            const float lo = lane ? before : 0.f, hi = lane < 31 ? after : 0.f;
+            const float start = __shfl_sync(0xffffffffu, lo, lane & ~7);  // L before the 32-token block
+            const float4 L = make_float4(lo + p[0], lo + p[1], lo + p[2], lo + p[3]);
+            reinterpret_cast<float4*>(arr)[lane] = L;
+            reinterpret_cast<float4*>(arr + 128)[lane] = make_float4(sn[0], sn[1], sn[2], sn[3]);
+            reinterpret_cast<float4*>(arr + 256)[lane] = exp2_4(make_float4(hi + sfx[0], hi + sfx[1], hi + sfx[2], hi + sfx[3]));
+            reinterpret_cast<float4*>(arr + 384)[lane] = exp2_4(L);
+            reinterpret_cast<float4*>(arr + 512)[lane] = exp2_4(make_float4(L.x - start, L.y - start, L.z - start, L.w - start));
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(bars + gGate + st);
+            if (it + 1 < NI) fetch(it + 1);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(*tmem_slot, 512);
+}
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 152;
+    return n;
+}
+
+// Heads per block: the number of waves times (heads + the block's own cost, about a head and a half) is least.
+int grad_heads_tc(const ScanShape& sh) {
+    const int per = sh.H / sh.G, sms = sm_count();
+    const long long chunks = sh.seqs.units(kQ) * sh.G;
+    int best = per;
+    double cost = 1e30;
+    for (int splits = 1; splits <= per; ++splits) {
+        const int heads = (per + splits - 1) / splits;
+        if ((per + heads - 1) / heads != splits) continue;
+        const double waves = static_cast<double>((chunks * splits + sms - 1) / sms);
+        const double c = waves * (heads * (sh.P / kCols) + 1.5) * (1 + 0.02 * splits);
+        if (c < cost) {
+            cost = c;
+            best = heads;
+        }
+    }
+    return best;
+}
+
+// The walk over chunks: whole sequences while both directions' blocks about fill the SMs, else units of 1024 tokens
+// or more whose starting states come from a pass over their increments first.
+int walk_unit_tc(const ScanShape& sh) {
+    const long long chains = 2LL * sh.seqs.B * sh.H * (sh.P / kCols), sms = sm_count();
+    const int whole = (sh.seqs.T + kQ - 1) / kQ * kQ;
+    if (10 * chains >= 8 * sms) return whole;
+    const long long rows = sh.seqs.rows(), units = (2 * sms * sh.seqs.B + chains - 1) / chains;
+    long long len = ((rows + units - 1) / units + kQ - 1) / kQ * kQ;
+    if (len < 1024) len = 1024;
+    return len >= whole ? whole : static_cast<int>(len);
+}
+
+struct BwdTc {
+    int unit, heads, splits;
+    bool cut;
+    size_t h0, dh, dd, part, states, states_b, decay, decay_b, total;  // bytes
+};
+BwdTc bwd_plan(const ScanShape& sh) {
+    BwdTc p;
+    p.unit = walk_unit_tc(sh);
+    p.cut = p.unit < sh.seqs.T;
+    p.heads = grad_heads_tc(sh);
+    p.splits = (sh.H / sh.G + p.heads - 1) / p.heads;
+    const size_t chunks = static_cast<size_t>(sh.seqs.units(kQ)), st = chunks * sh.H * sh.N * sh.P * 2;
+    const size_t units = p.cut ? static_cast<size_t>(sh.seqs.units(p.unit)) : 0, us = units * sh.H * sh.N * sh.P * 4;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += align_up(bytes, 256);
+        return here;
+    };
+    p.h0 = take(st);
+    p.dh = take(st);
+    p.dd = take(chunks * sh.H * 4);
+    p.part = take(p.splits > 1 ? 2ull * p.splits * sh.seqs.rows() * sh.G * sh.N * 4 : 0);
+    p.states = take(us);
+    p.states_b = take(us);
+    p.decay = take(units * sh.H * 4);
+    p.decay_b = take(units * sh.H * 4);
+    p.total = at;
+    return p;
+}
+
+}  // namespace
+
+size_t ssm_tc_bwd_workspace(const ScanShape& sh) { return bwd_plan(sh).total; }
+
+cudaError_t launch_ssm_tc_bwd(const ScanShape& sh, const ScanIn& in, const ScanGrads& gr, void* wsv, cudaStream_t s, long long wait_ns) {
+    uint8_t* ws = static_cast<uint8_t*>(wsv);
+    const BwdTc p = bwd_plan(sh);
+    auto f = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
+    const WalkJob jobs[2] = {{in.bm, in.x, in.s0, nullptr, f(p.states), f(p.decay), ws + p.h0, 0},
+                             {in.cm, gr.dy, gr.ds1, gr.ds0, f(p.states_b), f(p.decay_b), ws + p.dh, 1}};
+    cudaError_t e;
+    // d_initial_state is a result in fp32; the saved states feed bf16 results
+    const int exact = gr.ds0 != nullptr;
+    if (p.cut) {
+        if ((e = launch_ssm_walk_tc(sh, in.step, in.g, jobs, 2, p.unit, 1, 0, exact, s, wait_ns)) != cudaSuccess) return e;
+        if ((e = launch_ssm_chain(sh, p.unit, in.s0, nullptr, f(p.states), f(p.decay), 0, s)) != cudaSuccess) return e;
+        if ((e = launch_ssm_chain(sh, p.unit, gr.ds1, gr.ds0, f(p.states_b), f(p.decay_b), 1, s)) != cudaSuccess) return e;
+        WalkJob again[2] = {jobs[0], jobs[1]};
+        again[1].last = nullptr;  // the chain has written it
+        e = launch_ssm_walk_tc(sh, in.step, in.g, again, 2, p.unit, 0, 1, 0, s, wait_ns);
+    } else {
+        e = launch_ssm_walk_tc(sh, in.step, in.g, jobs, 2, p.unit, 0, 0, exact, s, wait_ns);
+    }
+    if (e != cudaSuccess) return e;
+    GradMaps maps;
+    const long long rows = sh.seqs.rows();
+    if (!rows_map(&maps.x, in.x.p, in.x.ld, sh.P, sh.H, rows, kQ) || !rows_map(&maps.dy, gr.dy.p, gr.dy.ld, sh.P, sh.H, rows, kQ) ||
+        !rows_map(&maps.b, in.bm.p, in.bm.ld, sh.N, sh.G, rows, kQ) || !rows_map(&maps.c, in.cm.p, in.cm.ld, sh.N, sh.G, rows, kQ) ||
+        !rows_map(&maps.dx, gr.dx.p, gr.dx.ld, sh.P, sh.H, rows, kQ))
+        return cudaErrorInvalidValue;
+    GradTcArgs a{};
+    a.seqs = sh.seqs;
+    a.H = sh.H; a.G = sh.G; a.P = sh.P; a.N = sh.N;
+    a.heads = p.heads;
+    a.splits = p.splits;
+    a.rows = rows;
+    using BF = __nv_bfloat16;
+    a.step = static_cast<const BF*>(in.step);
+    a.g = static_cast<const BF*>(in.g);
+    a.d = in.d;
+    a.h0 = ws + p.h0;
+    a.dh = ws + p.dh;
+    a.dx = static_cast<BF*>(gr.dx.p);
+    a.db = static_cast<BF*>(gr.dbm.p);
+    a.dc = static_cast<BF*>(gr.dcm.p);
+    a.dstep = static_cast<BF*>(gr.dstep);
+    a.dg = static_cast<BF*>(gr.dg);
+    a.ld_dx = gr.dx.ld;
+    a.ld_db = gr.dbm.ld;
+    a.ld_dc = gr.dcm.ld;
+    a.part = f(p.part);
+    a.dd_part = gr.dd ? f(p.dd) : nullptr;
+    a.wait_ns = wait_ns;
+    if ((e = cudaFuncSetAttribute(grad_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448)) != cudaSuccess) return e;
+    // groups' shares of one chunk next to each other: B, C and the gates stay in L2
+    grad_tc_kernel<<<dim3(sh.G * p.splits, static_cast<unsigned>(sh.seqs.units(kQ))), kGradTc, 232448, s>>>(maps, a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return launch_ssm_grad_sums(sh, gr, a.part, p.splits, a.dd_part, static_cast<int>(sh.seqs.units(kQ)), s);
+}
+
+int ssm_tc_grad_read_clear_status(cudaStream_t s) { return read_clear_status(s); }
+
+}  // namespace gdn2
