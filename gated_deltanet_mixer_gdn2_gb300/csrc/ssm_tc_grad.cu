@@ -168,31 +168,44 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
                     } else {
                         float x[32], pf[32];
                         tmem_ld_cols<2>(at, x);
-                        const float rf = b > q ? ex2_approx(arr[32 * b - 1] - Lj) : 1.f;
-                        // Off the diagonal block the decay factors through the start of the column's block, both
-                        // factors <= 1; on it, one exponential per entry.
+                        if (b > q) {
+                            // Off the diagonal block the decay factors through the start of the column's block,
+                            // both factors <= 1: an exponential per row and block.
+                            const float rf = ex2_approx(arr[32 * b - 1] - Lj);
+                            const uint64_t rf2 = f32x2(rf, rf), sj2 = f32x2(sj, sj);
+                            uint64_t c2 = 0;
 #pragma unroll
-                        for (int k4 = 0; k4 < 8; ++k4) {
-                            const float4 f = *reinterpret_cast<const float4*>(arr + (b > q ? 512 : 0) + 32 * b + 4 * k4);
-                            const float fv[4] = {f.x, f.y, f.z, f.w};
-                            float p1[4], sl[4];
+                            for (int k4 = 0; k4 < 8; ++k4) {
+                                const float4 f = *reinterpret_cast<const float4*>(arr + 512 + 32 * b + 4 * k4);
+                                const uint64_t fv[2] = {f32x2(f.x, f.y), f32x2(f.z, f.w)};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int k = 4 * k4 + e;
-                                float w;
-                                if (b > q) w = rf * fv[e];
-                                else w = k >= lane ? ex2_approx(fv[e] - Lj) : 0.f;
-                                const uint32_t s2 = sp[bb][k >> 1];
-                                const float S = __uint_as_float(k & 1 ? s2 & 0xffff0000u : s2 << 16);
-                                p1[e] = b == q && k < lane ? 0.f : x[k] * (w * sj);
-                                sl[e] = b == q && k < lane ? 0.f : S * w;
-                                pf[k] = b == q && k <= lane ? 0.f : S * p1[e];
-                                cols += pf[k];
+                                for (int e = 0; e < 2; ++e) {
+                                    const int k = 2 * k4 + e;
+                                    const uint64_t w = mul_f32x2(rf2, fv[e]), S = bf16x2_widen(sp[bb][k]);
+                                    const uint64_t p1 = mul_f32x2(f32x2(x[2 * k], x[2 * k + 1]), mul_f32x2(w, sj2)), pp = mul_f32x2(S, p1);
+                                    c2 = add_f32x2(c2, pp);
+                                    f32x2_split(pp, pf[2 * k], pf[2 * k + 1]);
+                                    m1[k] = bf16x2_narrow(p1);
+                                    m2[k] = bf16x2_narrow(mul_f32x2(S, w));
+                                }
                             }
-                            m1[2 * k4] = pack_bf16x2(p1[0], p1[1]);
-                            m1[2 * k4 + 1] = pack_bf16x2(p1[2], p1[3]);
-                            m2[2 * k4] = pack_bf16x2(sl[0], sl[1]);
-                            m2[2 * k4 + 1] = pack_bf16x2(sl[2], sl[3]);
+                            float c0, c1;
+                            f32x2_split(c2, c0, c1);
+                            cols += c0 + c1;
+                        } else {
+                            // on the diagonal block an exponential per entry, i >= j
+#pragma unroll
+                            for (int k2 = 0; k2 < 16; ++k2) {
+                                const float2 f = *reinterpret_cast<const float2*>(arr + 32 * b + 2 * k2);
+                                const float w0 = 2 * k2 >= lane ? ex2_approx(f.x - Lj) : 0.f, w1 = 2 * k2 + 1 >= lane ? ex2_approx(f.y - Lj) : 0.f;
+                                const float S0 = __uint_as_float(sp[bb][k2] << 16), S1 = __uint_as_float(sp[bb][k2] & 0xffff0000u);
+                                const float p0 = x[2 * k2] * (w0 * sj), p1 = x[2 * k2 + 1] * (w1 * sj);
+                                pf[2 * k2] = 2 * k2 > lane ? S0 * p0 : 0.f;
+                                pf[2 * k2 + 1] = 2 * k2 + 1 > lane ? S1 * p1 : 0.f;
+                                cols += pf[2 * k2] + pf[2 * k2 + 1];
+                                m1[k2] = pack_bf16x2(p0, p1);
+                                m2[k2] = pack_bf16x2(S0 * w0, S1 * w1);
+                            }
                         }
                         rowsum = transpose_sum(pf, lane);
                     }
