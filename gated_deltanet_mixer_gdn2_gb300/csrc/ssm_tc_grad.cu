@@ -28,24 +28,23 @@ constexpr uint32_t DH = H0 + kTileBytes;
 constexpr uint32_t P1 = DH + kTileBytes;          // (R W s)^T [j][i]: 2 tiles
 constexpr uint32_t GATE = P1 + 2 * kTileBytes;    // 2 stages x {L, s, wend, eL, col}[128]
 constexpr uint32_t kGateStage = 5 * 512;
-constexpr uint32_t SUM = GATE + 2 * kGateStage;   // 2 heads' {row sums [4], column sums [2], v [2], q [2], du [2]}[128]
-constexpr uint32_t kSumStage = 12 * 512;
-constexpr uint32_t RED = SUM + 2 * kSumStage;     // 2 heads' {<A, H>, dD} per warp
-constexpr uint32_t BAR = RED + 2 * 64;
+constexpr uint32_t SUM = GATE + 2 * kGateStage;   // a head's {row sums, column sums, v, q, du}[4][128]
+constexpr uint32_t RED = SUM + 20 * 512;          // a head's {<A, H>, dD} per warp
+constexpr uint32_t BAR = RED + 128;
 constexpr uint32_t TOTAL = BAR + 256;
 }  // namespace sg
 static_assert(sg::TOTAL + 1024 <= 232448, "gradient kernel shared memory");
 
 enum GradBar {
     gBc = 0, gXy = 1, gXyDone = 3, gXyFree = 5, gGate = 7, gGateFree = 9, gHd = 11, gHdFree, gS, gSRead, gR, gTu, gPReady, gUScaled,
-    gDx, gURead, gAll, gDrain, gBars
+    gDx, gURead, gAll, gSumFree, gOut, gDrain = gOut + 2, gBars
 };
 static_assert(gBars * 8 + 16 <= 256, "barrier room");
 
-// tensor-memory columns: S^T, then each head's R^T and, in its place, per 32 columns 16 packed of (R W s)^T and 16
+// tensor-memory columns: S^T, then each head's R^T and, in its place, per 16 columns 8 packed of (R W s)^T and 8
 // of (S W)^T; dB; dC; C H; U
 constexpr uint32_t kTR = 0, kTdB = 128, kTdC = 256, kTT = 384, kTU = 448;
-constexpr int kGradTc = 352;  // eight compute warps, then products, copies, gates
+constexpr int kGradTc = 640;  // sixteen compute warps, then products, copies, gates, results
 
 struct GradMaps {
     CUtensorMap x, dy, b, c, dx;
@@ -63,12 +62,10 @@ struct GradTcArgs {
     long long wait_ns;
 };
 
-__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-
-// Sum over the warp's lanes of each of 32 values: lane l returns the sum of v[l]. Halves the values at each step.
-__device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
+// Sum over the warp's lanes of each of 16 values: lane l returns the sum of v[l mod 16]. Each step halves the values.
+__device__ __forceinline__ float transpose_sum(float (&v)[16], int lane) {
 #pragma unroll
-    for (int d = 16; d; d >>= 1) {
+    for (int d = 8; d; d >>= 1) {
         const bool up = lane & d;
 #pragma unroll
         for (int k = 0; k < d; ++k) {
@@ -76,7 +73,13 @@ __device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
             v[k] = keep + __shfl_xor_sync(0xffffffffu, give, d);
         }
     }
-    return v[0];
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ GradTcArgs a) {
@@ -104,8 +107,8 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
 
     if (tid == 0) {
         for (int i = 0; i < gBars; ++i)
-            mbar_init(bars + i, i == gGateFree || i == gGateFree + 1 || i == gSRead || i == gPReady || i == gUScaled || i == gURead ? 8
-                                : i == gHdFree ? 9 : 1);
+            mbar_init(bars + i, i == gSRead || i == gPReady || i == gUScaled || i == gURead || i == gOut || i == gOut + 1 ? 16
+                                : i == gGateFree || i == gGateFree + 1 || i == gHdFree ? 17 : 1);
         *err = 0;
         fence_mbar_init();
     }
@@ -117,203 +120,196 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
     __syncthreads();
     tc_fence_after();
 
-    if (warp < 8) {
-        // ---- row j of the transposed pair matrices (token j), half of their columns (and of 64 value columns)
-        const int q = warp & 3, half = warp >> 2, j = 32 * q + lane;
-        const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
+    if (warp < 16) {
+        // ---- row j of the transposed pair matrices (token j): one of their four blocks of 32 columns, and 16 of the
+        // 64 value columns, per thread
+        const int q = warp & 3, b = warp >> 2, j = 32 * q + lane;
+        const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16, pair = lane_base + kTR + 32 * b, val = lane_base + 16 * b;
+        float* const sums = reinterpret_cast<float*>(sm + sg::SUM);
         bool ok = wait_bar(bars + gS, 0, lim, err);
-        uint32_t sp[2][16];  // this row and half of S^T, bf16 pairs: kept over the heads
+        uint32_t sp[2][8];  // this row and block of S^T, bf16 pairs: kept over the heads
         if (ok) {
             tc_fence_after();
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                float x[32];
-                tmem_ld_cols<2>(lane_base + kTR + 64 * half + 32 * b, x);
+            for (int k = 0; k < 2; ++k) {
+                float x[16];
+                tmem_ld_cols<1>(pair + 16 * k, x);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) sp[b][k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+                for (int e = 0; e < 8; ++e) sp[k][e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive1(bars + gSRead);
         }
         float e_acc = 0.f, dd_acc = 0.f;
-        for (int it = 0; it < NI; ++it) {
-            const int st = it & 1, hi_ = it / pbs, pi = it - hi_ * pbs, h = h_lo + hi_;
+        int pi = 0, h = h_lo;
+        for (int it = 0; ok && it < NI; ++it) {
+            const int st = it & 1;
             const uint32_t ph = (it >> 1) & 1, ph1 = it & 1;
-            float* sums = reinterpret_cast<float*>(sm + sg::SUM + (hi_ & 1) * sg::kSumStage);
             const float* arr = reinterpret_cast<const float*>(sm + sg::GATE + st * sg::kGateStage);
             const bool fresh = pi == 0;
-            const float dk = a.d ? a.d[h] : 0.f;
             uint8_t *xt = sm + sg::X + st * kTileBytes + j * 128, *yt = sm + sg::DY + st * kTileBytes + j * 128;
-            uint4 xr[4], yr[4];
-            float sj = 0.f, wej = 0.f, eLj = 0.f;
-            if (ok) ok = wait_bar(bars + gXy + st, ph, lim, err) && wait_bar(bars + gGate + st, ph, lim, err) && wait_bar(bars + gR, ph1, lim, err);
-            if (ok) {
-                tc_fence_after();
-                const float Lj = arr[j];
-                sj = arr[128 + j];
-                wej = arr[256 + j];
-                eLj = arr[384 + j];
-                float cols = 0.f;
+            const int cell0 = ((2 * b) ^ (j & 7)) << 4, cell1 = ((2 * b + 1) ^ (j & 7)) << 4;
+            if (!(ok = wait_bar(bars + gXy + st, ph, lim, err) && wait_bar(bars + gGate + st, ph, lim, err) && wait_bar(bars + gR, ph1, lim, err))) break;
+            tc_fence_after();
+            const float Lj = arr[j], sj = arr[128 + j], wej = arr[256 + j], eLj = arr[384 + j];
+            float cols = 0.f;
+            uint8_t* p1t = sm + sg::P1 + (b >> 1) * kTileBytes + j * 128;
+            const float dk = a.d ? __ldg(a.d + h) : 0.f;
+            float* rs = sums + 128 * q + 32 * b + (lane & 15);  // row sums of tokens i, over this warp's rows
+            float rsum[2] = {0.f, 0.f};
+            if (b < q) {  // every i of the block lies before every j
+                const uint32_t z[8] = {};
 #pragma unroll
-                for (int bb = 0; bb < 2; ++bb) {
-                    const int b = 2 * half + bb;
-                    const uint32_t at = lane_base + kTR + 32 * b;
-                    uint8_t* p1t = sm + sg::P1 + half * kTileBytes + j * 128;
-                    uint32_t m1[16], m2[16];
-                    float rowsum = 0.f;
-                    if (b < q) {  // i before j
+                for (int k = 0; k < 4; ++k) tmem_st8(pair + 8 * k, z);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) m1[k] = m2[k] = 0;
-                    } else {
-                        float x[32], pf[32];
-                        tmem_ld_cols<2>(at, x);
-                        if (b > q) {
-                            // Off the diagonal block the decay factors through the start of the column's block,
-                            // both factors <= 1: an exponential per row and block.
-                            const float rf = ex2_approx(arr[32 * b - 1] - Lj);
-                            const uint64_t rf2 = f32x2(rf, rf), sj2 = f32x2(sj, sj);
-                            uint64_t c2 = 0;
+                for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(p1t + (((4 * (b & 1) + k) ^ (j & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+            } else {
+                const bool off = b > q;
+                // Off the diagonal block the decay factors through the start of the column's block, both factors <= 1:
+                // an exponential per row and block. On it, an exponential per entry.
+                const float rf = off ? ex2_approx(arr[32 * b - 1] - Lj) : 1.f;
 #pragma unroll
-                            for (int k4 = 0; k4 < 8; ++k4) {
-                                const float4 f = *reinterpret_cast<const float4*>(arr + 512 + 32 * b + 4 * k4);
-                                const uint64_t fv[2] = {f32x2(f.x, f.y), f32x2(f.z, f.w)};
+                for (int sub = 0; sub < 2; ++sub) {
+                    float x[16], pf[16];
+                    uint32_t m1[8], m2[8];
+                    tmem_ld_cols<1>(pair + 16 * sub, x);
+                    if (off) {
+                        const uint64_t rf2 = f32x2(rf, rf), sj2 = f32x2(sj, sj);
+                        uint64_t c2 = 0;
 #pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const int k = 2 * k4 + e;
-                                    const uint64_t w = mul_f32x2(rf2, fv[e]), S = bf16x2_widen(sp[bb][k]);
-                                    const uint64_t p1 = mul_f32x2(f32x2(x[2 * k], x[2 * k + 1]), mul_f32x2(w, sj2)), pp = mul_f32x2(S, p1);
-                                    c2 = add_f32x2(c2, pp);
-                                    f32x2_split(pp, pf[2 * k], pf[2 * k + 1]);
-                                    m1[k] = bf16x2_narrow(p1);
-                                    m2[k] = bf16x2_narrow(mul_f32x2(S, w));
-                                }
-                            }
-                            float c0, c1;
-                            f32x2_split(c2, c0, c1);
-                            cols += c0 + c1;
-                        } else {
-                            // on the diagonal block an exponential per entry, i >= j
+                        for (int k4 = 0; k4 < 4; ++k4) {
+                            const float4 f = *reinterpret_cast<const float4*>(arr + 512 + 32 * b + 16 * sub + 4 * k4);
+                            const uint64_t fv[2] = {f32x2(f.x, f.y), f32x2(f.z, f.w)};
 #pragma unroll
-                            for (int k2 = 0; k2 < 16; ++k2) {
-                                const float2 f = *reinterpret_cast<const float2*>(arr + 32 * b + 2 * k2);
-                                const float w0 = 2 * k2 >= lane ? ex2_approx(f.x - Lj) : 0.f, w1 = 2 * k2 + 1 >= lane ? ex2_approx(f.y - Lj) : 0.f;
-                                const float S0 = __uint_as_float(sp[bb][k2] << 16), S1 = __uint_as_float(sp[bb][k2] & 0xffff0000u);
-                                const float p0 = x[2 * k2] * (w0 * sj), p1 = x[2 * k2 + 1] * (w1 * sj);
-                                pf[2 * k2] = 2 * k2 > lane ? S0 * p0 : 0.f;
-                                pf[2 * k2 + 1] = 2 * k2 + 1 > lane ? S1 * p1 : 0.f;
-                                cols += pf[2 * k2] + pf[2 * k2 + 1];
-                                m1[k2] = pack_bf16x2(p0, p1);
-                                m2[k2] = pack_bf16x2(S0 * w0, S1 * w1);
+                            for (int e = 0; e < 2; ++e) {
+                                const int k = 2 * k4 + e;
+                                const uint64_t w = mul_f32x2(rf2, fv[e]), S = bf16x2_widen(sp[sub][k]);
+                                const uint64_t p1 = mul_f32x2(f32x2(x[2 * k], x[2 * k + 1]), mul_f32x2(w, sj2)), pp = mul_f32x2(S, p1);
+                                c2 = add_f32x2(c2, pp);
+                                f32x2_split(pp, pf[2 * k], pf[2 * k + 1]);
+                                m1[k] = bf16x2_narrow(p1);
+                                m2[k] = bf16x2_narrow(mul_f32x2(S, w));
                             }
                         }
-                        rowsum = transpose_sum(pf, lane);
+                        float c0, c1;
+                        f32x2_split(c2, c0, c1);
+                        cols += c0 + c1;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int i0 = 16 * sub + 2 * k;
+                            const float2 f = *reinterpret_cast<const float2*>(arr + 32 * b + i0);
+                            const float w0 = i0 >= lane ? ex2_approx(f.x - Lj) : 0.f, w1 = i0 + 1 >= lane ? ex2_approx(f.y - Lj) : 0.f;
+                            const float S0 = __uint_as_float(sp[sub][k] << 16), S1 = __uint_as_float(sp[sub][k] & 0xffff0000u);
+                            const float p0 = x[2 * k] * (w0 * sj), p1 = x[2 * k + 1] * (w1 * sj);
+                            pf[2 * k] = i0 > lane ? S0 * p0 : 0.f;
+                            pf[2 * k + 1] = i0 + 1 > lane ? S1 * p1 : 0.f;
+                            cols += pf[2 * k] + pf[2 * k + 1];
+                            m1[k] = pack_bf16x2(p0, p1);
+                            m2[k] = pack_bf16x2(S0 * w0, S1 * w1);
+                        }
                     }
-                    tmem_st16(at, m1);
-                    tmem_st16(at + 16, m2);
+                    tmem_st8(pair + 16 * sub, m1);
+                    tmem_st8(pair + 16 * sub + 8, m2);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        *reinterpret_cast<uint4*>(p1t + (((4 * bb + k) ^ (j & 7)) << 4)) = make_uint4(m1[4 * k], m1[4 * k + 1], m1[4 * k + 2], m1[4 * k + 3]);
-                    float* rs = sums + 128 * q + 32 * b + lane;  // token i = 32 b + lane, over this warp's rows
-                    *rs = fresh ? rowsum : *rs + rowsum;
+                    for (int k = 0; k < 2; ++k)
+                        *reinterpret_cast<uint4*>(p1t + (((4 * (b & 1) + 2 * sub + k) ^ (j & 7)) << 4)) = make_uint4(m1[4 * k], m1[4 * k + 1], m1[4 * k + 2], m1[4 * k + 3]);
+                    rsum[sub] = transpose_sum(pf, lane);
                 }
-                float* cs = sums + 512 + 128 * half + j;
-                *cs = fresh ? cols : *cs + cols;
-                // X~ in place of X, e^{L} dY beside dY
-                uint8_t* wt = sm + sg::DYW + j * 128;
-                const float wx = sj * wej;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int cell = ((4 * half + k) ^ (j & 7)) << 4;
-                    xr[k] = *reinterpret_cast<const uint4*>(xt + cell);
-                    yr[k] = *reinterpret_cast<const uint4*>(yt + cell);
-                    float v[8];
-                    unpack8(xr[k], v);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] *= wx;
-                    *reinterpret_cast<uint4*>(xt + cell) = pack8(v);
-                    unpack8(yr[k], v);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] *= eLj;
-                    *reinterpret_cast<uint4*>(wt + cell) = pack8(v);
-                }
-                fence_proxy_async_smem();
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive1(bars + gPReady);
-                ok = wait_bar(bars + gHd, ph1, lim, err);
             }
-            if (ok) {
-                if (j < a.N) {
-                    const uint8_t *ht = sm + sg::H0 + j * 128, *dt = sm + sg::DH + j * 128;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int cell = ((4 * half + k) ^ (j & 7)) << 4;
-                        float v[8], w[8];
-                        unpack8(*reinterpret_cast<const uint4*>(ht + cell), v);
-                        unpack8(*reinterpret_cast<const uint4*>(dt + cell), w);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) e_acc = fmaf(v[e], w[e], e_acc);
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive1(bars + gHdFree);
-                ok = wait_bar(bars + gTu, ph1, lim, err);
+            // the thread's part of the head's sums of token j: column sums, v, q, du
+            auto keep = [&](int which, float v) {
+                float* to = sums + 512 * which + 128 * b + j;
+                *to = fresh ? v : *to + v;
+            };
+            // the sums of the head before have been used
+            if (fresh && it && !(ok = wait_bar(bars + gSumFree, ((it / pbs) & 1) ^ 1, lim, err))) break;
+            {
+                float* to = rs + (lane & 16);
+                const float v = lane < 16 ? rsum[0] : rsum[1];
+                *to = fresh ? v : *to + v;
             }
-            if (ok) {
-                // B A in U's columns: its share of dg, then scaled as U's start; C H: its share of dg
-                tc_fence_after();
-                float t[32], vq = 0.f;
-                tmem_ld_cols<2>(lane_base + kTU + 32 * half, t);
+            keep(1, cols);
+            // X~ in place of X, e^{L} dY beside dY
+            const uint4 xr[2] = {*reinterpret_cast<const uint4*>(xt + cell0), *reinterpret_cast<const uint4*>(xt + cell1)};
+            const uint4 yr[2] = {*reinterpret_cast<const uint4*>(yt + cell0), *reinterpret_cast<const uint4*>(yt + cell1)};
+            uint8_t* wt = sm + sg::DYW + j * 128;
+            const float wx = sj * wej;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float v[8];
-                    unpack8(xr[k], v);
+            for (int k = 0; k < 2; ++k) {
+                const int cell = k ? cell1 : cell0;
+                float v[8];
+                unpack8(xr[k], v);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        vq = fmaf(v[e], t[8 * k + e], vq);
-                        t[8 * k + e] *= wej;
-                    }
-                }
+                for (int e = 0; e < 8; ++e) v[e] *= wx;
+                *reinterpret_cast<uint4*>(xt + cell) = pack8(v);
+                unpack8(yr[k], v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= eLj;
+                *reinterpret_cast<uint4*>(wt + cell) = pack8(v);
+            }
+            fence_proxy_async_smem();
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(bars + gPReady);
+            if (!(ok = wait_bar(bars + gHd, ph1, lim, err))) break;
+            if (j < a.N) {
+                const uint8_t *ht = sm + sg::H0 + j * 128, *dt = sm + sg::DH + j * 128;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    uint32_t r[16];
+                    const int cell = k ? cell1 : cell0;
+                    float v[8], w[8];
+                    unpack8(*reinterpret_cast<const uint4*>(ht + cell), v);
+                    unpack8(*reinterpret_cast<const uint4*>(dt + cell), w);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(t[16 * k + e]);
-                    tmem_st16(lane_base + kTU + 32 * half + 16 * k, r);
+                    for (int e = 0; e < 8; ++e) e_acc = fmaf(v[e], w[e], e_acc);
                 }
-                float* vs = sums + 768 + 128 * half + j;
-                vq *= sj * wej;
-                *vs = fresh ? vq : *vs + vq;
-                tmem_ld_cols<2>(lane_base + kTT + 32 * half, t);
-                vq = 0.f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float v[8];
-                    unpack8(yr[k], v);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) vq = fmaf(v[e], t[8 * k + e], vq);
-                }
-                float* qs = sums + 1024 + 128 * half + j;
-                vq *= eLj;
-                *qs = fresh ? vq : *qs + vq;
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive1(bars + gUScaled);
-                ok = wait_bar(bars + gDx, ph1, lim, err);
             }
-            if (ok) {
-                tc_fence_after();
-                float t[32], du = 0.f;
-                tmem_ld_cols<2>(lane_base + kTU + 32 * half, t);
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(bars + gHdFree);
+            if (!(ok = wait_bar(bars + gTu, ph1, lim, err))) break;
+            tc_fence_after();
+            {
+                // B A in U's columns: its share of dg, then scaled as U's start; C H: its share of dg
+                uint32_t t[16], c[16];
+                tmem_ld16(val + kTU, t);
+                tmem_ld16(val + kTT, c);
+                tmem_ld_wait();
+                float vs = 0.f, qs = 0.f;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float v[8], w[8];
+                    unpack8(xr[k], v);
+                    unpack8(yr[k], w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float ba = __uint_as_float(t[8 * k + e]);
+                        vs = fmaf(v[e], ba, vs);
+                        qs = fmaf(w[e], __uint_as_float(c[8 * k + e]), qs);
+                        t[8 * k + e] = __float_as_uint(ba * wej);
+                    }
+                }
+                tmem_st16(val + kTU, t);
+                keep(2, vs * wx);
+                keep(3, qs * eLj);
+                tmem_st_wait();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(bars + gUScaled);
+            if (!(ok = wait_bar(bars + gDx, ph1, lim, err))) break;
+            tc_fence_after();
+            {
+                float t[16], du = 0.f;
+                tmem_ld_cols<1>(val + kTU, t);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive1(bars + gURead);
-                __nv_bfloat16* to = a.dx + static_cast<size_t>(row + j) * a.ld_dx + static_cast<size_t>(h) * a.P + pi * kCols + 32 * half;
+                __nv_bfloat16* to = a.dx + static_cast<size_t>(row + j) * a.ld_dx + static_cast<size_t>(h) * a.P + pi * kCols + 16 * b;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 2; ++k) {
                     float v[8], w[8];
                     unpack8(xr[k], v);
                     unpack8(yr[k], w);
@@ -324,53 +320,109 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
                         w[e] = fmaf(dk, w[e], sj * t[8 * k + e]);
                     }
                     const uint4 o = pack8(w);
-                    if (!tail) *reinterpret_cast<uint4*>(yt + (((4 * half + k) ^ (j & 7)) << 4)) = o;
+                    if (!tail) *reinterpret_cast<uint4*>(yt + (k ? cell1 : cell0)) = o;
                     else if (j < n) reinterpret_cast<uint4*>(to)[k] = o;
                 }
-                float* ds = sums + 1280 + 128 * half + j;
-                *ds = fresh ? du : *ds + du;
-                fence_proxy_async_smem();
+                keep(4, du);
             }
-            const bool last = pi == pbs - 1;
-            float* red = reinterpret_cast<float*>(sm + sg::RED + (hi_ & 1) * 64);
-            if (last) {
+            if (++pi == pbs) {
 #pragma unroll
                 for (int d = 16; d; d >>= 1) {
                     e_acc += __shfl_xor_sync(0xffffffffu, e_acc, d);
                     dd_acc += __shfl_xor_sync(0xffffffffu, dd_acc, d);
                 }
-                if (lane == 0) {
-                    red[2 * warp] = e_acc;
-                    red[2 * warp + 1] = dd_acc;
-                }
+                if (lane == 0) *reinterpret_cast<float2*>(sm + sg::RED + 8 * warp) = make_float2(e_acc, dd_acc);
                 e_acc = dd_acc = 0.f;
+                pi = 0;
+                ++h;
             }
-            compute_sync();  // reached by all compute warps in every iteration, whatever happened
-            if (tid == 0 && ok) {
-                if (!tail) {
-                    tma_store_3d(&maps.dx, sm + sg::DY + st * kTileBytes, pi * kCols, h, row);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive1(bars + gOut + st);
+                mbar_arrive1(bars + gGateFree + st);
+            }
+        }
+        // dB and dC: rows j and i, 32 columns per thread
+        if (ok) ok = wait_bar(bars + gAll, (NI - 1) & 1, lim, err);
+        if (ok && 32 * b < a.N) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                const int o = k >> 1, c0 = 32 * b + 16 * (k & 1);
+                float f[16];
+                tmem_ld_cols<1>(lane_base + (o ? kTdC : kTdB) + c0, f);
+                const int col = grp * a.N + c0;
+                if (j < n) {
+                    if (a.splits == 1) {
+                        uint4* to = reinterpret_cast<uint4*>((o ? a.dc : a.db) + static_cast<size_t>(row + j) * (o ? a.ld_dc : a.ld_db) + col);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            to[e] = make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
+                                               pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
+                    } else {
+                        const size_t gn = static_cast<size_t>(a.G) * a.N;
+                        float4* to = reinterpret_cast<float4*>(a.part + ((static_cast<size_t>(o) * a.splits + split) * a.rows + row + j) * gn + col);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) to[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                    }
+                }
+            }
+        }
+    } else if (warp == 19) {
+        // ---- results of an iteration: dx's tile, and at a head's end dg and dstep, four tokens per lane
+        const float* sums = reinterpret_cast<const float*>(sm + sg::SUM);
+        int pi = 0, h = h_lo;
+        for (int it = 0; it < NI; ++it) {
+            const int st = it & 1;
+            if (!wait_bar(bars + gOut + st, (it >> 1) & 1, lim, err)) break;
+            const int pi_done = pi;
+            if (++pi < pbs) {
+                if (lane == 0 && !tail) {
+                    tma_store_3d(&maps.dx, sm + sg::DY + st * kTileBytes, pi_done * kCols, h, row);
                     bulk_commit();
-                    bulk_wait_read_all();
                 }
-                mbar_arrive1(bars + gXyFree + st);
-            }
-            if (last && warp == 1 && ok) {
-                // dg and dstep of the head: four tokens per lane
+            } else {
+                const float* arr = reinterpret_cast<const float*>(sm + sg::GATE + st * sg::kGateStage);
+                auto four = [&](int which, float (&v)[4]) {  // the four parts' sum
+                    float4 s = reinterpret_cast<const float4*>(sums + 512 * which)[lane];
+#pragma unroll
+                    for (int k = 1; k < 4; ++k) {
+                        const float4 x = reinterpret_cast<const float4*>(sums + 512 * which + 128 * k)[lane];
+                        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+                    }
+                    v[0] = s.x; v[1] = s.y; v[2] = s.z; v[3] = s.w;
+                };
+                float s4[4], c4[4], v4[4], q4[4], d4[4], p4[4];
+                four(0, s4);
+                four(1, c4);
+                four(2, v4);
+                four(3, q4);
+                four(4, d4);
+                const float eEnd = arr[384 + 127];
                 float E = 0.f, D = 0.f;
-#pragma unroll
-                for (int w = 0; w < 8; ++w) {
-                    E += red[2 * w];
-                    D += red[2 * w + 1];
+                if (lane < 16) {
+                    const float2 r = *reinterpret_cast<const float2*>(sm + sg::RED + 8 * lane);
+                    E = r.x;
+                    D = r.y;
                 }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive1(bars + gSumFree);  // the next head's sums wait for this
+                    if (!tail) {
+                        tma_store_3d(&maps.dx, sm + sg::DY + st * kTileBytes, pi_done * kCols, h, row);
+                        bulk_commit();
+                    }
+                }
+#pragma unroll
+                for (int d = 8; d; d >>= 1) {
+                    E += __shfl_xor_sync(0xffffffffu, E, d);
+                    D += __shfl_xor_sync(0xffffffffu, D, d);
+                }
+                E = __shfl_sync(0xffffffffu, E, 0);
                 if (a.dd_part && lane == 0) a.dd_part[static_cast<size_t>(blockIdx.y) * a.H + h] = D;
-                float s4[4], p4[4], v4[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 4 * lane + e;
-                    const float rs = (sums[t] + sums[128 + t]) + (sums[256 + t] + sums[384 + t]);
-                    s4[e] = rs - (sums[512 + t] + sums[640 + t]) + (sums[1024 + t] + sums[1152 + t]);
-                    v4[e] = sums[768 + t] + sums[896 + t];
-                }
+                for (int e = 0; e < 4; ++e) s4[e] += q4[e] - c4[e];
                 s4[2] += s4[3]; s4[1] += s4[2]; s4[0] += s4[1];
                 p4[0] = 0.f; p4[1] = v4[0]; p4[2] = p4[1] + v4[1]; p4[3] = p4[2] + v4[2];
                 float suf = s4[0], pre = p4[3] + v4[3];
@@ -381,54 +433,28 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
                     if (lane >= d) pre += y;
                 }
                 const float after = __shfl_down_sync(0xffffffffu, suf, 1), before = __shfl_up_sync(0xffffffffu, pre, 1);
-                const float sb_ = lane < 31 ? after : 0.f, pb_ = lane ? before : 0.f, tot = arr[384 + 127] * E;
+                const float behind = lane < 31 ? after : 0.f, ahead = (lane ? before : 0.f) + eEnd * E;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = 4 * lane + e;
                     if (t < n) {
                         const size_t at = static_cast<size_t>(row + t) * a.H + h;
-                        a.dg[at] = __float2bfloat16_rn((s4[e] + sb_) + (p4[e] + pb_) + tot);
-                        a.dstep[at] = __float2bfloat16_rn(sums[1280 + t] + sums[1408 + t]);
+                        a.dg[at] = __float2bfloat16_rn((s4[e] + behind) + (p4[e] + ahead));
+                        a.dstep[at] = __float2bfloat16_rn(d4[e]);
                     }
                 }
+                pi = 0;
+                ++h;
             }
+            if (lane == 0) bulk_wait_read_all();
             __syncwarp();
-            if (lane == 0) mbar_arrive1(bars + gGateFree + st);
-        }
-        if (tid == 0) bulk_wait_all();
-        // dB and dC: rows j and i, 64 columns per half
-        if (ok) ok = wait_bar(bars + gAll, (NI - 1) & 1, lim, err);
-        if (ok && 64 * half < a.N) {
-            tc_fence_after();
-#pragma unroll 1
-            for (int o = 0; o < 2; ++o) {
-#pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t r[16];
-                    tmem_ld16(lane_base + (o ? kTdC : kTdB) + 64 * half + 16 * k, r);
-                    tmem_ld_wait();
-                    const int col = grp * a.N + 64 * half + 16 * k;
-                    if (j < n) {
-                        if (a.splits == 1) {
-                            uint4* to = reinterpret_cast<uint4*>((o ? a.dc : a.db) + static_cast<size_t>(row + j) * (o ? a.ld_dc : a.ld_db) + col);
-                            float f[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(r[e]);
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                to[e] = make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
-                                                   pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
-                        } else {
-                            const size_t gn = static_cast<size_t>(a.G) * a.N;
-                            uint4* to = reinterpret_cast<uint4*>(a.part + ((static_cast<size_t>(o) * a.splits + split) * a.rows + row + j) * gn + col);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) to[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
-                        }
-                    }
-                }
+            if (lane == 0) {
+                mbar_arrive1(bars + gXyFree + st);
+                mbar_arrive1(bars + gGateFree + st);
             }
         }
-    } else if (warp == 8) {
+        if (lane == 0) bulk_wait_all();
+    } else if (warp == 16) {
         // ---- products
         const uint32_t lead = elect_one();
         const uint32_t dk = uniform(desc_lo(sb, 16)), dm = uniform(desc_lo(sb, kTileBytes));
@@ -467,13 +493,13 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
             if (!(ok = wait(gPReady, ph1))) break;
 #pragma unroll
             for (int s = 0; s < 8; ++s)  // dB += (R W s)^T C + X~ A^T
-                mma_ts_by(lead, kTdB, kTR + 32 * (s >> 1) + 8 * (s & 1), dm + (sg::C >> 4) + s * 128, id_nm, it > 0 || s > 0);
+                mma_ts_by(lead, kTdB, kTR + 16 * s, dm + (sg::C >> 4) + s * 128, id_nm, it > 0 || s > 0);
 #pragma unroll
             for (int s = 0; s < 4; ++s) mma_by(lead, kTdB, dk + xo + s * 2, dk + (sg::DH >> 4) + s * 2, id_nk, 1);
             if (!(ok = wait(gUScaled, ph1))) break;
 #pragma unroll
             for (int s = 0; s < 8; ++s)  // U += (S W)^T dY
-                mma_ts_by(lead, kTU, kTR + 32 * (s >> 1) + 16 + 8 * (s & 1), dm + yo + s * 128, id_t, 1);
+                mma_ts_by(lead, kTU, kTR + 16 * s + 8, dm + yo + s * 128, id_t, 1);
             commit_by(lead, bars + gDx);
 #pragma unroll
             for (int s = 0; s < 8; ++s)  // dC += (R W s) B + (e^L dY) H^T
@@ -486,7 +512,7 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
         }
         commit_by(lead, bars + gDrain);
         mbar_wait(bars + gDrain, 0, kDefaultWaitNs);
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         // ---- copies
         if (lane == 0) {
             const int halves = a.N / 64;
