@@ -3,7 +3,9 @@
 //     step = softplus(delta + delta_bias),      g = a step
 // and the gradients of all of it. Both directions stream rows once and are bound by HBM.
 #include <initializer_list>
+#include <type_traits>
 
+#include "ptx.cuh"
 #include "ssm_common.cuh"
 
 namespace gdn2 {
@@ -20,13 +22,28 @@ struct Chan {
     };
     __device__ static Raw load(const T* p) { return *reinterpret_cast<const Raw*>(p); }
     __device__ static void widen(const Raw& r, float (&x)[CH]) {
+        if constexpr (sizeof(T) == 2 && CH % 2 == 0) {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
 #pragma unroll
-        for (int i = 0; i < CH; ++i) x[i] = to_f32(r.v[i]);
+            for (int i = 0; i < CH / 2; ++i) {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) x[i] = to_f32(r.v[i]);
+        }
     }
     __device__ static void store(T* p, const float (&x)[CH]) {
         Raw r;
+        if constexpr (sizeof(T) == 2 && CH % 2 == 0) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(&r);
 #pragma unroll
-        for (int i = 0; i < CH; ++i) r.v[i] = from_f32<T>(x[i]);
+            for (int i = 0; i < CH / 2; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) r.v[i] = from_f32<T>(x[i]);
+        }
         *reinterpret_cast<Raw*>(p) = r;
     }
 };
@@ -34,11 +51,12 @@ struct Chan {
 struct ConvArgs {
     Seqs seqs;
     long long rows;
-    int channels, H, silu, run;  // run: token rows per block
+    int channels, H, run;  // run: token rows per block
     const float *weight, *bias, *state;  // [channels][4], [channels] or null, [B][3][channels] or null
     const float *a, *delta_bias;         // [H]
     long long ld_x, ld_delta;
     int conv_blocks_x, conv_blocks_y;    // channel blocks, runs
+    int gate_blocks;                     // the grid's first blocks
 };
 
 // The three samples before row r of the sequence that starts at `start`: rows, then the given state, then zeros.
@@ -61,18 +79,40 @@ __device__ __forceinline__ void window_before(const ConvArgs& a, const T* x, int
     }
 }
 
-// One thread holds CH channels and walks down a run of rows with the window of the last three in
-// registers; kAhead rows are in flight at a time. Rows between sequences (none, with sound offsets) are
-// skipped. The blocks past the conv's compute the gates.
-template <typename T, int CH>
-__global__ void __launch_bounds__(kThreads)
+__device__ __forceinline__ float sigmoid_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-kLog2e * x)));
+    return r;
+}
+// The convolution at one row: taps over the three rows before it and itself.
+template <int CH>
+__device__ __forceinline__ void taps(const float (&w)[kTaps][CH], const float (&bias)[CH], const float (&a)[CH], const float (&b)[CH],
+                                     const float (&c)[CH], const float (&d)[CH], float (&v)[CH]) {
+    if constexpr (CH % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < CH; e += 2) {
+            uint64_t t = fma_f32x2(f32x2(w[0][e], w[0][e + 1]), f32x2(a[e], a[e + 1]), f32x2(bias[e], bias[e + 1]));
+            t = fma_f32x2(f32x2(w[1][e], w[1][e + 1]), f32x2(b[e], b[e + 1]), t);
+            t = fma_f32x2(f32x2(w[2][e], w[2][e + 1]), f32x2(c[e], c[e + 1]), t);
+            t = fma_f32x2(f32x2(w[3][e], w[3][e + 1]), f32x2(d[e], d[e + 1]), t);
+            f32x2_split(t, v[e], v[e + 1]);
+        }
+    } else {
+        v[0] = fmaf(w[3][0], d[0], fmaf(w[2][0], c[0], fmaf(w[1][0], b[0], fmaf(w[0][0], a[0], bias[0]))));
+    }
+}
+
+// One thread holds CH channels and walks down a run of rows with the window of the last three in registers and the next
+// four rows in flight. Rows between sequences (none, with sound offsets) are skipped. The first blocks compute the
+// gates, so that they do not trail behind.
+template <typename T, int CH, bool kSilu>
+__global__ void __launch_bounds__(kThreads, 8)
     prologue_kernel(ConvArgs a, const T* __restrict__ x, const T* __restrict__ delta, T* __restrict__ u, T* __restrict__ step,
                     T* __restrict__ g) {
-    constexpr int kAhead = 8;
-    const int conv_blocks = a.conv_blocks_x * a.conv_blocks_y;
-    if (static_cast<int>(blockIdx.x) >= conv_blocks) {
-        const long long n = a.rows * a.H, stride = static_cast<long long>(gridDim.x - conv_blocks) * kThreads;
-        for (long long i = (blockIdx.x - conv_blocks) * static_cast<long long>(kThreads) + threadIdx.x; i < n; i += stride) {
+    using Ch = Chan<T, CH>;
+    if (static_cast<int>(blockIdx.x) < a.gate_blocks) {
+        const long long n = a.rows * a.H, stride = static_cast<long long>(a.gate_blocks) * kThreads;
+        for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < n; i += stride) {
             const long long r = i / a.H;
             const int h = static_cast<int>(i - r * a.H);
             const float st = ssm_softplus(to_f32(delta[r * a.ld_delta + h]) + a.delta_bias[h]);
@@ -81,50 +121,63 @@ __global__ void __launch_bounds__(kThreads)
         }
         return;
     }
-    const int by = blockIdx.x / a.conv_blocks_x, bx = blockIdx.x - by * a.conv_blocks_x;
+    const int blk = blockIdx.x - a.gate_blocks;
+    const int by = blk / a.conv_blocks_x, bx = blk - by * a.conv_blocks_x;
     const int c = CH * (bx * kThreads + threadIdx.x);
     if (c >= a.channels) return;
-    float w[CH][kTaps], bias[CH];
+    float w[kTaps][CH], bias[CH];
 #pragma unroll
     for (int e = 0; e < CH; ++e) {
         const float4 v = __ldg(reinterpret_cast<const float4*>(a.weight) + c + e);
-        w[e][0] = v.x; w[e][1] = v.y; w[e][2] = v.z; w[e][3] = v.w;
+        w[0][e] = v.x; w[1][e] = v.y; w[2][e] = v.z; w[3][e] = v.w;
         bias[e] = a.bias ? __ldg(a.bias + c + e) : 0.f;
     }
     const int r0 = by * a.run, r1 = static_cast<int>(min(static_cast<long long>(r0) + a.run, a.rows));
-    float win[kTaps - 1][CH];
-    int end = r0;
-    bool in = false;
-    for (int rb = r0; rb < r1; rb += kAhead) {
-        typename Chan<T, CH>::Raw raw[kAhead];
-#pragma unroll
-        for (int q = 0; q < kAhead; ++q)
-            if (rb + q < r1) raw[q] = Chan<T, CH>::load(x + static_cast<size_t>(rb + q) * a.ld_x + c);
-#pragma unroll
-        for (int q = 0; q < kAhead; ++q) {
-            const int r = rb + q;
-            if (r >= r1) break;
-            if (r >= end) {  // into another sequence (uniform over the block)
-                int seq, start;
-                in = find_row(a.seqs, r, seq, start, end);
-                if (in) window_before<T, CH>(a, x, c, r, start, seq, win);
-                else end = r + 1;
-            }
-            float cur[CH], out[CH];
-            Chan<T, CH>::widen(raw[q], cur);
-#pragma unroll
-            for (int e = 0; e < CH; ++e) {
-                float v = fmaf(w[e][0], win[0][e], bias[e]);
-                v = fmaf(w[e][1], win[1][e], v);
-                v = fmaf(w[e][2], win[2][e], v);
-                v = fmaf(w[e][3], cur[e], v);
-                out[e] = a.silu ? v * ssm_sigmoid(v) : v;
-                win[0][e] = win[1][e];
-                win[1][e] = win[2][e];
-                win[2][e] = cur[e];
-            }
-            if (in) Chan<T, CH>::store(u + static_cast<size_t>(r) * a.channels + c, out);
+    // one stretch of a sequence after the other; within it four rows at a time, the next four in flight
+    for (int lo = r0; lo < r1;) {
+        int seq, start, end;
+        if (!find_row(a.seqs, lo, seq, start, end)) {
+            ++lo;
+            continue;
         }
+        const int hi = min(end, r1);
+        float win[kTaps][CH];  // rows r-3, r-2, r-1 at [r & 3 ..]: rotated by the unrolled loop
+        {
+            float before[kTaps - 1][CH];
+            window_before<T, CH>(a, x, c, lo, start, seq, before);
+#pragma unroll
+            for (int j = 0; j < kTaps - 1; ++j)
+#pragma unroll
+                for (int e = 0; e < CH; ++e) win[j][e] = before[j][e];
+        }
+        const T* xp = x + static_cast<size_t>(lo) * a.ld_x + c;
+        T* up = u + static_cast<size_t>(lo) * a.channels + c;
+        typename Ch::Raw next[kTaps];
+#pragma unroll
+        for (int q = 0; q < kTaps; ++q)
+            if (lo + q < hi) next[q] = Ch::load(xp + static_cast<size_t>(q) * a.ld_x);
+        for (int r = lo; r < hi; r += kTaps) {
+            typename Ch::Raw raw[kTaps];
+#pragma unroll
+            for (int q = 0; q < kTaps; ++q) raw[q] = next[q];
+            xp += kTaps * a.ld_x;
+#pragma unroll
+            for (int q = 0; q < kTaps; ++q)
+                if (r + kTaps + q < hi) next[q] = Ch::load(xp + static_cast<size_t>(q) * a.ld_x);
+#pragma unroll
+            for (int q = 0; q < kTaps; ++q) {
+                float v[CH];
+                Ch::widen(raw[q], win[(q + 3) & 3]);
+                taps<CH>(w, bias, win[q], win[(q + 1) & 3], win[(q + 2) & 3], win[(q + 3) & 3], v);
+                if (kSilu) {
+#pragma unroll
+                    for (int e = 0; e < CH; ++e) v[e] *= sigmoid_approx(v[e]);
+                }
+                if (r + q < hi) Ch::store(up + static_cast<size_t>(q) * a.channels, v);
+            }
+            up += static_cast<size_t>(kTaps) * a.channels;
+        }
+        lo = hi;
     }
 }
 
@@ -152,12 +205,11 @@ __global__ void __launch_bounds__(256) window_kernel(Seqs seqs, const T* __restr
 // ---------------------------------------------------------------------------------------------
 // gradients
 
-constexpr int kGateRows = 64;  // token rows of one gate block
+constexpr int kGateRows = 16;  // token rows of one gate block
 
 struct ConvGradArgs {
     ConvArgs c;
     long long ld_du, ld_dx, ld_ddelta;
-    int gate_blocks;
     float *part, *gate_part;  // [runs][channels][5]; [gate blocks][H][2]
 };
 
@@ -166,23 +218,25 @@ struct ConvGradArgs {
 // r it forms dv_r and, from it and the three before, dx_{r-3}. The three rows after the run (of its last
 // sequence) are formed again here for its own dx and belong to the next run's sums. Sums of a run go
 // to `part`; sum_kernel adds the runs in order.
-template <typename T, int CH>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int CH, bool kSilu>
+__global__ void __launch_bounds__(kThreads, 3)
     prologue_grad_kernel(ConvGradArgs ga, const T* __restrict__ x, const T* __restrict__ delta, const T* __restrict__ du,
                          const T* __restrict__ dstep, const T* __restrict__ dg, T* __restrict__ dx, T* __restrict__ ddelta) {
-    constexpr int kAhead = 8;
+    using Ch = Chan<T, CH>;
     const ConvArgs& a = ga.c;
-    const int conv_blocks = a.conv_blocks_x * a.conv_blocks_y;
-    if (static_cast<int>(blockIdx.x) >= conv_blocks) {
+    if (static_cast<int>(blockIdx.x) < a.gate_blocks) {
         __shared__ float red[kThreads / 32][32][2];
-        const int blk = blockIdx.x - conv_blocks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        const long long lo = static_cast<long long>(blk) * kGateRows, hi = min(lo + kGateRows, a.rows);
+        const int blk = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const long long lo = static_cast<long long>(blk) * kGateRows;
         for (int h0 = 0; h0 < a.H; h0 += 32) {
             const int h = h0 + lane;
             float sa = 0.f, sb = 0.f;
             if (h < a.H) {
                 const float av = a.a[h], bv = a.delta_bias[h];
-                for (long long r = lo + warp; r < hi; r += kThreads / 32) {
+#pragma unroll
+                for (int k = 0; k < kGateRows / 4; ++k) {
+                    const long long r = lo + warp + 4 * k;
+                    if (r >= a.rows) continue;
                     const float v = to_f32(delta[r * a.ld_delta + h]) + bv, dgv = to_f32(dg[r * a.H + h]);
                     const float dv = fmaf(av, dgv, to_f32(dstep[r * a.H + h])) * ssm_sigmoid(v);
                     ddelta[r * ga.ld_ddelta + h] = from_f32<T>(dv);
@@ -202,116 +256,111 @@ __global__ void __launch_bounds__(kThreads)
         }
         return;
     }
-    const int by = blockIdx.x / a.conv_blocks_x, bx = blockIdx.x - by * a.conv_blocks_x;
+    const int cblk = blockIdx.x - a.gate_blocks;
+    const int by = cblk / a.conv_blocks_x, bx = cblk - by * a.conv_blocks_x;
     const int c = CH * (bx * kThreads + threadIdx.x);
     if (c >= a.channels) return;
-    float w[CH][kTaps], bias[CH], dw[CH][kTaps] = {}, db[CH] = {};
+    float w[kTaps][CH], bias[CH], dw[kTaps][CH] = {}, db[CH] = {};
 #pragma unroll
     for (int e = 0; e < CH; ++e) {
         const float4 v = __ldg(reinterpret_cast<const float4*>(a.weight) + c + e);
-        w[e][0] = v.x; w[e][1] = v.y; w[e][2] = v.z; w[e][3] = v.w;
+        w[0][e] = v.x; w[1][e] = v.y; w[2][e] = v.z; w[3][e] = v.w;
         bias[e] = a.bias ? __ldg(a.bias + c + e) : 0.f;
     }
     const int rows = static_cast<int>(a.rows);
     const int r0 = by * a.run, r1 = min(r0 + a.run, rows);
-    float win[kTaps - 1][CH], dvw[kTaps - 1][CH];  // x and dv of rows r-3, r-2, r-1
-#pragma unroll
-    for (int j = 0; j < kTaps - 1; ++j)
-#pragma unroll
-        for (int e = 0; e < CH; ++e) win[j][e] = dvw[j][e] = 0.f;
-    int start = r0, end = r0;
-    bool in = false;
-    // dx of row s from dvw (rows s .. s+2) and the row after, `last` (zeros past the sequence)
-    auto put = [&](int s, const float (&last)[CH]) {
-        float out[CH];
-#pragma unroll
-        for (int e = 0; e < CH; ++e)
-            out[e] = fmaf(w[e][3], dvw[0][e], fmaf(w[e][2], dvw[1][e], fmaf(w[e][1], dvw[2][e], w[e][0] * last[e])));
-        Chan<T, CH>::store(dx + static_cast<size_t>(s) * ga.ld_dx + c, out);
-    };
-    auto push = [&](const float (&v)[CH]) {
-#pragma unroll
-        for (int e = 0; e < CH; ++e) {
-            dvw[0][e] = dvw[1][e];
-            dvw[1][e] = dvw[2][e];
-            dvw[2][e] = v[e];
+    for (int lo = r0; lo < r1;) {
+        int seq, start, end;
+        if (!find_row(a.seqs, lo, seq, start, end)) {
+            ++lo;
+            continue;
         }
-    };
-    const float zero[CH] = {};
-    // the last (up to) three rows of a sequence have no rows after them; `upto`: the row after its last
-    auto flush = [&](int upto) {
+        // rows [lo, hi) of the run, then (up to) three more of the sequence for this run's last dx
+        const int hi = min(end, r1), stop = min(end, r1 + kTaps - 1);
+        float win[kTaps][CH], dvw[kTaps][CH];  // x and dv of rows r-3, r-2, r-1 at [r & 3 ..], rotated by the unrolled loop
+        {
+            float before[kTaps - 1][CH];
+            window_before<T, CH>(a, x, c, lo, start, seq, before);
 #pragma unroll
-        for (int j = 0; j < kTaps - 1; ++j) {
-            const int s = upto - (kTaps - 1) + j;
-            if (s >= max(start, r0) && s < r1) put(s, zero);
-            push(zero);
+            for (int j = 0; j < kTaps - 1; ++j)
+#pragma unroll
+                for (int e = 0; e < CH; ++e) {
+                    win[j][e] = before[j][e];
+                    dvw[j][e] = 0.f;
+                }
         }
-    };
-    const int stop = min(r1 + kTaps - 1, rows);
-    bool open = false;  // a sequence whose last dx rows are still to come
-    for (int rb = r0; rb < stop; rb += kAhead) {
-        typename Chan<T, CH>::Raw rx[kAhead], rd[kAhead];
+        const T *xp = x + static_cast<size_t>(lo) * a.ld_x + c, *dp = du + static_cast<size_t>(lo) * ga.ld_du + c;
+        T* op = dx + static_cast<size_t>(lo) * ga.ld_dx + c;
+        typename Ch::Raw nx[kTaps], nd[kTaps];
 #pragma unroll
-        for (int q = 0; q < kAhead; ++q)
-            if (rb + q < stop) {
-                rx[q] = Chan<T, CH>::load(x + static_cast<size_t>(rb + q) * a.ld_x + c);
-                rd[q] = Chan<T, CH>::load(du + static_cast<size_t>(rb + q) * ga.ld_du + c);
+        for (int q = 0; q < kTaps; ++q)
+            if (lo + q < stop) {
+                nx[q] = Ch::load(xp + static_cast<size_t>(q) * a.ld_x);
+                nd[q] = Ch::load(dp + static_cast<size_t>(q) * ga.ld_du);
             }
+        // three rows past the last one, of zero dv, bring out the last dx of the sequence
+        for (int r = lo; r < hi + kTaps - 1; r += kTaps) {
+            typename Ch::Raw rx[kTaps], rd[kTaps];
 #pragma unroll
-        for (int q = 0; q < kAhead; ++q) {
-            const int r = rb + q;
-            if (r >= stop) break;
-            if (r >= end) {
-                if (open) flush(end);
-                open = false;
-                if (r >= r1) break;  // the rows after the run are another sequence's
-                int seq;
-                in = find_row(a.seqs, r, seq, start, end);
-                if (in) {
-                    window_before<T, CH>(a, x, c, r, start, seq, win);
-                    open = true;
-                } else {
-                    end = r + 1;
+            for (int q = 0; q < kTaps; ++q) {
+                rx[q] = nx[q];
+                rd[q] = nd[q];
+            }
+            xp += kTaps * a.ld_x;
+            dp += kTaps * ga.ld_du;
+#pragma unroll
+            for (int q = 0; q < kTaps; ++q)
+                if (r + kTaps + q < stop) {
+                    nx[q] = Ch::load(xp + static_cast<size_t>(q) * a.ld_x);
+                    nd[q] = Ch::load(dp + static_cast<size_t>(q) * ga.ld_du);
+                }
+#pragma unroll
+            for (int q = 0; q < kTaps; ++q) {
+                const int t = r + q;
+                float (&cur)[CH] = win[(q + 3) & 3], (&dv)[CH] = dvw[(q + 3) & 3];
+                float v[CH];
+                const bool real = t < stop;
+                Ch::widen(rx[q], cur);
+                Ch::widen(rd[q], dv);
+                taps<CH>(w, bias, win[q], win[(q + 1) & 3], win[(q + 2) & 3], cur, v);
+                if (kSilu) {
+#pragma unroll
+                    for (int e = 0; e < CH; ++e) {
+                        const float sg = sigmoid_approx(v[e]);
+                        dv[e] *= sg * fmaf(v[e], 1.f - sg, 1.f);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < CH; ++e) dv[e] = real ? dv[e] : 0.f;
+                if (t < hi) {
+#pragma unroll
+                    for (int e = 0; e < CH; ++e) {
+                        dw[0][e] = fmaf(dv[e], win[q][e], dw[0][e]);
+                        dw[1][e] = fmaf(dv[e], win[(q + 1) & 3][e], dw[1][e]);
+                        dw[2][e] = fmaf(dv[e], win[(q + 2) & 3][e], dw[2][e]);
+                        dw[3][e] = fmaf(dv[e], cur[e], dw[3][e]);
+                        db[e] += dv[e];
+                    }
+                }
+                const int s = t - (kTaps - 1);  // the row whose dx is complete
+                if (s >= lo && s < hi) {
+                    float out[CH];
+                    // dx_s = W_3 dv_s + W_2 dv_{s+1} + W_1 dv_{s+2} + W_0 dv_{s+3}
+                    const float (&d0)[CH] = dvw[q], (&d1)[CH] = dvw[(q + 1) & 3], (&d2)[CH] = dvw[(q + 2) & 3];
+#pragma unroll
+                    for (int e = 0; e < CH; ++e)
+                        out[e] = fmaf(w[3][e], d0[e], fmaf(w[2][e], d1[e], fmaf(w[1][e], d2[e], w[0][e] * dv[e])));
+                    Ch::store(op + (static_cast<long long>(s) - lo) * ga.ld_dx, out);
                 }
             }
-            if (!in) continue;
-            float cur[CH], dv[CH];
-            Chan<T, CH>::widen(rx[q], cur);
-            Chan<T, CH>::widen(rd[q], dv);
-            const bool own = r < r1;
-#pragma unroll
-            for (int e = 0; e < CH; ++e) {
-                float v = fmaf(w[e][0], win[0][e], bias[e]);
-                v = fmaf(w[e][1], win[1][e], v);
-                v = fmaf(w[e][2], win[2][e], v);
-                v = fmaf(w[e][3], cur[e], v);
-                if (a.silu) {
-                    const float sg = ssm_sigmoid(v);
-                    dv[e] *= sg * fmaf(v, 1.f - sg, 1.f);
-                }
-                if (own) {
-                    dw[e][0] = fmaf(dv[e], win[0][e], dw[e][0]);
-                    dw[e][1] = fmaf(dv[e], win[1][e], dw[e][1]);
-                    dw[e][2] = fmaf(dv[e], win[2][e], dw[e][2]);
-                    dw[e][3] = fmaf(dv[e], cur[e], dw[e][3]);
-                    db[e] += dv[e];
-                }
-                win[0][e] = win[1][e];
-                win[1][e] = win[2][e];
-                win[2][e] = cur[e];
-            }
-            if (r - (kTaps - 1) >= max(start, r0)) put(r - (kTaps - 1), dv);
-            push(dv);
         }
-    }
-    if (open) {
-        if (end <= stop) flush(end);  // the sequence ends within what was read
+        lo = hi;
     }
     float* to = ga.part + (static_cast<size_t>(by) * a.channels + c) * 5;
 #pragma unroll
     for (int e = 0; e < CH; ++e) {
 #pragma unroll
-        for (int j = 0; j < kTaps; ++j) to[5 * e + j] = dw[e][j];
+        for (int j = 0; j < kTaps; ++j) to[5 * e + j] = dw[j][e];
         to[5 * e + 4] = db[e];
     }
 }
@@ -328,8 +377,17 @@ __global__ void __launch_bounds__(256)
     const float* src = conv ? part : gate_part;
     const int count = conv ? runs : gate_blocks;
     float v = 0.f;
-    if (i < n)
-        for (int k = warp; k < count; k += 8) v += src[static_cast<size_t>(k) * n + i];
+    if (i < n) {
+        int k = warp;
+        for (; k + 56 < count; k += 64) {  // eight loads in flight
+            float t[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) t[q] = src[static_cast<size_t>(k + 8 * q) * n + i];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v += t[q];
+        }
+        for (; k < count; k += 8) v += src[static_cast<size_t>(k) * n + i];
+    }
     red[warp][lane] = v;
     __syncthreads();
     if (warp || i >= n) return;
@@ -359,32 +417,30 @@ int run_rows(long long rows, int blocks_x, int per_sm, int least) {
     return static_cast<int>(run < least ? least : run);
 }
 
-ConvArgs conv_args(const Seqs& seqs, int channels, int H, int silu, int ch_per_thread, int per_sm, int least) {
+ConvArgs conv_args(const Seqs& seqs, int channels, int H, int ch_per_thread, int per_sm, int least) {
     ConvArgs a{};
     a.seqs = seqs;
     a.rows = seqs.rows();
     a.channels = channels;
     a.H = H;
-    a.silu = silu ? 1 : 0;
     a.conv_blocks_x = (channels + ch_per_thread * kThreads - 1) / (ch_per_thread * kThreads);
     a.run = run_rows(a.rows, a.conv_blocks_x, per_sm, least);
     a.conv_blocks_y = static_cast<int>((a.rows + a.run - 1) / a.run);
     return a;
 }
 
-constexpr int kGradPerSm = 4, kGradLeast = 16;
+constexpr int kGradPerSm = 3, kGradLeast = 16;
 
 struct GradPlan {
     ConvArgs c;
-    int gate_blocks;
     size_t part, gate_part;  // floats
 };
-GradPlan grad_plan(const Seqs& seqs, int channels, int H, int silu, int ch_per_thread) {
+GradPlan grad_plan(const Seqs& seqs, int channels, int H, int ch_per_thread) {
     GradPlan p;
-    p.c = conv_args(seqs, channels, H, silu, ch_per_thread, kGradPerSm, kGradLeast);
-    p.gate_blocks = static_cast<int>((p.c.rows + kGateRows - 1) / kGateRows);
+    p.c = conv_args(seqs, channels, H, ch_per_thread, kGradPerSm, kGradLeast);
+    p.c.gate_blocks = static_cast<int>((p.c.rows + kGateRows - 1) / kGateRows);
     p.part = static_cast<size_t>(p.c.conv_blocks_y) * channels * 5;
-    p.gate_part = static_cast<size_t>(p.gate_blocks) * H * 2;
+    p.gate_part = static_cast<size_t>(p.c.gate_blocks) * H * 2;
     return p;
 }
 
@@ -435,8 +491,8 @@ gdn2_status gdn2_ssm_prologue(const void* xbc, long long ld_xbc, const void* del
         return GDN2_ERR_MISALIGNED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf = dt == GDN2_BF16;
-    const int ch = word({{xbc, ld_xbc}}, esz, bf ? 8 : 4);
-    ConvArgs c = conv_args(seqs, channels, H, silu, ch, 16, 8);
+    const int ch = word({{xbc, ld_xbc}}, esz, 4);
+    ConvArgs c = conv_args(seqs, channels, H, ch, 24, 8);
     c.weight = conv_weight;
     c.bias = conv_bias;
     c.state = conv_state;
@@ -445,15 +501,20 @@ gdn2_status gdn2_ssm_prologue(const void* xbc, long long ld_xbc, const void* del
     c.ld_x = ld_xbc;
     c.ld_delta = ld_delta;
     const long long gates = (c.rows * H + 4 * kThreads - 1) / (4 * kThreads), conv = (long long)c.conv_blocks_x * c.conv_blocks_y;
-    const unsigned grid = static_cast<unsigned>(conv + (gates < 4096 ? gates : 4096));
+    c.gate_blocks = static_cast<int>(gates < 2048 ? gates : 2048);
+    const unsigned grid = static_cast<unsigned>(conv + c.gate_blocks);
     auto go = [&](auto kernel, auto zero) {
         using T = decltype(zero);
         kernel<<<grid, kThreads, 0, s>>>(c, static_cast<const T*>(xbc), static_cast<const T*>(delta), static_cast<T*>(u),
                                          static_cast<T*>(step), static_cast<T*>(g));
     };
     using BF = __nv_bfloat16;
-    if (bf) go(ch == 8 ? prologue_kernel<BF, 8> : ch == 4 ? prologue_kernel<BF, 4> : ch == 2 ? prologue_kernel<BF, 2> : prologue_kernel<BF, 1>, BF{});
-    else go(ch == 4 ? prologue_kernel<float, 4> : ch == 2 ? prologue_kernel<float, 2> : prologue_kernel<float, 1>, 0.f);
+    auto pick = [&](auto act) {
+        constexpr bool kSilu = decltype(act)::value;
+        if (bf) go(ch == 4 ? prologue_kernel<BF, 4, kSilu> : ch == 2 ? prologue_kernel<BF, 2, kSilu> : prologue_kernel<BF, 1, kSilu>, BF{});
+        else go(ch == 4 ? prologue_kernel<float, 4, kSilu> : ch == 2 ? prologue_kernel<float, 2, kSilu> : prologue_kernel<float, 1, kSilu>, 0.f);
+    };
+    if (silu) pick(std::true_type{}); else pick(std::false_type{});
     if (cudaGetLastError() != cudaSuccess) return GDN2_ERR_CUDA;
     if (conv_state) {
         const unsigned n = static_cast<unsigned>(((long long)B * channels + 255) / 256);
@@ -469,7 +530,7 @@ size_t gdn2_ssm_prologue_backward_workspace_size(int B, int T, int channels, int
     if (sizes(B, T, channels, H, dt, seqs) != GDN2_OK || B == 0 || seqs.rows() == 0) return 0;
     size_t most = 0;  // whatever the word that the rows' alignment allows
     for (int ch = 1; ch <= 4; ch *= 2) {
-        const GradPlan p = grad_plan(seqs, channels, H, 1, ch);
+        const GradPlan p = grad_plan(seqs, channels, H, ch);
         if (p.part + p.gate_part > most) most = p.part + p.gate_part;
     }
     return align_up(sizeof(float) * most, 256);
@@ -505,7 +566,7 @@ gdn2_status gdn2_ssm_prologue_backward(const void* xbc, long long ld_xbc, const 
         !aligned_to(dconv_weight, 4) || !aligned_to(dconv_bias, 4) || !aligned_to(da, 4) || !aligned_to(ddelta_bias, 4))
         return GDN2_ERR_MISALIGNED;
     const int ch = word({{xbc, ld_xbc}, {du, ld_du}, {dxbc, ld_dxbc}}, esz, 4);
-    GradPlan p = grad_plan(seqs, channels, H, silu, ch);
+    GradPlan p = grad_plan(seqs, channels, H, ch);
     if (!workspace || ws_bytes < gdn2_ssm_prologue_backward_workspace_size(B, T, channels, H, offsets != nullptr, dt))
         return GDN2_ERR_WORKSPACE;
     if (!aligned16(workspace)) return GDN2_ERR_MISALIGNED;
@@ -516,8 +577,8 @@ gdn2_status gdn2_ssm_prologue_backward(const void* xbc, long long ld_xbc, const 
     p.c.ld_x = ld_xbc;
     p.c.ld_delta = ld_delta;
     float* part = static_cast<float*>(workspace);
-    const ConvGradArgs ga{p.c, ld_du, ld_dxbc, ld_ddelta, p.gate_blocks, part, part + p.part};
-    const unsigned grid = static_cast<unsigned>(p.c.conv_blocks_x * p.c.conv_blocks_y + p.gate_blocks);
+    const ConvGradArgs ga{p.c, ld_du, ld_dxbc, ld_ddelta, part, part + p.part};
+    const unsigned grid = static_cast<unsigned>(p.c.conv_blocks_x * p.c.conv_blocks_y + p.c.gate_blocks);
     auto go = [&](auto kernel, auto zero) {
         using T = decltype(zero);
         kernel<<<grid, kThreads, 0, s>>>(ga, static_cast<const T*>(xbc), static_cast<const T*>(delta), static_cast<const T*>(du),
@@ -525,11 +586,17 @@ gdn2_status gdn2_ssm_prologue_backward(const void* xbc, long long ld_xbc, const 
                                          static_cast<T*>(ddelta));
     };
     using BF = __nv_bfloat16;
-    if (dt == GDN2_BF16) go(ch == 4 ? prologue_grad_kernel<BF, 4> : ch == 2 ? prologue_grad_kernel<BF, 2> : prologue_grad_kernel<BF, 1>, BF{});
-    else go(ch == 4 ? prologue_grad_kernel<float, 4> : ch == 2 ? prologue_grad_kernel<float, 2> : prologue_grad_kernel<float, 1>, 0.f);
+    auto pick = [&](auto act) {
+        constexpr bool kSilu = decltype(act)::value;
+        if (dt == GDN2_BF16)
+            go(ch == 4 ? prologue_grad_kernel<BF, 4, kSilu> : ch == 2 ? prologue_grad_kernel<BF, 2, kSilu> : prologue_grad_kernel<BF, 1, kSilu>, BF{});
+        else
+            go(ch == 4 ? prologue_grad_kernel<float, 4, kSilu> : ch == 2 ? prologue_grad_kernel<float, 2, kSilu> : prologue_grad_kernel<float, 1, kSilu>, 0.f);
+    };
+    if (silu) pick(std::true_type{}); else pick(std::false_type{});
     if (cudaGetLastError() != cudaSuccess) return GDN2_ERR_CUDA;
     const int conv_blocks = (channels * 5 + 31) / 32, gate_blocks = (H * 2 + 31) / 32;
-    sum_kernel<<<conv_blocks + gate_blocks, 256, 0, s>>>(ga.part, ga.gate_part, p.c.conv_blocks_y, p.gate_blocks, channels, H,
+    sum_kernel<<<conv_blocks + gate_blocks, 256, 0, s>>>(ga.part, ga.gate_part, p.c.conv_blocks_y, p.c.gate_blocks, channels, H,
                                                          conv_blocks, dconv_weight, dconv_bias, da, ddelta_bias);
     return cudaGetLastError() == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA;
 }
