@@ -18,115 +18,214 @@ struct NormArgs {
     float eps;
 };
 
-// Sum over the block; the same value in every thread. `red` holds one float per warp.
-__device__ __forceinline__ float block_sum(float v, float* red) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    const int warps = blockDim.x >> 5;
-    __syncthreads();  // earlier readers of red are done
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = 0.f;
-    for (int w = 0; w < warps; ++w) s += red[w];
-    return s;
+    return v;
 }
 
-// Sums over each group of 8-element vectors: vec[] holds every vector's part, out[] the groups' sums.
-__device__ __forceinline__ void group_sums(float* vec, float* out, int nvec, int groups) {
-    __syncthreads();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, per = nvec / groups;
-    for (int g = warp; g < groups; g += warps) {
-        float v = 0.f;
-        for (int i = lane; i < per; i += 32) v += vec[g * per + i];
+// Room for the sums over a row and over its groups. `slot` alternates between the sums that follow one another, so
+// that one barrier orders each.
+struct RowSums {
+    float part[2][2][kMaxD / 8 / 32];  // [slot][which][32 vectors or a warp]
+    float vec[kMaxD / 8], group[kMaxD / 8];
+};
+
+// Sums over the whole row of kWhich values per thread, the same in every thread.
+template <int kWhich>
+__device__ __forceinline__ void row_total(RowSums& rs, int slot, float (&v)[kWhich]) {
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-        if (lane == 0) out[g] = v;
+    for (int w = 0; w < kWhich; ++w) {
+        const float t = warp_sum(v[w]);
+        if ((threadIdx.x & 31) == 0) rs.part[slot][w][warp] = t;
     }
     __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWhich; ++w) {
+        float t = 0.f;
+        for (int k = 0; k < warps; ++k) t += rs.part[slot][w][k];
+        v[w] = t;
+    }
 }
 
+// Where a thread's vectors lie among the groups. Where groups are whole warps' worth of vectors (every common width)
+// their sums take a warp sum per 32 vectors and one barrier; else every vector's part and two more barriers.
+template <int VPT>
+struct Groups {
+    int per, blocks, first[VPT];  // vectors per group; 32-vector blocks per group and this vector's first one, or its group
+    bool whole;
+    __device__ __forceinline__ Groups(int nvec, int groups) {
+        per = nvec / groups;
+        whole = per % 32 == 0;
+        blocks = per / 32;
+#pragma unroll
+        for (int m = 0; m < VPT; ++m) {
+            const int i = threadIdx.x + m * blockDim.x, g = i < nvec ? i / per : 0;
+            first[m] = whole ? g * blocks : g;
+        }
+    }
+};
+template <int VPT>
+__device__ __forceinline__ void group_sums(RowSums& rs, int slot, const Groups<VPT>& gr, int groups, const bool (&in)[VPT], float (&v)[VPT]) {
+    const int tid = threadIdx.x;
+    if (gr.whole) {
+#pragma unroll
+        for (int m = 0; m < VPT; ++m) {
+            const float t = warp_sum(v[m]);
+            if (in[m] && (tid & 31) == 0) rs.part[slot][0][(tid + m * blockDim.x) >> 5] = t;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < VPT; ++m) {
+            float t = 0.f;
+            for (int k = 0; k < gr.blocks; ++k) t += rs.part[slot][0][gr.first[m] + k];
+            v[m] = t;
+        }
+        return;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < VPT; ++m)
+        if (in[m]) rs.vec[tid + m * blockDim.x] = v[m];
+    __syncthreads();
+    const int warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
+    for (int g = warp; g < groups; g += warps) {
+        float t = 0.f;
+        for (int i = lane; i < gr.per; i += 32) t += rs.vec[g * gr.per + i];
+        t = warp_sum(t);
+        if (lane == 0) rs.group[g] = t;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < VPT; ++m) v[m] = rs.group[gr.first[m]];
+}
+
+// Eight elements as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) { Vec8<T>::load(p, x); }
+struct alignas(16) Raw8 {
+    uint4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw(const T* p) {
+    Raw8<T> r;
+#pragma unroll
+    for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k) r.w[k] = reinterpret_cast<const uint4*>(p)[k];
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void widen8(const Raw8<T>& r, float (&x)[8]) {
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else {
+        const float* f = reinterpret_cast<const float*>(&r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = f[i];
+    }
+}
 
 __device__ __forceinline__ void weights8(const float* w, int c, bool in, float (&x)[8]) {
+    if (w && in) {
+        const float4 a = reinterpret_cast<const float4*>(w + c)[0], b = reinterpret_cast<const float4*>(w + c)[1];
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = w && in ? __ldg(w + c + e) : 1.f;
+        for (int e = 0; e < 8; ++e) x[e] = 1.f;
+    }
 }
 
-// One row per block and trip, VPT vectors of eight elements per thread; the weights stay in registers
-// over the block's rows.
-template <typename T, int VPT>
-__global__ void __launch_bounds__(512)
-    norm_kernel(NormArgs a, const T* __restrict__ x, const T* __restrict__ z, const T* __restrict__ residual, T* __restrict__ r_out,
-                T* __restrict__ n_out) {
-    __shared__ float red[32], vec[kMaxD / 8], gsum[kMaxD / 8];
+// One row per block and trip, VPT vectors of eight elements per thread. The weights stay in registers over the
+// block's rows (at 512 threads of 64 registers they were fetched again for every row: 181 us instead of 108 us at
+// 16384 x 4096), and the next row's loads are in flight while a row is summed.
+template <typename T, int VPT, int kMaxThreads, int kPerSm>
+__global__ void __launch_bounds__(kMaxThreads, kPerSm)
+    norm_kernel(NormArgs a, const T* x, const T* z, const T* residual, T* r_out, T* n_out) {
+    __shared__ RowSums rs;
     const int tid = threadIdx.x, nvec = a.d / 8;
     float post[VPT][8], scale[VPT][8], pre[VPT][8];
     bool in[VPT];
-    int group[VPT];
+    int at[VPT];
 #pragma unroll
     for (int m = 0; m < VPT; ++m) {
         const int i = tid + m * blockDim.x;
         in[m] = i < nvec;
-        group[m] = in[m] ? i / (nvec / a.groups) : 0;
-        weights8(a.post, 8 * i, in[m], post[m]);
-        weights8(a.scale, 8 * i, in[m], scale[m]);
-        weights8(a.pre, 8 * i, in[m], pre[m]);
+        at[m] = 8 * i;
+        weights8(a.post, at[m], in[m], post[m]);
+        weights8(a.scale, at[m], in[m], scale[m]);
+        weights8(a.pre, at[m], in[m], pre[m]);
     }
-    const float inv_width = static_cast<float>(a.groups) / a.d;
-    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const float inv_width = static_cast<float>(a.groups) / a.d, inv_d = 1.f / a.d;
+    const Groups<VPT> gr(nvec, a.groups);
+    Raw8<T> rx[VPT], rz[VPT], rr[VPT];
+    auto fetch = [&](long long row) {
+        if (row >= a.rows) return;
         const size_t base = static_cast<size_t>(row) * a.d;
-        float t[VPT][8], res[VPT][8];
-        float ss = 0.f;
 #pragma unroll
         for (int m = 0; m < VPT; ++m) {
-            const size_t at = base + 8 * (tid + m * static_cast<int>(blockDim.x));
+            if (!in[m]) continue;
+            rx[m] = load_raw(x + base + at[m]);
+            if (z) rz[m] = load_raw(z + base + at[m]);
+            if (residual) rr[m] = load_raw(residual + base + at[m]);
+        }
+    };
+    fetch(blockIdx.x);
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const size_t base = static_cast<size_t>(row) * a.d;
+        float t[VPT][8], res[VPT][8], part[VPT];
+#pragma unroll
+        for (int m = 0; m < VPT; ++m) {
+            part[m] = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) t[m][e] = res[m][e] = 0.f;
             if (!in[m]) continue;
-            load8(x + at, t[m]);
-            if (residual) load8(residual + at, res[m]);
+            widen8(rx[m], t[m]);
+            if (residual) widen8(rr[m], res[m]);
             if (z) {
                 float zz[8];
-                load8(z + at, zz);
+                widen8(rz[m], zz);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) t[m][e] *= zz[e] * ssm_sigmoid(zz[e]);
             }
-            float v = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v = fmaf(t[m][e], t[m][e], v);
-            ss += v;
-            if (a.post && a.groups > 1) vec[tid + m * blockDim.x] = v;
+            for (int e = 0; e < 8; ++e) part[m] = fmaf(t[m][e], t[m][e], part[m]);
         }
+        fetch(row + gridDim.x);
         if (a.post) {
-            float all = 0.f;
-            if (a.groups > 1) group_sums(vec, gsum, nvec, a.groups);
-            else all = block_sum(ss, red);
+            group_sums<VPT>(rs, 0, gr, a.groups, in, part);
 #pragma unroll
             for (int m = 0; m < VPT; ++m) {
-                const float inv = rsqrtf(fmaf(a.groups > 1 ? gsum[group[m]] : all, inv_width, a.eps));
+                const float inv = rsqrtf(fmaf(part[m], inv_width, a.eps));
 #pragma unroll
                 for (int e = 0; e < 8; ++e) t[m][e] *= inv * post[m][e];
             }
         }
-        float rr = 0.f;
 #pragma unroll
         for (int m = 0; m < VPT; ++m) {
+            part[m] = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 t[m][e] = fmaf(t[m][e], scale[m][e], res[m][e]);
-                rr = fmaf(t[m][e], t[m][e], rr);
+                part[m] = fmaf(t[m][e], t[m][e], part[m]);
             }
-            if (r_out && in[m]) Vec8<T>::store(r_out + base + 8 * (tid + m * static_cast<int>(blockDim.x)), t[m]);
+            if (r_out && in[m]) Vec8<T>::store(r_out + base + at[m], t[m]);
         }
         if (n_out) {
-            const float inv = rsqrtf(block_sum(rr, red) / a.d + a.eps);
+            float total[1] = {0.f};
+#pragma unroll
+            for (int m = 0; m < VPT; ++m) total[0] += part[m];
+            row_total<1>(rs, 1, total);
+            const float inv = rsqrtf(fmaf(total[0], inv_d, a.eps));
 #pragma unroll
             for (int m = 0; m < VPT; ++m) {
                 if (!in[m]) continue;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) t[m][e] *= inv * pre[m][e];
-                Vec8<T>::store(n_out + base + 8 * (tid + m * static_cast<int>(blockDim.x)), t[m]);
+                Vec8<T>::store(n_out + base + at[m], t[m]);
             }
         }
     }
@@ -140,80 +239,109 @@ struct NormGradArgs {
 // The forward's row again, then backwards through it: with nh = r / rms(r) and th = t / rms_group(t),
 //     dr = d_r + (k - nh mean(k nh)) / rms(r),    k = d_n pre
 //     dt = (q - th mean_group(q th)) / rms_group(t), q = dr scale post
-// dx = dt silu(z), dz = dt x silu'(z); the parameters' sums stay in registers over the block's rows.
-template <typename T, int VPT, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads)
-    norm_grad_kernel(NormGradArgs ga, const T* __restrict__ x, const T* __restrict__ z, const T* __restrict__ residual,
-                     const T* __restrict__ d_r, const T* __restrict__ d_n, T* __restrict__ dx, T* __restrict__ dz,
-                     T* __restrict__ dres) {
+// dx = dt silu(z), dz = dt x silu'(z). The parameters' sums stay in registers over the block's rows, the weights in
+// shared memory, the next row's loads in flight.
+template <typename T, int VPT, int kMaxThreads, int kPerSm>
+__global__ void __launch_bounds__(kMaxThreads, kPerSm)
+    norm_grad_kernel(NormGradArgs ga, const T* x, const T* z, const T* residual, const T* d_r, const T* d_n, T* dx, T* dz, T* dres) {
     const NormArgs& a = ga.n;
-    __shared__ float red[32], vec[kMaxD / 8], gsum[kMaxD / 8];
+    __shared__ RowSums rs;
+    extern __shared__ float4 weights_f4[];
+    float* const weights = reinterpret_cast<float*>(weights_f4);  // post, scale, pre; ones where absent
     const int tid = threadIdx.x, nvec = a.d / 8;
+    for (int i = tid; i < a.d; i += blockDim.x) {
+        weights[i] = a.post ? a.post[i] : 1.f;
+        weights[a.d + i] = a.scale ? a.scale[i] : 1.f;
+        weights[2 * a.d + i] = a.pre ? a.pre[i] : 1.f;
+    }
+    __syncthreads();
     float apost[VPT][8] = {}, ascale[VPT][8] = {}, apre[VPT][8] = {};
     bool in[VPT];
-    int group[VPT];
+    int at[VPT];
 #pragma unroll
     for (int m = 0; m < VPT; ++m) {
-        const int i = tid + m * blockDim.x;
-        in[m] = i < nvec;
-        group[m] = in[m] ? i / (nvec / a.groups) : 0;
+        in[m] = tid + m * static_cast<int>(blockDim.x) < nvec;
+        at[m] = in[m] ? 8 * (tid + m * static_cast<int>(blockDim.x)) : 0;
     }
+    auto weight = [&](int which, int m, float (&w)[8]) {
+        const float4* p = reinterpret_cast<const float4*>(weights + which * a.d + at[m]);
+        const float4 u = p[0], v = p[1];
+        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w; w[4] = v.x; w[5] = v.y; w[6] = v.z; w[7] = v.w;
+    };
     const float inv_width = static_cast<float>(a.groups) / a.d, inv_d = 1.f / a.d;
-    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const Groups<VPT> gr(nvec, a.groups);
+    Raw8<T> rx[VPT], rz[VPT], rr[VPT], rdr[VPT], rdn[VPT];
+    auto fetch = [&](long long row) {
+        if (row >= a.rows) return;
         const size_t base = static_cast<size_t>(row) * a.d;
-        float xv[VPT][8], zv[VPT][8], t[VPT][8], r[VPT][8], dr[VPT][8], k[VPT][8], inv_t[VPT];
-        float ss = 0.f;
 #pragma unroll
         for (int m = 0; m < VPT; ++m) {
-            const size_t at = base + 8 * (tid + m * static_cast<int>(blockDim.x));
+            if (!in[m]) continue;
+            rx[m] = load_raw(x + base + at[m]);
+            if (z) rz[m] = load_raw(z + base + at[m]);
+            if (residual) rr[m] = load_raw(residual + base + at[m]);
+            if (d_r) rdr[m] = load_raw(d_r + base + at[m]);
+            if (d_n) rdn[m] = load_raw(d_n + base + at[m]);
+        }
+    };
+    fetch(blockIdx.x);
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const size_t base = static_cast<size_t>(row) * a.d;
+        float t[VPT][8], r[VPT][8], dr[VPT][8], k[VPT][8], one[VPT], inv_t[VPT], both[2] = {0.f, 0.f};
+        Raw8<T> kx[VPT], kz[VPT];  // x and z for the end of the row
 #pragma unroll
-            for (int e = 0; e < 8; ++e) xv[m][e] = zv[m][e] = r[m][e] = dr[m][e] = k[m][e] = 0.f;
-            if (in[m]) {
-                load8(x + at, xv[m]);
-                if (z) load8(z + at, zv[m]);
-                if (residual) load8(residual + at, r[m]);
-                if (d_r) load8(d_r + at, dr[m]);
-                if (d_n) load8(d_n + at, k[m]);
-            }
-            float v = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                t[m][e] = z ? xv[m][e] * zv[m][e] * ssm_sigmoid(zv[m][e]) : xv[m][e];
-                v = fmaf(t[m][e], t[m][e], v);
-            }
-            ss += v;
+        for (int m = 0; m < VPT; ++m) {
+            kx[m] = rx[m];
+            kz[m] = rz[m];
+            one[m] = 0.f;
             inv_t[m] = 1.f;
-            if (a.post && a.groups > 1 && in[m]) vec[tid + m * blockDim.x] = v;
-        }
-        if (a.post) {
-            float all = 0.f;
-            if (a.groups > 1) group_sums(vec, gsum, nvec, a.groups);
-            else all = block_sum(ss, red);
 #pragma unroll
-            for (int m = 0; m < VPT; ++m) inv_t[m] = rsqrtf(fmaf(a.groups > 1 ? gsum[group[m]] : all, inv_width, a.eps));
+            for (int e = 0; e < 8; ++e) t[m][e] = r[m][e] = dr[m][e] = k[m][e] = 0.f;
+            if (!in[m]) continue;
+            widen8(rx[m], t[m]);
+            if (residual) widen8(rr[m], r[m]);
+            if (d_r) widen8(rdr[m], dr[m]);
+            if (d_n) widen8(rdn[m], k[m]);
+            if (z) {
+                float zv[8];
+                widen8(rz[m], zv);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[m][e] *= zv[e] * ssm_sigmoid(zv[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) one[m] = fmaf(t[m][e], t[m][e], one[m]);
         }
-        float rr = 0.f, kr = 0.f;
+        fetch(row + gridDim.x);
+        if (a.post) {
+            group_sums<VPT>(rs, 0, gr, a.groups, in, one);
+#pragma unroll
+            for (int m = 0; m < VPT; ++m) {
+                inv_t[m] = rsqrtf(fmaf(one[m], inv_width, a.eps));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[m][e] *= inv_t[m];  // th
+            }
+        }
 #pragma unroll
         for (int m = 0; m < VPT; ++m) {
             float post[8], scale[8], pre[8];
-            const int c = 8 * (tid + m * static_cast<int>(blockDim.x));
-            weights8(a.post, c, in[m], post);
-            weights8(a.scale, c, in[m], scale);
-            weights8(a.pre, c, in[m], pre);
+            weight(0, m, post);
+            weight(1, m, scale);
+            weight(2, m, pre);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                r[m][e] = fmaf(t[m][e] * inv_t[m] * post[e], scale[e], r[m][e]);
-                rr = fmaf(r[m][e], r[m][e], rr);
-                kr = fmaf(k[m][e] * pre[e], r[m][e], kr);
+                r[m][e] = fmaf(t[m][e] * post[e], scale[e], r[m][e]);
+                both[0] = fmaf(r[m][e], r[m][e], both[0]);
+                both[1] = fmaf(k[m][e] * pre[e], r[m][e], both[1]);
             }
         }
         if (d_n) {
-            const float inv = rsqrtf(fmaf(block_sum(rr, red), inv_d, a.eps));
-            const float mean = block_sum(kr, red) * inv * inv_d;  // mean(k nh)
+            row_total<2>(rs, 1, both);
+            const float inv = rsqrtf(fmaf(both[0], inv_d, a.eps));
+            const float mean = both[1] * inv * inv_d;  // mean(k nh)
 #pragma unroll
             for (int m = 0; m < VPT; ++m) {
                 float pre[8];
-                weights8(a.pre, 8 * (tid + m * static_cast<int>(blockDim.x)), in[m], pre);
+                weight(2, m, pre);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float nh = r[m][e] * inv;
@@ -222,63 +350,59 @@ __global__ void __launch_bounds__(kMaxThreads)
                 }
             }
         }
-        float qs = 0.f;
 #pragma unroll
         for (int m = 0; m < VPT; ++m) {
             float post[8], scale[8];
-            const int c = 8 * (tid + m * static_cast<int>(blockDim.x));
-            weights8(a.post, c, in[m], post);
-            weights8(a.scale, c, in[m], scale);
-            if (dres && in[m]) Vec8<T>::store(dres + base + c, dr[m]);
-            float v = 0.f;
+            weight(0, m, post);
+            weight(1, m, scale);
+            if (dres && in[m]) Vec8<T>::store(dres + base + at[m], dr[m]);
+            one[m] = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float th = t[m][e] * inv_t[m];
-                ascale[m][e] = fmaf(dr[m][e], th * post[e], ascale[m][e]);
+                ascale[m][e] = fmaf(dr[m][e], t[m][e] * post[e], ascale[m][e]);
                 const float dp = dr[m][e] * scale[e];
-                apost[m][e] = fmaf(dp, th, apost[m][e]);
+                apost[m][e] = fmaf(dp, t[m][e], apost[m][e]);
                 k[m][e] = dp * post[e];
-                v = fmaf(k[m][e], th, v);
+                one[m] = fmaf(k[m][e], t[m][e], one[m]);
             }
-            qs += v;
-            if (a.post && a.groups > 1 && in[m]) vec[tid + m * blockDim.x] = v;
         }
-        float all = 0.f;
         if (a.post) {
-            if (a.groups > 1) group_sums(vec, gsum, nvec, a.groups);
-            else all = block_sum(qs, red);
+            group_sums<VPT>(rs, 0, gr, a.groups, in, one);
+#pragma unroll
+            for (int m = 0; m < VPT; ++m) {
+                const float mean = one[m] * inv_width;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) k[m][e] = inv_t[m] * fmaf(-t[m][e], mean, k[m][e]);
+            }
         }
 #pragma unroll
         for (int m = 0; m < VPT; ++m) {
             if (!in[m]) continue;
-            const size_t at = base + 8 * (tid + m * static_cast<int>(blockDim.x));
-            const float mean = a.post ? (a.groups > 1 ? gsum[group[m]] : all) * inv_width : 0.f;
-            float dzv[8];
+            if (z) {
+                float xv[8], zv[8], dzv[8];
+                widen8(kx[m], xv);
+                widen8(kz[m], zv);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float th = t[m][e] * inv_t[m];
-                float dt = a.post ? inv_t[m] * fmaf(-th, mean, k[m][e]) : k[m][e];
-                if (z) {
-                    const float sg = ssm_sigmoid(zv[m][e]);
-                    dzv[e] = dt * xv[m][e] * sg * fmaf(zv[m][e], 1.f - sg, 1.f);
-                    dt *= zv[m][e] * sg;
+                for (int e = 0; e < 8; ++e) {
+                    const float sg = ssm_sigmoid(zv[e]);
+                    dzv[e] = k[m][e] * xv[e] * sg * fmaf(zv[e], 1.f - sg, 1.f);
+                    k[m][e] *= zv[e] * sg;
                 }
-                k[m][e] = dt;
+                Vec8<T>::store(dz + base + at[m], dzv);
             }
-            Vec8<T>::store(dx + at, k[m]);
-            if (z) Vec8<T>::store(dz + at, dzv);
+            Vec8<T>::store(dx + base + at[m], k[m]);
         }
     }
     float* to = ga.part + static_cast<size_t>(blockIdx.x) * 3 * a.d;
 #pragma unroll
     for (int m = 0; m < VPT; ++m) {
         if (!in[m]) continue;
-        const int c = 8 * (tid + m * static_cast<int>(blockDim.x));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            to[c + e] = apost[m][e];
-            to[a.d + c + e] = ascale[m][e];
-            to[2 * a.d + c + e] = apre[m][e];
+        for (int e = 0; e < 2; ++e) {
+            const float* const acc[3] = {apost[m], ascale[m], apre[m]};
+#pragma unroll
+            for (int w = 0; w < 3; ++w)
+                reinterpret_cast<float4*>(to + w * a.d + at[m])[e] = make_float4(acc[w][4 * e], acc[w][4 * e + 1], acc[w][4 * e + 2], acc[w][4 * e + 3]);
         }
     }
 }
@@ -293,8 +417,19 @@ __global__ void __launch_bounds__(256)
     if (!out) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float v = 0.f;
-    if (c < d)
-        for (int k = warp; k < blocks; k += 8) v += part[(static_cast<size_t>(k) * 3 + blockIdx.y) * d + c];
+    if (c < d) {
+        const float* src = part + static_cast<size_t>(blockIdx.y) * d + c;
+        const size_t step = 3 * static_cast<size_t>(d);
+        int k = warp;
+        for (; k + 56 < blocks; k += 64) {  // eight loads in flight
+            float t[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) t[q] = src[(k + 8 * q) * step];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v += t[q];
+        }
+        for (; k < blocks; k += 8) v += src[k * step];
+    }
     red[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && c < d)
@@ -311,21 +446,20 @@ int sm_count() {
 struct NormLaunch {
     int vpt, threads, blocks;
 };
-// Whole warps over the row's vectors, at most 512 threads; as many blocks as `threads_per_sm` allows, each
-// walking over rows.
-NormLaunch norm_launch(long long rows, int d, int threads_per_sm) {
+// Whole warps over the row's vectors, one (gradients up to 4096 wide) or two per thread, and the blocks that the
+// registers allow on each SM at 128 per thread, each walking over rows.
+NormLaunch norm_launch(long long rows, int d, int vpt) {
     NormLaunch l;
     const int nvec = d / 8;
-    l.vpt = nvec <= 512 ? 1 : 2;
+    l.vpt = vpt;
     l.threads = ((nvec + l.vpt - 1) / l.vpt + 31) / 32 * 32;
-    int per = threads_per_sm / l.threads;
+    int per = 512 / l.threads;
     if (per < 1) per = 1;
-    if (per > 32) per = 32;
     const long long most = (long long)sm_count() * per;
     l.blocks = static_cast<int>(rows < most ? rows : most);
     return l;
 }
-constexpr int kFwdThreadsPerSm = 1024, kGradThreadsPerSm = 512;
+NormLaunch norm_grad_launch(long long rows, int d) { return norm_launch(rows, d, d <= 4096 ? 1 : 2); }
 
 gdn2_status norm_check(long long rows, int d, int groups, float eps, const void* post, gdn2_dtype dt) {
     if ((dt != GDN2_F32 && dt != GDN2_BF16) || rows < 0 || d <= 0 || groups <= 0 || !(eps >= 0.f)) return GDN2_ERR_INVALID_ARG;
@@ -356,12 +490,12 @@ gdn2_status gdn2_block_norm(const void* x, const void* z, const float* post_weig
     if (rows == 0) return GDN2_OK;
     if (!x) return GDN2_ERR_INVALID_ARG;
     if (!all_aligned({x, z, post_weight, residual, scale, pre_weight, r, n})) return GDN2_ERR_MISALIGNED;
-    const NormLaunch l = norm_launch(rows, d, kFwdThreadsPerSm);
+    const NormLaunch l = norm_launch(rows, d, 2);
     const NormArgs a{post_weight, scale, pre_weight, rows, d, groups, eps};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     auto go = [&](auto zero) {
         using T = decltype(zero);
-        auto* k = l.vpt == 1 ? norm_kernel<T, 1> : norm_kernel<T, 2>;
+        auto* k = l.threads <= 256 ? norm_kernel<T, 2, 256, 2> : norm_kernel<T, 2, 512, 1>;
         k<<<l.blocks, l.threads, 0, s>>>(a, static_cast<const T*>(x), static_cast<const T*>(z), static_cast<const T*>(residual),
                                          static_cast<T*>(r), static_cast<T*>(n));
     };
@@ -371,7 +505,7 @@ gdn2_status gdn2_block_norm(const void* x, const void* z, const float* post_weig
 
 size_t gdn2_block_norm_backward_workspace_size(long long rows, int d) {
     if (rows <= 0 || d <= 0 || d % 8 || d > kMaxD) return 0;
-    return align_up(sizeof(float) * 3 * d * static_cast<size_t>(norm_launch(rows, d, kGradThreadsPerSm).blocks), 256);
+    return align_up(sizeof(float) * 3 * d * static_cast<size_t>(norm_grad_launch(rows, d).blocks), 256);
 }
 
 gdn2_status gdn2_block_norm_backward(const void* x, const void* z, const float* post_weight, const void* residual,
@@ -397,17 +531,20 @@ gdn2_status gdn2_block_norm_backward(const void* x, const void* z, const float* 
         return GDN2_ERR_MISALIGNED;
     if (!workspace || ws_bytes < gdn2_block_norm_backward_workspace_size(rows, d)) return GDN2_ERR_WORKSPACE;
     if (!aligned16(workspace)) return GDN2_ERR_MISALIGNED;
-    const NormLaunch l = norm_launch(rows, d, kGradThreadsPerSm);
+    const NormLaunch l = norm_grad_launch(rows, d);
+    const int smem = 3 * d * static_cast<int>(sizeof(float));
     const NormGradArgs a{{post_weight, scale, pre_weight, rows, d, groups, eps}, static_cast<float*>(workspace)};
     auto go = [&](auto zero) {
         using T = decltype(zero);
-        auto* k = l.vpt == 2 ? norm_grad_kernel<T, 2, 512> : l.threads <= 256 ? norm_grad_kernel<T, 1, 256> : norm_grad_kernel<T, 1, 512>;
-        k<<<l.blocks, l.threads, 0, s>>>(a, static_cast<const T*>(x), static_cast<const T*>(z), static_cast<const T*>(residual),
-                                         static_cast<const T*>(d_r), static_cast<const T*>(d_n), static_cast<T*>(dx),
-                                         static_cast<T*>(dz), static_cast<T*>(dresidual));
+        auto* k = l.vpt == 2 ? norm_grad_kernel<T, 2, 512, 1> : l.threads <= 256 ? norm_grad_kernel<T, 1, 256, 2> : norm_grad_kernel<T, 1, 512, 1>;
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * kMaxD * static_cast<int>(sizeof(float))) != cudaSuccess)
+            return false;
+        k<<<l.blocks, l.threads, smem, s>>>(a, static_cast<const T*>(x), static_cast<const T*>(z), static_cast<const T*>(residual),
+                                            static_cast<const T*>(d_r), static_cast<const T*>(d_n), static_cast<T*>(dx),
+                                            static_cast<T*>(dz), static_cast<T*>(dresidual));
+        return cudaGetLastError() == cudaSuccess;
     };
-    if (dt == GDN2_BF16) go(__nv_bfloat16{}); else go(0.f);
-    if (cudaGetLastError() != cudaSuccess) return GDN2_ERR_CUDA;
+    if (!(dt == GDN2_BF16 ? go(__nv_bfloat16{}) : go(0.f))) return GDN2_ERR_CUDA;
     if (dpost_weight || dscale || dpre_weight)
         norm_sum_kernel<<<dim3((d + 31) / 32, 3), 256, 0, s>>>(a.part, l.blocks, d, dpost_weight, dscale, dpre_weight);
     return cudaGetLastError() == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA;

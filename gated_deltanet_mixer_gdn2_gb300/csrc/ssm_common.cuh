@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace gdn2 {
 
@@ -122,7 +123,12 @@ __device__ __forceinline__ bool find_row(const Seqs& s, int r, int& seq, int& st
     return r >= start && r < end;
 }
 
-__device__ __forceinline__ float ssm_sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+// 1 / (1 + e^-v) with the hardware's approximations (each within 2 units in the last place)
+__device__ __forceinline__ float ssm_sigmoid(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-kLog2e * v)));
+    return r;
+}
 // log(1 + e^v), exact to fp32 for either sign
 __device__ __forceinline__ float ssm_softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
 

@@ -5,7 +5,6 @@
 #include <initializer_list>
 #include <type_traits>
 
-#include "ptx.cuh"
 #include "ssm_common.cuh"
 
 namespace gdn2 {
@@ -79,11 +78,6 @@ __device__ __forceinline__ void window_before(const ConvArgs& a, const T* x, int
     }
 }
 
-__device__ __forceinline__ float sigmoid_approx(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-kLog2e * x)));
-    return r;
-}
 // The convolution at one row: taps over the three rows before it and itself.
 template <int CH>
 __device__ __forceinline__ void taps(const float (&w)[kTaps][CH], const float (&bias)[CH], const float (&a)[CH], const float (&b)[CH],
@@ -171,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 8)
                 taps<CH>(w, bias, win[q], win[(q + 1) & 3], win[(q + 2) & 3], win[(q + 3) & 3], v);
                 if (kSilu) {
 #pragma unroll
-                    for (int e = 0; e < CH; ++e) v[e] *= sigmoid_approx(v[e]);
+                    for (int e = 0; e < CH; ++e) v[e] *= ssm_sigmoid(v[e]);
                 }
                 if (r + q < hi) Ch::store(up + static_cast<size_t>(q) * a.channels, v);
             }
@@ -326,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 3)
                 if (kSilu) {
 #pragma unroll
                     for (int e = 0; e < CH; ++e) {
-                        const float sg = sigmoid_approx(v[e]);
+                        const float sg = ssm_sigmoid(v[e]);
                         dv[e] *= sg * fmaf(v[e], 1.f - sg, 1.f);
                     }
                 }
