@@ -42,11 +42,8 @@ __device__ __forceinline__ void row_total(RowSums& rs, int slot, float (&v)[kWhi
     }
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWhich; ++w) {
-        float t = 0.f;
-        for (int k = 0; k < warps; ++k) t += rs.part[slot][w][k];
-        v[w] = t;
-    }
+    for (int w = 0; w < kWhich; ++w)
+        v[w] = warp_sum(static_cast<int>(threadIdx.x & 31) < warps ? rs.part[slot][w][threadIdx.x & 31] : 0.f);
 }
 
 // Where a thread's vectors lie among the groups. Where groups are whole warps' worth of vectors (every common width)
@@ -139,26 +136,36 @@ __device__ __forceinline__ void weights8(const float* w, int c, bool in, float (
     }
 }
 
-// One row per block and trip, VPT vectors of eight elements per thread. The weights stay in registers over the
-// block's rows (at 512 threads of 64 registers they were fetched again for every row: 181 us instead of 108 us at
-// 16384 x 4096), and the next row's loads are in flight while a row is summed.
+// One row per block and trip, VPT vectors of eight elements per thread. The weights lie in shared memory, so that one
+// vector per thread fits 64 registers and 32 warps cover the loads and the two barriers of a row: at 16384 x 4096,
+// 122 us (5.5 TB/s, 81% of the copy rate); with two vectors per thread and 24 warps 140 us, with the weights in the
+// registers of 16 warps 159 us. The next row's loads are in flight while a row is summed.
 template <typename T, int VPT, int kMaxThreads, int kPerSm>
 __global__ void __launch_bounds__(kMaxThreads, kPerSm)
     norm_kernel(NormArgs a, const T* x, const T* z, const T* residual, T* r_out, T* n_out) {
     __shared__ RowSums rs;
     const int tid = threadIdx.x, nvec = a.d / 8;
-    float post[VPT][8], scale[VPT][8], pre[VPT][8];
+    extern __shared__ float4 weights_f4[];
+    float* const weights = reinterpret_cast<float*>(weights_f4);  // post, scale, pre; ones where absent
+    for (int i = tid; i < a.d; i += blockDim.x) {
+        weights[i] = a.post ? a.post[i] : 1.f;
+        weights[a.d + i] = a.scale ? a.scale[i] : 1.f;
+        weights[2 * a.d + i] = a.pre ? a.pre[i] : 1.f;
+    }
+    __syncthreads();
     bool in[VPT];
     int at[VPT];
 #pragma unroll
     for (int m = 0; m < VPT; ++m) {
         const int i = tid + m * blockDim.x;
         in[m] = i < nvec;
-        at[m] = 8 * i;
-        weights8(a.post, at[m], in[m], post[m]);
-        weights8(a.scale, at[m], in[m], scale[m]);
-        weights8(a.pre, at[m], in[m], pre[m]);
+        at[m] = in[m] ? 8 * i : 0;
     }
+    auto weight = [&](int which, int m, float (&w)[8]) {
+        const float4* p = reinterpret_cast<const float4*>(weights + which * a.d + at[m]);
+        const float4 u = p[0], v = p[1];
+        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w; w[4] = v.x; w[5] = v.y; w[6] = v.z; w[7] = v.w;
+    };
     const float inv_width = static_cast<float>(a.groups) / a.d, inv_d = 1.f / a.d;
     const Groups<VPT> gr(nvec, a.groups);
     Raw8<T> rx[VPT], rz[VPT], rr[VPT];
@@ -200,16 +207,20 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
 #pragma unroll
             for (int m = 0; m < VPT; ++m) {
                 const float inv = rsqrtf(fmaf(part[m], inv_width, a.eps));
+                float post[8];
+                weight(0, m, post);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) t[m][e] *= inv * post[m][e];
+                for (int e = 0; e < 8; ++e) t[m][e] *= inv * post[e];
             }
         }
 #pragma unroll
         for (int m = 0; m < VPT; ++m) {
             part[m] = 0.f;
+            float scale[8];
+            weight(1, m, scale);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                t[m][e] = fmaf(t[m][e], scale[m][e], res[m][e]);
+                t[m][e] = fmaf(t[m][e], scale[e], res[m][e]);
                 part[m] = fmaf(t[m][e], t[m][e], part[m]);
             }
             if (r_out && in[m]) Vec8<T>::store(r_out + base + at[m], t[m]);
@@ -223,8 +234,10 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
 #pragma unroll
             for (int m = 0; m < VPT; ++m) {
                 if (!in[m]) continue;
+                float pre[8];
+                weight(2, m, pre);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) t[m][e] *= inv * pre[m][e];
+                for (int e = 0; e < 8; ++e) t[m][e] *= inv * pre[e];
                 Vec8<T>::store(n_out + base + at[m], t[m]);
             }
         }
@@ -233,41 +246,35 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
 
 struct NormGradArgs {
     NormArgs n;
-    float* part;  // [blocks][3][d]: dpost, dscale, dpre
+    float* part;  // [blocks][2][d]: sums of dr th, of d_n nh
 };
 
 // The forward's row again, then backwards through it: with nh = r / rms(r) and th = t / rms_group(t),
 //     dr = d_r + (k - nh mean(k nh)) / rms(r),    k = d_n pre
 //     dt = (q - th mean_group(q th)) / rms_group(t), q = dr scale post
-// dx = dt silu(z), dz = dt x silu'(z). The parameters' sums stay in registers over the block's rows, the weights in
-// shared memory, the next row's loads in flight.
+// dx = dt silu(z), dz = dt x silu'(z). dpost and dscale are one sum over the rows, of dr th, times scale and post; it and
+// dpre's, and the weights, stay in registers over the block's rows, the next row's loads in flight.
 template <typename T, int VPT, int kMaxThreads, int kPerSm>
 __global__ void __launch_bounds__(kMaxThreads, kPerSm)
     norm_grad_kernel(NormGradArgs ga, const T* x, const T* z, const T* residual, const T* d_r, const T* d_n, T* dx, T* dz, T* dres) {
     const NormArgs& a = ga.n;
     __shared__ RowSums rs;
-    extern __shared__ float4 weights_f4[];
-    float* const weights = reinterpret_cast<float*>(weights_f4);  // post, scale, pre; ones where absent
     const int tid = threadIdx.x, nvec = a.d / 8;
-    for (int i = tid; i < a.d; i += blockDim.x) {
-        weights[i] = a.post ? a.post[i] : 1.f;
-        weights[a.d + i] = a.scale ? a.scale[i] : 1.f;
-        weights[2 * a.d + i] = a.pre ? a.pre[i] : 1.f;
-    }
-    __syncthreads();
-    float apost[VPT][8] = {}, ascale[VPT][8] = {}, apre[VPT][8] = {};
+    float sp[VPT][8], pre[VPT][8];           // scale post, pre
+    float asum[VPT][8] = {}, apre[VPT][8] = {};  // sums of dr th (dpost = scale asum, dscale = post asum) and of d_n nh
     bool in[VPT];
     int at[VPT];
 #pragma unroll
     for (int m = 0; m < VPT; ++m) {
         in[m] = tid + m * static_cast<int>(blockDim.x) < nvec;
         at[m] = in[m] ? 8 * (tid + m * static_cast<int>(blockDim.x)) : 0;
+        float post[8];
+        weights8(a.post, at[m], in[m], post);
+        weights8(a.scale, at[m], in[m], sp[m]);
+        weights8(a.pre, at[m], in[m], pre[m]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sp[m][e] *= post[e];
     }
-    auto weight = [&](int which, int m, float (&w)[8]) {
-        const float4* p = reinterpret_cast<const float4*>(weights + which * a.d + at[m]);
-        const float4 u = p[0], v = p[1];
-        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w; w[4] = v.x; w[5] = v.y; w[6] = v.z; w[7] = v.w;
-    };
     const float inv_width = static_cast<float>(a.groups) / a.d, inv_d = 1.f / a.d;
     const Groups<VPT> gr(nvec, a.groups);
     Raw8<T> rx[VPT], rz[VPT], rr[VPT], rdr[VPT], rdn[VPT];
@@ -323,15 +330,11 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
         }
 #pragma unroll
         for (int m = 0; m < VPT; ++m) {
-            float post[8], scale[8], pre[8];
-            weight(0, m, post);
-            weight(1, m, scale);
-            weight(2, m, pre);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                r[m][e] = fmaf(t[m][e] * post[e], scale[e], r[m][e]);
+                r[m][e] = fmaf(t[m][e], sp[m][e], r[m][e]);
                 both[0] = fmaf(r[m][e], r[m][e], both[0]);
-                both[1] = fmaf(k[m][e] * pre[e], r[m][e], both[1]);
+                both[1] = fmaf(k[m][e] * pre[m][e], r[m][e], both[1]);
             }
         }
         if (d_n) {
@@ -340,29 +343,22 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
             const float mean = both[1] * inv * inv_d;  // mean(k nh)
 #pragma unroll
             for (int m = 0; m < VPT; ++m) {
-                float pre[8];
-                weight(2, m, pre);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float nh = r[m][e] * inv;
                     apre[m][e] = fmaf(k[m][e], nh, apre[m][e]);
-                    dr[m][e] = fmaf(inv, fmaf(-nh, mean, k[m][e] * pre[e]), dr[m][e]);
+                    dr[m][e] = fmaf(inv, fmaf(-nh, mean, k[m][e] * pre[m][e]), dr[m][e]);
                 }
             }
         }
 #pragma unroll
         for (int m = 0; m < VPT; ++m) {
-            float post[8], scale[8];
-            weight(0, m, post);
-            weight(1, m, scale);
             if (dres && in[m]) Vec8<T>::store(dres + base + at[m], dr[m]);
             one[m] = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                ascale[m][e] = fmaf(dr[m][e], t[m][e] * post[e], ascale[m][e]);
-                const float dp = dr[m][e] * scale[e];
-                apost[m][e] = fmaf(dp, t[m][e], apost[m][e]);
-                k[m][e] = dp * post[e];
+                asum[m][e] = fmaf(dr[m][e], t[m][e], asum[m][e]);
+                k[m][e] = dr[m][e] * sp[m][e];
                 one[m] = fmaf(k[m][e], t[m][e], one[m]);
             }
         }
@@ -393,33 +389,29 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
             Vec8<T>::store(dx + base + at[m], k[m]);
         }
     }
-    float* to = ga.part + static_cast<size_t>(blockIdx.x) * 3 * a.d;
+    float* to = ga.part + static_cast<size_t>(blockIdx.x) * 2 * a.d;
 #pragma unroll
     for (int m = 0; m < VPT; ++m) {
         if (!in[m]) continue;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float* const acc[3] = {apost[m], ascale[m], apre[m]};
-#pragma unroll
-            for (int w = 0; w < 3; ++w)
-                reinterpret_cast<float4*>(to + w * a.d + at[m])[e] = make_float4(acc[w][4 * e], acc[w][4 * e + 1], acc[w][4 * e + 2], acc[w][4 * e + 3]);
+            reinterpret_cast<float4*>(to + at[m])[e] = make_float4(asum[m][4 * e], asum[m][4 * e + 1], asum[m][4 * e + 2], asum[m][4 * e + 3]);
+            reinterpret_cast<float4*>(to + a.d + at[m])[e] = make_float4(apre[m][4 * e], apre[m][4 * e + 1], apre[m][4 * e + 2], apre[m][4 * e + 3]);
         }
     }
 }
 
 // The blocks' parameter sums in a fixed order.
 __global__ void __launch_bounds__(256)
-    norm_sum_kernel(const float* __restrict__ part, int blocks, int d, float* __restrict__ dpost, float* __restrict__ dscale,
-                    float* __restrict__ dpre) {
+    norm_sum_kernel(const float* __restrict__ part, int blocks, int d, const float* __restrict__ post, const float* __restrict__ scale,
+                    float* __restrict__ dpost, float* __restrict__ dscale, float* __restrict__ dpre) {
     __shared__ float red[8][33];
-    float* const outs[3] = {dpost, dscale, dpre};
-    float* out = outs[blockIdx.y];
-    if (!out) return;
+    if (blockIdx.y ? !dpre : !dpost && !dscale) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float v = 0.f;
     if (c < d) {
         const float* src = part + static_cast<size_t>(blockIdx.y) * d + c;
-        const size_t step = 3 * static_cast<size_t>(d);
+        const size_t step = 2 * static_cast<size_t>(d);
         int k = warp;
         for (; k + 56 < blocks; k += 64) {  // eight loads in flight
             float t[8];
@@ -432,8 +424,14 @@ __global__ void __launch_bounds__(256)
     }
     red[warp][lane] = v;
     __syncthreads();
-    if (warp == 0 && c < d)
-        out[c] = ((red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane])) + ((red[4][lane] + red[5][lane]) + (red[6][lane] + red[7][lane]));
+    if (warp || c >= d) return;
+    v = ((red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane])) + ((red[4][lane] + red[5][lane]) + (red[6][lane] + red[7][lane]));
+    if (blockIdx.y) {
+        dpre[c] = v;
+    } else {
+        if (dpost) dpost[c] = scale ? scale[c] * v : v;
+        if (dscale) dscale[c] = post ? post[c] * v : v;
+    }
 }
 
 int sm_count() {
@@ -446,20 +444,21 @@ int sm_count() {
 struct NormLaunch {
     int vpt, threads, blocks;
 };
-// Whole warps over the row's vectors, one (gradients up to 4096 wide) or two per thread, and the blocks that the
-// registers allow on each SM at 128 per thread, each walking over rows.
-NormLaunch norm_launch(long long rows, int d, int vpt) {
+// Whole warps over the row's vectors, one per thread up to 4096 wide, else two; as many blocks per SM as
+// `threads_per_sm` allows, each walking over rows.
+NormLaunch norm_launch(long long rows, int d, int threads_per_sm) {
     NormLaunch l;
     const int nvec = d / 8;
-    l.vpt = vpt;
+    l.vpt = d <= 4096 ? 1 : 2;
     l.threads = ((nvec + l.vpt - 1) / l.vpt + 31) / 32 * 32;
-    int per = 512 / l.threads;
+    int per = threads_per_sm / l.threads;
     if (per < 1) per = 1;
     const long long most = (long long)sm_count() * per;
     l.blocks = static_cast<int>(rows < most ? rows : most);
     return l;
 }
-NormLaunch norm_grad_launch(long long rows, int d) { return norm_launch(rows, d, d <= 4096 ? 1 : 2); }
+NormLaunch norm_fwd_launch(long long rows, int d) { return norm_launch(rows, d, d <= 4096 ? 1024 : 512); }
+NormLaunch norm_grad_launch(long long rows, int d) { return norm_launch(rows, d, 512); }
 
 gdn2_status norm_check(long long rows, int d, int groups, float eps, const void* post, gdn2_dtype dt) {
     if ((dt != GDN2_F32 && dt != GDN2_BF16) || rows < 0 || d <= 0 || groups <= 0 || !(eps >= 0.f)) return GDN2_ERR_INVALID_ARG;
@@ -490,22 +489,25 @@ gdn2_status gdn2_block_norm(const void* x, const void* z, const float* post_weig
     if (rows == 0) return GDN2_OK;
     if (!x) return GDN2_ERR_INVALID_ARG;
     if (!all_aligned({x, z, post_weight, residual, scale, pre_weight, r, n})) return GDN2_ERR_MISALIGNED;
-    const NormLaunch l = norm_launch(rows, d, 2);
+    const NormLaunch l = norm_fwd_launch(rows, d);
+    const int smem = 3 * d * static_cast<int>(sizeof(float));
     const NormArgs a{post_weight, scale, pre_weight, rows, d, groups, eps};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     auto go = [&](auto zero) {
         using T = decltype(zero);
-        auto* k = l.threads <= 256 ? norm_kernel<T, 2, 256, 2> : norm_kernel<T, 2, 512, 1>;
-        k<<<l.blocks, l.threads, 0, s>>>(a, static_cast<const T*>(x), static_cast<const T*>(z), static_cast<const T*>(residual),
-                                         static_cast<T*>(r), static_cast<T*>(n));
+        auto* k = l.vpt == 1 ? norm_kernel<T, 1, 512, 2> : norm_kernel<T, 2, 512, 1>;
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * kMaxD * static_cast<int>(sizeof(float))) != cudaSuccess)
+            return false;
+        k<<<l.blocks, l.threads, smem, s>>>(a, static_cast<const T*>(x), static_cast<const T*>(z), static_cast<const T*>(residual),
+                                            static_cast<T*>(r), static_cast<T*>(n));
+        return cudaGetLastError() == cudaSuccess;
     };
-    if (dt == GDN2_BF16) go(__nv_bfloat16{}); else go(0.f);
-    return cudaGetLastError() == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA;
+    return (dt == GDN2_BF16 ? go(__nv_bfloat16{}) : go(0.f)) ? GDN2_OK : GDN2_ERR_CUDA;
 }
 
 size_t gdn2_block_norm_backward_workspace_size(long long rows, int d) {
     if (rows <= 0 || d <= 0 || d % 8 || d > kMaxD) return 0;
-    return align_up(sizeof(float) * 3 * d * static_cast<size_t>(norm_grad_launch(rows, d).blocks), 256);
+    return align_up(sizeof(float) * 2 * d * static_cast<size_t>(norm_grad_launch(rows, d).blocks), 256);
 }
 
 gdn2_status gdn2_block_norm_backward(const void* x, const void* z, const float* post_weight, const void* residual,
@@ -532,21 +534,18 @@ gdn2_status gdn2_block_norm_backward(const void* x, const void* z, const float* 
     if (!workspace || ws_bytes < gdn2_block_norm_backward_workspace_size(rows, d)) return GDN2_ERR_WORKSPACE;
     if (!aligned16(workspace)) return GDN2_ERR_MISALIGNED;
     const NormLaunch l = norm_grad_launch(rows, d);
-    const int smem = 3 * d * static_cast<int>(sizeof(float));
     const NormGradArgs a{{post_weight, scale, pre_weight, rows, d, groups, eps}, static_cast<float*>(workspace)};
     auto go = [&](auto zero) {
         using T = decltype(zero);
         auto* k = l.vpt == 2 ? norm_grad_kernel<T, 2, 512, 1> : l.threads <= 256 ? norm_grad_kernel<T, 1, 256, 2> : norm_grad_kernel<T, 1, 512, 1>;
-        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * kMaxD * static_cast<int>(sizeof(float))) != cudaSuccess)
-            return false;
-        k<<<l.blocks, l.threads, smem, s>>>(a, static_cast<const T*>(x), static_cast<const T*>(z), static_cast<const T*>(residual),
+        k<<<l.blocks, l.threads, 0, s>>>(a, static_cast<const T*>(x), static_cast<const T*>(z), static_cast<const T*>(residual),
                                             static_cast<const T*>(d_r), static_cast<const T*>(d_n), static_cast<T*>(dx),
                                             static_cast<T*>(dz), static_cast<T*>(dresidual));
         return cudaGetLastError() == cudaSuccess;
     };
     if (!(dt == GDN2_BF16 ? go(__nv_bfloat16{}) : go(0.f))) return GDN2_ERR_CUDA;
     if (dpost_weight || dscale || dpre_weight)
-        norm_sum_kernel<<<dim3((d + 31) / 32, 3), 256, 0, s>>>(a.part, l.blocks, d, dpost_weight, dscale, dpre_weight);
+        norm_sum_kernel<<<dim3((d + 31) / 32, 2), 256, 0, s>>>(a.part, l.blocks, d, post_weight, scale, dpost_weight, dscale, dpre_weight);
     return cudaGetLastError() == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA;
 }
 
