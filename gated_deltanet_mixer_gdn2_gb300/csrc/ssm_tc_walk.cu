@@ -11,21 +11,24 @@
 namespace gdn2 {
 namespace {
 
+// Two stages of keys and values; X~ replaces its values in place, with three parts the other two have a buffer per
+// stage. With one part two blocks fit an SM and hide each other's waits (4 x 2048 x 32 heads, both directions: see
+// launch_ssm_walk_tc).
 template <int kParts>
 struct Sw {
-    static constexpr int kStages = kParts == 1 ? 3 : 2;
-    static constexpr uint32_t K = 0;                                    // keys: kStages x 2 tiles
-    static constexpr uint32_t X = K + kStages * 2 * kTileBytes;         // values
-    static constexpr uint32_t XW = X + kStages * kTileBytes;            // X~: two sets of kParts
-    static constexpr uint32_t STG = XW + 2 * kParts * kTileBytes;       // a saved state on its way out
-    static constexpr uint32_t GATE = STG + kTileBytes;                  // {weight [128], decay} per stage
+    static constexpr uint32_t K = 0;                                    // 2 stages x 2 tiles
+    static constexpr uint32_t X = K + 4 * kTileBytes;                   // 2 stages
+    static constexpr uint32_t XW = X + 2 * kTileBytes;                  // 2 stages x (kParts - 1)
+    static constexpr uint32_t GATE = XW + 2 * (kParts - 1) * kTileBytes;  // {weight [128], decay} per stage
     static constexpr uint32_t kGateStage = 512 + 16;
-    static constexpr uint32_t BAR = GATE + kStages * kGateStage;
-    static constexpr uint32_t TOTAL = BAR + 256;
-    static_assert(TOTAL + 1024 <= 232448 && BAR % 8 == 0, "walk kernel shared memory");
+    static constexpr uint32_t BAR = GATE + 2 * kGateStage;
+    static constexpr uint32_t TOTAL = BAR + 128;
+    static constexpr uint32_t kAlloc = TOTAL + 1024;
+    static constexpr int kPerSm = kParts == 1 ? 2 : 1;
+    static_assert(kPerSm * (kAlloc + 1024 + 16) <= 228 * 1024 && BAR % 8 == 0, "walk kernel shared memory");
 };
-enum WalkBar { wFull = 0, wReady = 3, wEmpty = 6, wXwReady = 9, wXwFree = 15, wDFull = 21, wDEmpty = 23, wDrain = 25, wBars };
-static_assert(wBars * 8 + 16 <= 256, "barrier room");
+enum WalkBar { wFull = 0, wReady = 2, wEmpty = 4, wXwReady = 6, wDFull = 8, wDEmpty = 10, wDrain = 12, wBars };
+static_assert(wBars * 8 + 16 <= 128, "barrier room");
 constexpr int kWalkThreadsTc = 384;
 
 struct WalkMaps {
@@ -39,10 +42,8 @@ struct WalkTcArgs {
     long long wait_ns;
 };
 
-__device__ __forceinline__ void state_warps_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-
 template <int kParts>
-__global__ void __launch_bounds__(kWalkThreadsTc, 1) walk_tc_kernel(const __grid_constant__ WalkMaps maps, const __grid_constant__ WalkTcArgs a) {
+__global__ void __launch_bounds__(kWalkThreadsTc, Sw<kParts>::kPerSm) walk_tc_kernel(const __grid_constant__ WalkMaps maps, const __grid_constant__ WalkTcArgs a) {
     using sw = Sw<kParts>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -50,6 +51,7 @@ __global__ void __launch_bounds__(kWalkThreadsTc, 1) walk_tc_kernel(const __grid
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + sw::BAR);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + sw::BAR + wBars * 8);
     volatile int* err = reinterpret_cast<volatile int*>(sm + sw::BAR + wBars * 8 + 8);
+    __shared__ float totals[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const WalkJob& job = a.job[blockIdx.z];
     const bool back = job.back != 0;
@@ -63,7 +65,7 @@ __global__ void __launch_bounds__(kWalkThreadsTc, 1) walk_tc_kernel(const __grid
 
     if (tid == 0) {
         for (int i = 0; i < wBars; ++i)
-            mbar_init(bars + i, (i >= wXwReady && i < wXwFree) || (i >= wDEmpty && i < wDrain) ? 8 : 1);
+            mbar_init(bars + i, (i >= wXwReady && i < wDFull) || (i >= wDEmpty && i < wDrain) ? 8 : 1);
         *err = 0;
         fence_mbar_init();
     }
@@ -86,8 +88,8 @@ __global__ void __launch_bounds__(kWalkThreadsTc, 1) walk_tc_kernel(const __grid
             prefetch_tensormap(mx);
             int n = 0;
             for (; n < NC; ++n) {
-                const int st = n % sw::kStages, row = u.row + chunk_at(n) * kQ;
-                if (n >= sw::kStages && !mbar_wait_or_abort(bars + wEmpty + st, ((n / sw::kStages) & 1) ^ 1, lim, err)) {
+                const int st = n & 1, row = u.row + chunk_at(n) * kQ;
+                if (n >= 2 && !mbar_wait_or_abort(bars + wEmpty + st, ((n >> 1) & 1) ^ 1, lim, err)) {
                     note_failure(err);
                     break;
                 }
@@ -95,37 +97,34 @@ __global__ void __launch_bounds__(kWalkThreadsTc, 1) walk_tc_kernel(const __grid
                 for (int k = 0; k < halves; ++k) tma_load_3d(sm + sw::K + (2 * st + k) * kTileBytes, mk, 64 * k, grp, row, bars + wFull + st);
                 tma_load_3d(sm + sw::X + st * kTileBytes, mx, p0, h, row, bars + wFull + st);
             }
-            for (int c = n > sw::kStages ? n - sw::kStages : 0; c < n; ++c)  // nothing in flight when the block ends
-                mbar_wait(bars + wFull + c % sw::kStages, (c / sw::kStages) & 1, kDefaultWaitNs);
+            for (int c = n > 2 ? n - 2 : 0; c < n; ++c)  // nothing in flight when the block ends
+                mbar_wait(bars + wFull + (c & 1), (c >> 1) & 1, kDefaultWaitNs);
         }
     } else if (warp == 1) {
         const uint32_t id_d = idesc_bf16(128, 64, true, true), lead = elect_one();
         const uint32_t dm = uniform(desc_lo(sb, kTileBytes));
         bool ok = true;
         for (int c = 0; c < NC; ++c) {
-            const int st = c % sw::kStages, set = c & 1;
+            const int st = c & 1;
             const uint32_t ph = (c >> 1) & 1;
-            if (!(ok = wait_bar(bars + wFull + st, (c / sw::kStages) & 1, lim, err) && wait_bar(bars + wReady + st, (c / sw::kStages) & 1, lim, err))) break;
-            if (c >= 2 && !(ok = wait_bar(bars + wDEmpty + set, ph ^ 1, lim, err))) break;
+            if (!(ok = wait_bar(bars + wFull + st, ph, lim, err) && wait_bar(bars + wXwReady + st, ph, lim, err))) break;
+            if (c >= 2 && !(ok = wait_bar(bars + wDEmpty + st, ph ^ 1, lim, err))) break;
+            tc_fence_after();
             const uint32_t km = dm + ((sw::K + 2 * st * kTileBytes) >> 4);
 #pragma unroll 1
             for (int k = 0; k < kParts; ++k) {
-                const int buf = set * kParts + k;
-                if (!(ok = wait_bar(bars + wXwReady + buf, ph, lim, err))) break;
-                tc_fence_after();
-                const uint32_t xa = dm + ((sw::XW + buf * kTileBytes) >> 4);
+                const uint32_t xa = dm + ((k ? sw::XW + (st * (kParts - 1) + k - 1) * kTileBytes : sw::X + st * kTileBytes) >> 4);
 #pragma unroll
-                for (int s = 0; s < 8; ++s) mma_by(lead, tmem + 64 * set, km + s * 128, xa + s * 128, id_d, k > 0 || s > 0);
-                commit_by(lead, bars + wXwFree + buf);
+                for (int s = 0; s < 8; ++s) mma_by(lead, tmem + 64 * st, km + s * 128, xa + s * 128, id_d, k > 0 || s > 0);
             }
-            if (!ok) break;
-            commit_by(lead, bars + wDFull + set);
+            commit_by(lead, bars + wDFull + st);
             commit_by(lead, bars + wEmpty + st);
         }
         commit_by(lead, bars + wDrain);
         mbar_wait(bars + wDrain, 0, kDefaultWaitNs);
-    } else if (warp == 2) {
-        // gates of the next chunk are in registers before this chunk's are due; four tokens per lane
+    } else if (warp < 4) {
+        // ---- gates, four tokens per lane. A head's values lie 2 H bytes apart and take 3500 cycles to arrive, about two
+        // chunks: two warps take the chunks in turn, each with its next chunk's values in flight.
         float gn[4], sn[4], total = 0.f;
         auto fetch = [&](int c) {
 #pragma unroll
@@ -136,10 +135,10 @@ __global__ void __launch_bounds__(kWalkThreadsTc, 1) walk_tc_kernel(const __grid
                 sn[e] = back ? 1.f : t < u.len ? __bfloat162float(a.step[at]) : 0.f;
             }
         };
-        if (NC > 0) fetch(0);
-        for (int c = 0; c < NC; ++c) {
-            const int st = c % sw::kStages;
-            if (!wait_bar(bars + wFull + st, (c / sw::kStages) & 1, lim, err)) break;
+        if (warp - 2 < NC) fetch(warp - 2);
+        for (int c = warp - 2; c < NC; c += 2) {
+            const int st = c & 1;
+            if (!wait_bar(bars + wFull + st, (c >> 1) & 1, lim, err)) break;
             // forward: the decay behind the token up to the chunk's end; backward: up to and with the token.
             // Sums from the nearer side, so that small values keep their digits behind strong decays.
             float p[4], acc;
@@ -177,9 +176,9 @@ __global__ void __launch_bounds__(kWalkThreadsTc, 1) walk_tc_kernel(const __grid
             }
             __syncwarp();
             if (lane == 0) mbar_arrive1(bars + wReady + st);
-            if (c + 1 < NC) fetch(c + 1);
+            if (c + 2 < NC) fetch(c + 2);
         }
-        if (a.increments && lane == 0 && pi == 0) job.decay[static_cast<size_t>(blockIdx.y) * a.H + h] = total * 0.69314718056f;
+        if (lane == 0) totals[warp - 2] = total;
     } else if (warp >= 4) {
         // X~ of the next chunk, then the state over this one: row r per thread, half of the 64 columns per four warps
         const int q = warp & 3, half = warp >= 8, r = 32 * q + lane;
@@ -203,73 +202,58 @@ __global__ void __launch_bounds__(kWalkThreadsTc, 1) walk_tc_kernel(const __grid
             save = static_cast<uint8_t*>(job.save) + ((first_chunk * a.H + h) * pb + pi) * tile;
         }
         const size_t save_step = static_cast<size_t>(a.H) * pb * tile;
-        const bool writer = tid == 4 * 32;
         float decay = 1.f;
         bool ok = true;
         for (int c = -1; c < NC; ++c) {
             const int n = c + 1;
             const float decay_c = decay;
-            if (ok && n < NC) {
-                const int st = n % sw::kStages, set = n & 1;
-                ok = wait_bar(bars + wFull + st, (n / sw::kStages) & 1, lim, err) && wait_bar(bars + wReady + st, (n / sw::kStages) & 1, lim, err);
-                if (ok && n >= 2) ok = wait_bar(bars + wXwFree + set * kParts + kParts - 1, ((n >> 1) & 1) ^ 1, lim, err);
-                if (ok) {
-                    const float* arr = reinterpret_cast<const float*>(sm + sw::GATE + st * sw::kGateStage);
-                    const float w = arr[r];
-                    decay = arr[128];
-                    const uint8_t* xt = sm + sw::X + st * kTileBytes + r * 128;
-                    uint8_t* to = sm + sw::XW + set * kParts * kTileBytes + r * 128;
+            if (n < NC) {
+                const int st = n & 1;
+                const uint32_t ph = (n >> 1) & 1;
+                if (!(ok = wait_bar(bars + wFull + st, ph, lim, err) && wait_bar(bars + wReady + st, ph, lim, err))) break;
+                const float* arr = reinterpret_cast<const float*>(sm + sw::GATE + st * sw::kGateStage);
+                const float w = arr[r];
+                decay = arr[128];
+                uint8_t* xt = sm + sw::X + st * kTileBytes + r * 128;
+                uint8_t* more = sm + sw::XW + st * (kParts - 1) * kTileBytes + r * 128;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int cell = ((4 * half + k) ^ (r & 7)) << 4;
-                        float v[8];
-                        unpack8(*reinterpret_cast<const uint4*>(xt + cell), v);
+                for (int k = 0; k < 4; ++k) {
+                    const int cell = ((4 * half + k) ^ (r & 7)) << 4;
+                    float v[8];
+                    unpack8(*reinterpret_cast<const uint4*>(xt + cell), v);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] *= w;
+                    for (int e = 0; e < 8; ++e) v[e] *= w;
 #pragma unroll
-                        for (int part = 0; part < kParts; ++part) {
-                            const uint4 o = pack8(v);
-                            *reinterpret_cast<uint4*>(to + part * kTileBytes + cell) = o;
-                            if (part + 1 < kParts) {
-                                float hi[8];
-                                unpack8(o, hi);
+                    for (int part = 0; part < kParts; ++part) {
+                        const uint4 o = pack8(v);
+                        *reinterpret_cast<uint4*>((part ? more + (part - 1) * kTileBytes : xt) + cell) = o;
+                        if (part + 1 < kParts) {
+                            float hi[8];
+                            unpack8(o, hi);
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) v[e] -= hi[e];
-                            }
+                            for (int e = 0; e < 8; ++e) v[e] -= hi[e];
                         }
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        for (int part = 0; part < kParts; ++part) mbar_arrive1(bars + wXwReady + set * kParts + part);
                 }
-            }
-            if (ok && c >= 0) {
-                const int set = c & 1;
-                if ((ok = wait_bar(bars + wDFull + set, (c >> 1) & 1, lim, err))) {
-                    tc_fence_after();
-                    float x[32];
-                    tmem_ld_cols<2>(tmem + lane_base + 64 * set + 32 * half, x);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) hx[k] = fmaf(decay_c, hx[k], x[k]);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive1(bars + wDEmpty + set);
-                }
-            }
-            if (save && n < NC) {  // every warp of the group comes here for every chunk, whatever happened
-                if (writer) bulk_wait_read_all();
-                state_warps_sync();
-                if (real) st_row_bf16x32(sm + sw::STG, r, 4 * half, hx);
                 fence_proxy_async_smem();
-                state_warps_sync();
-                if (writer && ok) {
-                    bulk_store(save + static_cast<size_t>(chunk_at(n)) * save_step, sm + sw::STG, tile);
-                    bulk_commit();
-                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(bars + wXwReady + st);
             }
+            if (c >= 0) {
+                const int set = c & 1;
+                if (!(ok = wait_bar(bars + wDFull + set, (c >> 1) & 1, lim, err))) break;
+                tc_fence_after();
+                float x[32];
+                tmem_ld_cols<2>(tmem + lane_base + 64 * set + 32 * half, x);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) hx[k] = fmaf(decay_c, hx[k], x[k]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(bars + wDEmpty + set);
+            }
+            if (save && n < NC && real)  // the 32-byte sectors of the operand layout are whole
+                st_row_bf16x32(save + static_cast<size_t>(chunk_at(n)) * save_step, r, 4 * half, hx);
         }
-        if (writer) bulk_wait_all();
         float* to = nullptr;
         if (ok && a.increments) to = job.states + unit_plane;
         else if (ok && job.last && u.k == (back ? 0 : u.count - 1)) to = job.last + seq_plane;
@@ -281,6 +265,7 @@ __global__ void __launch_bounds__(kWalkThreadsTc, 1) walk_tc_kernel(const __grid
     }
     tc_fence_before();
     __syncthreads();
+    if (a.increments && tid == 0 && pi == 0) job.decay[static_cast<size_t>(blockIdx.y) * a.H + h] = (totals[0] + totals[1]) * 0.69314718056f;
     if (warp == 0) tmem_dealloc(*tmem_slot, 128);
 }
 
@@ -306,10 +291,10 @@ cudaError_t launch_ssm_walk_tc(const ScanShape& sh, const void* step, const void
     a.g = static_cast<const __nv_bfloat16*>(g);
     a.wait_ns = wait_ns;
     auto* kernel = exact ? walk_tc_kernel<3> : walk_tc_kernel<1>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    const uint32_t smem = exact ? Sw<3>::kAlloc : Sw<1>::kAlloc;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    // the whole shared memory: no operand descriptor reaches past the block's own
-    kernel<<<dim3(sh.H * (sh.P / kCols), static_cast<unsigned>(sh.seqs.units(unit)), n_jobs), kWalkThreadsTc, 232448, s>>>(maps, a);
+    kernel<<<dim3(sh.H * (sh.P / kCols), static_cast<unsigned>(sh.seqs.units(unit)), n_jobs), kWalkThreadsTc, smem, s>>>(maps, a);
     return cudaGetLastError();
 }
 
