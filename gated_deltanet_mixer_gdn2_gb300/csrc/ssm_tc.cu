@@ -6,8 +6,8 @@
 // One block walks over the chunks of its unit for 64 value columns of one head; all five products run on
 // tcgen05 with their accumulators in tensor memory, and the state stays in registers in fp32. Only the
 // update of the state is serial from chunk to chunk (64 multiply-adds per thread), so the block is a
-// pipeline of warp roles over different chunks: copies (warps 0 and 3), products (warp 1), gates
-// (warp 2), M (warps 4-7), Y (warps 8-11), X~ and state (warps 12-15).
+// pipeline of warp roles over different chunks: copies (warp 0), products (warp 1), gates (warps 2 and 3), M (warps 4-7),
+// Y (warps 8-15), X~ and state (warps 16-23).
 #include "ssm_tc.cuh"
 
 namespace gdn2 {
@@ -33,12 +33,12 @@ struct So {
 };
 
 enum Bar {
-    kFullB = 0, kFullC = 2, kFullX = 4, kReady = 7, kBEmpty = 10, kCEmpty = 12, kXEmpty = 14, kSFull = 17, kXwReady = 19,
-    kXwFree = 22, kMReady = 25, kYFull, kYEmpty, kDFull, kDEmpty, kHReady, kHFree, kDrain, kBars
+    kFullB = 0, kFullC = 2, kFullX = 4, kReady = 7, kBEmpty = 10, kCEmpty = 12, kXEmpty = 14, kSFull = 17, kXwReady = 19, kMReady, kYFull,
+    kYEmpty, kDFull, kHReady, kHFree, kYOut, kDrain = kYOut + 4, kBars
 };
 constexpr uint32_t kBarBytes = 8 * kBars + 16;
 static_assert(kBarBytes <= 320, "barrier room");
-constexpr int kScanThreads = 640;
+constexpr int kScanThreads = 768;
 
 // tensor-memory columns: scores of two chunks, each half replaced by M (16 packed columns at the start of every
 // 32); Y's sum over the chunk, its readouts of the state of two chunks, the state's increment
@@ -114,9 +114,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
 
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) {
-            const bool four = (i >= kXEmpty && i < kXEmpty + 3) || i == kMReady || i == kYEmpty;
-            const bool eight = (i >= kXwReady && i < kXwReady + 3) || i == kDEmpty || i == kHReady;
-            mbar_init(bars + i, four ? 4 : eight ? 8 : 1);
+            const bool four = (i >= kXEmpty && i < kXEmpty + 3) || i == kMReady;
+            const bool eight = i == kXwReady || i == kHReady || i == kYEmpty;
+            mbar_init(bars + i, four ? 4 : eight ? 8 : i >= kYOut && i < kDrain ? 2 : 1);
         }
         *err = 0;
         fence_mbar_init();
@@ -132,45 +132,61 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     const int ks = a.N / 16;  // K steps over the state size
     const size_t plane = static_cast<size_t>(a.N) * a.P;
 
-    if (warp == 0 || warp == 3) {
-        // copies: B and C (warp 0) are free again earlier than X, whose room Y leaves through (warp 3)
+    if (warp == 0) {
         if (lane == 0) {
-            const bool bc = warp == 0;
+            // ---- copies: each kind of tile as soon as its stage is free, whichever that is
             const int halves = a.N / 64;
-            prefetch_tensormap(bc ? &maps.b : &maps.x);
-            if (bc) prefetch_tensormap(&maps.c);
+            prefetch_tensormap(&maps.b);
+            prefetch_tensormap(&maps.c);
+            prefetch_tensormap(&maps.x);
+            int nb = 0, nc = 0, nx = 0;
+            uint64_t t0 = globaltimer_ns();
+            auto free_of = [&](int n, int stages, int empty) {
+                return n < NC && (n < stages || mbar_test_wait(bars + empty + n % stages, ((n / stages) & 1) ^ 1));
+            };
+            while (nb < NC || nc < NC || nx < NC) {
+                bool any = false;
+                if (free_of(nb, 2, kBEmpty)) {
+                    const int st = nb & 1;
+                    mbar_arrive_expect_tx(bars + kFullB + st, so::kTile * halves);
+                    for (int k = 0; k < halves; ++k)
+                        tma_load_3d(sm + so::B + (2 * st + k) * so::kTile, &maps.b, 64 * k, grp, u.row + nb * kQ, bars + kFullB + st);
+                    ++nb;
+                    any = true;
+                }
+                if (free_of(nc, so::kCS, kCEmpty)) {
+                    const int st = nc % so::kCS;
+                    mbar_arrive_expect_tx(bars + kFullC + st, so::kTile * halves);
+                    for (int k = 0; k < halves; ++k)
+                        tma_load_3d(sm + so::C + (2 * st + k) * so::kTile, &maps.c, 64 * k, grp, u.row + nc * kQ, bars + kFullC + st);
+                    ++nc;
+                    any = true;
+                }
+                if (free_of(nx, so::kXS, kXEmpty)) {
+                    const int st = nx % so::kXS;
+                    mbar_arrive_expect_tx(bars + kFullX + st, so::kTile);
+                    tma_load_3d(sm + so::X + st * so::kTile, &maps.x, p0, h, u.row + nx * kQ, bars + kFullX + st);
+                    ++nx;
+                    any = true;
+                }
+                if (any) {
+                    t0 = globaltimer_ns();
+                } else {
+                    if (*err) break;
+                    if (lim <= 0 || (long long)(globaltimer_ns() - t0) > lim) {
+                        note_failure(err);
+                        break;
+                    }
+                    __nanosleep(64);
+                }
+            }
             auto drain = [&](int issued, int full, int stages) {  // nothing in flight when the block ends
                 for (int c = issued > stages ? issued - stages : 0; c < issued; ++c)
                     mbar_wait(bars + full + c % stages, (c / stages) & 1, kDefaultWaitNs);
             };
-            int n0 = 0, n1 = 0;
-            if (bc) {
-                // tiles of one or two halves lie two tiles apart
-                for (int c = 0; c < NC; ++c, ++n1) {
-                    const int st = c & 1, sc = c % so::kCS;
-                    if (c >= 2 && !mbar_wait_or_abort(bars + kBEmpty + st, ((c >> 1) & 1) ^ 1, lim, err)) break;
-                    mbar_arrive_expect_tx(bars + kFullB + st, so::kTile * halves);
-                    for (int k = 0; k < halves; ++k)
-                        tma_load_3d(sm + so::B + (2 * st + k) * so::kTile, &maps.b, 64 * k, grp, u.row + c * kQ, bars + kFullB + st);
-                    ++n0;
-                    if (c >= so::kCS && !mbar_wait_or_abort(bars + kCEmpty + sc, ((c / so::kCS) & 1) ^ 1, lim, err)) break;
-                    mbar_arrive_expect_tx(bars + kFullC + sc, so::kTile * halves);
-                    for (int k = 0; k < halves; ++k)
-                        tma_load_3d(sm + so::C + (2 * sc + k) * so::kTile, &maps.c, 64 * k, grp, u.row + c * kQ, bars + kFullC + sc);
-                }
-                if (n1 < NC) note_failure(err);
-                drain(n0, kFullB, 2);
-                drain(n1, kFullC, so::kCS);
-            } else {
-                for (int c = 0; c < NC; ++c, ++n0) {
-                    const int xs = c % so::kXS;
-                    if (c >= so::kXS && !mbar_wait_or_abort(bars + kXEmpty + xs, ((c / so::kXS) & 1) ^ 1, lim, err)) break;
-                    mbar_arrive_expect_tx(bars + kFullX + xs, so::kTile);
-                    tma_load_3d(sm + so::X + xs * so::kTile, &maps.x, p0, h, u.row + c * kQ, bars + kFullX + xs);
-                }
-                if (n0 < NC) note_failure(err);
-                drain(n0, kFullX, so::kXS);
-            }
+            drain(nb, kFullB, 2);
+            drain(nc, kFullC, so::kCS);
+            drain(nx, kFullX, so::kXS);
         }
     } else if (warp == 1) {
         const uint32_t id_s = idesc_bf16(128, 128, false, false), id_d = idesc_bf16(128, 64, true, true),
@@ -184,66 +200,52 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             tc_fence_after();
             return w;
         };
+        // Every wait costs this warp about a hundred cycles in which the tensor core runs dry, so each is for the last of
+        // what it stands for: X~ ready implies X loaded and a short chunk's rows cleared; the state ready, the increment
+        // before it taken; Y's sums taken, that chunk's products done.
         bool ok = true;
         for (int c = -1; c < NC && NC > 0; ++c) {
             const uint32_t ph1 = c & 1;  // phase of the barriers used once per chunk
             if (c >= 0) {
-                // state increment
-                const uint32_t bm = dm + ((so::B + 2 * (c & 1) * so::kTile) >> 4);
-                if (c >= 1 && !(ok = wait(kDEmpty, ph1 ^ 1))) break;
-#pragma unroll 1
-                for (int k = 0; k < kParts; ++k) {
-                    if (!(ok = wait(kXwReady + k, ph1))) break;
-                    const uint32_t xa = dm + ((so::XW + k * so::kTile) >> 4);
-#pragma unroll
-                    for (int s = 0; s < 8; ++s) mma_by(lead, kTD, bm + s * 128, xa + s * 128, id_d, k > 0 || s > 0);
-                    commit_by(lead, bars + kXwFree + k);
-                }
-                if (!ok) break;
-                commit_by(lead, bars + kDFull);
-                commit_by(lead, bars + kBEmpty + (c & 1));
                 // readout of the state
                 if (!(ok = wait(kHReady, ph1))) break;
-                const uint32_t ck = dk + ((so::C + 2 * (c % so::kCS) * so::kTile) >> 4), hb = dm + (so::HB >> 4);
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    if (s < ks) mma_by(lead, kTYx + 64 * (c & 1), ck + (((s >> 2) * so::kTile + (s & 3) * 32) >> 4), hb + s * 128, id_x, s > 0);
+                mma_steps<false>(lead, kTYx + 64 * (c & 1), dk + ((so::C + 2 * (c % so::kCS) * so::kTile) >> 4), dm + (so::HB >> 4), id_x, 0, ks / 4, 4,
+                                 kStepK, kStepMn, kJumpK, 0);
                 commit_by(lead, bars + kCEmpty + c % so::kCS);
                 commit_by(lead, bars + kHFree);
+                // state increment
+                if (!(ok = wait(kXwReady, ph1))) break;
+#pragma unroll 1
+                for (int k = 0; k < kParts; ++k)
+                    mma_steps<false>(lead, kTD, dm + ((so::B + 2 * (c & 1) * so::kTile) >> 4), dm + ((so::XW + k * so::kTile) >> 4), id_d, k > 0, 1, 8,
+                                     kStepMn, kStepMn, 0, 0);
+                commit_by(lead, bars + kDFull);
+                commit_by(lead, bars + kBEmpty + (c & 1));
             }
             // The next chunk's scores go in here: their tiles were asked for when the chunk before this one was
             // read out, and M of the next chunk can start while this one's is still used.
             const int n = c + 1, st = n & 1;
+            if (c >= 1 && !(ok = wait(kYEmpty, ph1 ^ 1))) break;
             if (n < NC) {
                 if (!(ok = wait(kFullB + st, (n >> 1) & 1) && wait(kFullC + n % so::kCS, (n / so::kCS) & 1))) break;
                 // a short chunk's rows of B are cleared first
                 if (u.len - n * kQ < kQ && !(ok = wait(kReady + n % so::kXS, (n / so::kXS) & 1))) break;
-                // M of two chunks before, in the same columns, has been used
-                if (n >= 2 && !(ok = wait(kYFull, n & 1))) break;
-                const uint32_t ca = dk + ((so::C + 2 * (n % so::kCS) * so::kTile) >> 4), ba = dk + ((so::B + 2 * st * so::kTile) >> 4);
-#pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    const uint32_t off = ((s >> 2) * so::kTile + (s & 3) * 32) >> 4;
-                    if (s < ks) mma_by(lead, kTS + 128 * st, ca + off, ba + off, id_s, s > 0);
-                }
+                mma_steps<false>(lead, kTS + 128 * st, dk + ((so::C + 2 * (n % so::kCS) * so::kTile) >> 4), dk + ((so::B + 2 * st * so::kTile) >> 4), id_s, 0,
+                                 ks / 4, 4, kStepK, kStepK, kJumpK, kJumpK);
                 commit_by(lead, bars + kSFull + st);
             }
             // within the chunk
             if (c >= 0) {
-                const int xs = c % so::kXS;
-                if (!(ok = wait(kFullX + xs, (c / so::kXS) & 1) && wait(kReady + xs, (c / so::kXS) & 1) && wait(kMReady, ph1))) break;
-                if (c >= 1 && !(ok = wait(kYEmpty, ph1 ^ 1))) break;
-                const uint32_t xm = dm + ((so::X + xs * so::kTile) >> 4);
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    mma_ts_by(lead, kTYi, kTS + 128 * (c & 1) + 32 * (s >> 1) + 8 * (s & 1), xm + s * 128, id_x, s > 0);
+                if (!(ok = wait(kMReady, ph1))) break;
+                mma_steps<true>(lead, kTYi, kTS + 128 * (c & 1), dm + ((so::X + (c % so::kXS) * so::kTile) >> 4), id_x, 0, 4, 2, 8, kStepMn, 16, 0);
                 commit_by(lead, bars + kYFull);
             }
         }
         commit_by(lead, bars + kDrain);
         mbar_wait(bars + kDrain, 0, kDefaultWaitNs);
-    } else if (warp == 2) {
-        // gates of the next chunk are in registers before this chunk's are due
+    } else if (warp < 4) {
+        // ---- gates. A head's values lie 2 H bytes apart and take up to 3500 cycles to arrive, about two chunks: two warps
+        // take the chunks in turn, each with its next chunk's values in flight.
         float gn[4], sn[4];
         auto fetch = [&](int c) {
 #pragma unroll
@@ -254,15 +256,15 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 sn[e] = t < u.len ? __bfloat162float(a.step[at]) : 0.f;
             }
         };
-        if (NC > 0) fetch(0);
-        for (int c = 0; c < NC; ++c) {
+        if (warp - 2 < NC) fetch(warp - 2);
+        for (int c = warp - 2; c < NC; c += 2) {
             const int st = c & 1, xs = c % so::kXS;
-            // X's arrival says that the arrays of its stage have been read (Y, the last reader, frees both)
-            if (!wait_bar(bars + kFullX + xs, (c / so::kXS) & 1, lim, err)) break;
+            // the arrays of the stage have been read: Y, the last reader, frees them with X
+            if (c >= so::kXS && !wait_bar(bars + kXEmpty + xs, ((c / so::kXS) & 1) ^ 1, lim, err)) break;
             gate_arrays(reinterpret_cast<float*>(sm + so::GATE + xs * so::kGateStage), lane, gn, sn);
             const int n = u.len - c * kQ;
             if (n < kQ) {
-                if (!wait_bar(bars + kFullB + st, (c >> 1) & 1, lim, err)) break;
+                if (!wait_bar(bars + kFullB + st, (c >> 1) & 1, lim, err) || !wait_bar(bars + kFullX + xs, (c / so::kXS) & 1, lim, err)) break;
                 // the rows past the sequence hold other tokens: zeros, so that not even their NaN enters a sum
                 const uint4 z = make_uint4(0, 0, 0, 0);
                 for (int i = n * 8 + lane; i < kQ * 8; i += 32) {
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             }
             __syncwarp();
             if (lane == 0) mbar_arrive1(bars + kReady + xs);
-            if (c + 1 < NC) fetch(c + 1);
+            if (c + 2 < NC) fetch(c + 2);
         }
     } else if (warp >= 4 && warp < 8) {
         // ---- M: row i of the chunk per thread, in place of the scores; blocks of 32 columns. Below the diagonal
@@ -338,63 +340,66 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             __syncwarp();
             if (lane == 0) mbar_arrive1(bars + kMReady);
         }
-    } else if (warp >= 8 && warp < 12) {
-        // ---- Y: row i of the chunk per thread, all 64 columns; replaces the row of X and leaves by a bulk store
-        const int q = warp & 3, i = 32 * q + lane;
-        const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
+    } else if (warp >= 8 && warp < 16) {
+        // ---- Y: row i of the chunk and half of the 64 columns per thread; replaces that part of X, and the two warps of
+        // 32 rows leave by one bulk store. Both sums are taken out of tensor memory before anything else, for the next
+        // chunk's products wait for their room.
+        const int q = warp & 3, half = warp >= 12, i = 32 * q + lane;
+        const uint32_t lane_base = (static_cast<uint32_t>(32 * q) << 16) + 32 * half;
         const float dk = a.d ? a.d[h] : 0.f;
         for (int c = 0; c < NC; ++c) {
             const int xs = c % so::kXS;
-            if (!wait_bar(bars + kFullX + xs, (c / so::kXS) & 1, lim, err)) break;
-            if (!wait_bar(bars + kReady + xs, (c / so::kXS) & 1, lim, err)) break;
-            if (!wait_bar(bars + kYFull, c & 1, lim, err)) break;
-            tc_fence_after();
+            const uint32_t xph = (c / so::kXS) & 1;
+            if (!wait_bar(bars + kFullX + xs, xph, lim, err) || !wait_bar(bars + kReady + xs, xph, lim, err)) break;
             const float eL = ex2_approx(reinterpret_cast<const float*>(sm + so::GATE + xs * so::kGateStage)[i]);
             uint8_t* xt = sm + so::X + xs * so::kTile;
             const int n = u.len - c * kQ;
-            __nv_bfloat16* yrow = a.y + (static_cast<size_t>(u.row + c * kQ + i) * a.H + h) * a.P + p0;
-#pragma unroll 1
-            for (int part = 0; part < 2; ++part) {
-                uint32_t yi[2][16], yx[2][16];
+            if (!wait_bar(bars + kYFull, c & 1, lim, err)) break;
+            tc_fence_after();
+            uint32_t yi[2][16], yx[2][16];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    tmem_ld16(tmem + lane_base + kTYi + 32 * part + 16 * k, yi[k]);
-                    tmem_ld16(tmem + lane_base + kTYx + 64 * (c & 1) + 32 * part + 16 * k, yx[k]);
-                }
-                tmem_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint4* cell = reinterpret_cast<uint4*>(xt + i * 128 + (((4 * part + k) ^ (i & 7)) << 4));
-                    float xv[8], out[8];
-                    unpack8(*cell, xv);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        out[e] = fmaf(dk, xv[e], fmaf(eL, __uint_as_float(yx[k >> 1][8 * (k & 1) + e]), __uint_as_float(yi[k >> 1][8 * (k & 1) + e])));
-                    const uint4 o = pack8(out);
-                    if (n >= kQ) *cell = o;
-                    else if (i < n) reinterpret_cast<uint4*>(yrow)[4 * part + k] = o;
-                }
+            for (int k = 0; k < 2; ++k) {
+                tmem_ld16(lane_base + kTYi + 16 * k, yi[k]);
+                tmem_ld16(lane_base + kTYx + 64 * (c & 1) + 16 * k, yx[k]);
             }
+            tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive1(bars + kYEmpty);
-            if (n >= kQ) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    tma_store_3d(&maps.y, xt + 4096 * q, p0, h, u.row + c * kQ + 32 * q);
-                    bulk_commit();
-                    bulk_wait_read_all();
-                }
+            uint4* yrow = reinterpret_cast<uint4*>(a.y + (static_cast<size_t>(u.row + c * kQ + i) * a.H + h) * a.P + p0 + 32 * half);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint4* cell = reinterpret_cast<uint4*>(xt + i * 128 + (((4 * half + k) ^ (i & 7)) << 4));
+                float xv[8], out[8];
+                unpack8(*cell, xv);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    out[e] = fmaf(dk, xv[e], fmaf(eL, __uint_as_float(yx[k >> 1][8 * (k & 1) + e]), __uint_as_float(yi[k >> 1][8 * (k & 1) + e])));
+                const uint4 o = pack8(out);
+                if (n >= kQ) *cell = o;
+                else if (i < n) yrow[k] = o;
             }
+            fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive1(bars + kXEmpty + xs);
+            if (lane == 0) mbar_arrive1(bars + kYOut + q);
+            if (half == 0) {
+                if (!wait_bar(bars + kYOut + q, c & 1, lim, err)) break;
+                if (lane == 0) {
+                    if (n >= kQ) {
+                        tma_store_3d(&maps.y, xt + 4096 * q, p0, h, u.row + c * kQ + 32 * q);
+                        bulk_commit();
+                        bulk_wait_read_all();
+                    }
+                    mbar_arrive1(bars + kXEmpty + xs);
+                }
+                __syncwarp();
+            }
         }
         if (lane == 0) bulk_wait_all();
-    } else if (warp >= 12) {
+    } else {
         // ---- X~ of the next chunk, then the state over this one: row n of the state (token of X~) per thread, half
         // of the 64 columns per group of four warps
-        const int q = warp & 3, half = warp >= 16, r = 32 * q + lane;
+        const int q = warp & 3, half = warp >= 20, r = 32 * q + lane;
         const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
         const bool real = r < a.N;
         const size_t at = static_cast<size_t>(real ? r : 0) * a.P + p0 + 32 * half;
@@ -412,15 +417,28 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         bool ok = true;
         for (int c = -1; c < NC; ++c) {
             const int n = c + 1;
-            const float decay_c = decay;
+            if (c >= 0) {
+                if (!(ok = wait_bar(bars + kDFull, c & 1, lim, err))) break;
+                tc_fence_after();
+                float x[32];
+                tmem_ld_cols<2>(tmem + lane_base + kTD + 32 * half, x);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) hx[k] = fmaf(decay, hx[k], x[k]);
+                tc_fence_before();
+            }
             if (n < NC) {
-                // X~ of chunk n, row r: each part is the bf16 rounding of what the parts before it leave
+                if (c >= 0 && !(ok = wait_bar(bars + kHFree, c & 1, lim, err))) break;
+                st_row_bf16x32(sm + so::HB, r, 4 * half, hx);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(bars + kHReady);
+                // X~ of chunk n, row r, once the increment before it has been formed from the last: each part is the bf16
+                // rounding of what the parts before it leave
                 const int xs = n % so::kXS;
                 if (!(ok = wait_bar(bars + kFullX + xs, (n / so::kXS) & 1, lim, err) && wait_bar(bars + kReady + xs, (n / so::kXS) & 1, lim, err))) break;
                 const float* arr = reinterpret_cast<const float*>(sm + so::GATE + xs * so::kGateStage);
                 const float w = arr[256 + r];
                 decay = ex2_approx(arr[127]);
-                if (n >= 1 && !(ok = wait_bar(bars + kXwFree + kParts - 1, (n & 1) ^ 1, lim, err))) break;  // the last part's product follows the others'
                 const uint8_t* xt = sm + so::X + xs * so::kTile + r * 128;
                 uint8_t* to = sm + so::XW + r * 128;
 #pragma unroll
@@ -444,26 +462,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0)
-                    for (int part = 0; part < kParts; ++part) mbar_arrive1(bars + kXwReady + part);
-            }
-            if (c >= 0) {
-                if (!(ok = wait_bar(bars + kDFull, c & 1, lim, err))) break;
-                tc_fence_after();
-                float x[32];
-                tmem_ld_cols<2>(tmem + lane_base + kTD + 32 * half, x);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) hx[k] = fmaf(decay_c, hx[k], x[k]);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive1(bars + kDEmpty);
-            }
-            if (n < NC) {
-                if (c >= 0 && !(ok = wait_bar(bars + kHFree, c & 1, lim, err))) break;
-                st_row_bf16x32(sm + so::HB, r, 4 * half, hx);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive1(bars + kHReady);
+                if (lane == 0) mbar_arrive1(bars + kXwReady);
             }
         }
         if (ok && a.s1 && u.k == u.count - 1 && real) {
@@ -493,9 +492,28 @@ bool ssm_tc_shape(const ScanShape& sh) {
     return sh.dt == GDN2_BF16 && sh.P % 64 == 0 && (sh.N == 64 || sh.N == 128) && sh.seqs.units(kQ) <= 65535;
 }
 
-size_t ssm_tc_fwd_workspace(const ScanShape&) { return 0; }
+namespace {
+int fwd_unit(const ScanShape& sh) {
+    int dev = 0, sms = 152;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) sms = 152;
+    const int whole = (sh.seqs.T + kQ - 1) / kQ * kQ;
+    const long long chains = static_cast<long long>(sh.H) * (sh.P / kCols), chunks = (sh.seqs.rows() + kQ - 1) / kQ;
+    if (10 * chains * sh.seqs.B >= 8 * sms) return whole;
+    // about six blocks per SM, of 1024 tokens or more
+    long long len = (chains * chunks + 6LL * sms - 1) / (6LL * sms) * kQ;
+    if (len < 1024) len = 1024;
+    return 2 * len > whole ? whole : static_cast<int>(len);
+}
+}  // namespace
 
-cudaError_t launch_ssm_tc_fwd(const ScanShape& sh, const ScanIn& in, void* y, float* s1, void*, cudaStream_t s, long long wait_ns) {
+// States and decays of the units, when sequences are cut.
+size_t ssm_tc_fwd_workspace(const ScanShape& sh) {
+    const int unit = fwd_unit(sh);
+    if (unit >= sh.seqs.T) return 0;
+    return align_up(sizeof(float) * static_cast<size_t>(sh.seqs.units(unit)) * sh.H * (static_cast<size_t>(sh.N) * sh.P + 4), 256);
+}
+
+cudaError_t launch_ssm_tc_fwd(const ScanShape& sh, const ScanIn& in, void* y, float* s1, void* ws, cudaStream_t s, long long wait_ns) {
     ScanMaps maps;
     const long long rows = sh.seqs.rows();
     if (!rows_map(&maps.x, in.x.p, in.x.ld, sh.P, sh.H, rows, kQ) || !rows_map(&maps.b, in.bm.p, in.bm.ld, sh.N, sh.G, rows, kQ) ||
@@ -503,17 +521,27 @@ cudaError_t launch_ssm_tc_fwd(const ScanShape& sh, const ScanIn& in, void* y, fl
         return cudaErrorInvalidValue;
     ScanTcArgs a{};
     a.seqs = sh.seqs;
-    a.unit = (sh.seqs.T + kQ - 1) / kQ * kQ;
+    a.unit = fwd_unit(sh);
+    a.cut = a.unit < sh.seqs.T;
     a.step = static_cast<const __nv_bfloat16*>(in.step);
     a.g = static_cast<const __nv_bfloat16*>(in.g);
     a.d = in.d;
     a.s0 = in.s0;
-    a.s1 = s1;
+    a.s1 = a.cut ? nullptr : s1;
     a.y = static_cast<__nv_bfloat16*>(y);
     a.H = sh.H; a.G = sh.G; a.P = sh.P; a.N = sh.N;
     a.wait_ns = wait_ns;
     const dim3 grid(sh.H * (sh.P / kCols), static_cast<unsigned>(sh.seqs.units(a.unit)));
-    return s1 ? launch_scan<3>(maps, a, grid, s) : launch_scan<1>(maps, a, grid, s);
+    if (a.cut) {
+        // the units' increments, exact where the last state is a result, and their starting states
+        a.states = static_cast<float*>(ws);
+        a.decay = a.states + static_cast<size_t>(sh.seqs.units(a.unit)) * sh.H * sh.N * sh.P;
+        const WalkJob job{in.bm, in.x, in.s0, nullptr, a.states, a.decay, nullptr, 0};
+        cudaError_t e = launch_ssm_walk_tc(sh, in.step, in.g, &job, 1, a.unit, 1, 0, s1 != nullptr, s, wait_ns);
+        if (e != cudaSuccess) return e;
+        if ((e = launch_ssm_chain(sh, a.unit, in.s0, s1, a.states, a.decay, 0, s)) != cudaSuccess) return e;
+    }
+    return a.s1 ? launch_scan<3>(maps, a, grid, s) : launch_scan<1>(maps, a, grid, s);
 }
 
 int ssm_tc_read_clear_status(cudaStream_t s) { return read_clear_status(s); }

@@ -53,6 +53,30 @@ __device__ __forceinline__ void mma_ts_by(uint32_t lead, uint32_t d, uint32_t at
         "r"(kDescHi)
         : "memory");
 }
+// A product over `outer` x `inner` steps of 16 along K, the operands' start advancing by a step and, after each `inner`
+// steps, by a jump. Rolled: unrolled, the issuing warp ran through kilobytes of code once per chunk and waited for
+// instructions two thirds of the time (140 cycles per step, where the tensor core takes 32 to 64).
+template <bool kFromTmem>
+__device__ __forceinline__ void mma_steps(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc, int outer, int inner,
+                                          uint32_t da, uint32_t db, uint32_t ja, uint32_t jb) {
+#pragma unroll 1
+    for (int o = 0; o < outer; ++o) {
+#pragma unroll 1
+        for (int i = 0; i < inner; ++i) {
+            if (kFromTmem) mma_ts_by(lead, d, a, b, id, acc);
+            else mma_by(lead, d, a, b, id, acc);
+            acc = 1;
+            a += da;
+            b += db;
+        }
+        a += ja;
+        b += jb;
+    }
+}
+// Operand advances in descriptor units (16 bytes): K-major tiles hold 64 channels in 128-byte rows (32 bytes a step, the
+// next tile after four); MN-major ones a token or state row per 128 bytes (16 rows a step).
+constexpr uint32_t kStepK = 2, kJumpK = (kTileBytes >> 4) - 8, kStepMn = 128;
+
 __device__ __forceinline__ void commit_by(uint32_t lead, uint64_t* bar) {
     asm volatile(
         "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"

@@ -466,12 +466,9 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
             tc_fence_after();
             return w;
         };
-        constexpr uint32_t kT = kTileBytes >> 4;
         bool ok = wait(gBc, 0) && (!tail || wait(gGate, 0));
         if (ok) {
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-                if (s < ks) mma_by(lead, kTR, dk + (sg::B >> 4) + (s >> 2) * kT + (s & 3) * 2, dk + (sg::C >> 4) + (s >> 2) * kT + (s & 3) * 2, id_kk, s > 0);
+            mma_steps<false>(lead, kTR, dk + (sg::B >> 4), dk + (sg::C >> 4), id_kk, 0, ks / 4, 4, kStepK, kStepK, kJumpK, kJumpK);
             commit_by(lead, bars + gS);
         }
         for (int it = 0; ok && it < NI; ++it) {
@@ -479,33 +476,23 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
             const uint32_t ph = (it >> 1) & 1, ph1 = it & 1;
             const uint32_t xo = (sg::X + st * kTileBytes) >> 4, yo = (sg::DY + st * kTileBytes) >> 4;
             if (!(ok = wait(gXy + st, ph) && (!tail || wait(gGate + st, ph)) && (it ? wait(gAll, ph1 ^ 1) : wait(gSRead, 0)))) break;
-#pragma unroll
-            for (int s = 0; s < 4; ++s) mma_by(lead, kTR, dk + xo + s * 2, dk + yo + s * 2, id_kk, s > 0);  // R^T = X dY^T
+            mma_steps<false>(lead, kTR, dk + xo, dk + yo, id_kk, 0, 1, 4, kStepK, kStepK, 0, 0);  // R^T = X dY^T
             commit_by(lead, bars + gR);
             if (!(ok = wait(gHd, ph1) && (it == 0 || wait(gURead, ph1 ^ 1)))) break;
-#pragma unroll
-            for (int s = 0; s < 8; ++s)  // C H and B A
-                if (s < ks) mma_by(lead, kTT, dk + (sg::C >> 4) + (s >> 2) * kT + (s & 3) * 2, dm + (sg::H0 >> 4) + s * 128, id_t, s > 0);
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-                if (s < ks) mma_by(lead, kTU, dk + (sg::B >> 4) + (s >> 2) * kT + (s & 3) * 2, dm + (sg::DH >> 4) + s * 128, id_t, s > 0);
+            // C H and B A
+            mma_steps<false>(lead, kTT, dk + (sg::C >> 4), dm + (sg::H0 >> 4), id_t, 0, ks / 4, 4, kStepK, kStepMn, kJumpK, 0);
+            mma_steps<false>(lead, kTU, dk + (sg::B >> 4), dm + (sg::DH >> 4), id_t, 0, ks / 4, 4, kStepK, kStepMn, kJumpK, 0);
             commit_by(lead, bars + gTu);
             if (!(ok = wait(gPReady, ph1))) break;
-#pragma unroll
-            for (int s = 0; s < 8; ++s)  // dB += (R W s)^T C + X~ A^T
-                mma_ts_by(lead, kTdB, kTR + 16 * s, dm + (sg::C >> 4) + s * 128, id_nm, it > 0 || s > 0);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) mma_by(lead, kTdB, dk + xo + s * 2, dk + (sg::DH >> 4) + s * 2, id_nk, 1);
+            // dB += (R W s)^T C + X~ A^T
+            mma_steps<true>(lead, kTdB, kTR, dm + (sg::C >> 4), id_nm, it > 0, 1, 8, 16, kStepMn, 0, 0);
+            mma_steps<false>(lead, kTdB, dk + xo, dk + (sg::DH >> 4), id_nk, 1, 1, 4, kStepK, kStepK, 0, 0);
             if (!(ok = wait(gUScaled, ph1))) break;
-#pragma unroll
-            for (int s = 0; s < 8; ++s)  // U += (S W)^T dY
-                mma_ts_by(lead, kTU, kTR + 16 * s + 8, dm + yo + s * 128, id_t, 1);
+            mma_steps<true>(lead, kTU, kTR + 8, dm + yo, id_t, 1, 1, 8, 16, kStepMn, 0, 0);  // U += (S W)^T dY
             commit_by(lead, bars + gDx);
-#pragma unroll
-            for (int s = 0; s < 8; ++s)  // dC += (R W s) B + (e^L dY) H^T
-                mma_by(lead, kTdC, dm + (sg::P1 >> 4) + s * 128, dm + (sg::B >> 4) + s * 128, id_mm, it > 0 || s > 0);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) mma_by(lead, kTdC, dk + (sg::DYW >> 4) + s * 2, dk + (sg::H0 >> 4) + s * 2, id_nk, 1);
+            // dC += (R W s) B + (e^L dY) H^T
+            mma_steps<false>(lead, kTdC, dm + (sg::P1 >> 4), dm + (sg::B >> 4), id_mm, it > 0, 1, 8, kStepMn, kStepMn, 0, 0);
+            mma_steps<false>(lead, kTdC, dk + (sg::DYW >> 4), dk + (sg::H0 >> 4), id_nk, 1, 1, 4, kStepK, kStepK, 0, 0);
             commit_by(lead, bars + gAll);
             commit_by(lead, bars + gXyDone + st);
             commit_by(lead, bars + gHdFree);
