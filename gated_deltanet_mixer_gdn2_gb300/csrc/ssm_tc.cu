@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + so::BAR);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + so::BAR + kBars * 8);
     volatile int* err = reinterpret_cast<volatile int*>(sm + so::BAR + kBars * 8 + 8);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int pb = a.P / kCols, h = blockIdx.x / pb, p0 = (blockIdx.x - h * pb) * kCols, grp = h / (a.H / a.G);
     Unit u;
     if (!find_unit(a.seqs, a.unit, blockIdx.y, u)) return;
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         const uint32_t lead = elect_one();
         // K-major tiles: 16 channels are 32 bytes of a row, the next 64 the next tile. MN-major: 16 tokens (or
         // state rows) are 16 rows of 128 bytes.
-        const uint32_t dk = uniform(desc_lo(sb, 16)), dm = uniform(desc_lo(sb, so::kTile));
+        const uint32_t dk = desc_lo(sb, 16), dm = desc_lo(sb, so::kTile);
         auto wait = [&](int bar, uint32_t parity) {
             const bool w = wait_bar(bars + bar, parity, lim, err);
             tc_fence_after();

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + sg::BAR);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + sg::BAR + gBars * 8);
     volatile int* err = reinterpret_cast<volatile int*>(sm + sg::BAR + gBars * 8 + 8);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int grp = blockIdx.x / a.splits, split = blockIdx.x - grp * a.splits, per = a.H / a.G;
     const int h_lo = grp * per + split * a.heads, h_hi = min(h_lo + a.heads, (grp + 1) * per);
     const int pbs = a.P / kCols, NI = uniform((h_hi - h_lo) * pbs);
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
     } else if (warp == 16) {
         // ---- products
         const uint32_t lead = elect_one();
-        const uint32_t dk = uniform(desc_lo(sb, 16)), dm = uniform(desc_lo(sb, kTileBytes));
+        const uint32_t dk = desc_lo(sb, 16), dm = desc_lo(sb, kTileBytes);
         const uint32_t id_kk = idesc_bf16(128, 128, false, false), id_t = idesc_bf16(128, 64, false, true);
         const uint32_t id_nk = idesc_bf16(128, a.N, false, false), id_nm = idesc_bf16(128, a.N, false, true), id_mm = idesc_bf16(128, a.N, true, true);
         const int ks = a.N / 16;

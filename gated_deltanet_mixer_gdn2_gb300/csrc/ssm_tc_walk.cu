@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kWalkThreadsTc, Sw<kParts>::kPerSm) walk_tc_ke
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + sw::BAR + wBars * 8);
     volatile int* err = reinterpret_cast<volatile int*>(sm + sw::BAR + wBars * 8 + 8);
     __shared__ float totals[2];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const WalkJob& job = a.job[blockIdx.z];
     const bool back = job.back != 0;
     const int pb = a.P / kCols, h = blockIdx.x / pb, pi = blockIdx.x - h * pb, p0 = pi * kCols, grp = h / (a.H / a.G);
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kWalkThreadsTc, Sw<kParts>::kPerSm) walk_tc_ke
         }
     } else if (warp == 1) {
         const uint32_t id_d = idesc_bf16(128, 64, true, true), lead = elect_one();
-        const uint32_t dm = uniform(desc_lo(sb, kTileBytes));
+        const uint32_t dm = desc_lo(sb, kTileBytes);
         bool ok = true;
         for (int c = 0; c < NC; ++c) {
             const int st = c & 1;
