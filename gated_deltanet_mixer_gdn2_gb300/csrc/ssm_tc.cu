@@ -33,15 +33,15 @@ struct So {
 };
 
 enum Bar {
-    kFullB = 0, kFullC = 2, kFullX = 4, kReady = 7, kBEmpty = 10, kCEmpty = 12, kXEmpty = 14, kSFull = 17, kXwReady = 19, kMReady, kYFull,
-    kYEmpty, kDFull, kHReady, kHFree, kYOut, kDrain = kYOut + 4, kBars
+    kFullB = 0, kFullC = 2, kFullX = 4, kReady = 7, kXEmpty = 10, kSFull = 13, kDFull = 15, kXwReady = 17, kMReady, kYFull, kYEmpty,
+    kYOut, kDrain = kYOut + 4, kBars
 };
 constexpr uint32_t kBarBytes = 8 * kBars + 16;
 static_assert(kBarBytes <= 320, "barrier room");
 constexpr int kScanThreads = 768;
 
-// tensor-memory columns: scores of two chunks, each half replaced by M (16 packed columns at the start of every
-// 32); Y's sum over the chunk, its readouts of the state of two chunks, the state's increment
+// tensor-memory columns: scores of two chunks, each half replaced by M (8 packed columns at the start of every
+// 16); Y's sum over the chunk, its readouts of the state of two chunks, the state's increment
 constexpr uint32_t kTS = 0, kTYi = 256, kTYx = 320, kTD = 448;
 
 struct ScanMaps {
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) {
             const bool four = (i >= kXEmpty && i < kXEmpty + 3) || i == kMReady;
-            const bool eight = i == kXwReady || i == kHReady || i == kYEmpty;
+            const bool eight = i == kXwReady || i == kYEmpty;
             mbar_init(bars + i, four ? 4 : eight ? 8 : i >= kYOut && i < kDrain ? 2 : 1);
         }
         *err = 0;
@@ -141,12 +141,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             prefetch_tensormap(&maps.x);
             int nb = 0, nc = 0, nx = 0;
             uint64_t t0 = globaltimer_ns();
-            auto free_of = [&](int n, int stages, int empty) {
-                return n < NC && (n < stages || mbar_test_wait(bars + empty + n % stages, ((n / stages) & 1) ^ 1));
-            };
+            // the increment of chunk c follows the last other product of B and C of that chunk
+            auto used = [&](int c) { return mbar_test_wait(bars + kDFull + (c & 1), (c >> 1) & 1); };
             while (nb < NC || nc < NC || nx < NC) {
                 bool any = false;
-                if (free_of(nb, 2, kBEmpty)) {
+                if (nb < NC && (nb < 2 || used(nb - 2))) {
                     const int st = nb & 1;
                     mbar_arrive_expect_tx(bars + kFullB + st, so::kTile * halves);
                     for (int k = 0; k < halves; ++k)
@@ -154,7 +153,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                     ++nb;
                     any = true;
                 }
-                if (free_of(nc, so::kCS, kCEmpty)) {
+                if (nc < NC && (nc < so::kCS || used(nc - so::kCS))) {
                     const int st = nc % so::kCS;
                     mbar_arrive_expect_tx(bars + kFullC + st, so::kTile * halves);
                     for (int k = 0; k < halves; ++k)
@@ -162,7 +161,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                     ++nc;
                     any = true;
                 }
-                if (free_of(nx, so::kXS, kXEmpty)) {
+                if (nx < NC && (nx < so::kXS || mbar_test_wait(bars + kXEmpty + nx % so::kXS, ((nx / so::kXS) & 1) ^ 1))) {
                     const int st = nx % so::kXS;
                     mbar_arrive_expect_tx(bars + kFullX + st, so::kTile);
                     tma_load_3d(sm + so::X + st * so::kTile, &maps.x, p0, h, u.row + nx * kQ, bars + kFullX + st);
@@ -195,49 +194,45 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         // K-major tiles: 16 channels are 32 bytes of a row, the next 64 the next tile. MN-major: 16 tokens (or
         // state rows) are 16 rows of 128 bytes.
         const uint32_t dk = desc_lo(sb, 16), dm = desc_lo(sb, so::kTile);
-        auto wait = [&](int bar, uint32_t parity) {
-            const bool w = wait_bar(bars + bar, parity, lim, err);
-            tc_fence_after();
-            return w;
-        };
-        // Every wait costs this warp about a hundred cycles in which the tensor core runs dry, so each is for the last of
-        // what it stands for: X~ ready implies X loaded and a short chunk's rows cleared; the state ready, the increment
-        // before it taken; Y's sums taken, that chunk's products done.
+        auto wait = [&](int bar, uint32_t parity) { return wait_bar(bars + bar, parity, lim, err); };
+        // Two stretches of products per chunk, each behind one set of waits and one tensor-memory fence, which lets the
+        // tensor core run dry. Each wait stands for all it can: X~ ready implies the state ready, X loaded, a short
+        // chunk's rows cleared and the increment before it taken; Y's sums taken, that chunk's products done; the
+        // increment's commit frees B, C and the state's operand.
         bool ok = true;
         for (int c = -1; c < NC && NC > 0; ++c) {
             const uint32_t ph1 = c & 1;  // phase of the barriers used once per chunk
-            if (c >= 0) {
-                // readout of the state
-                if (!(ok = wait(kHReady, ph1))) break;
-                mma_steps<false>(lead, kTYx + 64 * (c & 1), dk + ((so::C + 2 * (c % so::kCS) * so::kTile) >> 4), dm + (so::HB >> 4), id_x, 0, ks / 4, 4,
-                                 kStepK, kStepMn, kJumpK, 0);
-                commit_by(lead, bars + kCEmpty + c % so::kCS);
-                commit_by(lead, bars + kHFree);
-                // state increment
-                if (!(ok = wait(kXwReady, ph1))) break;
-#pragma unroll 1
-                for (int k = 0; k < kParts; ++k)
-                    mma_steps<false>(lead, kTD, dm + ((so::B + 2 * (c & 1) * so::kTile) >> 4), dm + ((so::XW + k * so::kTile) >> 4), id_d, k > 0, 1, 8,
-                                     kStepMn, kStepMn, 0, 0);
-                commit_by(lead, bars + kDFull);
-                commit_by(lead, bars + kBEmpty + (c & 1));
-            }
-            // The next chunk's scores go in here: their tiles were asked for when the chunk before this one was
-            // read out, and M of the next chunk can start while this one's is still used.
             const int n = c + 1, st = n & 1;
+            if (c >= 0 && !(ok = wait(kXwReady, ph1))) break;
             if (c >= 1 && !(ok = wait(kYEmpty, ph1 ^ 1))) break;
             if (n < NC) {
-                if (!(ok = wait(kFullB + st, (n >> 1) & 1) && wait(kFullC + n % so::kCS, (n / so::kCS) & 1))) break;
+                if (!(ok = wait(kFullB + st, (n >> 1) & 1))) break;
                 // a short chunk's rows of B are cleared first
                 if (u.len - n * kQ < kQ && !(ok = wait(kReady + n % so::kXS, (n / so::kXS) & 1))) break;
-                mma_steps<false>(lead, kTS + 128 * st, dk + ((so::C + 2 * (n % so::kCS) * so::kTile) >> 4), dk + ((so::B + 2 * st * so::kTile) >> 4), id_s, 0,
-                                 ks / 4, 4, kStepK, kStepK, kJumpK, kJumpK);
+            }
+            tc_fence_after();
+            if (c >= 0) {
+                // readout of the state, then its increment
+                mma_steps<false, kStepK, kStepMn, kJumpK, 0>(lead, kTYx + 64 * (c & 1), dk + ((so::C + 2 * (c % so::kCS) * so::kTile) >> 4),
+                                                             dm + (so::HB >> 4), id_x, 0, ks);
+#pragma unroll 1
+                for (int k = 0; k < kParts; ++k)
+                    mma_steps<false, kStepMn, kStepMn, 0, 0>(lead, kTD, dm + ((so::B + 2 * (c & 1) * so::kTile) >> 4),
+                                                             dm + ((so::XW + k * so::kTile) >> 4), id_d, k > 0, 8);
+                commit_by(lead, bars + kDFull + (c & 1));
+            }
+            if (n < NC) {
+                // the next chunk's scores: M of the next chunk is formed while this one's is used
+                if (!(ok = wait(kFullC + n % so::kCS, (n / so::kCS) & 1))) break;
+                mma_steps<false, kStepK, kStepK, kJumpK, kJumpK>(lead, kTS + 128 * st, dk + ((so::C + 2 * (n % so::kCS) * so::kTile) >> 4),
+                                                                 dk + ((so::B + 2 * st * so::kTile) >> 4), id_s, 0, ks);
                 commit_by(lead, bars + kSFull + st);
             }
             // within the chunk
             if (c >= 0) {
                 if (!(ok = wait(kMReady, ph1))) break;
-                mma_steps<true>(lead, kTYi, kTS + 128 * (c & 1), dm + ((so::X + (c % so::kXS) * so::kTile) >> 4), id_x, 0, 4, 2, 8, kStepMn, 16, 0);
+                tc_fence_after();
+                mma_steps<true, 16, kStepMn, 0, 0>(lead, kTYi, kTS + 128 * (c & 1), dm + ((so::X + (c % so::kXS) * so::kTile) >> 4), id_x, 0, 8);
                 commit_by(lead, bars + kYFull);
             }
         }
@@ -333,7 +328,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                         }
                     }
                 }
-                tmem_st16(at + 32 * b, m);
+                const uint32_t m0[8] = {m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7]}, m1[8] = {m[8], m[9], m[10], m[11], m[12], m[13], m[14], m[15]};
+                tmem_st8(at + 32 * b, m0);
+                tmem_st8(at + 32 * b + 16, m1);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -418,7 +415,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         for (int c = -1; c < NC; ++c) {
             const int n = c + 1;
             if (c >= 0) {
-                if (!(ok = wait_bar(bars + kDFull, c & 1, lim, err))) break;
+                if (!(ok = wait_bar(bars + kDFull + (c & 1), (c >> 1) & 1, lim, err))) break;
                 tc_fence_after();
                 float x[32];
                 tmem_ld_cols<2>(tmem + lane_base + kTD + 32 * half, x);
@@ -427,11 +424,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 tc_fence_before();
             }
             if (n < NC) {
-                if (c >= 0 && !(ok = wait_bar(bars + kHFree, c & 1, lim, err))) break;
                 st_row_bf16x32(sm + so::HB, r, 4 * half, hx);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive1(bars + kHReady);
                 // X~ of chunk n, row r, once the increment before it has been formed from the last: each part is the bf16
                 // rounding of what the parts before it leave
                 const int xs = n % so::kXS;

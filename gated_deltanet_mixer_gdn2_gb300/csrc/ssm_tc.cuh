@@ -53,29 +53,29 @@ __device__ __forceinline__ void mma_ts_by(uint32_t lead, uint32_t d, uint32_t at
         "r"(kDescHi)
         : "memory");
 }
-// A product over `outer` x `inner` steps of 16 along K, the operands' start advancing by a step and, after each `inner`
-// steps, by a jump. Rolled: unrolled, the issuing warp ran through kilobytes of code once per chunk and waited for
-// instructions two thirds of the time (140 cycles per step, where the tensor core takes 32 to 64).
-template <bool kFromTmem>
-__device__ __forceinline__ void mma_steps(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc, int outer, int inner,
-                                          uint32_t da, uint32_t db, uint32_t ja, uint32_t jb) {
-#pragma unroll 1
-    for (int o = 0; o < outer; ++o) {
-#pragma unroll 1
-        for (int i = 0; i < inner; ++i) {
-            if (kFromTmem) mma_ts_by(lead, d, a, b, id, acc);
-            else mma_by(lead, d, a, b, id, acc);
-            acc = 1;
-            a += da;
-            b += db;
-        }
-        a += ja;
-        b += jb;
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// A product over up to 8 steps of 16 along K (`steps` 4 or 8), the operands' start advancing by a step and, after four
+// steps, by a jump more. Unrolled to a handful of instructions per step: the other warps of the issuing warp's
+// scheduler leave it few slots (under a full load of multiplications a rolled loop took 1200 cycles per step, this one
+// 240; alone both take the tensor core's 48).
+template <bool kFromTmem, int kDa, int kDb, int kJa, int kJb>
+__device__ __forceinline__ void mma_steps(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc, int steps) {
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+        if (s >= 4 && steps <= 4) break;
+        const uint32_t as = a + s * kDa + (s >= 4 ? kJa : 0), bs = b + s * kDb + (s >= 4 ? kJb : 0);
+        if (kFromTmem) mma_ts_by(lead, d, as, bs, id, s ? 1 : acc);
+        else mma_by(lead, d, as, bs, id, s ? 1 : acc);
     }
 }
 // Operand advances in descriptor units (16 bytes): K-major tiles hold 64 channels in 128-byte rows (32 bytes a step, the
 // next tile after four); MN-major ones a token or state row per 128 bytes (16 rows a step).
-constexpr uint32_t kStepK = 2, kJumpK = (kTileBytes >> 4) - 8, kStepMn = 128;
+constexpr int kStepK = 2, kJumpK = (kTileBytes >> 4) - 8, kStepMn = 128;
 
 __device__ __forceinline__ void commit_by(uint32_t lead, uint64_t* bar) {
     asm volatile(

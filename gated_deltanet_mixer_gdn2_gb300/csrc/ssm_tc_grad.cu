@@ -76,12 +76,6 @@ __device__ __forceinline__ float transpose_sum(float (&v)[16], int lane) {
     return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
 __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ GradTcArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -468,7 +462,7 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
         };
         bool ok = wait(gBc, 0) && (!tail || wait(gGate, 0));
         if (ok) {
-            mma_steps<false>(lead, kTR, dk + (sg::B >> 4), dk + (sg::C >> 4), id_kk, 0, ks / 4, 4, kStepK, kStepK, kJumpK, kJumpK);
+            mma_steps<false, kStepK, kStepK, kJumpK, kJumpK>(lead, kTR, dk + (sg::B >> 4), dk + (sg::C >> 4), id_kk, 0, ks);
             commit_by(lead, bars + gS);
         }
         for (int it = 0; ok && it < NI; ++it) {
@@ -476,23 +470,23 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
             const uint32_t ph = (it >> 1) & 1, ph1 = it & 1;
             const uint32_t xo = (sg::X + st * kTileBytes) >> 4, yo = (sg::DY + st * kTileBytes) >> 4;
             if (!(ok = wait(gXy + st, ph) && (!tail || wait(gGate + st, ph)) && (it ? wait(gAll, ph1 ^ 1) : wait(gSRead, 0)))) break;
-            mma_steps<false>(lead, kTR, dk + xo, dk + yo, id_kk, 0, 1, 4, kStepK, kStepK, 0, 0);  // R^T = X dY^T
+            mma_steps<false, kStepK, kStepK, 0, 0>(lead, kTR, dk + xo, dk + yo, id_kk, 0, 4);  // R^T = X dY^T
             commit_by(lead, bars + gR);
             if (!(ok = wait(gHd, ph1) && (it == 0 || wait(gURead, ph1 ^ 1)))) break;
             // C H and B A
-            mma_steps<false>(lead, kTT, dk + (sg::C >> 4), dm + (sg::H0 >> 4), id_t, 0, ks / 4, 4, kStepK, kStepMn, kJumpK, 0);
-            mma_steps<false>(lead, kTU, dk + (sg::B >> 4), dm + (sg::DH >> 4), id_t, 0, ks / 4, 4, kStepK, kStepMn, kJumpK, 0);
+            mma_steps<false, kStepK, kStepMn, kJumpK, 0>(lead, kTT, dk + (sg::C >> 4), dm + (sg::H0 >> 4), id_t, 0, ks);
+            mma_steps<false, kStepK, kStepMn, kJumpK, 0>(lead, kTU, dk + (sg::B >> 4), dm + (sg::DH >> 4), id_t, 0, ks);
             commit_by(lead, bars + gTu);
             if (!(ok = wait(gPReady, ph1))) break;
             // dB += (R W s)^T C + X~ A^T
-            mma_steps<true>(lead, kTdB, kTR, dm + (sg::C >> 4), id_nm, it > 0, 1, 8, 16, kStepMn, 0, 0);
-            mma_steps<false>(lead, kTdB, dk + xo, dk + (sg::DH >> 4), id_nk, 1, 1, 4, kStepK, kStepK, 0, 0);
+            mma_steps<true, 16, kStepMn, 0, 0>(lead, kTdB, kTR, dm + (sg::C >> 4), id_nm, it > 0, 8);
+            mma_steps<false, kStepK, kStepK, 0, 0>(lead, kTdB, dk + xo, dk + (sg::DH >> 4), id_nk, 1, 4);
             if (!(ok = wait(gUScaled, ph1))) break;
-            mma_steps<true>(lead, kTU, kTR + 8, dm + yo, id_t, 1, 1, 8, 16, kStepMn, 0, 0);  // U += (S W)^T dY
+            mma_steps<true, 16, kStepMn, 0, 0>(lead, kTU, kTR + 8, dm + yo, id_t, 1, 8);  // U += (S W)^T dY
             commit_by(lead, bars + gDx);
             // dC += (R W s) B + (e^L dY) H^T
-            mma_steps<false>(lead, kTdC, dm + (sg::P1 >> 4), dm + (sg::B >> 4), id_mm, it > 0, 1, 8, kStepMn, kStepMn, 0, 0);
-            mma_steps<false>(lead, kTdC, dk + (sg::DYW >> 4), dk + (sg::H0 >> 4), id_nk, 1, 1, 4, kStepK, kStepK, 0, 0);
+            mma_steps<false, kStepMn, kStepMn, 0, 0>(lead, kTdC, dm + (sg::P1 >> 4), dm + (sg::B >> 4), id_mm, it > 0, 8);
+            mma_steps<false, kStepK, kStepK, 0, 0>(lead, kTdC, dk + (sg::DYW >> 4), dk + (sg::H0 >> 4), id_nk, 1, 4);
             commit_by(lead, bars + gAll);
             commit_by(lead, bars + gXyDone + st);
             commit_by(lead, bars + gHdFree);

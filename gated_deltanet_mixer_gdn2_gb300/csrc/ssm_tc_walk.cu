@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kWalkThreadsTc, Sw<kParts>::kPerSm) walk_tc_ke
 #pragma unroll 1
             for (int k = 0; k < kParts; ++k) {
                 const uint32_t xa = dm + ((k ? sw::XW + (st * (kParts - 1) + k - 1) * kTileBytes : sw::X + st * kTileBytes) >> 4);
-                mma_steps<false>(lead, tmem + 64 * st, km, xa, id_d, k > 0, 1, 8, kStepMn, kStepMn, 0, 0);
+                mma_steps<false, kStepMn, kStepMn, 0, 0>(lead, tmem + 64 * st, km, xa, id_d, k > 0, 8);
             }
             commit_by(lead, bars + wDFull + st);
             commit_by(lead, bars + wEmpty + st);
