@@ -203,15 +203,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         for (int c = -1; c < NC && NC > 0; ++c) {
             const uint32_t ph1 = c & 1;  // phase of the barriers used once per chunk
             const int n = c + 1, st = n & 1;
-            if (c >= 0 && !(ok = wait(kXwReady, ph1))) break;
-            if (c >= 1 && !(ok = wait(kYEmpty, ph1 ^ 1))) break;
-            if (n < NC) {
-                if (!(ok = wait(kFullB + st, (n >> 1) & 1))) break;
-                // a short chunk's rows of B are cleared first
-                if (u.len - n * kQ < kQ && !(ok = wait(kReady + n % so::kXS, (n / so::kXS) & 1))) break;
-            }
-            tc_fence_after();
             if (c >= 0) {
+                if (!(ok = wait(kXwReady, ph1))) break;
+                tc_fence_after();
                 // readout of the state, then its increment
                 mma_steps<false, kStepK, kStepMn, kJumpK, 0>(lead, kTYx + 64 * (c & 1), dk + ((so::C + 2 * (c % so::kCS) * so::kTile) >> 4),
                                                              dm + (so::HB >> 4), id_x, 0, ks);
@@ -221,9 +215,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                                                              dm + ((so::XW + k * so::kTile) >> 4), id_d, k > 0, 8);
                 commit_by(lead, bars + kDFull + (c & 1));
             }
+            if (c >= 1 && !(ok = wait(kYEmpty, ph1 ^ 1))) break;
             if (n < NC) {
                 // the next chunk's scores: M of the next chunk is formed while this one's is used
-                if (!(ok = wait(kFullC + n % so::kCS, (n / so::kCS) & 1))) break;
+                if (!(ok = wait(kFullB + st, (n >> 1) & 1) && wait(kFullC + n % so::kCS, (n / so::kCS) & 1))) break;
+                // a short chunk's rows of B are cleared first
+                if (u.len - n * kQ < kQ && !(ok = wait(kReady + n % so::kXS, (n / so::kXS) & 1))) break;
                 mma_steps<false, kStepK, kStepK, kJumpK, kJumpK>(lead, kTS + 128 * st, dk + ((so::C + 2 * (n % so::kCS) * so::kTile) >> 4),
                                                                  dk + ((so::B + 2 * st * so::kTile) >> 4), id_s, 0, ks);
                 commit_by(lead, bars + kSFull + st);
