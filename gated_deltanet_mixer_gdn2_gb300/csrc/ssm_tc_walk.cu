@@ -11,24 +11,26 @@
 namespace gdn2 {
 namespace {
 
-// Two stages of keys and values; X~ replaces its values in place, with three parts the other two have a buffer per
-// stage. With one part two blocks fit an SM and hide each other's waits (4 x 2048 x 32 heads, both directions: see
-// launch_ssm_walk_tc).
+// Stages of keys and values; X~ replaces its values in place, with three parts the other two have two sets of buffers.
+// With one part two stages let two blocks share an SM and hide each other's waits; a tile takes 2300 cycles from its
+// request, so the one block that three parts leave room for has three (two: 197 us instead of 150 us for 2 x 32768
+// tokens, 32 heads).
 template <int kParts>
 struct Sw {
-    static constexpr uint32_t K = 0;                                    // 2 stages x 2 tiles
-    static constexpr uint32_t X = K + 4 * kTileBytes;                   // 2 stages
-    static constexpr uint32_t XW = X + 2 * kTileBytes;                  // 2 stages x (kParts - 1)
+    static constexpr int kStages = kParts == 1 ? 2 : 3;
+    static constexpr uint32_t K = 0;                                    // kStages x 2 tiles
+    static constexpr uint32_t X = K + 2 * kStages * kTileBytes;         // kStages
+    static constexpr uint32_t XW = X + kStages * kTileBytes;            // 2 sets x (kParts - 1)
     static constexpr uint32_t GATE = XW + 2 * (kParts - 1) * kTileBytes;  // {weight [128], decay} per stage
     static constexpr uint32_t kGateStage = 512 + 16;
-    static constexpr uint32_t BAR = GATE + 2 * kGateStage;
-    static constexpr uint32_t TOTAL = BAR + 128;
+    static constexpr uint32_t BAR = GATE + kStages * kGateStage;
+    static constexpr uint32_t TOTAL = BAR + 160;
     static constexpr uint32_t kAlloc = TOTAL + 1024;
     static constexpr int kPerSm = kParts == 1 ? 2 : 1;
     static_assert(kPerSm * (kAlloc + 1024 + 16) <= 228 * 1024 && BAR % 8 == 0, "walk kernel shared memory");
 };
-enum WalkBar { wFull = 0, wReady = 2, wEmpty = 4, wXwReady = 6, wDFull = 8, wDEmpty = 10, wDrain = 12, wBars };
-static_assert(wBars * 8 + 16 <= 128, "barrier room");
+enum WalkBar { wFull = 0, wReady = 3, wEmpty = 6, wXwReady = 9, wDFull = 12, wDEmpty = 14, wDrain = 16, wBars };
+static_assert(wBars * 8 + 16 <= 160, "barrier room");
 constexpr int kWalkThreadsTc = 384;
 
 struct WalkMaps {
@@ -88,8 +90,8 @@ __global__ void __launch_bounds__(kWalkThreadsTc, Sw<kParts>::kPerSm) walk_tc_ke
             prefetch_tensormap(mx);
             int n = 0;
             for (; n < NC; ++n) {
-                const int st = n & 1, row = u.row + chunk_at(n) * kQ;
-                if (n >= 2 && !mbar_wait_or_abort(bars + wEmpty + st, ((n >> 1) & 1) ^ 1, lim, err)) {
+                const int st = n % sw::kStages, row = u.row + chunk_at(n) * kQ;
+                if (n >= sw::kStages && !mbar_wait_or_abort(bars + wEmpty + st, ((n / sw::kStages) & 1) ^ 1, lim, err)) {
                     note_failure(err);
                     break;
                 }
@@ -97,26 +99,25 @@ __global__ void __launch_bounds__(kWalkThreadsTc, Sw<kParts>::kPerSm) walk_tc_ke
                 for (int k = 0; k < halves; ++k) tma_load_3d(sm + sw::K + (2 * st + k) * kTileBytes, mk, 64 * k, grp, row, bars + wFull + st);
                 tma_load_3d(sm + sw::X + st * kTileBytes, mx, p0, h, row, bars + wFull + st);
             }
-            for (int c = n > 2 ? n - 2 : 0; c < n; ++c)  // nothing in flight when the block ends
-                mbar_wait(bars + wFull + (c & 1), (c >> 1) & 1, kDefaultWaitNs);
+            for (int c = n > sw::kStages ? n - sw::kStages : 0; c < n; ++c)  // nothing in flight when the block ends
+                mbar_wait(bars + wFull + c % sw::kStages, (c / sw::kStages) & 1, kDefaultWaitNs);
         }
     } else if (warp == 1) {
         const uint32_t id_d = idesc_bf16(128, 64, true, true), lead = elect_one();
         const uint32_t dm = desc_lo(sb, kTileBytes);
         bool ok = true;
         for (int c = 0; c < NC; ++c) {
-            const int st = c & 1;
-            const uint32_t ph = (c >> 1) & 1;
-            if (!(ok = wait_bar(bars + wFull + st, ph, lim, err) && wait_bar(bars + wXwReady + st, ph, lim, err))) break;
-            if (c >= 2 && !(ok = wait_bar(bars + wDEmpty + st, ph ^ 1, lim, err))) break;
+            const int st = c % sw::kStages, set = c & 1;
+            if (!(ok = wait_bar(bars + wXwReady + st, (c / sw::kStages) & 1, lim, err))) break;  // after the tiles' arrival
+            if (c >= 2 && !(ok = wait_bar(bars + wDEmpty + set, ((c >> 1) & 1) ^ 1, lim, err))) break;
             tc_fence_after();
             const uint32_t km = dm + ((sw::K + 2 * st * kTileBytes) >> 4);
 #pragma unroll 1
             for (int k = 0; k < kParts; ++k) {
-                const uint32_t xa = dm + ((k ? sw::XW + (st * (kParts - 1) + k - 1) * kTileBytes : sw::X + st * kTileBytes) >> 4);
-                mma_steps<false, kStepMn, kStepMn, 0, 0>(lead, tmem + 64 * st, km, xa, id_d, k > 0, 8);
+                const uint32_t xa = dm + ((k ? sw::XW + (set * (kParts - 1) + k - 1) * kTileBytes : sw::X + st * kTileBytes) >> 4);
+                mma_steps<false, kStepMn, kStepMn, 0, 0>(lead, tmem + 64 * set, km, xa, id_d, k > 0, 8);
             }
-            commit_by(lead, bars + wDFull + st);
+            commit_by(lead, bars + wDFull + set);
             commit_by(lead, bars + wEmpty + st);
         }
         commit_by(lead, bars + wDrain);
@@ -136,8 +137,8 @@ __global__ void __launch_bounds__(kWalkThreadsTc, Sw<kParts>::kPerSm) walk_tc_ke
         };
         if (warp - 2 < NC) fetch(warp - 2);
         for (int c = warp - 2; c < NC; c += 2) {
-            const int st = c & 1;
-            if (!wait_bar(bars + wFull + st, (c >> 1) & 1, lim, err)) break;
+            const int st = c % sw::kStages;
+            if (!wait_bar(bars + wFull + st, (c / sw::kStages) & 1, lim, err)) break;
             // forward: the decay behind the token up to the chunk's end; backward: up to and with the token.
             // Sums from the nearer side, so that small values keep their digits behind strong decays.
             float p[4], acc;
@@ -207,14 +208,14 @@ __global__ void __launch_bounds__(kWalkThreadsTc, Sw<kParts>::kPerSm) walk_tc_ke
             const int n = c + 1;
             const float decay_c = decay;
             if (n < NC) {
-                const int st = n & 1;
-                const uint32_t ph = (n >> 1) & 1;
+                const int st = n % sw::kStages;
+                const uint32_t ph = (n / sw::kStages) & 1;
                 if (!(ok = wait_bar(bars + wFull + st, ph, lim, err) && wait_bar(bars + wReady + st, ph, lim, err))) break;
                 const float* arr = reinterpret_cast<const float*>(sm + sw::GATE + st * sw::kGateStage);
                 const float w = arr[r];
                 decay = arr[128];
                 uint8_t* xt = sm + sw::X + st * kTileBytes + r * 128;
-                uint8_t* more = sm + sw::XW + st * (kParts - 1) * kTileBytes + r * 128;
+                uint8_t* more = sm + sw::XW + (n & 1) * (kParts - 1) * kTileBytes + r * 128;  // of two chunks before: taken with its increment
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int cell = ((4 * half + k) ^ (r & 7)) << 4;
