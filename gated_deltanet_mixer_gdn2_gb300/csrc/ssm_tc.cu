@@ -6,7 +6,8 @@
 // One block walks over the chunks of its unit for 64 value columns of one head; all five products run on
 // tcgen05 with their accumulators in tensor memory, and the state stays in registers in fp32. Only the
 // update of the state is serial from chunk to chunk (64 multiply-adds per thread), so the block is a
-// pipeline of warp roles over different chunks: copies (warp 0), products (warp 1), gates (warps 2 and 3), M (warps 4-7),
+// pipeline of warp roles over different chunks: products (warp 0: rows 0-31 of M are
+// the least work, so its scheduler is the least loaded), copies (warp 1), gates (warps 2 and 3), M (warps 4-7),
 // Y (warps 8-15), X~ and state (warps 16-23).
 #include "ssm_tc.cuh"
 
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     const int ks = a.N / 16;  // K steps over the state size
     const size_t plane = static_cast<size_t>(a.N) * a.P;
 
-    if (warp == 0) {
+    if (warp == 1) {
         if (lane == 0) {
             // ---- copies: each kind of tile as soon as its stage is free, whichever that is
             const int halves = a.N / 64;
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             drain(nc, kFullC, so::kCS);
             drain(nx, kFullX, so::kXS);
         }
-    } else if (warp == 1) {
+    } else if (warp == 0) {
         const uint32_t id_s = idesc_bf16(128, 128, false, false), id_d = idesc_bf16(128, 64, true, true),
                        id_x = idesc_bf16(128, 64, false, true);
         const uint32_t lead = elect_one();

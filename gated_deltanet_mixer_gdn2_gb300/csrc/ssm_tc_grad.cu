@@ -44,7 +44,7 @@ static_assert(gBars * 8 + 16 <= 256, "barrier room");
 // tensor-memory columns: S^T, then each head's R^T and, in its place, per 16 columns 8 packed of (R W s)^T and 8
 // of (S W)^T; dB; dC; C H; U
 constexpr uint32_t kTR = 0, kTdB = 128, kTdC = 256, kTT = 384, kTU = 448;
-constexpr int kGradTc = 640;  // sixteen compute warps, then products, copies, gates, results
+constexpr int kGradTc = 640;  // sixteen compute warps, then results, copies, gates, products
 
 struct GradMaps {
     CUtensorMap x, dy, b, c, dx;
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
                 }
             }
         }
-    } else if (warp == 19) {
+    } else if (warp == 16) {
         // ---- results of an iteration: dx's tile, and at a head's end dg and dstep, four tokens per lane
         const float* sums = reinterpret_cast<const float*>(sm + sg::SUM);
         int pi = 0, h = h_lo;
@@ -448,8 +448,8 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
             }
         }
         if (lane == 0) bulk_wait_all();
-    } else if (warp == 16) {
-        // ---- products
+    } else if (warp == 19) {
+        // ---- products (rows 96-127 have three blocks of zeros: its scheduler is the least loaded)
         const uint32_t lead = elect_one();
         const uint32_t dk = desc_lo(sb, 16), dm = desc_lo(sb, kTileBytes);
         const uint32_t id_kk = idesc_bf16(128, 128, false, false), id_t = idesc_bf16(128, 64, false, true);
