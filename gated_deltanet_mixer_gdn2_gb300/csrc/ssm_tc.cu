@@ -34,7 +34,7 @@ struct So {
 };
 
 enum Bar {
-    kFullB = 0, kFullC = 2, kFullX = 4, kReady = 7, kXEmpty = 10, kSFull = 13, kDFull = 15, kXwReady = 17, kMReady, kYFull, kYEmpty,
+    kFullB = 0, kFullC = 2, kFullX = 4, kReady = 7, kXEmpty = 10, kSFull = 13, kDFull = 15, kXwReady = 17, kMReady, kYFull = kMReady + 2, kYEmpty,
     kYOut, kDrain = kYOut + 4, kBars
 };
 constexpr uint32_t kBarBytes = 8 * kBars + 16;
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
 
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) {
-            const bool four = (i >= kXEmpty && i < kXEmpty + 3) || i == kMReady;
+            const bool four = (i >= kXEmpty && i < kXEmpty + 3) || i == kMReady || i == kMReady + 1;
             const bool eight = i == kXwReady || i == kYEmpty;
             mbar_init(bars + i, four ? 4 : eight ? 8 : i >= kYOut && i < kDrain ? 2 : 1);
         }
@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             }
             // within the chunk
             if (c >= 0) {
-                if (!(ok = wait(kMReady, ph1))) break;
+                // two barriers: M of the next chunk may be ready before this is looked at
+                if (!(ok = wait(kMReady + (c & 1), (c >> 1) & 1))) break;
                 tc_fence_after();
                 mma_steps<true, 16, kStepMn, 0, 0>(lead, kTYi, kTS + 128 * (c & 1), dm + ((so::X + (c % so::kXS) * so::kTile) >> 4), id_x, 0, 8);
                 commit_by(lead, bars + kYFull);
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive1(bars + kMReady);
+            if (lane == 0) mbar_arrive1(bars + kMReady + (c & 1));
         }
     } else if (warp >= 8 && warp < 16) {
         // ---- Y: row i of the chunk and half of the 64 columns per thread; replaces that part of X, and the two warps of
