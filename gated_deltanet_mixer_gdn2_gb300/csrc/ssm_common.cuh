@@ -135,6 +135,15 @@ __device__ __forceinline__ float ssm_softplus(float v) { return fmaxf(v, 0.f) + 
 // Log-decays enter every exponential floored (common.cuh): a full reset (g = -inf) keeps sums finite.
 __device__ __forceinline__ float ssm_gate(float g) { return fmaxf(g, kGateFloor); }
 
+constexpr float kLn2 = 0.69314718056f;
+
+// e^g as the fp32 sum x + y. A state that decays by 1 - 1e-3 a token is multiplied by thousands of factors in which one
+// value's rounding, repeated, would add up to 1e-5 and more; with its remainder the factor is exact to 2^-24 |g|.
+__device__ __forceinline__ float2 ssm_decay(float g) {
+    const float a = expf(g);
+    return make_float2(a, a >= 0.5f && a <= 2.f ? expm1f(g) - (a - 1.f) : 0.f);  // a - 1 is exact there
+}
+
 inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // One tensor of the scan: pointer and row (token) stride in elements; heads and channels are dense.

@@ -52,7 +52,7 @@ template <typename T, typename S>
 __global__ void __launch_bounds__(kThreads)
     decode_kernel(DecodeArgs a, const T* __restrict__ x, const T* __restrict__ delta, S* __restrict__ state, T* __restrict__ y) {
     __shared__ __align__(16) float sB[kMaxN], sC[kMaxN], sX[kMaxP], red[kThreads / 32][kMaxP];
-    __shared__ float sGate[2];
+    __shared__ float sGate[3];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int parts = gridDim.x / a.G, grp = blockIdx.x / parts, part = blockIdx.x - grp * parts, b = blockIdx.y;
     const int per = a.H / a.G, h_lo = grp * per + part * a.heads, h_hi = min(h_lo + a.heads, (grp + 1) * per);
@@ -64,13 +64,12 @@ __global__ void __launch_bounds__(kThreads)
     constexpr int kBatch = 8;
     const size_t plane = static_cast<size_t>(a.N) * a.P;
     S* st = state + (static_cast<size_t>(slot) * a.H + h_lo) * plane;
-    const bool used = r0 < rpp;  // P = 48, 80, ..: the threads past the last whole row idle
     float4 s[kBatch];
     auto fetch = [&](const S* base, int i0) {
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
             const int n = (i0 + q) * rpp + r0;
-            if (used && n < a.N && i0 + q < passes) s[q] = Quad<S>::load(base + static_cast<size_t>(n) * a.P + c4);
+            if (n < a.N && i0 + q < passes) s[q] = Quad<S>::load(base + static_cast<size_t>(n) * a.P + c4);
         }
     };
     fetch(st, 0);
@@ -126,26 +125,28 @@ __global__ void __launch_bounds__(kThreads)
         }
         if (tid == kThreads - 1) {
             const float sp = ssm_softplus(to_f32(delta[static_cast<size_t>(b) * a.ld_delta + h]) + a.delta_bias[h]);
-            sGate[0] = expf(ssm_gate(a.a[h] * sp));
-            sGate[1] = sp;
+            const float2 e = ssm_decay(ssm_gate(a.a[h] * sp));
+            sGate[0] = e.x;
+            sGate[1] = e.y;
+            sGate[2] = sp;
         }
         __syncthreads();
-        const float al = sGate[0], sp = sGate[1];
-        float4 xv = make_float4(0.f, 0.f, 0.f, 0.f), acc = xv;
-        if (used) xv = *reinterpret_cast<const float4*>(&sX[c4]);
+        const float al = sGate[0], lo = sGate[1], sp = sGate[2];
+        const float4 xv = *reinterpret_cast<const float4*>(&sX[c4]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         const float4 xs = make_float4(sp * xv.x, sp * xv.y, sp * xv.z, sp * xv.w);
         for (int i0 = 0; i0 < passes; i0 += kBatch) {
             if (i0) fetch(st, i0);
 #pragma unroll
             for (int q = 0; q < kBatch; ++q) {
                 const int n = (i0 + q) * rpp + r0;
-                if (!used || n >= a.N || i0 + q >= passes) continue;
+                if (n >= a.N || i0 + q >= passes) continue;
                 const float bv = sB[n], cv = sC[n];
                 float4 v = s[q];
-                v.x = fmaf(al, v.x, bv * xs.x);
-                v.y = fmaf(al, v.y, bv * xs.y);
-                v.z = fmaf(al, v.z, bv * xs.z);
-                v.w = fmaf(al, v.w, bv * xs.w);
+                v.x = fmaf(al, v.x, fmaf(lo, v.x, bv * xs.x));
+                v.y = fmaf(al, v.y, fmaf(lo, v.y, bv * xs.y));
+                v.z = fmaf(al, v.z, fmaf(lo, v.z, bv * xs.z));
+                v.w = fmaf(al, v.w, fmaf(lo, v.w, bv * xs.w));
                 acc.x = fmaf(cv, v.x, acc.x);
                 acc.y = fmaf(cv, v.y, acc.y);
                 acc.z = fmaf(cv, v.z, acc.z);
@@ -154,16 +155,14 @@ __global__ void __launch_bounds__(kThreads)
             }
         }
         if (h + 1 < h_hi) fetch(st + plane, 0);
-        // y: over the threads of a column. Within a warp while whole rows fit it, then over the warps.
-        if (quads <= 32 && (quads & (quads - 1)) == 0) {
-            for (int d = quads; d < 32; d <<= 1) {
-                acc.x += __shfl_xor_sync(0xffffffffu, acc.x, d);
-                acc.y += __shfl_xor_sync(0xffffffffu, acc.y, d);
-                acc.z += __shfl_xor_sync(0xffffffffu, acc.z, d);
-                acc.w += __shfl_xor_sync(0xffffffffu, acc.w, d);
-            }
-            if (lane < quads) *reinterpret_cast<float4*>(&red[warp][c4]) = acc;
+        // y: over the threads of a column, within the warp (P / 4 is a power of two up to 32), then over the warps
+        for (int d = quads; d < 32; d <<= 1) {
+            acc.x += __shfl_xor_sync(0xffffffffu, acc.x, d);
+            acc.y += __shfl_xor_sync(0xffffffffu, acc.y, d);
+            acc.z += __shfl_xor_sync(0xffffffffu, acc.z, d);
+            acc.w += __shfl_xor_sync(0xffffffffu, acc.w, d);
         }
+        if (lane < quads) *reinterpret_cast<float4*>(&red[warp][c4]) = acc;
         __syncthreads();
         if (tid < a.P) {
             float v = a.dskip ? a.dskip[h] * sX[tid] : 0.f;

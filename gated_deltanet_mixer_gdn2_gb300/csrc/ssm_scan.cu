@@ -30,7 +30,7 @@ __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
 }
 
 // Token by token through one unit, the state in registers: warp w holds rows w N/4 .. of 32 columns.
-// Three multiply-adds per state element and token and one shared-memory read of B and C for four rows
+// Four multiply-adds per state element and token and one shared-memory read of B and C for four rows
 // bound it; the sum over N crosses the four warps once per tile of tokens.
 //   kForward        y, from the unit's starting state (units > 1 per sequence: `states`, else s0)
 //   kIncrement      the unit's state from zero into `states`, its total log-decay into `decay`
@@ -42,7 +42,8 @@ __global__ void __launch_bounds__(kWalkThreads)
                 float* __restrict__ states, float* __restrict__ decay, int use_states, int H, int G, int P) {
     constexpr int N = 4 * NPT;
     __shared__ float sB[kWalkTile][N], sC[kMode == kForward ? kWalkTile : 1][N], sX[kWalkTile][kWalkCols];
-    __shared__ float sY[kMode == kForward ? kWalkTile : 1][4][kWalkCols], sA[kWalkTile], sS[kWalkTile];
+    __shared__ float sY[kMode == kForward ? kWalkTile : 1][4][kWalkCols], sS[kWalkTile];
+    __shared__ float2 sA[kWalkTile];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.y, grp = h / (H / G), p = blockIdx.z * kWalkCols + lane;
     Unit u;
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kWalkThreads)
         }
         if (tid < n) {
             const float gt = ssm_gate(to_f32(g[(row + tid) * H + h]));
-            sA[tid] = expf(gt);
+            sA[tid] = ssm_decay(gt);
             sS[tid] = kMode == kIncrementBack ? gt : to_f32(step[(row + tid) * H + h]);
             if (kMode == kIncrement) sY[0][0][tid] = gt;
         }
@@ -91,21 +92,24 @@ __global__ void __launch_bounds__(kWalkThreads)
             for (int t = 0; t < n; ++t) gsum += kMode == kIncrement ? sY[0][0][t] : sS[t];
         for (int q = 0; q < n; ++q) {
             const int t = kMode == kIncrementBack ? n - 1 - q : q;
-            const float a = sA[t], x = kMode == kIncrementBack ? sX[t][lane] : sX[t][lane] * sS[t];
+            const float2 al = sA[t];
+            const float a = al.x, lo = al.y, x = kMode == kIncrementBack ? sX[t][lane] : sX[t][lane] * sS[t];
             float acc0 = 0.f, acc1 = 0.f;
 #pragma unroll
             for (int i = 0; i < NPT; i += 4) {
                 const float4 b = *reinterpret_cast<const float4*>(&sB[t][warp * NPT + i]);
                 if (kMode == kIncrementBack) {
-                    st[i] = a * fmaf(b.x, x, st[i]);
-                    st[i + 1] = a * fmaf(b.y, x, st[i + 1]);
-                    st[i + 2] = a * fmaf(b.z, x, st[i + 2]);
-                    st[i + 3] = a * fmaf(b.w, x, st[i + 3]);
+                    const float u0 = fmaf(b.x, x, st[i]), u1 = fmaf(b.y, x, st[i + 1]);
+                    const float u2 = fmaf(b.z, x, st[i + 2]), u3 = fmaf(b.w, x, st[i + 3]);
+                    st[i] = fmaf(a, u0, lo * u0);
+                    st[i + 1] = fmaf(a, u1, lo * u1);
+                    st[i + 2] = fmaf(a, u2, lo * u2);
+                    st[i + 3] = fmaf(a, u3, lo * u3);
                 } else {
-                    st[i] = fmaf(a, st[i], b.x * x);
-                    st[i + 1] = fmaf(a, st[i + 1], b.y * x);
-                    st[i + 2] = fmaf(a, st[i + 2], b.z * x);
-                    st[i + 3] = fmaf(a, st[i + 3], b.w * x);
+                    st[i] = fmaf(a, st[i], fmaf(lo, st[i], b.x * x));
+                    st[i + 1] = fmaf(a, st[i + 1], fmaf(lo, st[i + 1], b.y * x));
+                    st[i + 2] = fmaf(a, st[i + 2], fmaf(lo, st[i + 2], b.z * x));
+                    st[i + 3] = fmaf(a, st[i + 3], fmaf(lo, st[i + 3], b.w * x));
                 }
                 if (kMode == kForward) {
                     const float4 c = *reinterpret_cast<const float4*>(&sC[t][warp * NPT + i]);

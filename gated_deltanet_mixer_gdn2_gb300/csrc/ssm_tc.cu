@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 hx[4 * k] = f.x; hx[4 * k + 1] = f.y; hx[4 * k + 2] = f.z; hx[4 * k + 3] = f.w;
             }
         }
-        float decay = 1.f;
+        float2 decay = make_float2(1.f, 0.f);
         bool ok = true;
         for (int c = -1; c < NC; ++c) {
             const int n = c + 1;
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 float x[32];
                 tmem_ld_cols<2>(tmem + lane_base + kTD + 32 * half, x);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) hx[k] = fmaf(decay, hx[k], x[k]);
+                for (int k = 0; k < 32; ++k) hx[k] = fmaf(decay.x, hx[k], kParts == 1 ? x[k] : fmaf(decay.y, hx[k], x[k]));
                 tc_fence_before();
             }
             if (n < NC) {
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 if (!(ok = wait_bar(bars + kFullX + xs, (n / so::kXS) & 1, lim, err) && wait_bar(bars + kReady + xs, (n / so::kXS) & 1, lim, err))) break;
                 const float* arr = reinterpret_cast<const float*>(sm + so::GATE + xs * so::kGateStage);
                 const float w = arr[256 + r];
-                decay = ex2_approx(arr[127]);
+                decay = kParts == 1 ? make_float2(ex2_approx(arr[127]), 0.f) : ssm_decay(kLn2 * arr[127]);
                 const uint8_t* xt = sm + so::X + xs * so::kTile + r * 128;
                 uint8_t* to = sm + so::XW + r * 128;
 #pragma unroll

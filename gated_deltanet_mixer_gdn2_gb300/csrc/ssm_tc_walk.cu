@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kWalkThreadsTc, Sw<kParts>::kPerSm) walk_tc_ke
             w.x *= sn[0]; w.y *= sn[1]; w.z *= sn[2]; w.w *= sn[3];
             uint8_t* arr = sm + sw::GATE + st * sw::kGateStage;
             reinterpret_cast<float4*>(arr)[lane] = w;
-            if (lane == 0) *reinterpret_cast<float*>(arr + 512) = ex2_approx(end);
+            if (lane == 0) *reinterpret_cast<float2*>(arr + 512) = kParts == 1 ? make_float2(ex2_approx(end), 0.f) : ssm_decay(kLn2 * end);
             const int n = u.len - chunk_at(c) * kQ;
             if (n < kQ) {  // the rows past the sequence hold other tokens: zeros, so that not even their NaN enters a sum
                 const uint4 z = make_uint4(0, 0, 0, 0);
@@ -202,18 +202,18 @@ __global__ void __launch_bounds__(kWalkThreadsTc, Sw<kParts>::kPerSm) walk_tc_ke
             save = static_cast<uint8_t*>(job.save) + ((first_chunk * a.H + h) * pb + pi) * tile;
         }
         const size_t save_step = static_cast<size_t>(a.H) * pb * tile;
-        float decay = 1.f;
+        float2 decay = make_float2(1.f, 0.f);
         bool ok = true;
         for (int c = -1; c < NC; ++c) {
             const int n = c + 1;
-            const float decay_c = decay;
+            const float2 decay_c = decay;
             if (n < NC) {
                 const int st = n % sw::kStages;
                 const uint32_t ph = (n / sw::kStages) & 1;
                 if (!(ok = wait_bar(bars + wFull + st, ph, lim, err) && wait_bar(bars + wReady + st, ph, lim, err))) break;
                 const float* arr = reinterpret_cast<const float*>(sm + sw::GATE + st * sw::kGateStage);
                 const float w = arr[r];
-                decay = arr[128];
+                decay = *reinterpret_cast<const float2*>(arr + 128);
                 uint8_t* xt = sm + sw::X + st * kTileBytes + r * 128;
                 uint8_t* more = sm + sw::XW + (n & 1) * (kParts - 1) * kTileBytes + r * 128;  // of two chunks before: taken with its increment
 #pragma unroll
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kWalkThreadsTc, Sw<kParts>::kPerSm) walk_tc_ke
                 float x[32];
                 tmem_ld_cols<2>(tmem + lane_base + 64 * set + 32 * half, x);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) hx[k] = fmaf(decay_c, hx[k], x[k]);
+                for (int k = 0; k < 32; ++k) hx[k] = fmaf(decay_c.x, hx[k], kParts == 1 ? x[k] : fmaf(decay_c.y, hx[k], x[k]));
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive1(bars + wDEmpty + set);
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kWalkThreadsTc, Sw<kParts>::kPerSm) walk_tc_ke
     }
     tc_fence_before();
     __syncthreads();
-    if (a.increments && tid == 0 && pi == 0) job.decay[static_cast<size_t>(blockIdx.y) * a.H + h] = (totals[0] + totals[1]) * 0.69314718056f;
+    if (a.increments && tid == 0 && pi == 0) job.decay[static_cast<size_t>(blockIdx.y) * a.H + h] = (totals[0] + totals[1]) * kLn2;
     if (warp == 0) tmem_dealloc(*tmem_slot, 128);
 }
 
