@@ -182,8 +182,14 @@ struct ScanGrads {
 size_t ssm_simt_bwd_workspace(const ScanShape& sh);
 cudaError_t launch_ssm_simt_bwd(const ScanShape& sh, const ScanIn& in, const ScanGrads& gr, void* ws, cudaStream_t s);
 
-cudaError_t launch_ssm_chain(const ScanShape& sh, int unit, const float* first, float* last, float* states, const float* decay,
-                             int back, cudaStream_t s);
+// From units' increments to the states at their starts (back: the adjoints at their ends), one or two directions.
+struct ChainJob {
+    const float* first;   // state before the first unit, or null
+    float *last, *states; // state after the last unit, or null; increments, replaced
+    const float* decay;
+    int back;
+};
+cudaError_t launch_ssm_chain(const ScanShape& sh, int unit, const ChainJob* jobs, int n, cudaStream_t s);
 
 // dB and dC from the head shares and dD from the units' parts (ssm_scan.cu).
 cudaError_t launch_ssm_grad_sums(const ScanShape& sh, const ScanGrads& gr, const float* part, int splits, const float* dd_part, int units,

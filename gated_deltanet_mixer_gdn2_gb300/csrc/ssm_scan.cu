@@ -35,19 +35,33 @@ __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
 //   kForward        y, from the unit's starting state (units > 1 per sequence: `states`, else s0)
 //   kIncrement      the unit's state from zero into `states`, its total log-decay into `decay`
 //   kIncrementBack  the adjoint's: sum_i e^{g_1 + .. + g_i} C_i dy_i^T (bm = C, x = dy, no step)
+struct WalkArgs {
+    Seqs seqs;
+    int unit, use_states, H, G, P;
+    Rows x, b, c;
+    const void *step, *g;
+    const float *d, *s0;
+    float* s1;
+    void* y;
+    float *states, *decay;
+};
+
 template <typename T, int NPT, int kMode>
-__global__ void __launch_bounds__(kWalkThreads)
-    walk_kernel(Seqs seqs, int unit, Rows xr, Rows br, Rows cr, const T* __restrict__ step, const T* __restrict__ g,
-                const float* __restrict__ dskip, const float* s0, float* s1, T* __restrict__ y,
-                float* __restrict__ states, float* __restrict__ decay, int use_states, int H, int G, int P) {
+__device__ __forceinline__ void walk_block(const WalkArgs& a, int cols) {
+    const Rows xr = a.x, br = a.b, cr = a.c;
+    const T *__restrict__ step = static_cast<const T*>(a.step), *__restrict__ g = static_cast<const T*>(a.g);
+    T* __restrict__ y = static_cast<T*>(a.y);
+    const float *dskip = a.d, *s0 = a.s0;
+    float *s1 = a.s1, *states = a.states, *decay = a.decay;
+    const int H = a.H, G = a.G, P = a.P;
     constexpr int N = 4 * NPT;
     __shared__ float sB[kWalkTile][N], sC[kMode == kForward ? kWalkTile : 1][N], sX[kWalkTile][kWalkCols];
     __shared__ float sY[kMode == kForward ? kWalkTile : 1][4][kWalkCols], sS[kWalkTile];
     __shared__ float2 sA[kWalkTile];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int h = blockIdx.y, grp = h / (H / G), p = blockIdx.z * kWalkCols + lane;
+    const int h = blockIdx.y, grp = h / (H / G), p = cols * kWalkCols + lane;
     Unit u;
-    if (!find_unit(seqs, unit, blockIdx.x, u)) return;
+    if (!find_unit(a.seqs, a.unit, blockIdx.x, u)) return;
     const bool col = p < P;
     const size_t plane = static_cast<size_t>(N) * P;
     const size_t mine = static_cast<size_t>(warp * NPT) * P + (col ? p : 0);
@@ -56,7 +70,7 @@ __global__ void __launch_bounds__(kWalkThreads)
     {
         const float* from = nullptr;
         if (kMode == kForward)
-            from = use_states ? states + (static_cast<size_t>(blockIdx.x) * H + h) * plane
+            from = a.use_states ? states + (static_cast<size_t>(blockIdx.x) * H + h) * plane
                               : (s0 ? s0 + (static_cast<size_t>(u.seq) * H + h) * plane : nullptr);
 #pragma unroll
         for (int i = 0; i < NPT; ++i) st[i] = from && col ? from[mine + static_cast<size_t>(i) * P] : 0.f;
@@ -78,7 +92,7 @@ __global__ void __launch_bounds__(kWalkThreads)
         }
         for (int i = tid; i < n * kWalkCols; i += kWalkThreads) {
             const int t = i / kWalkCols, c = i - t * kWalkCols;
-            const int pc = blockIdx.z * kWalkCols + c;
+            const int pc = cols * kWalkCols + c;
             sX[t][c] = pc < P ? to_f32(xp[(row + t) * xr.ld + pc]) : 0.f;
         }
         if (tid < n) {
@@ -93,7 +107,7 @@ __global__ void __launch_bounds__(kWalkThreads)
         for (int q = 0; q < n; ++q) {
             const int t = kMode == kIncrementBack ? n - 1 - q : q;
             const float2 al = sA[t];
-            const float a = al.x, lo = al.y, x = kMode == kIncrementBack ? sX[t][lane] : sX[t][lane] * sS[t];
+            const float e = al.x, lo = al.y, x = kMode == kIncrementBack ? sX[t][lane] : sX[t][lane] * sS[t];
             float acc0 = 0.f, acc1 = 0.f;
 #pragma unroll
             for (int i = 0; i < NPT; i += 4) {
@@ -101,15 +115,15 @@ __global__ void __launch_bounds__(kWalkThreads)
                 if (kMode == kIncrementBack) {
                     const float u0 = fmaf(b.x, x, st[i]), u1 = fmaf(b.y, x, st[i + 1]);
                     const float u2 = fmaf(b.z, x, st[i + 2]), u3 = fmaf(b.w, x, st[i + 3]);
-                    st[i] = fmaf(a, u0, lo * u0);
-                    st[i + 1] = fmaf(a, u1, lo * u1);
-                    st[i + 2] = fmaf(a, u2, lo * u2);
-                    st[i + 3] = fmaf(a, u3, lo * u3);
+                    st[i] = fmaf(e, u0, lo * u0);
+                    st[i + 1] = fmaf(e, u1, lo * u1);
+                    st[i + 2] = fmaf(e, u2, lo * u2);
+                    st[i + 3] = fmaf(e, u3, lo * u3);
                 } else {
-                    st[i] = fmaf(a, st[i], fmaf(lo, st[i], b.x * x));
-                    st[i + 1] = fmaf(a, st[i + 1], fmaf(lo, st[i + 1], b.y * x));
-                    st[i + 2] = fmaf(a, st[i + 2], fmaf(lo, st[i + 2], b.z * x));
-                    st[i + 3] = fmaf(a, st[i + 3], fmaf(lo, st[i + 3], b.w * x));
+                    st[i] = fmaf(e, st[i], fmaf(lo, st[i], b.x * x));
+                    st[i + 1] = fmaf(e, st[i + 1], fmaf(lo, st[i + 1], b.y * x));
+                    st[i + 2] = fmaf(e, st[i + 2], fmaf(lo, st[i + 2], b.z * x));
+                    st[i + 3] = fmaf(e, st[i + 3], fmaf(lo, st[i + 3], b.w * x));
                 }
                 if (kMode == kForward) {
                     const float4 c = *reinterpret_cast<const float4*>(&sC[t][warp * NPT + i]);
@@ -124,7 +138,7 @@ __global__ void __launch_bounds__(kWalkThreads)
         if (kMode == kForward) {
             __syncthreads();
             for (int i = tid; i < n * kWalkCols; i += kWalkThreads) {
-                const int t = i / kWalkCols, c = i - t * kWalkCols, pc = blockIdx.z * kWalkCols + c;
+                const int t = i / kWalkCols, c = i - t * kWalkCols, pc = cols * kWalkCols + c;
                 const float v = (sY[t][0][c] + sY[t][1][c]) + (sY[t][2][c] + sY[t][3][c]);
                 if (pc < P) y[((row + t) * H + h) * P + pc] = from_f32<T>(fmaf(dk, sX[t][c], v));
             }
@@ -143,17 +157,33 @@ __global__ void __launch_bounds__(kWalkThreads)
 #pragma unroll
             for (int i = 0; i < NPT; ++i) to[mine + static_cast<size_t>(i) * P] = st[i];
         }
-        if (tid == 0 && blockIdx.z == 0) decay[static_cast<size_t>(blockIdx.x) * H + h] = gsum;
+        if (tid == 0 && cols == 0) decay[static_cast<size_t>(blockIdx.x) * H + h] = gsum;
     }
+}
+
+template <typename T, int NPT, int kMode>
+__global__ void __launch_bounds__(kWalkThreads) walk_kernel(WalkArgs a) {
+    walk_block<T, NPT, kMode>(a, blockIdx.z);
+}
+// Both directions' increments in one launch: the adjoint's beside the state's.
+template <typename T, int NPT>
+__global__ void __launch_bounds__(kWalkThreads) walk_pair_kernel(WalkArgs f, WalkArgs b) {
+    const int half = gridDim.z / 2;
+    if (blockIdx.z < half) walk_block<T, NPT, kIncrement>(f, blockIdx.z);
+    else walk_block<T, NPT, kIncrementBack>(b, blockIdx.z - half);
 }
 
 // From the units' increments to the states at their starts (back: the adjoints at their ends), in
 // place: four state elements per thread, eight units' loads in flight. Memory-bound: each increment is
-// read once and replaced once. `last`: the state after the final unit (back: before the first).
-__global__ void __launch_bounds__(256)
-    chain_kernel(Seqs seqs, int unit, const float* __restrict__ first, float* __restrict__ last,
-                 float* __restrict__ states, const float* __restrict__ decay, int H, int plane4, int back) {
-    const int e = blockIdx.x * blockDim.x + threadIdx.x, h = blockIdx.y, seq = blockIdx.z;
+// read once and replaced once. `last`: the state after the final unit (back: before the first). The two directions
+// of a gradient run in one launch.
+__global__ void __launch_bounds__(256) chain_kernel(Seqs seqs, int unit, ChainJob j0, ChainJob j1, int H, int plane4) {
+    const ChainJob& job = blockIdx.y < H ? j0 : j1;
+    const float* first = job.first;
+    float *last = job.last, *states = job.states;
+    const float* decay = job.decay;
+    const int back = job.back;
+    const int e = blockIdx.x * blockDim.x + threadIdx.x, h = blockIdx.y % H, seq = blockIdx.z;
     int start, len;
     const int base = units_before(seqs, unit, seq);
     seqs.span(seq, start, len);
@@ -246,17 +276,20 @@ __global__ void __launch_bounds__(kGradThreads)
         }
     }
     __syncthreads();
-    const int pi = tid >> 3, pj = (tid & 7) * 4;  // this thread's entries (pi, pj .. pj + 3) of the Q x Q matrices
+    // this thread's entries (pi, pj + 8 e) of the Q x Q matrices: neighbouring lanes read neighbouring rows of b and x, whose
+    // stride of 4 floats past a multiple of 32 keeps them in different banks
+    const int pi = tid >> 3, pj = tid & 7;
     float sc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int k = 0; k < N; k += 4) {
         const float4 c = *reinterpret_cast<const float4*>(&s.c[pi][k]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float4 b = *reinterpret_cast<const float4*>(&s.b[pj + e][k]);
+            const float4 b = *reinterpret_cast<const float4*>(&s.b[pj + 8 * e][k]);
             sc[e] += c.x * b.x + c.y * b.y + c.z * b.z + c.w * b.w;
         }
     }
-    // tiles of 4 tokens x 4 states of dB and dC
+    // tiles of 4 tokens x 4 states (n0 + N / 4 e) of dB and dC: lanes run over the states, so token rows are read once for
+    // all of them and the rows of H and A without bank conflicts (four neighbouring states per thread took 4 times as long)
     constexpr int kTiles = 8 * (N / 4), kPer = (kTiles + kGradThreads - 1) / kGradThreads;
     float ab[kPer][4][4] = {}, ac[kPer][4][4] = {};
 
@@ -306,14 +339,14 @@ __global__ void __launch_bounds__(kGradThreads)
                     const float4 a = *reinterpret_cast<const float4*>(&s.dy[pi][k]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float4 b = *reinterpret_cast<const float4*>(&s.x[pj + e][k]);
+                        const float4 b = *reinterpret_cast<const float4*>(&s.x[pj + 8 * e][k]);
                         r[e] += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
                     }
                 }
                 float rs = 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int j = pj + e;
+                    const int j = pj + 8 * e;
                     const float w = pi >= j ? expf(s.L[pi] - s.L[j]) : 0.f;
                     const float p1 = r[e] * w * s.stp[j], pf = pi > j ? sc[e] * p1 : 0.f;
                     s.p1[pi][j] = p1;
@@ -335,16 +368,27 @@ __global__ void __launch_bounds__(kGradThreads)
             for (int m = 0; m < kPer; ++m) {
                 const int tile = tid + m * kGradThreads;
                 if (kTiles % kGradThreads == 0 || tile < kTiles) {
-                    // lanes run over the state index, so token rows are read once for all of them
-                    const int n0 = 4 * (tile % (N / 4)), t0 = 4 * (tile / (N / 4));
-                    for (int j = 0; j < Q; ++j) {
-                        const float4 b = *reinterpret_cast<const float4*>(&s.b[j][n0]);
-                        const float4 c = *reinterpret_cast<const float4*>(&s.c[j][n0]);
+                    const int n0 = tile % (N / 4), t0 = 4 * (tile / (N / 4));
+                    for (int j = 0; j < t0 + 4; ++j) {  // p1 is lower triangular
+                        float b[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) b[e] = s.b[j][n0 + N / 4 * e];
 #pragma unroll
                         for (int t = 0; t < 4; ++t) {
-                            const float w = s.p1[t0 + t][j], z = s.p1[j][t0 + t];
-                            ac[m][t][0] += w * b.x; ac[m][t][1] += w * b.y; ac[m][t][2] += w * b.z; ac[m][t][3] += w * b.w;
-                            ab[m][t][0] += z * c.x; ab[m][t][1] += z * c.y; ab[m][t][2] += z * c.z; ab[m][t][3] += z * c.w;
+                            const float w = s.p1[t0 + t][j];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) ac[m][t][e] += w * b[e];
+                        }
+                    }
+                    for (int j = t0; j < Q; ++j) {
+                        float c[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) c[e] = s.c[j][n0 + N / 4 * e];
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            const float z = s.p1[j][t0 + t];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) ab[m][t][e] += z * c[e];
                         }
                     }
                     float xb[4][4] = {}, xc[4][4] = {};
@@ -352,8 +396,8 @@ __global__ void __launch_bounds__(kGradThreads)
                         float4 hh[4], dd[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            hh[e] = *reinterpret_cast<const float4*>(&s.h0[n0 + e][k]);
-                            dd[e] = *reinterpret_cast<const float4*>(&s.dh[n0 + e][k]);
+                            hh[e] = *reinterpret_cast<const float4*>(&s.h0[n0 + N / 4 * e][k]);
+                            dd[e] = *reinterpret_cast<const float4*>(&s.dh[n0 + N / 4 * e][k]);
                         }
 #pragma unroll
                         for (int t = 0; t < 4; ++t) {
@@ -378,33 +422,37 @@ __global__ void __launch_bounds__(kGradThreads)
                 }
             }
             // dx and the per-token sums over P: PB / 4 lanes per token
-            constexpr int kQuads = PB / 4, kRows = kGradThreads / kQuads;
+            constexpr int kQuads = PB / 4, kRows = kGradThreads / kQuads, kPerT = Q / kRows;
             const int pq = 4 * (tid % kQuads);
+            float a2[kPerT][4] = {}, a3[kPerT][4] = {};
+            for (int k = 0; k < N; ++k) {  // A and H are read once for all of a thread's tokens
+                const float4 d = *reinterpret_cast<const float4*>(&s.dh[k][pq]);
+                const float4 e = *reinterpret_cast<const float4*>(&s.h0[k][pq]);
 #pragma unroll
-            for (int m = 0; m < Q / kRows; ++m) {
+                for (int m = 0; m < kPerT; ++m) {
+                    const float bv = s.b[tid / kQuads + m * kRows][k], cv = s.c[tid / kQuads + m * kRows][k];
+                    a2[m][0] += bv * d.x; a2[m][1] += bv * d.y; a2[m][2] += bv * d.z; a2[m][3] += bv * d.w;
+                    a3[m][0] += cv * e.x; a3[m][1] += cv * e.y; a3[m][2] += cv * e.z; a3[m][3] += cv * e.w;
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < kPerT; ++m) {
                 const int j = tid / kQuads + m * kRows;
-                float a1[4] = {}, a2[4] = {}, a3[4] = {};
+                float a1[4] = {};
                 for (int i = j; i < Q; ++i) {
                     const float w = s.sw[i][j];
                     const float4 d = *reinterpret_cast<const float4*>(&s.dy[i][pq]);
                     a1[0] += w * d.x; a1[1] += w * d.y; a1[2] += w * d.z; a1[3] += w * d.w;
                 }
-                for (int k = 0; k < N; ++k) {
-                    const float bv = s.b[j][k], cv = s.c[j][k];
-                    const float4 d = *reinterpret_cast<const float4*>(&s.dh[k][pq]);
-                    const float4 e = *reinterpret_cast<const float4*>(&s.h0[k][pq]);
-                    a2[0] += bv * d.x; a2[1] += bv * d.y; a2[2] += bv * d.z; a2[3] += bv * d.w;
-                    a3[0] += cv * e.x; a3[1] += cv * e.y; a3[2] += cv * e.z; a3[3] += cv * e.w;
-                }
                 const float we = s.wend[j], sj = s.stp[j];
                 float du = 0.f, v = 0.f, q = 0.f, out[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float xv = s.x[j][pq + e], dv = s.dy[j][pq + e], U = a1[e] + we * a2[e];
+                    const float xv = s.x[j][pq + e], dv = s.dy[j][pq + e], U = a1[e] + we * a2[m][e];
                     out[e] = sj * U + dk * dv;
                     du += xv * U;
-                    v += xv * a2[e];
-                    q += dv * a3[e];
+                    v += xv * a2[m][e];
+                    q += dv * a3[m][e];
                     dd_acc += xv * dv;
                 }
                 if (j < n && pq < pw) {
@@ -463,7 +511,7 @@ __global__ void __launch_bounds__(kGradThreads)
     for (int m = 0; m < kPer; ++m) {
         const int tile = tid + m * kGradThreads;
         if (tile >= kTiles) continue;
-        const int n0 = 4 * (tile % (N / 4)), t0 = 4 * (tile / (N / 4));
+        const int n0 = tile % (N / 4), t0 = 4 * (tile / (N / 4));
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             if (t0 + t >= n) continue;
@@ -473,25 +521,42 @@ __global__ void __launch_bounds__(kGradThreads)
                 T* tc = static_cast<T*>(dcr.p) + r * dcr.ld + static_cast<size_t>(grp) * N + n0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    tb[e] = from_f32<T>(ab[m][t][e]);
-                    tc[e] = from_f32<T>(ac[m][t][e]);
+                    tb[N / 4 * e] = from_f32<T>(ab[m][t][e]);
+                    tc[N / 4 * e] = from_f32<T>(ac[m][t][e]);
                 }
             } else {
                 const size_t gn = static_cast<size_t>(G) * N, at = (static_cast<size_t>(split) * rows + r) * gn + static_cast<size_t>(grp) * N + n0;
-                *reinterpret_cast<float4*>(part + at) = make_float4(ab[m][t][0], ab[m][t][1], ab[m][t][2], ab[m][t][3]);
-                *reinterpret_cast<float4*>(part + static_cast<size_t>(splits) * rows * gn + at) =
-                    make_float4(ac[m][t][0], ac[m][t][1], ac[m][t][2], ac[m][t][3]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    part[at + N / 4 * e] = ab[m][t][e];
+                    part[static_cast<size_t>(splits) * rows * gn + at + N / 4 * e] = ac[m][t][e];
+                }
             }
         }
     }
 }
 
-// dB and dC: the sum of the head shares in a fixed order, then one rounding.
+// dB and dC: the sum of the head shares in a fixed order, then one rounding. dD, by the third row of blocks: the sum over the
+// units, one block per head, in a fixed order.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    share_sum_kernel(const float* __restrict__ part, RowsOut dbr, RowsOut dcr, long long rows, int gn, int splits) {
+    sums_kernel(const float* __restrict__ part, RowsOut dbr, RowsOut dcr, long long rows, int gn, int splits,
+                const float* __restrict__ dd_part, float* __restrict__ dd, int units, int H) {
+    if (blockIdx.y == 2) {
+        __shared__ float red[8];
+        const int h = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        if (!dd || h >= H) return;
+        float v = 0.f;
+        for (int k = threadIdx.x; k < units; k += 256) v += dd_part[static_cast<size_t>(k) * H + h];
+#pragma unroll
+        for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        if (lane == 0) red[warp] = v;
+        __syncthreads();
+        if (threadIdx.x == 0) dd[h] = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
+        return;
+    }
     const long long i = blockIdx.x * 256LL + threadIdx.x;
-    if (i >= rows * (gn / 4)) return;
+    if (splits <= 1 || i >= rows * (gn / 4)) return;
     const long long r = i / (gn / 4);
     const int c = 4 * static_cast<int>(i - r * (gn / 4));
     const float* src = part + (blockIdx.y ? static_cast<size_t>(splits) * rows * gn : 0);
@@ -503,19 +568,6 @@ __global__ void __launch_bounds__(256)
     const RowsOut o = blockIdx.y ? dcr : dbr;
     T* to = static_cast<T*>(o.p) + r * o.ld + c;
     to[0] = from_f32<T>(a.x); to[1] = from_f32<T>(a.y); to[2] = from_f32<T>(a.z); to[3] = from_f32<T>(a.w);
-}
-
-// dD: the sum over the units, one block per head, in a fixed order.
-__global__ void __launch_bounds__(256) dskip_kernel(const float* __restrict__ part, float* __restrict__ dd, int units, int H) {
-    __shared__ float red[8];
-    const int h = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float v = 0.f;
-    for (int k = threadIdx.x; k < units; k += 256) v += part[static_cast<size_t>(k) * H + h];
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    if (lane == 0) red[warp] = v;
-    __syncthreads();
-    if (threadIdx.x == 0) dd[h] = ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
 }
 
 int sm_count() {
@@ -542,48 +594,41 @@ size_t state_floats(const ScanShape& sh, int unit) {
     return static_cast<size_t>(sh.seqs.units(unit)) * sh.H * (static_cast<size_t>(sh.N) * sh.P + 4);
 }
 
+WalkArgs walk_args(const ScanShape& sh, int unit, Rows x, Rows b, Rows c, const ScanIn& in, float* states, float* decay) {
+    WalkArgs a{};
+    a.seqs = sh.seqs;
+    a.unit = unit;
+    a.H = sh.H; a.G = sh.G; a.P = sh.P;
+    a.x = x; a.b = b; a.c = c;
+    a.step = in.step; a.g = in.g;
+    a.states = states;
+    a.decay = decay;
+    return a;
+}
+
+// One walk, or with `b` the increments of both directions.
 template <typename T, int NPT>
-cudaError_t walk(const ScanShape& sh, int mode, int unit, Rows x, Rows b, Rows c, const void* step, const void* g,
-                 const float* d, const float* s0, float* s1, void* y, float* states, float* decay, int use_states,
-                 cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(sh.seqs.units(unit)), sh.H, (sh.P + kWalkCols - 1) / kWalkCols);
-    auto go = [&](auto kernel) {
-        kernel<<<grid, kWalkThreads, 0, s>>>(sh.seqs, unit, x, b, c, static_cast<const T*>(step), static_cast<const T*>(g),
-                                             d, s0, s1, static_cast<T*>(y), states, decay, use_states, sh.H, sh.G, sh.P);
-        return cudaGetLastError();
-    };
-    if (mode == kForward) return go(walk_kernel<T, NPT, kForward>);
-    if (mode == kIncrement) return go(walk_kernel<T, NPT, kIncrement>);
-    return go(walk_kernel<T, NPT, kIncrementBack>);
+cudaError_t walk(const ScanShape& sh, int mode, const WalkArgs& a, const WalkArgs* b, cudaStream_t s) {
+    const unsigned units = static_cast<unsigned>(sh.seqs.units(a.unit)), cols = (sh.P + kWalkCols - 1) / kWalkCols;
+    if (b) walk_pair_kernel<T, NPT><<<dim3(units, sh.H, 2 * cols), kWalkThreads, 0, s>>>(a, *b);
+    else if (mode == kForward) walk_kernel<T, NPT, kForward><<<dim3(units, sh.H, cols), kWalkThreads, 0, s>>>(a);
+    else walk_kernel<T, NPT, kIncrement><<<dim3(units, sh.H, cols), kWalkThreads, 0, s>>>(a);
+    return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t walk_n(const ScanShape& sh, int mode, int unit, Rows x, Rows b, Rows c, const void* step, const void* g,
-                   const float* d, const float* s0, float* s1, void* y, float* states, float* decay, int use_states,
-                   cudaStream_t s) {
+cudaError_t walk_n(const ScanShape& sh, int mode, const WalkArgs& a, const WalkArgs* b, cudaStream_t s) {
     switch (sh.N) {
-        case 16: return walk<T, 4>(sh, mode, unit, x, b, c, step, g, d, s0, s1, y, states, decay, use_states, s);
-        case 32: return walk<T, 8>(sh, mode, unit, x, b, c, step, g, d, s0, s1, y, states, decay, use_states, s);
-        case 64: return walk<T, 16>(sh, mode, unit, x, b, c, step, g, d, s0, s1, y, states, decay, use_states, s);
-        case 128: return walk<T, 32>(sh, mode, unit, x, b, c, step, g, d, s0, s1, y, states, decay, use_states, s);
-        default: return walk<T, 64>(sh, mode, unit, x, b, c, step, g, d, s0, s1, y, states, decay, use_states, s);
+        case 16: return walk<T, 4>(sh, mode, a, b, s);
+        case 32: return walk<T, 8>(sh, mode, a, b, s);
+        case 64: return walk<T, 16>(sh, mode, a, b, s);
+        case 128: return walk<T, 32>(sh, mode, a, b, s);
+        default: return walk<T, 64>(sh, mode, a, b, s);
     }
 }
 
-cudaError_t walk_any(const ScanShape& sh, int mode, int unit, Rows x, Rows b, Rows c, const void* step, const void* g,
-                     const float* d, const float* s0, float* s1, void* y, float* states, float* decay, int use_states,
-                     cudaStream_t s) {
-    if (sh.dt == GDN2_BF16)
-        return walk_n<__nv_bfloat16>(sh, mode, unit, x, b, c, step, g, d, s0, s1, y, states, decay, use_states, s);
-    return walk_n<float>(sh, mode, unit, x, b, c, step, g, d, s0, s1, y, states, decay, use_states, s);
-}
-
-cudaError_t chain(const ScanShape& sh, int unit, const float* first, float* last, float* states, const float* decay,
-                  int back, cudaStream_t s) {
-    const int plane4 = sh.N * sh.P / 4;
-    chain_kernel<<<dim3((plane4 + 255) / 256, sh.H, sh.seqs.B), 256, 0, s>>>(sh.seqs, unit, first, last, states, decay,
-                                                                            sh.H, plane4, back);
-    return cudaGetLastError();
+cudaError_t walk_any(const ScanShape& sh, int mode, const WalkArgs& a, const WalkArgs* b, cudaStream_t s) {
+    return sh.dt == GDN2_BF16 ? walk_n<__nv_bfloat16>(sh, mode, a, b, s) : walk_n<float>(sh, mode, a, b, s);
 }
 
 // Heads per block of the gradient kernel: all of a group while that alone gives two blocks per SM.
@@ -641,23 +686,20 @@ cudaError_t grad_n(const ScanShape& sh, const ScanIn& in, const ScanGrads& gr, f
 
 }  // namespace
 
-cudaError_t launch_ssm_chain(const ScanShape& sh, int unit, const float* first, float* last, float* states, const float* decay,
-                             int back, cudaStream_t s) {
-    return chain(sh, unit, first, last, states, decay, back, s);
+cudaError_t launch_ssm_chain(const ScanShape& sh, int unit, const ChainJob* jobs, int n, cudaStream_t s) {
+    const int plane4 = sh.N * sh.P / 4;
+    chain_kernel<<<dim3((plane4 + 255) / 256, n * sh.H, sh.seqs.B), 256, 0, s>>>(sh.seqs, unit, jobs[0], jobs[n - 1], sh.H, plane4);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_ssm_grad_sums(const ScanShape& sh, const ScanGrads& gr, const float* part, int splits, const float* dd_part, int units,
                                  cudaStream_t s) {
-    cudaError_t e;
-    if (splits > 1) {
-        const long long rows = sh.seqs.rows(), n = rows * (sh.G * sh.N / 4);
-        const dim3 grid(static_cast<unsigned>((n + 255) / 256), 2);
-        if (sh.dt == GDN2_BF16) share_sum_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(part, gr.dbm, gr.dcm, rows, sh.G * sh.N, splits);
-        else share_sum_kernel<float><<<grid, 256, 0, s>>>(part, gr.dbm, gr.dcm, rows, sh.G * sh.N, splits);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    if (!gr.dd) return cudaSuccess;
-    dskip_kernel<<<sh.H, 256, 0, s>>>(dd_part, gr.dd, units, sh.H);
+    if (splits <= 1 && !gr.dd) return cudaSuccess;
+    const long long rows = sh.seqs.rows(), n = splits > 1 ? (rows * (sh.G * sh.N / 4) + 255) / 256 : 0;
+    const dim3 grid(static_cast<unsigned>(n > sh.H ? n : sh.H), 3);
+    auto go = [&](auto kernel) { kernel<<<grid, 256, 0, s>>>(part, gr.dbm, gr.dcm, rows, sh.G * sh.N, splits, dd_part, gr.dd, units, sh.H); };
+    if (sh.dt == GDN2_BF16) go(sums_kernel<__nv_bfloat16>);
+    else go(sums_kernel<float>);
     return cudaGetLastError();
 }
 
@@ -672,12 +714,18 @@ cudaError_t launch_ssm_simt_fwd(const ScanShape& sh, const ScanIn& in, void* y, 
     float* states = static_cast<float*>(ws);
     float* decay = cut ? states + static_cast<size_t>(sh.seqs.units(unit)) * sh.H * sh.N * sh.P : nullptr;
     cudaError_t e;
+    WalkArgs a = walk_args(sh, unit, in.x, in.bm, in.cm, in, states, decay);
     if (cut) {
-        e = walk_any(sh, kIncrement, unit, in.x, in.bm, in.cm, in.step, in.g, nullptr, nullptr, nullptr, nullptr, states, decay, 0, s);
-        if (e != cudaSuccess) return e;
-        if ((e = chain(sh, unit, in.s0, nullptr, states, decay, 0, s)) != cudaSuccess) return e;
+        if ((e = walk_any(sh, kIncrement, a, nullptr, s)) != cudaSuccess) return e;
+        const ChainJob job{in.s0, nullptr, states, decay, 0};
+        if ((e = launch_ssm_chain(sh, unit, &job, 1, s)) != cudaSuccess) return e;
     }
-    return walk_any(sh, kForward, unit, in.x, in.bm, in.cm, in.step, in.g, in.d, in.s0, s1, y, states, decay, cut, s);
+    a.use_states = cut;
+    a.d = in.d;
+    a.s0 = in.s0;
+    a.s1 = s1;
+    a.y = y;
+    return walk_any(sh, kForward, a, nullptr, s);
 }
 
 size_t ssm_simt_bwd_workspace(const ScanShape& sh) { return align_up(sizeof(float) * bwd_ws(sh).total, 256); }
@@ -685,14 +733,12 @@ size_t ssm_simt_bwd_workspace(const ScanShape& sh) { return align_up(sizeof(floa
 cudaError_t launch_ssm_simt_bwd(const ScanShape& sh, const ScanIn& in, const ScanGrads& gr, void* wsv, cudaStream_t s) {
     float* ws = static_cast<float*>(wsv);
     const BwdWs w = bwd_ws(sh);
-    cudaError_t e = walk_any(sh, kIncrement, kGradUnit, in.x, in.bm, in.cm, in.step, in.g, nullptr, nullptr, nullptr, nullptr,
-                             ws + w.h0, ws + w.decay, 0, s);
+    const WalkArgs fwd = walk_args(sh, kGradUnit, in.x, in.bm, in.cm, in, ws + w.h0, ws + w.decay);
+    const WalkArgs bwd = walk_args(sh, kGradUnit, gr.dy, in.cm, in.cm, in, ws + w.dh, ws + w.decay_b);
+    cudaError_t e = walk_any(sh, kIncrement, fwd, &bwd, s);
     if (e != cudaSuccess) return e;
-    e = walk_any(sh, kIncrementBack, kGradUnit, gr.dy, in.cm, in.cm, in.step, in.g, nullptr, nullptr, nullptr, nullptr,
-                 ws + w.dh, ws + w.decay_b, 0, s);
-    if (e != cudaSuccess) return e;
-    if ((e = chain(sh, kGradUnit, in.s0, nullptr, ws + w.h0, ws + w.decay, 0, s)) != cudaSuccess) return e;
-    if ((e = chain(sh, kGradUnit, gr.ds1, gr.ds0, ws + w.dh, ws + w.decay_b, 1, s)) != cudaSuccess) return e;
+    const ChainJob jobs[2] = {{in.s0, nullptr, ws + w.h0, ws + w.decay, 0}, {gr.ds1, gr.ds0, ws + w.dh, ws + w.decay_b, 1}};
+    if ((e = launch_ssm_chain(sh, kGradUnit, jobs, 2, s)) != cudaSuccess) return e;
     e = sh.dt == GDN2_BF16 ? grad_n<__nv_bfloat16>(sh, in, gr, ws, w, s) : grad_n<float>(sh, in, gr, ws, w, s);
     if (e != cudaSuccess) return e;
     return launch_ssm_grad_sums(sh, gr, ws + w.part, w.splits, ws + w.dd, static_cast<int>(sh.seqs.units(kGradUnit)), s);

@@ -531,7 +531,8 @@ cudaError_t launch_ssm_tc_fwd(const ScanShape& sh, const ScanIn& in, void* y, fl
         const WalkJob job{in.bm, in.x, in.s0, nullptr, a.states, a.decay, nullptr, 0};
         cudaError_t e = launch_ssm_walk_tc(sh, in.step, in.g, &job, 1, a.unit, 1, 0, s1 != nullptr, s, wait_ns);
         if (e != cudaSuccess) return e;
-        if ((e = launch_ssm_chain(sh, a.unit, in.s0, s1, a.states, a.decay, 0, s)) != cudaSuccess) return e;
+        const ChainJob chain{in.s0, s1, a.states, a.decay, 0};
+        if ((e = launch_ssm_chain(sh, a.unit, &chain, 1, s)) != cudaSuccess) return e;
     }
     return a.s1 ? launch_scan<3>(maps, a, grid, s) : launch_scan<1>(maps, a, grid, s);
 }

@@ -675,8 +675,8 @@ cudaError_t launch_ssm_tc_bwd(const ScanShape& sh, const ScanIn& in, const ScanG
     const int exact = gr.ds0 != nullptr;
     if (p.cut) {
         if ((e = launch_ssm_walk_tc(sh, in.step, in.g, jobs, 2, p.unit, 1, 0, exact, s, wait_ns)) != cudaSuccess) return e;
-        if ((e = launch_ssm_chain(sh, p.unit, in.s0, nullptr, f(p.states), f(p.decay), 0, s)) != cudaSuccess) return e;
-        if ((e = launch_ssm_chain(sh, p.unit, gr.ds1, gr.ds0, f(p.states_b), f(p.decay_b), 1, s)) != cudaSuccess) return e;
+        const ChainJob chains[2] = {{in.s0, nullptr, f(p.states), f(p.decay), 0}, {gr.ds1, gr.ds0, f(p.states_b), f(p.decay_b), 1}};
+        if ((e = launch_ssm_chain(sh, p.unit, chains, 2, s)) != cudaSuccess) return e;
         WalkJob again[2] = {jobs[0], jobs[1]};
         again[1].last = nullptr;  // the chain has written it
         e = launch_ssm_walk_tc(sh, in.step, in.g, again, 2, p.unit, 0, 1, 0, s, wait_ns);
