@@ -36,8 +36,8 @@ constexpr uint32_t TOTAL = BAR + 256;
 static_assert(sg::TOTAL + 1024 <= 232448, "gradient kernel shared memory");
 
 enum GradBar {
-    gBc = 0, gXy = 1, gXyDone = 3, gXyFree = 5, gGate = 7, gGateFree = 9, gHd = 11, gHdFree, gS, gSRead, gR, gTu, gPReady, gUScaled,
-    gDx, gURead, gAll, gSumFree, gOut, gDrain = gOut + 2, gBars
+    gBc = 0, gXy = 1, gXyDone = 3, gXyFree = 5, gGate = 7, gGateFree = 9, gHd = 11, gHdFree, gS, gSRead, gR, gTu, gPReady, gDx,
+    gURead, gTrFree, gAll, gSumFree, gOut, gDrain = gOut + 2, gBars
 };
 static_assert(gBars * 8 + 16 <= 256, "barrier room");
 
@@ -62,10 +62,10 @@ struct GradTcArgs {
     long long wait_ns;
 };
 
-// Sum over the warp's lanes of each of 16 values: lane l returns the sum of v[l mod 16]. Each step halves the values.
-__device__ __forceinline__ float transpose_sum(float (&v)[16], int lane) {
+// Sum over the warp's lanes of each of 32 values: lane l returns the sum of v[l]. Each step halves the values.
+__device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
 #pragma unroll
-    for (int d = 8; d; d >>= 1) {
+    for (int d = 16; d; d >>= 1) {
         const bool up = lane & d;
 #pragma unroll
         for (int k = 0; k < d; ++k) {
@@ -73,7 +73,7 @@ __device__ __forceinline__ float transpose_sum(float (&v)[16], int lane) {
             v[k] = keep + __shfl_xor_sync(0xffffffffu, give, d);
         }
     }
-    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+    return v[0];
 }
 
 __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ GradTcArgs a) {
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
 
     if (tid == 0) {
         for (int i = 0; i < gBars; ++i)
-            mbar_init(bars + i, i == gSRead || i == gPReady || i == gUScaled || i == gURead || i == gOut || i == gOut + 1 ? 16
+            mbar_init(bars + i, i == gSRead || i == gPReady || i == gURead || i == gOut || i == gOut + 1 ? 16
                                 : i == gGateFree || i == gGateFree + 1 || i == gHdFree ? 17 : 1);
         *err = 0;
         fence_mbar_init();
@@ -150,23 +150,21 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
             float cols = 0.f;
             uint8_t* p1t = sm + sg::P1 + (b >> 1) * kTileBytes + j * 128;
             const float dk = a.d ? __ldg(a.d + h) : 0.f;
-            float* rs = sums + 128 * q + 32 * b + (lane & 15);  // row sums of tokens i, over this warp's rows
-            float rsum[2] = {0.f, 0.f};
+            float rsum = 0.f;  // of token i = 32 b + lane, over this warp's rows
+            uint32_t m1[2][8] = {};
             if (b < q) {  // every i of the block lies before every j
-                const uint32_t z[8] = {};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_st8(pair + 8 * k, z);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(p1t + (((4 * (b & 1) + k) ^ (j & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                for (int k = 0; k < 4; ++k) tmem_st8(pair + 8 * k, m1[0]);
             } else {
                 const bool off = b > q;
                 // Off the diagonal block the decay factors through the start of the column's block, both factors <= 1:
                 // an exponential per row and block. On it, an exponential per entry.
                 const float rf = off ? ex2_approx(arr[32 * b - 1] - Lj) : 1.f;
+                float pf[32];
 #pragma unroll
                 for (int sub = 0; sub < 2; ++sub) {
-                    float x[16], pf[16];
-                    uint32_t m1[8], m2[8];
+                    float x[16];
+                    uint32_t m2[8];
                     tmem_ld_cols<1>(pair + 16 * sub, x);
                     if (off) {
                         const uint64_t rf2 = f32x2(rf, rf), sj2 = f32x2(sj, sj);
@@ -181,8 +179,8 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
                                 const uint64_t w = mul_f32x2(rf2, fv[e]), S = bf16x2_widen(sp[sub][k]);
                                 const uint64_t p1 = mul_f32x2(f32x2(x[2 * k], x[2 * k + 1]), mul_f32x2(w, sj2)), pp = mul_f32x2(S, p1);
                                 c2 = add_f32x2(c2, pp);
-                                f32x2_split(pp, pf[2 * k], pf[2 * k + 1]);
-                                m1[k] = bf16x2_narrow(p1);
+                                f32x2_split(pp, pf[16 * sub + 2 * k], pf[16 * sub + 2 * k + 1]);
+                                m1[sub][k] = bf16x2_narrow(p1);
                                 m2[k] = bf16x2_narrow(mul_f32x2(S, w));
                             }
                         }
@@ -197,20 +195,25 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
                             const float w0 = i0 >= lane ? ex2_approx(f.x - Lj) : 0.f, w1 = i0 + 1 >= lane ? ex2_approx(f.y - Lj) : 0.f;
                             const float S0 = __uint_as_float(sp[sub][k] << 16), S1 = __uint_as_float(sp[sub][k] & 0xffff0000u);
                             const float p0 = x[2 * k] * (w0 * sj), p1 = x[2 * k + 1] * (w1 * sj);
-                            pf[2 * k] = i0 > lane ? S0 * p0 : 0.f;
-                            pf[2 * k + 1] = i0 + 1 > lane ? S1 * p1 : 0.f;
-                            cols += pf[2 * k] + pf[2 * k + 1];
-                            m1[k] = pack_bf16x2(p0, p1);
+                            pf[i0] = i0 > lane ? S0 * p0 : 0.f;
+                            pf[i0 + 1] = i0 + 1 > lane ? S1 * p1 : 0.f;
+                            cols += pf[i0] + pf[i0 + 1];
+                            m1[sub][k] = pack_bf16x2(p0, p1);
                             m2[k] = pack_bf16x2(S0 * w0, S1 * w1);
                         }
                     }
-                    tmem_st8(pair + 16 * sub, m1);
+                    tmem_st8(pair + 16 * sub, m1[sub]);
                     tmem_st8(pair + 16 * sub + 8, m2);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        *reinterpret_cast<uint4*>(p1t + (((4 * (b & 1) + 2 * sub + k) ^ (j & 7)) << 4)) = make_uint4(m1[4 * k], m1[4 * k + 1], m1[4 * k + 2], m1[4 * k + 3]);
-                    rsum[sub] = transpose_sum(pf, lane);
                 }
+                rsum = transpose_sum(pf, lane);
+            }
+            // the products of the head before have read (R W s) and e^L dY
+            if (it && !(ok = wait_bar(bars + gAll, ph1 ^ 1, lim, err))) break;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t(&m)[8] = m1[k >> 1];
+                const int e = 4 * (k & 1);
+                *reinterpret_cast<uint4*>(p1t + (((4 * (b & 1) + k) ^ (j & 7)) << 4)) = make_uint4(m[e], m[e + 1], m[e + 2], m[e + 3]);
             }
             // the thread's part of the head's sums of token j: column sums, v, q, du
             auto keep = [&](int which, float v) {
@@ -220,9 +223,8 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
             // the sums of the head before have been used
             if (fresh && it && !(ok = wait_bar(bars + gSumFree, ((it / pbs) & 1) ^ 1, lim, err))) break;
             {
-                float* to = rs + (lane & 16);
-                const float v = lane < 16 ? rsum[0] : rsum[1];
-                *to = fresh ? v : *to + v;
+                float* to = sums + 128 * q + 32 * b + lane;
+                *to = fresh ? rsum : *to + rsum;
             }
             keep(1, cols);
             // X~ in place of X, e^{L} dY beside dY
@@ -243,26 +245,6 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
                 for (int e = 0; e < 8; ++e) v[e] *= eLj;
                 *reinterpret_cast<uint4*>(wt + cell) = pack8(v);
             }
-            fence_proxy_async_smem();
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive1(bars + gPReady);
-            if (!(ok = wait_bar(bars + gHd, ph1, lim, err))) break;
-            if (j < a.N) {
-                const uint8_t *ht = sm + sg::H0 + j * 128, *dt = sm + sg::DH + j * 128;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int cell = k ? cell1 : cell0;
-                    float v[8], w[8];
-                    unpack8(*reinterpret_cast<const uint4*>(ht + cell), v);
-                    unpack8(*reinterpret_cast<const uint4*>(dt + cell), w);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) e_acc = fmaf(v[e], w[e], e_acc);
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive1(bars + gHdFree);
             if (!(ok = wait_bar(bars + gTu, ph1, lim, err))) break;
             tc_fence_after();
             {
@@ -288,11 +270,27 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
                 tmem_st16(val + kTU, t);
                 keep(2, vs * wx);
                 keep(3, qs * eLj);
-                tmem_st_wait();
             }
+            fence_proxy_async_smem();
+            tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive1(bars + gUScaled);
+            if (lane == 0) mbar_arrive1(bars + gPReady);
+            if (!(ok = wait_bar(bars + gHd, ph1, lim, err))) break;
+            if (j < a.N) {
+                const uint8_t *ht = sm + sg::H0 + j * 128, *dt = sm + sg::DH + j * 128;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int cell = k ? cell1 : cell0;
+                    float v[8], w[8];
+                    unpack8(*reinterpret_cast<const uint4*>(ht + cell), v);
+                    unpack8(*reinterpret_cast<const uint4*>(dt + cell), w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) e_acc = fmaf(v[e], w[e], e_acc);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(bars + gHdFree);
             if (!(ok = wait_bar(bars + gDx, ph1, lim, err))) break;
             tc_fence_after();
             {
@@ -465,25 +463,32 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
             mma_steps<false, kStepK, kStepK, kJumpK, kJumpK>(lead, kTR, dk + (sg::B >> 4), dk + (sg::C >> 4), id_kk, 0, ks);
             commit_by(lead, bars + gS);
         }
+        auto pairs = [&](int it) {  // R^T = X dY^T
+            const int st = it & 1;
+            const uint32_t ph = (it >> 1) & 1, xo = (sg::X + st * kTileBytes) >> 4, yo = (sg::DY + st * kTileBytes) >> 4;
+            if (!(wait(gXy + st, ph) && (!tail || wait(gGate + st, ph)))) return false;
+            mma_steps<false, kStepK, kStepK, 0, 0>(lead, kTR, dk + xo, dk + yo, id_kk, 0, 4);
+            commit_by(lead, bars + gR);
+            return true;
+        };
+        ok = ok && wait(gSRead, 0) && pairs(0);
         for (int it = 0; ok && it < NI; ++it) {
             const int st = it & 1;
-            const uint32_t ph = (it >> 1) & 1, ph1 = it & 1;
-            const uint32_t xo = (sg::X + st * kTileBytes) >> 4, yo = (sg::DY + st * kTileBytes) >> 4;
-            if (!(ok = wait(gXy + st, ph) && (!tail || wait(gGate + st, ph)) && (it ? wait(gAll, ph1 ^ 1) : wait(gSRead, 0)))) break;
-            mma_steps<false, kStepK, kStepK, 0, 0>(lead, kTR, dk + xo, dk + yo, id_kk, 0, 4);  // R^T = X dY^T
-            commit_by(lead, bars + gR);
+            const uint32_t ph1 = it & 1, xo = (sg::X + st * kTileBytes) >> 4, yo = (sg::DY + st * kTileBytes) >> 4;
             if (!(ok = wait(gHd, ph1) && (it == 0 || wait(gURead, ph1 ^ 1)))) break;
             // C H and B A
             mma_steps<false, kStepK, kStepMn, kJumpK, 0>(lead, kTT, dk + (sg::C >> 4), dm + (sg::H0 >> 4), id_t, 0, ks);
             mma_steps<false, kStepK, kStepMn, kJumpK, 0>(lead, kTU, dk + (sg::B >> 4), dm + (sg::DH >> 4), id_t, 0, ks);
             commit_by(lead, bars + gTu);
             if (!(ok = wait(gPReady, ph1))) break;
-            // dB += (R W s)^T C + X~ A^T
+            // what the block waits for first: U += (S W)^T dY; then dB += (R W s)^T C + X~ A^T, the last reader of the pair
+            // matrices' room, which the next head's R^T takes; dC last, beside the next head's pair matrices
+            mma_steps<true, 16, kStepMn, 0, 0>(lead, kTU, kTR + 8, dm + yo, id_t, 1, 8);
+            commit_by(lead, bars + gDx);
             mma_steps<true, 16, kStepMn, 0, 0>(lead, kTdB, kTR, dm + (sg::C >> 4), id_nm, it > 0, 8);
             mma_steps<false, kStepK, kStepK, 0, 0>(lead, kTdB, dk + xo, dk + (sg::DH >> 4), id_nk, 1, 4);
-            if (!(ok = wait(gUScaled, ph1))) break;
-            mma_steps<true, 16, kStepMn, 0, 0>(lead, kTU, kTR + 8, dm + yo, id_t, 1, 8);  // U += (S W)^T dY
-            commit_by(lead, bars + gDx);
+            commit_by(lead, bars + gTrFree);
+            if (it + 1 < NI && !(ok = wait(gTrFree, ph1) && pairs(it + 1))) break;
             // dC += (R W s) B + (e^L dY) H^T
             mma_steps<false, kStepMn, kStepMn, 0, 0>(lead, kTdC, dm + (sg::P1 >> 4), dm + (sg::B >> 4), id_mm, it > 0, 8);
             mma_steps<false, kStepK, kStepK, 0, 0>(lead, kTdC, dk + (sg::DYW >> 4), dk + (sg::H0 >> 4), id_nk, 1, 4);
