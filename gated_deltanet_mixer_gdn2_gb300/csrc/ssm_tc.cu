@@ -35,7 +35,7 @@ struct So {
 
 enum Bar {
     kFullB = 0, kFullC = 2, kFullX = 4, kReady = 7, kXEmpty = 10, kSFull = 13, kDFull = 15, kXwReady = 17, kMReady, kYFull = kMReady + 2, kYEmpty,
-    kYOut, kDrain = kYOut + 4, kBars
+    kCFree, kYOut = kCFree + 2, kDrain = kYOut + 4, kBars
 };
 constexpr uint32_t kBarBytes = 8 * kBars + 16;
 static_assert(kBarBytes <= 320, "barrier room");
@@ -142,11 +142,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             prefetch_tensormap(&maps.x);
             int nb = 0, nc = 0, nx = 0;
             uint64_t t0 = globaltimer_ns();
-            // the increment of chunk c follows the last other product of B and C of that chunk
-            auto used = [&](int c) { return mbar_test_wait(bars + kDFull + (c & 1), (c >> 1) & 1); };
+            // C is free after the state's readout, B after its increment
+            auto used = [&](int bar, int c) { return mbar_test_wait(bars + bar + (c & 1), (c >> 1) & 1); };
             while (nb < NC || nc < NC || nx < NC) {
                 bool any = false;
-                if (nb < NC && (nb < 2 || used(nb - 2))) {
+                if (nb < NC && (nb < 2 || used(kDFull, nb - 2))) {
                     const int st = nb & 1;
                     mbar_arrive_expect_tx(bars + kFullB + st, so::kTile * halves);
                     for (int k = 0; k < halves; ++k)
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                     ++nb;
                     any = true;
                 }
-                if (nc < NC && (nc < so::kCS || used(nc - so::kCS))) {
+                if (nc < NC && (nc < so::kCS || used(kCFree, nc - so::kCS))) {
                     const int st = nc % so::kCS;
                     mbar_arrive_expect_tx(bars + kFullC + st, so::kTile * halves);
                     for (int k = 0; k < halves; ++k)
@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 // readout of the state, then its increment
                 mma_steps<false, kStepK, kStepMn, kJumpK, 0>(lead, kTYx + 64 * (c & 1), dk + ((so::C + 2 * (c % so::kCS) * so::kTile) >> 4),
                                                              dm + (so::HB >> 4), id_x, 0, ks);
+                commit_by(lead, bars + kCFree + (c & 1));
 #pragma unroll 1
                 for (int k = 0; k < kParts; ++k)
                     mma_steps<false, kStepMn, kStepMn, 0, 0>(lead, kTD, dm + ((so::B + 2 * (c & 1) * so::kTile) >> 4),
