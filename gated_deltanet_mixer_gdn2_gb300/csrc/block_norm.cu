@@ -253,7 +253,9 @@ struct NormGradArgs {
 //     dr = d_r + (k - nh mean(k nh)) / rms(r),    k = d_n pre
 //     dt = (q - th mean_group(q th)) / rms_group(t), q = dr scale post
 // dx = dt silu(z), dz = dt x silu'(z). dpost and dscale are one sum over the rows, of dr th, times scale and post; it and
-// dpre's, and the weights, stay in registers over the block's rows, the next row's loads in flight.
+// dpre's, and the weights, stay in registers over the block's rows, the next row's loads in flight. 8192 x 2048 bf16 with
+// all of its inputs: 68 us, 4 TB/s, 58% of the copy rate: the sums' registers leave room for 16 warps, and two row sums
+// with their barriers stand between a row's loads and its stores.
 template <typename T, int VPT, int kMaxThreads, int kPerSm>
 __global__ void __launch_bounds__(kMaxThreads, kPerSm)
     norm_grad_kernel(NormGradArgs ga, const T* x, const T* z, const T* residual, const T* d_r, const T* d_n, T* dx, T* dz, T* dres) {

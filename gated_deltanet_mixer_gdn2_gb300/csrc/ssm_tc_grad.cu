@@ -9,8 +9,14 @@
 // over R^T in tensor memory as operands; dB and dC accumulate there over the block's heads, so the sum over a
 // group's heads costs nothing. The double sum of dg is a suffix sum of (row sums - column sums) of one fp32
 // matrix: what cancels in it cancels exactly.
-// The products of one (chunk, head) take about 2600 tensor-core cycles at these shapes and bound the kernel
-// together with shared-memory bandwidth.
+// Roundings: the pair matrices, e^L dY, X~ and the saved states are bf16 operands, once each, of products whose sums are
+// fp32; row and column sums, dstep's and dg's sums and dD are fp32 throughout.
+// 4 x 2048 tokens, 32 heads of 64 values, N = 128: 96 us of a call's 145 (walk 41, sums 7). A head of a chunk takes about
+// 10500 cycles: the pair matrices, 4500 (a third of it the sums across lanes), the state's shares 1800, U 800, dx 2200, each
+// waiting for the one before; its 48 products take 3500 of them to issue, beside the rest. What limits overlapping two
+// heads is tensor memory: dB, dC and one pair matrix take three quarters of it.
+#include <cuda_fp16.h>
+
 #include "ssm_tc.cuh"
 
 namespace gdn2 {
@@ -121,20 +127,30 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
         const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16, pair = lane_base + kTR + 32 * b, val = lane_base + 16 * b;
         float* const sums = reinterpret_cast<float*>(sm + sg::SUM);
         bool ok = wait_bar(bars + gS, 0, lim, err);
-        uint32_t sp[2][8];  // this row and block of S^T, bf16 pairs: kept over the heads
+        // This row and block of S^T, kept over the heads in the registers that bf16 would take: fp16 under a power of two
+        // that brings its largest entry to 2^14 .. 2^15, so entries down to 2^-29 of that keep 11 bits. It goes into
+        // dstep and dg; as bf16 (8 bits) dstep was off by 2.8e-3 of its norm instead of 2.4e-3, for 2 us less of 96.
+        uint32_t sp[2][8];
+        float unscale = 1.f;
         if (ok) {
             tc_fence_after();
+            float x[32], top = 0.f;
+            tmem_ld_cols<2>(pair, x);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float x[16];
-                tmem_ld_cols<1>(pair + 16 * k, x);
+            for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(x[e]));
+            const int ex = max(static_cast<int>(__float_as_uint(top) >> 23), 15);
+            const float scale = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
+            unscale = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sp[k][e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+            for (int e = 0; e < 16; ++e) {
+                const __half2 v = __floats2half2_rn(x[2 * e] * scale, x[2 * e + 1] * scale);
+                sp[e >> 3][e & 7] = *reinterpret_cast<const uint32_t*>(&v);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive1(bars + gSRead);
         }
+        auto score = [&](uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); };
         float e_acc = 0.f, dd_acc = 0.f;
         int pi = 0, h = h_lo;
         for (int it = 0; ok && it < NI; ++it) {
@@ -167,7 +183,7 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
                     uint32_t m2[8];
                     tmem_ld_cols<1>(pair + 16 * sub, x);
                     if (off) {
-                        const uint64_t rf2 = f32x2(rf, rf), sj2 = f32x2(sj, sj);
+                        const uint64_t rf2 = f32x2(rf, rf), sj2 = f32x2(sj, sj), un2 = f32x2(unscale, unscale);
                         uint64_t c2 = 0;
 #pragma unroll
                         for (int k4 = 0; k4 < 4; ++k4) {
@@ -176,7 +192,8 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const int k = 2 * k4 + e;
-                                const uint64_t w = mul_f32x2(rf2, fv[e]), S = bf16x2_widen(sp[sub][k]);
+                                const float2 s2 = score(sp[sub][k]);
+                                const uint64_t w = mul_f32x2(rf2, fv[e]), S = mul_f32x2(f32x2(s2.x, s2.y), un2);
                                 const uint64_t p1 = mul_f32x2(f32x2(x[2 * k], x[2 * k + 1]), mul_f32x2(w, sj2)), pp = mul_f32x2(S, p1);
                                 c2 = add_f32x2(c2, pp);
                                 f32x2_split(pp, pf[16 * sub + 2 * k], pf[16 * sub + 2 * k + 1]);
@@ -193,7 +210,8 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
                             const int i0 = 16 * sub + 2 * k;
                             const float2 f = *reinterpret_cast<const float2*>(arr + 32 * b + i0);
                             const float w0 = i0 >= lane ? ex2_approx(f.x - Lj) : 0.f, w1 = i0 + 1 >= lane ? ex2_approx(f.y - Lj) : 0.f;
-                            const float S0 = __uint_as_float(sp[sub][k] << 16), S1 = __uint_as_float(sp[sub][k] & 0xffff0000u);
+                            const float2 s2 = score(sp[sub][k]);
+                            const float S0 = s2.x * unscale, S1 = s2.y * unscale;
                             const float p0 = x[2 * k] * (w0 * sj), p1 = x[2 * k + 1] * (w1 * sj);
                             pf[i0] = i0 > lane ? S0 * p0 : 0.f;
                             pf[i0 + 1] = i0 + 1 > lane ? S1 * p1 : 0.f;

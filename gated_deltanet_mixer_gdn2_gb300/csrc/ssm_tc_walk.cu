@@ -5,7 +5,9 @@
 //     backward  A  = e^{L_end} A' + C^T Y~,   Y~_i = e^{L_i} dy_i
 // One block per unit and 64 value columns of a head; both directions of a call run in one launch. Per chunk it
 // reads the keys (from L2, shared by a group's heads) and the values once and writes nothing but the saved
-// state, so HBM bounds it while enough blocks run; one block alone is bound by forming X~.
+// state. Both directions of 4 x 2048 tokens, 32 heads of 64 values, N = 128: 41 us for 134 MB of saved states and 290 MB
+// of tiles from L2, 2.6 us per chunk and block: the latency of a chunk's tiles and its two handshakes, which two blocks per
+// SM hide in part. Saved states are bf16, operands of products whose results are bf16.
 #include "ssm_tc.cuh"
 
 namespace gdn2 {
@@ -13,7 +15,7 @@ namespace {
 
 // Stages of keys and values; X~ replaces its values in place, with three parts the other two have two sets of buffers.
 // With one part two stages let two blocks share an SM and hide each other's waits; a tile takes 2300 cycles from its
-// request, so the one block that three parts leave room for has three (two: 197 us instead of 150 us for 2 x 32768
+// request, so the one block that three parts leave room for has three (two: 197 us instead of 160 us for 2 x 32768
 // tokens, 32 heads).
 template <int kParts>
 struct Sw {
