@@ -311,15 +311,15 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                         for (int j4 = 0; j4 < 8; ++j4) {
                             const float4 L = *reinterpret_cast<const float4*>(arr + 32 * b + 4 * j4);
                             const float4 s = *reinterpret_cast<const float4*>(arr + 384 + 32 * b + 4 * j4);
-                            const float l4[4] = {L.x, L.y, L.z, L.w}, s4[4] = {s.x, s.y, s.z, s.w};
-                            float v[4];
+                            const uint64_t l2[2] = {f32x2(L.x, L.y), f32x2(L.z, L.w)}, s2[2] = {f32x2(s.x, s.y), f32x2(s.z, s.w)};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float w = ex2_approx(Li - l4[e]) * s4[e];
-                                v[e] = 4 * j4 + e <= lane ? x[4 * j4 + e] * w : 0.f;
+                            for (int e = 0; e < 2; ++e) {
+                                const int j = 4 * j4 + 2 * e;
+                                float d0, d1, v0, v1;
+                                f32x2_split(sub_f32x2(f32x2(Li, Li), l2[e]), d0, d1);
+                                f32x2_split(mul_f32x2(mul_f32x2(f32x2(x[j], x[j + 1]), s2[e]), f32x2(ex2_approx(d0), ex2_approx(d1))), v0, v1);
+                                m[2 * j4 + e] = pack_bf16x2(j <= lane ? v0 : 0.f, j + 1 <= lane ? v1 : 0.f);
                             }
-                            m[2 * j4] = pack_bf16x2(v[0], v[1]);
-                            m[2 * j4 + 1] = pack_bf16x2(v[2], v[3]);
                         }
                     } else {
                         const float rf = ex2_approx(Li - arr[32 * b + 31]);
@@ -373,12 +373,17 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 uint4* cell = reinterpret_cast<uint4*>(xt + i * 128 + (((4 * half + k) ^ (i & 7)) << 4));
-                float xv[8], out[8];
-                unpack8(*cell, xv);
+                const uint4 xv = *cell;
+                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                uint32_t ow[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    out[e] = fmaf(dk, xv[e], fmaf(eL, __uint_as_float(yx[k >> 1][8 * (k & 1) + e]), __uint_as_float(yi[k >> 1][8 * (k & 1) + e])));
-                const uint4 o = pack8(out);
+                for (int e = 0; e < 4; ++e) {
+                    const int at = 8 * (k & 1) + 2 * e;
+                    const uint64_t yxe = f32x2(__uint_as_float(yx[k >> 1][at]), __uint_as_float(yx[k >> 1][at + 1]));
+                    const uint64_t yie = f32x2(__uint_as_float(yi[k >> 1][at]), __uint_as_float(yi[k >> 1][at + 1]));
+                    ow[e] = bf16x2_narrow(fma_f32x2(f32x2(dk, dk), bf16x2_widen(xw[e]), fma_f32x2(f32x2(eL, eL), yxe, yie)));
+                }
+                const uint4 o = make_uint4(ow[0], ow[1], ow[2], ow[3]);
                 if (n >= kQ) *cell = o;
                 else if (i < n) yrow[k] = o;
             }
@@ -426,7 +431,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 float x[32];
                 tmem_ld_cols<2>(tmem + lane_base + kTD + 32 * half, x);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) hx[k] = fmaf(decay.x, hx[k], kParts == 1 ? x[k] : fmaf(decay.y, hx[k], x[k]));
+                for (int k = 0; k < 16; ++k) {
+                    const uint64_t h2 = f32x2(hx[2 * k], hx[2 * k + 1]), d2 = f32x2(x[2 * k], x[2 * k + 1]);
+                    f32x2_split(fma_f32x2(f32x2(decay.x, decay.x), h2, kParts == 1 ? d2 : fma_f32x2(f32x2(decay.y, decay.y), h2, d2)), hx[2 * k], hx[2 * k + 1]);
+                }
                 tc_fence_before();
             }
             if (n < NC) {
@@ -443,19 +451,19 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int cell = ((4 * half + k) ^ (r & 7)) << 4;
-                    float v[8];
-                    unpack8(*reinterpret_cast<const uint4*>(xt + cell), v);
+                    const uint4 xv = *reinterpret_cast<const uint4*>(xt + cell);
+                    uint64_t v[4] = {bf16x2_widen(xv.x), bf16x2_widen(xv.y), bf16x2_widen(xv.z), bf16x2_widen(xv.w)};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] *= w;
+                    for (int e = 0; e < 4; ++e) v[e] = mul_f32x2(v[e], f32x2(w, w));
 #pragma unroll
                     for (int part = 0; part < kParts; ++part) {
-                        const uint4 o = pack8(v);
+                        const uint4 o = make_uint4(bf16x2_narrow(v[0]), bf16x2_narrow(v[1]), bf16x2_narrow(v[2]), bf16x2_narrow(v[3]));
                         *reinterpret_cast<uint4*>(to + part * so::kTile + cell) = o;
                         if (part + 1 < kParts) {
-                            float hi[8];
-                            unpack8(o, hi);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) v[e] -= hi[e];
+                            v[0] = sub_f32x2(v[0], bf16x2_widen(o.x));
+                            v[1] = sub_f32x2(v[1], bf16x2_widen(o.y));
+                            v[2] = sub_f32x2(v[2], bf16x2_widen(o.z));
+                            v[3] = sub_f32x2(v[3], bf16x2_widen(o.w));
                         }
                     }
                 }
