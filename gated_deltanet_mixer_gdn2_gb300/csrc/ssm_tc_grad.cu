@@ -68,6 +68,22 @@ struct GradTcArgs {
     long long wait_ns;
 };
 
+__device__ __forceinline__ float sum_of(uint64_t v) {
+    float a, b;
+    f32x2_split(v, a, b);
+    return a + b;
+}
+// Pair k of the 16 bf16 values of two 16-byte words, widened.
+__device__ __forceinline__ uint64_t pair_of(const uint4 (&v)[2], int k) {
+    const uint4& u = v[k >> 2];
+    return bf16x2_widen((k & 3) == 0 ? u.x : (k & 3) == 1 ? u.y : (k & 3) == 2 ? u.z : u.w);
+}
+__device__ __forceinline__ uint4 scaled8(const uint4& u, float w) {
+    const uint64_t w2 = f32x2(w, w);
+    return make_uint4(bf16x2_narrow(mul_f32x2(bf16x2_widen(u.x), w2)), bf16x2_narrow(mul_f32x2(bf16x2_widen(u.y), w2)),
+                      bf16x2_narrow(mul_f32x2(bf16x2_widen(u.z), w2)), bf16x2_narrow(mul_f32x2(bf16x2_widen(u.w), w2)));
+}
+
 // Sum over the warp's lanes of each of 32 values: lane l returns the sum of v[l]. Each step halves the values.
 __device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
 #pragma unroll
@@ -151,7 +167,7 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
             if (lane == 0) mbar_arrive1(bars + gSRead);
         }
         auto score = [&](uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); };
-        float e_acc = 0.f, dd_acc = 0.f;
+        uint64_t e_acc = 0, dd_acc = 0;  // pairs of partial sums
         int pi = 0, h = h_lo;
         for (int it = 0; ok && it < NI; ++it) {
             const int st = it & 1;
@@ -209,15 +225,18 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
                         for (int k = 0; k < 8; ++k) {
                             const int i0 = 16 * sub + 2 * k;
                             const float2 f = *reinterpret_cast<const float2*>(arr + 32 * b + i0);
-                            const float w0 = i0 >= lane ? ex2_approx(f.x - Lj) : 0.f, w1 = i0 + 1 >= lane ? ex2_approx(f.y - Lj) : 0.f;
+                            float d0, d1, f0, f1;
+                            f32x2_split(sub_f32x2(f32x2(f.x, f.y), f32x2(Lj, Lj)), d0, d1);
+                            const uint64_t w = f32x2(i0 >= lane ? ex2_approx(d0) : 0.f, i0 + 1 >= lane ? ex2_approx(d1) : 0.f);
                             const float2 s2 = score(sp[sub][k]);
-                            const float S0 = s2.x * unscale, S1 = s2.y * unscale;
-                            const float p0 = x[2 * k] * (w0 * sj), p1 = x[2 * k + 1] * (w1 * sj);
-                            pf[i0] = i0 > lane ? S0 * p0 : 0.f;
-                            pf[i0 + 1] = i0 + 1 > lane ? S1 * p1 : 0.f;
+                            const uint64_t S = mul_f32x2(f32x2(s2.x, s2.y), f32x2(unscale, unscale));
+                            const uint64_t p1 = mul_f32x2(f32x2(x[2 * k], x[2 * k + 1]), mul_f32x2(w, f32x2(sj, sj)));
+                            f32x2_split(mul_f32x2(S, p1), f0, f1);
+                            pf[i0] = i0 > lane ? f0 : 0.f;
+                            pf[i0 + 1] = i0 + 1 > lane ? f1 : 0.f;
                             cols += pf[i0] + pf[i0 + 1];
-                            m1[sub][k] = pack_bf16x2(p0, p1);
-                            m2[k] = pack_bf16x2(S0 * w0, S1 * w1);
+                            m1[sub][k] = bf16x2_narrow(p1);
+                            m2[k] = bf16x2_narrow(mul_f32x2(S, w));
                         }
                     }
                     tmem_st8(pair + 16 * sub, m1[sub]);
@@ -253,15 +272,8 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int cell = k ? cell1 : cell0;
-                float v[8];
-                unpack8(xr[k], v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= wx;
-                *reinterpret_cast<uint4*>(xt + cell) = pack8(v);
-                unpack8(yr[k], v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= eLj;
-                *reinterpret_cast<uint4*>(wt + cell) = pack8(v);
+                *reinterpret_cast<uint4*>(xt + cell) = scaled8(xr[k], wx);
+                *reinterpret_cast<uint4*>(wt + cell) = scaled8(yr[k], eLj);
             }
             if (!(ok = wait_bar(bars + gTu, ph1, lim, err))) break;
             tc_fence_after();
@@ -271,23 +283,20 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
                 tmem_ld16(val + kTU, t);
                 tmem_ld16(val + kTT, c);
                 tmem_ld_wait();
-                float vs = 0.f, qs = 0.f;
+                uint64_t vs = 0, qs = 0;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float v[8], w[8];
-                    unpack8(xr[k], v);
-                    unpack8(yr[k], w);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float ba = __uint_as_float(t[8 * k + e]);
-                        vs = fmaf(v[e], ba, vs);
-                        qs = fmaf(w[e], __uint_as_float(c[8 * k + e]), qs);
-                        t[8 * k + e] = __float_as_uint(ba * wej);
-                    }
+                for (int k = 0; k < 8; ++k) {
+                    const uint64_t ba = f32x2(__uint_as_float(t[2 * k]), __uint_as_float(t[2 * k + 1]));
+                    vs = fma_f32x2(pair_of(xr, k), ba, vs);
+                    qs = fma_f32x2(pair_of(yr, k), f32x2(__uint_as_float(c[2 * k]), __uint_as_float(c[2 * k + 1])), qs);
+                    float b0, b1;
+                    f32x2_split(mul_f32x2(ba, f32x2(wej, wej)), b0, b1);
+                    t[2 * k] = __float_as_uint(b0);
+                    t[2 * k + 1] = __float_as_uint(b1);
                 }
                 tmem_st16(val + kTU, t);
-                keep(2, vs * wx);
-                keep(3, qs * eLj);
+                keep(2, sum_of(vs) * wx);
+                keep(3, sum_of(qs) * eLj);
             }
             fence_proxy_async_smem();
             tmem_st_wait();
@@ -297,22 +306,18 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
             if (!(ok = wait_bar(bars + gHd, ph1, lim, err))) break;
             if (j < a.N) {
                 const uint8_t *ht = sm + sg::H0 + j * 128, *dt = sm + sg::DH + j * 128;
+                const uint4 hr[2] = {*reinterpret_cast<const uint4*>(ht + cell0), *reinterpret_cast<const uint4*>(ht + cell1)};
+                const uint4 ar[2] = {*reinterpret_cast<const uint4*>(dt + cell0), *reinterpret_cast<const uint4*>(dt + cell1)};
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int cell = k ? cell1 : cell0;
-                    float v[8], w[8];
-                    unpack8(*reinterpret_cast<const uint4*>(ht + cell), v);
-                    unpack8(*reinterpret_cast<const uint4*>(dt + cell), w);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) e_acc = fmaf(v[e], w[e], e_acc);
-                }
+                for (int k = 0; k < 8; ++k) e_acc = fma_f32x2(pair_of(hr, k), pair_of(ar, k), e_acc);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive1(bars + gHdFree);
             if (!(ok = wait_bar(bars + gDx, ph1, lim, err))) break;
             tc_fence_after();
             {
-                float t[16], du = 0.f;
+                float t[16];
+                uint64_t du = 0;
                 tmem_ld_cols<1>(val + kTU, t);
                 tc_fence_before();
                 __syncwarp();
@@ -320,29 +325,29 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
                 __nv_bfloat16* to = a.dx + static_cast<size_t>(row + j) * a.ld_dx + static_cast<size_t>(h) * a.P + pi * kCols + 16 * b;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    float v[8], w[8];
-                    unpack8(xr[k], v);
-                    unpack8(yr[k], w);
+                    uint32_t w[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        du = fmaf(v[e], t[8 * k + e], du);
-                        dd_acc = fmaf(v[e], w[e], dd_acc);
-                        w[e] = fmaf(dk, w[e], sj * t[8 * k + e]);
+                    for (int e = 0; e < 4; ++e) {
+                        const uint64_t xv = pair_of(xr, 4 * k + e), yv = pair_of(yr, 4 * k + e), U = f32x2(t[8 * k + 2 * e], t[8 * k + 2 * e + 1]);
+                        du = fma_f32x2(xv, U, du);
+                        dd_acc = fma_f32x2(xv, yv, dd_acc);
+                        w[e] = bf16x2_narrow(fma_f32x2(f32x2(dk, dk), yv, mul_f32x2(f32x2(sj, sj), U)));
                     }
-                    const uint4 o = pack8(w);
+                    const uint4 o = make_uint4(w[0], w[1], w[2], w[3]);
                     if (!tail) *reinterpret_cast<uint4*>(yt + (k ? cell1 : cell0)) = o;
                     else if (j < n) reinterpret_cast<uint4*>(to)[k] = o;
                 }
-                keep(4, du);
+                keep(4, sum_of(du));
             }
             if (++pi == pbs) {
+                float es = sum_of(e_acc), ds = sum_of(dd_acc);
 #pragma unroll
                 for (int d = 16; d; d >>= 1) {
-                    e_acc += __shfl_xor_sync(0xffffffffu, e_acc, d);
-                    dd_acc += __shfl_xor_sync(0xffffffffu, dd_acc, d);
+                    es += __shfl_xor_sync(0xffffffffu, es, d);
+                    ds += __shfl_xor_sync(0xffffffffu, ds, d);
                 }
-                if (lane == 0) *reinterpret_cast<float2*>(sm + sg::RED + 8 * warp) = make_float2(e_acc, dd_acc);
-                e_acc = dd_acc = 0.f;
+                if (lane == 0) *reinterpret_cast<float2*>(sm + sg::RED + 8 * warp) = make_float2(es, ds);
+                e_acc = dd_acc = 0;
                 pi = 0;
                 ++h;
             }

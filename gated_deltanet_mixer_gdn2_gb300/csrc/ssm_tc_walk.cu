@@ -221,19 +221,19 @@ __global__ void __launch_bounds__(kWalkThreadsTc, Sw<kParts>::kPerSm) walk_tc_ke
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int cell = ((4 * half + k) ^ (r & 7)) << 4;
-                    float v[8];
-                    unpack8(*reinterpret_cast<const uint4*>(xt + cell), v);
+                    const uint4 xv = *reinterpret_cast<const uint4*>(xt + cell);
+                    uint64_t v[4] = {bf16x2_widen(xv.x), bf16x2_widen(xv.y), bf16x2_widen(xv.z), bf16x2_widen(xv.w)};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] *= w;
+                    for (int e = 0; e < 4; ++e) v[e] = mul_f32x2(v[e], f32x2(w, w));
 #pragma unroll
                     for (int part = 0; part < kParts; ++part) {
-                        const uint4 o = pack8(v);
+                        const uint4 o = make_uint4(bf16x2_narrow(v[0]), bf16x2_narrow(v[1]), bf16x2_narrow(v[2]), bf16x2_narrow(v[3]));
                         *reinterpret_cast<uint4*>((part ? more + (part - 1) * kTileBytes : xt) + cell) = o;
                         if (part + 1 < kParts) {
-                            float hi[8];
-                            unpack8(o, hi);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) v[e] -= hi[e];
+                            v[0] = sub_f32x2(v[0], bf16x2_widen(o.x));
+                            v[1] = sub_f32x2(v[1], bf16x2_widen(o.y));
+                            v[2] = sub_f32x2(v[2], bf16x2_widen(o.z));
+                            v[3] = sub_f32x2(v[3], bf16x2_widen(o.w));
                         }
                     }
                 }
@@ -248,7 +248,11 @@ __global__ void __launch_bounds__(kWalkThreadsTc, Sw<kParts>::kPerSm) walk_tc_ke
                 float x[32];
                 tmem_ld_cols<2>(tmem + lane_base + 64 * set + 32 * half, x);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) hx[k] = fmaf(decay_c.x, hx[k], kParts == 1 ? x[k] : fmaf(decay_c.y, hx[k], x[k]));
+                for (int k = 0; k < 16; ++k) {
+                    const uint64_t h2 = f32x2(hx[2 * k], hx[2 * k + 1]), d2 = f32x2(x[2 * k], x[2 * k + 1]);
+                    f32x2_split(fma_f32x2(f32x2(decay_c.x, decay_c.x), h2, kParts == 1 ? d2 : fma_f32x2(f32x2(decay_c.y, decay_c.y), h2, d2)),
+                                hx[2 * k], hx[2 * k + 1]);
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive1(bars + wDEmpty + set);
