@@ -141,51 +141,48 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
 
     if (warp == 1) {
         if (lane == 0) {
-            // ---- copies: each kind of tile as soon as its stage is free, whichever that is
+            // ---- copies, in the order in which their stages come free: C after the state's readout, B after its increment,
+            // X when the chunk before has left through it. (Looking at all three in turn, whichever is free first, took
+            // as many instructions as all other warps together.)
             const int halves = a.N / 64;
             prefetch_tensormap(&maps.b);
             prefetch_tensormap(&maps.c);
             prefetch_tensormap(&maps.x);
             int nb = 0, nc = 0, nx = 0;
-            uint64_t t0 = globaltimer_ns();
-            // C is free after the state's readout, B after its increment
-            auto used = [&](int bar, int c) { return mbar_test_wait(bars + bar + (c & 1), (c >> 1) & 1); };
-            while (nb < NC || nc < NC || nx < NC) {
-                bool any = false;
-                if (nb < NC && (nb < 2 || used(kDFull, nb - 2))) {
-                    const int st = nb & 1;
-                    mbar_arrive_expect_tx(bars + kFullB + st, so::kTile * halves);
-                    for (int k = 0; k < halves; ++k)
-                        tma_load_3d(sm + so::B + (2 * st + k) * so::kTile, &maps.b, 64 * k, grp, u.row + nb * kQ, bars + kFullB + st);
-                    ++nb;
-                    any = true;
-                }
-                if (nc < NC && (nc < so::kCS || used(kCFree, nc - so::kCS))) {
-                    const int st = nc % so::kCS;
-                    mbar_arrive_expect_tx(bars + kFullC + st, so::kTile * halves);
-                    for (int k = 0; k < halves; ++k)
-                        tma_load_3d(sm + so::C + (2 * st + k) * so::kTile, &maps.c, 64 * k, grp, u.row + nc * kQ, bars + kFullC + st);
-                    ++nc;
-                    any = true;
-                }
-                if (nx < NC && (nx < so::kXS || mbar_test_wait(bars + kXEmpty + nx % so::kXS, ((nx / so::kXS) & 1) ^ 1))) {
-                    const int st = nx % so::kXS;
-                    mbar_arrive_expect_tx(bars + kFullX + st, so::kTile);
-                    tma_load_3d(sm + so::X + st * so::kTile, &maps.x, p0, h, u.row + nx * kQ, bars + kFullX + st);
-                    ++nx;
-                    any = true;
-                }
-                if (any) {
-                    t0 = globaltimer_ns();
-                } else {
-                    if (*err) break;
-                    if (lim <= 0 || (long long)(globaltimer_ns() - t0) > lim) {
-                        note_failure(err);
-                        break;
-                    }
-                    __nanosleep(64);
-                }
+            auto load_b = [&]() {
+                const int st = nb & 1;
+                mbar_arrive_expect_tx(bars + kFullB + st, so::kTile * halves);
+                for (int k = 0; k < halves; ++k)
+                    tma_load_3d(sm + so::B + (2 * st + k) * so::kTile, &maps.b, 64 * k, grp, u.row + nb * kQ, bars + kFullB + st);
+                ++nb;
+            };
+            auto load_c = [&]() {
+                const int st = nc % so::kCS;
+                mbar_arrive_expect_tx(bars + kFullC + st, so::kTile * halves);
+                for (int k = 0; k < halves; ++k)
+                    tma_load_3d(sm + so::C + (2 * st + k) * so::kTile, &maps.c, 64 * k, grp, u.row + nc * kQ, bars + kFullC + st);
+                ++nc;
+            };
+            auto load_x = [&]() {
+                const int st = nx % so::kXS;
+                mbar_arrive_expect_tx(bars + kFullX + st, so::kTile);
+                tma_load_3d(sm + so::X + st * so::kTile, &maps.x, p0, h, u.row + nx * kQ, bars + kFullX + st);
+                ++nx;
+            };
+            auto free_of = [&](int bar, uint32_t parity) { return mbar_wait_or_abort(bars + bar, parity, lim, err); };
+            bool ok = true;
+            for (int k = 0; k < 2 && k < NC; ++k) {
+                if (k < so::kCS) load_c();
+                load_b();
+                load_x();
             }
+            if (nx < NC) load_x();
+            for (int c = 0; ok && (nc < NC || nb < NC || nx < NC); ++c) {
+                if (nc < NC && (ok = free_of(kCFree + (c & 1), (c >> 1) & 1))) load_c();
+                if (ok && nb < NC && (ok = free_of(kDFull + (c & 1), (c >> 1) & 1))) load_b();
+                if (ok && c >= 1 && nx < NC && (ok = free_of(kXEmpty + (c - 1) % so::kXS, ((c - 1) / so::kXS) & 1))) load_x();
+            }
+            if (!ok) note_failure(err);
             auto drain = [&](int issued, int full, int stages) {  // nothing in flight when the block ends
                 for (int c = issued > stages ? issued - stages : 0; c < issued; ++c)
                     mbar_wait(bars + full + c % stages, (c / stages) & 1, kDefaultWaitNs);
