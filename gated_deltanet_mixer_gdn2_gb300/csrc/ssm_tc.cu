@@ -10,11 +10,13 @@
 // the least work, so its scheduler is the least loaded), copies (warp 1), gates (warps 2 and 3), M (warps 4-7),
 // Y (warps 8-15), X~ and state (warps 16-23).
 // Roundings to bf16: M, X~ and the state as operands of Y, once each; sums, states and decays are fp32.
-// 4 x 2048 tokens, 32 heads of 64 values, N = 128: 35 us, 2.2 us per chunk and block (CUDA cores: 935 us; even 16 tokens
-// of 8 heads take 10 us here and 12 us there); with the state as a result 53 us. The products need 1500 of a chunk's 3700
-// cycles. B and C have two stages, each held for the load (2500 cycles) and the chunk from its scores to its increment,
-// so a chunk takes 3100 cycles before any role's own work; no role left out alone saves more than a sixth. Pairs of blocks
-// that share B and C by multicast loads were slower (42 us): they wait for one another every chunk.
+// 4 x 2048 tokens, 32 heads of 64 values, N = 128: 32 us, 2 us per chunk and block (CUDA cores: 836 us; even 16 tokens
+// of 8 heads take 10 us here and 12 us there); with the state as a result 49 us. The products need 1500 of a chunk's 3150
+// cycles. Three things take about as long as the chunk: issuing its 32 products and 8 waits from one warp; the state's way
+// round from X~ ready to X~ ready (product, read-out, operand, X~); and X's three stages, each held for its load (2300),
+// two chunks and Y's way out. Slower for what they cost the others: two issuing warps (36 us), Y straight to global memory
+// (34 us), X~ formed by Y's warps (39 us before the packed arithmetic's 35), pairs of blocks that share B and C by
+// multicast loads (42 for 35).
 #include "ssm_tc.cuh"
 
 namespace gdn2 {
@@ -62,13 +64,10 @@ struct ScanTcArgs {
     const float *d, *s0;
     float* s1;
     __nv_bfloat16* y;
-    float* states;                   // [units][H][N][P]: read by the full form when `cut`, written by the state form
-    float* decay;                    // [units][H] log: written by the state form
-    __nv_bfloat16* save;             // state form: the state before every chunk, or null
+    float* states;                   // [units][H][N][P] when `cut`: the states before the units
     int cut, H, G, P, N;
     long long wait_ns;
 };
-
 
 // Gate arrays of one chunk, by one warp, four tokens per lane: L and the decay sums in units of log 2.
 // The decay to the chunk's end is a suffix sum of its own: as a difference of prefix sums it would lose
@@ -100,7 +99,7 @@ __device__ __forceinline__ void gate_arrays(float* arr, int lane, const float (&
 }
 
 // kParts bf16 parts of X~ enter the state's product: one where the state only feeds bf16 results, three
-// (2^-24 of every term) where it is returned in fp32.
+// (2^-24 of every term) where it is returned in fp32 (4 x 2048 tokens of 32 heads: 35 and 49 us).
 template <int kParts>
 __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_constant__ ScanMaps maps, const ScanTcArgs a) {
     using so = So<kParts>;
@@ -142,8 +141,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     if (warp == 1) {
         if (lane == 0) {
             // ---- copies, in the order in which their stages come free: C after the state's readout, B after its increment,
-            // X when the chunk before has left through it. (Looking at all three in turn, whichever is free first, took
-            // as many instructions as all other warps together.)
+            // X when the chunk before has left through it.
             const int halves = a.N / 64;
             prefetch_tensormap(&maps.b);
             prefetch_tensormap(&maps.c);
@@ -498,8 +496,8 @@ bool ssm_tc_shape(const ScanShape& sh) {
 
 namespace {
 // Tokens per block: whole sequences while their chains fill four fifths of the SMs, else units whose starting states come
-// from a pass over their increments (2 x 32768 tokens, 32 heads: 412 us cut, 741 whole; 1 x 8192, 8 heads: 43 and 104; a
-// packed batch of 8 with enough chains: 145 cut, 113 whole).
+// from a pass over their increments (2 x 32768 tokens, 32 heads, with the last state: 386 us cut, 607 whole; 1 x 8192, 8 heads: 43
+// and 96; a packed batch of 8 with enough chains: 138 cut, 95 whole).
 int fwd_unit(const ScanShape& sh) {
     int dev = 0, sms = 152;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) sms = 152;
@@ -542,11 +540,11 @@ cudaError_t launch_ssm_tc_fwd(const ScanShape& sh, const ScanIn& in, void* y, fl
     if (a.cut) {
         // the units' increments, exact where the last state is a result, and their starting states
         a.states = static_cast<float*>(ws);
-        a.decay = a.states + static_cast<size_t>(sh.seqs.units(a.unit)) * sh.H * sh.N * sh.P;
-        const WalkJob job{in.bm, in.x, in.s0, nullptr, a.states, a.decay, nullptr, 0};
+        float* decay = a.states + static_cast<size_t>(sh.seqs.units(a.unit)) * sh.H * sh.N * sh.P;
+        const WalkJob job{in.bm, in.x, in.s0, nullptr, a.states, decay, nullptr, 0};
         cudaError_t e = launch_ssm_walk_tc(sh, in.step, in.g, &job, 1, a.unit, 1, 0, s1 != nullptr, s, wait_ns);
         if (e != cudaSuccess) return e;
-        const ChainJob chain{in.s0, s1, a.states, a.decay, 0};
+        const ChainJob chain{in.s0, s1, a.states, decay, 0};
         if ((e = launch_ssm_chain(sh, a.unit, &chain, 1, s)) != cudaSuccess) return e;
     }
     return a.s1 ? launch_scan<3>(maps, a, grid, s) : launch_scan<1>(maps, a, grid, s);

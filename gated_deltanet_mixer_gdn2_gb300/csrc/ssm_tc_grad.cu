@@ -11,9 +11,9 @@
 // matrix: what cancels in it cancels exactly.
 // Roundings: the pair matrices, e^L dY, X~ and the saved states are bf16 operands, once each, of products whose sums are
 // fp32; row and column sums, dstep's and dg's sums and dD are fp32 throughout.
-// 4 x 2048 tokens, 32 heads of 64 values, N = 128: 96 us of a call's 145 (walk 41, sums 7). A head of a chunk takes about
-// 10500 cycles: the pair matrices, 4500 (a third of it the sums across lanes), the state's shares 1800, U 800, dx 2200, each
-// waiting for the one before; its 48 products take 3500 of them to issue, beside the rest. What limits overlapping two
+// 4 x 2048 tokens, 32 heads of 64 values, N = 128: 90 us of a call's 137 (walk 41, sums 7; CUDA cores: 1870). A head of a
+// chunk takes about 10000 cycles: the pair matrices, 4500 (a fifth of it the sums across lanes), the state's shares 1800, U
+// 800, dx 2000, each waiting for the one before; its 48 products take 3500 to issue, beside the rest. What limits overlapping two
 // heads is tensor memory: dB, dC and one pair matrix take three quarters of it.
 #include <cuda_fp16.h>
 
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
         bool ok = wait_bar(bars + gS, 0, lim, err);
         // This row and block of S^T, kept over the heads in the registers that bf16 would take: fp16 under a power of two
         // that brings its largest entry to 2^14 .. 2^15, so entries down to 2^-29 of that keep 11 bits. It goes into
-        // dstep and dg; as bf16 (8 bits) dstep was off by 2.8e-3 of its norm instead of 2.4e-3, for 2 us less of 96.
+        // dstep and dg; as bf16 (8 bits) dstep was off by 2.8e-3 of its norm instead of 2.4e-3, for 2 us less.
         uint32_t sp[2][8];
         float unscale = 1.f;
         if (ok) {

@@ -15,8 +15,8 @@ namespace {
 
 // Stages of keys and values; X~ replaces its values in place, with three parts the other two have two sets of buffers.
 // With one part two stages let two blocks share an SM and hide each other's waits; a tile takes 2300 cycles from its
-// request, so the one block that three parts leave room for has three (two: 197 us instead of 160 us for 2 x 32768
-// tokens, 32 heads).
+// request, so the one block that three parts leave room for has three (two: 197 us instead of 160 us, now 157, for
+// 2 x 32768 tokens, 32 heads).
 template <int kParts>
 struct Sw {
     static constexpr int kStages = kParts == 1 ? 2 : 3;
