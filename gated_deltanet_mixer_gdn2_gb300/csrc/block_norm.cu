@@ -254,7 +254,7 @@ struct NormGradArgs {
 //     dt = (q - th mean_group(q th)) / rms_group(t), q = dr scale post
 // dx = dt silu(z), dz = dt x silu'(z). dpost and dscale are one sum over the rows, of dr th, times scale and post; it and
 // dpre's, and the weights, stay in registers over the block's rows, the next row's loads in flight. 8192 x 2048 bf16 with
-// all of its inputs: 68 us, 4 TB/s, 58% of the copy rate: the sums' registers leave room for 16 warps, and two row sums
+// all of its inputs: 67 us with the sums, 4 TB/s, 59% of the copy rate: the sums' registers leave room for 16 warps, and two row sums
 // with their barriers stand between a row's loads and its stores.
 template <typename T, int VPT, int kMaxThreads, int kPerSm>
 __global__ void __launch_bounds__(kMaxThreads, kPerSm)
@@ -404,30 +404,30 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
 }
 
 // The blocks' parameter sums in a fixed order.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
     norm_sum_kernel(const float* __restrict__ part, int blocks, int d, const float* __restrict__ post, const float* __restrict__ scale,
                     float* __restrict__ dpost, float* __restrict__ dscale, float* __restrict__ dpre) {
-    __shared__ float red[8][33];
+    __shared__ float red[32][33];
     if (blockIdx.y ? !dpre : !dpost && !dscale) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float v = 0.f;
     if (c < d) {
         const float* src = part + static_cast<size_t>(blockIdx.y) * d + c;
         const size_t step = 2 * static_cast<size_t>(d);
-        int k = warp;
-        for (; k + 56 < blocks; k += 64) {  // eight loads in flight
-            float t[8];
+        for (int k = warp; k < blocks; k += 32 * 10) {  // ten loads in flight: all of two blocks per SM at once
+            float t[10];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) t[q] = src[(k + 8 * q) * step];
+            for (int q = 0; q < 10; ++q) t[q] = k + 32 * q < blocks ? src[(k + 32 * q) * step] : 0.f;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v += t[q];
+            for (int q = 0; q < 10; ++q) v += t[q];
         }
-        for (; k < blocks; k += 8) v += src[k * step];
     }
     red[warp][lane] = v;
     __syncthreads();
     if (warp || c >= d) return;
-    v = ((red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane])) + ((red[4][lane] + red[5][lane]) + (red[6][lane] + red[7][lane]));
+    v = 0.f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v += red[k][lane];
     if (blockIdx.y) {
         dpre[c] = v;
     } else {
@@ -547,7 +547,7 @@ gdn2_status gdn2_block_norm_backward(const void* x, const void* z, const float* 
     };
     if (!(dt == GDN2_BF16 ? go(__nv_bfloat16{}) : go(0.f))) return GDN2_ERR_CUDA;
     if (dpost_weight || dscale || dpre_weight)
-        norm_sum_kernel<<<dim3((d + 31) / 32, 2), 256, 0, s>>>(a.part, l.blocks, d, post_weight, scale, dpost_weight, dscale, dpre_weight);
+        norm_sum_kernel<<<dim3((d + 31) / 32, 2), 1024, 0, s>>>(a.part, l.blocks, d, post_weight, scale, dpost_weight, dscale, dpre_weight);
     return cudaGetLastError() == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA;
 }
 
