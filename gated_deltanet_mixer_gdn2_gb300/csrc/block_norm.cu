@@ -24,8 +24,9 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Room for the sums over a row and over its groups. `slot` alternates between the sums that follow one another, so
-// that one barrier orders each.
+// Room for the sums over a row and over its groups. Every sum takes the other slot than the sum before it, of whatever kind
+// and in whichever row (`slot` changes with each), so that one barrier per sum is enough: a sum's writes to a slot lie
+// behind the barrier of the sum between, and that one behind all reads of the slot's last sum.
 struct RowSums {
     float part[2][2][kMaxD / 8 / 32];  // [slot][which][32 vectors or a warp]
     float vec[kMaxD / 8], group[kMaxD / 8];
@@ -33,17 +34,19 @@ struct RowSums {
 
 // Sums over the whole row of kWhich values per thread, the same in every thread.
 template <int kWhich>
-__device__ __forceinline__ void row_total(RowSums& rs, int slot, float (&v)[kWhich]) {
+__device__ __forceinline__ void row_total(RowSums& rs, int& slot, float (&v)[kWhich]) {
     const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    float (&part)[2][kMaxD / 8 / 32] = rs.part[slot];
+    slot ^= 1;
 #pragma unroll
     for (int w = 0; w < kWhich; ++w) {
         const float t = warp_sum(v[w]);
-        if ((threadIdx.x & 31) == 0) rs.part[slot][w][warp] = t;
+        if ((threadIdx.x & 31) == 0) part[w][warp] = t;
     }
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWhich; ++w)
-        v[w] = warp_sum(static_cast<int>(threadIdx.x & 31) < warps ? rs.part[slot][w][threadIdx.x & 31] : 0.f);
+        v[w] = warp_sum(static_cast<int>(threadIdx.x & 31) < warps ? part[w][threadIdx.x & 31] : 0.f);
 }
 
 // Where a thread's vectors lie among the groups. Where groups are whole warps' worth of vectors (every common width)
@@ -64,19 +67,21 @@ struct Groups {
     }
 };
 template <int VPT>
-__device__ __forceinline__ void group_sums(RowSums& rs, int slot, const Groups<VPT>& gr, int groups, const bool (&in)[VPT], float (&v)[VPT]) {
+__device__ __forceinline__ void group_sums(RowSums& rs, int& slot, const Groups<VPT>& gr, int groups, const bool (&in)[VPT], float (&v)[VPT]) {
     const int tid = threadIdx.x;
+    float (&part)[kMaxD / 8 / 32] = rs.part[slot][0];
+    slot ^= 1;
     if (gr.whole) {
 #pragma unroll
         for (int m = 0; m < VPT; ++m) {
             const float t = warp_sum(v[m]);
-            if (in[m] && (tid & 31) == 0) rs.part[slot][0][(tid + m * blockDim.x) >> 5] = t;
+            if (in[m] && (tid & 31) == 0) part[(tid + m * blockDim.x) >> 5] = t;
         }
         __syncthreads();
 #pragma unroll
         for (int m = 0; m < VPT; ++m) {
             float t = 0.f;
-            for (int k = 0; k < gr.blocks; ++k) t += rs.part[slot][0][gr.first[m] + k];
+            for (int k = 0; k < gr.blocks; ++k) t += part[gr.first[m] + k];
             v[m] = t;
         }
         return;
@@ -180,6 +185,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
             if (residual) rr[m] = load_raw(residual + base + at[m]);
         }
     };
+    int slot = 0;
     fetch(blockIdx.x);
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const size_t base = static_cast<size_t>(row) * a.d;
@@ -203,7 +209,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
         }
         fetch(row + gridDim.x);
         if (a.post) {
-            group_sums<VPT>(rs, 0, gr, a.groups, in, part);
+            group_sums<VPT>(rs, slot, gr, a.groups, in, part);
 #pragma unroll
             for (int m = 0; m < VPT; ++m) {
                 const float inv = rsqrtf(fmaf(part[m], inv_width, a.eps));
@@ -229,7 +235,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
             float total[1] = {0.f};
 #pragma unroll
             for (int m = 0; m < VPT; ++m) total[0] += part[m];
-            row_total<1>(rs, 1, total);
+            row_total<1>(rs, slot, total);
             const float inv = rsqrtf(fmaf(total[0], inv_d, a.eps));
 #pragma unroll
             for (int m = 0; m < VPT; ++m) {
@@ -293,6 +299,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
             if (d_n) rdn[m] = load_raw(d_n + base + at[m]);
         }
     };
+    int slot = 0;
     fetch(blockIdx.x);
     for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const size_t base = static_cast<size_t>(row) * a.d;
@@ -322,7 +329,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
         }
         fetch(row + gridDim.x);
         if (a.post) {
-            group_sums<VPT>(rs, 0, gr, a.groups, in, one);
+            group_sums<VPT>(rs, slot, gr, a.groups, in, one);
 #pragma unroll
             for (int m = 0; m < VPT; ++m) {
                 inv_t[m] = rsqrtf(fmaf(one[m], inv_width, a.eps));
@@ -340,7 +347,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
             }
         }
         if (d_n) {
-            row_total<2>(rs, 1, both);
+            row_total<2>(rs, slot, both);
             const float inv = rsqrtf(fmaf(both[0], inv_d, a.eps));
             const float mean = both[1] * inv * inv_d;  // mean(k nh)
 #pragma unroll
@@ -365,7 +372,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm)
             }
         }
         if (a.post) {
-            group_sums<VPT>(rs, 0, gr, a.groups, in, one);
+            group_sums<VPT>(rs, slot, gr, a.groups, in, one);
 #pragma unroll
             for (int m = 0; m < VPT; ++m) {
                 const float mean = one[m] * inv_width;
