@@ -9,8 +9,9 @@ namespace gdn2 {
 
 // The sequences of a call. offsets == nullptr: B sequences of T tokens, sequence b at rows b*T.. .
 // Otherwise sequence b is rows [offsets[b], offsets[b+1]) of T rows in all. Offsets live on the device
-// and cannot be checked on the host, so every use goes through span(), which clamps them to [0, T]:
-// wrong offsets give wrong results, never an access outside the tensors.
+// and cannot be checked on the host, so every use goes through span(), which clamps them to [0, T], and what
+// lies in a workspace per unit through held(): wrong offsets give wrong results, never an access outside the
+// tensors or the workspace.
 struct Seqs {
     const int* offsets;
     int B, T;
@@ -29,10 +30,15 @@ struct Seqs {
     // lengths, an upper bound (unknown to the host) for packed ones.
     __host__ __device__ long long units(int unit) const {
         if (!offsets) return (long long)B * (T > 0 ? (T + unit - 1) / unit : 1);
-        return (long long)T / unit + B;
+        return static_cast<long long>(T / unit) + B;
     }
     // Units of one sequence.
-    __device__ __forceinline__ static int units_of(int len, int unit) { return len > unit ? (len + unit - 1) / unit : 1; }
+    __host__ __device__ __forceinline__ static int units_of(int len, int unit) { return len > unit ? (len + unit - 1) / unit : 1; }
+    // How many of a sequence's `count` units from number `base` on a workspace of `room` = units(unit) entries holds: all,
+    // unless the offsets do not ascend, for then the lengths add up to more than T. The rest is neither written nor read.
+    __host__ __device__ __forceinline__ static int held(long long base, int count, int room) {
+        return room - base >= count ? count : room > base ? static_cast<int>(room - base) : 0;
+    }
 };
 
 // One unit of a sequence: its place among the sequence's units and its tokens.
@@ -88,11 +94,11 @@ __device__ __forceinline__ bool find_unit(const Seqs& s, int unit, int idx, Unit
     return true;
 }
 
-// Units of the sequences before `seq`, by a whole warp.
-__device__ __forceinline__ int units_before(const Seqs& s, int unit, int seq) {
-    if (!s.offsets) return seq * Seqs::units_of(s.T, unit);
+// Units of the sequences before `seq`, by a whole warp (64 bits: offsets that do not ascend may add up to any length).
+__device__ __forceinline__ long long units_before(const Seqs& s, int unit, int seq) {
+    if (!s.offsets) return static_cast<long long>(seq) * Seqs::units_of(s.T, unit);
     const int lane = threadIdx.x & 31;
-    int n = 0;
+    long long n = 0;
     for (int b = lane; b < seq; b += 32) {
         int start, len;
         s.span(b, start, len);

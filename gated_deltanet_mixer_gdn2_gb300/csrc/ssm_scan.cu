@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kWalkThreads) walk_pair_kernel(WalkArgs f, Wal
 // place: four state elements per thread, eight units' loads in flight. Memory-bound: each increment is
 // read once and replaced once. `last`: the state after the final unit (back: before the first). The two directions
 // of a gradient run in one launch.
-__global__ void __launch_bounds__(256) chain_kernel(Seqs seqs, int unit, ChainJob j0, ChainJob j1, int H, int plane4) {
+__global__ void __launch_bounds__(256) chain_kernel(Seqs seqs, int unit, int room, ChainJob j0, ChainJob j1, int H, int plane4) {
     const ChainJob& job = blockIdx.y < H ? j0 : j1;
     const float* first = job.first;
     float *last = job.last, *states = job.states;
@@ -185,9 +185,9 @@ __global__ void __launch_bounds__(256) chain_kernel(Seqs seqs, int unit, ChainJo
     const int back = job.back;
     const int e = blockIdx.x * blockDim.x + threadIdx.x, h = blockIdx.y % H, seq = blockIdx.z;
     int start, len;
-    const int base = units_before(seqs, unit, seq);
+    const long long before = units_before(seqs, unit, seq);
     seqs.span(seq, start, len);
-    const int count = Seqs::units_of(len, unit);
+    const int count = Seqs::held(before, Seqs::units_of(len, unit), room), base = static_cast<int>(before);
     if (e >= plane4) return;
     const size_t at = (static_cast<size_t>(seq) * H + h) * plane4 + e;
     float4 cur = first ? reinterpret_cast<const float4*>(first)[at] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -692,7 +692,8 @@ cudaError_t grad_n(const ScanShape& sh, const ScanIn& in, const ScanGrads& gr, f
 
 cudaError_t launch_ssm_chain(const ScanShape& sh, int unit, const ChainJob* jobs, int n, cudaStream_t s) {
     const int plane4 = sh.N * sh.P / 4;
-    chain_kernel<<<dim3((plane4 + 255) / 256, n * sh.H, sh.seqs.B), 256, 0, s>>>(sh.seqs, unit, jobs[0], jobs[n - 1], sh.H, plane4);
+    chain_kernel<<<dim3((plane4 + 255) / 256, n * sh.H, sh.seqs.B), 256, 0, s>>>(sh.seqs, unit, static_cast<int>(sh.seqs.units(unit)),
+                                                                                     jobs[0], jobs[n - 1], sh.H, plane4);
     return cudaGetLastError();
 }
 

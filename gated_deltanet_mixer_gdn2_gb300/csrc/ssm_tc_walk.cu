@@ -200,8 +200,9 @@ __global__ void __launch_bounds__(kWalkThreadsTc, Sw<kParts>::kPerSm) walk_tc_ke
         const uint32_t tile = a.N * 128;  // bytes of a saved state
         uint8_t* save = nullptr;
         if (job.save && !a.increments) {
-            const size_t first_chunk = units_before(a.seqs, kQ, u.seq) + static_cast<size_t>(u.k) * (a.unit / kQ);
-            save = static_cast<uint8_t*>(job.save) + ((first_chunk * a.H + h) * pb + pi) * tile;
+            const long long first_chunk = units_before(a.seqs, kQ, u.seq) + static_cast<long long>(u.k) * (a.unit / kQ);
+            if (Seqs::held(first_chunk, NC, static_cast<int>(a.seqs.units(kQ))) == NC)
+                save = static_cast<uint8_t*>(job.save) + ((static_cast<size_t>(first_chunk) * a.H + h) * pb + pi) * tile;
         }
         const size_t save_step = static_cast<size_t>(a.H) * pb * tile;
         float2 decay = make_float2(1.f, 0.f);
