@@ -381,6 +381,28 @@ def _raw_stream(stream, t):
     return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
+def _on_stream(call):
+    """`call` with what it allocates, workspace and results, from the memory of the stream that it runs on: that of its
+    `stream` argument where one is given. The workspace is let go of when the call returns, with its kernels still to run;
+    only work behind them may have that memory next, and their results lie in none that other streams still work on.
+    Results are marked as in use by the caller's stream too. (To order inputs and results between streams is the caller's.)"""
+    @functools.wraps(call)
+    def run(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        import torch
+
+        caller = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            got = call(*args, **kw)
+        for t in got if isinstance(got, tuple) else (got,):
+            if t is not None:
+                t.record_stream(caller)
+        return got
+
+    return run
+
+
 def _dense(t, dtype, shape, name):
     """Pointer of a contiguous CUDA tensor of this dtype and shape; None for None."""
     if t is None:
@@ -490,11 +512,13 @@ def gdn2_ssm_prologue(xbc, delta, conv_weight, conv_bias, a, delta_bias, u, step
     return _prologue(xbc, delta, conv_weight, conv_bias, a, delta_bias, conv_state, offsets, silu, stream, (u, step, g))
 
 
+@_on_stream
 def ssm_prologue(xbc, delta, conv_weight, conv_bias, a, delta_bias, conv_state=None, offsets=None, *, silu=True, stream=None):
     """Returns (u, step, g); conv_state, if given, is updated in place."""
     return _prologue(xbc, delta, conv_weight, conv_bias, a, delta_bias, conv_state, offsets, silu, stream, None)
 
 
+@_on_stream
 def gdn2_ssm_prologue_backward(xbc, delta, conv_weight, conv_bias, a, delta_bias, du, dstep, dg, dxbc, ddelta, dconv_weight,
                                dconv_bias, da, ddelta_bias, offsets=None, *, silu=True, workspace=None, stream=None):
     """Gradients of gdn2_ssm_prologue from zero convolution states (C ABI gdn2_ssm_prologue_backward); writes dxbc,
@@ -516,6 +540,7 @@ def gdn2_ssm_prologue_backward(xbc, delta, conv_weight, conv_bias, a, delta_bias
     return dxbc, ddelta, dconv_weight, dconv_bias, da, ddelta_bias
 
 
+@_on_stream
 def ssm_prologue_backward(xbc, delta, conv_weight, conv_bias, a, delta_bias, du, dstep, dg, offsets=None, *, silu=True,
                           stream=None):
     """Returns (dxbc, ddelta, dconv_weight, dconv_bias or None, da, ddelta_bias)."""
@@ -553,6 +578,7 @@ def _scan(x, step, g, bm, cm, d, initial_state, final_state, offsets, path, work
     return y, final_state
 
 
+@_on_stream
 def gdn2_ssm_chunk_fwd(x, step, g, bm, cm, y, d=None, initial_state=None, final_state=None, offsets=None, *, path="auto",
                        workspace=None, stream=None):
     """Selective state-space scan (C ABI gdn2_ssm_chunk_fwd): per head H_t = e^{g_t} H_{t-1} + step_t B_t x_t^T,
@@ -565,6 +591,7 @@ def gdn2_ssm_chunk_fwd(x, step, g, bm, cm, y, d=None, initial_state=None, final_
     return _scan(x, step, g, bm, cm, d, initial_state, final_state, offsets, path, workspace, stream, y, False)
 
 
+@_on_stream
 def ssm_chunk_fwd(x, step, g, bm, cm, d=None, initial_state=None, offsets=None, *, output_final_state=True, path="auto",
                   workspace=None, stream=None):
     """Returns (y, final_state or None)."""
@@ -606,6 +633,7 @@ def _scan_grad(x, step, g, bm, cm, d_y, d, initial_state, d_final_state, offsets
     return outs
 
 
+@_on_stream
 def gdn2_ssm_backward(x, step, g, bm, cm, d_y, dx, dstep, dg, dbm, dcm, dd=None, d=None, initial_state=None,
                       d_final_state=None, d_initial_state=None, offsets=None, *, path="auto", workspace=None, stream=None):
     """Gradients of gdn2_ssm_chunk_fwd (C ABI gdn2_ssm_backward); writes dx, dstep, dg, dbm, dcm (token dtype; dx, dbm
@@ -614,6 +642,7 @@ def gdn2_ssm_backward(x, step, g, bm, cm, d_y, dx, dstep, dg, dbm, dcm, dd=None,
                       (dx, dstep, dg, dbm, dcm, dd, d_initial_state))
 
 
+@_on_stream
 def ssm_backward(x, step, g, bm, cm, d_y, d=None, initial_state=None, d_final_state=None, offsets=None, *, path="auto",
                  workspace=None, stream=None):
     """Returns (dx, dstep, dg, dbm, dcm, dd, d_initial_state); dd is None without d, d_initial_state without initial_state.
@@ -621,6 +650,7 @@ def ssm_backward(x, step, g, bm, cm, d_y, d=None, initial_state=None, d_final_st
     return _scan_grad(x, step, g, bm, cm, d_y, d, initial_state, d_final_state, offsets, path, workspace, stream, None)
 
 
+@_on_stream
 def gdn2_ssm_decode_step(xbc, delta, conv_weight, conv_bias, a, delta_bias, d, conv_state, state, y, slots=None, *, stream=None):
     """One token of the selective state-space mixer between its projections (C ABI gdn2_ssm_decode_step): convolution
     with SiLU, gates, state update and readout in one launch.
@@ -650,6 +680,7 @@ def gdn2_ssm_decode_step(xbc, delta, conv_weight, conv_bias, a, delta_bias, d, c
     return y
 
 
+@_on_stream
 def ssm_decode_step(xbc, delta, conv_weight, conv_bias, a, delta_bias, d, conv_state, state, slots=None, *, stream=None):
     """Returns y [B, H, P]; conv_state and state are updated in place. Rows of inactive slots are left unwritten."""
     return gdn2_ssm_decode_step(xbc, delta, conv_weight, conv_bias, a, delta_bias, d, conv_state, state, None, slots, stream=stream)
@@ -672,6 +703,7 @@ def gdn2_block_norm(x, z, post_weight, residual, scale, pre_weight, r, n, *, gro
     return r, n
 
 
+@_on_stream
 def block_norm(x, z=None, post_weight=None, residual=None, scale=None, pre_weight=None, *, groups=1, eps=1e-5, stream=None):
     """Returns (r, n): r is None when there is a norm before the next block but no residual to carry on; n is None
     without pre_weight."""
@@ -682,6 +714,7 @@ def block_norm(x, z=None, post_weight=None, residual=None, scale=None, pre_weigh
     return gdn2_block_norm(x, z, post_weight, residual, scale, pre_weight, r, n, groups=groups, eps=eps, stream=stream)
 
 
+@_on_stream
 def gdn2_block_norm_backward(x, z, post_weight, residual, scale, pre_weight, d_r, d_n, dx, dz, dpost_weight, dresidual, dscale,
                              dpre_weight, *, groups=1, eps=1e-5, workspace=None, stream=None):
     """Gradients of gdn2_block_norm (C ABI gdn2_block_norm_backward) given those of r (d_r, or None) and n (d_n, with
@@ -702,6 +735,7 @@ def gdn2_block_norm_backward(x, z, post_weight, residual, scale, pre_weight, d_r
     return dx, dz, dpost_weight, dresidual, dscale, dpre_weight
 
 
+@_on_stream
 def block_norm_backward(x, z=None, post_weight=None, residual=None, scale=None, pre_weight=None, d_r=None, d_n=None, *,
                         groups=1, eps=1e-5, stream=None):
     """Returns (dx, dz, dpost_weight, dresidual, dscale, dpre_weight), None for inputs not given."""
