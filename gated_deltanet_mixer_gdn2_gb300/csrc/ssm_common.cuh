@@ -25,6 +25,12 @@ struct Seqs {
         start = lo;
         len = max(hi - lo, 0);
     }
+    // Token rows [lo, hi) of all sequences together: each ends where the next one starts, so with ascending offsets they are
+    // one stretch. Rows before and behind it belong to no sequence.
+    __device__ __forceinline__ void covered(long long& lo, long long& hi) const {
+        lo = offsets ? min(max(__ldg(offsets), 0), T) : 0;
+        hi = offsets ? min(max(__ldg(offsets + B), 0), T) : static_cast<long long>(B) * T;
+    }
     long long rows() const { return offsets ? (long long)T : (long long)B * T; }
     // Units of `unit` tokens over all sequences, an empty sequence counted as one unit: exact for equal
     // lengths, an upper bound (unknown to the host) for packed ones.

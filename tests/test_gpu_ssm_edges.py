@@ -1,0 +1,59 @@
+"""The selective state-space operators where their inputs are unusual but allowed: packed buffers with rows of no sequence.
+
+Tolerances as in test_gpu_ssm.py, and for the same reasons: a result's own rounding and a handful of 2^-24 roundings per
+term."""
+import numpy as np
+import pytest
+
+from oracle import ssm
+from tests.test_gpu_ssm import TOL, _close, _dev, _f32, _np, _prologue_inputs, g2  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _int32(v):
+    import torch
+
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+# ---- rows of no sequence: before the first offset and behind the last one --------------------------------
+
+FRONT, BACK = 7, 90
+PADDED = [130, 0, 1, 40]  # lengths of the sequences between them
+
+
+def _padded(a, fill, dtype):
+    """Rows of `fill` around the sequences' rows."""
+    a = np.asarray(a)
+    return _dev(np.concatenate([np.full((n, *a.shape[1:]), fill) if n else a for n in (FRONT, 0, BACK)]), dtype)
+
+
+def _padded_offsets():
+    return _int32([FRONT + v for v in np.concatenate([[0], np.cumsum(PADDED)]).tolist()])
+
+
+def _untouched(name, t, canary=7.0):
+    assert bool((t[:FRONT] == canary).all()) and bool((t[-BACK:] == canary).all()), name
+
+
+def _canvas(like, *shape):
+    import torch
+
+    return torch.full(shape or like.shape, 7.0, dtype=like.dtype, device="cuda")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prologue_leaves_rows_of_no_sequence(g2, dtype):  # noqa: F811
+    ch, H = 136, 5
+    p = _prologue_inputs(dtype, PADDED, ch, H, 71)
+    seqs = ssm.spans(0, 0, np.concatenate([[0], np.cumsum(PADDED)]))
+    row, off = _padded(p["row"], np.nan, dtype), _padded_offsets()
+    u, step, g = _canvas(row, len(row), ch), _canvas(row, len(row), H), _canvas(row, len(row), H)
+    conv = _f32(p["conv"])
+    g2.gdn2_ssm_prologue(row[:, :ch], row[:, ch:ch + H], *(_f32(p[k]) for k in ("w", "bias", "a", "db")), u, step, g, conv, off)
+    want = ssm.prologue(p["row"][:, :ch], p["row"][:, ch:ch + H], p["w"], p["bias"], p["a"], p["db"], seqs, p["conv"])
+    for name, t, r in zip(("u", "step", "g"), (u, step, g), want):
+        _untouched(name, t)
+        _close(name, t[FRONT:-BACK], r, TOL[dtype])
+    assert np.array_equal(_np(conv), want[3])
