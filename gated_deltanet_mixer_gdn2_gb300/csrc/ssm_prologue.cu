@@ -228,6 +228,8 @@ __global__ void __launch_bounds__(kThreads, 3)
         __shared__ float red[kThreads / 32][32][2];
         const int blk = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         const long long lo = static_cast<long long>(blk) * kGateRows;
+        long long first, last;  // rows of no sequence enter no sum
+        a.seqs.covered(first, last);
         for (int h0 = 0; h0 < a.H; h0 += 32) {
             const int h = h0 + lane;
             float sa = 0.f, sb = 0.f;
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
                 for (int k = 0; k < kGateRows / 4; ++k) {
                     const long long r = lo + warp + 4 * k;
-                    if (r >= a.rows) continue;
+                    if (r < first || r >= last) continue;
                     const float v = to_f32(delta[r * a.ld_delta + h]) + bv, dgv = to_f32(dg[r * a.H + h]);
                     const float dv = fmaf(av, dgv, to_f32(dstep[r * a.H + h])) * ssm_sigmoid(v);
                     ddelta[r * ga.ld_ddelta + h] = from_f32<T>(dv);
@@ -267,8 +269,9 @@ __global__ void __launch_bounds__(kThreads, 3)
         w[0][e] = v.x; w[1][e] = v.y; w[2][e] = v.z; w[3][e] = v.w;
         bias[e] = a.bias ? __ldg(a.bias + c + e) : 0.f;
     }
-    const int rows = static_cast<int>(a.rows);
-    const int r0 = by * a.run, r1 = min(r0 + a.run, rows);
+    long long first, last;
+    a.seqs.covered(first, last);
+    const int r0 = static_cast<int>(max(static_cast<long long>(by) * a.run, first)), r1 = static_cast<int>(min((by + 1LL) * a.run, last));
     for (int lo = r0; lo < r1;) {
         int seq, start, end;
         if (!find_row(a.seqs, lo, seq, start, end)) {

@@ -57,3 +57,24 @@ def test_prologue_leaves_rows_of_no_sequence(g2, dtype):  # noqa: F811
         _untouched(name, t)
         _close(name, t[FRONT:-BACK], r, TOL[dtype])
     assert np.array_equal(_np(conv), want[3])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prologue_gradients_leave_rows_of_no_sequence(g2, dtype):  # noqa: F811
+    """NaN in the rows of no sequence reaches no sum over the rows, and nothing is written there."""
+    ch, H = 136, 5
+    p = _prologue_inputs(dtype, PADDED, ch, H, 72)
+    seqs = ssm.spans(0, 0, np.concatenate([[0], np.cumsum(PADDED)]))
+    row, off = _padded(p["row"], np.nan, dtype), _padded_offsets()
+    par = [_f32(p[k]) for k in ("w", "bias", "a", "db")]
+    dxbc, ddelta = _canvas(row, len(row), ch), _canvas(row, len(row), H)
+    sums = [_canvas(t) for t in par]
+    g2.gdn2_ssm_prologue_backward(row[:, :ch], row[:, ch:ch + H], *par, *(_padded(p[k], np.nan, dtype) for k in ("du", "dstep", "dg")),
+                                  dxbc, ddelta, *sums, off)
+    want = ssm.prologue_grad(p["row"][:, :ch], p["row"][:, ch:ch + H], p["w"], p["bias"], p["a"], p["db"], p["du"], p["dstep"],
+                             p["dg"], seqs)
+    for name, t, r in zip(("dxbc", "ddelta"), (dxbc, ddelta), want):
+        _untouched(name, t)
+        _close(name, t[FRONT:-BACK], r, TOL[dtype])
+    for name, t, r in zip(("dweight", "dbias", "da", "ddelta_bias"), sums, want[2:]):
+        _close(name, t, r, TOL["f32"])
