@@ -539,11 +539,11 @@ __global__ void __launch_bounds__(kGradThreads)
     }
 }
 
-// dB and dC: the sum of the head shares in a fixed order, then one rounding. dD, by the third row of blocks: the sum over the
+// dB and dC: the sum of the head shares in a fixed order, then one rounding; rows of no sequence have no shares. dD, by the third row of blocks: the sum over the
 // units, one block per head, in a fixed order.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    sums_kernel(const float* __restrict__ part, RowsOut dbr, RowsOut dcr, long long rows, int gn, int splits,
+    sums_kernel(Seqs seqs, const float* __restrict__ part, RowsOut dbr, RowsOut dcr, long long rows, int gn, int splits,
                 const float* __restrict__ dd_part, float* __restrict__ dd, int units, int H) {
     if (blockIdx.y == 2) {
         __shared__ float red[8];
@@ -561,6 +561,9 @@ __global__ void __launch_bounds__(256)
     const long long i = blockIdx.x * 256LL + threadIdx.x;
     if (splits <= 1 || i >= rows * (gn / 4)) return;
     const long long r = i / (gn / 4);
+    long long first, last;
+    seqs.covered(first, last);
+    if (r < first || r >= last) return;
     const int c = 4 * static_cast<int>(i - r * (gn / 4));
     const float* src = part + (blockIdx.y ? static_cast<size_t>(splits) * rows * gn : 0);
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -702,7 +705,7 @@ cudaError_t launch_ssm_grad_sums(const ScanShape& sh, const ScanGrads& gr, const
     if (splits <= 1 && !gr.dd) return cudaSuccess;
     const long long rows = sh.seqs.rows(), n = splits > 1 ? (rows * (sh.G * sh.N / 4) + 255) / 256 : 0;
     const dim3 grid(static_cast<unsigned>(n > sh.H ? n : sh.H), 3);
-    auto go = [&](auto kernel) { kernel<<<grid, 256, 0, s>>>(part, gr.dbm, gr.dcm, rows, sh.G * sh.N, splits, dd_part, gr.dd, units, sh.H); };
+    auto go = [&](auto kernel) { kernel<<<grid, 256, 0, s>>>(sh.seqs, part, gr.dbm, gr.dcm, rows, sh.G * sh.N, splits, dd_part, gr.dd, units, sh.H); };
     if (sh.dt == GDN2_BF16) go(sums_kernel<__nv_bfloat16>);
     else go(sums_kernel<float>);
     return cudaGetLastError();

@@ -6,9 +6,11 @@ import numpy as np
 import pytest
 
 from oracle import ssm
-from tests.test_gpu_ssm import TOL, _close, _dev, _f32, _np, _prologue_inputs, g2  # noqa: F401
+from tests.test_gpu_ssm import TOL, Scan, _close, _dev, _f32, _np, _prologue_inputs, g2  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+NAMES = ("dx", "dstep", "dg", "dbm", "dcm")
 
 
 def _int32(v):
@@ -78,3 +80,32 @@ def test_prologue_gradients_leave_rows_of_no_sequence(g2, dtype):  # noqa: F811
         _close(name, t[FRONT:-BACK], r, TOL[dtype])
     for name, t, r in zip(("dweight", "dbias", "da", "ddelta_bias"), sums, want[2:]):
         _close(name, t, r, TOL["f32"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,G", [(6, 1), (3, 3)], ids=["heads shared out", "a head per group"])
+def test_scan_leaves_rows_of_no_sequence(g2, dtype, H, G):  # noqa: F811
+    import torch
+
+    c = Scan(dtype, PADDED, True, H, G, 64, 128, seed=73)
+    off = _padded_offsets()
+    row = _padded(c.row, np.nan, dtype)
+    x, bm, cm = (t.unflatten(-1, s) for t, s in zip(row.split([H * 64, G * 128, G * 128], -1), ((H, 64), (G, 128), (G, 128))))
+    step, g, dy = (_padded(t, np.nan, dtype) for t in (c.step, c.g, c.dy))
+    y, s1 = _canvas(x), torch.empty(4, H, 128, 64, device="cuda")
+    g2.gdn2_ssm_chunk_fwd(x, step, g, bm, cm, y, _f32(c.d), _f32(c.s0), s1, off)
+    ry, rs = c.ref()
+    _untouched("y", y)
+    _close("y", y[FRONT:-BACK], ry, TOL[dtype])
+    _close("state", s1, rs, TOL["f32"])
+    outs = [_canvas(t) for t in (x, step, g, bm, cm)]
+    dd, ds0 = torch.empty(H, device="cuda"), torch.empty_like(s1)
+    need = g2.lib.gdn2_ssm_backward_workspace_size(0, 4, len(row), H, G, 64, 128, 1, g2._dtype_code(x))
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")  # NaN wherever it is read before it is written
+    g2.gdn2_ssm_backward(x, step, g, bm, cm, dy, *outs, dd, _f32(c.d), _f32(c.s0), _f32(c.ds1), ds0, off, workspace=ws)
+    want = c.ref_grad()
+    for name, t, r in zip(NAMES, outs, want):
+        _untouched(name, t)
+        _close(name, t[FRONT:-BACK], r, TOL[dtype])
+    _close("dd", dd, want[5], TOL["f32"])
+    _close("ds0", ds0, want[6], TOL["f32"])
