@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(kGradThreads)
     const int h_lo = grp * per + split * heads, h_hi = min(h_lo + heads, (grp + 1) * per);
     const int n = real ? u.len : 0;
     if (n == 0) {  // no such unit, or an empty sequence: nothing but its share of dD
-        if (dd_part && tid < h_hi - h_lo) dd_part[static_cast<size_t>(blockIdx.x) * H + h_lo + tid] = 0.f;
+        if (dd_part)
+            for (int h = h_lo + tid; h < h_hi; h += kGradThreads) dd_part[static_cast<size_t>(blockIdx.x) * H + h] = 0.f;
         return;
     }
     const size_t row = u.row;

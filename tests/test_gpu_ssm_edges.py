@@ -1,4 +1,5 @@
-"""The selective state-space operators where their inputs are unusual but allowed: packed buffers with rows of no sequence.
+"""The selective state-space operators where their inputs are unusual but allowed: packed buffers with rows of no sequence,
+groups of many heads.
 
 Tolerances as in test_gpu_ssm.py, and for the same reasons: a result's own rounding and a handful of 2^-24 roundings per
 term."""
@@ -109,3 +110,21 @@ def test_scan_leaves_rows_of_no_sequence(g2, dtype, H, G):  # noqa: F811
         _close(name, t[FRONT:-BACK], r, TOL[dtype])
     _close("dd", dd, want[5], TOL["f32"])
     _close("ds0", ds0, want[6], TOL["f32"])
+
+
+# ---- more heads in a group than a block has threads -------------------------------------------------------
+
+def test_skip_gradient_of_many_heads(g2):  # noqa: F811
+    """Packed, 320 heads of one group, and tokens enough for a block to take all of them: dd is sum(x dy) per head, whatever the
+    workspace held."""
+    import torch
+
+    c = Scan("f32", [11000, 0, 3], True, 320, 1, 8, 16, seed=74, states=False)
+    x, step, g, bm, cm = c.device()
+    need = g2.lib.gdn2_ssm_backward_workspace_size(0, 3, c.rows, 320, 1, 8, 16, 1, g2.GDN2_F32)
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(t) for t in (x, step, g, bm, cm)]
+    dd = torch.empty(320, device="cuda")
+    g2.gdn2_ssm_backward(x, step, g, bm, cm, _dev(c.dy, "f32"), *outs, dd, _f32(c.d), offsets=c.offsets(), workspace=ws)
+    _close("dd", dd, (c.x * c.dy).sum((0, 2)), TOL["f32"])
+    assert all(bool(torch.isfinite(t).all()) for t in outs)
