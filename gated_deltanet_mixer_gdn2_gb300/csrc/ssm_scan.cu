@@ -229,7 +229,7 @@ struct GradSmem {
     static constexpr int NS = N + 4, XS = PB + 4, Q = kGradUnit, PS = Q + 1;
     float b[Q][NS], c[Q][NS], x[Q][XS], dy[Q][XS], h0[N][XS], dh[N][XS];
     float p1[Q][PS], sw[Q][PS], pf[Q][PS];
-    float L[Q], eL[Q], wend[Q], stp[Q];     // inclusive log-decay, e^L, e^{L_end - L}, step
+    float g[Q], eL[Q], wend[Q], stp[Q];     // log-decay, e^L, e^{L_end - L}, step
     float rows[Q], cols[Q], q[Q], v[Q], du[Q];
     float red[kGradThreads / 32][2];
 };
@@ -242,12 +242,13 @@ struct GradSmem {
 //   dg_t = sum_{i >= t > j} S R W s + sum_{i >= t} e^{L_i} dY_i . H0^T C_i
 //          + sum_{j < t} s_j e^{L_end - L_j} x_j . dH^T B_j + e^{L_end} <dH, H0>
 // The double sum is a suffix sum of (row sums - column sums) of one matrix held in fp32, so what
-// cancels in it cancels exactly. Every exponent is <= 0.
+// cancels in it cancels exactly. Every exponent is <= 0, and each is a sum of just the gates that it stands for: as a difference
+// of two L it would lose the digits of ordinary decays behind strong ones (fp32, twelve resets before them: 3.5e-4).
 // Multiply-adds from shared memory bound it, two blocks per SM: fp32, 1364 packed tokens, 8 heads of 64 values, N = 64,
 // 50 us of a call's 72 (walk of both directions 21, chain 10, sums 4), 27000 of each scheduler's 62000 cycles issuing.
 // Value columns in halves of 32, which let three blocks share an SM, took 79 us instead of 75.
 template <typename T, int N, int PB>
-__global__ void __launch_bounds__(kGradThreads)
+__global__ void __launch_bounds__(kGradThreads, N <= 64 ? 2 : 1)
     grad_kernel(Seqs seqs, Rows xr, Rows br, Rows cr, Rows dyr, const T* __restrict__ step, const T* __restrict__ g,
                 const float* __restrict__ dskip, const float* __restrict__ h0, const float* __restrict__ dhe,
                 RowsOut dxr, RowsOut dbr, RowsOut dcr, T* __restrict__ dstep, T* __restrict__ dg,
@@ -301,21 +302,23 @@ __global__ void __launch_bounds__(kGradThreads)
     for (int h = h_lo; h < h_hi; ++h) {
         const size_t uh = static_cast<size_t>(blockIdx.x) * H + h;
         if (warp == 0) {
-            float L = lane < n ? ssm_gate(to_f32(g[(row + lane) * H + h])) : 0.f;
+            const float gt = lane < n ? ssm_gate(to_f32(g[(row + lane) * H + h])) : 0.f;
+            float L = gt, rest = gt;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const float v = __shfl_up_sync(0xffffffffu, L, d);
+                const float v = __shfl_up_sync(0xffffffffu, L, d), w = __shfl_down_sync(0xffffffffu, rest, d);
                 if (lane >= d) L += v;
+                if (lane + d < 32) rest += w;
             }
-            const float end = __shfl_sync(0xffffffffu, L, 31);
-            s.L[lane] = L;
+            rest = __shfl_down_sync(0xffffffffu, rest, 1);
+            s.g[lane] = gt;
             s.eL[lane] = expf(L);
-            s.wend[lane] = expf(end - L);
+            s.wend[lane] = lane < 31 ? expf(rest) : 1.f;
             s.stp[lane] = lane < n ? to_f32(step[(row + lane) * H + h]) : 0.f;
             s.rows[lane] = s.cols[lane] = s.q[lane] = s.v[lane] = s.du[lane] = 0.f;
         }
         const float dk = dskip ? dskip[h] : 0.f;
-        float e_acc = 0.f, dd_acc = 0.f;
+        float e_acc = 0.f, dd_acc = 0.f, wp[4];  // wp: W of this thread's entries
         for (int p0 = 0; p0 < P; p0 += PB) {
             const T* xp = static_cast<const T*>(xr.p) + static_cast<size_t>(h) * P + p0;
             const T* dyp = static_cast<const T*>(dyr.p) + static_cast<size_t>(h) * P + p0;
@@ -337,6 +340,17 @@ __global__ void __launch_bounds__(kGradThreads)
                 e_acc += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
             }
             __syncthreads();
+            if (p0 == 0) {
+                float sum = 0.f;  // of the gates behind token j up to token pi, eight at a time
+#pragma unroll
+                for (int e = 3; e >= 0; --e) {
+                    float eight = 0.f;
+#pragma unroll
+                    for (int k = pj + 8 * e + 1, d = 0; d < 8; ++k, ++d) eight += k <= pi ? s.g[k] : 0.f;
+                    sum += eight;
+                    wp[e] = pi >= pj + 8 * e ? expf(sum) : 0.f;
+                }
+            }
             {
                 float r[4] = {0.f, 0.f, 0.f, 0.f};
                 for (int k = 0; k < PB; k += 4) {
@@ -351,10 +365,9 @@ __global__ void __launch_bounds__(kGradThreads)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int j = pj + 8 * e;
-                    const float w = pi >= j ? expf(s.L[pi] - s.L[j]) : 0.f;
-                    const float p1 = r[e] * w * s.stp[j], pf = pi > j ? sc[e] * p1 : 0.f;
+                    const float p1 = r[e] * wp[e] * s.stp[j], pf = pi > j ? sc[e] * p1 : 0.f;
                     s.p1[pi][j] = p1;
-                    s.sw[pi][j] = sc[e] * w;
+                    s.sw[pi][j] = sc[e] * wp[e];
                     s.pf[pi][j] = pf;
                     rs += pf;
                 }

@@ -1,12 +1,13 @@
 """The selective state-space operators where their inputs are unusual but allowed: packed buffers with rows of no sequence,
-groups of many heads.
+groups of many heads, gates that reset the state again and again.
 
 Tolerances as in test_gpu_ssm.py, and for the same reasons: a result's own rounding and a handful of 2^-24 roundings per
-term."""
+term. Where a test looks at a part of a result only (the tokens behind resets), it is held to the same bound of that part's
+largest value: nothing in the arithmetic of these tokens depends on what the resets have wiped out."""
 import numpy as np
 import pytest
 
-from oracle import ssm
+from oracle import max_rel_err, ssm
 from tests.test_gpu_ssm import TOL, Scan, _close, _dev, _f32, _np, _prologue_inputs, g2  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -128,3 +129,23 @@ def test_skip_gradient_of_many_heads(g2):  # noqa: F811
     g2.gdn2_ssm_backward(x, step, g, bm, cm, _dev(c.dy, "f32"), *outs, dd, _f32(c.d), offsets=c.offsets(), workspace=ws)
     _close("dd", dd, (c.x * c.dy).sum((0, 2)), TOL["f32"])
     assert all(bool(torch.isfinite(t).all()) for t in outs)
+
+
+# ---- gates -------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("path", ["auto", "simt"])
+@pytest.mark.parametrize("reset", [-np.inf, -40.0])
+def test_gradients_behind_resets(g2, dtype, path, reset):  # noqa: F811
+    """Ordinary decays behind many resets keep their digits: the tokens behind them are held to the bound on their own."""
+    c = Scan(dtype, [32, 32], False, 2, 1, 64, 64, seed=75, decay=0.5)
+    c.g = c.g.reshape(2, 32, 2)
+    c.g[:, :20] = reset
+    c.g = c.g.reshape(64, 2)
+    got, want = c.run_grad(g2, path=path), c.ref_grad()
+    for name, a, b in zip(NAMES, got, want):
+        a, b = _np(a), c.lead(b)
+        assert np.isfinite(a).all(), name
+        e = max_rel_err(a[:, 20:], b[:, 20:])
+        assert e <= TOL[dtype], (name, e)
+    _close("ds0", got[6], want[6], TOL["f32"])
