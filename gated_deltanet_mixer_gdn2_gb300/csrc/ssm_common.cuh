@@ -144,8 +144,9 @@ __device__ __forceinline__ float ssm_sigmoid(float v) {
 // log(1 + e^v), exact to fp32 for either sign
 __device__ __forceinline__ float ssm_softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
 
-// Log-decays enter every exponential floored (common.cuh): a full reset (g = -inf) keeps sums finite.
-__device__ __forceinline__ float ssm_gate(float g) { return fmaxf(g, kGateFloor); }
+// Log-decays enter every exponential floored (common.cuh): a full reset (g = -inf) keeps sums finite. NaN stays NaN (fmaxf
+// would make it a reset).
+__device__ __forceinline__ float ssm_gate(float g) { return g < kGateFloor ? kGateFloor : g; }
 
 constexpr float kLn2 = 0.69314718056f;
 

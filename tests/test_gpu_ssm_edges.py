@@ -1,5 +1,5 @@
 """The selective state-space operators where their inputs are unusual but allowed: packed buffers with rows of no sequence,
-groups of many heads, gates that reset the state again and again.
+groups of many heads, gates that are not finite or reset the state again and again.
 
 Tolerances as in test_gpu_ssm.py, and for the same reasons: a result's own rounding and a handful of 2^-24 roundings per
 term. Where a test looks at a part of a result only (the tokens behind resets), it is held to the same bound of that part's
@@ -149,3 +149,45 @@ def test_gradients_behind_resets(g2, dtype, path, reset):  # noqa: F811
         e = max_rel_err(a[:, 20:], b[:, 20:])
         assert e <= TOL[dtype], (name, e)
     _close("ds0", got[6], want[6], TOL["f32"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("at", [0, 40, 131])
+def test_gate_that_is_nan(g2, dtype, at):  # noqa: F811
+    """A NaN gate is no reset: what the recurrence takes through it is not finite; another head, another sequence keeps every bit."""
+    import torch
+
+    lens, H = [60, 140, 33], 3
+    c = Scan(dtype, lens, True, H, H, 64, 128, seed=76)
+    y, s1 = c.run(g2)
+    grads = c.run_grad(g2)
+    t = lens[0] + at
+    c.g[t, 1] = np.nan
+    yb, sb = c.run(g2)
+    gb = c.run_grad(g2)
+    end = lens[0] + lens[1]
+    none = lambda v: not bool(torch.isfinite(v).any())  # noqa: E731
+    assert none(yb[t:end, 1]) and none(sb[1, 1])
+    dx, dstep, dg, dbm, dcm, _, ds0 = gb
+    assert none(dx[lens[0]:t, 1]) and none(dstep[lens[0]:t, 1]) and none(dbm[lens[0]:t, 1]) and none(dcm[t:end, 1])
+    assert none(dg[t:t + 1, 1]) and none(ds0[1, 1])
+    keep = np.r_[0:lens[0], end:sum(lens)]
+    for a, b in zip((y, *grads[:5]), (yb, *gb[:5])):
+        assert torch.equal(a[keep], b[keep]) and torch.equal(a[:, [0, 2]], b[:, [0, 2]])
+    for a, b in ((s1, sb), (grads[6], ds0)):
+        assert torch.equal(a[[0, 2]], b[[0, 2]]) and torch.equal(a[1, [0, 2]], b[1, [0, 2]])
+
+
+def test_decode_gate_that_is_nan(g2):  # noqa: F811
+    import torch
+
+    torch.manual_seed(0)
+    B, H, P, N = 2, 3, 16, 32
+    ch = H * P + 2 * N
+    f = lambda *s: torch.randn(*s, device="cuda")  # noqa: E731
+    a = -f(H).abs()
+    a[1] = float("nan")
+    conv, st = f(B, 3, ch), f(B, H, N, P)
+    y = g2.ssm_decode_step(f(B, ch), f(B, H), f(ch, 4), None, a, f(H), None, conv, st)
+    assert not bool(torch.isfinite(y[:, 1]).any()) and not bool(torch.isfinite(st[:, 1]).any())
+    assert bool(torch.isfinite(y[:, [0, 2]]).all()) and bool(torch.isfinite(st[:, [0, 2]]).all())
