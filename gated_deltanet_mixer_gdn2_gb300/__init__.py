@@ -368,17 +368,30 @@ def gdn2_mixer_decode_step(xq, xk, xv, conv_q, conv_k, conv_v, ag, ab, aw, state
 
 # ---- selective state-space mixer ------------------------------------------------------------------------
 # A call here costs as much host time as many of the kernels run for, so arguments are checked and marshalled
-# in one pass, pointers go to ctypes as integers, and workspace sizes are looked up by the call's sizes.
+# in one pass, pointers go to ctypes as integers, and workspace sizes are looked up by the call's sizes and device (they
+# depend on its number of SMs).
 
 @functools.lru_cache(maxsize=4096)
-def _size_of(fn, *sizes) -> int:
+def _size_of(fn, dev, *sizes) -> int:
     return getattr(lib, fn)(*sizes)
 
 
-def _raw_stream(stream, t):
+def _device(t) -> int:
+    """The index of the tensor's device, which has to be the current one: kernels are launched there."""
     import torch
 
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must live on a CUDA device")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError("tensors must live on the current CUDA device")
+    return dev
+
+
+def _raw_stream(stream, dev):
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _on_stream(call):
@@ -400,33 +413,34 @@ def _on_stream(call):
                 t.record_stream(caller)
         return got
 
+    run.plain = call  # for a call within a call
     return run
 
 
-def _dense(t, dtype, shape, name):
-    """Pointer of a contiguous CUDA tensor of this dtype and shape; None for None."""
+def _dense(t, dtype, shape, name, dev):
+    """Pointer of a contiguous tensor of this dtype and shape on device `dev`; None for None."""
     if t is None:
         return None
     if t.dtype is not dtype:
         raise TypeError(f"{name} is {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError("tensors must live on a CUDA device")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: all tensors must live on the same CUDA device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _rows(t, dtype, shape, tail, name):
+def _rows(t, dtype, shape, tail, name, dev):
     """(pointer, row stride) of a token tensor [..., *tail]: each row's last `tail` dimensions are dense, the rows lie
     one stride apart (a slice of a wider row is fine)."""
     if t.dtype is not dtype:
         raise TypeError(f"{name}: all token tensors share one dtype, {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError("tensors must live on a CUDA device")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: all tensors must live on the same CUDA device")
     width = shape[-1] if tail == 1 else shape[-1] * shape[-2]
     if t.is_contiguous():
         return t.data_ptr(), width
@@ -448,7 +462,7 @@ def _rows(t, dtype, shape, tail, name):
     return t.data_ptr(), width if ld is None else ld
 
 
-def _lead(t, tail, offsets):
+def _lead(t, tail, offsets, dev):
     """Leading dimensions, B, T and the offsets' pointer of a call whose token tensors are [B, T, ...], or [T, ...] with
     offsets."""
     import torch
@@ -462,10 +476,10 @@ def _lead(t, tail, offsets):
         raise ValueError("with offsets, token tensors are [T, ...]")
     if offsets.dtype is not torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 1:
         raise TypeError("offsets is an int32 tensor of one entry more than sequences")
-    return lead, offsets.shape[0] - 1, lead[0], _dense(offsets, torch.int32, offsets.shape, "offsets")
+    return lead, offsets.shape[0] - 1, lead[0], _dense(offsets, torch.int32, offsets.shape, "offsets", dev)
 
 
-def _workspace(need, like, given):
+def _workspace(need, like, given, dev):
     """(tensor, pointer, bytes) of a call's workspace, allocated when none is given and one is needed."""
     import torch
 
@@ -473,28 +487,29 @@ def _workspace(need, like, given):
         if not need:
             return None, None, 0
         given = torch.empty(need, dtype=torch.uint8, device=like.device)
-    return given, _dense(given, torch.uint8, given.shape, "workspace"), given.shape[0]
+    return given, _dense(given, torch.uint8, given.shape, "workspace", dev), given.shape[0]
 
 
 def _prologue(xbc, delta, conv_weight, conv_bias, a, delta_bias, conv_state, offsets, silu, stream, outs):
     import torch
 
-    lead, B, T, off = _lead(xbc, 1, offsets)
+    dev = _device(xbc)
+    lead, B, T, off = _lead(xbc, 1, offsets, dev)
     ch, H, dtype, f32 = xbc.shape[-1], delta.shape[-1], xbc.dtype, torch.float32
     wide, narrow = (*lead, ch), (*lead, H)
-    px, lx = _rows(xbc, dtype, wide, 1, "xbc")
-    pd, ld = _rows(delta, dtype, narrow, 1, "delta")
+    px, lx = _rows(xbc, dtype, wide, 1, "xbc", dev)
+    pd, ld = _rows(delta, dtype, narrow, 1, "delta", dev)
     if outs is None:
-        dev = xbc.device
-        outs = (torch.empty(wide, dtype=dtype, device=dev), torch.empty(narrow, dtype=dtype, device=dev),
-                torch.empty(narrow, dtype=dtype, device=dev))
+        at = xbc.device
+        outs = (torch.empty(wide, dtype=dtype, device=at), torch.empty(narrow, dtype=dtype, device=at),
+                torch.empty(narrow, dtype=dtype, device=at))
         ptrs = [t.data_ptr() for t in outs]
     else:
-        ptrs = [_dense(t, dtype, s, n) for t, s, n in zip(outs, (wide, narrow, narrow), ("u", "step", "g"))]
-    _check(lib.gdn2_ssm_prologue(px, lx, pd, ld, _dense(conv_weight, f32, (ch, 4), "conv_weight"),
-                                 _dense(conv_bias, f32, (ch,), "conv_bias"), _dense(a, f32, (H,), "a"),
-                                 _dense(delta_bias, f32, (H,), "delta_bias"), _dense(conv_state, f32, (B, 3, ch), "conv_state"),
-                                 off, *ptrs, B, T, ch, H, 1 if silu else 0, _dtype_code(xbc), _raw_stream(stream, xbc)),
+        ptrs = [_dense(t, dtype, s, n, dev) for t, s, n in zip(outs, (wide, narrow, narrow), ("u", "step", "g"))]
+    _check(lib.gdn2_ssm_prologue(px, lx, pd, ld, _dense(conv_weight, f32, (ch, 4), "conv_weight", dev),
+                                 _dense(conv_bias, f32, (ch,), "conv_bias", dev), _dense(a, f32, (H,), "a", dev),
+                                 _dense(delta_bias, f32, (H,), "delta_bias", dev), _dense(conv_state, f32, (B, 3, ch), "conv_state", dev),
+                                 off, *ptrs, B, T, ch, H, 1 if silu else 0, _dtype_code(xbc), _raw_stream(stream, dev)),
            "gdn2_ssm_prologue")
     return outs
 
@@ -525,17 +540,18 @@ def gdn2_ssm_prologue_backward(xbc, delta, conv_weight, conv_bias, a, delta_bias
     ddelta (token dtype; may be slices of wider rows) and the float32 parameter gradients (dconv_bias may be None)."""
     import torch
 
-    lead, B, T, off = _lead(xbc, 1, offsets)
+    dev = _device(xbc)
+    lead, B, T, off = _lead(xbc, 1, offsets, dev)
     ch, H, dtype, f32 = xbc.shape[-1], delta.shape[-1], xbc.dtype, torch.float32
     wide, narrow, dt = (*lead, ch), (*lead, H), _dtype_code(xbc)
-    ws, pw, nw = _workspace(_size_of("gdn2_ssm_prologue_backward_workspace_size", B, T, ch, H, int(off is not None), dt), xbc, workspace)
+    ws, pw, nw = _workspace(_size_of("gdn2_ssm_prologue_backward_workspace_size", dev, B, T, ch, H, int(off is not None), dt), xbc, workspace, dev)
     _check(lib.gdn2_ssm_prologue_backward(
-        *_rows(xbc, dtype, wide, 1, "xbc"), *_rows(delta, dtype, narrow, 1, "delta"),
-        _dense(conv_weight, f32, (ch, 4), "conv_weight"), _dense(conv_bias, f32, (ch,), "conv_bias"), _dense(a, f32, (H,), "a"),
-        _dense(delta_bias, f32, (H,), "delta_bias"), off, *_rows(du, dtype, wide, 1, "du"), _dense(dstep, dtype, narrow, "dstep"),
-        _dense(dg, dtype, narrow, "dg"), *_rows(dxbc, dtype, wide, 1, "dxbc"), *_rows(ddelta, dtype, narrow, 1, "ddelta"),
-        _dense(dconv_weight, f32, (ch, 4), "dconv_weight"), _dense(dconv_bias, f32, (ch,), "dconv_bias"), _dense(da, f32, (H,), "da"),
-        _dense(ddelta_bias, f32, (H,), "ddelta_bias"), B, T, ch, H, 1 if silu else 0, dt, pw, nw, _raw_stream(stream, xbc)),
+        *_rows(xbc, dtype, wide, 1, "xbc", dev), *_rows(delta, dtype, narrow, 1, "delta", dev),
+        _dense(conv_weight, f32, (ch, 4), "conv_weight", dev), _dense(conv_bias, f32, (ch,), "conv_bias", dev), _dense(a, f32, (H,), "a", dev),
+        _dense(delta_bias, f32, (H,), "delta_bias", dev), off, *_rows(du, dtype, wide, 1, "du", dev), _dense(dstep, dtype, narrow, "dstep", dev),
+        _dense(dg, dtype, narrow, "dg", dev), *_rows(dxbc, dtype, wide, 1, "dxbc", dev), *_rows(ddelta, dtype, narrow, 1, "ddelta", dev),
+        _dense(dconv_weight, f32, (ch, 4), "dconv_weight", dev), _dense(dconv_bias, f32, (ch,), "dconv_bias", dev), _dense(da, f32, (H,), "da", dev),
+        _dense(ddelta_bias, f32, (H,), "ddelta_bias", dev), B, T, ch, H, 1 if silu else 0, dt, pw, nw, _raw_stream(stream, dev)),
         "gdn2_ssm_prologue_backward")
     return dxbc, ddelta, dconv_weight, dconv_bias, da, ddelta_bias
 
@@ -548,32 +564,33 @@ def ssm_prologue_backward(xbc, delta, conv_weight, conv_bias, a, delta_bias, du,
 
     dev = xbc.device
     new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=dev)
-    return gdn2_ssm_prologue_backward(xbc, delta, conv_weight, conv_bias, a, delta_bias, du, dstep, dg, new(xbc), new(delta),
-                                      new(conv_weight), new(conv_bias) if conv_bias is not None else None, new(a),
-                                      new(delta_bias), offsets, silu=silu, stream=stream)
+    return gdn2_ssm_prologue_backward.plain(xbc, delta, conv_weight, conv_bias, a, delta_bias, du, dstep, dg, new(xbc), new(delta),
+                                            new(conv_weight), new(conv_bias) if conv_bias is not None else None, new(a),
+                                            new(delta_bias), offsets, silu=silu, stream=stream)
 
 
 def _scan(x, step, g, bm, cm, d, initial_state, final_state, offsets, path, workspace, stream, y, want_state):
     import torch
 
-    lead, B, T, off = _lead(x, 2, offsets)
+    dev = _device(x)
+    lead, B, T, off = _lead(x, 2, offsets, dev)
     H, P = x.shape[-2:]
     G, N = bm.shape[-2:]
     dtype, f32, dt, pth = x.dtype, torch.float32, _dtype_code(x), PATHS[path]
     full, heads, keys, state = (*lead, H, P), (*lead, H), (*lead, G, N), (B, H, N, P)
-    rx = _rows(x, dtype, full, 2, "x")
+    rx = _rows(x, dtype, full, 2, "x", dev)
     if y is None:
         y = torch.empty(full, dtype=dtype, device=x.device)
         py = y.data_ptr()
     else:
-        py = _dense(y, dtype, full, "y")
+        py = _dense(y, dtype, full, "y", dev)
     if want_state:
         final_state = torch.empty(state, dtype=f32, device=x.device)
-    ws, pw, nw = _workspace(_size_of("gdn2_ssm_chunk_fwd_workspace_size", pth, B, T, H, G, P, N, int(off is not None), dt), x, workspace)
+    ws, pw, nw = _workspace(_size_of("gdn2_ssm_chunk_fwd_workspace_size", dev, pth, B, T, H, G, P, N, int(off is not None), dt), x, workspace, dev)
     _check(lib.gdn2_ssm_chunk_fwd(
-        pth, *rx, _dense(step, dtype, heads, "step"), _dense(g, dtype, heads, "g"), *_rows(bm, dtype, keys, 2, "bm"),
-        *_rows(cm, dtype, keys, 2, "cm"), _dense(d, f32, (H,), "d"), _dense(initial_state, f32, state, "initial_state"),
-        _dense(final_state, f32, state, "final_state"), off, py, B, T, H, G, P, N, dt, pw, nw, _raw_stream(stream, x)),
+        pth, *rx, _dense(step, dtype, heads, "step", dev), _dense(g, dtype, heads, "g", dev), *_rows(bm, dtype, keys, 2, "bm", dev),
+        *_rows(cm, dtype, keys, 2, "cm", dev), _dense(d, f32, (H,), "d", dev), _dense(initial_state, f32, state, "initial_state", dev),
+        _dense(final_state, f32, state, "final_state", dev), off, py, B, T, H, G, P, N, dt, pw, nw, _raw_stream(stream, dev)),
         "gdn2_ssm_chunk_fwd")
     return y, final_state
 
@@ -601,35 +618,36 @@ def ssm_chunk_fwd(x, step, g, bm, cm, d=None, initial_state=None, offsets=None, 
 def _scan_grad(x, step, g, bm, cm, d_y, d, initial_state, d_final_state, offsets, path, workspace, stream, outs):
     import torch
 
-    lead, B, T, off = _lead(x, 2, offsets)
+    dev = _device(x)
+    lead, B, T, off = _lead(x, 2, offsets, dev)
     H, P = x.shape[-2:]
     G, N = bm.shape[-2:]
     dtype, f32, dt, pth = x.dtype, torch.float32, _dtype_code(x), PATHS[path]
     full, heads, keys, state = (*lead, H, P), (*lead, H), (*lead, G, N), (B, H, N, P)
-    rx, rb, rc = _rows(x, dtype, full, 2, "x"), _rows(bm, dtype, keys, 2, "bm"), _rows(cm, dtype, keys, 2, "cm")
+    rx, rb, rc = _rows(x, dtype, full, 2, "x", dev), _rows(bm, dtype, keys, 2, "bm", dev), _rows(cm, dtype, keys, 2, "cm", dev)
     if outs is None:
-        dev, hp, gn = x.device, H * P, G * N
+        at, hp, gn = x.device, H * P, G * N
         ch = hp + 2 * gn
-        row = torch.empty((*lead, ch), dtype=dtype, device=dev)
+        row = torch.empty((*lead, ch), dtype=dtype, device=at)
         back = (ch,) if off is not None else (T * ch, ch)
         dx = row.as_strided(full, (*back, P, 1))
         dbm, dcm = row.as_strided(keys, (*back, N, 1), hp), row.as_strided(keys, (*back, N, 1), hp + gn)
-        dstep, dg = torch.empty(heads, dtype=dtype, device=dev), torch.empty(heads, dtype=dtype, device=dev)
-        dd = torch.empty((H,), dtype=f32, device=dev) if d is not None else None
-        ds0 = torch.empty(state, dtype=f32, device=dev) if initial_state is not None else None
+        dstep, dg = torch.empty(heads, dtype=dtype, device=at), torch.empty(heads, dtype=dtype, device=at)
+        dd = torch.empty((H,), dtype=f32, device=at) if d is not None else None
+        ds0 = torch.empty(state, dtype=f32, device=at) if initial_state is not None else None
         outs = (dx, dstep, dg, dbm, dcm, dd, ds0)
         base, es = row.data_ptr(), row.element_size()
         ox, ob, oc = (base, ch), (base + es * hp, ch), (base + es * (hp + gn), ch)
     else:
         dx, dstep, dg, dbm, dcm, dd, ds0 = outs
-        ox, ob, oc = _rows(dx, dtype, full, 2, "dx"), _rows(dbm, dtype, keys, 2, "dbm"), _rows(dcm, dtype, keys, 2, "dcm")
-    ws, pw, nw = _workspace(_size_of("gdn2_ssm_backward_workspace_size", pth, B, T, H, G, P, N, int(off is not None), dt), x, workspace)
+        ox, ob, oc = _rows(dx, dtype, full, 2, "dx", dev), _rows(dbm, dtype, keys, 2, "dbm", dev), _rows(dcm, dtype, keys, 2, "dcm", dev)
+    ws, pw, nw = _workspace(_size_of("gdn2_ssm_backward_workspace_size", dev, pth, B, T, H, G, P, N, int(off is not None), dt), x, workspace, dev)
     _check(lib.gdn2_ssm_backward(
-        pth, *rx, _dense(step, dtype, heads, "step"), _dense(g, dtype, heads, "g"), *rb, *rc, _dense(d, f32, (H,), "d"),
-        _dense(initial_state, f32, state, "initial_state"), *_rows(d_y, dtype, full, 2, "d_y"),
-        _dense(d_final_state, f32, state, "d_final_state"), off, *ox, _dense(dstep, dtype, heads, "dstep"),
-        _dense(dg, dtype, heads, "dg"), *ob, *oc, _dense(dd, f32, (H,), "dd"), _dense(ds0, f32, state, "d_initial_state"),
-        B, T, H, G, P, N, dt, pw, nw, _raw_stream(stream, x)), "gdn2_ssm_backward")
+        pth, *rx, _dense(step, dtype, heads, "step", dev), _dense(g, dtype, heads, "g", dev), *rb, *rc, _dense(d, f32, (H,), "d", dev),
+        _dense(initial_state, f32, state, "initial_state", dev), *_rows(d_y, dtype, full, 2, "d_y", dev),
+        _dense(d_final_state, f32, state, "d_final_state", dev), off, *ox, _dense(dstep, dtype, heads, "dstep", dev),
+        _dense(dg, dtype, heads, "dg", dev), *ob, *oc, _dense(dd, f32, (H,), "dd", dev), _dense(ds0, f32, state, "d_initial_state", dev),
+        B, T, H, G, P, N, dt, pw, nw, _raw_stream(stream, dev)), "gdn2_ssm_backward")
     return outs
 
 
@@ -661,6 +679,7 @@ def gdn2_ssm_decode_step(xbc, delta, conv_weight, conv_bias, a, delta_bias, d, c
     """
     import torch
 
+    dev = _device(xbc)
     B, ch = xbc.shape
     rows, H, N, P = state.shape
     G = (ch - H * P) // (2 * N)
@@ -672,18 +691,18 @@ def gdn2_ssm_decode_step(xbc, delta, conv_weight, conv_bias, a, delta_bias, d, c
     if y is None:
         y = torch.empty((B, H, P), dtype=dtype, device=xbc.device)
     _check(lib.gdn2_ssm_decode_step(
-        *_rows(xbc, dtype, (B, ch), 1, "xbc"), *_rows(delta, dtype, (B, H), 1, "delta"), _dense(conv_weight, f32, (ch, 4), "conv_weight"),
-        _dense(conv_bias, f32, (ch,), "conv_bias"), _dense(a, f32, (H,), "a"), _dense(delta_bias, f32, (H,), "delta_bias"),
-        _dense(d, f32, (H,), "d"), _dense(conv_state, f32, (rows, 3, ch), "conv_state"), _dense(state, state.dtype, state.shape, "state"),
-        _dtype_code(state), _dense(slots, torch.int32, (B,), "slots"), rows if slots is not None else 0,
-        _dense(y, dtype, (B, H, P), "y"), B, H, G, P, N, _dtype_code(xbc), _raw_stream(stream, xbc)), "gdn2_ssm_decode_step")
+        *_rows(xbc, dtype, (B, ch), 1, "xbc", dev), *_rows(delta, dtype, (B, H), 1, "delta", dev), _dense(conv_weight, f32, (ch, 4), "conv_weight", dev),
+        _dense(conv_bias, f32, (ch,), "conv_bias", dev), _dense(a, f32, (H,), "a", dev), _dense(delta_bias, f32, (H,), "delta_bias", dev),
+        _dense(d, f32, (H,), "d", dev), _dense(conv_state, f32, (rows, 3, ch), "conv_state", dev), _dense(state, state.dtype, state.shape, "state", dev),
+        _dtype_code(state), _dense(slots, torch.int32, (B,), "slots", dev), rows if slots is not None else 0,
+        _dense(y, dtype, (B, H, P), "y", dev), B, H, G, P, N, _dtype_code(xbc), _raw_stream(stream, dev)), "gdn2_ssm_decode_step")
     return y
 
 
 @_on_stream
 def ssm_decode_step(xbc, delta, conv_weight, conv_bias, a, delta_bias, d, conv_state, state, slots=None, *, stream=None):
     """Returns y [B, H, P]; conv_state and state are updated in place. Rows of inactive slots are left unwritten."""
-    return gdn2_ssm_decode_step(xbc, delta, conv_weight, conv_bias, a, delta_bias, d, conv_state, state, None, slots, stream=stream)
+    return gdn2_ssm_decode_step.plain(xbc, delta, conv_weight, conv_bias, a, delta_bias, d, conv_state, state, None, slots, stream=stream)
 
 
 def gdn2_block_norm(x, z, post_weight, residual, scale, pre_weight, r, n, *, groups=1, eps=1e-5, stream=None):
@@ -692,14 +711,15 @@ def gdn2_block_norm(x, z, post_weight, residual, scale, pre_weight, r, n, *, gro
     may each be None; r may be None when n is wanted alone. x, z, residual, r, n: [..., d]; weights: float32 [d]."""
     import torch
 
+    dev = _device(x)
     shape, dtype, f32 = x.shape, x.dtype, torch.float32
     dim = shape[-1]
     vec = (dim,)
     _check(lib.gdn2_block_norm(
-        _dense(x, dtype, shape, "x"), _dense(z, dtype, shape, "z"), _dense(post_weight, f32, vec, "post_weight"),
-        _dense(residual, dtype, shape, "residual"), _dense(scale, f32, vec, "scale"), _dense(pre_weight, f32, vec, "pre_weight"),
-        _dense(r, dtype, shape, "r"), _dense(n, dtype, shape, "n"), x.numel() // dim if dim else 0, dim, groups, float(eps),
-        _dtype_code(x), _raw_stream(stream, x)), "gdn2_block_norm")
+        _dense(x, dtype, shape, "x", dev), _dense(z, dtype, shape, "z", dev), _dense(post_weight, f32, vec, "post_weight", dev),
+        _dense(residual, dtype, shape, "residual", dev), _dense(scale, f32, vec, "scale", dev), _dense(pre_weight, f32, vec, "pre_weight", dev),
+        _dense(r, dtype, shape, "r", dev), _dense(n, dtype, shape, "n", dev), x.numel() // dim if dim else 0, dim, groups, float(eps),
+        _dtype_code(x), _raw_stream(stream, dev)), "gdn2_block_norm")
     return r, n
 
 
@@ -721,17 +741,18 @@ def gdn2_block_norm_backward(x, z, post_weight, residual, scale, pre_weight, d_r
     pre_weight): one output for each input given; dresidual may be None."""
     import torch
 
+    dev = _device(x)
     shape, dtype, f32 = x.shape, x.dtype, torch.float32
     dim = shape[-1]
     rows, vec = x.numel() // dim if dim else 0, (dim,)
-    ws, pw, nw = _workspace(_size_of("gdn2_block_norm_backward_workspace_size", rows, dim), x, workspace)
-    tok = lambda t, k: _dense(t, dtype, shape, k)
-    par = lambda t, k: _dense(t, f32, vec, k)
+    ws, pw, nw = _workspace(_size_of("gdn2_block_norm_backward_workspace_size", dev, rows, dim), x, workspace, dev)
+    tok = lambda t, k: _dense(t, dtype, shape, k, dev)
+    par = lambda t, k: _dense(t, f32, vec, k, dev)
     _check(lib.gdn2_block_norm_backward(
         tok(x, "x"), tok(z, "z"), par(post_weight, "post_weight"), tok(residual, "residual"), par(scale, "scale"),
         par(pre_weight, "pre_weight"), tok(d_r, "d_r"), tok(d_n, "d_n"), tok(dx, "dx"), tok(dz, "dz"),
         par(dpost_weight, "dpost_weight"), tok(dresidual, "dresidual"), par(dscale, "dscale"), par(dpre_weight, "dpre_weight"),
-        rows, dim, groups, float(eps), _dtype_code(x), pw, nw, _raw_stream(stream, x)), "gdn2_block_norm_backward")
+        rows, dim, groups, float(eps), _dtype_code(x), pw, nw, _raw_stream(stream, dev)), "gdn2_block_norm_backward")
     return dx, dz, dpost_weight, dresidual, dscale, dpre_weight
 
 
@@ -742,5 +763,5 @@ def block_norm_backward(x, z=None, post_weight=None, residual=None, scale=None, 
     import torch
 
     new = lambda t: torch.empty_like(t) if t is not None else None
-    return gdn2_block_norm_backward(x, z, post_weight, residual, scale, pre_weight, d_r, d_n, new(x), new(z), new(post_weight),
-                                    new(residual), new(scale), new(pre_weight), groups=groups, eps=eps, stream=stream)
+    return gdn2_block_norm_backward.plain(x, z, post_weight, residual, scale, pre_weight, d_r, d_n, new(x), new(z), new(post_weight),
+                                          new(residual), new(scale), new(pre_weight), groups=groups, eps=eps, stream=stream)
