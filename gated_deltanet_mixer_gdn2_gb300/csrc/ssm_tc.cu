@@ -483,6 +483,7 @@ template <int kParts>
 cudaError_t launch_scan(const ScanMaps& maps, const ScanTcArgs& a, dim3 grid, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(scan_tc_kernel<kParts>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
     if (e != cudaSuccess) return e;
+    g_launched.store(true, std::memory_order_relaxed);
     // the whole shared memory: one block per SM, and no operand descriptor reaches past the block's own
     scan_tc_kernel<kParts><<<grid, kScanThreads, 232448, s>>>(maps, a);
     return cudaGetLastError();

@@ -3,6 +3,8 @@
 // namespace has internal linkage; each translation unit has its own device status word.
 #pragma once
 
+#include <atomic>
+
 #include "ssm_common.cuh"
 #include "tc_common.cuh"
 
@@ -96,7 +98,12 @@ bool rows_map(CUtensorMap* m, const void* p, long long ld, int width, int heads,
     return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Whether this translation unit's kernels have been launched or captured in this process. Until then their status word
+// holds nothing, and reading it (two waits of the stream) would only make the other kernels' status later.
+std::atomic<bool> g_launched{false};
+
 int read_clear_status(cudaStream_t s) {
+    if (!g_launched.load(std::memory_order_relaxed)) return 0;
     int v = 0;
     if (cudaMemcpyFromSymbolAsync(&v, g_status_tc, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess) return -1;
     if (cudaStreamSynchronize(s) != cudaSuccess) return -1;

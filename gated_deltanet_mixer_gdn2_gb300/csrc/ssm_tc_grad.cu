@@ -742,6 +742,7 @@ cudaError_t launch_ssm_tc_bwd(const ScanShape& sh, const ScanIn& in, const ScanG
     a.dd_part = gr.dd ? f(p.dd) : nullptr;
     a.wait_ns = wait_ns;
     if ((e = cudaFuncSetAttribute(grad_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448)) != cudaSuccess) return e;
+    g_launched.store(true, std::memory_order_relaxed);
     // groups' shares of one chunk next to each other: B, C and the gates stay in L2
     grad_tc_kernel<<<dim3(sh.G * p.splits, static_cast<unsigned>(sh.seqs.units(kQ))), kGradTc, 232448, s>>>(maps, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -301,6 +301,7 @@ cudaError_t launch_ssm_walk_tc(const ScanShape& sh, const void* step, const void
     const uint32_t smem = exact ? Sw<3>::kAlloc : Sw<1>::kAlloc;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
+    g_launched.store(true, std::memory_order_relaxed);
     kernel<<<dim3(sh.H * (sh.P / kCols), static_cast<unsigned>(sh.seqs.units(unit)), n_jobs), kWalkThreadsTc, smem, s>>>(maps, a);
     return cudaGetLastError();
 }
