@@ -9,12 +9,14 @@
 // over R^T in tensor memory as operands; dB and dC accumulate there over the block's heads, so the sum over a
 // group's heads costs nothing. The double sum of dg is a suffix sum of (row sums - column sums) of one fp32
 // matrix: what cancels in it cancels exactly.
-// Roundings: the pair matrices, e^L dY, X~ and the saved states are bf16 operands, once each, of products whose sums are
-// fp32; row and column sums, dstep's and dg's sums and dD are fp32 throughout.
-// 4 x 2048 tokens, 32 heads of 64 values, N = 128: 90 us of a call's 137 (walk 41, sums 7; CUDA cores: 1870). A head of a
-// chunk takes about 10000 cycles: the pair matrices, 4500 (a fifth of it the sums across lanes), the state's shares 1800, U
-// 800, dx 2000, each waiting for the one before; its 48 products take 3500 to issue, beside the rest. What limits overlapping two
-// heads is tensor memory: dB, dC and one pair matrix take three quarters of it.
+// Roundings: the pair matrices and the saved states are bf16 operands, once each, of products whose sums are fp32; e^L dY
+// and X~, which meet the states, enter as two bf16 parts (2^-16), so that no term of dB or dC has two roundings to bf16 before
+// the result's own. Row and column sums, dstep's and dg's sums and dD are fp32 throughout.
+// 4 x 2048 tokens, 32 heads of 64 values, N = 128: 96 us of a call's 143 (walk 41, sums 7; CUDA cores: 1870); with one part of e^L dY
+// and X~ 90 us, and dC off by 2.9e-3 of its norm instead of 2.4e-3 where given states are most of it (its own rounding: 1.7e-3). A
+// head of a chunk takes about 10700 cycles: the pair matrices, 4500 (a fifth of it the sums across lanes), the state's
+// shares 1800, U 800, dx 2000, each waiting for the one before; its 60 products take 4200 to issue, beside the rest. What limits
+// overlapping two heads is tensor memory: dB, dC and one pair matrix take three quarters of it.
 #include <cuda_fp16.h>
 
 #include "ssm_tc.cuh"
@@ -26,10 +28,10 @@ namespace {
 namespace sg {
 constexpr uint32_t B = 0;                         // 2 tiles
 constexpr uint32_t C = B + 2 * kTileBytes;        // 2 tiles
-constexpr uint32_t X = C + 2 * kTileBytes;        // 2 stages; X~ replaces X
+constexpr uint32_t X = C + 2 * kTileBytes;        // 2 stages; X~'s first part replaces X
 constexpr uint32_t DY = X + 2 * kTileBytes;       // 2 stages; dx leaves through dY's room
-constexpr uint32_t DYW = DY + 2 * kTileBytes;     // e^{L} dY
-constexpr uint32_t H0 = DYW + kTileBytes;
+constexpr uint32_t XL = DY + 2 * kTileBytes;      // X~'s second part
+constexpr uint32_t H0 = XL + kTileBytes;
 constexpr uint32_t DH = H0 + kTileBytes;
 constexpr uint32_t P1 = DH + kTileBytes;          // (R W s)^T [j][i]: 2 tiles
 constexpr uint32_t GATE = P1 + 2 * kTileBytes;    // 2 stages x {L, s, wend, eL, col}[128]
@@ -48,7 +50,7 @@ enum GradBar {
 static_assert(gBars * 8 + 16 <= 256, "barrier room");
 
 // tensor-memory columns: S^T, then each head's R^T and, in its place, per 16 columns 8 packed of (R W s)^T and 8
-// of (S W)^T; dB; dC; C H; U
+// of (S W)^T; dB; dC; C H, then in its place, per 16 columns, 8 packed of each part of e^L dY; U
 constexpr uint32_t kTR = 0, kTdB = 128, kTdC = 256, kTT = 384, kTU = 448;
 constexpr int kGradTc = 640;  // sixteen compute warps, then results, copies, gates, products
 
@@ -78,10 +80,11 @@ __device__ __forceinline__ uint64_t pair_of(const uint4 (&v)[2], int k) {
     const uint4& u = v[k >> 2];
     return bf16x2_widen((k & 3) == 0 ? u.x : (k & 3) == 1 ? u.y : (k & 3) == 2 ? u.z : u.w);
 }
-__device__ __forceinline__ uint4 scaled8(const uint4& u, float w) {
-    const uint64_t w2 = f32x2(w, w);
-    return make_uint4(bf16x2_narrow(mul_f32x2(bf16x2_widen(u.x), w2)), bf16x2_narrow(mul_f32x2(bf16x2_widen(u.y), w2)),
-                      bf16x2_narrow(mul_f32x2(bf16x2_widen(u.z), w2)), bf16x2_narrow(mul_f32x2(bf16x2_widen(u.w), w2)));
+// A pair times w as two bf16 parts.
+__device__ __forceinline__ void scaled_parts(uint32_t u, uint64_t w2, uint32_t& hi, uint32_t& lo) {
+    const uint64_t v = mul_f32x2(bf16x2_widen(u), w2);
+    hi = bf16x2_narrow(v);
+    lo = bf16x2_narrow(sub_f32x2(v, bf16x2_widen(hi)));
 }
 
 // Sum over the warp's lanes of each of 32 values: lane l returns the sum of v[l]. Each step halves the values.
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
                 }
                 rsum = transpose_sum(pf, lane);
             }
-            // the products of the head before have read (R W s) and e^L dY
+            // the products of the head before have read (R W s) and X~
             if (it && !(ok = wait_bar(bars + gAll, ph1 ^ 1, lim, err))) break;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -264,21 +267,27 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
                 *to = fresh ? rsum : *to + rsum;
             }
             keep(1, cols);
-            // X~ in place of X, e^{L} dY beside dY
+            // X~: one part in place of X
             const uint4 xr[2] = {*reinterpret_cast<const uint4*>(xt + cell0), *reinterpret_cast<const uint4*>(xt + cell1)};
             const uint4 yr[2] = {*reinterpret_cast<const uint4*>(yt + cell0), *reinterpret_cast<const uint4*>(yt + cell1)};
-            uint8_t* wt = sm + sg::DYW + j * 128;
+            uint8_t* xl = sm + sg::XL + j * 128;
             const float wx = sj * wej;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int cell = k ? cell1 : cell0;
-                *reinterpret_cast<uint4*>(xt + cell) = scaled8(xr[k], wx);
-                *reinterpret_cast<uint4*>(wt + cell) = scaled8(yr[k], eLj);
+                const uint64_t w2 = f32x2(wx, wx);
+                uint4 hi, lo;
+                scaled_parts(xr[k].x, w2, hi.x, lo.x);
+                scaled_parts(xr[k].y, w2, hi.y, lo.y);
+                scaled_parts(xr[k].z, w2, hi.z, lo.z);
+                scaled_parts(xr[k].w, w2, hi.w, lo.w);
+                *reinterpret_cast<uint4*>(xt + cell) = hi;
+                *reinterpret_cast<uint4*>(xl + cell) = lo;
             }
             if (!(ok = wait_bar(bars + gTu, ph1, lim, err))) break;
             tc_fence_after();
             {
-                // B A in U's columns: its share of dg, then scaled as U's start; C H: its share of dg
+                // B A in U's columns: its share of dg, then scaled as U's start; C H: its share of dg, then the parts of e^L dY
                 uint32_t t[16], c[16];
                 tmem_ld16(val + kTU, t);
                 tmem_ld16(val + kTT, c);
@@ -295,6 +304,13 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
                     t[2 * k + 1] = __float_as_uint(b1);
                 }
                 tmem_st16(val + kTU, t);
+                const uint64_t eL2 = f32x2(eLj, eLj);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint4& u = yr[k >> 2];
+                    scaled_parts((k & 3) == 0 ? u.x : (k & 3) == 1 ? u.y : (k & 3) == 2 ? u.z : u.w, eL2, c[k], c[8 + k]);
+                }
+                tmem_st16(val + kTT, c);
                 keep(2, sum_of(vs) * wx);
                 keep(3, sum_of(qs) * eLj);
             }
@@ -504,20 +520,24 @@ __global__ void __launch_bounds__(kGradTc, 1) grad_tc_kernel(const __grid_consta
             mma_steps<false, kStepK, kStepMn, kJumpK, 0>(lead, kTU, dk + (sg::B >> 4), dm + (sg::DH >> 4), id_t, 0, ks);
             commit_by(lead, bars + gTu);
             if (!(ok = wait(gPReady, ph1))) break;
-            // what the block waits for first: U += (S W)^T dY; then dB += (R W s)^T C + X~ A^T, the last reader of the pair
-            // matrices' room, which the next head's R^T takes; dC last, beside the next head's pair matrices
+            // what the block waits for first: U += (S W)^T dY; then dB += (R W s)^T C, the last reader of the pair matrices'
+            // room, which the next head's R^T takes; the rest beside the next head's pair matrices
             mma_steps<true, 16, kStepMn, 0, 0>(lead, kTU, kTR + 8, dm + yo, id_t, 1, 8);
             commit_by(lead, bars + gDx);
             mma_steps<true, 16, kStepMn, 0, 0>(lead, kTdB, kTR, dm + (sg::C >> 4), id_nm, it > 0, 8);
-            mma_steps<false, kStepK, kStepK, 0, 0>(lead, kTdB, dk + xo, dk + (sg::DH >> 4), id_nk, 1, 4);
             commit_by(lead, bars + gTrFree);
             if (it + 1 < NI && !(ok = wait(gTrFree, ph1) && pairs(it + 1))) break;
-            // dC += (R W s) B + (e^L dY) H^T
-            mma_steps<false, kStepMn, kStepMn, 0, 0>(lead, kTdC, dm + (sg::P1 >> 4), dm + (sg::B >> 4), id_mm, it > 0, 8);
-            mma_steps<false, kStepK, kStepK, 0, 0>(lead, kTdC, dk + (sg::DYW >> 4), dk + (sg::H0 >> 4), id_nk, 1, 4);
+            // the states' products first, for the next H and A wait for their room: dB += X~ A^T, dC += (e^L dY) H^T. C H of the next
+            // head, which takes the room of e^L dY, waits for that copy
+            mma_steps<false, kStepK, kStepK, 0, 0>(lead, kTdB, dk + xo, dk + (sg::DH >> 4), id_nk, 1, 4);
+            mma_steps<false, kStepK, kStepK, 0, 0>(lead, kTdB, dk + (sg::XL >> 4), dk + (sg::DH >> 4), id_nk, 1, 4);
+            mma_steps<true, 16, kStepK, 0, 0>(lead, kTdC, kTT, dk + (sg::H0 >> 4), id_nk, it > 0, 4);
+            mma_steps<true, 16, kStepK, 0, 0>(lead, kTdC, kTT + 8, dk + (sg::H0 >> 4), id_nk, 1, 4);
+            commit_by(lead, bars + gHdFree);
+            // dC += (R W s) B
+            mma_steps<false, kStepMn, kStepMn, 0, 0>(lead, kTdC, dm + (sg::P1 >> 4), dm + (sg::B >> 4), id_mm, 1, 8);
             commit_by(lead, bars + gAll);
             commit_by(lead, bars + gXyDone + st);
-            commit_by(lead, bars + gHdFree);
         }
         commit_by(lead, bars + gDrain);
         mbar_wait(bars + gDrain, 0, kDefaultWaitNs);
