@@ -261,7 +261,8 @@ struct NormGradArgs {
 // dx = dt silu(z), dz = dt x silu'(z). dpost and dscale are one sum over the rows, of dr th, times scale and post; it and
 // dpre's, and the weights, stay in registers over the block's rows, the next row's loads in flight. 8192 x 2048 bf16 with
 // all of its inputs: 67 us with the sums, 4 TB/s, 59% of the copy rate: the sums' registers leave room for 16 warps, and two row sums
-// with their barriers stand between a row's loads and its stores.
+// with their barriers stand between a row's loads and its stores. Two vectors per thread (above 4096 columns) do not fit the
+// registers and spill: 2048 x 8192 takes 150 us, 2048 x 4096 48 us.
 template <typename T, int VPT, int kMaxThreads, int kPerSm>
 __global__ void __launch_bounds__(kMaxThreads, kPerSm)
     norm_grad_kernel(NormGradArgs ga, const T* x, const T* z, const T* residual, const T* d_r, const T* d_n, T* dx, T* dz, T* dres) {

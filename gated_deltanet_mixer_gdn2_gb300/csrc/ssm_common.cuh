@@ -135,7 +135,8 @@ __device__ __forceinline__ bool find_row(const Seqs& s, int r, int& seq, int& st
     return r >= start && r < end;
 }
 
-// 1 / (1 + e^-v) with the hardware's approximations (each within 2 units in the last place)
+// 1 / (1 + e^-v) with the hardware's approximations, each within 2 units in the last place, of an argument rounded once: relative
+// error 2^-22 + 2^-23 |v| where e^-v counts (1e-6 at v = -20)
 __device__ __forceinline__ float ssm_sigmoid(float v) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-kLog2e * v)));
@@ -181,7 +182,7 @@ struct ScanIn {
     const float *d, *s0;       // [H] or null; [B, H, N, P] or null
 };
 
-// Launchers of the two kernel families (ssm_scan.cu: CUDA cores; ssm_tc.cu: tensor cores).
+// Launchers of the two kernel families (ssm_scan.cu: CUDA cores; ssm_tc*.cu: tensor cores).
 size_t ssm_simt_fwd_workspace(const ScanShape& sh);
 cudaError_t launch_ssm_simt_fwd(const ScanShape& sh, const ScanIn& in, void* y, float* s1, void* ws, cudaStream_t s);
 

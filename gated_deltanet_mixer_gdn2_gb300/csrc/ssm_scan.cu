@@ -1,5 +1,5 @@
-// ssm_scan.cu -- the selective state-space scan on CUDA cores, any dtype and every supported shape, and
-// its entry points (argument checks and the choice of the kernel family).
+// ssm_scan.cu -- the selective state-space scan and its gradients on CUDA cores, any dtype and every supported shape
+// (entry points, argument checks and the choice of the kernel family: ssm_api.cu).
 //
 // Per sequence and head, on a state H in R^{N x P}, with a scalar log-decay g_t <= 0, a step s_t, keys
 // B_t and readouts C_t (R^N, shared by the heads of a group) and values x_t (R^P):
@@ -245,7 +245,7 @@ struct GradSmem {
 // cancels in it cancels exactly. Every exponent is <= 0, and each is a sum of just the gates that it stands for: as a difference
 // of two L it would lose the digits of ordinary decays behind strong ones (fp32, twelve resets before them: 3.5e-4).
 // Multiply-adds from shared memory bound it, two blocks per SM: fp32, 1364 packed tokens, 8 heads of 64 values, N = 64,
-// 50 us of a call's 72 (walk of both directions 21, chain 10, sums 4), 27000 of each scheduler's 62000 cycles issuing.
+// 50 us of a call's 74 (walk of both directions 21, chain 10, sums 4), 28000 of each scheduler's 64000 cycles issuing.
 // Value columns in halves of 32, which let three blocks share an SM, took 79 us instead of 75.
 template <typename T, int N, int PB>
 __global__ void __launch_bounds__(kGradThreads, N <= 64 ? 2 : 1)

@@ -99,7 +99,7 @@ __device__ __forceinline__ void gate_arrays(float* arr, int lane, const float (&
 }
 
 // kParts bf16 parts of X~ enter the state's product: one where the state only feeds bf16 results, three
-// (2^-24 of every term) where it is returned in fp32 (4 x 2048 tokens of 32 heads: 35 and 49 us).
+// (2^-24 of every term) where it is returned in fp32 (4 x 2048 tokens of 32 heads: 32 and 49 us).
 template <int kParts>
 __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_constant__ ScanMaps maps, const ScanTcArgs a) {
     using so = So<kParts>;
@@ -498,7 +498,8 @@ bool ssm_tc_shape(const ScanShape& sh) {
 namespace {
 // Tokens per block: whole sequences while their chains fill four fifths of the SMs, else units whose starting states come
 // from a pass over their increments (2 x 32768 tokens, 32 heads, with the last state: 386 us cut, 607 whole; 1 x 8192, 8 heads: 43
-// and 96; a packed batch of 8 with enough chains: 138 cut, 95 whole).
+// and 96; a packed batch of 8 with enough chains: 138 cut, 95 whole). The rule sees the number of sequences, not their lengths:
+// one of 30000 tokens among seven of a few takes 348 us, 197 alone.
 int fwd_unit(const ScanShape& sh) {
     int dev = 0, sms = 152;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) sms = 152;

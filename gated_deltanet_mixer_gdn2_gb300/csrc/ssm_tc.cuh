@@ -115,7 +115,7 @@ int read_clear_status(cudaStream_t s) {
 
 }  // namespace
 
-// One walk of the states over chunks (ssm_tc_bwd.cu): forward of B and x, or backward of C and dy.
+// One walk of the states over chunks (ssm_tc_walk.cu): forward of B and x, or backward of C and dy.
 struct WalkJob {
     Rows keys, values;       // B and x, or C and dy
     const float* first;      // [B][H][N][P] state at the sequences' start (back: adjoint at their end), or null

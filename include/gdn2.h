@@ -342,14 +342,16 @@ gdn2_status gdn2_backward_recurrent(const void* q, const void* k, const void* v,
  *   - Sequences: offsets == NULL means B sequences of T tokens, token t of sequence b in row b * T + t.
  *     Otherwise offsets is an int32 device array of B + 1 entries and sequence b is rows
  *     [offsets[b], offsets[b + 1]) of T rows in all; sequences may be empty, and rows outside all of them
- *     are left unwritten. Offsets are read on the device and clamped to [0, T] there.
+ *     are neither read into any result nor written. Offsets ascend; they are read on the device and clamped
+ *     to [0, T] there, so that wrong ones give wrong results, but no access outside tensors or workspace.
  *   - Rows: ld_* is the stride from one token row to the next in elements, for tensors that are slices of
  *     wider rows; within a row heads and channels are dense. Rows of x, bm, cm, d_y and their gradients start
  *     on 16-byte boundaries and their ld is a multiple of 8 (GDN2_ERR_MISALIGNED). Rows of xbc, du, delta and
  *     their gradients, and step and g, need only their element's alignment (wider is faster for xbc and du).
  *     Tensors without ld are contiguous.
- *   - A token that is not finite makes its own sequence's results from its chunk on (128 tokens, or the
- *     token itself on the CUDA-core path) not finite; it never reaches another sequence.
+ *   - A token that is not finite, in its gates too (only g = -inf is a value, a full reset), makes its own
+ *     sequence's results from its chunk on (128 tokens, or the token itself on the CUDA-core path) not
+ *     finite; it never reaches another sequence.
  * Errors: GDN2_ERR_INVALID_ARG (dtype, sizes, H % G, null required pointer, ld below the row's width),
  * GDN2_ERR_UNSUPPORTED (shape not built, too large), GDN2_ERR_MISALIGNED, GDN2_ERR_WORKSPACE,
  * GDN2_ERR_CUDA. Asynchronous on `stream`; no entry point allocates or synchronises.
@@ -364,7 +366,8 @@ gdn2_status gdn2_backward_recurrent(const void* q, const void* k, const void* v,
  *   a (negative for a decay), delta_bias fp32 [H]
  *   conv_state  fp32 [B][3][channels] (x_{-3}, x_{-2}, x_{-1}) read and then replaced by the last three
  *               samples of [state, x]; NULL = zeros in, nothing written
- * channels a multiple of 8 (C of the scan, B and x side by side: H P + 2 G N). For one token pass T = 1.
+ * channels a multiple of 8 (C of the scan, B and x side by side: H P + 2 G N). For one token pass T = 1
+ * (gdn2_ssm_decode_step has the silu always).
  */
 gdn2_status gdn2_ssm_prologue(const void* xbc, long long ld_xbc, const void* delta, long long ld_delta,
                               const float* conv_weight, const float* conv_bias, const float* a,
@@ -396,7 +399,10 @@ gdn2_status gdn2_ssm_prologue_backward(const void* xbc, long long ld_xbc, const 
  *   d      fp32 [H] or NULL (0)
  *   initial_state, final_state  fp32 [B, H, N, P] or NULL (zeros / not written); may alias
  * The final state of an empty sequence is its initial state. Supported: P a multiple of 8 up to 256, N in
- * {16, 32, 64, 128, 256}; B <= 65535.
+ * {16, 32, 64, 128, 256}; B <= 65535. On the tensor cores (GDN2_PATH_TCGEN05, and GDN2_PATH_AUTO where it can):
+ * bf16, P a multiple of 64, N 64 or 128, and at most 65535 chunks of 128 tokens, every sequence's last one counted
+ * whole. There y has the same precision with final_state and without, but not the same bits: a returned state is
+ * formed from more parts of its inputs.
  * workspace: gdn2_ssm_chunk_fwd_workspace_size(...) bytes (packed != 0 for calls with offsets), 16-byte
  * aligned; may be NULL when that is 0.
  */
@@ -428,7 +434,8 @@ gdn2_status gdn2_ssm_backward(gdn2_path path, const void* x, long long ld_x, con
 
 /*
  * gdn2_ssm_decode_step -- one token of the mixer between its projections in one launch: the prologue's
- * convolution (with silu) and gates and the scan's update and readout, with u, step and g kept in fp32.
+ * convolution (with silu) and gates and the scan's update and readout, with u, step and g kept in fp32 (between
+ * prologue and scan they are rounded to dt: a prompt's decays differ from its tokens' by that rounding).
  *   xbc        [B, channels] dt, channels = H P + 2 G N: x, B and C side by side; delta [B, H] dt
  *   conv_state fp32 [B][3][channels] and state [B, H, N, P] of state_dt (GDN2_F32, or GDN2_BF16: widened on
  *              load, rounded on store), read and replaced; with slots (int32 [B]) both are pools of n_slots
