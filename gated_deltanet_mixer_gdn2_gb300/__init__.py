@@ -31,6 +31,8 @@ EXPORTS = (
     "gdn2_ssm_prologue", "gdn2_ssm_prologue_backward_workspace_size", "gdn2_ssm_prologue_backward",
     "gdn2_ssm_chunk_fwd_workspace_size", "gdn2_ssm_chunk_fwd", "gdn2_ssm_backward_workspace_size", "gdn2_ssm_backward",
     "gdn2_ssm_decode_step", "gdn2_block_norm", "gdn2_block_norm_backward_workspace_size", "gdn2_block_norm_backward",
+    "gdn2_attn_prologue", "gdn2_attn_prologue_paged", "gdn2_attn_prologue_backward_workspace_size", "gdn2_attn_prologue_backward",
+    "gdn2_attn_decode_workspace_size", "gdn2_attn_decode", "gdn2_pages_append", "gdn2_pages_fork", "gdn2_pages_release", "gdn2_pages_copy",
 )
 
 
@@ -80,6 +82,16 @@ def _load() -> ctypes.CDLL:
         "gdn2_block_norm": (I, [P] * 8 + [L, I, I, F, I, P]),
         "gdn2_block_norm_backward_workspace_size": (Z, [L, I]),
         "gdn2_block_norm_backward": (I, [P] * 14 + [L, I, I, F, I, P, Z, P]),
+        "gdn2_attn_prologue": (I, [P, L, P, L] + [P] * 7 + [I] * 7 + [F, I, P]),
+        "gdn2_attn_prologue_paged": (I, [P, L, P, L, P, L] + [P] * 11 + [I] * 4 + [I] * 7 + [F, I, P]),
+        "gdn2_attn_prologue_backward_workspace_size": (Z, [I] * 4),
+        "gdn2_attn_prologue_backward": (I, [P, L, P, L] + [P] * 5 + [P, L] * 4 + [P, P] + [I] * 7 + [F, I, P, Z, P]),
+        "gdn2_attn_decode_workspace_size": (Z, [I] * 5 + [I]),
+        "gdn2_attn_decode": (I, [P, L] + [P] * 5 + [I] * 4 + [P] + [I] * 5 + [F, I, I, P, Z, P]),
+        "gdn2_pages_append": (I, [P] * 5 + [I, P] + [I] * 5 + [P]),
+        "gdn2_pages_fork": (I, [P] * 8 + [I] * 5 + [P]),
+        "gdn2_pages_release": (I, [P] * 4 + [I] * 4 + [P]),
+        "gdn2_pages_copy": (I, [P, P, I, P, P, I, I, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -765,3 +777,248 @@ def block_norm_backward(x, z=None, post_weight=None, residual=None, scale=None, 
     new = lambda t: torch.empty_like(t) if t is not None else None
     return gdn2_block_norm_backward.plain(x, z, post_weight, residual, scale, pre_weight, d_r, d_n, new(x), new(z), new(post_weight),
                                           new(residual), new(scale), new(pre_weight), groups=groups, eps=eps, stream=stream)
+
+
+# ---- attention layers: norm and rotation, a cache in pages, attention over it ---------------------------------------
+
+def _turned(q, k, q_weight, k_weight, inv_freq, positions, offsets, dev):
+    """What the prologue's calls share: leading dimensions, sizes and the pointers of the tensors that all of them take."""
+    import torch
+
+    lead, B, T, off = _lead(q, 2, offsets, dev)
+    (Hq, d), Hkv, f32 = q.shape[-2:], k.shape[-2], torch.float32
+    if inv_freq is not None and inv_freq.dim() != 1:
+        raise ValueError("inv_freq holds one frequency for each pair of rotated elements")
+    rot = 2 * inv_freq.shape[0] if inv_freq is not None else 0
+    params = (_dense(q_weight, f32, (d,), "q_weight", dev), _dense(k_weight, f32, (d,), "k_weight", dev),
+              _dense(inv_freq, f32, (rot // 2,), "inv_freq", dev), _dense(positions, torch.int32, lead, "positions", dev), off)
+    heads, keys = (*lead, Hq, d), (*lead, Hkv, d)
+    return (*_rows(q, q.dtype, heads, 2, "q", dev), *_rows(k, q.dtype, keys, 2, "k", dev)), params, heads, keys, (B, T, Hq, Hkv, d, rot)
+
+
+@_on_stream
+def gdn2_attn_prologue(q, k, q_weight, k_weight, inv_freq, q_out, k_out, positions=None, offsets=None, *, interleaved=False, eps=1e-6,
+                       stream=None):
+    """RMS norm of each head of q and k and rotation by position (C ABI gdn2_attn_prologue); writes q_out and k_out.
+
+    q, q_out: [B, T, H_q, d]; k, k_out: [B, T, H_kv, d]; weights: float32 [d] or None (no norm); inv_freq: float32, one for each pair
+    of rotated elements, or None (no rotation); positions: int32 [B, T] or None (the index in the sequence). With offsets (int32
+    [B + 1], on the device) the sequences are packed and token tensors are [T, ...]. q and k may be slices of wider rows.
+    """
+    dev = _device(q)
+    rows, params, heads, keys, sizes = _turned(q, k, q_weight, k_weight, inv_freq, positions, offsets, dev)
+    _check(lib.gdn2_attn_prologue(*rows, *params, _dense(q_out, q.dtype, heads, "q_out", dev), _dense(k_out, q.dtype, keys, "k_out", dev),
+                                  *sizes, int(bool(interleaved)), float(eps), _dtype_code(q), _raw_stream(stream, dev)), "gdn2_attn_prologue")
+    return q_out, k_out
+
+
+@_on_stream
+def attn_prologue(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=None, offsets=None, *, interleaved=False, eps=1e-6,
+                  stream=None):
+    """Returns (q, k), normalised and rotated."""
+    import torch
+
+    return gdn2_attn_prologue.plain(q, k, q_weight, k_weight, inv_freq, torch.empty(q.shape, dtype=q.dtype, device=q.device),
+                                    torch.empty(k.shape, dtype=q.dtype, device=q.device), positions, offsets, interleaved=interleaved,
+                                    eps=eps, stream=stream)
+
+
+def _cache(table, lengths, slots, B, dev):
+    """Pointers and sizes of a cache's table, lengths and slots for a call of B rows."""
+    import torch
+
+    if table.dim() != 2:
+        raise ValueError("table is [n_slots, max_pages]")
+    rows = table.shape[0]
+    if slots is None and rows != B:
+        raise ValueError("without slots, the table has one row per sequence")
+    i32 = torch.int32
+    return (_dense(table, i32, table.shape, "table", dev), _dense(lengths, i32, (rows,), "lengths", dev),
+            _dense(slots, i32, (B,), "slots", dev)), rows, table.shape[1]
+
+
+def _pool(pages, dtype, Hkv, d, name, dev, like=None):
+    """Pointer of a layer's pool [n_pages, H_kv, page, d]."""
+    if pages.dim() != 4 or pages.shape[1] != Hkv or pages.shape[3] != d or (like is not None and pages.shape != like.shape):
+        raise ValueError(f"{name} is [n_pages, H_kv, page, d], alike for keys and values")
+    return _dense(pages, dtype, pages.shape, name, dev)
+
+
+@_on_stream
+def gdn2_attn_prologue_paged(q, k, v, k_pages, v_pages, table, lengths, q_out, slots=None, q_weight=None, k_weight=None, inv_freq=None,
+                             positions=None, offsets=None, *, interleaved=False, eps=1e-6, stream=None):
+    """The prologue for serving (C ABI gdn2_attn_prologue_paged): writes q_out, and k (normalised and rotated) and v to their places in
+    the cache.
+
+    q, k, v: as for gdn2_attn_prologue; k_pages, v_pages: [n_pages, H_kv, page, d]; table: int32 [n_slots, max_pages]; lengths: int32
+    [n_slots], the call's tokens among them; slots: int32 [B] or None. positions, if given, are for the angles alone.
+    """
+    dev = _device(q)
+    rows, params, heads, keys, sizes = _turned(q, k, q_weight, k_weight, inv_freq, positions, offsets, dev)
+    B, _, _, Hkv, d, _ = sizes
+    where, n_slots, wide = _cache(table, lengths, slots, B, dev)
+    if q_out is None:
+        import torch
+
+        q_out = torch.empty(heads, dtype=q.dtype, device=q.device)
+    _check(lib.gdn2_attn_prologue_paged(
+        *rows, *_rows(v, q.dtype, keys, 2, "v", dev), *params, _dense(q_out, q.dtype, heads, "q_out", dev),
+        _pool(k_pages, q.dtype, Hkv, d, "k_pages", dev), _pool(v_pages, q.dtype, Hkv, d, "v_pages", dev, k_pages), *where, n_slots,
+        k_pages.shape[0], wide, k_pages.shape[2], *sizes, int(bool(interleaved)), float(eps), _dtype_code(q), _raw_stream(stream, dev)),
+        "gdn2_attn_prologue_paged")
+    return q_out
+
+
+@_on_stream
+def attn_prologue_paged(q, k, v, k_pages, v_pages, table, lengths, slots=None, q_weight=None, k_weight=None, inv_freq=None, positions=None,
+                        offsets=None, *, interleaved=False, eps=1e-6, stream=None):
+    """Returns q, normalised and rotated; k_pages and v_pages are updated in place. Rows of inactive slots are left unwritten."""
+    return gdn2_attn_prologue_paged.plain(q, k, v, k_pages, v_pages, table, lengths, None, slots, q_weight, k_weight, inv_freq, positions,
+                                          offsets, interleaved=interleaved, eps=eps, stream=stream)
+
+
+@_on_stream
+def gdn2_attn_prologue_backward(q, k, dq_out, dk_out, q_weight, k_weight, inv_freq, dq, dk, dq_weight, dk_weight, positions=None,
+                                offsets=None, *, interleaved=False, eps=1e-6, workspace=None, stream=None):
+    """Gradients of gdn2_attn_prologue (C ABI gdn2_attn_prologue_backward) given those of its outputs; writes dq and dk (may be slices of
+    wider rows) and the float32 dq_weight and dk_weight, each with its weight."""
+    import torch
+
+    dev = _device(q)
+    rows, params, heads, keys, sizes = _turned(q, k, q_weight, k_weight, inv_freq, positions, offsets, dev)
+    B, T, _, _, d, _ = sizes
+    need = _size_of("gdn2_attn_prologue_backward_workspace_size", dev, B, T, d, int(offsets is not None)) if dq_weight is not None or dk_weight is not None else 0
+    ws, pw, nw = _workspace(need, q, workspace, dev)
+    _check(lib.gdn2_attn_prologue_backward(
+        *rows, *params, *_rows(dq_out, q.dtype, heads, 2, "dq_out", dev), *_rows(dk_out, q.dtype, keys, 2, "dk_out", dev),
+        *_rows(dq, q.dtype, heads, 2, "dq", dev), *_rows(dk, q.dtype, keys, 2, "dk", dev),
+        _dense(dq_weight, torch.float32, (d,), "dq_weight", dev), _dense(dk_weight, torch.float32, (d,), "dk_weight", dev), *sizes,
+        int(bool(interleaved)), float(eps), _dtype_code(q), pw, nw, _raw_stream(stream, dev)), "gdn2_attn_prologue_backward")
+    return dq, dk, dq_weight, dk_weight
+
+
+@_on_stream
+def attn_prologue_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, inv_freq=None, positions=None, offsets=None, *,
+                           interleaved=False, eps=1e-6, stream=None):
+    """Returns (dq, dk, dq_weight, dk_weight), the latter None without their weights."""
+    import torch
+
+    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=q.device) if t is not None else None
+    return gdn2_attn_prologue_backward.plain(q, k, dq_out, dk_out, q_weight, k_weight, inv_freq, new(q), new(k), new(q_weight), new(k_weight),
+                                             positions, offsets, interleaved=interleaved, eps=eps, stream=stream)
+
+
+@_on_stream
+def gdn2_attn_decode(q, k_pages, v_pages, table, lengths, o, slots=None, *, scale=None, window=0, workspace=None, stream=None):
+    """Attention of the newest tokens of each row over its cache (C ABI gdn2_attn_decode); writes o.
+
+    q, o: [B, N, H_q, d], or [B, H_q, d] for one token each (q may be a slice of wider rows); k_pages, v_pages: [n_pages, H_kv, page, d];
+    table: int32 [n_slots, max_pages]; lengths: int32 [n_slots], these tokens among them; slots: int32 [B] or None. Token n sees the
+    keys up to number lengths - N + n, with window > 0 the last `window` of them. scale: d ** -0.5 when None.
+    """
+    import torch
+
+    dev = _device(q)
+    if q.dim() not in (3, 4) or k_pages.dim() != 4:
+        raise ValueError("q is [B, N, H_q, d] or [B, H_q, d], k_pages [n_pages, H_kv, page, d]")
+    B, (Hq, d), N, Hkv = q.shape[0], q.shape[-2:], q.shape[1] if q.dim() == 4 else 1, k_pages.shape[1]
+    where, n_slots, wide = _cache(table, lengths, slots, B, dev)
+    dt = _dtype_code(q)
+    if o is None:
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    ws, pw, nw = _workspace(_size_of("gdn2_attn_decode_workspace_size", dev, B, N, Hq, Hkv, d, dt), q, workspace, dev)
+    _check(lib.gdn2_attn_decode(
+        *_rows(q, q.dtype, q.shape, 2, "q", dev), _pool(k_pages, q.dtype, Hkv, d, "k_pages", dev),
+        _pool(v_pages, q.dtype, Hkv, d, "v_pages", dev, k_pages), *where, n_slots, k_pages.shape[0], wide, k_pages.shape[2],
+        _dense(o, q.dtype, q.shape, "o", dev), B, N, Hq, Hkv, d, float(d ** -0.5 if scale is None else scale), int(window), dt, pw, nw,
+        _raw_stream(stream, dev)), "gdn2_attn_decode")
+    return o
+
+
+@_on_stream
+def attn_decode(q, k_pages, v_pages, table, lengths, slots=None, *, scale=None, window=0, stream=None):
+    """Returns o, like q. Rows of inactive slots are left unwritten."""
+    return gdn2_attn_decode.plain(q, k_pages, v_pages, table, lengths, None, slots, scale=scale, window=window, stream=stream)
+
+
+def _pages(table, lengths, refs, dev):
+    """Pointers and sizes of a cache's table, lengths and references."""
+    import torch
+
+    if table.dim() != 2 or refs.dim() != 1:
+        raise ValueError("table is [n_slots, max_pages], refs [n_pages]")
+    i32, (rows, wide), pages = torch.int32, table.shape, refs.shape[0]
+    return (_dense(table, i32, table.shape, "table", dev), _dense(lengths, i32, (rows,), "lengths", dev),
+            _dense(refs, i32, (pages,), "refs", dev)), rows, pages, wide
+
+
+def _indices(t, name, dev, n=None):
+    """Pointer of an int32 tensor [n] of row or page numbers."""
+    import torch
+
+    if t.dim() != 1:
+        raise ValueError(f"{name} is an int32 tensor [n]")
+    return _dense(t, torch.int32, (t.shape[0] if n is None else n,), name, dev)
+
+
+@_on_stream
+def pages_append(table, lengths, refs, slots, tokens, *, page, stream=None):
+    """Room for more tokens behind rows `slots` (C ABI gdn2_pages_append): lengths grows by `tokens` (an int for every row, or int32 [n])
+    and the rows get the free pages that this takes, lowest first; table, lengths and refs are updated in place. slots are distinct.
+    Returns ok: int32 [n], 0 where the row stays as it was (inactive, full, or no pages left)."""
+    import torch
+
+    dev = _device(table)
+    where, rows, pages, wide = _pages(table, lengths, refs, dev)
+    n = slots.shape[0]
+    each = tokens if isinstance(tokens, int) else 0
+    if not isinstance(tokens, (int, torch.Tensor)):
+        raise TypeError("tokens is an int or an int32 tensor")
+    ok = torch.empty((n,), dtype=torch.int32, device=table.device)
+    _check(lib.gdn2_pages_append(*where, _indices(slots, "slots", dev), None if isinstance(tokens, int) else _indices(tokens, "tokens", dev, n),
+                                 each, ok.data_ptr(), n, rows, pages, wide, page, _raw_stream(stream, dev)), "gdn2_pages_append")
+    return ok
+
+
+@_on_stream
+def pages_fork(table, lengths, refs, src, dst, *, page, stream=None):
+    """Rows `dst` (distinct) become rows like `src` (C ABI gdn2_pages_fork): dst rows are emptied, full pages shared, a last page that is not full
+    gets a free page of its own; table, lengths and refs are updated in place. Returns (copy_from, copy_to, ok), int32 [n] each: what to copy in
+    every layer's pools (pages_copy; -1 for nothing), and 0 where dst is left empty (inactive, or no pages left)."""
+    import torch
+
+    dev = _device(table)
+    where, rows, pages, wide = _pages(table, lengths, refs, dev)
+    n = src.shape[0]
+    got = torch.empty((3, n), dtype=torch.int32, device=table.device)
+    base = got.data_ptr()
+    _check(lib.gdn2_pages_fork(*where, _indices(src, "src", dev), _indices(dst, "dst", dev, n), base, base + 4 * n, base + 8 * n, n, rows, pages,
+                               wide, page, _raw_stream(stream, dev)), "gdn2_pages_fork")
+    return got.unbind(0)
+
+
+@_on_stream
+def pages_release(table, lengths, refs, slots, *, stream=None):
+    """Empties rows `slots` (C ABI gdn2_pages_release): their pages are given back; table, lengths and refs are updated in place."""
+    dev = _device(table)
+    where, rows, pages, wide = _pages(table, lengths, refs, dev)
+    _check(lib.gdn2_pages_release(*where, _indices(slots, "slots", dev), slots.shape[0], rows, pages, wide, _raw_stream(stream, dev)),
+           "gdn2_pages_release")
+
+
+@_on_stream
+def pages_copy(pools, copy_from, copy_to, *, stream=None):
+    """Copies rows copy_from[i] to rows copy_to[i] (int32 [n]; pairs with an index out of range are skipped) in each of `pools` (C ABI
+    gdn2_pages_copy): a layer's pages, or the mixers' states by slot. Pools are contiguous, of any type, with equally many rows. The copy_to rows
+    are distinct, and none is a copy_from row."""
+    if not pools:
+        return
+    dev, rows, n = _device(pools[0]), pools[0].shape[0], copy_from.shape[0]
+    ptrs, sizes = (ctypes.c_void_p * len(pools))(), (ctypes.c_longlong * len(pools))()
+    for i, t in enumerate(pools):
+        if t.shape[0] != rows:
+            raise ValueError("pools have equally many rows")
+        ptrs[i] = _dense(t, t.dtype, t.shape, "pools", dev)
+        sizes[i] = t.numel() // rows * t.element_size() if rows else 0
+    _check(lib.gdn2_pages_copy(ptrs, sizes, len(pools), _indices(copy_from, "copy_from", dev), _indices(copy_to, "copy_to", dev, n), n, rows,
+                               _raw_stream(stream, dev)), "gdn2_pages_copy")

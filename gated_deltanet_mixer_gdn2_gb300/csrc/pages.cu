@@ -1,0 +1,329 @@
+// pages.cu -- the pages of a cache (attn_common.cuh) and the rows of pools: making room, sharing, giving back, copying. Pages are counted:
+// refs[p] table entries name page p, and a page that none names is free. Everything is on the device, so that a serving step needs no
+// answer on the host and can be captured. Free pages are given out lowest first and in the order of the requests: the same calls leave
+// the same tables, whatever the blocks' order.
+//
+// Bound by latency: a call is a few dependent passes over some kilobytes. One cluster of blocks does a whole call in one launch, its passes
+// ordered by cluster barriers. The copies are bound by memory: 32 KB pieces, eight 16-byte loads in flight per thread.
+#include <cooperative_groups.h>
+
+#include "attn_common.cuh"
+
+namespace gdn2 {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 1024;
+constexpr int kCluster = 8;  // the portable size
+
+struct PagesArgs {
+    int *table, *lengths, *refs;
+    const int *src, *dst;       // fork: from row src[i] to row dst[i]; append, release: dst
+    const int* tokens;          // append: tokens of each request, or each of `every`
+    int *copy_from, *copy_to, *ok;
+    int n, every, n_slots, n_pages, max_pages, page;
+};
+
+__device__ __forceinline__ bool is_row(const PagesArgs& a, int s) { return s >= 0 && s < a.n_slots; }
+__device__ __forceinline__ bool is_page(const PagesArgs& a, int p) { return p >= 0 && p < a.n_pages; }
+__device__ __forceinline__ int length_of(const PagesArgs& a, int s) {
+    return static_cast<int>(min(max(static_cast<long long>(a.lengths[s]), 0LL), static_cast<long long>(a.max_pages) * a.page));
+}
+
+// Empties the rows dst[i]. An entry is taken by an exchange, so that a row listed twice is given back once.
+__device__ __forceinline__ void release_rows(const PagesArgs& a, long long first, long long step) {
+    const long long entries = static_cast<long long>(a.n) * a.max_pages;
+    for (long long e = first; e < entries; e += step) {
+        const int i = static_cast<int>(e / a.max_pages), j = static_cast<int>(e - static_cast<long long>(i) * a.max_pages), s = a.dst[i];
+        if (!is_row(a, s)) continue;
+        const int p = atomicExch(a.table + static_cast<long long>(s) * a.max_pages + j, -1);
+        if (is_page(a, p)) atomicSub(a.refs + p, 1);
+        if (j == 0) a.lengths[s] = 0;
+    }
+}
+
+// What request i asks for: pages, and where they go in its row. False: the request cannot be met at all.
+struct Want {
+    int row, first, pages;
+};
+__device__ __forceinline__ bool want_of(const PagesArgs& a, int i, bool fork, Want& w) {
+    w = Want{a.dst[i], 0, 0};
+    if (!is_row(a, w.row)) return false;
+    if (fork) {
+        const int s = a.src[i];
+        if (!is_row(a, s)) return false;
+        const int len = length_of(a, s);
+        w.first = len / a.page;
+        w.pages = len % a.page != 0;
+        return true;
+    }
+    const long long len = length_of(a, w.row), more = a.tokens ? a.tokens[i] : a.every;
+    if (more < 0) return false;
+    const long long have = (len + a.page - 1) / a.page, want = (len + more + a.page - 1) / a.page;
+    if (want > a.max_pages) return false;
+    w.first = static_cast<int>(have);
+    w.pages = static_cast<int>(want - have);
+    return true;
+}
+
+// Inclusive sum over the block's threads in order; total: of all of them.
+__device__ __forceinline__ int block_scan(int v, int* red, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += o;
+    }
+    __syncthreads();  // the last call's readers
+    if (lane == 31) red[warp] = v;
+    __syncthreads();
+    int t = red[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, t, d);
+        if (lane >= d) t += o;
+    }
+    total = __shfl_sync(0xffffffffu, t, 31);
+    const int before = __shfl_sync(0xffffffffu, t, (warp + 31) & 31);
+    return v + (warp ? before : 0);
+}
+
+// fork: dst[i] becomes a row like src[i]; append: room for tokens behind row dst[i]. Requests' pages are numbered in order (ok[i] holds
+// the number behind request i's last one meanwhile), the free pages too, and page number r goes to the request that holds number r. A
+// request whose last number is past the free pages gets none.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) pages_kernel(const __grid_constant__ PagesArgs a, bool fork) {
+    __shared__ int red[32], free_here;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = static_cast<int>(cluster.block_rank()), tid = threadIdx.x;
+    const long long first = rank * kThreads + tid, step = kCluster * kThreads;
+    if (fork) {
+        release_rows(a, first, step);
+        __threadfence();
+        cluster.sync();
+    }
+    // the requests' numbers (first block), and each block's share of the pages: those that are free
+    const int share = (a.n_pages + kCluster - 1) / kCluster, lo = min(rank * share, a.n_pages), hi = min(lo + share, a.n_pages);
+    if (rank == 0) {
+        int before = 0;
+        for (int i0 = 0; i0 < a.n; i0 += kThreads) {
+            Want w{};
+            const int i = i0 + tid;
+            const bool can = i < a.n && want_of(a, i, fork, w);
+            int total;
+            const int end = block_scan(can ? w.pages : 0, red, total) + before;
+            if (i < a.n) a.ok[i] = end;
+            before += total;
+        }
+    }
+    int count = 0;
+    for (int p = lo + tid; p < hi; p += kThreads) count += __ldcg(a.refs + p) <= 0;
+    int here;
+    block_scan(count, red, here);
+    if (tid == 0) free_here = here;
+    __threadfence();
+    cluster.sync();
+    int before = 0, free = 0;
+    for (int r = 0; r < kCluster; ++r) {
+        const int n = *cluster.map_shared_rank(&free_here, r);
+        if (r < rank) before += n;
+        free += n;
+    }
+    const int asked = __ldcg(a.ok + a.n - 1);
+    // the requests' answers
+    for (int p0 = lo; p0 < hi && before < asked; p0 += kThreads) {
+        const int p = p0 + tid;
+        const bool is_free = p < hi && __ldcg(a.refs + p) <= 0;
+        int total;
+        const int number = block_scan(is_free, red, total) + before - 1;
+        before += total;
+        if (!is_free || number >= asked) continue;
+        int l = 0, h = a.n - 1;  // the first request that ends behind this number
+        while (l < h) {
+            const int m = (l + h) / 2;
+            if (__ldcg(a.ok + m) > number) h = m; else l = m + 1;
+        }
+        const int end = __ldcg(a.ok + l);
+        if (end > free) continue;
+        Want w;
+        want_of(a, l, fork, w);
+        a.table[static_cast<long long>(w.row) * a.max_pages + w.first + number - (end - w.pages)] = p;
+        a.refs[p] = 1;
+        if (fork) a.copy_to[l] = p;
+    }
+    __threadfence();
+    cluster.sync();
+    if (fork) {  // the full pages are shared
+        const long long entries = static_cast<long long>(a.n) * a.max_pages;
+        for (long long e = first; e < entries; e += step) {
+            const int i = static_cast<int>(e / a.max_pages), j = static_cast<int>(e - static_cast<long long>(i) * a.max_pages);
+            Want w;
+            if (!want_of(a, i, true, w) || j >= w.first || (w.pages && __ldcg(a.ok + i) > free)) continue;
+            const int p = a.table[static_cast<long long>(a.src[i]) * a.max_pages + j];
+            if (!is_page(a, p)) continue;
+            a.table[static_cast<long long>(w.row) * a.max_pages + j] = p;
+            atomicAdd(a.refs + p, 1);
+        }
+    }
+    for (long long i = first; i < a.n; i += step) {
+        Want w;
+        const bool can = want_of(a, static_cast<int>(i), fork, w) && (w.pages == 0 || __ldcg(a.ok + i) <= free);
+        long long len = can ? length_of(a, fork ? a.src[i] : w.row) : -1;
+        if (fork) {
+            const bool copied = can && w.pages;
+            const int last = copied ? a.table[static_cast<long long>(a.src[i]) * a.max_pages + w.first] : -1;
+            a.copy_from[i] = is_page(a, last) ? last : -1;
+            if (!copied) a.copy_to[i] = -1;
+        } else if (can) {
+            len += a.tokens ? a.tokens[i] : a.every;
+        }
+        a.ok[i] = static_cast<int>(len);
+    }
+    cluster.sync();  // no length is set before the last one has been read
+    for (long long i = first; i < a.n; i += step) {
+        const int len = a.ok[i];
+        if (len >= 0) a.lengths[a.dst[i]] = len;
+        a.ok[i] = len >= 0;
+    }
+}
+
+__global__ void __launch_bounds__(256) release_kernel(const __grid_constant__ PagesArgs a) {
+    release_rows(a, blockIdx.x * 256LL + threadIdx.x, gridDim.x * 256LL);
+}
+
+// ---------------------------------------------------------------------------------------------------------------------------------
+
+constexpr int kPools = 32;      // pools of one launch
+constexpr int kPiece = 32768;   // bytes that a block copies at a time
+constexpr int kCopyThreads = 256;
+
+struct CopyArgs {
+    unsigned char* pool[kPools];
+    long long bytes[kPools];
+    int pieces[kPools + 1];  // pieces of a row in the pools before
+    const int *from, *to;
+    int n, n_rows, pools;
+};
+
+template <typename V>
+__device__ __forceinline__ void copy_piece(unsigned char* to, const unsigned char* from, int bytes) {
+    constexpr int kFlight = 8;
+    const int n = bytes / static_cast<int>(sizeof(V));
+    const V* s = reinterpret_cast<const V*>(from);
+    V* d = reinterpret_cast<V*>(to);
+    for (int i0 = threadIdx.x; i0 < n; i0 += kFlight * kCopyThreads) {
+        V v[kFlight];
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u)
+            if (i0 + u * kCopyThreads < n) v[u] = __ldcs(s + i0 + u * kCopyThreads);
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u)
+            if (i0 + u * kCopyThreads < n) __stcs(d + i0 + u * kCopyThreads, v[u]);
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
+    const long long units = static_cast<long long>(a.pieces[a.pools]) * a.n;
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+        const int piece = static_cast<int>(u / a.n), i = static_cast<int>(u - static_cast<long long>(piece) * a.n);
+        const int from = __ldg(a.from + i), to = __ldg(a.to + i);
+        if (from < 0 || from >= a.n_rows || to < 0 || to >= a.n_rows || from == to) continue;
+        int k = 0;
+        while (a.pieces[k + 1] <= piece) ++k;
+        const long long row = a.bytes[k], at = static_cast<long long>(piece - a.pieces[k]) * kPiece;
+        const int bytes = static_cast<int>(row - at < kPiece ? row - at : kPiece);
+        unsigned char* d = a.pool[k] + to * row + at;
+        const unsigned char* s = a.pool[k] + from * row + at;
+        const unsigned odd = static_cast<unsigned>(reinterpret_cast<uintptr_t>(a.pool[k])) | static_cast<unsigned>(row);
+        if (!(odd & 15)) copy_piece<uint4>(d, s, bytes);
+        else if (!(odd & 3)) copy_piece<unsigned>(d, s, bytes);
+        else copy_piece<unsigned char>(d, s, bytes);
+    }
+}
+
+gdn2_status pages_check(const PagesArgs& a) {
+    if (a.n < 0 || a.n_slots < 0 || a.n_pages < 0 || a.max_pages <= 0 || a.page <= 0) return GDN2_ERR_INVALID_ARG;
+    if (a.page > 65536 || static_cast<long long>(a.max_pages) * a.page >= (1LL << 30) || a.n_pages >= (1 << 30) || a.n >= (1 << 24) ||
+        static_cast<long long>(a.n) * a.max_pages >= (1LL << 31) - 1)
+        return GDN2_ERR_UNSUPPORTED;
+    if (a.n == 0) return GDN2_OK;
+    if (!a.table || !a.lengths || !a.refs || !a.dst) return GDN2_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)a.table, (const void*)a.lengths, (const void*)a.refs, (const void*)a.src, (const void*)a.dst,
+                          (const void*)a.tokens, (const void*)a.copy_from, (const void*)a.copy_to, (const void*)a.ok})
+        if (!aligned_to(p, 4)) return GDN2_ERR_MISALIGNED;
+    return GDN2_OK;
+}
+
+}  // namespace
+}  // namespace gdn2
+
+using namespace gdn2;
+
+extern "C" {
+
+gdn2_status gdn2_pages_fork(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* src, const int32_t* dst, int32_t* copy_from,
+                            int32_t* copy_to, int32_t* ok, int n, int n_slots, int n_pages, int max_pages, int page, void* stream) {
+    PagesArgs a{table, lengths, refs, src, dst, nullptr, copy_from, copy_to, ok, n, 0, n_slots, n_pages, max_pages, page};
+    const gdn2_status st = pages_check(a);
+    if (st != GDN2_OK || n == 0) return st;
+    if (!src || !copy_from || !copy_to || !ok) return GDN2_ERR_INVALID_ARG;
+    pages_kernel<<<kCluster, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a, true);
+    return cudaGetLastError() == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA;
+}
+
+gdn2_status gdn2_pages_append(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* slots, const int32_t* tokens, int every,
+                              int32_t* ok, int n, int n_slots, int n_pages, int max_pages, int page, void* stream) {
+    PagesArgs a{table, lengths, refs, nullptr, slots, tokens, nullptr, nullptr, ok, n, every, n_slots, n_pages, max_pages, page};
+    const gdn2_status st = pages_check(a);
+    if (st != GDN2_OK) return st;
+    if (!tokens && every < 0) return GDN2_ERR_INVALID_ARG;
+    if (n == 0) return GDN2_OK;
+    if (!ok) return GDN2_ERR_INVALID_ARG;
+    pages_kernel<<<kCluster, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a, false);
+    return cudaGetLastError() == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA;
+}
+
+gdn2_status gdn2_pages_release(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* slots, int n, int n_slots, int n_pages,
+                               int max_pages, void* stream) {
+    PagesArgs a{table, lengths, refs, nullptr, slots, nullptr, nullptr, nullptr, nullptr, n, 0, n_slots, n_pages, max_pages, 1};
+    const gdn2_status st = pages_check(a);
+    if (st != GDN2_OK || n == 0) return st;
+    const long long blocks = (static_cast<long long>(n) * max_pages + 255) / 256;
+    release_kernel<<<static_cast<unsigned>(blocks < 1216 ? blocks : 1216), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    return cudaGetLastError() == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA;
+}
+
+gdn2_status gdn2_pages_copy(void* const* pools, const long long* row_bytes, int n_pools, const int32_t* from, const int32_t* to, int n,
+                            int n_rows, void* stream) {
+    if (n_pools < 0 || n < 0 || n_rows < 0 || (n_pools && (!pools || !row_bytes))) return GDN2_ERR_INVALID_ARG;
+    for (int k = 0; k < n_pools; ++k) {
+        if (row_bytes[k] < 0 || (n_rows && row_bytes[k] && !pools[k])) return GDN2_ERR_INVALID_ARG;
+        if (row_bytes[k] >= (1LL << 40)) return GDN2_ERR_UNSUPPORTED;
+    }
+    if (n == 0 || n_rows == 0 || n_pools == 0) return GDN2_OK;
+    if (!from || !to) return GDN2_ERR_INVALID_ARG;
+    if (!aligned_to(from, 4) || !aligned_to(to, 4)) return GDN2_ERR_MISALIGNED;
+    for (int k0 = 0; k0 < n_pools; k0 += kPools) {
+        CopyArgs a{};
+        a.from = from;
+        a.to = to;
+        a.n = n;
+        a.n_rows = n_rows;
+        a.pools = n_pools - k0 < kPools ? n_pools - k0 : kPools;
+        long long pieces = 0;
+        for (int k = 0; k < a.pools; ++k) {
+            a.pool[k] = static_cast<unsigned char*>(pools[k0 + k]);
+            a.bytes[k] = row_bytes[k0 + k];
+            pieces += (a.bytes[k] + kPiece - 1) / kPiece;
+            if (pieces >= (1LL << 31)) return GDN2_ERR_UNSUPPORTED;
+            a.pieces[k + 1] = static_cast<int>(pieces);
+        }
+        const long long units = pieces * n, most = 4 * 152;
+        if (units == 0) continue;
+        copy_kernel<<<static_cast<unsigned>(units < most ? units : most), kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+        if (cudaGetLastError() != cudaSuccess) return GDN2_ERR_CUDA;
+    }
+    return GDN2_OK;
+}
+
+}  // extern "C"

@@ -477,6 +477,112 @@ gdn2_status gdn2_block_norm_backward(const void* x, const void* z, const float* 
                                      void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * Attention layers beside the mixers, for stacks that hold both: norm and rotation of queries and keys, a cache of keys and values in
+ * pages, attention of the newest tokens over it, and the calls that manage its pages.
+ *
+ * Shared by the entry points below:
+ *   - The cache. k_pages and v_pages [n_pages, H_kv, page, d] dt are one layer's pools. table int32 [n_slots, max_pages]: row s names
+ *     the pages of one sequence in order, token t of it lying in page table[s][t / page] at t % page; an entry outside [0, n_pages) (-1
+ *     by custom) is no page. lengths int32 [n_slots] counts a row's tokens, those of the present call among them: with N tokens in the
+ *     call, the first is number lengths - N. refs int32 [n_pages] counts the table entries that name a page; a page with none is free.
+ *     slots int32 [B] maps the call's rows to rows of the table, as it maps them to rows of the mixers' state pools (NULL: row b is row
+ *     b); a slot outside [0, n_slots) marks the row inactive: nothing of it is read or written. All of this is read on the device;
+ *     lengths are clamped to [0, max_pages * page], so that wrong values give wrong results, but no access outside the tensors.
+ *   - Sizes: d a multiple of 16 up to 256, page any size up to 65536, max_pages * page below 2^30.
+ *   - Sequences, rows and ld_* as for the gdn2_ssm_* entry points: token tensors may be slices of wider rows that start on 16-byte
+ *     boundaries, their ld a multiple of 8 elements. Rows of no sequence (packed) are neither read nor written. Outputs do not overlap inputs.
+ * Errors: GDN2_ERR_INVALID_ARG (dtype, sizes, H_q % H_kv, null required pointer, ld below the row's width), GDN2_ERR_UNSUPPORTED (size not
+ * built, too large), GDN2_ERR_MISALIGNED, GDN2_ERR_WORKSPACE, GDN2_ERR_CUDA. Asynchronous on `stream`; no entry point allocates or
+ * synchronises.
+ */
+
+/*
+ * gdn2_attn_prologue -- RMS norm of each head of q and k and rotation by position:
+ *     n = weight x / sqrt(mean_d(x^2) + eps);   (y_a, y_b) = (n_a cos - n_b sin, n_b cos + n_a sin),  angle = position * inv_freq[j]
+ * for the pairs (a, b) = (j, j + rot / 2), or (2 j, 2 j + 1) when interleaved != 0, of the first rot elements; the rest pass.
+ *   q [rows, H_q, d], k [rows, H_kv, d] dt -> q_out, k_out, contiguous
+ *   q_weight, k_weight  fp32 [d] or NULL (that side is not normalised)
+ *   inv_freq            fp32 [rot / 2]; rot a multiple of 16 up to d, 0 for no rotation (inv_freq may then be NULL)
+ *   positions           int32, one per row, or NULL: the token's index in its sequence
+ * Angles are formed modulo a turn in 64-bit fixed point: exact to fp32 at every 32-bit position.
+ */
+gdn2_status gdn2_attn_prologue(const void* q, long long ld_q, const void* k, long long ld_k, const float* q_weight,
+                               const float* k_weight, const float* inv_freq, const int32_t* positions, const int32_t* offsets,
+                               void* q_out, void* k_out, int B, int T, int Hq, int Hkv, int d, int rot, int interleaved, float eps,
+                               gdn2_dtype dt, void* stream);
+
+/*
+ * gdn2_attn_prologue_paged -- the same for serving: q_out as above, k (normalised and rotated) and v go to their places in the cache in
+ * the same pass. Token t of sequence b (T tokens, or offsets[b + 1] - offsets[b]) is number lengths - T + t of its row; where it has no
+ * page it is not stored. positions, if given, are for the angles alone; NULL: the token's number in its row.
+ */
+gdn2_status gdn2_attn_prologue_paged(const void* q, long long ld_q, const void* k, long long ld_k, const void* v, long long ld_v,
+                                     const float* q_weight, const float* k_weight, const float* inv_freq, const int32_t* positions,
+                                     const int32_t* offsets, void* q_out, void* k_pages, void* v_pages, const int32_t* table,
+                                     const int32_t* lengths, const int32_t* slots, int n_slots, int n_pages, int max_pages, int page,
+                                     int B, int T, int Hq, int Hkv, int d, int rot, int interleaved, float eps, gdn2_dtype dt,
+                                     void* stream);
+
+/*
+ * gdn2_attn_prologue_backward -- gradients of gdn2_attn_prologue given those of q_out and k_out: dq, dk (dt; may be slices of wider rows)
+ * and fp32 dq_weight, dk_weight [d], which go with the weights, summed over rows and heads in a fixed order.
+ * workspace: gdn2_attn_prologue_backward_workspace_size(...) bytes (packed != 0 for calls with offsets), 16-byte aligned; not used
+ * without weights.
+ */
+size_t gdn2_attn_prologue_backward_workspace_size(int B, int T, int d, int packed);
+gdn2_status gdn2_attn_prologue_backward(const void* q, long long ld_q, const void* k, long long ld_k, const float* q_weight,
+                                        const float* k_weight, const float* inv_freq, const int32_t* positions,
+                                        const int32_t* offsets, const void* dq_out, long long ld_dqo, const void* dk_out,
+                                        long long ld_dko, void* dq, long long ld_dq, void* dk, long long ld_dk, float* dq_weight,
+                                        float* dk_weight, int B, int T, int Hq, int Hkv, int d, int rot, int interleaved, float eps,
+                                        gdn2_dtype dt, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * gdn2_attn_decode -- attention of the newest N tokens of each row over the row's cache, in which their own keys and values lie already:
+ *     o = softmax(scale q K^T) V  over the keys that a token sees: token n those up to number lengths - N + n, with window > 0 the last
+ *     `window` of them (itself the last), and of these the ones that have a page. A token that sees none gets zeros.
+ *   q [B, N, H_q, d] dt (ld_q between tokens), o [B, N, H_q, d] dt; query head h reads key head h / (H_q / H_kv)
+ * Keys and values that a token does not see do not reach it, whatever they hold. Scores, sums and outputs are fp32; B up to 65535.
+ * workspace: gdn2_attn_decode_workspace_size(...) bytes, 16-byte aligned.
+ */
+size_t gdn2_attn_decode_workspace_size(int B, int N, int Hq, int Hkv, int d, gdn2_dtype dt);
+gdn2_status gdn2_attn_decode(const void* q, long long ld_q, const void* k_pages, const void* v_pages, const int32_t* table,
+                             const int32_t* lengths, const int32_t* slots, int n_slots, int n_pages, int max_pages, int page, void* o,
+                             int B, int N, int Hq, int Hkv, int d, float scale, int window, gdn2_dtype dt, void* workspace,
+                             size_t ws_bytes, void* stream);
+
+/*
+ * The pages of a cache, for all layers at once (the layers' pools share one table). Free pages are given out lowest first, in the order
+ * of the requests; answers are on the device, so that nothing waits for the host.
+ *
+ * gdn2_pages_append -- room for more tokens behind rows slots[i] (distinct): lengths grows by tokens[i] (int32 [n], or `every` each where
+ * tokens is NULL), and the row gets the pages that this takes. ok[i] (int32 [n]) is 1, or 0 with the row unchanged: an inactive slot,
+ * fewer than 0 tokens, more than max_pages, or not enough free pages for this request after those before it (which keep their claim
+ * whether or not they were met).
+ *
+ * gdn2_pages_fork -- row dst[i] (distinct) becomes one like row src[i]: dst rows are emptied first, full pages are shared, a last page that
+ * is not full gets a free page of its own. copy_from[i], copy_to[i] (int32 [n]) say what to copy in every layer's pools
+ * (gdn2_pages_copy), -1 for nothing. ok[i] is 1, or 0 with dst[i] left empty: an inactive slot, or no free page. A source that is among
+ * the dst rows counts as empty.
+ *
+ * gdn2_pages_release -- empties rows slots[i]: their pages are given back, entries become -1, lengths 0. Slots out of range are skipped.
+ */
+gdn2_status gdn2_pages_append(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* slots, const int32_t* tokens, int every,
+                              int32_t* ok, int n, int n_slots, int n_pages, int max_pages, int page, void* stream);
+gdn2_status gdn2_pages_fork(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* src, const int32_t* dst, int32_t* copy_from,
+                            int32_t* copy_to, int32_t* ok, int n, int n_slots, int n_pages, int max_pages, int page, void* stream);
+gdn2_status gdn2_pages_release(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* slots, int n, int n_slots, int n_pages,
+                               int max_pages, void* stream);
+
+/*
+ * gdn2_pages_copy -- copies row from[i] to row to[i] (int32 [n], on the device) in each of n_pools pools of n_rows rows: pages of the
+ * layers' pools, or the mixers' state and convolution pools by slot. pools and row_bytes are host arrays; rows of any size and alignment
+ * (16-byte ones are fastest). Pairs with an index out of range are skipped. The to rows are distinct and none of them is a from row.
+ */
+gdn2_status gdn2_pages_copy(void* const* pools, const long long* row_bytes, int n_pools, const int32_t* from, const int32_t* to, int n,
+                            int n_rows, void* stream);
+
+/*
  * gdn2_selftest_umma -- diagnostics: one tcgen05 product D[128][N] = A * B (bf16 in, fp32 out)
  * with the operand layouts the tensor-core chunked kernels use, so that a test can check them
  * against a host matrix product. The operands are row-major bf16 device arrays:
