@@ -86,7 +86,7 @@ def _load() -> ctypes.CDLL:
         "gdn2_attn_prologue_paged": (I, [P, L, P, L, P, L] + [P] * 11 + [I] * 4 + [I] * 7 + [F, I, P]),
         "gdn2_attn_prologue_backward_workspace_size": (Z, [I] * 4),
         "gdn2_attn_prologue_backward": (I, [P, L, P, L] + [P] * 5 + [P, L] * 4 + [P, P] + [I] * 7 + [F, I, P, Z, P]),
-        "gdn2_attn_decode_workspace_size": (Z, [I] * 5 + [I]),
+        "gdn2_attn_decode_workspace_size": (Z, [I] * 7 + [I]),
         "gdn2_attn_decode": (I, [P, L] + [P] * 5 + [I] * 4 + [P] + [I] * 5 + [F, I, I, P, Z, P]),
         "gdn2_pages_append": (I, [P] * 5 + [I, P] + [I] * 5 + [P]),
         "gdn2_pages_fork": (I, [P] * 8 + [I] * 5 + [P]),
@@ -926,7 +926,7 @@ def gdn2_attn_decode(q, k_pages, v_pages, table, lengths, o, slots=None, *, scal
     dt = _dtype_code(q)
     if o is None:
         o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    ws, pw, nw = _workspace(_size_of("gdn2_attn_decode_workspace_size", dev, B, N, Hq, Hkv, d, dt), q, workspace, dev)
+    ws, pw, nw = _workspace(_size_of("gdn2_attn_decode_workspace_size", dev, B, N, Hq, Hkv, d, wide, k_pages.shape[2], dt), q, workspace, dev)
     _check(lib.gdn2_attn_decode(
         *_rows(q, q.dtype, q.shape, 2, "q", dev), _pool(k_pages, q.dtype, Hkv, d, "k_pages", dev),
         _pool(v_pages, q.dtype, Hkv, d, "v_pages", dev, k_pages), *where, n_slots, k_pages.shape[0], wide, k_pages.shape[2],

@@ -3,9 +3,9 @@
 //     n = w x / sqrt(mean(x^2) + eps)        (y_a, y_b) = (n_a cos - n_b sin, n_b cos + n_a sin),  angle = position * inv_freq
 // for the pairs (a, b) of the first `rot` elements: (j, j + rot / 2), or (2 j, 2 j + 1) when interleaved.
 //
-// Bound by memory: every element is read once and written once for some 10 operations. A head's row belongs to a group of lanes, eight
-// elements each, so that its sum of squares and the pairs' other halves come by shuffles; a group keeps to one token, whose cosines
-// and sines it holds in registers, and has several rows' loads in flight.
+// Bound by memory: every element is read once and written once for some 10 operations, which are packed two by two. A head's row belongs to
+// a group of lanes, eight elements each (both sides of four pairs), whose sum of squares comes by shuffles; a group keeps to one token, whose
+// cosines and sines it holds in registers, and has several rows' loads in flight.
 #include "attn_common.cuh"
 
 namespace gdn2 {
@@ -14,6 +14,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTokens = 8;    // tokens of a tile at most: the angles of a tile are formed once, two or so per thread
 constexpr int kMaxD = 256;
+constexpr int kGradBlocks = 2;  // per SM
 
 struct PrologueArgs {
     const void *q, *k, *v;
@@ -47,8 +48,8 @@ __device__ __forceinline__ unsigned long long turns_of(float f) {
 
 // What the threads of a block share: of each token of the tile its position and where it goes, and the angles.
 struct TileShared {
-    int position[kTokens], live[kTokens], page[kTokens], at[kTokens];
     float cs[kTokens][kMaxD / 2], sn[kTokens][kMaxD / 2];
+    int position[kTokens], live[kTokens], page[kTokens], at[kTokens];
     unsigned long long turns[kMaxD / 2];
     float bad[kMaxD / 2];  // 0, or NaN where the frequency is not finite
 };
@@ -95,165 +96,212 @@ __device__ __forceinline__ void enter_tile(const PrologueArgs& a, TileShared& sh
     __syncthreads();
 }
 
+// A lane's eight elements of a head: two runs of four, at e0 and e1. Rotated by halves they are both sides of four pairs, so a rotation needs
+// no other lane; else they lie side by side.
+struct Place {
+    int e0, e1;
+    bool mine, turned;  // within the head; rotated
+};
+template <bool kPairs>
+__device__ __forceinline__ Place place_of(int lane, int d, int rot) {
+    Place p{8 * lane, 8 * lane + 4, 8 * lane < d, 8 * lane < rot};
+    if (!p.mine) {  // reads along, for nothing
+        p.e0 = 0;
+        p.e1 = 4;
+    } else if (!kPairs && p.turned) {
+        p.e0 = 4 * lane;
+        p.e1 = 4 * lane + rot / 2;
+    }
+    return p;
+}
+
+// Eight elements as they are loaded, and as four packed pairs of fp32.
 template <typename T>
-struct Raw8;  // eight elements as they are loaded
+struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
-    uint4 u;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        const unsigned w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+    uint2 u[2];
+    static constexpr int kFlight = 3, kGradFlight = 2, kBlocks = 4;  // rows on their way, blocks per SM
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, const Place& at) {
+        u[0] = __ldg(reinterpret_cast<const uint2*>(p + at.e0));
+        u[1] = __ldg(reinterpret_cast<const uint2*>(p + at.e1));
     }
-    static constexpr int kFlight = 4;
+    __device__ __forceinline__ void get(uint64_t (&x)[4]) const {
+        x[0] = bf16x2_widen(u[0].x); x[1] = bf16x2_widen(u[0].y); x[2] = bf16x2_widen(u[1].x); x[3] = bf16x2_widen(u[1].y);
+    }
+    __device__ __forceinline__ void set(const uint64_t (&x)[4]) {
+        u[0] = make_uint2(bf16x2_narrow(x[0]), bf16x2_narrow(x[1]));
+        u[1] = make_uint2(bf16x2_narrow(x[2]), bf16x2_narrow(x[3]));
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16* p, const Place& at) const {
+        *reinterpret_cast<uint2*>(p + at.e0) = u[0];
+        *reinterpret_cast<uint2*>(p + at.e1) = u[1];
+    }
 };
 template <>
 struct Raw8<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = __ldg(reinterpret_cast<const float4*>(p));
-        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    ulonglong2 u[2];
+    static constexpr int kFlight = 2, kGradFlight = 1, kBlocks = 3;
+    __device__ __forceinline__ void load(const float* p, const Place& at) {
+        u[0] = __ldg(reinterpret_cast<const ulonglong2*>(p + at.e0));
+        u[1] = __ldg(reinterpret_cast<const ulonglong2*>(p + at.e1));
     }
-    __device__ __forceinline__ void store(float* p) const {
-        reinterpret_cast<float4*>(p)[0] = a;
-        reinterpret_cast<float4*>(p)[1] = b;
+    __device__ __forceinline__ void get(uint64_t (&x)[4]) const { x[0] = u[0].x; x[1] = u[0].y; x[2] = u[1].x; x[3] = u[1].y; }
+    __device__ __forceinline__ void set(const uint64_t (&x)[4]) {
+        u[0] = make_ulonglong2(x[0], x[1]);
+        u[1] = make_ulonglong2(x[2], x[3]);
     }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    __device__ __forceinline__ void store(float* p, const Place& at) const {
+        *reinterpret_cast<ulonglong2*>(p + at.e0) = u[0];
+        *reinterpret_cast<ulonglong2*>(p + at.e1) = u[1];
     }
-    static constexpr int kFlight = 2;
 };
 
-template <int L>
-__device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-    for (int m = L / 2; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-    return v;
+// The lane's weights of a side, ones without.
+__device__ __forceinline__ void weights_of(const float* weight, const Place& at, uint64_t (&wv)[4]) {
+    if (weight) {
+        const float4 p = __ldg(reinterpret_cast<const float4*>(weight + at.e0)), q = __ldg(reinterpret_cast<const float4*>(weight + at.e1));
+        wv[0] = f32x2(p.x, p.y); wv[1] = f32x2(p.z, p.w); wv[2] = f32x2(q.x, q.y); wv[3] = f32x2(q.z, q.w);
+    } else {
+        wv[0] = wv[1] = wv[2] = wv[3] = f32x2(1.f, 1.f);
+    }
 }
 
-// The lane's part of a token's rotation: elements 8 lane .. 8 lane + 7.
+// x . y of the lane's elements
+__device__ __forceinline__ float lane_dot(const uint64_t (&x)[4], const uint64_t (&y)[4]) {
+    uint64_t s = mul_f32x2(x[0], y[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) s = fma_f32x2(x[i], y[i], s);
+    float lo, hi;
+    f32x2_split(s, lo, hi);
+    return lo + hi;
+}
+// Sums over the group's lanes, n of them side by side; all lanes of the warp take part.
+template <int L, int n>
+__device__ __forceinline__ void group_sums(float (&v)[n]) {
+#pragma unroll
+    for (int m = L / 2; m; m >>= 1)
+#pragma unroll
+        for (int i = 0; i < n; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], m);
+}
+
+// The lane's part of a token's rotation. By halves: x[0], x[1] are the first sides a, x[2], x[3] the second sides b of its pairs.
 template <bool kPairs>
 struct Turn {
-    float c[8], s[8];  // of each element; kPairs: of its four pairs, in the first half
-    int partner;       // lane with the pairs' other halves; negative: these elements are not rotated
-    __device__ __forceinline__ void set(const PrologueArgs& a, const TileShared& sh, int token, int lane) {
-        const int half = a.rot / 2, i0 = 8 * lane;
-        partner = -1;
-        if (i0 >= a.rot) return;
+    uint64_t c[kPairs ? 4 : 2], s[kPairs ? 4 : 2];
+    __device__ __forceinline__ void set(const TileShared& sh, int token, const Place& at) {
+        if (!at.turned) return;
         if constexpr (kPairs) {
-            partner = lane;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                c[i] = sh.cs[token][i0 / 2 + i];
-                s[i] = sh.sn[token][i0 / 2 + i];
+                const int j = at.e0 / 2 + i;
+                c[i] = f32x2(sh.cs[token][j], sh.cs[token][j]);
+                s[i] = f32x2(-sh.sn[token][j], sh.sn[token][j]);
             }
         } else {
-            const bool low = i0 < half;
-            partner = low ? lane + half / 8 : lane - half / 8;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                c[i] = sh.cs[token][(low ? i0 : i0 - half) + i];
-                s[i] = low ? -sh.sn[token][i0 + i] : sh.sn[token][i0 - half + i];  // a cos - b sin, b cos + a sin
-            }
+            const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&sh.cs[token][at.e0]), v = *reinterpret_cast<const ulonglong2*>(&sh.sn[token][at.e0]);
+            c[0] = u.x; c[1] = u.y; s[0] = v.x; s[1] = v.y;
         }
     }
-    // Rotates x in place; back: by the opposite angle. All lanes of the warp take part; `first` is the group's first lane.
+    // Rotates x in place; kBack: by the opposite angle.
     template <bool kBack>
-    __device__ __forceinline__ void apply(float (&x)[8], int first) const {
+    __device__ __forceinline__ void apply(uint64_t (&x)[4], bool turned) const {
+        if (!turned) return;
         if constexpr (kPairs) {
-            if (partner < 0) return;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float p = x[2 * i], q = x[2 * i + 1], sv = kBack ? -s[i] : s[i];
-                x[2 * i] = fmaf(p, c[i], -q * sv);
-                x[2 * i + 1] = fmaf(q, c[i], p * sv);
+                float lo, hi;
+                f32x2_split(x[i], lo, hi);
+                x[i] = fma_f32x2(x[i], c[i], mul_f32x2(kBack ? f32x2(-hi, -lo) : f32x2(hi, lo), s[i]));
             }
         } else {
-            const int from = first + (partner < 0 ? 0 : partner);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float o = __shfl_sync(0xffffffffu, x[i], from);
-                if (partner >= 0) x[i] = fmaf(x[i], c[i], o * (kBack ? -s[i] : s[i]));
+            for (int i = 0; i < 2; ++i) {
+                const uint64_t a = x[i], b = x[2 + i];
+                const uint64_t bs = mul_f32x2(b, s[i]), as = mul_f32x2(a, s[i]);
+                x[i] = kBack ? fma_f32x2(a, c[i], bs) : sub_f32x2(mul_f32x2(a, c[i]), bs);
+                x[2 + i] = kBack ? sub_f32x2(mul_f32x2(b, c[i]), as) : fma_f32x2(b, c[i], as);
             }
         }
     }
 };
 
-// Group geometry of a block: kThreads / L groups, those of one token apart by `tokens`.
+// The groups of a block lie `tokens` apart for one token; blockIdx.y shares its heads out further.
 template <typename T, int L, bool kPairs>
-__global__ void __launch_bounds__(kThreads, 3) prologue_kernel(const __grid_constant__ PrologueArgs a) {
-    __shared__ TileShared sh;
-    __shared__ __align__(16) float w[2][kMaxD];
+__global__ void __launch_bounds__(kThreads, Raw8<T>::kBlocks) prologue_kernel(const __grid_constant__ PrologueArgs a) {
+    __shared__ __align__(16) TileShared sh;
     const long long rows = a.seqs.offsets ? a.seqs.T : static_cast<long long>(a.seqs.B) * a.seqs.T;
     const long long row0 = static_cast<long long>(blockIdx.x) * a.tokens;
-    for (int j = threadIdx.x; j < a.d; j += kThreads) {
-        w[0][j] = a.q_weight ? a.q_weight[j] : 1.f;
-        w[1][j] = a.k_weight ? a.k_weight[j] : 1.f;
-    }
+    const int lane = threadIdx.x % L, group = threadIdx.x / L, per = kThreads / L / a.tokens;
+    const int token = group % a.tokens, base = blockIdx.y * per, part = base + group / a.tokens, step = per * gridDim.y;
+    const Place at = place_of<kPairs>(lane, a.d, a.rot);
+    const long long r = row0 + token, r_in = r < rows ? r : rows - 1;
+    const int d = a.d;
+    constexpr int kFlight = Raw8<T>::kFlight;
+    // Heads part, part + step, .. of one side; those past the last one are read as the last one, and rows of no sequence as they are,
+    // so that every load is made, and dropped.
+    const T *qs = static_cast<const T*>(a.q) + r_in * a.ld_q, *ks = static_cast<const T*>(a.k) + r_in * a.ld_k;
+    auto fetch = [&](Raw8<T>& to, const T* src, int h, int H) { to.load(src + min(h, H - 1) * d, at); };
+    Raw8<T> raw[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) fetch(raw[u], qs, part + u * step, a.Hq);  // on their way while the tile's positions and angles are formed
     frequencies(a, sh);
     enter_tile(a, sh, row0, rows);
 
-    const int lane = threadIdx.x % L, group = threadIdx.x / L, groups = kThreads / L, first = (threadIdx.x & 31) - lane;
-    const int token = group % a.tokens, part = group / a.tokens + blockIdx.y * (groups / a.tokens), step = groups / a.tokens * gridDim.y;
-    const bool mine = 8 * lane < a.d;
-    const bool live = sh.live[token];
+    const bool live = sh.live[token] && at.mine;
     Turn<kPairs> turn;
-    turn.set(a, sh, token, lane);
-    const int page = sh.page[token], at = sh.at[token];
-    const long long r = row0 + token;
-    const int heads = a.Hq + a.Hkv + (a.cache.table ? a.Hkv : 0);
-    constexpr int kFlight = Raw8<T>::kFlight;
-    for (int h0 = part; __any_sync(0xffffffffu, h0 < heads); h0 += kFlight * step) {
-        Raw8<T> raw[kFlight];
+    turn.set(sh, token, at);
+    const int page = sh.page[token];
+    // keys and values: in the cache, heads lie a page apart
+    const int kv_step = a.cache.table ? a.cache.page * d : d;
+    const long long kv = a.cache.table ? (static_cast<long long>(page) * a.Hkv * a.cache.page + sh.at[token]) * d : r * a.Hkv * d;
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
-            const int h = h0 + u * step;
-            if (!live || !mine || h >= heads) continue;
-            const T* row = h < a.Hq           ? static_cast<const T*>(a.q) + r * a.ld_q + static_cast<long long>(h) * a.d
-                           : h < a.Hq + a.Hkv ? static_cast<const T*>(a.k) + r * a.ld_k + static_cast<long long>(h - a.Hq) * a.d
-                                              : static_cast<const T*>(a.v) + r * a.ld_v + static_cast<long long>(h - a.Hq - a.Hkv) * a.d;
-            raw[u].load(row + 8 * lane);
+    for (int side = 0; side < 2; ++side) {
+        const int H = side ? a.Hkv : a.Hq, rounds = (H - base + step - 1) / step, to_step = side ? kv_step : d;
+        const T* src = side ? ks : qs;
+        T* to = side ? static_cast<T*>(a.k_out) + kv : static_cast<T*>(a.q_out) + r * a.Hq * d;
+        const float* weight = side ? a.k_weight : a.q_weight;
+        uint64_t wv[4];
+        weights_of(weight, at, wv);
+        const int last = live && (!side || !a.cache.table || page >= 0) ? H : 0;  // heads behind it are not stored
+        if (side) {
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) fetch(raw[u], src, part + u * step, H);
         }
+        int h = part;
+        for (int i = 0; i < rounds; i += kFlight) {
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
-            const int h = h0 + u * step;
-            if (!__any_sync(0xffffffffu, h < heads)) break;
-            const bool here = live && mine && h < heads;
-            const int kind = h < a.Hq ? 0 : h < a.Hq + a.Hkv ? 1 : 2, hk = h - a.Hq - (kind == 2 ? a.Hkv : 0);
-            float x[8];
-            if (here) {
+            for (int u = 0; u < kFlight; ++u) {
+                if (u && i + u >= rounds) break;
+                uint64_t x[4];
                 raw[u].get(x);
-            } else {
+                fetch(raw[u], src, h + kFlight * step, H);
+                if (weight) {  // without weights there is no norm
+                    float ss[1] = {at.mine ? lane_dot(x, x) : 0.f};
+                    group_sums<L>(ss);
+                    const float inv = rsqrtf(fmaf(ss[0], a.inv_d, a.eps));
+                    const uint64_t inv2 = f32x2(inv, inv);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = 0.f;
+                    for (int e = 0; e < 4; ++e) x[e] = mul_f32x2(x[e], mul_f32x2(wv[e], inv2));
+                }
+                turn.template apply<false>(x, at.turned);
+                if (h < last) {
+                    Raw8<T> y;
+                    y.set(x);
+                    y.store(to + static_cast<long long>(h) * to_step, at);
+                }
+                h += step;
             }
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-            ss = group_sum<L>(ss);
-            if ((kind ? a.k_weight : a.q_weight) && mine) {  // without weights there is no norm
-                const float inv = rsqrtf(fmaf(ss, a.inv_d, a.eps));
-                const float4 w0 = *reinterpret_cast<const float4*>(&w[kind & 1][8 * lane]), w1 = *reinterpret_cast<const float4*>(&w[kind & 1][8 * lane + 4]);
-                const float wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] *= inv * wv[i];
-            }
-            turn.template apply<false>(x, first);
-            if (!here) continue;
-            if (kind == 0) {
-                Vec8<T>::store(static_cast<T*>(a.q_out) + (r * a.Hq + h) * a.d + 8 * lane, x);
-            } else if (!a.cache.table) {
-                Vec8<T>::store(static_cast<T*>(a.k_out) + (r * a.Hkv + hk) * a.d + 8 * lane, x);
-            } else if (page >= 0) {
-                const long long to = ((static_cast<long long>(page) * a.Hkv + hk) * a.cache.page + at) * a.d + 8 * lane;
-                if (kind == 1) Vec8<T>::store(static_cast<T*>(a.k_out) + to, x);
-                else raw[u].store(static_cast<T*>(a.v_out) + to);
-            }
+        }
+    }
+    if (a.cache.table && live && page >= 0) {  // values pass as they are
+        const T* vs = static_cast<const T*>(a.v) + r * a.ld_v;
+        T* vo = static_cast<T*>(a.v_out) + kv;
+#pragma unroll 4
+        for (int g = part; g < a.Hkv; g += step) {
+            Raw8<T> v;
+            v.load(vs + g * d, at);
+            v.store(vo + static_cast<long long>(g) * kv_step, at);
         }
     }
 }
@@ -261,76 +309,80 @@ __global__ void __launch_bounds__(kThreads, 3) prologue_kernel(const __grid_cons
 // Gradients: dn = dy turned back; dw = sum over tokens and heads of dn xh with xh = x inv; dx = inv (w dn - xh mean(w dn xh)).
 // Blocks walk tiles one after another and leave one partial sum of the weights' gradients each.
 template <typename T, int L, bool kPairs>
-__global__ void __launch_bounds__(kThreads, 3) prologue_grad_kernel(const __grid_constant__ PrologueArgs a) {
-    __shared__ TileShared sh;
+__global__ void __launch_bounds__(kThreads, kGradBlocks) prologue_grad_kernel(const __grid_constant__ PrologueArgs a) {
+    __shared__ __align__(16) TileShared sh;
     __shared__ __align__(16) float red[kThreads / L][L * 8];
     const long long rows = a.seqs.offsets ? a.seqs.T : static_cast<long long>(a.seqs.B) * a.seqs.T;
-    const int lane = threadIdx.x % L, group = threadIdx.x / L, groups = kThreads / L, first = (threadIdx.x & 31) - lane;
+    const int lane = threadIdx.x % L, group = threadIdx.x / L, groups = kThreads / L;
     const int token = group % a.tokens, part = group / a.tokens, step = groups / a.tokens;
-    const bool mine = 8 * lane < a.d;
-    float acc[2][8] = {};
+    const Place at = place_of<kPairs>(lane, a.d, a.rot);
+    uint64_t acc[2][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[0][i] = acc[1][i] = 0;
     frequencies(a, sh);
+    constexpr int kFlight = Raw8<T>::kGradFlight;
+    Raw8<T> rx[kFlight], rg[kFlight];
     for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
         const long long row0 = static_cast<long long>(tile) * a.tokens;
+        const long long r = row0 + token, r_in = r < rows ? r : rows - 1;
+        // as in the forward, every load is made
+        auto fetch = [&](int u, int h, bool side) {
+            const int o = min(h, (side ? a.Hkv : a.Hq) - 1) * a.d;
+            rg[u].load((side ? static_cast<const T*>(a.gk) + r_in * a.ld_gk : static_cast<const T*>(a.gq) + r_in * a.ld_gq) + o, at);
+            if (side ? a.k_weight : a.q_weight)
+                rx[u].load((side ? static_cast<const T*>(a.k) + r_in * a.ld_k : static_cast<const T*>(a.q) + r_in * a.ld_q) + o, at);
+        };
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) fetch(u, part + u * step, false);
         __syncthreads();
         enter_tile(a, sh, row0, rows);
-        const bool live = sh.live[token];
+        const bool live = sh.live[token] && at.mine;
         Turn<kPairs> turn;
-        turn.set(a, sh, token, lane);
-        const long long r = row0 + token;
+        turn.set(sh, token, at);
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
             const int H = side ? a.Hkv : a.Hq;
             const float* weight = side ? a.k_weight : a.q_weight;
-            const T* xs = static_cast<const T*>(side ? a.k : a.q) + r * (side ? a.ld_k : a.ld_q) + 8 * lane;
-            const T* gs = static_cast<const T*>(side ? a.gk : a.gq) + r * (side ? a.ld_gk : a.ld_gq) + 8 * lane;
-            T* out = static_cast<T*>(side ? a.k_out : a.q_out) + r * (side ? a.ld_dk : a.ld_dq) + 8 * lane;
-            float wv[8];
+            T* out = static_cast<T*>(side ? a.k_out : a.q_out) + r * (side ? a.ld_dk : a.ld_dq);
+            uint64_t wv[4];
+            weights_of(weight, at, wv);
+            if (side) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) wv[i] = weight && mine ? __ldg(weight + 8 * lane + i) : 1.f;
-            constexpr int kFlight = 2;
-            for (int h0 = part; __any_sync(0xffffffffu, h0 < H); h0 += kFlight * step) {
-                Raw8<T> rx[kFlight], rg[kFlight];
-#pragma unroll
-                for (int u = 0; u < kFlight; ++u) {
-                    const int h = h0 + u * step;
-                    if (!live || !mine || h >= H) continue;
-                    rg[u].load(gs + static_cast<long long>(h) * a.d);
-                    if (weight) rx[u].load(xs + static_cast<long long>(h) * a.d);
-                }
+                for (int u = 0; u < kFlight; ++u) fetch(u, part + u * step, true);
+            }
+            const int rounds = (H + step - 1) / step;
+            int h = part;
+            for (int i = 0; i < rounds; i += kFlight) {
 #pragma unroll
                 for (int u = 0; u < kFlight; ++u) {
-                    const int h = h0 + u * step;
-                    if (!__any_sync(0xffffffffu, h < H)) break;
-                    const bool here = live && mine && h < H;
-                    float g[8], x[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) g[i] = x[i] = 0.f;
-                    if (here) {
-                        rg[u].get(g);
-                        if (weight) rx[u].get(x);
-                    }
-                    turn.template apply<true>(g, first);
+                    if (u && i + u >= rounds) break;
+                    uint64_t g[4], x[4];
+                    rg[u].get(g);
+                    if (weight) rx[u].get(x);
+                    fetch(u, h + kFlight * step, side);
+                    turn.template apply<true>(g, at.turned);
+                    const bool here = live && h < H;
                     if (weight) {
-                        float ss = 0.f, gx = 0.f;
+                        uint64_t gw[4];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            ss = fmaf(x[i], x[i], ss);
-                            gx = fmaf(g[i] * wv[i], x[i], gx);
-                        }
-                        ss = group_sum<L>(ss);
-                        gx = group_sum<L>(gx);
-                        const float inv = rsqrtf(fmaf(ss, a.inv_d, a.eps)), m = gx * inv * a.inv_d;
-                        if (here) {
+                        for (int e = 0; e < 4; ++e) gw[e] = mul_f32x2(g[e], wv[e]);
+                        float sums[2] = {at.mine ? lane_dot(x, x) : 0.f, at.mine ? lane_dot(gw, x) : 0.f};
+                        group_sums<L>(sums);
+                        const float inv = rsqrtf(fmaf(sums[0], a.inv_d, a.eps)), m = -inv * sums[1] * inv * a.inv_d;
+                        const uint64_t inv2 = f32x2(inv, inv), m2 = f32x2(m, m);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float xh = x[i] * inv;
-                                acc[side][i] = fmaf(g[i], xh, acc[side][i]);
-                                g[i] = inv * fmaf(-xh, m, g[i] * wv[i]);
-                            }
+                        for (int e = 0; e < 4; ++e) {
+                            const uint64_t next = fma_f32x2(g[e], mul_f32x2(x[e], inv2), acc[side][e]);
+                            acc[side][e] = here ? next : acc[side][e];  // what is read along may not be finite
+                            g[e] = mul_f32x2(inv2, fma_f32x2(x[e], m2, gw[e]));
                         }
                     }
-                    if (here) Vec8<T>::store(out + static_cast<long long>(h) * a.d, g);
+                    if (here) {
+                        Raw8<T> y;
+                        y.set(g);
+                        y.store(out + h * a.d, at);
+                    }
+                    h += step;
                 }
             }
         }
@@ -339,8 +391,10 @@ __global__ void __launch_bounds__(kThreads, 3) prologue_grad_kernel(const __grid
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) red[group][8 * lane + i] = acc[side][i];
+        if (at.mine) {
+            *reinterpret_cast<ulonglong2*>(&red[group][at.e0]) = make_ulonglong2(acc[side][0], acc[side][1]);
+            *reinterpret_cast<ulonglong2*>(&red[group][at.e1]) = make_ulonglong2(acc[side][2], acc[side][3]);
+        }
         __syncthreads();
         for (int c = threadIdx.x; c < a.d; c += kThreads) {
             float v = 0.f;
@@ -350,20 +404,23 @@ __global__ void __launch_bounds__(kThreads, 3) prologue_grad_kernel(const __grid
     }
 }
 
-// The blocks' partial sums, added in their order: 32 columns a block, its warps each a share of the parts.
-__global__ void __launch_bounds__(kThreads) weight_grad_kernel(const float* parts, int n, int d, float* dq_weight, float* dk_weight) {
-    __shared__ float red[kThreads / 32][33];
+// The blocks' partial sums, added in a fixed order: 32 columns a block, its warps each a share of the parts.
+__global__ void __launch_bounds__(1024) weight_grad_kernel(const float* parts, int n, int d, float* dq_weight, float* dk_weight) {
+    __shared__ float red[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, side = blockIdx.y, c = blockIdx.x * 32 + lane;
+    float* out = side ? dk_weight : dq_weight;
+    if (!out) return;
     float v = 0.f;
-    if (c < d)
-        for (int k = warp; k < n; k += kThreads / 32) v += parts[(static_cast<long long>(k) * 2 + side) * d + c];
+    if (c < d) {
+#pragma unroll 8
+        for (int k = warp; k < n; k += 32) v += parts[(static_cast<long long>(k) * 2 + side) * d + c];
+    }
     red[warp][lane] = v;
     __syncthreads();
-    float* out = side ? dk_weight : dq_weight;
-    if (warp == 0 && c < d && out) {
-        for (int k = 1; k < kThreads / 32; ++k) v += red[k][lane];
-        out[c] = v;
-    }
+    v = red[lane][warp];
+#pragma unroll
+    for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    if (lane == 0 && blockIdx.x * 32 + warp < d) out[blockIdx.x * 32 + warp] = v;
 }
 
 int sm_count() {
@@ -400,7 +457,7 @@ int tokens_of(int d, long long rows) {
 
 int grad_blocks(int d, long long rows) {
     const int t = tokens_of(d, rows);
-    const long long tiles = (rows + t - 1) / t, most = 3LL * sm_count();
+    const long long tiles = (rows + t - 1) / t, most = static_cast<long long>(kGradBlocks) * sm_count();
     return static_cast<int>(tiles < most ? tiles : most);
 }
 
@@ -539,7 +596,7 @@ gdn2_status gdn2_attn_prologue_backward(const void* q, long long ld_q, const voi
     cudaError_t e = dt == GDN2_BF16 ? launch<__nv_bfloat16>(a, dim3(blocks), interleaved != 0, true, s)
                                     : launch<float>(a, dim3(blocks), interleaved != 0, true, s);
     if (e == cudaSuccess && a.parts) {
-        weight_grad_kernel<<<dim3((d + 31) / 32, 2), kThreads, 0, s>>>(a.parts, blocks, d, dq_weight, dk_weight);
+        weight_grad_kernel<<<dim3((d + 31) / 32, 2), 1024, 0, s>>>(a.parts, blocks, d, dq_weight, dk_weight);
         e = cudaGetLastError();
     }
     return e == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA;

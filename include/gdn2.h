@@ -543,9 +543,9 @@ gdn2_status gdn2_attn_prologue_backward(const void* q, long long ld_q, const voi
  *     `window` of them (itself the last), and of these the ones that have a page. A token that sees none gets zeros.
  *   q [B, N, H_q, d] dt (ld_q between tokens), o [B, N, H_q, d] dt; query head h reads key head h / (H_q / H_kv)
  * Keys and values that a token does not see do not reach it, whatever they hold. Scores, sums and outputs are fp32; B up to 65535.
- * workspace: gdn2_attn_decode_workspace_size(...) bytes, 16-byte aligned.
+ * workspace: gdn2_attn_decode_workspace_size(...) bytes, 16-byte aligned; may be NULL when that is 0.
  */
-size_t gdn2_attn_decode_workspace_size(int B, int N, int Hq, int Hkv, int d, gdn2_dtype dt);
+size_t gdn2_attn_decode_workspace_size(int B, int N, int Hq, int Hkv, int d, int max_pages, int page, gdn2_dtype dt);
 gdn2_status gdn2_attn_decode(const void* q, long long ld_q, const void* k_pages, const void* v_pages, const int32_t* table,
                              const int32_t* lengths, const int32_t* slots, int n_slots, int n_pages, int max_pages, int page, void* o,
                              int B, int N, int Hq, int Hkv, int d, float scale, int window, gdn2_dtype dt, void* workspace,

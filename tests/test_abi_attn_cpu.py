@@ -69,11 +69,12 @@ def test_decode_argument_errors(g):  # noqa: F811
     assert _decode(g, q=0) == bad and _decode(g, o=0) == bad and _decode(g, ld=255) == bad
     assert _decode(g, d=72) == no and _decode(g, d=272) == no and _decode(g, B=65536) == no and _decode(g, N=5000) == no
     assert _decode(g, ld=1 << 31) == no
-    assert _decode(g, q=A + 8) == off and _decode(g, o=A + 4) == off and _decode(g, ld=260) == off and _decode(g, ws=A + 8) == off
-    assert _decode(g, ws=0) == g.GDN2_ERR_WORKSPACE and _decode(g, wsb=1000) == g.GDN2_ERR_WORKSPACE
+    assert _decode(g, q=A + 8) == off and _decode(g, o=A + 4) == off and _decode(g, ld=260) == off and _decode(g, wide=999, ws=A + 8) == off
+    assert _decode(g, wide=999, ws=0) == g.GDN2_ERR_WORKSPACE and _decode(g, wide=999, wsb=1000) == g.GDN2_ERR_WORKSPACE
     assert _decode(g, B=0, q=0, o=0, ws=0) == g.GDN2_OK and _decode(g, N=0, q=0, o=0, ws=0) == g.GDN2_OK
     size = g.lib.gdn2_attn_decode_workspace_size
-    assert size(1, 1, 4, 2, 64, BF16) > 0 and size(0, 1, 4, 2, 64, BF16) == 0 and size(1, 1, 4, 3, 64, BF16) == 0 and size(1, 1, 4, 2, 64, F32) > 0
+    assert size(1, 1, 4, 2, 64, 999, 16, BF16) > 0 and size(1, 1, 4, 2, 64, 999, 16, F32) > 0 and size(0, 1, 4, 2, 64, 999, 16, BF16) == 0
+    assert size(1, 1, 4, 3, 64, 999, 16, BF16) == 0 and size(1, 1, 4, 2, 64, 0, 16, BF16) == 0 and size(1, 1, 4, 2, 64, 4, 16, BF16) == 0  # short rows: no parts
 
 
 def _fork(g, table=A, src=A, out=A, n=1, n_slots=4, n_pages=8, wide=4, page=16):  # noqa: F811
