@@ -156,8 +156,9 @@ __device__ __forceinline__ Limits limits_of(const DecodeArgs& a, const Span& s, 
 }
 
 // bf16: both products on matrix instructions of 16 x 8 x 16, a warp's 16 keys as two columns' worth of scores and one depth of V. Weights
-// enter the second product as two bf16 parts (2^-17), so that the result's only rounding is its own; the sum takes them in fp32. One tile
-// keeps its queries in registers up to 128 wide; two share every fragment of K and V that is read.
+// enter the second product as two bf16 parts (2^-17), so that the result's only rounding is its own; the sum takes them in fp32. The maximum
+// that weights refer to follows the scores only where they pass it by 8: until then a weight is at most 2^8, and the output is not rescaled
+// (64 rows: 175 -> 170 us). One tile keeps its queries in registers up to 128 wide; two share every fragment of K and V that is read.
 template <int D, int M>
 struct WarpBf16 {
     static constexpr int kChunks = D / 8, kDepth = D / 16;
@@ -269,37 +270,38 @@ struct WarpBf16 {
                         if (!(there >> key & 1) || at < x.low || at > x.limit) s[k][i][j] = kNone;
                     }
             }
-            float f[2];
+            float top[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float x = fmaxf(fmaxf(s[k][0][2 * h], s[k][0][2 * h + 1]), fmaxf(s[k][1][2 * h], s[k][1][2 * h + 1]));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                const float now = fmaxf(m[k][h], x), ref = now == kNone ? 0.f : now;  // no key yet: every weight is 2^-inf = 0
-                f[h] = ex2_approx(m[k][h] - ref);
-                m[k][h] = now;
-                float sum = 0.f;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float p = ex2_approx(s[k][i][2 * h + j] - ref);
-                        s[k][i][2 * h + j] = p;
-                        sum += p;
-                    }
-                l[k][h] = fmaf(l[k][h], f[h], sum);
+                top[h] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
             }
-            if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+            if (__any_sync(0xffffffffu, top[0] > m[k][0] + 8.f || top[1] > m[k][1] + 8.f)) {
+                float f[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float now = fmaxf(m[k][h], top[h]);
+                    f[h] = now == kNone ? 0.f : ex2_approx(m[k][h] - now);
+                    m[k][h] = now;
+                    l[k][h] *= f[h];
+                }
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) {
                     o[k][i][0] *= f[0]; o[k][i][1] *= f[0]; o[k][i][2] *= f[1]; o[k][i][3] *= f[1];
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {  // (row, keys 0-7), (row + 8, keys 0-7), then keys 8-15
-                const float x = s[k][i >> 1][2 * (i & 1)], y = s[k][i >> 1][2 * (i & 1) + 1];
-                hi[k][i] = pack2(x, y);
-                lo[k][i] = pack2(x - __uint_as_float(hi[k][i] << 16), y - __uint_as_float(hi[k][i] & 0xffff0000u));
+            for (int h = 0; h < 2; ++h) {
+                const float ref = m[k][h] == kNone ? 0.f : m[k][h];  // no key yet: every weight is 2^-inf = 0
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {  // (row, keys 0-7), (row + 8, keys 0-7), then keys 8-15
+                    const float x = ex2_approx(s[k][i][2 * h] - ref), y = ex2_approx(s[k][i][2 * h + 1] - ref);
+                    l[k][h] += x + y;
+                    const uint32_t u = pack2(x, y);
+                    hi[k][2 * i + h] = u;
+                    lo[k][2 * i + h] = pack2(x - __uint_as_float(u << 16), y - __uint_as_float(u & 0xffff0000u));
+                }
             }
         }
         if (all) {
@@ -320,7 +322,7 @@ struct WarpBf16 {
         }
     }
 
-    // Maximum and sum of each row, from the lanes that hold them.
+    // Reference maximum and sum of each row, from the lanes that hold them.
     __device__ __forceinline__ void statistics(float* ms, float* ls) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
