@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -930,7 +931,8 @@ def gdn2_attn_decode(q, k_pages, v_pages, table, lengths, o, slots=None, *, scal
     _check(lib.gdn2_attn_decode(
         *_rows(q, q.dtype, q.shape, 2, "q", dev), _pool(k_pages, q.dtype, Hkv, d, "k_pages", dev),
         _pool(v_pages, q.dtype, Hkv, d, "v_pages", dev, k_pages), *where, n_slots, k_pages.shape[0], wide, k_pages.shape[2],
-        _dense(o, q.dtype, q.shape, "o", dev), B, N, Hq, Hkv, d, float(d ** -0.5 if scale is None else scale), int(window), dt, pw, nw,
+        _dense(o, q.dtype, q.shape, "o", dev), B, N, Hq, Hkv, d, float(d ** -0.5 if scale is None else scale),
+        min(_int(window, "window", 0, 2 ** 62), 2 ** 31 - 1), dt, pw, nw,
         _raw_stream(stream, dev)), "gdn2_attn_decode")
     return o
 
@@ -952,6 +954,14 @@ def _pages(table, lengths, refs, dev):
             _dense(refs, i32, (pages,), "refs", dev)), rows, pages, wide
 
 
+def _int(v, name, least, most):
+    """v as an int in [least, most]: the C types would wrap what lies outside."""
+    v = operator.index(v)
+    if not least <= v <= most:
+        raise ValueError(f"{name}: {least} to {most} expected, got {v}")
+    return v
+
+
 def _indices(t, name, dev, n=None):
     """Pointer of an int32 tensor [n] of row or page numbers."""
     import torch
@@ -970,13 +980,14 @@ def pages_append(table, lengths, refs, slots, tokens, *, page, stream=None):
 
     dev = _device(table)
     where, rows, pages, wide = _pages(table, lengths, refs, dev)
-    n = slots.shape[0]
-    each = tokens if isinstance(tokens, int) else 0
-    if not isinstance(tokens, (int, torch.Tensor)):
-        raise TypeError("tokens is an int or an int32 tensor")
+    n, each, counts = slots.shape[0], 0, None
+    if isinstance(tokens, torch.Tensor):
+        counts = _indices(tokens, "tokens", dev, n)
+    else:
+        each = _int(tokens, "tokens", 0, 2 ** 31 - 1)
     ok = torch.empty((n,), dtype=torch.int32, device=table.device)
-    _check(lib.gdn2_pages_append(*where, _indices(slots, "slots", dev), None if isinstance(tokens, int) else _indices(tokens, "tokens", dev, n),
-                                 each, ok.data_ptr(), n, rows, pages, wide, page, _raw_stream(stream, dev)), "gdn2_pages_append")
+    _check(lib.gdn2_pages_append(*where, _indices(slots, "slots", dev), counts, each, ok.data_ptr(), n, rows, pages, wide,
+                                 _int(page, "page", 1, 65536), _raw_stream(stream, dev)), "gdn2_pages_append")
     return ok
 
 
@@ -990,11 +1001,10 @@ def pages_fork(table, lengths, refs, src, dst, *, page, stream=None):
     dev = _device(table)
     where, rows, pages, wide = _pages(table, lengths, refs, dev)
     n = src.shape[0]
-    got = torch.empty((3, n), dtype=torch.int32, device=table.device)
-    base = got.data_ptr()
-    _check(lib.gdn2_pages_fork(*where, _indices(src, "src", dev), _indices(dst, "dst", dev, n), base, base + 4 * n, base + 8 * n, n, rows, pages,
-                               wide, page, _raw_stream(stream, dev)), "gdn2_pages_fork")
-    return got.unbind(0)
+    copy_from, copy_to, ok = (torch.empty((n,), dtype=torch.int32, device=table.device) for _ in range(3))
+    _check(lib.gdn2_pages_fork(*where, _indices(src, "src", dev), _indices(dst, "dst", dev, n), copy_from.data_ptr(), copy_to.data_ptr(),
+                               ok.data_ptr(), n, rows, pages, wide, _int(page, "page", 1, 65536), _raw_stream(stream, dev)), "gdn2_pages_fork")
+    return copy_from, copy_to, ok
 
 
 @_on_stream

@@ -1,6 +1,8 @@
 // attn_common.cuh -- shared by the operators of attention layers: the paged cache of keys and values, and the position rotation.
 #pragma once
 
+#include <atomic>
+
 #include "ssm_common.cuh"
 
 namespace gdn2 {
@@ -25,6 +27,18 @@ struct Cache {
         return p >= 0 && p < n_pages ? p : -1;
     }
 };
+
+// SMs of the current device, asked for once per device (a call's grid and workspace go by it). 152 where there is none.
+inline int sm_count() {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 152;
+    if (dev < kDevices && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
+    if (dev < kDevices) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
 
 inline bool attn_dtype_ok(gdn2_dtype dt) { return dt == GDN2_F32 || dt == GDN2_BF16; }
 inline size_t attn_esize(gdn2_dtype dt) { return dt == GDN2_BF16 ? 2 : 4; }

@@ -823,12 +823,6 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
     for (int c = threadIdx.x; c < a.d; c += 128) o[c] = from_f32<T>(((outs[0][c] + outs[1][c]) + (outs[2][c] + outs[3][c])) * inv);
 }
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
-    return n > 0 ? n : 152;
-}
-
 // Widths that a kernel is built for, and blocks per SM: some 128 KB of copies in flight on an SM, which its share of the copy rate takes.
 int width_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 // Two tiles of query rows share the copies of K and V where there are two and their sums fit the registers.

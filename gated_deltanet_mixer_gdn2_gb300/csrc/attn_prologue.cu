@@ -121,7 +121,7 @@ struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
     uint2 u[2];
-    static constexpr int kFlight = 3, kGradFlight = 2, kBlocks = 4;  // rows on their way, blocks per SM
+    static constexpr int kFlight = 3, kGradFlight = 3, kBlocks = 4;  // rows on their way, blocks per SM
     __device__ __forceinline__ void load(const __nv_bfloat16* p, const Place& at) {
         u[0] = __ldg(reinterpret_cast<const uint2*>(p + at.e0));
         u[1] = __ldg(reinterpret_cast<const uint2*>(p + at.e1));
@@ -141,7 +141,7 @@ struct Raw8<__nv_bfloat16> {
 template <>
 struct Raw8<float> {
     ulonglong2 u[2];
-    static constexpr int kFlight = 2, kGradFlight = 1, kBlocks = 3;
+    static constexpr int kFlight = 2, kGradFlight = 2, kBlocks = 3;
     __device__ __forceinline__ void load(const float* p, const Place& at) {
         u[0] = __ldg(reinterpret_cast<const ulonglong2*>(p + at.e0));
         u[1] = __ldg(reinterpret_cast<const ulonglong2*>(p + at.e1));
@@ -316,9 +316,12 @@ __global__ void __launch_bounds__(kThreads, kGradBlocks) prologue_grad_kernel(co
     const int lane = threadIdx.x % L, group = threadIdx.x / L, groups = kThreads / L;
     const int token = group % a.tokens, part = group / a.tokens, step = groups / a.tokens;
     const Place at = place_of<kPairs>(lane, a.d, a.rot);
-    uint64_t acc[2][4];
+    // the lane's sums of q's weight, and of k's in its own places of shared memory: registers are wanted for loads
+    uint64_t acc[4];
+    ulonglong2* const own[2] = {reinterpret_cast<ulonglong2*>(&red[group][at.e0]), reinterpret_cast<ulonglong2*>(&red[group][at.e1])};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[0][i] = acc[1][i] = 0;
+    for (int i = 0; i < 4; ++i) acc[i] = 0;
+    if (at.mine) *own[0] = *own[1] = make_ulonglong2(0, 0);
     frequencies(a, sh);
     constexpr int kFlight = Raw8<T>::kGradFlight;
     Raw8<T> rx[kFlight], rg[kFlight];
@@ -352,6 +355,9 @@ __global__ void __launch_bounds__(kThreads, kGradBlocks) prologue_grad_kernel(co
             }
             const int rounds = (H + step - 1) / step;
             int h = part;
+            uint64_t sum[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] = side ? 0 : acc[e];
             for (int i = 0; i < rounds; i += kFlight) {
 #pragma unroll
                 for (int u = 0; u < kFlight; ++u) {
@@ -372,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, kGradBlocks) prologue_grad_kernel(co
                         const uint64_t inv2 = f32x2(inv, inv), m2 = f32x2(m, m);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const uint64_t next = fma_f32x2(g[e], mul_f32x2(x[e], inv2), acc[side][e]);
-                            acc[side][e] = here ? next : acc[side][e];  // what is read along may not be finite
+                            const uint64_t next = fma_f32x2(g[e], mul_f32x2(x[e], inv2), sum[e]);
+                            sum[e] = here ? next : sum[e];  // what is read along may not be finite
                             g[e] = mul_f32x2(inv2, fma_f32x2(x[e], m2, gw[e]));
                         }
                     }
@@ -385,19 +391,30 @@ __global__ void __launch_bounds__(kThreads, kGradBlocks) prologue_grad_kernel(co
                     h += step;
                 }
             }
+            if (!side) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[e] = sum[e];
+            } else if (weight && at.mine) {
+                ulonglong2 p = *own[0], q = *own[1];
+                *own[0] = make_ulonglong2(add_f32x2(p.x, sum[0]), add_f32x2(p.y, sum[1]));
+                *own[1] = make_ulonglong2(add_f32x2(q.x, sum[2]), add_f32x2(q.y, sum[3]));
+            }
         }
     }
     if (!a.parts) return;
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
+    for (int side = 1; side >= 0; --side) {
         __syncthreads();
-        if (at.mine) {
-            *reinterpret_cast<ulonglong2*>(&red[group][at.e0]) = make_ulonglong2(acc[side][0], acc[side][1]);
-            *reinterpret_cast<ulonglong2*>(&red[group][at.e1]) = make_ulonglong2(acc[side][2], acc[side][3]);
+        if (!side) {
+            if (at.mine) {
+                *own[0] = make_ulonglong2(acc[0], acc[1]);
+                *own[1] = make_ulonglong2(acc[2], acc[3]);
+            }
+            __syncthreads();
         }
-        __syncthreads();
         for (int c = threadIdx.x; c < a.d; c += kThreads) {
             float v = 0.f;
+#pragma unroll 8
             for (int k = 0; k < groups; ++k) v += red[k][c];
             a.parts[(static_cast<long long>(blockIdx.x) * 2 + side) * a.d + c] = v;
         }
@@ -421,12 +438,6 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const float* parts, i
 #pragma unroll
     for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
     if (lane == 0 && blockIdx.x * 32 + warp < d) out[blockIdx.x * 32 + warp] = v;
-}
-
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
-    return n > 0 ? n : 152;
 }
 
 template <typename T, int L>

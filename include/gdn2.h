@@ -488,6 +488,7 @@ gdn2_status gdn2_block_norm_backward(const void* x, const void* z, const float* 
  *     slots int32 [B] maps the call's rows to rows of the table, as it maps them to rows of the mixers' state pools (NULL: row b is row
  *     b); a slot outside [0, n_slots) marks the row inactive: nothing of it is read or written. All of this is read on the device;
  *     lengths are clamped to [0, max_pages * page], so that wrong values give wrong results, but no access outside the tensors.
+ *   - A workspace serves one call at a time: calls, and graphs, whose kernels may overlap have one each.
  *   - Sizes: d a multiple of 16 up to 256, page any size up to 65536, max_pages * page below 2^30.
  *   - Sequences, rows and ld_* as for the gdn2_ssm_* entry points: token tensors may be slices of wider rows that start on 16-byte
  *     boundaries, their ld a multiple of 8 elements. Rows of no sequence (packed) are neither read nor written. Outputs do not overlap inputs.

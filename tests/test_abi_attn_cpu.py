@@ -178,6 +178,11 @@ def test_binding_refusals(g2):  # noqa: F811
         (TypeError, lambda: g2.pages_release.plain(table, lengths, new(0, 5, dtype=i32), slots.long())),
         (ValueError, lambda: g2.pages_release.plain(new(1, 2, 4, dtype=i32), lengths, new(0, 5, dtype=i32), slots)),
         (TypeError, lambda: g2.pages_append.plain(table, lengths, new(0, 5, dtype=i32), slots, 1.5, page=16)),
+        (ValueError, lambda: g2.pages_append.plain(table, lengths, new(0, 5, dtype=i32), slots, -1, page=16)),
+        (ValueError, lambda: g2.pages_append.plain(table, lengths, new(0, 5, dtype=i32), slots, 2 ** 32 + 1, page=16)),  # would wrap to 1
+        (ValueError, lambda: g2.pages_append.plain(table, lengths, new(0, 5, dtype=i32), slots, 1, page=2 ** 32 + 16)),
+        (ValueError, lambda: g2.pages_fork.plain(table, lengths, new(0, 5, dtype=i32), slots, slots, page=0)),
+        (ValueError, lambda: g2.gdn2_attn_decode.plain(q, *pools, table, lengths, ok, slots, window=-1, workspace=ws)),
     ]:
         with pytest.raises(exc):
             f_()
