@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kTile = 16;   // query rows of a matrix instruction; a unit has one or two such tiles
 constexpr int kKeys = 16;   // keys of a warp's step
+constexpr int kKept = 256;  // rows whose slots and lengths a block keeps
 constexpr float kNone = -INFINITY;
 
 struct DecodeArgs {
@@ -35,12 +36,12 @@ struct Span {
     int slot, lo, hi;
     __device__ __forceinline__ int base() const { return lo & ~(kKeys - 1); }
 };
+__device__ __forceinline__ Span span_of(const DecodeArgs& a, int slot, int length) {
+    return Span{slot, a.window ? max(length - a.N - a.window + 1, 0) : 0, length};
+}
 __device__ __forceinline__ Span span_of(const DecodeArgs& a, int b) {
-    Span s{a.cache.row_of(b), 0, 0};
-    if (s.slot < 0) return s;
-    s.hi = a.cache.length_of(s.slot);
-    if (a.window) s.lo = max(s.hi - a.N - a.window + 1, 0);
-    return s;
+    const int slot = a.cache.row_of(b);
+    return slot < 0 ? Span{-1, 0, 0} : span_of(a, slot, a.cache.length_of(slot));
 }
 
 template <int kStep>
@@ -116,30 +117,50 @@ struct Layout {
     static constexpr int kSmem = W * S * kStage + kQ + kOut + kProb;
 };
 
-// Where a block's walk over the steps stands.
+// What a unit costs beside its steps, in steps: its queries' way in, the joining of its warps, and its way out. Stretches are dealt out by steps
+// and toll, or a block that gets a run of rows of one token each would take as long as several: 59 rows of which every other holds a few
+// tokens take 26 us (51 without toll, 32 with 1, 29 with 8), 64 ragged rows 162 (169, 168, 160).
+constexpr int kToll = 4;
+__device__ __forceinline__ long long cost_of(int steps, int units) { return steps > 0 ? static_cast<long long>(steps + kToll) * units : 0; }
+
+// Where a block's walk over its stretch stands, and the steps (and tolls) that are left of it. The lanes of a warp walk together.
 template <int kStep>
 struct Cursor {
-    int b, ht, step, steps;  // row; key head and tile of query rows; step of the unit and its steps
+    int b, ht, step, steps;  // row; key head and tiles of query rows; step of the unit and its steps
+    long long left;
     Span span;
-    // To row b or the first after it that has steps; b = B at the end.
-    __device__ __forceinline__ void settle(const DecodeArgs& a) {
-        for (; b < a.B; ++b) {
-            span = span_of(a, b);
-            steps = steps_of<kStep>(span);
-            if (steps > 0) return;
+    // To row b or the first after it that has steps, 32 rows at a look; nothing is left behind the last one.
+    template <typename Rows>
+    __device__ __forceinline__ void settle(const DecodeArgs& a, const Rows& rows) {
+        const int lane = threadIdx.x & 31;
+        for (; b < a.B; b += 32) {
+            const Span s = b + lane < a.B ? rows(b + lane) : Span{-1, 0, 0};
+            const int n = steps_of<kStep>(s);
+            const unsigned some = __ballot_sync(0xffffffffu, n > 0);
+            if (some) {
+                const int from = __ffs(some) - 1;
+                b += from;
+                steps = __shfl_sync(0xffffffffu, n, from);
+                span = Span{__shfl_sync(0xffffffffu, s.slot, from), __shfl_sync(0xffffffffu, s.lo, from), __shfl_sync(0xffffffffu, s.hi, from)};
+                return;
+            }
         }
         span = Span{-1, 0, 0};
         steps = 0;
+        left = 0;
     }
     // Goes on; true when that is another unit.
-    __device__ __forceinline__ bool next(const DecodeArgs& a, int by) {
+    template <typename Rows>
+    __device__ __forceinline__ bool next(const DecodeArgs& a, const Rows& rows, int by) {
         step += by;
-        if (step < steps) return false;
+        left -= by;
+        if (step < steps || left <= 0) return false;
         step = 0;
+        left -= kToll;
         if (++ht < a.Hkv * a.tiles) return true;
         ht = 0;
         ++b;
-        settle(a);
+        settle(a, rows);
         return true;
     }
 };
@@ -537,6 +558,7 @@ __global__ void __launch_bounds__(32 * W) decode_kernel(const __grid_constant__ 
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long red[W], shared_first;
     __shared__ int shared_row;
+    __shared__ int2 kept[kKept];
     __shared__ unsigned seen[W][S];  // which of a stage's keys were copied
     __shared__ float sm[W][kRows], sl[W][kRows], sf[W][kRows], top[kRows], sum[kRows];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
@@ -546,47 +568,47 @@ __global__ void __launch_bounds__(32 * W) decode_kernel(const __grid_constant__ 
     float* out = reinterpret_cast<float*>(qs + Lay::kQ);
     float* prob = out + kRows * D + warp * (kKeys * kRows + kRows);
 
-    // the steps of row b's units, all together
-    auto steps_at = [&](int b) { return b < a.B ? static_cast<long long>(steps_of<kStep>(span_of(a, b))) * units : 0LL; };
-    // rows without a visible key
+    // Rows without a visible key.
     auto clear_row = [&](int b) {
         T* o = static_cast<T*>(a.o) + static_cast<long long>(b) * a.N * a.Hq * a.d;
         for (int i = tid; i < a.N * a.Hq * a.d; i += kThreads) o[i] = from_f32<T>(0.f);
     };
-    auto clear_rows = [&]() {
-        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-            const Span s = span_of(a, b);
-            if (s.slot >= 0 && steps_of<kStep>(s) == 0) clear_row(b);
-        }
-    };
+    // The rows' slots and lengths, of the first ones from shared memory.
+    auto row_span = [&](int b) { return b < kKept ? span_of(a, kept[b].x, kept[b].y) : span_of(a, b); };
     if (!a.whole) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining blocks may come up meanwhile; they wait for all of this
 
     Cursor<kStep> at;
-    long long left;
     if (a.whole) {
         at.b = blockIdx.x / units;
         at.span = span_of(a, at.b);
         at.steps = steps_of<kStep>(at.span);
         at.ht = blockIdx.x - at.b * units;
         at.step = 0;
-        left = at.steps;
-        if (left == 0) {
+        at.left = at.steps;
+        if (at.steps == 0) {
             if (at.ht == 0 && at.span.slot >= 0) clear_row(at.b);
             return;
         }
     } else {
-        // this block's stretch of all steps, and the row that holds its first
-        const long long n0 = steps_at(tid);
+        // this block's stretch of all steps and tolls, and the row that holds its first
+        for (int b = tid; b < min(a.B, kKept); b += kThreads) {
+            const Span s = span_of(a, b);
+            kept[b] = make_int2(s.slot, s.hi);
+        }
+        __syncthreads();
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+            const Span s = row_span(b);
+            if (s.slot >= 0 && steps_of<kStep>(s) == 0) clear_row(b);
+        }
+        auto cost_at = [&](int b) { return b < a.B ? cost_of(steps_of<kStep>(row_span(b)), units) : 0LL; };
+        const long long n0 = cost_at(tid);
         long long rest = 0, total, more = 0;
-        for (int b = tid + kThreads; b < a.B; b += kThreads) rest += steps_at(b);
-        long long behind = block_scan<kThreads>(n0, red, total);  // the steps up to and with this thread's row
+        for (int b = tid + kThreads; b < a.B; b += kThreads) rest += cost_at(b);
+        long long behind = block_scan<kThreads>(n0, red, total);  // what is in front of the row after this thread's
         if (a.B > kThreads) block_scan<kThreads>(rest, red, more);
         const long long all = total + more, per = steps_per_block(all, gridDim.x);
         const long long begin = blockIdx.x * per, end = begin + per < all ? begin + per : all;
-        if (begin >= end) {
-            clear_rows();
-            return;
-        }
+        if (begin >= end) return;
         if (tid == 0) shared_row = -1;
         __syncthreads();
         long long n = n0, before = 0;
@@ -600,19 +622,22 @@ __global__ void __launch_bounds__(32 * W) decode_kernel(const __grid_constant__ 
             before += total;
             b0 += kThreads;
             if (b0 >= a.B) return;  // not with lengths that stay as they are
-            n = steps_at(b0 + tid);
+            n = cost_at(b0 + tid);
             behind = block_scan<kThreads>(n, red, total) + before;
         }
         at.b = shared_row;
-        at.settle(a);
-        if (at.b >= a.B) return;
+        at.left = end - begin;
+        at.settle(a, row_span);
+        if (at.left <= 0) return;
+        // a unit's toll lies in front of its steps
         const long long in = begin - shared_first;
-        at.ht = static_cast<int>(in / at.steps);
-        at.step = static_cast<int>(in - static_cast<long long>(at.ht) * at.steps);
-        left = end - begin;
+        at.ht = static_cast<int>(in / (at.steps + kToll));
+        const int place = static_cast<int>(in - static_cast<long long>(at.ht) * (at.steps + kToll));
+        at.step = max(place - kToll, 0);
+        at.left -= max(kToll - place, 0);
+        if (at.left <= 0) return;
     }
     Cursor<kStep> ahead = at;
-    long long unread = left;
 
     // The copies of one step, all lanes taking part; `from`: where its keys lie (found a step ahead). Keys that no token of the row sees, or
     // that have no page, are not read: their places become zeros, since what is there may not be finite.
@@ -641,7 +666,7 @@ __global__ void __launch_bounds__(32 * W) decode_kernel(const __grid_constant__ 
     constexpr int kPer = kKeys * kChunks / 32, kRowsPer = kChunks < 32 ? 32 / kChunks : 1;  // copies per lane, rows that one of them spans
     const int lane_row = kChunks < 32 ? lane / kChunks : 0, lane_chunk = lane % kChunks;
     auto copy = [&](int stage) {
-        if (unread > 0) {
+        if (ahead.left > 0) {
             const uint32_t kt = smem_u32(stages + stage * Lay::kStage);
             unsigned there;
             if constexpr (kPaged) {
@@ -672,10 +697,8 @@ __global__ void __launch_bounds__(32 * W) decode_kernel(const __grid_constant__ 
                     copy16(to + Lay::kHalf, vp + at, ok);
                 }
             }
-            if (--unread > 0) {
-                if (ahead.next(a, 1)) ahead_head = ahead.ht / a.tiles;
-                from = where();
-            }
+            if (ahead.next(a, row_span, 1)) ahead_head = ahead.ht / a.tiles;
+            if (ahead.left > 0) from = where();
         }
         copies_commit();
     };
@@ -684,10 +707,9 @@ __global__ void __launch_bounds__(32 * W) decode_kernel(const __grid_constant__ 
 
     typename WarpOf<T, D, M>::type acc;
     int stage = 0;
-    while (left > 0) {
+    while (at.left > 0) {
         const int unit_row = at.ht % a.tiles * kRows, head = at.ht / a.tiles;
-        const int n_steps = static_cast<int>(left < at.steps - at.step ? left : at.steps - at.step);
-        if (n_steps <= 0) return;
+        const int n_steps = static_cast<int>(at.left < at.steps - at.step ? at.left : at.steps - at.step);
         const int valid = min(kRows, a.N * a.G - unit_row);
         // the unit's queries, zeros for rows that it does not have
         for (int i = tid; i < kRows * kChunks; i += kThreads) {
@@ -758,11 +780,9 @@ __global__ void __launch_bounds__(32 * W) decode_kernel(const __grid_constant__ 
                 part[kRows * D + kRows + tid] = sum[tid];
             }
         }
-        left -= n_steps;
-        if (left > 0) at.next(a, n_steps);
+        at.next(a, row_span, n_steps);
         __syncthreads();  // the block's output, statistics and queries are free again
     }
-    if (!a.whole) clear_rows();
 }
 
 // Joins the parts of a unit that several blocks hold: one block per unit and row, its warps each a share of the parts. It comes up while the
@@ -777,7 +797,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, r = blockIdx.y, row = tile * kRows + r;
     long long lead = 0, all = 0;
     for (int i = threadIdx.x; i < a.B; i += 128) {
-        const long long n = steps_of<kStep>(span_of(a, i));
+        const long long n = cost_of(steps_of<kStep>(span_of(a, i)), units);
         all += n;
         if (i < b) lead += n;
     }
@@ -786,7 +806,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
     lead = total;
     block_scan<128>(all, red, total);
     const int steps = steps_of<kStep>(span_of(a, b));
-    const long long per = steps_per_block(total * units, blocks), start = lead * units + static_cast<long long>(ht) * steps;
+    const long long per = steps_per_block(total, blocks), start = lead + static_cast<long long>(ht) * (steps + kToll) + kToll;
     const int c0 = static_cast<int>(start / per), c1 = static_cast<int>((start + steps - 1) / per);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (steps <= 1 || c0 == c1 || row >= a.N * a.G) return;
@@ -835,7 +855,7 @@ int blocks_of(int d, int tiles, gdn2_dtype dt) {
 template <typename T, int D, int W, int S, int M, bool kPaged>
 cudaError_t launch(DecodeArgs& a, int blocks, cudaStream_t s) {
     using Lay = Layout<T, D, W, S, M>;
-    static_assert(Lay::kSmem + 4096 <= 232448, "shared memory of a block");
+    static_assert(Lay::kSmem + 6144 <= 232448, "shared memory of a block");
     cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, D, W, S, M, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmem);
     if (e != cudaSuccess) return e;
     const int units = a.B * a.Hkv * a.tiles;
