@@ -2,12 +2,18 @@
 //     o = softmax(scale q K^T over the visible tokens) V,   token n of N sees the tokens up to length - N + n (and within the window)
 //
 // Every key and value is read once for 4 N H_q / H_kv operations per element: bound by memory. A unit is the cache of one key head of one
-// row against up to 16 of its query rows (N tokens times the heads of the group, the matrix instruction's height); its keys are cut into
-// steps of 16 per warp. All units' steps, one after another, are dealt out to the blocks in equal stretches, found from the lengths on the
-// device: a long row is split over many blocks and short rows share one, whatever the batch. Each warp streams its own keys through its own
-// stages of shared memory, by asynchronous copies that run ahead across units, and keeps its own running maximum, sum and output: no block
-// barrier but at a unit's end, where the warps' results are joined. A unit that lies in one block leaves as the result; of one that does
-// not, each block leaves its part in the workspace, and a second launch joins the parts in their order (no atomics).
+// row against 16 or 32 of its query rows (N tokens times the heads of the group); its keys are cut into steps of 16 per warp. All units'
+// steps, one after another, are dealt out to the blocks in equal stretches, found from the lengths on the device: a long row is split over
+// many blocks and short rows share one, whatever the batch. Each warp streams its own keys through its own stages of shared memory, by
+// asynchronous copies that run ahead across units, and keeps its own running maximum, sum and output: no block barrier but at a unit's end,
+// where the warps' results are joined. A unit that lies in one block leaves as the result; of one that does not, each block leaves its part
+// in the workspace, and a second launch joins the parts in their order (no atomics).
+//
+// 131072 tokens of 8 key heads of 128 in bf16: 88 us, 6.1 TB/s (0.90 of the copy rate); 64 rows of 0 to 16384 tokens, 2 heads of 256: 162 us
+// (0.93). Of the time, some 12 us are the way in (lengths, table, first keys) and out (parts), whatever the length. The products have 16
+// rows where a tensor-memory product has 128, so they run on warp-wide matrix instructions: their pipe is a quarter busy at the copy rate.
+// With two tiles (drafted tokens) it is the latency of a step's chain that bounds it: 16 rows of 8192 tokens, 4 tokens of 32 heads each, 69 us
+// for 38 of copies. A warp per tile that shares copies with its neighbour was slower (89), two tiles as two units read everything twice (84).
 #include "attn_common.cuh"
 
 namespace gdn2 {
@@ -70,7 +76,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* red, lon
     return v;
 }
 
-// Steps of a block: all blocks together cover them. One step is enough (900 tokens of 4 key heads: 9.7 us; with two at least 12.4, four 13.8).
+// Steps and tolls of a block: all blocks together cover them. One is enough (900 tokens of 4 key heads: 9.7 us; with two at least 12.4, four 13.8).
 __device__ __forceinline__ long long steps_per_block(long long total, int blocks) {
     const long long per = (total + blocks - 1) / blocks;
     return per > 0 ? per : 1;
@@ -122,6 +128,38 @@ struct Layout {
 // tokens take 26 us (51 without toll, 32 with 1, 29 with 8), 64 ragged rows 162 (169, 168, 160).
 constexpr int kToll = 4;
 __device__ __forceinline__ long long cost_of(int steps, int units) { return steps > 0 ? static_cast<long long>(steps + kToll) * units : 0; }
+
+// All rows' costs in a row, dealt out in stretches: a thread has a run of rows, `mine` their cost, `behind` the cost up to and with them.
+template <int kThreads, int kStep>
+struct Dealing {
+    int first, last;
+    long long mine, behind, total;
+    template <typename Rows>
+    __device__ __forceinline__ void count(const DecodeArgs& a, const Rows& rows, int units, long long* red) {
+        const int run = (a.B + kThreads - 1) / kThreads;
+        first = min(static_cast<int>(threadIdx.x) * run, a.B);
+        last = min(first + run, a.B);
+        mine = 0;
+#pragma unroll 4
+        for (int b = first; b < last; ++b) mine += cost_of(steps_of<kStep>(rows(b)), units);
+        behind = block_scan<kThreads>(mine, red, total);
+    }
+    // The thread that has place v among all costs (v < total) leaves there the row that holds it and the cost before that row.
+    template <typename Rows>
+    __device__ __forceinline__ void find(const DecodeArgs& a, const Rows& rows, int units, long long v, int* row, long long* before) const {
+        long long at = behind - mine;
+        if (v < at || v >= behind) return;
+        for (int b = first; b < last; ++b) {
+            const long long n = cost_of(steps_of<kStep>(rows(b)), units);
+            if (v < at + n) {
+                *row = b;
+                *before = at;
+                return;
+            }
+            at += n;
+        }
+    }
+};
 
 // Where a block's walk over its stretch stands, and the steps (and tolls) that are left of it. The lanes of a warp walk together.
 template <int kStep>
@@ -568,10 +606,11 @@ __global__ void __launch_bounds__(32 * W) decode_kernel(const __grid_constant__ 
     float* out = reinterpret_cast<float*>(qs + Lay::kQ);
     float* prob = out + kRows * D + warp * (kKeys * kRows + kRows);
 
-    // Rows without a visible key.
+    // Rows without a visible key: a warp clears one.
     auto clear_row = [&](int b) {
-        T* o = static_cast<T*>(a.o) + static_cast<long long>(b) * a.N * a.Hq * a.d;
-        for (int i = tid; i < a.N * a.Hq * a.d; i += kThreads) o[i] = from_f32<T>(0.f);
+        const int n = a.N * a.Hq * a.d * (int)sizeof(T) / 16;
+        uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + static_cast<long long>(b) * a.N * a.Hq * a.d);
+        for (int i = lane; i < n; i += 32) o[i] = make_uint4(0, 0, 0, 0);
     };
     // The rows' slots and lengths, of the first ones from shared memory.
     auto row_span = [&](int b) { return b < kKept ? span_of(a, kept[b].x, kept[b].y) : span_of(a, b); };
@@ -586,7 +625,7 @@ __global__ void __launch_bounds__(32 * W) decode_kernel(const __grid_constant__ 
         at.step = 0;
         at.left = at.steps;
         if (at.steps == 0) {
-            if (at.ht == 0 && at.span.slot >= 0) clear_row(at.b);
+            if (at.ht == 0 && warp == 0 && at.span.slot >= 0) clear_row(at.b);
             return;
         }
     } else {
@@ -595,36 +634,20 @@ __global__ void __launch_bounds__(32 * W) decode_kernel(const __grid_constant__ 
             const Span s = span_of(a, b);
             kept[b] = make_int2(s.slot, s.hi);
         }
+        if (tid == 0) shared_row = -1;
         __syncthreads();
-        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        for (int b = blockIdx.x * W + warp; b < a.B; b += gridDim.x * W) {
             const Span s = row_span(b);
             if (s.slot >= 0 && steps_of<kStep>(s) == 0) clear_row(b);
         }
-        auto cost_at = [&](int b) { return b < a.B ? cost_of(steps_of<kStep>(row_span(b)), units) : 0LL; };
-        const long long n0 = cost_at(tid);
-        long long rest = 0, total, more = 0;
-        for (int b = tid + kThreads; b < a.B; b += kThreads) rest += cost_at(b);
-        long long behind = block_scan<kThreads>(n0, red, total);  // what is in front of the row after this thread's
-        if (a.B > kThreads) block_scan<kThreads>(rest, red, more);
-        const long long all = total + more, per = steps_per_block(all, gridDim.x);
-        const long long begin = blockIdx.x * per, end = begin + per < all ? begin + per : all;
+        Dealing<kThreads, kStep> all;
+        all.count(a, row_span, units, red);
+        const long long per = steps_per_block(all.total, gridDim.x);
+        const long long begin = blockIdx.x * per, end = begin + per < all.total ? begin + per : all.total;
         if (begin >= end) return;
-        if (tid == 0) shared_row = -1;
+        all.find(a, row_span, units, begin, &shared_row, &shared_first);
         __syncthreads();
-        long long n = n0, before = 0;
-        for (int b0 = 0;;) {
-            if (begin >= behind - n && begin < behind) {
-                shared_row = b0 + tid;
-                shared_first = behind - n;
-            }
-            __syncthreads();
-            if (shared_row >= 0) break;
-            before += total;
-            b0 += kThreads;
-            if (b0 >= a.B) return;  // not with lengths that stay as they are
-            n = cost_at(b0 + tid);
-            behind = block_scan<kThreads>(n, red, total) + before;
-        }
+        if (shared_row < 0) return;  // not with lengths that stay as they are
         at.b = shared_row;
         at.left = end - begin;
         at.settle(a, row_span);
@@ -785,31 +808,36 @@ __global__ void __launch_bounds__(32 * W) decode_kernel(const __grid_constant__ 
     }
 }
 
-// Joins the parts of a unit that several blocks hold: one block per unit and row, its warps each a share of the parts. It comes up while the
-// parts are still being made and finds its place meanwhile.
+// Joins the parts of a unit that several blocks hold: one block per end of a stretch and query row, which acts where that end is the first inside
+// its unit's steps; its warps take a share of the parts each. It comes up while the parts are still being made and finds its place meanwhile.
 template <typename T, int D, int W, int M>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ DecodeArgs a, int blocks) {
     constexpr int kStep = kKeys * W, kRows = kTile * M, kCols = D / 32;
-    __shared__ long long red[4];
+    __shared__ long long red[4], before;
+    __shared__ int shared_row;
     __shared__ float tops[4], sums[4];
-    __shared__ float outs[4][D];
-    const int units = a.Hkv * a.tiles, b = blockIdx.x / units, ht = blockIdx.x % units, tile = ht % a.tiles, head = ht / a.tiles;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, r = blockIdx.y, row = tile * kRows + r;
-    long long lead = 0, all = 0;
-    for (int i = threadIdx.x; i < a.B; i += 128) {
-        const long long n = cost_of(steps_of<kStep>(span_of(a, i)), units);
-        all += n;
-        if (i < b) lead += n;
+    __shared__ __align__(16) float outs[4][D];  // written two columns at a time
+    const int units = a.Hkv * a.tiles, warp = threadIdx.x / 32, lane = threadIdx.x & 31, r = blockIdx.y;
+    auto row_span = [&](int b) { return span_of(a, b); };
+    if (threadIdx.x == 0) shared_row = -1;
+    Dealing<128, kStep> all;
+    all.count(a, row_span, units, red);
+    const long long per = steps_per_block(all.total, blocks), v = (blockIdx.x + 1) * per;
+    if (v < all.total) all.find(a, row_span, units, v, &shared_row, &before);
+    __syncthreads();
+    int b = -1, ht = 0, c0 = 0, c1 = 0;
+    if (shared_row >= 0) {
+        b = shared_row;
+        const int steps = steps_of<kStep>(row_span(b));
+        ht = static_cast<int>((v - before) / (steps + kToll));
+        const long long start = before + static_cast<long long>(ht) * (steps + kToll) + kToll;
+        c0 = static_cast<int>(start / per);
+        c1 = static_cast<int>((start + steps - 1) / per);
+        if (c0 != static_cast<int>(blockIdx.x) || c1 == c0) b = -1;
     }
-    long long total;
-    block_scan<128>(lead, red, total);
-    lead = total;
-    block_scan<128>(all, red, total);
-    const int steps = steps_of<kStep>(span_of(a, b));
-    const long long per = steps_per_block(total, blocks), start = lead + static_cast<long long>(ht) * (steps + kToll) + kToll;
-    const int c0 = static_cast<int>(start / per), c1 = static_cast<int>((start + steps - 1) / per);
+    const int tile = ht % a.tiles, head = ht / a.tiles, row = tile * kRows + r;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (steps <= 1 || c0 == c1 || row >= a.N * a.G) return;
+    if (b < 0 || row >= a.N * a.G) return;
     auto part = [&](int c) { return part_of(a, c, c == c0 ? 1 : 0, D, kRows); };
     float m = kNone;
     for (int c = c0 + static_cast<int>(threadIdx.x); c <= c1; c += 128) m = fmaxf(m, part(c)[kRows * D + r]);
@@ -858,11 +886,11 @@ cudaError_t launch(DecodeArgs& a, int blocks, cudaStream_t s) {
     static_assert(Lay::kSmem + 6144 <= 232448, "shared memory of a block");
     cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, D, W, S, M, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmem);
     if (e != cudaSuccess) return e;
-    const int units = a.B * a.Hkv * a.tiles;
+    const int units = a.B * a.Hkv * a.tiles;  // of all rows
     decode_kernel<T, D, W, S, M, kPaged><<<a.whole ? units : blocks, Lay::kThreads, Lay::kSmem, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess || a.whole) return e;
+    if ((e = cudaGetLastError()) != cudaSuccess || a.whole || blocks < 2) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(units, a.N * a.G < Lay::kRows ? a.N * a.G : Lay::kRows);
+    cfg.gridDim = dim3(blocks - 1, a.N * a.G < Lay::kRows ? a.N * a.G : Lay::kRows);
     cfg.blockDim = dim3(128);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -878,12 +906,13 @@ cudaError_t launch(DecodeArgs& a, int blocks, cudaStream_t s) {
     return a.cache.page % kKeys ? launch<T, D, W, S, M, false>(a, blocks, s) : launch<T, D, W, S, M, true>(a, blocks, s);
 }
 
-// A block per unit, and no parts to join, where no row can be long: the start is quicker (no walk over the lengths) and there is no second launch.
-// 256 rows of 300 tokens, 2 key heads of 128: 26.7 us against 37.7 in stretches. With few units their blocks leave SMs idle: one row of 500
-// tokens and 4 key heads 13.1 against 10.3, of 77 tokens 6.2 against 8.3.
+// A block per unit, and no parts to join, where no row can be long: the start is quicker (no look at the other rows) and there is no second
+// launch. With few units their blocks leave SMs idle, the more the longer their rows. In us, whole against in stretches: one row of 77 tokens
+// and 4 key heads 6.2 / 7.6, of 500 12.5 / 9.0; 16 rows of 400 and 4 heads 12.4 / 12.4, 64 rows 17.8 / 22.6; 64 rows of 1000 and 2 heads
+// 25.3 / 24.0, 256 rows 55 / 62.
 bool whole_units(long long units, int max_pages, int page) {
     const long long keys = static_cast<long long>(max_pages) * page;
-    return keys <= 256 || (keys <= 512 && units >= sm_count());
+    return keys <= 256 || (keys <= 1024 && units * 512 >= keys * sm_count());
 }
 
 gdn2_status decode_check(int B, int N, int Hq, int Hkv, int d, gdn2_dtype dt) {

@@ -5,7 +5,11 @@
 //
 // Bound by memory: every element is read once and written once for some 10 operations, which are packed two by two. A head's row belongs to
 // a group of lanes, eight elements each (both sides of four pairs), whose sum of squares comes by shuffles; a group keeps to one token, whose
-// cosines and sines it holds in registers, and has several rows' loads in flight.
+// cosines and sines it holds in registers, and has several rows' loads in flight. A block has eight tokens, whose angles it forms together.
+//
+// 16384 tokens of 32 + 8 heads of 128 in bf16: 60 us, 5.6 TB/s (0.83 of the copy rate), the issue slots 59% busy; a third of a wave of blocks is
+// what is lost. Tokens by fours 66 us, two rows in flight 64, a group's own stretch of heads without block barriers 66, elements side by side
+// with the pairs' other sides by shuffles 82. Gradients: 103 us (0.72), 158 in fp32 (0.94); 8192 tokens of 18 heads 34.
 #include "attn_common.cuh"
 
 namespace gdn2 {
@@ -457,7 +461,7 @@ cudaError_t launch(const PrologueArgs& a, dim3 grid, bool pairs, bool grad, cuda
     return a.d <= 64 ? launch<T, 8>(a, grid, pairs, grad, s) : a.d <= 128 ? launch<T, 16>(a, grid, pairs, grad, s) : launch<T, 32>(a, grid, pairs, grad, s);
 }
 
-// Lanes of a head's row, and tokens of a tile: as many as there are blocks for all SMs without, eight at most.
+// Lanes of a head's row, and tokens of a tile: eight, but fewer while that leaves fewer blocks than the SMs hold (4 x 152).
 int lanes_of(int d) { return d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 int tokens_of(int d, long long rows) {
     int t = kTokens;

@@ -159,7 +159,9 @@ def _attend64(q, k_pages, v_pages, table, lengths, slots, scale):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("lens,Hq,Hkv,d,page", [
     ([50000], 8, 1, 64, 16), ([20011], 4, 4, 128, 40), ([30000, 5, 1000], 16, 2, 256, 64),
-    ([(37 * i * i) % 900 if i % 5 else 0 for i in range(300)], 4, 2, 64, 32), ([3] * 700, 2, 1, 128, 4)])
+    ([(37 * i * i) % 900 if i % 5 else 0 for i in range(300)], 4, 2, 64, 32), ([3] * 700, 2, 1, 128, 4),
+    ([0] * 400 + [5] * 30 + [0] * 200 + [4000] + [0] * 300, 4, 2, 64, 16),                       # long runs of empty rows
+    ([2000] + [(7 * i) % 23 if i % 3 else 0 for i in range(4999)], 2, 1, 64, 8)])
 def test_long_rows_and_many_rows(g2, lens, Hq, Hkv, d, page, dtype):  # noqa: F811
     c = Case(lens, 1, Hq, Hkv, d, page, dtype, seed=len(lens))
     got = c.run(g2)
