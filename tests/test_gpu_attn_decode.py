@@ -260,3 +260,56 @@ def test_two_streams_at_once(g2):  # noqa: F811
         got = [g2.attn_decode(*a, stream=s) for a, s in zip(args, streams)]
     torch.cuda.synchronize()
     assert all(x.equal(y) for x, y in zip(got, want))
+
+
+def _dense64(q, k_pages, v_pages, table, lengths, slots, scale, window):
+    """Any shape, on the device in fp64: rows of inactive slots NaN; and the sums of p |v|."""
+    import torch
+
+    B, N, Hq, d = q.shape
+    pages, Hkv, page, _ = k_pages.shape
+    wide = table.shape[1]
+    o = torch.full(q.shape, float("nan"), dtype=torch.float64, device="cuda")
+    mag = torch.zeros_like(o)
+    for b in range(B):
+        s = int(slots[b])
+        if not 0 <= s < len(table):
+            continue
+        entries = torch.as_tensor(table[s].astype(np.int64), device="cuda")
+        there = ((entries >= 0) & (entries < pages)).repeat_interleave(page)
+        k, v = (p[entries.clamp(0, pages - 1)].transpose(0, 1).flatten(1, 2).double() for p in (k_pages, v_pages))
+        length = min(max(int(lengths[s]), 0), wide * page)
+        key = torch.arange(wide * page, device="cuda")
+        last = length - N + torch.arange(N, device="cuda")[:, None]
+        see = there & (key <= last) & ((key > last - window) if window else True)                     # [N, keys]
+        z = (q[b].double().reshape(N, Hkv, -1, d).transpose(0, 1) @ k[:, None].transpose(-1, -2)) * scale  # [Hkv, N, G, keys]
+        w = torch.softmax(z.masked_fill(~see[None, :, None], -float("inf")), -1).nan_to_num(0.0)
+        o[b], mag[b] = ((w @ x[:, None]).transpose(0, 1).reshape(N, Hq, d) for x in (v, v.abs()))
+    return o.cpu().numpy(), mag.cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("seed", range(30))
+def test_any_shape(g2, seed, dtype):  # noqa: F811
+    """Sizes, holes, shared pages, inactive rows, lengths past the table and windows by chance; rows of inactive slots stay."""
+    import torch
+
+    rng = np.random.default_rng(100 + seed)
+    B, rows, Hkv, G, N = rng.integers(1, 40), 45, rng.integers(1, 5), int(rng.choice([1, 2, 3, 5, 8, 16, 20])), int(rng.choice([1, 1, 2, 3, 6]))
+    d, page = 16 * int(rng.integers(1, 17)), int(rng.choice([1, 3, 8, 16, 24, 32, 48, 64]))
+    wide = max(1, int(rng.choice([100, 400, 1500, 3000]) // page))
+    pages = wide + 5
+    table = rng.integers(0, pages, (rows, wide))  # pages that rows share
+    table[rng.random(table.shape) < 0.1] = rng.choice([-1, pages, 2 ** 30])
+    top = wide * page
+    lengths = np.where(rng.random(rows) < 0.3, rng.choice([-1, 0, 1, N, top, top + 1, 2 ** 31 - 1], rows), rng.integers(0, top + 1, rows))
+    slots = rng.permutation(rows + 6)[:B] - 3
+    window = int(rng.choice([0, 0, 1, 7, 100, 10 ** 6, 2 ** 31 - 1]))
+    pools = [_dev(rng.standard_normal((pages, Hkv, page, d)), dtype) for _ in range(2)]
+    q, scale = _dev(rng.standard_normal((B, N, Hkv * G, d)), dtype), float(rng.choice([d ** -0.5, -0.05, 1.0 / d]))
+    o = torch.full_like(q, 7.0)
+    g2.gdn2_attn_decode(q, *pools, _int32(table), _int32(lengths), o, _int32(slots), scale=scale, window=window)
+    want, mag = _dense64(q, *pools, table, lengths, slots, scale, window)
+    dead = np.isnan(want[:, 0, 0, 0])
+    assert bool((o[torch.as_tensor(dead, device="cuda")] == 7).all())
+    _check(_np(o), want, mag, _reach(_np(q), _np(pools[0]), scale, top, dtype), dtype)
