@@ -8,8 +8,8 @@
 // cosines and sines it holds in registers, and has several rows' loads in flight. A block has eight tokens, whose angles it forms together.
 //
 // 16384 tokens of 32 + 8 heads of 128 in bf16: 60 us, 5.6 TB/s (0.83 of the copy rate), the issue slots 59% busy; a third of a wave of blocks is
-// what is lost. Tokens by fours 66 us, two rows in flight 64, a group's own stretch of heads without block barriers 66, elements side by side
-// with the pairs' other sides by shuffles 82. Gradients: 103 us (0.72), 158 in fp32 (0.94); 8192 tokens of 18 heads 34.
+// what is lost. Two rows in flight 64 us, a group's own stretch of heads without block barriers 66, tokens by fours 66 and by sixteens 61, elements
+// side by side with the pairs' other sides by shuffles 82. In fp32 106 us (0.93). Gradients: 98 us (0.76), 155 in fp32 (0.96).
 #include "attn_common.cuh"
 
 namespace gdn2 {
@@ -242,10 +242,11 @@ __global__ void __launch_bounds__(kThreads, Raw8<T>::kBlocks) prologue_kernel(co
     const long long r = row0 + token, r_in = r < rows ? r : rows - 1;
     const int d = a.d;
     constexpr int kFlight = Raw8<T>::kFlight;
-    // Heads part, part + step, .. of one side; those past the last one are read as the last one, and rows of no sequence as they are,
-    // so that every load is made, and dropped.
+    // Heads part, part + step, .. of one side. Rows of no sequence are read and dropped.
     const T *qs = static_cast<const T*>(a.q) + r_in * a.ld_q, *ks = static_cast<const T*>(a.k) + r_in * a.ld_k;
-    auto fetch = [&](Raw8<T>& to, const T* src, int h, int H) { to.load(src + min(h, H - 1) * d, at); };
+    auto fetch = [&](Raw8<T>& to, const T* src, int h, int H) {
+        if (h < H) to.load(src + h * d, at);
+    };
     Raw8<T> raw[kFlight];
 #pragma unroll
     for (int u = 0; u < kFlight; ++u) fetch(raw[u], qs, part + u * step, a.Hq);  // on their way while the tile's positions and angles are formed
@@ -332,15 +333,19 @@ __global__ void __launch_bounds__(kThreads, kGradBlocks) prologue_grad_kernel(co
     for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
         const long long row0 = static_cast<long long>(tile) * a.tokens;
         const long long r = row0 + token, r_in = r < rows ? r : rows - 1;
-        // as in the forward, every load is made
-        auto fetch = [&](int u, int h, bool side) {
-            const int o = min(h, (side ? a.Hkv : a.Hq) - 1) * a.d;
-            rg[u].load((side ? static_cast<const T*>(a.gk) + r_in * a.ld_gk : static_cast<const T*>(a.gq) + r_in * a.ld_gq) + o, at);
-            if (side ? a.k_weight : a.q_weight)
-                rx[u].load((side ? static_cast<const T*>(a.k) + r_in * a.ld_k : static_cast<const T*>(a.q) + r_in * a.ld_q) + o, at);
+        const T *gs = static_cast<const T*>(a.gq) + r_in * a.ld_gq + part * a.d, *xs = static_cast<const T*>(a.q) + r_in * a.ld_q + part * a.d;
+        int next = part;
+        auto fetch = [&](int u, int H, bool normed) {
+            if (next < H) {
+                rg[u].load(gs, at);
+                if (normed) rx[u].load(xs, at);
+            }
+            next += step;
+            gs += step * a.d;
+            xs += step * a.d;
         };
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u) fetch(u, part + u * step, false);
+        for (int u = 0; u < kFlight; ++u) fetch(u, a.Hq, a.q_weight);
         __syncthreads();
         enter_tile(a, sh, row0, rows);
         const bool live = sh.live[token] && at.mine;
@@ -350,12 +355,15 @@ __global__ void __launch_bounds__(kThreads, kGradBlocks) prologue_grad_kernel(co
         for (int side = 0; side < 2; ++side) {
             const int H = side ? a.Hkv : a.Hq;
             const float* weight = side ? a.k_weight : a.q_weight;
-            T* out = static_cast<T*>(side ? a.k_out : a.q_out) + r * (side ? a.ld_dk : a.ld_dq);
+            T* out = static_cast<T*>(side ? a.k_out : a.q_out) + r * (side ? a.ld_dk : a.ld_dq) + part * a.d;
             uint64_t wv[4];
             weights_of(weight, at, wv);
             if (side) {
+                gs = static_cast<const T*>(a.gk) + r_in * a.ld_gk + part * a.d;
+                xs = static_cast<const T*>(a.k) + r_in * a.ld_k + part * a.d;
+                next = part;
 #pragma unroll
-                for (int u = 0; u < kFlight; ++u) fetch(u, part + u * step, true);
+                for (int u = 0; u < kFlight; ++u) fetch(u, H, weight);
             }
             const int rounds = (H + step - 1) / step;
             int h = part;
@@ -369,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, kGradBlocks) prologue_grad_kernel(co
                     uint64_t g[4], x[4];
                     rg[u].get(g);
                     if (weight) rx[u].get(x);
-                    fetch(u, h + kFlight * step, side);
+                    fetch(u, H, weight);
                     turn.template apply<true>(g, at.turned);
                     const bool here = live && h < H;
                     if (weight) {
@@ -382,16 +390,17 @@ __global__ void __launch_bounds__(kThreads, kGradBlocks) prologue_grad_kernel(co
                         const uint64_t inv2 = f32x2(inv, inv), m2 = f32x2(m, m);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const uint64_t next = fma_f32x2(g[e], mul_f32x2(x[e], inv2), sum[e]);
-                            sum[e] = here ? next : sum[e];  // what is read along may not be finite
+                            const uint64_t more = fma_f32x2(g[e], mul_f32x2(x[e], inv2), sum[e]);
+                            sum[e] = here ? more : sum[e];  // what is not a head of a token may be anything
                             g[e] = mul_f32x2(inv2, fma_f32x2(x[e], m2, gw[e]));
                         }
                     }
                     if (here) {
                         Raw8<T> y;
                         y.set(g);
-                        y.store(out + h * a.d, at);
+                        y.store(out, at);
                     }
+                    out += step * a.d;
                     h += step;
                 }
             }
