@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(32 * W) decode_kernel(const __grid_constant__ 
         }
         acc.begin(a, at.span, unit_row);
         const int first = unit_row / a.G, last = (unit_row + valid - 1) / a.G;  // its tokens
-        const int all_low = limits_of(a, at.span, last * a.G).low, all_limit = limits_of(a, at.span, first * a.G).limit;
+        const Limits newest = limits_of(a, at.span, last * a.G), oldest = limits_of(a, at.span, first * a.G);
         __syncthreads();
         acc.queries(smem_u32(qs));
         for (int i = 0; i < n_steps; ++i) {
@@ -754,10 +754,10 @@ __global__ void __launch_bounds__(32 * W) decode_kernel(const __grid_constant__ 
             copy(stage == 0 ? S - 1 : stage - 1);
             const int base = at.span.base() + (at.step + i) * kStep + warp * kKeys;
             const unsigned there = seen[warp][stage];
-            if (there) {
+            if (there && base <= newest.limit && base + kKeys > oldest.low) {  // a key that some row sees
                 const unsigned char* k = stages + stage * Lay::kStage;
                 // one token a row sees whatever was copied
-                const bool all = a.N == 1 || (base >= all_low && base + kKeys - 1 <= all_limit);
+                const bool all = a.N == 1 || (base >= newest.low && base + kKeys - 1 <= oldest.limit);
                 acc.step(a, qs, k, k + Lay::kHalf, base, there, all, unit_row, first, last, at.span, prob);
             }
             stage = stage == S - 1 ? 0 : stage + 1;
@@ -884,8 +884,16 @@ template <typename T, int D, int W, int S, int M, bool kPaged>
 cudaError_t launch(DecodeArgs& a, int blocks, cudaStream_t s) {
     using Lay = Layout<T, D, W, S, M>;
     static_assert(Lay::kSmem + 6144 <= 232448, "shared memory of a block");
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, D, W, S, M, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmem);
-    if (e != cudaSuccess) return e;
+    // the kernel's shared memory, asked for once per device
+    static std::atomic<unsigned long long> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const unsigned long long bit = e == cudaSuccess && dev >= 0 && dev < 64 ? 1ULL << dev : 0;
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(decode_kernel<T, D, W, S, M, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
     const int units = a.B * a.Hkv * a.tiles;  // of all rows
     decode_kernel<T, D, W, S, M, kPaged><<<a.whole ? units : blocks, Lay::kThreads, Lay::kSmem, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess || a.whole || blocks < 2) return e;

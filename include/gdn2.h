@@ -486,7 +486,7 @@ gdn2_status gdn2_block_norm_backward(const void* x, const void* z, const float* 
  *     by custom) is no page. lengths int32 [n_slots] counts a row's tokens, those of the present call among them: with N tokens in the
  *     call, the first is number lengths - N. refs int32 [n_pages] counts the table entries that name a page; a page with none is free.
  *     slots int32 [B] maps the call's rows to rows of the table, as it maps them to rows of the mixers' state pools (NULL: row b is row
- *     b); a slot outside [0, n_slots) marks the row inactive: nothing of it is read or written. All of this is read on the device;
+ *     b); a slot outside [0, n_slots) marks the row inactive: nothing of it is read or written. Rows that a call writes to name distinct slots. All of this is read on the device;
  *     lengths are clamped to [0, max_pages * page], so that wrong values give wrong results, but no access outside the tensors.
  *   - A workspace serves one call at a time: calls, and graphs, whose kernels may overlap have one each.
  *   - Sizes: d a multiple of 16 up to 256, page any size up to 65536, max_pages * page below 2^30.
@@ -543,7 +543,7 @@ gdn2_status gdn2_attn_prologue_backward(const void* q, long long ld_q, const voi
  *     o = softmax(scale q K^T) V  over the keys that a token sees: token n those up to number lengths - N + n, with window > 0 the last
  *     `window` of them (itself the last), and of these the ones that have a page. A token that sees none gets zeros.
  *   q [B, N, H_q, d] dt (ld_q between tokens), o [B, N, H_q, d] dt; query head h reads key head h / (H_q / H_kv)
- * Keys and values that a token does not see do not reach it, whatever they hold. Scores, sums and outputs are fp32; B up to 65535.
+ * Keys and values that a token does not see do not reach it, whatever they hold; ones that it sees and that are not finite make it not finite. Scores, sums and outputs are fp32; B up to 65535.
  * workspace: gdn2_attn_decode_workspace_size(...) bytes, 16-byte aligned; may be NULL when that is 0.
  */
 size_t gdn2_attn_decode_workspace_size(int B, int N, int Hq, int Hkv, int d, int max_pages, int page, gdn2_dtype dt);
@@ -563,7 +563,7 @@ gdn2_status gdn2_attn_decode(const void* q, long long ld_q, const void* k_pages,
  *
  * gdn2_pages_fork -- row dst[i] (distinct) becomes one like row src[i]: dst rows are emptied first, full pages are shared, a last page that
  * is not full gets a free page of its own. copy_from[i], copy_to[i] (int32 [n]) say what to copy in every layer's pools
- * (gdn2_pages_copy), -1 for nothing. ok[i] is 1, or 0 with dst[i] left empty: an inactive slot, or no free page. A source that is among
+ * (gdn2_pages_copy, before anything is written to or given back by these rows), -1 for nothing. ok[i] is 1, or 0 with dst[i] left empty: an inactive slot, or no free page. A source that is among
  * the dst rows counts as empty.
  *
  * gdn2_pages_release -- empties rows slots[i]: their pages are given back, entries become -1, lengths 0. Slots out of range are skipped.

@@ -61,6 +61,8 @@ CASES = [  # lens, N, Hq, Hkv, d, page, window
     ([700, 10, 1], 3, 12, 2, 64, 24, 5),
     ([400, 90], 2, 32, 2, 256, 128, 100),
     ([64, 65], 2, 2, 2, 128, 1, 1),
+    ([100, 30, 500], 40, 4, 2, 64, 16, 0),   # more tokens than a few: some see little or nothing of what the last one sees
+    ([100, 300], 33, 6, 2, 128, 24, 20),
 ]
 
 

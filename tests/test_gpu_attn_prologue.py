@@ -304,6 +304,18 @@ def test_prologue_gradients(g2, shape, pairs, dtype):
         assert (np.abs(_np(got[2 + side]) - dw) <= ((64 + items / 16) * 2.0 ** -24 + 2.0 ** -19) * terms).all()
 
 
+def test_gradients_at_given_positions(g2):
+    """The opposite rotation of the same positions: gradients of a rotation without norm, turned forward again, are what came in."""
+    pos = np.arange(50) * 40009 - 1000000
+    c = Call([20, 30], 2, 2, 64, 64, "f32", packed=True, norm=(False, False), positions=pos, base=1e6)
+    dq, dk, _, _ = g2.attn_prologue_backward(c.q, c.k, *c.grads, None, None, c.freq, c.positions, c.offsets)
+    q, k = g2.attn_prologue(dq, dk, None, None, c.freq, c.positions, c.offsets)
+    for got, want in zip((q, k), c.grads):  # two rotations, each within 2^-20 of the pair
+        assert (got - want).abs().max().item() <= 2.0 ** -18 * want.abs().max().item()
+    dx, _ = attn.prologue_grad(c.flat(c.q), None, _np(c.freq), pos, c.flat(c.grads[0]))
+    assert np.abs(c.flat(dq) - dx).max() <= 2.0 ** -18 * np.abs(dx).max()
+
+
 @pytest.mark.parametrize("norm", [(True, False), (False, True), (False, False)])
 def test_gradients_without_weights(g2, norm):
     c = Call([33], 4, 2, 64, 32, "f32", norm=norm)
