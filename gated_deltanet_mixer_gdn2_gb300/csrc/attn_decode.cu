@@ -132,32 +132,42 @@ __device__ __forceinline__ long long cost_of(int steps, int units) { return step
 // All rows' costs in a row, dealt out in stretches: a thread has a run of rows, `mine` their cost, `behind` the cost up to and with them.
 template <int kThreads, int kStep>
 struct Dealing {
-    int first, last;
+    int run, first, last;
     long long mine, behind, total;
     template <typename Rows>
     __device__ __forceinline__ void count(const DecodeArgs& a, const Rows& rows, int units, long long* red) {
-        const int run = (a.B + kThreads - 1) / kThreads;
+        run = (a.B + kThreads - 1) / kThreads;
         first = min(static_cast<int>(threadIdx.x) * run, a.B);
         last = min(first + run, a.B);
         mine = 0;
-#pragma unroll 4
+#pragma unroll 8
         for (int b = first; b < last; ++b) mine += cost_of(steps_of<kStep>(rows(b)), units);
         behind = block_scan<kThreads>(mine, red, total);
     }
-    // The thread that has place v among all costs (v < total) leaves there the row that holds it and the cost before that row.
+    // Leaves the row that holds place v among all costs, and the cost before that row; with a barrier behind it. The whole block takes part; a run
+    // of several rows is looked at once more, a thread per row.
     template <typename Rows>
-    __device__ __forceinline__ void find(const DecodeArgs& a, const Rows& rows, int units, long long v, int* row, long long* before) const {
-        long long at = behind - mine;
-        if (v < at || v >= behind) return;
-        for (int b = first; b < last; ++b) {
-            const long long n = cost_of(steps_of<kStep>(rows(b)), units);
-            if (v < at + n) {
-                *row = b;
-                *before = at;
-                return;
-            }
-            at += n;
+    __device__ __forceinline__ void find(const DecodeArgs& a, const Rows& rows, int units, long long v, long long* red, int* row, long long* before) const {
+        if (v >= behind - mine && v < behind) {
+            *row = first;
+            *before = behind - mine;
         }
+        __syncthreads();
+        if (run == 1 || *row < 0) return;
+        const int from = *row;
+        long long at = *before;
+        for (int i = 0; i < run; i += kThreads) {
+            const int b = from + i + threadIdx.x;
+            const long long n = i + static_cast<int>(threadIdx.x) < run && b < a.B ? cost_of(steps_of<kStep>(rows(b)), units) : 0;
+            long long sum;
+            const long long upto = at + block_scan<kThreads>(n, red, sum);  // its barriers lie behind everyone's look at row and before
+            if (v >= upto - n && v < upto) {
+                *row = b;
+                *before = upto - n;
+            }
+            at += sum;
+        }
+        __syncthreads();
     }
 };
 
@@ -645,8 +655,7 @@ __global__ void __launch_bounds__(32 * W) decode_kernel(const __grid_constant__ 
         const long long per = steps_per_block(all.total, gridDim.x);
         const long long begin = blockIdx.x * per, end = begin + per < all.total ? begin + per : all.total;
         if (begin >= end) return;
-        all.find(a, row_span, units, begin, &shared_row, &shared_first);
-        __syncthreads();
+        all.find(a, row_span, units, begin, red, &shared_row, &shared_first);
         if (shared_row < 0) return;  // not with lengths that stay as they are
         at.b = shared_row;
         at.left = end - begin;
@@ -823,8 +832,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
     Dealing<128, kStep> all;
     all.count(a, row_span, units, red);
     const long long per = steps_per_block(all.total, blocks), v = (blockIdx.x + 1) * per;
-    if (v < all.total) all.find(a, row_span, units, v, &shared_row, &before);
-    __syncthreads();
+    all.find(a, row_span, units, v, red, &shared_row, &before);
     int b = -1, ht = 0, c0 = 0, c1 = 0;
     if (shared_row >= 0) {
         b = shared_row;
