@@ -1024,11 +1024,12 @@ def pages_copy(pools, copy_from, copy_to, *, stream=None):
     if not pools:
         return
     dev, rows, n = _device(pools[0]), pools[0].shape[0], copy_from.shape[0]
-    ptrs, sizes = (ctypes.c_void_p * len(pools))(), (ctypes.c_longlong * len(pools))()
-    for i, t in enumerate(pools):
-        if t.shape[0] != rows:
+    ptrs, sizes, count = [], [], len(pools)
+    for t in pools:
+        shape = t.shape
+        if shape[0] != rows:
             raise ValueError("pools have equally many rows")
-        ptrs[i] = _dense(t, t.dtype, t.shape, "pools", dev)
-        sizes[i] = t.numel() // rows * t.element_size() if rows else 0
-    _check(lib.gdn2_pages_copy(ptrs, sizes, len(pools), _indices(copy_from, "copy_from", dev), _indices(copy_to, "copy_to", dev, n), n, rows,
-                               _raw_stream(stream, dev)), "gdn2_pages_copy")
+        ptrs.append(_dense(t, t.dtype, shape, "pools", dev))
+        sizes.append(t.nbytes // rows if rows else 0)
+    _check(lib.gdn2_pages_copy((ctypes.c_void_p * count)(*ptrs), (ctypes.c_longlong * count)(*sizes), count, _indices(copy_from, "copy_from", dev),
+                               _indices(copy_to, "copy_to", dev, n), n, rows, _raw_stream(stream, dev)), "gdn2_pages_copy")

@@ -525,13 +525,18 @@ struct WarpF32 {
 #pragma unroll 4
             for (int j = 0; j < kKeys; ++j) {
                 float x[kCols];
+                alignas(16) float p[R];
                 value(j, x);
+                if constexpr (R == 2) {
+                    *reinterpret_cast<float2*>(p) = *reinterpret_cast<const float2*>(prob + j * kRows);
+                } else {
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const float p = prob[j * kRows + r];
-#pragma unroll
-                    for (int c = 0; c < kCols; ++c) o[r][c] = fmaf(p, x[c], o[r][c]);
+                    for (int r = 0; r < R; r += 4) *reinterpret_cast<float4*>(p + r) = *reinterpret_cast<const float4*>(prob + j * kRows + r);
                 }
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c) o[r][c] = fmaf(p[r], x[c], o[r][c]);
             }
         } else {  // a value that is not finite is kept out of the rows that do not see its key
             for (int j = 0; j < kKeys; ++j) {
