@@ -185,8 +185,9 @@ gdn2_status gdn2_last_device_status(void* stream) {
     const int d = backward_tc_read_clear_status(s);
     const int e = step_read_clear_status(s);
     const int f = ssm_tc_read_clear_status(s), h = ssm_tc_walk_read_clear_status(s), i = ssm_tc_grad_read_clear_status(s);
-    if (a < 0 || b < 0 || c < 0 || d < 0 || e < 0 || f < 0 || h < 0 || i < 0) return GDN2_ERR_CUDA;
-    return (a | b | c | d | e | f | h | i) ? GDN2_ERR_TIMEOUT : GDN2_OK;
+    const int j = attn_decode_read_clear_status(s);
+    if (a < 0 || b < 0 || c < 0 || d < 0 || e < 0 || f < 0 || h < 0 || i < 0 || j < 0) return GDN2_ERR_CUDA;
+    return (a | b | c | d | e | f | h | i | j) ? GDN2_ERR_TIMEOUT : GDN2_OK;
 }
 
 void gdn2_set_wait_limit(long long ns) { g_wait_ns.store(ns < 0 ? kDefaultWaitNs : ns, std::memory_order_relaxed); }

@@ -12,8 +12,9 @@
 // 131072 tokens of 8 key heads of 128 in bf16: 88 us, 6.1 TB/s (0.90 of the copy rate); 64 rows of 0 to 16384 tokens, 2 heads of 256: 162 us
 // (0.93). Of the time, some 12 us are the way in (lengths, table, first keys) and out (parts), whatever the length. The products have 16
 // rows where a tensor-memory product has 128, so they run on warp-wide matrix instructions: their pipe is a quarter busy at the copy rate.
-// With two tiles (drafted tokens) it is the latency of a step's chain that bounds it: 16 rows of 8192 tokens, 4 tokens of 32 heads each, 69 us
-// for 38 of copies. A warp per tile that shares copies with its neighbour was slower (89), two tiles as two units read everything twice (84).
+// More than 16 query rows (drafted tokens) are another matter: with two tiles a warp the latency of a step's chain bounds it, so heads wider
+// than 64 take attn_decode_tc.cuh (16 rows of 8192 tokens, 4 tokens of 32/4 heads of 128: 63 us, with two tiles here 72; heads of 256, 8 rows: 60 and,
+// each tile reading everything, 99).
 #include "attn_common.cuh"
 
 namespace gdn2 {
@@ -34,6 +35,7 @@ struct DecodeArgs {
     bool whole;                              // a block per unit
     unsigned page_inverse;                   // 2^32 / page, rounded up (page 1: 2^32 - 1)
     float scale;  // times log2 e
+    long long wait_ns;
 };
 
 // What a row asks for: the keys [lo, hi) that its earliest and latest tokens see between them. Its steps start at a multiple of a warp's keys,
@@ -212,6 +214,29 @@ struct Cursor {
         return true;
     }
 };
+
+// Sets a block's walk to the start of its stretch of all steps and tolls; false: the block has nothing to do. The whole block takes part.
+template <int kThreads, int kStep, typename Rows>
+__device__ __forceinline__ bool begin_stretch(const DecodeArgs& a, const Rows& rows, int units, long long* red, int* row, long long* first, Cursor<kStep>& at) {
+    Dealing<kThreads, kStep> all;
+    all.count(a, rows, units, red);
+    const long long per = steps_per_block(all.total, gridDim.x);
+    const long long begin = blockIdx.x * per, end = begin + per < all.total ? begin + per : all.total;
+    if (begin >= end) return false;
+    all.find(a, rows, units, begin, red, row, first);
+    if (*row < 0) return false;  // not with lengths that stay as they are
+    at.b = *row;
+    at.left = end - begin;
+    at.settle(a, rows);
+    if (at.left <= 0) return false;
+    // a unit's toll lies in front of its steps
+    const long long in = begin - *first;
+    at.ht = static_cast<int>(in / (at.steps + kToll));
+    const int place = static_cast<int>(in - static_cast<long long>(at.ht) * (at.steps + kToll));
+    at.step = max(place - kToll, 0);
+    at.left -= max(kToll - place, 0);
+    return at.left > 0;
+}
 
 // The part of a query row of the unit: which of the row's tokens it is, and the keys it sees, [low, limit].
 struct Limits {
@@ -655,24 +680,7 @@ __global__ void __launch_bounds__(32 * W) decode_kernel(const __grid_constant__ 
             const Span s = row_span(b);
             if (s.slot >= 0 && steps_of<kStep>(s) == 0) clear_row(b);
         }
-        Dealing<kThreads, kStep> all;
-        all.count(a, row_span, units, red);
-        const long long per = steps_per_block(all.total, gridDim.x);
-        const long long begin = blockIdx.x * per, end = begin + per < all.total ? begin + per : all.total;
-        if (begin >= end) return;
-        all.find(a, row_span, units, begin, red, &shared_row, &shared_first);
-        if (shared_row < 0) return;  // not with lengths that stay as they are
-        at.b = shared_row;
-        at.left = end - begin;
-        at.settle(a, row_span);
-        if (at.left <= 0) return;
-        // a unit's toll lies in front of its steps
-        const long long in = begin - shared_first;
-        at.ht = static_cast<int>(in / (at.steps + kToll));
-        const int place = static_cast<int>(in - static_cast<long long>(at.ht) * (at.steps + kToll));
-        at.step = max(place - kToll, 0);
-        at.left -= max(kToll - place, 0);
-        if (at.left <= 0) return;
+        if (!begin_stretch<kThreads, kStep>(a, row_span, units, red, &shared_row, &shared_first, at)) return;
     }
     Cursor<kStep> ahead = at;
 
@@ -822,75 +830,146 @@ __global__ void __launch_bounds__(32 * W) decode_kernel(const __grid_constant__ 
     }
 }
 
-// Joins the parts of a unit that several blocks hold: one block per end of a stretch and query row, which acts where that end is the first inside
-// its unit's steps; its warps take a share of the parts each. It comes up while the parts are still being made and finds its place meanwhile.
+}  // namespace
+}  // namespace gdn2
+
+#include "attn_decode_tc.cuh"
+
+namespace gdn2 {
+namespace {
+
+// Joins the parts of a unit that several blocks hold: one block per end of a stretch and four query rows, which acts where that end is the first
+// inside its unit's steps. It comes up while the parts are still being made, where there is room, and finds its place meanwhile; then it is
+// the latency of reading what other SMs wrote that counts, so its warps ask for several parts each at once, and for all statistics behind
+// them. Small blocks, since all of them should fit beside each other: with a block per row and the statistics asked for along with each part,
+// 16 drafts took 73 us (63), 512 tokens of 2 key heads 11.7 (8.9), rows of 20000, 3000 and 7 tokens of 2 key heads 22.2 (19.9); with blocks of 8
+// warps 68, 10.4 and 21.3.
+constexpr int kJoinRows = 4, kJoinWarps = 4, kMaxBlocks = 512;
+
 template <typename T, int D, int W, int M>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ DecodeArgs a, int blocks) {
-    constexpr int kStep = kKeys * W, kRows = kTile * M, kCols = D / 32;
-    __shared__ long long red[4], before;
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ DecodeArgs a, int blocks) {
+    constexpr int kStep = kKeys * W, kRows = kTile * M, kThreads = 32 * kJoinWarps, kVecs = D <= 128 ? 1 : D / 128, kAtOnce = (M == 2 ? 2 : 4) / kVecs;
+    __shared__ long long red[kJoinWarps], before;
     __shared__ int shared_row;
-    __shared__ float tops[4], sums[4];
-    __shared__ __align__(16) float outs[4][D];  // written two columns at a time
-    const int units = a.Hkv * a.tiles, warp = threadIdx.x / 32, lane = threadIdx.x & 31, r = blockIdx.y;
+    __shared__ float4 factors[kMaxBlocks], sums[kMaxBlocks];  // of a part's four rows
+    __shared__ float inverse[kJoinRows];
+    __shared__ float4 outs[kJoinWarps][kJoinRows][D / 4];
+    const int units = a.Hkv * a.tiles, tid = threadIdx.x, warp = tid / 32, lane = tid & 31, r0 = blockIdx.y * kJoinRows;
     auto row_span = [&](int b) { return span_of(a, b); };
-    if (threadIdx.x == 0) shared_row = -1;
-    Dealing<128, kStep> all;
+    if (tid == 0) shared_row = -1;
+    Dealing<kThreads, kStep> all;
     all.count(a, row_span, units, red);
     const long long per = steps_per_block(all.total, blocks), v = (blockIdx.x + 1) * per;
     all.find(a, row_span, units, v, red, &shared_row, &before);
-    int b = -1, ht = 0, c0 = 0, c1 = 0;
+    int b = -1, ht = 0, c0 = 0, n = 0;
     if (shared_row >= 0) {
         b = shared_row;
         const int steps = steps_of<kStep>(row_span(b));
         ht = static_cast<int>((v - before) / (steps + kToll));
         const long long start = before + static_cast<long long>(ht) * (steps + kToll) + kToll;
         c0 = static_cast<int>(start / per);
-        c1 = static_cast<int>((start + steps - 1) / per);
-        if (c0 != static_cast<int>(blockIdx.x) || c1 == c0) b = -1;
+        n = static_cast<int>((start + steps - 1) / per) - c0 + 1;
+        if (c0 != static_cast<int>(blockIdx.x) || n == 1) b = -1;
     }
-    const int tile = ht % a.tiles, head = ht / a.tiles, row = tile * kRows + r;
+    const int tile = ht % a.tiles, head = ht / a.tiles, row0 = tile * kRows + r0, valid = min(kJoinRows, a.N * a.G - row0);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (b < 0 || row >= a.N * a.G) return;
-    auto part = [&](int c) { return part_of(a, c, c == c0 ? 1 : 0, D, kRows); };
-    float m = kNone;
-    for (int c = c0 + static_cast<int>(threadIdx.x); c <= c1; c += 128) m = fmaxf(m, part(c)[kRows * D + r]);
+    if (b < 0 || valid <= 0) return;
+    auto part = [&](int i) { return part_of(a, c0 + i, i == 0 ? 1 : 0, D, kRows); };
+    const bool lead = D >= 128 || lane < D / 4;
+    float4 x[kAtOnce][kJoinRows][kVecs], o[kJoinRows][kVecs] = {};
+    auto ask = [&](int first) {
 #pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (lane == 0) tops[warp] = m;
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int i = first + k * kJoinWarps;
+#pragma unroll
+            for (int r = 0; r < kJoinRows; ++r)
+#pragma unroll
+                for (int g = 0; g < kVecs; ++g)
+                    if (i < n && r < valid && lead) x[k][r][g] = *reinterpret_cast<const float4*>(part(i) + (r0 + r) * D + 128 * g + 4 * lane);
+        }
+    };
+    ask(warp);
+    for (int i = tid; i < n; i += kThreads) {
+        const float* p = part(i) + kRows * D + r0;
+        factors[i] = *reinterpret_cast<const float4*>(p);
+        sums[i] = *reinterpret_cast<const float4*>(p + kRows);
+    }
     __syncthreads();
-    m = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-    const float ref = m == kNone ? 0.f : m;
-    float l = 0.f, x[kCols] = {};
-#pragma unroll 8
-    for (int c = c0 + warp; c <= c1; c += 4) {
-        const float* p = part(c);
-        const float f = exp2f(p[kRows * D + r] - ref);
-        l = fmaf(f, p[kRows * D + kRows + r], l);
+    if (warp < kJoinRows) {  // a row each: maxima to factors, sums to their sum
+        float *f = reinterpret_cast<float*>(factors) + warp, *s = reinterpret_cast<float*>(sums) + warp;
+        float m = kNone, l = 0.f;
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, f[kJoinRows * i]);
 #pragma unroll
-        for (int i = 0; i < kCols; i += 2) {
-            const float2 v = *reinterpret_cast<const float2*>(p + r * D + 32 * i + 2 * lane);
-            x[i] = fmaf(f, v.x, x[i]);
-            x[i + 1] = fmaf(f, v.y, x[i + 1]);
+        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float ref = m == kNone ? 0.f : m;
+        for (int i = lane; i < n; i += 32) {
+            const float e = exp2f(f[kJoinRows * i] - ref);
+            f[kJoinRows * i] = e;
+            l = fmaf(e, s[kJoinRows * i], l);
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        if (lane == 0) inverse[warp] = l == 0.f ? 0.f : 1.f / l;
+    }
+    __syncthreads();
+    for (int first = warp; first < n; first += kAtOnce * kJoinWarps) {
+        if (first != warp) ask(first);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int i = first + k * kJoinWarps;
+            if (i >= n) break;
+            const float4 f4 = factors[i];
+            const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+            for (int r = 0; r < kJoinRows; ++r)
+#pragma unroll
+                for (int g = 0; g < kVecs; ++g) {
+                    o[r][g].x = fmaf(f[r], x[k][r][g].x, o[r][g].x);
+                    o[r][g].y = fmaf(f[r], x[k][r][g].y, o[r][g].y);
+                    o[r][g].z = fmaf(f[r], x[k][r][g].z, o[r][g].z);
+                    o[r][g].w = fmaf(f[r], x[k][r][g].w, o[r][g].w);
+                }
         }
     }
-    if (lane == 0) sums[warp] = l;
 #pragma unroll
-    for (int i = 0; i < kCols; i += 2) *reinterpret_cast<float2*>(&outs[warp][32 * i + 2 * lane]) = make_float2(x[i], x[i + 1]);
+    for (int r = 0; r < kJoinRows; ++r)
+#pragma unroll
+        for (int g = 0; g < kVecs; ++g)
+            if (lead) outs[warp][r][32 * g + lane] = o[r][g];
     __syncthreads();
-    l = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int n = row / a.G;
-    T* o = static_cast<T*>(a.o) + ((static_cast<long long>(b) * a.N + n) * a.Hq + head * a.G + row - n * a.G) * a.d;
-    for (int c = threadIdx.x; c < a.d; c += 128) o[c] = from_f32<T>(((outs[0][c] + outs[1][c]) + (outs[2][c] + outs[3][c])) * inv);
+    for (int i = tid; i < valid * a.d; i += kThreads) {
+        const int r = i / a.d, c = i - r * a.d, t = (row0 + r) / a.G;
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) sum += reinterpret_cast<const float*>(outs[w][r])[c];
+        static_cast<T*>(a.o)[((static_cast<long long>(b) * a.N + t) * a.Hq + head * a.G + row0 + r - t * a.G) * a.d + c] = from_f32<T>(sum * inverse[r]);
+    }
 }
 
 // Widths that a kernel is built for, and blocks per SM: some 128 KB of copies in flight on an SM, which its share of the copy rate takes.
 int width_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
-// Two tiles of query rows share the copies of K and V where there are two and their sums fit the registers.
-int tiles_of(int rows, int d, gdn2_dtype dt) { return dt == GDN2_BF16 && rows > kTile && width_of(d) <= 128 ? 2 : 1; }
+// Query rows of a unit, in tiles: over bf16 caches two share the copies of K and V where there are two.
+int tiles_of(int rows, int d, gdn2_dtype dt) { return dt == GDN2_BF16 && rows > kTile ? 2 : 1; }
 int blocks_of(int d, int tiles, gdn2_dtype dt) {
     const int D = width_of(d);
-    return sm_count() * (dt == GDN2_BF16 ? (D == 64 ? (tiles == 2 ? 2 : 3) : D == 128 && tiles == 1 ? 2 : 1) : D == 64 ? 2 : 1);
+    const int blocks = sm_count() * (dt == GDN2_BF16 ? (D == 64 ? (tiles == 2 ? 2 : 3) : D == 128 && tiles == 1 ? 2 : 1) : D == 64 ? 2 : 1);
+    return blocks < kMaxBlocks ? blocks : kMaxBlocks;
+}
+
+template <typename T, int D, int W, int M>
+cudaError_t launch_join(const DecodeArgs& a, int blocks, cudaStream_t s) {
+    if (a.whole || blocks < 2) return cudaSuccess;
+    cudaLaunchConfig_t cfg{};
+    const int rows = a.N * a.G < kTile * M ? a.N * a.G : kTile * M;
+    cfg.gridDim = dim3(blocks - 1, (rows + kJoinRows - 1) / kJoinRows);
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<T, D, W, M>, a, blocks);
 }
 
 template <typename T, int D, int W, int S, int M, bool kPaged>
@@ -909,17 +988,32 @@ cudaError_t launch(DecodeArgs& a, int blocks, cudaStream_t s) {
     }
     const int units = a.B * a.Hkv * a.tiles;  // of all rows
     decode_kernel<T, D, W, S, M, kPaged><<<a.whole ? units : blocks, Lay::kThreads, Lay::kSmem, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess || a.whole || blocks < 2) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(blocks - 1, a.N * a.G < Lay::kRows ? a.N * a.G : Lay::kRows);
-    cfg.blockDim = dim3(128);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<T, D, W, M>, static_cast<const DecodeArgs&>(a), blocks);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_join<T, D, W, M>(a, blocks, s);
+}
+
+bool pool_map(CUtensorMap* m, const void* p, int d, int page, long long planes) {
+    const uint64_t dims[3] = {(uint64_t)d, (uint64_t)page, (uint64_t)planes};
+    const uint64_t st[2] = {(uint64_t)d * 2, (uint64_t)page * d * 2};
+    const uint32_t box[3] = {64, kKeys, 1};
+    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int D>
+cudaError_t launch_tc(DecodeArgs& a, int blocks, cudaStream_t s) {
+    static_assert(TcLayout<D>::kSmall + sizeof(TcSmall<D>) + 1024 <= 232448, "shared memory of a block");
+    const cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    if (e != cudaSuccess) return e;
+    g_launched.store(true, std::memory_order_relaxed);
+    a.wait_ns = wait_limit_ns();
+    CacheMaps maps{};
+    const long long planes = static_cast<long long>(a.cache.n_pages) * a.Hkv;
+    const bool mapped = a.cache.page % kKeys == 0 && planes > 0 && planes < (1LL << 31) && pool_map(&maps.k, a.k, a.d, a.cache.page, planes) &&
+                        pool_map(&maps.v, a.v, a.d, a.cache.page, planes);
+    // the whole shared memory: one block per SM, and no operand descriptor reaches past the block's own
+    decode_tc_kernel<D><<<a.whole ? a.B * a.Hkv * a.tiles : blocks, kTcThreads, 232448, s>>>(a, maps, mapped);
+    const cudaError_t l = cudaGetLastError();
+    return l != cudaSuccess ? l : launch_join<__nv_bfloat16, D, kTcKeys / kKeys, kTcRows / kTile>(a, blocks, s);
 }
 
 template <typename T, int D, int W, int S, int M>
@@ -945,6 +1039,9 @@ gdn2_status decode_check(int B, int N, int Hq, int Hkv, int d, gdn2_dtype dt) {
 }
 
 }  // namespace
+
+int attn_decode_read_clear_status(cudaStream_t s) { return read_clear_status(s); }
+
 }  // namespace gdn2
 
 using namespace gdn2;
@@ -994,7 +1091,7 @@ gdn2_status gdn2_attn_decode(const void* q, long long ld_q, const void* k_pages,
     if (dt == GDN2_F32)
         e = D == 64 ? launch<float, 64, 4, 3, 1>(a, blocks, s) : D == 128 ? launch<float, 128, 4, 3, 1>(a, blocks, s) : launch<float, 256, 2, 2, 1>(a, blocks, s);
     else if (tiles == 2)
-        e = D == 64 ? launch<BF, 64, 4, 5, 2>(a, blocks, s) : launch<BF, 128, 8, 3, 2>(a, blocks, s);
+        e = D == 64 ? launch<BF, 64, 4, 5, 2>(a, blocks, s) : D == 128 ? launch_tc<128>(a, blocks, s) : launch_tc<256>(a, blocks, s);
     else
         e = D == 64 ? launch<BF, 64, 4, 4, 1>(a, blocks, s) : D == 128 ? launch<BF, 128, 4, 3, 1>(a, blocks, s) : launch<BF, 256, 4, 3, 1>(a, blocks, s);
     return e == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA;

@@ -104,6 +104,7 @@ int chunk_tc_read_clear_status(cudaStream_t s);
 int ssm_tc_read_clear_status(cudaStream_t s);
 int ssm_tc_walk_read_clear_status(cudaStream_t s);
 int ssm_tc_grad_read_clear_status(cudaStream_t s);
+int attn_decode_read_clear_status(cudaStream_t s);
 
 long long wait_limit_ns();
 
