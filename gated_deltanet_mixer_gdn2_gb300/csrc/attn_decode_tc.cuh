@@ -55,6 +55,15 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                  : "r"(taddr)
                  : "memory");
 }
+// As tma_load_3d, by the lane that has `lead`; the operands are the warp's, so that they lie in uniform registers (with a lane per panel each copy
+// took 170 cycles to issue).
+__device__ __forceinline__ void tma_load_by(uint32_t lead, uint32_t to, const void* map, int c0, int c1, int c2, uint64_t* bar) {
+    asm volatile(
+        "{\n .reg .pred e;\n setp.ne.b32 e, %6, 0;\n"
+        " @e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n}\n" ::"r"(to),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "r"(lead)
+        : "memory");
+}
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
@@ -182,6 +191,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         constexpr int kRowsPer = 32 / kChunks;  // keys that one copy of all lanes spans
         const int lane_row = lane / kChunks, chunk = lane % kChunks;
         Key next0 = look(key0), next1 = look(key1);
+        const uint32_t lead = elect_one();
         int slot = 0;
         unsigned tiles = 0;
         bool ok = true;
@@ -224,16 +234,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 __syncwarp();
                 unsigned char* tile = sm + slot * Lay::kTileBytes;
                 const unsigned char* src = (kv ? vp : kp) + 16 * chunk;
+#pragma unroll
+                for (int g = 0; g < 3; ++g) {
+                    if (!(whole >> g & 1)) continue;
+                    const Key& of = g < 2 ? here0 : here1;
+                    const int in = __shfl_sync(0xffffffffu, of.in, (g & 1) * 16), plane = __shfl_sync(0xffffffffu, of.entry, (g & 1) * 16) * a.Hkv + here_head;
+                    const uint32_t to = smem_u32(tile) + (part + 3 * g) * 2048;
+#pragma unroll
+                    for (int p = 0; p < Lay::kPanels; ++p)
+                        if (p < panels) tma_load_by(lead, to + p * kPanel, kv ? &maps.v : &maps.k, 64 * p, in, plane, bar);
+                }
 #pragma unroll 1
                 for (int g = 0; g < groups; ++g) {
-                    const int from = (g & 1) * 16;
-                    const Key of = g < 2 ? here0 : here1;
-                    const unsigned some = there(g);
-                    if (whole >> g & 1) {
-                        const int entry = __shfl_sync(0xffffffffu, of.entry, from), in = __shfl_sync(0xffffffffu, of.in, from);
-                        if (lane < panels)
-                            tma_load_3d(tile + lane * kPanel + (part + 3 * g) * 2048, kv ? &maps.v : &maps.k, 64 * lane, in, entry * a.Hkv + here_head, bar);
-                    } else {
+                    if (!(whole >> g & 1)) {
+                        const int from = (g & 1) * 16;
+                        const Key of = g < 2 ? here0 : here1;
+                        const unsigned some = there(g);
                         // all addresses first: a copy behind each one's shuffle would wait for it
                         long long row[16 / kRowsPer];
                         const long long mine = is(of) ? ((static_cast<long long>(of.entry) * a.Hkv + here_head) * a.cache.page + of.in) * row_bytes : 0;
@@ -363,13 +379,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int n_steps = static_cast<int>(at.left < at.steps - at.step ? at.left : at.steps - at.step);
             const int valid = min(kTcRows, a.N * a.G - unit_row);
             // the unit's queries, zeros for rows that it does not have; the products of the unit before have ended
-            for (int i = tid; i < kTcRows * kChunks; i += 128) {
-                const int r = i / kChunks, c = i % kChunks, row = unit_row + r, t = row / a.G;
+            uint4 asked[kTcRows * kChunks / 128];
+#pragma unroll
+            for (int i = 0; i < kTcRows * kChunks / 128; ++i) {
+                const int r = (tid + 128 * i) / kChunks, c = tid % kChunks, row = unit_row + r, t = row / a.G;
                 const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<long long>(at.b) * a.N + t) * a.ld_q +
                                            static_cast<long long>(head * a.G + row - t * a.G) * a.d + c * 8;
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (r < valid && c < chunks) u = __ldg(reinterpret_cast<const uint4*>(src));
-                *reinterpret_cast<uint4*>(sm + Lay::kQ + c / 8 * (kTcRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = u;
+                asked[i] = r < valid && c < chunks ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < kTcRows * kChunks / 128; ++i) {
+                const int r = (tid + 128 * i) / kChunks, c = tid % kChunks;
+                *reinterpret_cast<uint4*>(sm + Lay::kQ + c / 8 * (kTcRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = asked[i];
             }
             if (tid < kTcRows) x.lim[tid] = limits_of(a, at.span, unit_row + tid);
             const float zero[8] = {};
