@@ -13,7 +13,7 @@
 // (0.93). Of the time, some 12 us are the way in (lengths, table, first keys) and out (parts), whatever the length. The products have 16
 // rows where a tensor-memory product has 128, so they run on warp-wide matrix instructions: their pipe is a quarter busy at the copy rate.
 // More than 16 query rows (drafted tokens) are another matter: with two tiles a warp the latency of a step's chain bounds it, so heads wider
-// than 64 take attn_decode_tc.cuh (16 rows of 8192 tokens, 4 tokens of 32/4 heads of 128: 63 us, with two tiles here 72; heads of 256, 8 rows: 60 and,
+// than 64 take attn_decode_tc.cuh (16 rows of 8192 tokens, 4 tokens of 32/4 heads of 128: 60 us, with two tiles here 72; heads of 256, 8 rows: 61 and,
 // each tile reading everything, 99).
 #include "attn_common.cuh"
 
@@ -842,7 +842,7 @@ namespace {
 // inside its unit's steps. It comes up while the parts are still being made, where there is room, and finds its place meanwhile; then it is
 // the latency of reading what other SMs wrote that counts, so its warps ask for several parts each at once, and for all statistics behind
 // them. Small blocks, since all of them should fit beside each other: with a block per row and the statistics asked for along with each part,
-// 16 drafts took 73 us (63), 512 tokens of 2 key heads 11.7 (8.9), rows of 20000, 3000 and 7 tokens of 2 key heads 22.2 (19.9); with blocks of 8
+// 16 drafts took 73 us (then 63), 512 tokens of 2 key heads 11.7 (8.9), rows of 20000, 3000 and 7 tokens of 2 key heads 22.2 (19.9); with blocks of 8
 // warps 68, 10.4 and 21.3.
 constexpr int kJoinRows = 4, kJoinWarps = 4, kMaxBlocks = 512;
 

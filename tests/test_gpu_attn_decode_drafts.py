@@ -169,3 +169,21 @@ def test_timeout_then_correct(g2, d, page):  # noqa: F811
         g2.gdn2_set_wait_limit(-1)
     assert g2.gdn2_last_device_status() == g2.GDN2_OK
     c.check(c.run(g2))
+
+
+@pytest.mark.parametrize("page", [32, 24])
+def test_far_pages(g2, page):  # noqa: F811
+    """Pools of more than 2^31 elements: pages behind the 32-bit range are read, by tensor copies and key by key."""
+    import torch
+
+    pages, Hkv, d = 140_000 * 32 // page, 4, 128
+    pools = [torch.empty(pages, Hkv, page, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    at, length = [pages - 1, 3, pages - 2], 3 * page - 5
+    near = [torch.randn(3, Hkv, page, d, device="cuda").bfloat16() for _ in range(2)]
+    for p, n in zip(pools, near):
+        p[at] = n
+    q = torch.randn(1, 5, 32, d, device="cuda").bfloat16()
+    o = g2.attn_decode(q, *pools, _int32([at]), _int32([length]))
+    assert o.equal(g2.attn_decode(q, *near, _int32([[0, 1, 2]]), _int32([length])))
+    want, mag = _dense64(q, *near, np.array([[0, 1, 2]]), np.array([length]), [0], d ** -0.5, 0)
+    _check(_np(o), want, mag, _reach(_np(q), _np(near[0]), d ** -0.5, length, "bf16"), "bf16")
