@@ -375,7 +375,7 @@ struct WarpBf16 {
                 float f[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float now = fmaxf(m[k][h], top[h]);
+                    const float now = top[h] > m[k][h] + 8.f ? top[h] : m[k][h];  // each row by itself: its bits are not another's matter
                     f[h] = now == kNone ? 0.f : ex2_approx(m[k][h] - now);
                     m[k][h] = now;
                     l[k][h] *= f[h];

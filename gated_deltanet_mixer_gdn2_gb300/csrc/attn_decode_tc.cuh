@@ -430,26 +430,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 bool over = failed;
 #pragma unroll
                 for (int r = 0; r < kTcRows; ++r) {
-                    z[r] = fmaf(s[r], a.scale, -ref[r]);  // a row without a reference yet: +inf
+                    z[r] = fmaf(s[r], a.scale, -ref[r]);  // a row without a reference yet: +inf, or NaN
                     if (hidden >> r & 1) z[r] = kNone;
-                    over |= z[r] > 8.f;
+                    over |= !(z[r] <= 8.f);
                 }
                 if (weights_any(over)) {
-                    // some score passes its row's reference by 8: all references to their maxima, sums and output with them
+                    // Some score passes its row's reference by 8: such rows' references to their maxima, sums and output with them. The others
+                    // stay as they are, so that no row's bits depend on another's scores.
                     if ((stop = weights_any(failed))) break;
                     float v[kTcRows];
 #pragma unroll
                     for (int r = 0; r < kTcRows; ++r) v[r] = hidden >> r & 1 ? kNone : s[r] * a.scale;
                     x.over[warp][lane] = across(v, [](float p, float q) { return fmaxf(p, q); });
                     weights_sync();
-                    const float now = fmaxf(fmaxf(fmaxf(x.over[0][lane], x.over[1][lane]), fmaxf(x.over[2][lane], x.over[3][lane])), top);
+                    const float most = fmaxf(fmaxf(x.over[0][lane], x.over[1][lane]), fmaxf(x.over[2][lane], x.over[3][lane]));
+                    const float now = most > top + 8.f ? most : top;
                     const float f = now == kNone ? 0.f : ex2_approx(top - now);
                     top = now;
 #pragma unroll
                     for (int r = 0; r < kTcRows; ++r) {
                         ref[r] = __shfl_sync(0xffffffffu, now, r);
                         l[r] *= __shfl_sync(0xffffffffu, f, r);
-                        z[r] = hidden >> r & 1 ? kNone : fmaf(s[r], a.scale, -ref[r]);
+                        z[r] = hidden >> r & 1 ? kNone : fmaf(s[r], a.scale, ref[r] == kNone ? 0.f : -ref[r]);  // scores of -inf alone: weights of 0
                     }
                     if (i > 0) {
                         failed |= !wait_bar(&x.added, (n - 1) & 1, lim, err);

@@ -187,3 +187,35 @@ def test_far_pages(g2, page):  # noqa: F811
     assert o.equal(g2.attn_decode(q, *near, _int32([[0, 1, 2]]), _int32([length])))
     want, mag = _dense64(q, *near, np.array([[0, 1, 2]]), np.array([length]), [0], d ** -0.5, 0)
     _check(_np(o), want, mag, _reach(_np(q), _np(near[0]), d ** -0.5, length, "bf16"), "bf16")
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("G", [2, 8])
+def test_scores_below_all_numbers(g2, G, d):  # noqa: F811
+    """Scores that overflow to -inf, a whole step of them first: no weight, and the others as ever."""
+    c = Case([700, 300], 4, 2 * G, 2, d, 16, "bf16")
+    k = _np(c.pools[0]).copy()
+    k[..., 0] = 0.0
+    for s in c.slots:
+        for t in range(260):
+            k[c.table[s, t // 16], :, t % 16, 0] = -1e30
+    c.pools[0] = _dev(k, "bf16")
+    c.q[..., 0] = 1e10
+    got = c.run(g2)
+    rest = _np(c.q).copy()  # the reference's magnitudes without the part that overflows, which adds nothing to the other scores
+    rest[..., 0] = 1.0
+    want, mag = attn.attend(_np(c.q), k, _np(c.pools[1]), c.table, c.lengths, c.slots, c.scale)
+    k[..., 0] = 0.0
+    _check(_np(got), want, mag, _reach(rest, k, c.scale, 700, "bf16"), "bf16")
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("G", [2, 8])
+def test_rows_do_not_touch_each_other(g2, G, d):  # noqa: F811
+    """The newest token's key has one infinite component: its scores are infinite, and the other tokens' results keep their bits."""
+    c = Case([700, 300, 131], 4, 2 * G, 2, d, 16, "bf16")
+    want = c.run(g2)
+    for s in c.slots:
+        t = int(c.lengths[s]) - 1
+        c.pools[0][c.table[s, t // 16], :, t % 16, 0] = float("inf")
+    assert c.run(g2)[:, :-1].equal(want[:, :-1])
