@@ -540,7 +540,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 step_slot();
             }
             if (stop) break;
-            // the unit's sums, and its way out
+            // The unit's sums, and its way out. They take the place of the last step's maxima, which a warp may still be reading if that step moved a
+            // reference (a unit of one step always does): the four warps meet first.
+            weights_sync();
             x.over[warp][lane] = across(l, [](float p, float q) { return p + q; });
             failed |= !wait_bar(&x.added, (n - 1) & 1, lim, err);
             tc_fence_after();
