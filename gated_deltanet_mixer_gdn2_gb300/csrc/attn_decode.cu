@@ -52,6 +52,10 @@ __device__ __forceinline__ Span span_of(const DecodeArgs& a, int b) {
     return slot < 0 ? Span{-1, 0, 0} : span_of(a, slot, a.cache.length_of(slot));
 }
 
+// 16-byte vectors of a row's output, which has up to 2^31 elements (and so more bytes than an int counts); d is a multiple of 16.
+__host__ __device__ constexpr int vectors_of(int N, int Hq, int d, int esize) { return N * Hq * d / (16 / esize); }
+static_assert(vectors_of(4096, 512, 256, 4) == 1 << 27 && vectors_of(4096, 4096, 64, 2) == 1 << 27, "counted without overflow");
+
 template <int kStep>
 __device__ __forceinline__ int steps_of(const Span& s) {
     return s.hi > s.lo ? (s.hi - s.base() + kStep - 1) / kStep : 0;
@@ -648,7 +652,7 @@ __global__ void __launch_bounds__(32 * W) decode_kernel(const __grid_constant__ 
 
     // Rows without a visible key: a warp clears one.
     auto clear_row = [&](int b) {
-        const int n = a.N * a.Hq * a.d * (int)sizeof(T) / 16;
+        const int n = vectors_of(a.N, a.Hq, a.d, sizeof(T));
         uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + static_cast<long long>(b) * a.N * a.Hq * a.d);
         for (int i = lane; i < n; i += 32) o[i] = make_uint4(0, 0, 0, 0);
     };

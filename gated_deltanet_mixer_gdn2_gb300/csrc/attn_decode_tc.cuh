@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const long long lim = a.wait_ns;
 
     auto clear_row = [&](int b) {
-        const int n = a.N * a.Hq * a.d / 8;
+        const int n = vectors_of(a.N, a.Hq, a.d, 2);
         uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + static_cast<long long>(b) * a.N * a.Hq * a.d);
         for (int i = lane; i < n; i += 32) o[i] = make_uint4(0, 0, 0, 0);
     };
