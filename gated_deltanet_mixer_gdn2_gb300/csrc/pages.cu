@@ -164,6 +164,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) pag
             a.table[static_cast<long long>(w.row) * a.max_pages + j] = p;
             atomicAdd(a.refs + p, 1);
         }
+        cluster.sync();  // ok holds the numbers up to here: other threads look there for what their entries' requests get
     }
     for (long long i = first; i < a.n; i += step) {
         Want w;
