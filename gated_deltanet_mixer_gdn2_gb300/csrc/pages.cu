@@ -55,7 +55,7 @@ __device__ __forceinline__ bool want_of(const PagesArgs& a, int i, bool fork, Wa
         if (!is_row(a, s)) return false;
         const int len = length_of(a, s);
         w.first = len / a.page;
-        w.pages = len % a.page != 0;
+        w.pages = len % a.page != 0 && is_page(a, a.table[static_cast<long long>(s) * a.max_pages + w.first]);
         return true;
     }
     const long long len = length_of(a, w.row), more = a.tokens ? a.tokens[i] : a.every;

@@ -562,7 +562,7 @@ gdn2_status gdn2_attn_decode(const void* q, long long ld_q, const void* k_pages,
  * whether or not they were met).
  *
  * gdn2_pages_fork -- row dst[i] (distinct) becomes one like row src[i]: dst rows are emptied first, full pages are shared, a last page that
- * is not full gets a free page of its own. copy_from[i], copy_to[i] (int32 [n]) say what to copy in every layer's pools
+ * is not full gets a free page of its own, and an entry that names no page stays one. copy_from[i], copy_to[i] (int32 [n]) say what to copy in every layer's pools
  * (gdn2_pages_copy, before anything is written to or given back by these rows), -1 for nothing. ok[i] is 1, or 0 with dst[i] left empty: an inactive slot, or no free page. A source that is among
  * the dst rows counts as empty.
  *

@@ -133,13 +133,13 @@ class Pages:
         free, asked, copies, ok = self.free(), 0, [], []
         for s, t, n in zip(src, dst, before):
             good, copy = self.is_row(s) and self.is_row(t), (-1, -1)
-            part = n % self.page != 0
+            part = good and n % self.page != 0 and self.is_page(self.table[s][n // self.page])  # a gap stays one
             asked += good and part
             good = good and (not part or asked <= len(free))
             if good and part:
                 fresh, last = free[asked - 1], self.table[s][n // self.page]
                 self.table[t][n // self.page], self.refs[fresh] = fresh, 1
-                copy = (last if self.is_page(last) else -1, fresh)
+                copy = (last, fresh)
             copies.append(copy)
             ok.append(int(good))
         for s, t, n, good in zip(src, dst, before, ok):
