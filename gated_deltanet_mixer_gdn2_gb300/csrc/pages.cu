@@ -7,6 +7,8 @@
 // ordered by cluster barriers. The copies are bound by memory: 32 KB pieces, eight 16-byte loads in flight per thread.
 #include <cooperative_groups.h>
 
+#include <climits>
+
 #include "attn_common.cuh"
 
 namespace gdn2 {
@@ -43,9 +45,9 @@ __device__ __forceinline__ void release_rows(const PagesArgs& a, long long first
     }
 }
 
-// What request i asks for: pages, and where they go in its row. False: the request cannot be met at all.
+// What request i asks for: pages for the entries [first, behind) of its row. False: the request cannot be met at all.
 struct Want {
-    int row, first, pages;
+    int row, first, behind;
 };
 __device__ __forceinline__ bool want_of(const PagesArgs& a, int i, bool fork, Want& w) {
     w = Want{a.dst[i], 0, 0};
@@ -55,7 +57,7 @@ __device__ __forceinline__ bool want_of(const PagesArgs& a, int i, bool fork, Wa
         if (!is_row(a, s)) return false;
         const int len = length_of(a, s);
         w.first = len / a.page;
-        w.pages = len % a.page != 0 && is_page(a, a.table[static_cast<long long>(s) * a.max_pages + w.first]);
+        w.behind = w.first + (len % a.page != 0 && is_page(a, a.table[static_cast<long long>(s) * a.max_pages + w.first]));
         return true;
     }
     const long long len = length_of(a, w.row), more = a.tokens ? a.tokens[i] : a.every;
@@ -63,9 +65,25 @@ __device__ __forceinline__ bool want_of(const PagesArgs& a, int i, bool fork, Wa
     const long long have = (len + a.page - 1) / a.page, want = (len + more + a.page - 1) / a.page;
     if (want > a.max_pages) return false;
     w.first = static_cast<int>(have);
-    w.pages = static_cast<int>(want - have);
+    w.behind = static_cast<int>(want);
     return true;
 }
+
+// append: a row whose length was lowered still names the pages behind it. They are its own, and come first. False: other rows name one of them too,
+// and tokens are not written there. A row that was never shortened ends at its first entry.
+__device__ __forceinline__ bool keep_own(const PagesArgs& a, Want& w) {
+    for (; w.first < w.behind; ++w.first) {
+        const int p = a.table[static_cast<long long>(w.row) * a.max_pages + w.first], n = is_page(a, p) ? __ldcg(a.refs + p) : 0;
+        if (n > 1) return false;
+        if (n < 1) break;
+    }
+    return true;
+}
+
+// What becomes of a request is settled by the first pass and kept in ok meanwhile, since later passes change what it was settled by: the number behind its
+// last page among all that are asked for (kMost for more: there are fewer pages), and whether it takes no page, or cannot be met.
+constexpr int kMost = (1 << 30) - 1, kNoPage = 1 << 30, kRefused = INT_MIN;
+__device__ __forceinline__ bool is_met(int settled, int free) { return !(settled & kRefused) && (settled & kNoPage || (settled & kMost) <= free); }
 
 // Inclusive sum over the block's threads in order; total: of all of them.
 __device__ __forceinline__ int block_scan(int v, int* red, int& total) {
@@ -89,9 +107,8 @@ __device__ __forceinline__ int block_scan(int v, int* red, int& total) {
     return v + (warp ? before : 0);
 }
 
-// fork: dst[i] becomes a row like src[i]; append: room for tokens behind row dst[i]. Requests' pages are numbered in order (ok[i] holds
-// the number behind request i's last one meanwhile), the free pages too, and page number r goes to the request that holds number r. A
-// request whose last number is past the free pages gets none.
+// fork: dst[i] becomes a row like src[i]; append: room for tokens behind row dst[i]. Requests' pages are numbered in order, the free pages too, and
+// page number r goes to the request that holds number r. A request whose last number is past the free pages gets none.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) pages_kernel(const __grid_constant__ PagesArgs a, bool fork) {
     __shared__ int red[32], free_here;
     cg::cluster_group cluster = cg::this_cluster();
@@ -109,10 +126,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) pag
         for (int i0 = 0; i0 < a.n; i0 += kThreads) {
             Want w{};
             const int i = i0 + tid;
-            const bool can = i < a.n && want_of(a, i, fork, w);
+            const bool can = i < a.n && want_of(a, i, fork, w) && (fork || keep_own(a, w));
+            const int pages = can ? w.behind - w.first : 0;
             int total;
-            const int end = block_scan(can ? w.pages : 0, red, total) + before;
-            if (i < a.n) a.ok[i] = end;
+            const int end = block_scan(pages, red, total) + before;
+            if (i < a.n) a.ok[i] = min(end, kMost) | (can ? pages ? 0 : kNoPage : kRefused);
             before += total;
         }
     }
@@ -129,7 +147,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) pag
         if (r < rank) before += n;
         free += n;
     }
-    const int asked = __ldcg(a.ok + a.n - 1);
+    const int asked = __ldcg(a.ok + a.n - 1) & kMost;
     // the requests' answers
     for (int p0 = lo; p0 < hi && before < asked; p0 += kThreads) {
         const int p = p0 + tid;
@@ -141,13 +159,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) pag
         int l = 0, h = a.n - 1;  // the first request that ends behind this number
         while (l < h) {
             const int m = (l + h) / 2;
-            if (__ldcg(a.ok + m) > number) h = m; else l = m + 1;
+            if ((__ldcg(a.ok + m) & kMost) > number) h = m; else l = m + 1;
         }
-        const int end = __ldcg(a.ok + l);
+        const int end = __ldcg(a.ok + l) & kMost;
         if (end > free) continue;
         Want w;
         want_of(a, l, fork, w);
-        a.table[static_cast<long long>(w.row) * a.max_pages + w.first + number - (end - w.pages)] = p;
+        a.table[static_cast<long long>(w.row) * a.max_pages + w.behind - (end - number)] = p;
         a.refs[p] = 1;
         if (fork) a.copy_to[l] = p;
     }
@@ -158,22 +176,21 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) pag
         for (long long e = first; e < entries; e += step) {
             const int i = static_cast<int>(e / a.max_pages), j = static_cast<int>(e - static_cast<long long>(i) * a.max_pages);
             Want w;
-            if (!want_of(a, i, true, w) || j >= w.first || (w.pages && __ldcg(a.ok + i) > free)) continue;
+            if (!is_met(__ldcg(a.ok + i), free) || !want_of(a, i, true, w) || j >= w.first) continue;
             const int p = a.table[static_cast<long long>(a.src[i]) * a.max_pages + j];
             if (!is_page(a, p)) continue;
             a.table[static_cast<long long>(w.row) * a.max_pages + j] = p;
             atomicAdd(a.refs + p, 1);
         }
-        cluster.sync();  // ok holds the numbers up to here: other threads look there for what their entries' requests get
+        cluster.sync();  // ok holds what was settled up to here: other threads look there for what their entries' requests get
     }
     for (long long i = first; i < a.n; i += step) {
         Want w;
-        const bool can = want_of(a, static_cast<int>(i), fork, w) && (w.pages == 0 || __ldcg(a.ok + i) <= free);
+        const bool can = is_met(__ldcg(a.ok + i), free) && want_of(a, static_cast<int>(i), fork, w);
         long long len = can ? length_of(a, fork ? a.src[i] : w.row) : -1;
         if (fork) {
-            const bool copied = can && w.pages;
-            const int last = copied ? a.table[static_cast<long long>(a.src[i]) * a.max_pages + w.first] : -1;
-            a.copy_from[i] = is_page(a, last) ? last : -1;
+            const bool copied = can && w.behind > w.first;
+            a.copy_from[i] = copied ? a.table[static_cast<long long>(a.src[i]) * a.max_pages + w.first] : -1;
             if (!copied) a.copy_to[i] = -1;
         } else if (can) {
             len += a.tokens ? a.tokens[i] : a.every;
@@ -244,7 +261,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
 
 gdn2_status pages_check(const PagesArgs& a) {
     if (a.n < 0 || a.n_slots < 0 || a.n_pages < 0 || a.max_pages <= 0 || a.page <= 0) return GDN2_ERR_INVALID_ARG;
-    if (a.page > 65536 || static_cast<long long>(a.max_pages) * a.page >= (1LL << 30) || a.n_pages >= (1 << 30) || a.n >= (1 << 24) ||
+    if (a.page > 65536 || static_cast<long long>(a.max_pages) * a.page >= (1LL << 30) || a.n_pages >= kMost || a.n >= (1 << 24) ||
         static_cast<long long>(a.n) * a.max_pages >= (1LL << 31) - 1)
         return GDN2_ERR_UNSUPPORTED;
     if (a.n == 0) return GDN2_OK;

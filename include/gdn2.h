@@ -559,7 +559,9 @@ gdn2_status gdn2_attn_decode(const void* q, long long ld_q, const void* k_pages,
  * gdn2_pages_append -- room for more tokens behind rows slots[i] (distinct): lengths grows by tokens[i] (int32 [n], or `every` each where
  * tokens is NULL), and the row gets the pages that this takes. ok[i] (int32 [n]) is 1, or 0 with the row unchanged: an inactive slot,
  * fewer than 0 tokens, more than max_pages, or not enough free pages for this request after those before it (which keep their claim
- * whether or not they were met).
+ * whether or not they were met). A row is shortened (tokens taken back, such as drafts that were turned down) by lowering its length: it
+ * keeps the pages behind that, its next tokens go there first, and pages_release gives them back with the others. A request is also turned
+ * down where it would get to such a page that other rows name too (a row shortened to before its fork): a fork of the row leaves those pages behind.
  *
  * gdn2_pages_fork -- row dst[i] (distinct) becomes one like row src[i]: dst rows are emptied first, full pages are shared, a last page that
  * is not full gets a free page of its own, and an entry that names no page stays one. copy_from[i], copy_to[i] (int32 [n]) say what to copy in every layer's pools

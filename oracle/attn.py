@@ -111,12 +111,16 @@ class Pages:
             self.table[s], self.lengths[s] = [-1] * len(self.table[s]), 0
 
     def append(self, slots, tokens):
-        free, asked, ok = self.free(), 0, []
+        free, asked, ok, before = self.free(), 0, [], list(self.refs)
         for s, more in zip(slots, tokens):
             good = self.is_row(s) and more >= 0
             have = -(-self.length(s) // self.page) if good else 0
             want = -(-(self.length(s) + more) // self.page) if good else 0
             good = good and want <= len(self.table[s])
+            # what the row still names behind its length is its own, unless other rows name it too
+            while good and have < want and self.is_page(self.table[s][have]) and before[self.table[s][have]] > 0:
+                good = before[self.table[s][have]] == 1
+                have += good
             first, asked = asked, asked + (want - have if good else 0)
             good = good and (want == have or asked <= len(free))
             if good:
