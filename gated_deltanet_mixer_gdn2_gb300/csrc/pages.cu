@@ -45,12 +45,13 @@ __device__ __forceinline__ void release_rows(const PagesArgs& a, long long first
     }
 }
 
-// What request i asks for: pages for the entries [first, behind) of its row. False: the request cannot be met at all.
+// What request i asks for: pages for the entries [first, behind) of its row. part: of append, the entry of a page that has tokens and gets more, -1 for
+// none. False: the request cannot be met at all.
 struct Want {
-    int row, first, behind;
+    int row, first, behind, part;
 };
 __device__ __forceinline__ bool want_of(const PagesArgs& a, int i, bool fork, Want& w) {
-    w = Want{a.dst[i], 0, 0};
+    w = Want{a.dst[i], 0, 0, -1};
     if (!is_row(a, w.row)) return false;
     if (fork) {
         const int s = a.src[i];
@@ -66,14 +67,22 @@ __device__ __forceinline__ bool want_of(const PagesArgs& a, int i, bool fork, Wa
     if (want > a.max_pages) return false;
     w.first = static_cast<int>(have);
     w.behind = static_cast<int>(want);
+    if (more > 0 && len % a.page != 0) w.part = w.first - 1;
     return true;
 }
 
-// append: a row whose length was lowered still names the pages behind it. They are its own, and come first. False: other rows name one of them too,
-// and tokens are not written there. A row that was never shortened ends at its first entry.
+// append: a row whose length was lowered still names the pages behind it. They are its own, and come first. False: other rows name a page too that
+// the request's tokens would get to, the row's last one or one behind it (its length was lowered to before its fork), and nothing is written
+// there. A row that was never shortened ends at its first entry.
 __device__ __forceinline__ bool keep_own(const PagesArgs& a, Want& w) {
+    const int* entries = a.table + static_cast<long long>(w.row) * a.max_pages;
+    auto names = [&](int i) {  // entries that name this one's page; 0 where it is none
+        const int p = entries[i];
+        return is_page(a, p) ? __ldcg(a.refs + p) : 0;
+    };
+    if (w.part >= 0 && names(w.part) > 1) return false;
     for (; w.first < w.behind; ++w.first) {
-        const int p = a.table[static_cast<long long>(w.row) * a.max_pages + w.first], n = is_page(a, p) ? __ldcg(a.refs + p) : 0;
+        const int n = names(w.first);
         if (n > 1) return false;
         if (n < 1) break;
     }

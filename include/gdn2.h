@@ -561,7 +561,8 @@ gdn2_status gdn2_attn_decode(const void* q, long long ld_q, const void* k_pages,
  * fewer than 0 tokens, more than max_pages, or not enough free pages for this request after those before it (which keep their claim
  * whether or not they were met). A row is shortened (tokens taken back, such as drafts that were turned down) by lowering its length: it
  * keeps the pages behind that, its next tokens go there first, and pages_release gives them back with the others. A request is also turned
- * down where it would get to such a page that other rows name too (a row shortened to before its fork): a fork of the row leaves those pages behind.
+ * down where its tokens would get to a page that other rows name too (a row shortened to before its fork): a fork of the row copies such a
+ * last page and leaves those behind it.
  *
  * gdn2_pages_fork -- row dst[i] (distinct) becomes one like row src[i]: dst rows are emptied first, full pages are shared, a last page that
  * is not full gets a free page of its own, and an entry that names no page stays one. copy_from[i], copy_to[i] (int32 [n]) say what to copy in every layer's pools

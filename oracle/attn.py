@@ -117,7 +117,9 @@ class Pages:
             have = -(-self.length(s) // self.page) if good else 0
             want = -(-(self.length(s) + more) // self.page) if good else 0
             good = good and want <= len(self.table[s])
-            # what the row still names behind its length is its own, unless other rows name it too
+            # what the row still names behind its length is its own; where tokens would get to a page that other rows name too, there is no room
+            last = self.table[s][have - 1] if good and more > 0 and self.length(s) % self.page else -1
+            good = good and not (self.is_page(last) and before[last] > 1)
             while good and have < want and self.is_page(self.table[s][have]) and before[self.table[s][have]] > 0:
                 good = before[self.table[s][have]] == 1
                 have += good
