@@ -33,7 +33,8 @@ EXPORTS = (
     "gdn2_ssm_chunk_fwd_workspace_size", "gdn2_ssm_chunk_fwd", "gdn2_ssm_backward_workspace_size", "gdn2_ssm_backward",
     "gdn2_ssm_decode_step", "gdn2_block_norm", "gdn2_block_norm_backward_workspace_size", "gdn2_block_norm_backward",
     "gdn2_attn_prologue", "gdn2_attn_prologue_paged", "gdn2_attn_prologue_backward_workspace_size", "gdn2_attn_prologue_backward",
-    "gdn2_attn_decode_workspace_size", "gdn2_attn_decode", "gdn2_pages_append", "gdn2_pages_fork", "gdn2_pages_release", "gdn2_pages_copy",
+    "gdn2_attn_decode_workspace_size", "gdn2_attn_decode", "gdn2_pages_append", "gdn2_pages_append_active", "gdn2_pages_fork",
+    "gdn2_pages_fork_active", "gdn2_pages_release", "gdn2_pages_copy",
 )
 
 
@@ -90,7 +91,9 @@ def _load() -> ctypes.CDLL:
         "gdn2_attn_decode_workspace_size": (Z, [I] * 7 + [I]),
         "gdn2_attn_decode": (I, [P, L] + [P] * 5 + [I] * 4 + [P] + [I] * 5 + [F, I, I, P, Z, P]),
         "gdn2_pages_append": (I, [P] * 5 + [I, P] + [I] * 5 + [P]),
+        "gdn2_pages_append_active": (I, [P] * 5 + [I, P, P] + [I] * 5 + [P]),
         "gdn2_pages_fork": (I, [P] * 8 + [I] * 5 + [P]),
+        "gdn2_pages_fork_active": (I, [P] * 9 + [I] * 5 + [P]),
         "gdn2_pages_release": (I, [P] * 4 + [I] * 4 + [P]),
         "gdn2_pages_copy": (I, [P, P, I, P, P, I, I, P]),
     }
@@ -971,11 +974,23 @@ def _indices(t, name, dev, n=None):
     return _dense(t, torch.int32, (t.shape[0] if n is None else n,), name, dev)
 
 
+def _active(t, dev, n, *inputs):
+    """Pointer of the int32 tensor [n] that rows which take part are written to, apart from the call's own rows; None for None."""
+    if t is None:
+        return None
+    if n and any(t.data_ptr() == i.data_ptr() for i in inputs):
+        raise ValueError("active lies in memory of its own")
+    return _indices(t, "active", dev, n)
+
+
 @_on_stream
-def pages_append(table, lengths, refs, slots, tokens, *, page, stream=None):
-    """Room for more tokens behind rows `slots` (C ABI gdn2_pages_append): lengths grows by `tokens` (an int for every row, or int32 [n])
-    and the rows get the free pages that this takes, lowest first; table, lengths and refs are updated in place. slots are distinct.
-    Returns ok: int32 [n], 0 where the row stays as it was (inactive, full, or no pages left)."""
+def pages_append(table, lengths, refs, slots, tokens, *, page, active=None, stream=None):
+    """Room for more tokens behind rows `slots` (C ABI gdn2_pages_append, gdn2_pages_append_active): lengths grows by `tokens` (an int for every
+    row, or int32 [n]) and the rows get the free pages that this takes, lowest first; table, lengths and refs are updated in place. slots are
+    distinct. A row is shortened by lowering its length: its next tokens go to the pages that it keeps behind it.
+    Returns ok: int32 [n], 0 where the row stays as it was (inactive, full, no pages left, or tokens that would get to a page of other rows too).
+    active (int32 [n], beside slots): written with slots[i], or -1 where ok is 0: the slots of the step's other calls, which would else take such a
+    row's newest tokens for the step's own and write over them."""
     import torch
 
     dev = _device(table)
@@ -986,24 +1001,26 @@ def pages_append(table, lengths, refs, slots, tokens, *, page, stream=None):
     else:
         each = _int(tokens, "tokens", 0, 2 ** 31 - 1)
     ok = torch.empty((n,), dtype=torch.int32, device=table.device)
-    _check(lib.gdn2_pages_append(*where, _indices(slots, "slots", dev), counts, each, ok.data_ptr(), n, rows, pages, wide,
-                                 _int(page, "page", 1, 65536), _raw_stream(stream, dev)), "gdn2_pages_append")
+    _check(lib.gdn2_pages_append_active(*where, _indices(slots, "slots", dev), counts, each, ok.data_ptr(), _active(active, dev, n, slots), n, rows,
+                                        pages, wide, _int(page, "page", 1, 65536), _raw_stream(stream, dev)), "gdn2_pages_append")
     return ok
 
 
 @_on_stream
-def pages_fork(table, lengths, refs, src, dst, *, page, stream=None):
+def pages_fork(table, lengths, refs, src, dst, *, page, active=None, stream=None):
     """Rows `dst` (distinct) become rows like `src` (C ABI gdn2_pages_fork): dst rows are emptied, full pages shared, a last page that is not full
     gets a free page of its own; table, lengths and refs are updated in place. Returns (copy_from, copy_to, ok), int32 [n] each: what to copy in
-    every layer's pools (pages_copy; -1 for nothing), and 0 where dst is left empty (inactive, or no pages left)."""
+    every layer's pools (pages_copy; -1 for nothing), and 0 where dst is left empty (inactive, or no pages left). active (int32 [n], beside
+    dst): written with dst[i], or -1 where ok is 0 (gdn2_pages_fork_active): the slots of the calls behind it."""
     import torch
 
     dev = _device(table)
     where, rows, pages, wide = _pages(table, lengths, refs, dev)
     n = src.shape[0]
     copy_from, copy_to, ok = (torch.empty((n,), dtype=torch.int32, device=table.device) for _ in range(3))
-    _check(lib.gdn2_pages_fork(*where, _indices(src, "src", dev), _indices(dst, "dst", dev, n), copy_from.data_ptr(), copy_to.data_ptr(),
-                               ok.data_ptr(), n, rows, pages, wide, _int(page, "page", 1, 65536), _raw_stream(stream, dev)), "gdn2_pages_fork")
+    _check(lib.gdn2_pages_fork_active(*where, _indices(src, "src", dev), _indices(dst, "dst", dev, n), copy_from.data_ptr(), copy_to.data_ptr(),
+                                      ok.data_ptr(), _active(active, dev, n, src, dst), n, rows, pages, wide, _int(page, "page", 1, 65536),
+                                      _raw_stream(stream, dev)), "gdn2_pages_fork")
     return copy_from, copy_to, ok
 
 

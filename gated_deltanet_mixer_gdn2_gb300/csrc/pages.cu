@@ -23,7 +23,7 @@ struct PagesArgs {
     int *table, *lengths, *refs;
     const int *src, *dst;       // fork: from row src[i] to row dst[i]; append, release: dst
     const int* tokens;          // append: tokens of each request, or each of `every`
-    int *copy_from, *copy_to, *ok;
+    int *copy_from, *copy_to, *ok, *active;
     int n, every, n_slots, n_pages, max_pages, page;
 };
 
@@ -209,8 +209,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) pag
     cluster.sync();  // no length is set before the last one has been read
     for (long long i = first; i < a.n; i += step) {
         const int len = a.ok[i];
-        if (len >= 0) a.lengths[a.dst[i]] = len;
+        const int row = a.dst[i];
+        if (len >= 0) a.lengths[row] = len;
         a.ok[i] = len >= 0;
+        if (a.active) a.active[i] = len >= 0 ? row : -1;
     }
 }
 
@@ -276,7 +278,7 @@ gdn2_status pages_check(const PagesArgs& a) {
     if (a.n == 0) return GDN2_OK;
     if (!a.table || !a.lengths || !a.refs || !a.dst) return GDN2_ERR_INVALID_ARG;
     for (const void* p : {(const void*)a.table, (const void*)a.lengths, (const void*)a.refs, (const void*)a.src, (const void*)a.dst,
-                          (const void*)a.tokens, (const void*)a.copy_from, (const void*)a.copy_to, (const void*)a.ok})
+                          (const void*)a.tokens, (const void*)a.copy_from, (const void*)a.copy_to, (const void*)a.ok, (const void*)a.active})
         if (!aligned_to(p, 4)) return GDN2_ERR_MISALIGNED;
     return GDN2_OK;
 }
@@ -288,9 +290,10 @@ using namespace gdn2;
 
 extern "C" {
 
-gdn2_status gdn2_pages_fork(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* src, const int32_t* dst, int32_t* copy_from,
-                            int32_t* copy_to, int32_t* ok, int n, int n_slots, int n_pages, int max_pages, int page, void* stream) {
-    PagesArgs a{table, lengths, refs, src, dst, nullptr, copy_from, copy_to, ok, n, 0, n_slots, n_pages, max_pages, page};
+gdn2_status gdn2_pages_fork_active(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* src, const int32_t* dst,
+                                   int32_t* copy_from, int32_t* copy_to, int32_t* ok, int32_t* active, int n, int n_slots, int n_pages,
+                                   int max_pages, int page, void* stream) {
+    PagesArgs a{table, lengths, refs, src, dst, nullptr, copy_from, copy_to, ok, active, n, 0, n_slots, n_pages, max_pages, page};
     const gdn2_status st = pages_check(a);
     if (st != GDN2_OK || n == 0) return st;
     if (!src || !copy_from || !copy_to || !ok) return GDN2_ERR_INVALID_ARG;
@@ -298,9 +301,14 @@ gdn2_status gdn2_pages_fork(int32_t* table, int32_t* lengths, int32_t* refs, con
     return cudaGetLastError() == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA;
 }
 
-gdn2_status gdn2_pages_append(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* slots, const int32_t* tokens, int every,
-                              int32_t* ok, int n, int n_slots, int n_pages, int max_pages, int page, void* stream) {
-    PagesArgs a{table, lengths, refs, nullptr, slots, tokens, nullptr, nullptr, ok, n, every, n_slots, n_pages, max_pages, page};
+gdn2_status gdn2_pages_fork(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* src, const int32_t* dst, int32_t* copy_from,
+                            int32_t* copy_to, int32_t* ok, int n, int n_slots, int n_pages, int max_pages, int page, void* stream) {
+    return gdn2_pages_fork_active(table, lengths, refs, src, dst, copy_from, copy_to, ok, nullptr, n, n_slots, n_pages, max_pages, page, stream);
+}
+
+gdn2_status gdn2_pages_append_active(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* slots, const int32_t* tokens, int every,
+                                     int32_t* ok, int32_t* active, int n, int n_slots, int n_pages, int max_pages, int page, void* stream) {
+    PagesArgs a{table, lengths, refs, nullptr, slots, tokens, nullptr, nullptr, ok, active, n, every, n_slots, n_pages, max_pages, page};
     const gdn2_status st = pages_check(a);
     if (st != GDN2_OK) return st;
     if (!tokens && every < 0) return GDN2_ERR_INVALID_ARG;
@@ -310,9 +318,14 @@ gdn2_status gdn2_pages_append(int32_t* table, int32_t* lengths, int32_t* refs, c
     return cudaGetLastError() == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA;
 }
 
+gdn2_status gdn2_pages_append(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* slots, const int32_t* tokens, int every,
+                              int32_t* ok, int n, int n_slots, int n_pages, int max_pages, int page, void* stream) {
+    return gdn2_pages_append_active(table, lengths, refs, slots, tokens, every, ok, nullptr, n, n_slots, n_pages, max_pages, page, stream);
+}
+
 gdn2_status gdn2_pages_release(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* slots, int n, int n_slots, int n_pages,
                                int max_pages, void* stream) {
-    PagesArgs a{table, lengths, refs, nullptr, slots, nullptr, nullptr, nullptr, nullptr, n, 0, n_slots, n_pages, max_pages, 1};
+    PagesArgs a{table, lengths, refs, nullptr, slots, nullptr, nullptr, nullptr, nullptr, nullptr, n, 0, n_slots, n_pages, max_pages, 1};
     const gdn2_status st = pages_check(a);
     if (st != GDN2_OK || n == 0) return st;
     const long long blocks = (static_cast<long long>(n) * max_pages + 255) / 256;

@@ -563,18 +563,26 @@ gdn2_status gdn2_attn_decode(const void* q, long long ld_q, const void* k_pages,
  * keeps the pages behind that, its next tokens go there first, and pages_release gives them back with the others. A request is also turned
  * down where its tokens would get to a page that other rows name too (a row shortened to before its fork): a fork of the row copies such a
  * last page and leaves those behind it.
+ * A row that a request was turned down for holds what it held, so a step's other calls must leave it out: they would take its newest tokens for
+ * the step's own and write over them. gdn2_pages_append_active also leaves active[i] (int32 [n]): slots[i] where ok[i] is 1, else -1, which
+ * those calls take for their slots; nothing waits for the host.
  *
  * gdn2_pages_fork -- row dst[i] (distinct) becomes one like row src[i]: dst rows are emptied first, full pages are shared, a last page that
  * is not full gets a free page of its own, and an entry that names no page stays one. copy_from[i], copy_to[i] (int32 [n]) say what to copy in every layer's pools
  * (gdn2_pages_copy, before anything is written to or given back by these rows), -1 for nothing. ok[i] is 1, or 0 with dst[i] left empty: an inactive slot, or no free page. A source that is among
- * the dst rows counts as empty.
+ * the dst rows counts as empty. gdn2_pages_fork_active also leaves active[i] (int32 [n]): dst[i] where ok[i] is 1, else -1, the slots of an append behind it.
  *
  * gdn2_pages_release -- empties rows slots[i]: their pages are given back, entries become -1, lengths 0. Slots out of range are skipped.
  */
 gdn2_status gdn2_pages_append(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* slots, const int32_t* tokens, int every,
                               int32_t* ok, int n, int n_slots, int n_pages, int max_pages, int page, void* stream);
+gdn2_status gdn2_pages_append_active(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* slots, const int32_t* tokens, int every,
+                                     int32_t* ok, int32_t* active, int n, int n_slots, int n_pages, int max_pages, int page, void* stream);
 gdn2_status gdn2_pages_fork(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* src, const int32_t* dst, int32_t* copy_from,
                             int32_t* copy_to, int32_t* ok, int n, int n_slots, int n_pages, int max_pages, int page, void* stream);
+gdn2_status gdn2_pages_fork_active(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* src, const int32_t* dst,
+                                   int32_t* copy_from, int32_t* copy_to, int32_t* ok, int32_t* active, int n, int n_slots, int n_pages,
+                                   int max_pages, int page, void* stream);
 gdn2_status gdn2_pages_release(int32_t* table, int32_t* lengths, int32_t* refs, const int32_t* slots, int n, int n_slots, int n_pages,
                                int max_pages, void* stream);
 
