@@ -543,7 +543,10 @@ gdn2_status gdn2_attn_prologue_backward(const void* q, long long ld_q, const voi
  *     o = softmax(scale q K^T) V  over the keys that a token sees: token n those up to number lengths - N + n, with window > 0 the last
  *     `window` of them (itself the last), and of these the ones that have a page. A token that sees none gets zeros.
  *   q [B, N, H_q, d] dt (ld_q between tokens), o [B, N, H_q, d] dt; query head h reads key head h / (H_q / H_kv)
- * Keys and values that a token does not see do not reach it, whatever they hold; ones that it sees and that are not finite make it not finite. Scores, sums and outputs are fp32; B up to 65535.
+ * Keys and values that a token does not see do not reach it, whatever they hold. Of those that it sees, a key whose score is -inf has no weight (a
+ * token that has such scores alone gets zeros), and a score of +inf or NaN, or a value that is not finite, makes the token not finite.
+ * Scores, their maxima, sums and results are fp32 before the last rounding; scores beyond its range are infinite. Over bf16 caches a weight is taken
+ * by the hardware's 2^x (2^-21 of it) and goes into its product with the values as two bf16 parts (2^-17 of it); the sum takes it whole. B up to 65535.
  * workspace: gdn2_attn_decode_workspace_size(...) bytes, 16-byte aligned; may be NULL when that is 0.
  */
 size_t gdn2_attn_decode_workspace_size(int B, int N, int Hq, int Hkv, int d, int max_pages, int page, gdn2_dtype dt);
