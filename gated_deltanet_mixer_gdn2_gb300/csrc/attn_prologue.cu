@@ -37,8 +37,8 @@ struct PrologueArgs {
 };
 
 // inv_freq as turns per position in 64-bit fixed point, modulo one turn: f / (2 pi) = m 2^(e - 150) / (2 pi) with m the 24 bits of f, and
-// kTurns = 2^66 / (2 pi). position * turns, wrapping, is the angle modulo a turn to 2^-64 per position: exact enough (2^-33 of a turn) for
-// any 32-bit position, where a 32-bit product would lose the angle from some ten thousand positions on.
+// kTurns = 2^66 / (2 pi). position * turns, wrapping, is the angle modulo a turn to 2^-64 (1 + |f| / 2 pi) per position: 2^-33 of a turn
+// for any 32-bit position and frequencies of about one, where a 32-bit product would lose the angle from some ten thousand positions on.
 __device__ __forceinline__ unsigned long long turns_of(float f) {
     constexpr unsigned long long kTurns = 11743562013128004906ull;
     const unsigned bits = __float_as_uint(f);
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, Raw8<T>::kBlocks) prologue_kernel(co
     const long long r = row0 + token, r_in = r < rows ? r : rows - 1;
     const int d = a.d;
     constexpr int kFlight = Raw8<T>::kFlight;
-    // Heads part, part + step, .. of one side. Rows of no sequence are read and dropped.
+    // Heads part, part + step, .. of one side. Rows of no sequence and of inactive slots are loaded before that is known, and dropped.
     const T *qs = static_cast<const T*>(a.q) + r_in * a.ld_q, *ks = static_cast<const T*>(a.k) + r_in * a.ld_k;
     auto fetch = [&](Raw8<T>& to, const T* src, int h, int H) {
         if (h < H) to.load(src + h * d, at);

@@ -486,12 +486,12 @@ gdn2_status gdn2_block_norm_backward(const void* x, const void* z, const float* 
  *     by custom) is no page. lengths int32 [n_slots] counts a row's tokens, those of the present call among them: with N tokens in the
  *     call, the first is number lengths - N. refs int32 [n_pages] counts the table entries that name a page; a page with none is free.
  *     slots int32 [B] maps the call's rows to rows of the table, as it maps them to rows of the mixers' state pools (NULL: row b is row
- *     b); a slot outside [0, n_slots) marks the row inactive: nothing of it is read or written. Rows that a call writes to name distinct slots. All of this is read on the device;
+ *     b); a slot outside [0, n_slots) marks the row inactive: nothing of it is read into any result or written. Rows that a call writes to name distinct slots. All of this is read on the device;
  *     lengths are clamped to [0, max_pages * page], so that wrong values give wrong results, but no access outside the tensors.
  *   - A workspace serves one call at a time: calls, and graphs, whose kernels may overlap have one each.
  *   - Sizes: d a multiple of 16 up to 256, page any size up to 65536, max_pages * page below 2^30.
  *   - Sequences, rows and ld_* as for the gdn2_ssm_* entry points: token tensors may be slices of wider rows that start on 16-byte
- *     boundaries, their ld a multiple of 8 elements. Rows of no sequence (packed) are neither read nor written. Outputs do not overlap inputs.
+ *     boundaries, their ld a multiple of 8 elements. Rows of no sequence (packed) are neither read into any result nor written. Outputs do not overlap inputs.
  * Errors: GDN2_ERR_INVALID_ARG (dtype, sizes, H_q % H_kv, null required pointer, ld below the row's width), GDN2_ERR_UNSUPPORTED (size not
  * built, too large), GDN2_ERR_MISALIGNED, GDN2_ERR_WORKSPACE, GDN2_ERR_CUDA. Asynchronous on `stream`; no entry point allocates or
  * synchronises.
@@ -505,7 +505,8 @@ gdn2_status gdn2_block_norm_backward(const void* x, const void* z, const float* 
  *   q_weight, k_weight  fp32 [d] or NULL (that side is not normalised)
  *   inv_freq            fp32 [rot / 2]; rot a multiple of 16 up to d, 0 for no rotation (inv_freq may then be NULL)
  *   positions           int32, one per row, or NULL: the token's index in its sequence
- * Angles are formed modulo a turn in 64-bit fixed point: exact to fp32 at every 32-bit position.
+ * Angles are formed modulo a turn in 64-bit fixed point, within 2^-33 (1 + |inv_freq| / 2 pi) of a turn at every 32-bit position, and rounded to 24 bits
+ * of half a turn before their cosines and sines are taken.
  */
 gdn2_status gdn2_attn_prologue(const void* q, long long ld_q, const void* k, long long ld_k, const float* q_weight,
                                const float* k_weight, const float* inv_freq, const int32_t* positions, const int32_t* offsets,
