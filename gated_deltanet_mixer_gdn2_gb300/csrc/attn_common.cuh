@@ -41,7 +41,6 @@ inline int sm_count() {
 }
 
 inline bool attn_dtype_ok(gdn2_dtype dt) { return dt == GDN2_F32 || dt == GDN2_BF16; }
-inline size_t attn_esize(gdn2_dtype dt) { return dt == GDN2_BF16 ? 2 : 4; }
 
 // Sizes of a cache: every index of a table fits an int, as does the number of a row's tokens.
 inline gdn2_status cache_check(const int32_t* table, const int32_t* lengths, const int32_t* slots, int n_slots, int n_pages, int max_pages,

@@ -953,7 +953,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
 // Widths that a kernel is built for, and blocks per SM: some 128 KB of copies in flight on an SM, which its share of the copy rate takes.
 int width_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 // Query rows of a unit, in tiles: over bf16 caches two share the copies of K and V where there are two.
-int tiles_of(int rows, int d, gdn2_dtype dt) { return dt == GDN2_BF16 && rows > kTile ? 2 : 1; }
+int tiles_of(int rows, gdn2_dtype dt) { return dt == GDN2_BF16 && rows > kTile ? 2 : 1; }
 int blocks_of(int d, int tiles, gdn2_dtype dt) {
     const int D = width_of(d);
     const int blocks = sm_count() * (dt == GDN2_BF16 ? (D == 64 ? (tiles == 2 ? 2 : 3) : D == 128 && tiles == 1 ? 2 : 1) : D == 64 ? 2 : 1);
@@ -1054,7 +1054,7 @@ extern "C" {
 
 size_t gdn2_attn_decode_workspace_size(int B, int N, int Hq, int Hkv, int d, int max_pages, int page, gdn2_dtype dt) {
     if (decode_check(B, N, Hq, Hkv, d, dt) != GDN2_OK || B == 0 || N == 0 || max_pages <= 0 || page <= 0) return 0;
-    const int rows = N * (Hq / Hkv), tiles = tiles_of(rows, d, dt);
+    const int rows = N * (Hq / Hkv), tiles = tiles_of(rows, dt);
     if (whole_units(static_cast<long long>(B) * Hkv * ((rows + kTile * tiles - 1) / (kTile * tiles)), max_pages, page)) return 0;
     return sizeof(float) * 2 * blocks_of(d, tiles, dt) * static_cast<size_t>(part_floats(width_of(d), kTile * tiles));
 }
@@ -1082,7 +1082,7 @@ gdn2_status gdn2_attn_decode(const void* q, long long ld_q, const void* k_pages,
     a.parts = static_cast<float*>(workspace);
     a.cache = Cache{table, lengths, slots, n_slots, n_pages, max_pages, page};
     a.B = B; a.N = N; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.d = d;
-    const int tiles = tiles_of(N * a.G, d, dt);
+    const int tiles = tiles_of(N * a.G, dt);
     a.tiles = (N * a.G + kTile * tiles - 1) / (kTile * tiles);
     a.whole = whole_units(static_cast<long long>(B) * Hkv * a.tiles, max_pages, page);
     a.window = static_cast<long long>(window) >= static_cast<long long>(max_pages) * page ? 0 : window;
