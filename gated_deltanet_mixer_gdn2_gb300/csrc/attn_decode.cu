@@ -13,7 +13,7 @@
 // (0.93). Of the time, some 12 us are the way in (lengths, table, first keys) and out (parts), whatever the length. The products have 16
 // rows where a tensor-memory product has 128, so they run on warp-wide matrix instructions: their pipe is a quarter busy at the copy rate.
 // More than 16 query rows (drafted tokens) are another matter: with two tiles a warp the latency of a step's chain bounds it, so heads wider
-// than 64 take attn_decode_tc.cuh (16 rows of 8192 tokens, 4 tokens of 32/4 heads of 128: 60 us, with two tiles here 72; heads of 256, 8 rows: 61 and,
+// than 64 take attn_decode_tc.cuh (16 rows of 8192 tokens, 4 tokens of 32/4 heads of 128: 61 us, with two tiles here 72; heads of 256, 8 rows: 62 and,
 // each tile reading everything, 99).
 #include "attn_common.cuh"
 

@@ -7,7 +7,7 @@
 // scores, one column of the output and all rows of it. (A ninth warp would leave each thread 168 registers, and these need more.) The maximum
 // that weights refer to follows the scores only where they pass it by 8, as in the other form.
 //
-// 16 rows of 7600 to 8192 tokens, 4 tokens of 32/4 heads of 128: 60 us for 38 of copies, of which 5 are the joining launch and some 12 the
+// 16 rows of 7600 to 8192 tokens, 4 tokens of 32/4 heads of 128: 61 us for 38 of copies, of which 5 are the joining launch and some 12 the
 // way in and out of a unit, a good part of it code that runs for the first time. In between a step of 64 KB takes 1.5 us, a little more than its share of
 // the copy rate, with the copying warps never idle for long; its chain (scores, weights, values) takes 1.3. Copies of 16 bytes a lane instead
 // of tensor copies: 75 (what pages that are no multiples of 16 keys get); products issued by a warp that makes weights too: 77; every loop

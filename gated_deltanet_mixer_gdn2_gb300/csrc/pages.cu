@@ -3,8 +3,11 @@
 // answer on the host and can be captured. Free pages are given out lowest first and in the order of the requests: the same calls leave
 // the same tables, whatever the blocks' order.
 //
-// Bound by latency: a call is a few dependent passes over some kilobytes. One cluster of blocks does a whole call in one launch, its passes
-// ordered by cluster barriers. The copies are bound by memory: 32 KB pieces, eight 16-byte loads in flight per thread.
+// Bound by latency: a call is a few dependent passes over some kilobytes, and over all counts. One cluster of blocks does a whole call in one launch, its
+// passes ordered by cluster barriers. A token for 64 rows takes 9.5 us with a pool of 1250 pages, 11 with 10^5, 14.7 with 10^6; for 1024 rows 18 and 29
+// with the larger ones; a fork of 8 rows of up to 200 pages 13 to 14. What a shortened row holds is looked at by a warp per row: 8192 tokens behind
+// a row shortened to nothing take 14.6 us, 131072 (pages of 16) 108, against 19 with the pages given back first.
+// The copies are bound by memory: 32 KB pieces, eight 16-byte loads in flight per thread.
 #include <cooperative_groups.h>
 
 #include <climits>
@@ -73,20 +76,37 @@ __device__ __forceinline__ bool want_of(const PagesArgs& a, int i, bool fork, Wa
 
 // append: a row whose length was lowered still names the pages behind it. They are its own, and come first. False: other rows name a page too that
 // the request's tokens would get to, the row's last one or one behind it (its length was lowered to before its fork), and nothing is written
-// there. A row that was never shortened ends at its first entry.
-__device__ __forceinline__ bool keep_own(const PagesArgs& a, Want& w) {
-    const int* entries = a.table + static_cast<long long>(w.row) * a.max_pages;
-    auto names = [&](int i) {  // entries that name this one's page; 0 where it is none
-        const int p = entries[i];
+// there. A row that was never shortened ends at its first entry. Each lane has a request (can: one that may be met); from its second page on the
+// warp looks at 32 entries together.
+__device__ __forceinline__ bool keep_own(const PagesArgs& a, bool can, Want& w) {
+    const int lane = threadIdx.x & 31;
+    auto names = [&](int row, int i) {  // entries that name this one's page; 0 where it is none
+        const int p = a.table[static_cast<long long>(row) * a.max_pages + i];
         return is_page(a, p) ? __ldcg(a.refs + p) : 0;
     };
-    if (w.part >= 0 && names(w.part) > 1) return false;
-    for (; w.first < w.behind; ++w.first) {
-        const int n = names(w.first);
-        if (n > 1) return false;
-        if (n < 1) break;
+    bool shared = can && w.part >= 0 && names(w.row, w.part) > 1, on = false;
+    if (can && !shared && w.first < w.behind) {
+        const int n = names(w.row, w.first);
+        shared = n > 1;
+        on = n == 1 && ++w.first < w.behind;
     }
-    return true;
+    for (unsigned left = __ballot_sync(0xffffffffu, on); left; left &= left - 1) {
+        const int l = __ffs(left) - 1, row = __shfl_sync(0xffffffffu, w.row, l), behind = __shfl_sync(0xffffffffu, w.behind, l);
+        int at = __shfl_sync(0xffffffffu, w.first, l), n = 1;
+        for (; at < behind && n == 1; at += 32) {  // n: of the first entry that is not the row's own
+            const int here = at + lane < behind ? names(row, at + lane) : 0;
+            const unsigned others = __ballot_sync(0xffffffffu, here != 1);
+            if (!others) continue;
+            const int first = __ffs(others) - 1;
+            n = __shfl_sync(0xffffffffu, here, first);
+            at += first - 32;
+        }
+        if (lane == l) {
+            w.first = min(at, behind);
+            shared = n > 1;
+        }
+    }
+    return can && !shared;
 }
 
 // What becomes of a request is settled by the first pass and kept in ok meanwhile, since later passes change what it was settled by: the number behind its
@@ -135,7 +155,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) pag
         for (int i0 = 0; i0 < a.n; i0 += kThreads) {
             Want w{};
             const int i = i0 + tid;
-            const bool can = i < a.n && want_of(a, i, fork, w) && (fork || keep_own(a, w));
+            bool can = i < a.n && want_of(a, i, fork, w);
+            if (!fork) can = keep_own(a, can, w);
             const int pages = can ? w.behind - w.first : 0;
             int total;
             const int end = block_scan(pages, red, total) + before;
